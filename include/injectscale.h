@@ -78,6 +78,7 @@ typedef enum {
 #define IS_ST_POSITION     0x20u  /* seg_start < 0 or seg_start + length > IS_MAX_POSITION */
 #define IS_ST_COUNT        0x40u  /* n_ids[r] < 0 or > ids_stride */
 #define IS_ST_TIMEOUT      0x80u  /* a bounded device wait gave up */
+#define IS_ST_FREE_LIST    0x100u /* the free list has too few blocks, or its head is outside it */
 
 /* IS_FP8_E4M3 is a paged-cache type only (never a store type): 8-bit floats
  * in the OCP E4M3 format (no infinities, largest finite 448), the 8-bit KV
@@ -447,6 +448,160 @@ is_status_t is_inject_noalloc(const void* kv_arena, int64_t arena_tokens,
                               int32_t max_blocks_per_seq, const is_cache_desc_t* cache,
                               void* kv_cache, int32_t* seg_len_out, int64_t* slot_mapping_out,
                               uint32_t* status_out, cudaStream_t stream);
+
+/* ---- the serving step around the segment ---------------------------------------
+ * A request's memory segment is injected; its prompt and the tokens it
+ * generates follow.  Three calls carry them through one layer's paged cache:
+ * is_extend_block_table makes room for a step's new tokens, is_append rotates
+ * their queries and keys and writes their K/V behind the segment, and
+ * is_attend attends from them over the whole paged cache, segment included.
+ * The three need no store, allocate nothing and keep nothing between calls:
+ * every buffer is the caller's, and device-detected errors are OR-ed into the
+ * caller's status word, as in is_inject_noalloc.  Each takes its arguments in
+ * a struct that is read before the call returns, so a serving loop fills it
+ * once.  The device is the one that owns the call's buffers (the current
+ * device is put back afterwards) and the stream must belong to it.  All
+ * pointers are device (or managed) memory; outputs overlap neither one another
+ * nor any input unless said.  The kernels may start before the previous
+ * kernel of the stream has ended and wait for it before they touch memory. */
+
+/* is_extend_block_table: blocks, slots and positions of the tokens about to be
+ * computed.  Request r holds seq_len[r] tokens in the blocks its row of
+ * block_table names and gets new_len[r] more.  The blocks its row lacks for
+ * them are taken from free_blocks, in request order from index *free_head on,
+ * and entered in the row; the other entries are left as they are.
+ *   token_start_out   [R+1] first packed token of each request, then the total
+ *   slot_mapping_out  [max_tokens] slot of each new token, requests back to
+ *                     back; -1 behind the last one, as for a refused token
+ *   positions_out     [max_tokens] position of each new token (-1 if refused);
+ *                     left as it was behind the last one
+ *   seq_len_out       [R] seq_len + new_len (seq_len of a refused request)
+ *   free_head_out     [1] index behind the last block taken
+ * A request is refused, keeps its packed tokens and takes no blocks when
+ * seq_len or new_len is negative (IS_ST_COUNT; a negative new_len counts as 0
+ * tokens, one past IS_MAX_POSITION as IS_MAX_POSITION), its tokens would pass
+ * IS_MAX_POSITION (IS_ST_POSITION) or its table row (IS_ST_BLOCK_TABLE), or
+ * the free list runs out (IS_ST_FREE_LIST).  A token whose block id lies
+ * outside [0, num_blocks) gets slot -1 and a position (IS_ST_BLOCK_ID); tokens
+ * past max_tokens get neither (IS_ST_COUNT). */
+typedef struct {
+  int32_t num_requests;        /* R: 1 .. IS_MAX_REQUESTS */
+  int32_t num_free;            /* entries of free_blocks, >= 0 */
+  int32_t block_size;          /* 1 .. IS_MAX_POSITION, here and in the two calls below */
+  int32_t num_blocks;
+  int32_t max_blocks_per_seq;
+  int32_t max_tokens;          /* >= 1 */
+  const int32_t* seq_len;      /* [R] */
+  const int32_t* new_len;      /* [R] */
+  const int32_t* free_blocks;  /* [num_free] (NULL only with num_free 0) */
+  const int32_t* free_head;    /* [1] or NULL: 0 */
+  int32_t* block_table;        /* [R][max_blocks_per_seq], in and out */
+  int64_t* slot_mapping_out;
+  int32_t* positions_out;      /* or NULL */
+  int32_t* token_start_out;    /* or NULL */
+  int32_t* seq_len_out;        /* or NULL */
+  int32_t* free_head_out;      /* or NULL */
+  uint32_t* status_out;
+} is_extend_args_t;
+is_status_t is_extend_block_table(const is_extend_args_t* args, cudaStream_t stream);
+
+/* Which position axis turns which pair of a head (is_append).  Text has one
+ * axis.  Images and video have three (time, height, width): pair i of the
+ * head_dim / 2 turns by its own axis' position times w_i.
+ *   interleaved 0   the pairs in order: section[0] of axis 0, then section[1]
+ *                   of axis 1, then section[2] of axis 2
+ *   interleaved 1   the axes in turn: with A axes, axis a > 0 has the pairs
+ *                   a, a + A, ... (section[a] of them), axis 0 all others
+ * The sections add up to head_dim / 2.  A token whose positions agree on all
+ * axes is rotated as in text, and as is_inject rotates facts. */
+#define IS_MAX_ROPE_AXES 3
+typedef struct {
+  int32_t n_axes;                       /* 1 .. IS_MAX_ROPE_AXES */
+  int32_t interleaved;
+  int32_t section[IS_MAX_ROPE_AXES];    /* read when n_axes > 1 */
+  int32_t reserved;                     /* must be 0 */
+} is_rope_axes_t;
+
+/* is_append: rotate the queries and keys of num_tokens new tokens to their
+ * positions, write the queries to q_out and the keys and raw values to the
+ * tokens' slots of one layer's cache.  Rotation, rounding and the FP8 cache
+ * are those of is_inject.  A token with slot -1 (padding) is skipped: nothing
+ * is written for it, its q_out row included.  So is, with its status bit, one
+ * with any other slot outside the cache (IS_ST_BLOCK_ID) or a position outside
+ * [0, IS_MAX_POSITION) (IS_ST_POSITION).  Slots of one call must be distinct.
+ * q_out may be q itself (then q_stride is num_q_heads * head_dim); q, k and v
+ * are rows of any stride, for instance views of one projection's output. */
+typedef struct {
+  int32_t num_tokens;          /* >= 0 */
+  int32_t num_q_heads;         /* 0: keys and values only (q, q_out NULL) */
+  int32_t num_kv_heads;
+  int32_t head_dim;            /* power of two, 16 .. IS_MAX_HEAD_DIM; limits of is_rope_params_t */
+  int32_t dtype;               /* is_dtype_t of q, k, v, q_out: IS_F32, IS_BF16 or IS_F16 */
+  int32_t reserved;            /* must be 0 */
+  int64_t q_stride, k_stride, v_stride;  /* elements between tokens; rows 16-byte aligned */
+  const void* q;               /* [T] rows of [num_q_heads][head_dim] */
+  const void* k;               /* [T] rows of [num_kv_heads][head_dim], before rotation */
+  const void* v;
+  const int32_t* positions;    /* [n_axes][num_tokens] */
+  const int64_t* slot_mapping; /* [num_tokens] */
+  void* q_out;                 /* [T][num_q_heads][head_dim] */
+  void* layer_cache;           /* [2][num_blocks][block_size][num_kv_heads][head_dim] */
+  uint32_t* status_out;
+  is_rope_params_t rope;
+  is_rope_axes_t axes;
+  is_cache_desc_t cache;       /* dtype: the call's, or IS_FP8_E4M3 with a 16-bit one */
+  int32_t reserved2;           /* must be 0 */
+} is_append_args_t;
+is_status_t is_append(const is_append_args_t* args, cudaStream_t stream);
+
+/* is_attend: softmax attention of each request's last tokens over its paged
+ * cache.  Request r has seq_len[r] tokens in the cache, of which the last n =
+ * q_start[r+1] - q_start[r] have a query row (rows q_start[r] .. of q, out and
+ * lse_out).  Its i-th query stands at position p = seq_len[r] - n + i and sees
+ * the keys at positions max(0, p - window + 1) .. p (window 0: from 0):
+ *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q.k_j),
+ *   lse = log sum_j w_j.
+ * Query head h uses KV head h / (num_q_heads / num_kv_heads).  A row that sees
+ * no key gives out 0 and lse -inf.  Rows of no request are left as they were.
+ * Keys and values behind seq_len are not read into any row, whatever they
+ * hold.  A position whose block the table does not name (an id outside
+ * [0, num_blocks): IS_ST_BLOCK_ID; past the row's end: IS_ST_BLOCK_TABLE) is
+ * hidden from every row.  A request whose rows leave [0, num_tokens), are more
+ * than max_q_len or fewer than 0, or whose seq_len is outside
+ * [0, IS_MAX_POSITION], is left out (IS_ST_COUNT).
+ *   workspace   scratch of this call alone while it runs: calls that may
+ *               overlap (streams, captured graphs) have one each.
+ *               IS_ATTEND_WORKSPACE_BYTES is enough for every call;
+ *               its contents need no initialisation and mean nothing later.
+ * Products are summed in fp32; with a 16-bit q the weights w_j are rounded to
+ * 16 bits before they multiply the values.  head_dim is 64, 128 or 256. */
+#define IS_ATTEND_WORKSPACE_BYTES 67108864
+typedef struct {
+  int32_t num_requests;        /* R: 1 .. IS_MAX_REQUESTS */
+  int32_t num_tokens;          /* rows of q, out, lse_out */
+  int32_t max_q_len;           /* largest number of query rows of a request, >= 1 */
+  int32_t num_q_heads;         /* a multiple of num_kv_heads */
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t dtype;               /* is_dtype_t of q and out: IS_F32, IS_BF16 or IS_F16 */
+  int32_t max_blocks_per_seq;
+  int32_t window;              /* >= 0 */
+  float scale;                 /* finite */
+  int64_t q_stride;            /* elements between rows of q; rows 16-byte aligned */
+  const void* q;               /* rows of [num_q_heads][head_dim] */
+  const int32_t* q_start;      /* [R+1], or NULL: request r has row r alone */
+  const int32_t* seq_len;      /* [R] */
+  const int32_t* block_table;  /* [R][max_blocks_per_seq] */
+  const void* layer_cache;     /* [2][num_blocks][block_size][num_kv_heads][head_dim] */
+  void* out;                   /* [num_tokens][num_q_heads][head_dim] */
+  float* lse_out;              /* [num_tokens][num_q_heads] or NULL */
+  void* workspace;             /* 16-byte aligned */
+  int64_t workspace_bytes;     /* >= IS_ATTEND_WORKSPACE_BYTES */
+  uint32_t* status_out;
+  is_cache_desc_t cache;       /* dtype: the call's, or IS_FP8_E4M3 with a 16-bit one */
+  int32_t reserved;            /* must be 0 */
+} is_attend_args_t;
+is_status_t is_attend(const is_attend_args_t* args, cudaStream_t stream);
 
 /* ---- is_set_retrieval_mode -----------------------------------------------------
  * How the similarity is computed.  IS_RETRIEVAL_PER_QUERY: one launch in

@@ -12,7 +12,7 @@ from ctypes import byref, c_double, c_int64, c_uint32, c_void_p
 import numpy as np
 
 from . import _lib
-from ._lib import CacheDesc, RopeParams, StoreConfig, StoreInfo
+from ._lib import AppendArgs, AttendArgs, CacheDesc, ExtendArgs, RopeAxes, RopeParams, StoreConfig, StoreInfo
 
 DTYPE_CODES = {"f32": _lib.IS_F32, "bf16": _lib.IS_BF16, "f16": _lib.IS_F16, "e4m3": _lib.IS_FP8_E4M3}
 
@@ -301,6 +301,174 @@ def is_inject_noalloc(kv_arena, arena_tokens: int, fact_tok, fact_len, max_fact_
         stride, _ptr(seg_start), byref(rope), _ptr(block_table), int(block_table.shape[1]),
         byref(cache), _ptr(kv_cache), _ptr(seg_len_out), _ptr(slot_mapping_out), _ptr(status_out),
         _stream(stream)))
+
+
+def make_axes(sections=None, interleaved: bool = False) -> RopeAxes:
+    """The position axes of is_append: pairs per axis (None: one axis, text)."""
+    sections = [0] if sections is None else [int(n) for n in sections]
+    if not 1 <= len(sections) <= _lib.IS_MAX_ROPE_AXES:
+        raise ValueError(f"1 to {_lib.IS_MAX_ROPE_AXES} sections")
+    pad = sections + [0] * (_lib.IS_MAX_ROPE_AXES - len(sections))
+    return RopeAxes(len(sections), 1 if interleaved else 0, (ctypes.c_int32 * _lib.IS_MAX_ROPE_AXES)(*pad), 0)
+
+
+def _typed(name: str, t, dtype: str, shape=None, device=None, optional: bool = False):
+    """A contiguous CUDA tensor of a type and shape (None: any size there) on `device`."""
+    if t is None and optional:
+        return None
+    return _rows(name, t, dtype, shape, device, dense=True)
+
+
+def _rows(name: str, t, dtype: str, shape=None, device=None, dense: bool = False):
+    """As _typed, but the first dimension may have any stride."""
+    if not hasattr(t, "data_ptr") or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if str(t.dtype) != "torch." + dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    if dense and not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    if not dense and t.numel() and not t[0].is_contiguous():
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t
+
+
+_TORCH_NAMES = {"float32": "f32", "bfloat16": "bf16", "float16": "f16"}
+
+
+def _float_code(name: str, t) -> tuple[str, int]:
+    dt = str(getattr(t, "dtype", "")).replace("torch.", "")
+    if dt not in _TORCH_NAMES:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    return dt, DTYPE_CODES[_TORCH_NAMES[dt]]
+
+
+def _layer_cache(cache: CacheDesc, layer_cache, heads, dim, dtype: str, device):
+    """The layer's cache tensor [2][num_blocks][block_size][heads][dim]; FP8 as uint8 or float8_e4m3fn."""
+    if cache.dtype == _lib.IS_FP8_E4M3:
+        dtype = "float8_e4m3fn" if "float8_e4m3fn" in str(getattr(layer_cache, "dtype", "")) else "uint8"
+    return _typed("layer_cache", layer_cache, dtype, (2, cache.num_blocks, cache.block_size, heads, dim), device)
+
+
+def _prepared(fn_name: str, args, keep, stream, device):
+    """A callable that issues the call on the bound buffers (contents may change between calls)."""
+    fn = getattr(_lib.load(), fn_name)
+    ref = byref(args)
+    if stream is None:
+        import torch
+        stream = torch.cuda.current_stream(device)
+    st = c_void_p(_stream(stream))
+
+    def call():
+        status = fn(ref, st)
+        if status != _lib.IS_OK:
+            _check(status)
+    call.keep = (args, keep)                  # the struct and the bound tensors must outlive the callable
+    return call
+
+
+def prepare_extend_block_table(seq_len, new_len, free_blocks, block_size: int, num_blocks: int, block_table,
+                               slot_mapping_out, positions_out=None, token_start_out=None, seq_len_out=None,
+                               status_out=None, free_head=None, free_head_out=None, stream=None):
+    """is_extend_block_table with every argument marshalled once: a callable for
+    serving loops that reuse their buffers."""
+    dev = _typed("seq_len", seq_len, "int32", (None,)).device
+    R, T = int(seq_len.shape[0]), int(slot_mapping_out.shape[0])
+    args = ExtendArgs(
+        R, int(free_blocks.shape[0]), int(block_size), int(num_blocks), int(block_table.shape[1]), T,
+        _ptr(seq_len), _ptr(_typed("new_len", new_len, "int32", (R,), dev)),
+        _ptr(_typed("free_blocks", free_blocks, "int32", (None,), dev)) or None,
+        _ptr(_typed("free_head", free_head, "int32", (1,), dev, True)),
+        _ptr(_typed("block_table", block_table, "int32", (R, None), dev)),
+        _ptr(_typed("slot_mapping_out", slot_mapping_out, "int64", (None,), dev)),
+        _ptr(_typed("positions_out", positions_out, "int32", (T,), dev, True)),
+        _ptr(_typed("token_start_out", token_start_out, "int32", (R + 1,), dev, True)),
+        _ptr(_typed("seq_len_out", seq_len_out, "int32", (R,), dev, True)),
+        _ptr(_typed("free_head_out", free_head_out, "int32", (1,), dev, True)),
+        _ptr(_typed("status_out", status_out, "int32", (1,), dev)))
+    return _prepared("is_extend_block_table", args, (seq_len, new_len, free_blocks, free_head, block_table,
+                                                     slot_mapping_out, positions_out, token_start_out, seq_len_out,
+                                                     free_head_out, status_out), stream, dev)
+
+
+def is_extend_block_table(*args, **kw) -> None:
+    """Blocks, slots and positions of a step's new tokens; arguments as in the
+    prepared form.  status_out (int32 [1]) collects the IS_ST_* bits."""
+    prepare_extend_block_table(*args, **kw)()
+
+
+def prepare_append(q, k, v, positions, slot_mapping, rope: RopeParams, cache: CacheDesc, layer_cache, q_out,
+                   status_out, axes: RopeAxes | None = None, stream=None):
+    """is_append with every argument marshalled once.  q [T][Hq][D], k and v
+    [T][H][D] may be views with any token stride (q and q_out None: keys and
+    values only); positions int32 [n_axes][T] or [T]; q_out may be q."""
+    axes = make_axes() if axes is None else axes
+    dt, code = _float_code("k", k)
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens][heads][head_dim]")
+    T, H, D = (int(n) for n in k.shape)
+    dev = _rows("k", k, dt).device
+    _rows("v", v, dt, (T, H, D), dev)
+    Hq = 0
+    if q is not None:
+        Hq = int(q.shape[1])
+        _rows("q", q, dt, (T, Hq, D), dev)
+        _typed("q_out", q_out, dt, (T, Hq, D), dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _typed("positions", positions, "int32", (T,) if axes.n_axes == 1 and positions.dim() == 1 else (axes.n_axes, T), dev)
+    _typed("slot_mapping", slot_mapping, "int64", (T,), dev)
+    _layer_cache(cache, layer_cache, H, D, dt, dev)
+    args = AppendArgs(T, Hq, H, D, code, 0, int(q.stride(0)) if Hq else 0, int(k.stride(0)), int(v.stride(0)),
+                      q.data_ptr() if Hq else None, k.data_ptr(), v.data_ptr(), _ptr(positions), _ptr(slot_mapping),
+                      _ptr(q_out) if Hq else None, _ptr(layer_cache),
+                      _ptr(_typed("status_out", status_out, "int32", (1,), dev)), rope, axes, cache, 0)
+    return _prepared("is_append", args, (q, k, v, positions, slot_mapping, layer_cache, q_out, status_out), stream, dev)
+
+
+def is_append(*args, **kw) -> None:
+    """Rotate a step's queries and keys and write its K/V; arguments as in the prepared form."""
+    prepare_append(*args, **kw)()
+
+
+def attend_workspace(device=None):
+    """A workspace tensor that is enough for every is_attend call on ``device``."""
+    import torch
+    return torch.empty(_lib.IS_ATTEND_WORKSPACE_BYTES, dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def prepare_attend(q, seq_len, block_table, cache: CacheDesc, layer_cache, out, workspace, status_out, q_start=None,
+                   max_q_len: int = 1, scale: float | None = None, window: int = 0, lse_out=None, stream=None):
+    """is_attend with every argument marshalled once.  q [T][Hq][D] may be a
+    view with any token stride; scale None: head_dim ** -0.5."""
+    dt, code = _float_code("q", q)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens][heads][head_dim]")
+    T, Hq, D = (int(n) for n in q.shape)
+    dev = _rows("q", q, dt).device
+    R = int(_typed("seq_len", seq_len, "int32", (None,), dev).shape[0])
+    _typed("block_table", block_table, "int32", (R, None), dev)
+    _typed("q_start", q_start, "int32", (R + 1,), dev, True)
+    H = int(layer_cache.shape[3]) if layer_cache.dim() == 5 else 0
+    _layer_cache(cache, layer_cache, H, D, dt, dev)
+    _typed("out", out, dt, (T, Hq, D), dev)
+    _typed("lse_out", lse_out, "float32", (T, Hq), dev, True)
+    _typed("workspace", workspace, "uint8", (None,), dev)
+    args = AttendArgs(R, T, int(max_q_len), Hq, H, D, code, int(block_table.shape[1]), int(window),
+                      float(D ** -0.5 if scale is None else scale), int(q.stride(0)), q.data_ptr(), _ptr(q_start),
+                      _ptr(seq_len), _ptr(block_table), _ptr(layer_cache), _ptr(out), _ptr(lse_out), _ptr(workspace),
+                      int(workspace.shape[0]), _ptr(_typed("status_out", status_out, "int32", (1,), dev)), cache, 0)
+    return _prepared("is_attend", args, (q, q_start, seq_len, block_table, layer_cache, out, lse_out, workspace,
+                                         status_out), stream, dev)
+
+
+def is_attend(*args, **kw) -> None:
+    """Attention of each request's last tokens over its paged cache; arguments as in the prepared form."""
+    prepare_attend(*args, **kw)()
 
 
 def is_get_status(store: Store, stream=None) -> int:

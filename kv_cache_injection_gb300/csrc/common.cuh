@@ -122,6 +122,51 @@ constexpr int kPoolCtrWords = kPoolCtrs * kCtrStride;
 constexpr int kDoneCtrWord = 2 * kPoolCtrWords;
 constexpr int kCtrBlockWords = kDoneCtrWord + kCtrStride;
 
+// Rotation frequencies (as RopeTurns) and the position axis of each pair.
+struct AxisTurns {
+  RopeTurns t;
+  uint8_t axis[kMaxHalfDim];
+};
+
+// is_append with its checks done.
+struct AppendArgs {
+  const uint8_t* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  int64_t q_stride, k_stride, v_stride;   // bytes between tokens
+  const int32_t* positions;     // [n_axes][T]
+  const int64_t* slots;         // [T]
+  uint8_t* q_out;
+  uint8_t* k_cache;             // the layer's K rows; the V rows follow v_offset bytes on
+  int64_t v_offset;
+  int64_t n_slots;              // num_blocks * block_size
+  uint32_t* status;
+  int32_t T, Hq, H, D;
+  int32_t n_axes;
+  int32_t dtype, style, fp8;
+  float k_inv, v_inv;           // FP8 cache: fp32(1 / k_scale), fp32(1 / v_scale)
+};
+
+// is_attend with its checks done.
+struct AttendArgs {
+  const uint8_t* q;
+  int64_t q_stride;             // bytes between rows
+  const int32_t* q_start;       // [R+1] or null
+  const int32_t* seq_len;       // [R]
+  const int32_t* block_table;   // [R][max_blocks]
+  const uint8_t* k_cache;       // the layer's K rows; the V rows follow v_offset bytes on
+  int64_t v_offset;
+  uint8_t* out;
+  float* lse;                   // or null
+  uint8_t* workspace;
+  uint32_t* status;
+  int32_t R, T, max_q, Hq, H, G, D, max_blocks, block_size, num_blocks;
+  int32_t window;               // 0: none
+  float scale;                  // softmax scale times the K scale of an FP8 cache
+  float v_scale;
+  int32_t dtype, fp8;
+};
+
 // Uniform bins of the cosine in [-1, 1] used by the top-k's first pass.
 constexpr int kCosBins = 2048;
 

@@ -8,6 +8,23 @@
 
 namespace isk {
 
+// Makes `dev` the current device for a scope.
+class DeviceGuard {
+ public:
+  explicit DeviceGuard(int dev) {
+    cudaGetDevice(&prev_);
+    if (prev_ != dev) cudaSetDevice(dev);
+  }
+  ~DeviceGuard() {
+    int cur = -1;
+    cudaGetDevice(&cur);
+    if (cur != prev_) cudaSetDevice(prev_);
+  }
+
+ private:
+  int prev_ = 0;
+};
+
 struct LaunchCfg {
   cudaStream_t stream;
   int num_sms;
@@ -71,6 +88,11 @@ cudaError_t launch_inject(const InjectArgs& a, const RopeTurns& turns, int kv_dt
 
 // Context-Window Encoding capture: the fact tokens' rows of one layer into the arena.
 cudaError_t launch_capture_layer(const CaptureArgs& a, const LaunchCfg& cfg);
+
+// The serving step around the segment (is_extend_block_table, is_append, is_attend).
+cudaError_t launch_extend(const is_extend_args_t& a, const LaunchCfg& cfg);
+cudaError_t launch_append(const AppendArgs& a, const AxisTurns& turns, const LaunchCfg& cfg);
+cudaError_t launch_attend(const AttendArgs& a, const LaunchCfg& cfg);
 
 // Whether a row of row_bytes (K or V of one layer) and R requests fit the
 // inject kernel's shared-memory plan.

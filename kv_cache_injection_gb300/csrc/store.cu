@@ -93,22 +93,6 @@ int dtype_bytes(int dt) { return dt == IS_F32 ? 4 : 2; }
 bool valid_kv_dtype(int dt) { return dt == IS_F32 || dt == IS_BF16 || dt == IS_F16; }
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
-class DeviceGuard {
- public:
-  explicit DeviceGuard(int dev) {
-    cudaGetDevice(&prev_);
-    if (prev_ != dev) cudaSetDevice(dev);
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    cudaGetDevice(&cur);
-    if (cur != prev_) cudaSetDevice(prev_);
-  }
-
- private:
-  int prev_ = 0;
-};
-
 struct EventPair {
   cudaEvent_t a, b;
 };
