@@ -1,105 +1,880 @@
-// Softmax attention of each request's last tokens over its paged cache (is_attend).
+// Softmax attention of each request's last tokens over its paged cache
+// (is_attend), for few query rows per request: one new token, or a handful.
 //
-// One warp per (query row, query head): the lanes split the head, the running
-// maximum m and sum l of the softmax rescale the output as keys come by.
+// With one new token every key and value is used once per query head of its
+// group, so the time is that of reading the cache: 2 * keys * H * D elements.
+// What the kernel is built around:
+//
+// - One item is a (request, KV head, tile of up to 8 * NT query rows), its
+//   rows being the query heads of the group for each new token; the keys and
+//   values are read once for all of them.
+// - The items' keys are numbered in units of kWarps * KT keys over the whole
+//   call and each CTA of a persistent grid takes one contiguous run of units,
+//   found from the lengths on the device: a long request is spread over many
+//   CTAs, short ones share one, whatever the batch looks like.  An item that
+//   crosses CTAs leaves an unnormalised partial (m, l, O) per CTA in the
+//   workspace and attend_join_kernel adds them up in CTA order, so results do
+//   not depend on timing.
+// - Inside a CTA every warp runs alone on its own tiles of KT keys, with its
+//   own cp.async ring in shared memory (no block barrier in the loop) and its
+//   own running maximum m, sum l and output O, joined once at the end.
+// - The tensor cores take the transposed products S^T = K Q^T and
+//   O^T = V^T P^T (mma.m16n8k16): the keys and the head dimension fill the
+//   16-row side and the query rows the 8-column side, so a group of 4 to 8
+//   query heads wastes little.  tcgen05 wants 128 (or 64) rows and gains
+//   nothing here: the products take a tenth of the time the loads take.
+// - The maximum moves only when a logit passes it by more than 2^8 (in the
+//   base-2 exponent): the weights stay below 2^8, far from overflow in bf16
+//   and fp16, and the usual tile costs one vote instead of a reduction.
+//
+// Sums, maxima and O are fp32; the weights are rounded to 16 bits for the
+// second product (relative 2^-8 or 2^-11, like the output).  FP8 keys and
+// values are exact in fp16, so that path computes in fp16, a bf16 query row
+// being scaled by a power of two into fp16's range (exact, undone in fp32).
+// fp32 caches use fp32 fused multiply-adds throughout.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
+#include "block_scan.cuh"
 #include "common.cuh"
 #include "internal.h"
 
 namespace isk {
 
-template <typename T> __device__ __forceinline__ float to_f(T x) { return (float)x; }
-__device__ __forceinline__ float e4m3_f(uint8_t x) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(x, __NV_E4M3)));
+constexpr int kWarps = 4;
+constexpr int kAttendThreads = kWarps * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.f;             // how far a logit may pass the maximum in use
+
+// ---- primitives ---------------------------------------------------------------
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <typename M>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (sizeof(M) == 2 && std::is_same<M, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two E4M3 bytes (the low half of x) as two fp16 values, exact.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(x));
+  return r;
 }
 
-template <typename T, bool F8>
-__global__ void __launch_bounds__(256) attend_rows_kernel(const AttendArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int h = (int)(w % a.Hq);
-  w /= a.Hq;
-  const int i = (int)(w % a.max_q), r = (int)(w / a.max_q);
-  if (r >= a.R) return;
-  const int64_t s0 = a.q_start ? a.q_start[r] : r, s1 = a.q_start ? a.q_start[r + 1] : r + 1;
-  const int seq = a.seq_len[r];
-  const int64_t n = s1 - s0;
+// ---- the batch ------------------------------------------------------------------
+
+// One request as the kernel sees it.
+struct Req {
+  int32_t row0, n;       // first query row, query rows
+  int32_t seq;           // tokens in the cache
+  int32_t kb, ke;        // positions some row may see
+};
+
+// Requests whose rows or length make no sense have no rows.
+__device__ __forceinline__ Req read_request(const AttendArgs& a, int r, bool report) {
+  Req q;
+  const int32_t s0 = a.q_start ? a.q_start[r] : r, s1 = a.q_start ? a.q_start[r + 1] : r + 1;
+  const int32_t seq = a.seq_len[r];
+  const int64_t n = (int64_t)s1 - s0;
   if (n < 0 || n > a.max_q || s0 < 0 || s1 > a.T || seq < 0 || seq > IS_MAX_POSITION) {
-    if (lane == 0) latch(a.status, IS_ST_COUNT);
-    return;
+    if (report) latch(a.status, IS_ST_COUNT);
+    q.row0 = q.n = q.seq = q.kb = q.ke = 0;
+    return q;
   }
-  if (i >= n) return;
-  const int64_t row = s0 + i;
-  const int p = seq - (int)n + i;
-  const int first = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  const int epl = a.D / 32;
-  float q[8], o[8];
-  const T* qp = reinterpret_cast<const T*>(a.q + row * a.q_stride) + (size_t)h * a.D;
+  q.row0 = s0;
+  q.n = (int32_t)n;
+  q.seq = seq;
+  const int64_t cap = (int64_t)a.max_blocks * a.block_size;
+  q.ke = (int32_t)min((int64_t)seq, cap);
+  if (report && n > 0 && q.ke < seq) latch(a.status, IS_ST_BLOCK_TABLE);
+  q.kb = a.window > 0 ? max(0, (int32_t)max((int64_t)seq - n - a.window + 1, (int64_t)0)) : 0;
+  if (q.kb > q.ke) q.kb = q.ke;
+  return q;
+}
+
+// Item tables of a request: tiles of `rows` query rows, units of `unit` keys.
+__device__ __forceinline__ int32_t tiles_of(const AttendArgs& a, const Req& q, int rows) {
+  return (q.n * a.G + rows - 1) / rows;
+}
+__device__ __forceinline__ int32_t units_of(const Req& q, int unit) { return max(1, (q.ke - q.kb + unit - 1) / unit); }
+
+// ---- workspace -------------------------------------------------------------------
+// [ctas] join records, then two partials per CTA: of the item its run begins
+// in (slot 2 c) and of the one it ends in (2 c + 1), when those cross its ends.
+struct JoinRecord {
+  int32_t parts;         // 0: nothing to join
+  int32_t slot0;         // the first part; part i > 0 is slot 2 * (cta + i)
+  int32_t row0, n;       // of the request
+  int32_t head, tile;    // KV head, row tile
+};
+constexpr size_t kRecordBytes = 32;
+constexpr int kMaxCtas = 1024;
+template <int ROWS, int D>
+struct Partial {
+  float o[ROWS][D];
+  float m[ROWS], l[ROWS];
+};
+
+__device__ __forceinline__ JoinRecord* record_of(const AttendArgs& a, int cta) {
+  return reinterpret_cast<JoinRecord*>(a.workspace + (size_t)cta * kRecordBytes);
+}
+template <int ROWS, int D>
+__device__ __forceinline__ Partial<ROWS, D>* partial_of(const AttendArgs& a, int slot) {
+  return reinterpret_cast<Partial<ROWS, D>*>(a.workspace + (size_t)kMaxCtas * kRecordBytes) + slot;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_out(const AttendArgs& a, const Req& q, int head, int rho, int d, float x, float y) {
+  const int tok = rho / a.G;
+  T* p = reinterpret_cast<T*>(a.out) + ((size_t)(q.row0 + tok) * a.Hq + (size_t)head * a.G + (rho - tok * a.G)) * a.D + d;
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float2*>(p) = make_float2(x, y);
+  else
+    *reinterpret_cast<uint32_t*>(p) = Vec<T>::pack2(x, y);
+}
+__device__ __forceinline__ void store_lse(const AttendArgs& a, const Req& q, int head, int rho, float m, float l) {
+  if (!a.lse) return;
+  const int tok = rho / a.G;
+  a.lse[(size_t)(q.row0 + tok) * a.Hq + (size_t)head * a.G + (rho - tok * a.G)] =
+      l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// ---- tile engines -------------------------------------------------------------------
+// An engine holds one warp's share of an item: the query rows, m, l and O.
+//   kRows rows, kKeys keys a tile, kRowBytes bytes of a K or V row in shared memory
+//   begin   loads the query rows
+//   step    adds one tile (K rows at ks, V rows at vs, swizzled 16-byte chunks)
+//   finish  writes O to so[kRows][kPitch] and (m, l) to sm[2 kRows]
+
+// Which keys of a tile which rows see.
+struct TileMask {
+  int key0;              // position of the tile's first key
+  uint32_t valid;        // keys that are read (in range and named by the table)
+  bool check;            // some row does not see some valid key, or a key is not valid
+};
+
+// 16-byte chunk c of row `row`: rows of 128 bytes or more rotate their chunks
+// by the row so that eight rows' chunks of one column lie in different banks;
+// rows of 64 bytes, two to a line, by half the row.
+template <int ROWB>
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+  return (uint32_t)row * ROWB + (uint32_t)((ROWB >= 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) * 16);
+}
+
+template <typename T, bool F8, int D_, int NT>
+struct MmaEngine {
+  static constexpr int D = D_;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kRowBytes = F8 ? D : 2 * D;
+  static constexpr int kKeys = kRowBytes >= 256 ? 16 : 32;
+  static constexpr int kMt = kKeys / 16;
+  static constexpr int kPitch = D + 4;
+  static constexpr int kSharedQ = 0;
+  using M = typename std::conditional<F8, __half, T>::type;   // type of the products' operands
+
+  uint32_t q[D / 16][NT][2];
+  float o[D / 16][NT][4];
+  float m[NT][2], l[NT][2], sc[NT][2];
+  int lim[NT][2];        // last position the row sees; -1 and below: none
+
+  __device__ __forceinline__ void begin(const AttendArgs& a, const Req& rq, int head, int tile, float*) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    q[e] = e < epl ? to_f(qp[lane * epl + e]) : 0.f;
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  const float c = a.scale * 1.4426950408889634f;
-  for (int j = first; j <= p; ++j) {
-    const int b = j / a.block_size;
-    if (b >= a.max_blocks) {
-      if (lane == 0) latch(a.status, IS_ST_BLOCK_TABLE);
-      break;
-    }
-    const int id = a.block_table[(size_t)r * a.max_blocks + b];
-    if (id < 0 || id >= a.num_blocks) {
-      if (lane == 0) latch(a.status, IS_ST_BLOCK_ID);
-      continue;
-    }
-    const size_t at = (((size_t)id * a.block_size + (j - b * a.block_size)) * a.H + h / a.G) * a.D + lane * epl;
-    float k[8], v[8], s = 0.f;
+    for (int nt = 0; nt < NT; ++nt) {
+      const int rho = tile * kRows + nt * 8 + (lane >> 2), tok = rho / a.G;
+      const bool in = tok < rq.n;
+      const T* src = reinterpret_cast<const T*>(a.q + (int64_t)(rq.row0 + (in ? tok : 0)) * a.q_stride) +
+                     ((size_t)head * a.G + (in ? rho - tok * a.G : 0)) * D;
+      int shift = 0;
+      if (F8 && !std::is_same<T, __half>::value) {
+        // bf16 to fp16: scale the row by a power of two that brings its largest element to [2^14, 2^15)
+        float big = 0.f;
+        uint32_t raw[D / 16][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (e < epl) {
-        if (F8) {
-          k[e] = e4m3_f(a.k_cache[at + e]);
-          v[e] = e4m3_f(a.k_cache[a.v_offset + at + e]);
-        } else {
-          k[e] = to_f(reinterpret_cast<const T*>(a.k_cache)[at + e]);
-          v[e] = to_f(reinterpret_cast<const T*>(a.k_cache + a.v_offset)[at + e]);
+        for (int c = 0; c < D / 16; ++c) {
+          const uint2 w = in ? *reinterpret_cast<const uint2*>(src + 16 * c + 4 * t) : make_uint2(0, 0);
+          raw[c][0] = w.x;
+          raw[c][1] = w.y;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(raw[c][i] << 16)), fabsf(__uint_as_float(raw[c][i] & 0xffff0000u))));
         }
-        s = fmaf(q[e], k[e], s);
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        if (big > 0.f && big < INFINITY) shift = min(14 - (int)(((__float_as_uint(big) >> 23) & 255u) - 127), 120);
+        const float f = __uint_as_float((uint32_t)(shift + 127) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            q[c][nt][i] = Vec<__half>::pack2(__uint_as_float(raw[c][i] << 16) * f, __uint_as_float(raw[c][i] & 0xffff0000u) * f);
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          if (F8) {        // four consecutive elements: see the key fragments in step()
+            const uint2 w = in ? *reinterpret_cast<const uint2*>(src + 16 * c + 4 * t) : make_uint2(0, 0);
+            q[c][nt][0] = w.x;
+            q[c][nt][1] = w.y;
+          } else {
+            q[c][nt][0] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * c + 2 * t) : 0u;
+            q[c][nt][1] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * c + 2 * t + 8) : 0u;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {      // the columns of S^T this lane holds: rows 2 t and 2 t + 1
+        const int col = nt * 8 + 2 * t + i, ctok = (tile * kRows + col) / a.G;
+        lim[nt][i] = ctok < rq.n ? rq.seq - rq.n + ctok : -1;
+        m[nt][i] = -INFINITY;
+        l[nt][i] = 0.f;
+        const int sh = F8 ? __shfl_sync(0xffffffffu, shift, (2 * t + i) * 4) : 0;
+        sc[nt][i] = a.scale * kLog2e * (F8 ? __uint_as_float((uint32_t)(127 - sh) << 23) : 1.f);
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][nt][e] = 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void step(const AttendArgs& a, uint32_t ks, uint32_t vs, const TileMask& tm, float*) {
+    const int lane = threadIdx.x & 31;
+    float s[kMt][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+    // S^T.  ldmatrix lane i addresses row (i & 7) of 8x8 matrix i >> 3.
+    const int mrow = lane & 7, mat = lane >> 3;
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt) {
+      const int row = mt * 16 + (mat & 1) * 8 + mrow;
+      if constexpr (!F8) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t k[4];
+          ldmatrix4(ks + chunk_at<kRowBytes>(row, 2 * c + (mat >> 1)), k);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<M>(s[mt][nt], k, q[c][nt][0], q[c][nt][1]);
+        }
+      } else {
+        // A chunk holds 16 elements; lane t of a row gets elements 4 t .. 4 t + 3, which stand in for the
+        // product's k = 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (the query fragment uses the same order).
+#pragma unroll
+        for (int c = 0; c < D / 16; c += 2) {
+          uint32_t b[4];
+          ldmatrix4(ks + chunk_at<kRowBytes>(row, c + (mat >> 1)), b);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t lo = b[2 * u], hi = b[2 * u + 1];
+            const uint32_t k[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(hi), e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<M>(s[mt][nt], k, q[c + u][nt][0], q[c + u][nt][1]);
+          }
+        }
+      }
+    }
+    // Scaled logits (base 2), hidden keys at -inf.
+    bool over = false;
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[mt][nt][e] * sc[nt][e & 1];
+          if (tm.check) {
+            const int key = mt * 16 + (lane >> 2) + (e >> 1) * 8, j = tm.key0 + key;
+            const bool see = ((tm.valid >> key) & 1u) && j <= lim[nt][e & 1] &&
+                             (a.window == 0 || j > lim[nt][e & 1] - a.window);
+            if (!see) x = -INFINITY;
+          }
+          s[mt][nt][e] = x;
+          over |= x > m[nt][e & 1] + kLazy;
+        }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < kMt; ++mt) x = fmaxf(x, fmaxf(s[mt][nt][i], s[mt][nt][i + 2]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float mn = fmaxf(m[nt][i], x);
+          const float f = mn == -INFINITY ? 1.f : ex2(m[nt][i] - mn);
+          m[nt][i] = mn;
+          l[nt][i] *= f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            o[c][nt][i] *= f;
+            o[c][nt][i + 2] *= f;
+          }
+        }
+    }
+    uint32_t p[kMt][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt) {
+        const float p0 = ex2(s[mt][nt][0] - m0), p1 = ex2(s[mt][nt][1] - m1);
+        const float p2 = ex2(s[mt][nt][2] - m0), p3 = ex2(s[mt][nt][3] - m1);
+        l[nt][0] += p0 + p2;
+        l[nt][1] += p1 + p3;
+        // [key][row] pairs to the product's [row][key] pairs
+        p[mt][nt][0] = movmatrix_t(Vec<M>::pack2(p0, p1));
+        p[mt][nt][1] = movmatrix_t(Vec<M>::pack2(p2, p3));
+      }
+    }
+    // O^T += V^T P^T
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt) {
+      if constexpr (!F8) {
+        const int row = mt * 16 + (mat >> 1) * 8 + mrow;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t v[4];
+          ldmatrix4_t(vs + chunk_at<kRowBytes>(row, 2 * c + (mat & 1)), v);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<M>(o[c][nt], v, p[mt][nt][0], p[mt][nt][1]);
+        }
+      } else {
+        // A transposed 16-bit unit is a pair of elements (2 i, 2 i + 1) of one key; two keys' pairs are
+        // regrouped by element: output rows 0-7 are the chunk's even elements, rows 8-15 the odd ones.
+        const int row = mt * 16 + (mat & 1) * 8 + mrow;
+#pragma unroll
+        for (int c = 0; c < D / 16; c += 2) {
+          uint32_t b[4];
+          ldmatrix4_t(vs + chunk_at<kRowBytes>(row, c + (mat >> 1)), b);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t lo = __byte_perm(b[2 * u], 0, 0x3120), hi = __byte_perm(b[2 * u + 1], 0, 0x3120);
+            const uint32_t v[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi), e4m3x2_f16x2(hi >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<M>(o[c + u][nt], v, p[mt][nt][0], p[mt][nt][1]);
+          }
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void finish(float* so, float* sm) {
+    const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = l[nt][i];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        const int row = nt * 8 + 2 * t + i;
+        if (g == 0) {
+          sm[row] = m[nt][i];
+          sm[kRows + row] = x;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          so[row * kPitch + 16 * c + (F8 ? 2 * g : g)] = o[c][nt][i];
+          so[row * kPitch + 16 * c + (F8 ? 2 * g + 1 : g + 8)] = o[c][nt][i + 2];
+        }
+      }
+  }
+};
+
+// fp32: for the logits a lane has one key and kPer of the 8 rows, for the
+// output a 16-byte chunk of the head; the weights change hands through shared
+// memory.
+template <int D_>
+struct FmaEngine {
+  static constexpr int D = D_;
+  static constexpr int kRows = 8;
+  static constexpr int kRowBytes = 4 * D;
+  static constexpr int kKeys = D >= 128 ? 8 : 16;
+  static constexpr int kPitch = D + 4;
+  static constexpr int kSharedQ = kRows * D + kWarps * (kKeys * kRows + kRows);   // floats: q, then each warp's weights and factors
+  static constexpr int kPer = kRows * kKeys / 32;
+  static constexpr int kLaneChunks = D / 4 >= 32 ? D / 128 : 1;
+  static constexpr int kGroups = D / 4 >= 32 ? 1 : 32 / (D / 4);   // lanes sharing a chunk, each with its keys
+
+  float o[kRows][kLaneChunks * 4];
+  float m[kPer], l[kPer], sc;
+  int lim[kPer];
+
+  __device__ __forceinline__ void begin(const AttendArgs& a, const Req& rq, int head, int tile, float* sq) {
+    for (int i = threadIdx.x; i < kRows * D / 4; i += kAttendThreads) {
+      const int rho = tile * kRows + i / (D / 4), tok = rho / a.G;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (tok < rq.n)
+        x = *reinterpret_cast<const float4*>(a.q + (int64_t)(rq.row0 + tok) * a.q_stride +
+                                             (((size_t)head * a.G + (rho - tok * a.G)) * D + (i % (D / 4)) * 4) * 4);
+      reinterpret_cast<float4*>(sq)[i] = x;
+    }
+    __syncthreads();
+    const int part = (threadIdx.x & 31) / kKeys;
+    sc = a.scale * kLog2e;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int tok = (tile * kRows + part * kPer + i) / a.G;
+      lim[i] = tok < rq.n ? rq.seq - rq.n + tok : -1;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int e = 0; e < kLaneChunks * 4; ++e) o[r][e] = 0.f;
+  }
+
+  __device__ __forceinline__ void step(const AttendArgs& a, uint32_t ks, uint32_t vs, const TileMask& tm, float* sq) {
+    const int lane = threadIdx.x & 31, key = lane % kKeys, part = lane / kKeys;
+    float* sp = sq + kRows * D + (threadIdx.x >> 5) * (kKeys * kRows + kRows);   // [key][row]
+    float* sf = sp + kKeys * kRows;
+    float s[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s[i] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 4; ++c) {
+      float k[4];
+      Vec<float>::unpack(ld_shared_v4(ks + chunk_at<kRowBytes>(key, c)), k);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float4 q = reinterpret_cast<const float4*>(sq)[(part * kPer + i) * (D / 4) + c];
+        s[i] = fmaf(q.x, k[0], fmaf(q.y, k[1], fmaf(q.z, k[2], fmaf(q.w, k[3], s[i]))));
+      }
+    }
+    bool over = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      s[i] *= sc;
+      const int j = tm.key0 + key;
+      if (tm.check && !(((tm.valid >> key) & 1u) && j <= lim[i] && (a.window == 0 || j > lim[i] - a.window))) s[i] = -INFINITY;
+      over |= s[i] > m[i] + kLazy;
+    }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        float x = s[i];
+#pragma unroll
+        for (int d = kKeys / 2; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        const float mn = fmaxf(m[i], x);
+        const float f = mn == -INFINITY ? 1.f : ex2(m[i] - mn);
+        m[i] = mn;
+        l[i] *= f;
+        if (key == 0) sf[part * kPer + i] = f;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float f = sf[r];
+#pragma unroll
+        for (int e = 0; e < kLaneChunks * 4; ++e) o[r][e] *= f;
       }
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= c;
-    const float m1 = fmaxf(m, s);
-    const float base = m1 == -INFINITY ? 0.f : m1;
-    const float f = exp2f(m - base), w1 = exp2f(s - base);
-    l = l * f + w1;
+    for (int i = 0; i < kPer; ++i) {
+      const float p = ex2(s[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+      l[i] += p;
+      sp[key * kRows + part * kPer + i] = p;
+    }
+    __syncwarp();
+    const int chunk = kGroups > 1 ? lane % (D / 4) : lane, group = kGroups > 1 ? lane / (D / 4) : 0;
+#pragma unroll 4
+    for (int kk = 0; kk < kKeys / kGroups; ++kk) {
+      const int row = group * (kKeys / kGroups) + kk;
+      const float4 w0 = *reinterpret_cast<const float4*>(sp + row * kRows), w1 = *reinterpret_cast<const float4*>(sp + row * kRows + 4);
+      const float w[kRows] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < epl) o[e] = o[e] * f + w1 * v[e];
-    m = m1;
+      for (int u = 0; u < kLaneChunks; ++u) {
+        float v[4];
+        Vec<float>::unpack(ld_shared_v4(vs + chunk_at<kRowBytes>(row, chunk + 32 * u)), v);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[r][u * 4 + e] = fmaf(w[r], v[e], o[r][u * 4 + e]);
+      }
+    }
+    __syncwarp();                        // the weights are read before the next tile's are written
   }
-  T* out = reinterpret_cast<T*>(a.out) + ((size_t)row * a.Hq + h) * a.D + lane * epl;
-  const float inv = l == 0.f ? 0.f : a.v_scale / l;
+
+  __device__ __forceinline__ void finish(float* so, float* sm) {
+    const int lane = threadIdx.x & 31, part = lane / kKeys;
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < epl) out[e] = T(l == 0.f ? 0.f : o[e] * inv);
-  if (a.lse && lane == 0)
-    a.lse[(size_t)row * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    for (int i = 0; i < kPer; ++i) {
+      float x = l[i];
+#pragma unroll
+      for (int d = kKeys / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      if (lane % kKeys == 0) {
+        sm[part * kPer + i] = m[i];
+        sm[kRows + part * kPer + i] = x;
+      }
+    }
+    const int chunk = kGroups > 1 ? lane % (D / 4) : lane;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int e = 0; e < kLaneChunks * 4; ++e) {
+        float x = o[r][e];
+#pragma unroll
+        for (int d = D / 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        if (lane < D / 4 || kGroups == 1) so[r * kPitch + (chunk + 32 * (e / 4)) * 4 + (e & 3)] = x;
+      }
+  }
+};
+
+// ---- the split kernel ----------------------------------------------------------------
+
+template <class E>
+struct SplitShape {
+  static constexpr int kUnit = kWarps * E::kKeys;                     // keys of a unit
+  static constexpr int kTileBytes = 2 * E::kKeys * E::kRowBytes;      // K and V of a tile
+  static constexpr int kStages = 24576 / kTileBytes >= 3 ? 24576 / kTileBytes : 3;
+  static constexpr int kWarpBytes = kStages * kTileBytes;
+  static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes + (size_t)E::kSharedQ * 4;
+  static constexpr int kPerSm = 2 * (kSmem + 2048) <= 227 * 1024 ? 2 : 1;
+  static_assert(kSmem + 2048 <= 227 * 1024, "a CTA fits an SM");
+  static_assert(kWarpBytes >= E::kRows * E::kPitch * 4, "a warp's output is joined in its ring");
+};
+constexpr int kMinUnits = 4;             // units of a CTA's run, at least
+
+template <typename T, class E>
+__global__ void __launch_bounds__(kAttendThreads) attend_split_kernel(const AttendArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  using S = SplitShape<E>;
+  constexpr int ROWS = E::kRows, D = E::D, KT = E::kKeys, PITCH = E::kPitch;
+  __shared__ int64_t scratch[33];
+  __shared__ int64_t s_base;
+  __shared__ int32_t s_req;
+  __shared__ float s_ml[kWarps][2 * ROWS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* sq = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);
+  pdl_wait();
+  pdl_trigger();
+
+  // This CTA's run of units.
+  const int per = (a.R + kAttendThreads - 1) / kAttendThreads;
+  const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const Req q = read_request(a, r, blockIdx.x == 0);
+    mine += (int64_t)a.H * tiles_of(a, q, ROWS) * units_of(q, S::kUnit);
+  }
+  int64_t total;
+  int64_t at = block_exclusive_scan(mine, scratch, &total);
+  const int64_t run = max((int64_t)kMinUnits, (total + gridDim.x - 1) / gridDim.x);
+  int64_t u = (int64_t)blockIdx.x * run;
+  const int64_t u_first = u, u_end = min(total, u + run);
+  if (u >= u_end) {
+    if (tid == 0) record_of(a, blockIdx.x)->parts = 0;
+    return;
+  }
+  if (at <= u && u < at + mine) {
+    for (int r = r0; r < r1; ++r) {
+      const Req q = read_request(a, r, false);
+      const int64_t n = (int64_t)a.H * tiles_of(a, q, ROWS) * units_of(q, S::kUnit);
+      if (u < at + n) {
+        s_req = r;
+        s_base = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  int r = s_req;
+  int64_t base = s_base;                 // first unit of request r
+  bool crossed = false;                  // the last item goes on in the next CTA, and began here
+
+  const uint32_t ring = smem_addr(smem) + warp * S::kWarpBytes;
+  float* so = reinterpret_cast<float*>(smem + warp * S::kWarpBytes);
+  const int64_t token_bytes = (int64_t)a.H * E::kRowBytes;
+
+  while (u < u_end) {
+    Req q = read_request(a, r, false);
+    const int tiles = tiles_of(a, q, ROWS), units = units_of(q, S::kUnit);
+    if (u >= base + (int64_t)a.H * tiles * units) {
+      base += (int64_t)a.H * tiles * units;
+      ++r;
+      continue;
+    }
+    const int item = (int)((u - base) / units);
+    const int head = item / tiles, tile = item - head * tiles;
+    const int64_t item0 = base + (int64_t)item * units;
+    const int ua = (int)(u - item0);
+    const int ub = (int)min((int64_t)units, u_end - item0);
+    const bool whole = ua == 0 && ub == units;
+    // Keys of this segment that some row of the tile sees.
+    const int last_tok = min(q.n - 1, (tile * ROWS + ROWS - 1) / a.G), first_tok = tile * ROWS / a.G;
+    const int p_first = q.seq - q.n + first_tok, p_last = q.seq - q.n + last_tok;
+    const int k_lo = q.kb + ua * S::kUnit;
+    const int k_hi = min(min(q.ke, p_last + 1), q.kb + ub * S::kUnit);
+
+    E e;
+    e.begin(a, q, head, tile, sq);
+    const int n_tiles = k_hi > k_lo ? (k_hi - k_lo + KT - 1) / KT : 0;
+    const int n_mine = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
+    const int32_t* table = a.block_table + (size_t)r * a.max_blocks;
+    const uint8_t* kbase = a.k_cache + (size_t)head * E::kRowBytes;
+
+    // Lane i < KT looks up key i of a tile, one tile ahead of its loads.
+    int32_t id_next = 0, off_next = 0;
+    auto look_up = [&](int i) {
+      const int j = k_lo + (warp + i * kWarps) * KT + lane;
+      id_next = -1;
+      if (i < n_mine && lane < KT && j < k_hi) {
+        const int b = j / a.block_size;
+        off_next = j - b * a.block_size;
+        id_next = table[b];
+        if (id_next < 0 || id_next >= a.num_blocks) {
+          latch(a.status, IS_ST_BLOCK_ID);
+          id_next = -1;
+        }
+      }
+    };
+    uint32_t valid_of[S::kStages];
+    auto issue = [&](int i, int stage) {
+      uint32_t valid = 0;
+      if (i < n_mine) {
+        const long long off = id_next < 0 ? -1ll : ((long long)id_next * a.block_size + off_next) * token_bytes;
+        valid = __ballot_sync(0xffffffffu, off >= 0);
+        look_up(i + 1);
+        constexpr int CPR = E::kRowBytes / 16;             // chunks of a row
+        constexpr int RPI = CPR >= 32 ? 1 : 32 / CPR;      // rows of one pass of the warp
+        constexpr int PASS = CPR >= 32 ? CPR / 32 : 1;     // passes of one row
+        const uint32_t kd = ring + stage * S::kTileBytes, vd = kd + KT * E::kRowBytes;
+#pragma unroll
+        for (int x = 0; x < KT; x += RPI) {
+          const int row = x + (RPI > 1 ? lane / CPR : 0);
+          const long long o = __shfl_sync(0xffffffffu, off, row);
+          const bool in = o >= 0;
+#pragma unroll
+          for (int y = 0; y < PASS; ++y) {
+            const int c = (RPI > 1 ? lane % CPR : lane) + 32 * y;
+            const uint8_t* src = kbase + (in ? o : 0) + c * 16;
+            const uint32_t dst = chunk_at<E::kRowBytes>(row, c);
+            cp_async16(kd + dst, src, in);
+            cp_async16(vd + dst, src + a.v_offset, in);
+          }
+        }
+      }
+      cp_async_commit();
+      return valid;
+    };
+    look_up(0);
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) valid_of[s] = issue(s, s);
+    valid_of[S::kStages - 1] = 0;
+    for (int i0 = 0; i0 < n_mine; i0 += S::kStages) {
+#pragma unroll
+      for (int s = 0; s < S::kStages; ++s) {
+        const int i = i0 + s;
+        if (i < n_mine) {
+          cp_async_wait<S::kStages - 2>();
+          __syncwarp();                  // every lane's part of tile i has landed, and all are done with tile i - 1
+          const uint32_t valid = valid_of[s];
+          valid_of[(s + S::kStages - 1) % S::kStages] = issue(i + S::kStages - 1, (s + S::kStages - 1) % S::kStages);
+          TileMask tm;
+          tm.key0 = k_lo + (warp + i * kWarps) * KT;
+          tm.valid = valid;
+          constexpr uint32_t kFull = KT == 32 ? 0xffffffffu : (1u << KT) - 1u;
+          tm.check = valid != kFull || tm.key0 + KT - 1 > p_first || (a.window > 0 && tm.key0 <= p_last - a.window);
+          const uint32_t kd = ring + s * S::kTileBytes;
+          e.step(a, kd, kd + KT * E::kRowBytes, tm, sq);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+    e.finish(so, s_ml[warp]);
+    __syncthreads();
+
+    // Join the warps.  Every thread takes pairs of elements.
+    const int rho0 = tile * ROWS, rows = min(ROWS, q.n * a.G - rho0);
+    Partial<ROWS, D>* part = whole ? nullptr : partial_of<ROWS, D>(a, 2 * blockIdx.x + (u == u_first ? 0 : 1));
+    const float* all = reinterpret_cast<const float*>(smem);
+    for (int x = tid; x < rows * (D / 2); x += kAttendThreads) {
+      const int row = x / (D / 2), d = (x % (D / 2)) * 2;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_ml[w][row]);
+      const float m0 = mx == -INFINITY ? 0.f : mx;
+      float ox = 0.f, oy = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(s_ml[w][row] - m0);
+        const float2 v = *reinterpret_cast<const float2*>(all + (size_t)w * (S::kWarpBytes / 4) + row * PITCH + d);
+        ox = fmaf(f, v.x, ox);
+        oy = fmaf(f, v.y, oy);
+        l = fmaf(f, s_ml[w][ROWS + row], l);
+      }
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : a.v_scale / l;
+        store_out<T>(a, q, head, rho0 + row, d, l == 0.f ? 0.f : ox * inv, l == 0.f ? 0.f : oy * inv);
+        if (d == 0) store_lse(a, q, head, rho0 + row, mx, l);
+      } else {
+        *reinterpret_cast<float2*>(&part->o[row][d]) = make_float2(ox, oy);
+        if (d == 0) {
+          part->m[row] = mx;
+          part->l[row] = l;
+        }
+      }
+    }
+    if (!whole && ua == 0 && tid == 0) {
+      // The item begins here and ends in a later CTA: this CTA's record names its parts.
+      JoinRecord* rec = record_of(a, blockIdx.x);
+      rec->parts = (int32_t)((item0 + units - 1) / run - blockIdx.x) + 1;
+      rec->slot0 = 2 * blockIdx.x + (u == u_first ? 0 : 1);
+      rec->row0 = q.row0;
+      rec->n = q.n;
+      rec->head = head;
+      rec->tile = tile;
+    }
+    crossed = !whole && ua == 0;
+    u = item0 + ub;
+    __syncthreads();                     // the ring and s_ml are free again
+  }
+  if (!crossed && tid == 0) record_of(a, blockIdx.x)->parts = 0;
+}
+
+// Adds up the parts of an item that several CTAs worked on: one CTA per
+// (record, row), the threads splitting the parts and the head dimension.
+constexpr int kJoinThreads = 256;
+
+template <typename T, int ROWS, int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a) {
+  constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
+  __shared__ float4 s_o[GROUPS][LANES];
+  __shared__ float s_m[GROUPS], s_l[GROUPS];
+  pdl_wait();
+  pdl_trigger();
+  const int cta = blockIdx.x, row = blockIdx.y;
+  const JoinRecord rec = *record_of(a, cta);
+  if (rec.parts == 0 || rec.tile * ROWS + row >= rec.n * a.G) return;
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = group; i < rec.parts; i += GROUPS) {
+    const Partial<ROWS, D>* p = partial_of<ROWS, D>(a, i == 0 ? rec.slot0 : 2 * (cta + i));
+    const float pm = p->m[row], pl = p->l[row];
+    const float4 v = *reinterpret_cast<const float4*>(&p->o[row][lane * 4]);
+    const float mn = fmaxf(m, pm), mz = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - mz), g = ex2(pm - mz);
+    o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
+    l = l * f + pl * g;
+    m = mn;
+  }
+  s_o[group][lane] = o;
+  if (lane == 0) {
+    s_m[group] = m;
+    s_l[group] = l;
+  }
+  __syncthreads();
+  if (group != 0) return;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) mx = fmaxf(mx, s_m[g]);
+  const float mz = mx == -INFINITY ? 0.f : mx;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  l = 0.f;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    const float f = ex2(s_m[g] - mz);
+    const float4 v = s_o[g][lane];
+    o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
+    l = fmaf(f, s_l[g], l);
+  }
+  Req q;
+  q.row0 = rec.row0;
+  q.n = rec.n;
+  const float inv = l == 0.f ? 0.f : a.v_scale / l;
+  if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int rho = rec.tile * ROWS + row;
+  store_out<T>(a, q, rec.head, rho, lane * 4, o.x * inv, o.y * inv);
+  store_out<T>(a, q, rec.head, rho, lane * 4 + 2, o.z * inv, o.w * inv);
+  if (lane == 0) store_lse(a, q, rec.head, rho, mx, l);
+}
+
+// ---- host side -----------------------------------------------------------------------
+
+template <typename T, class E>
+static cudaError_t launch_split(const AttendArgs& a, const LaunchCfg& cfg) {
+  using S = SplitShape<E>;
+  auto* kern = attend_split_kernel<T, E>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
+  if (e != cudaSuccess) return e;
+  static_assert(kMaxCtas * (kRecordBytes + 2 * sizeof(Partial<E::kRows, E::D>)) <= IS_ATTEND_WORKSPACE_BYTES,
+                "the workspace holds every partial");
+  // As many CTAs as the SMs hold; fewer when the table's reach shows that there are fewer runs.
+  const int64_t keys = (int64_t)a.max_blocks * a.block_size;
+  const int64_t units = std::max<int64_t>(1, (std::min<int64_t>(keys, IS_MAX_POSITION) + S::kUnit - 1) / S::kUnit);
+  const int64_t items = (int64_t)a.R * a.H * ((a.max_q * (int64_t)a.G + E::kRows - 1) / E::kRows);
+  const int64_t runs = (items * units + kMinUnits - 1) / kMinUnits;
+  const int grid = (int)std::min<int64_t>(std::min<int64_t>(runs, (int64_t)S::kPerSm * cfg.num_sms), kMaxCtas);
+  e = launch_ex(kern, dim3(grid), dim3(kAttendThreads), S::kSmem, cfg.stream, cfg.pdl, a);
+  if (e != cudaSuccess) return e;
+  return launch_ex(attend_join_kernel<T, E::kRows, E::D>, dim3(grid, E::kRows), dim3(kJoinThreads), 0, cfg.stream,
+                   cfg.pdl, a);
+}
+
+template <typename T, bool F8>
+static cudaError_t launch_mma(const AttendArgs& a, const LaunchCfg& cfg) {
+  // Two column tiles when a request has more than 8 rows: the keys are then
+  // read once for 16 rows.  At head_dim 256 their output would not fit the registers.
+  const bool two = (int64_t)a.max_q * a.G > 8;
+  if (a.D == 64)
+    return two ? launch_split<T, MmaEngine<T, F8, 64, 2>>(a, cfg) : launch_split<T, MmaEngine<T, F8, 64, 1>>(a, cfg);
+  if (a.D == 128)
+    return two ? launch_split<T, MmaEngine<T, F8, 128, 2>>(a, cfg) : launch_split<T, MmaEngine<T, F8, 128, 1>>(a, cfg);
+  return launch_split<T, MmaEngine<T, F8, 256, 1>>(a, cfg);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, const LaunchCfg& cfg) {
-  const int64_t warps = (int64_t)a.R * a.max_q * a.Hq;
-  const int64_t blocks = (warps + 7) / 8;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  auto* kern = a.dtype == IS_F32 ? attend_rows_kernel<float, false>
-             : a.dtype == IS_BF16 ? (a.fp8 ? attend_rows_kernel<__nv_bfloat16, true> : attend_rows_kernel<__nv_bfloat16, false>)
-                                  : (a.fp8 ? attend_rows_kernel<__half, true> : attend_rows_kernel<__half, false>);
-  return launch_ex(kern, dim3((unsigned)blocks), dim3(256), 0, cfg.stream, cfg.pdl, a);
+  if (a.dtype == IS_BF16)
+    return a.fp8 ? launch_mma<__nv_bfloat16, true>(a, cfg) : launch_mma<__nv_bfloat16, false>(a, cfg);
+  if (a.dtype == IS_F16) return a.fp8 ? launch_mma<__half, true>(a, cfg) : launch_mma<__half, false>(a, cfg);
+  if (a.D == 64) return launch_split<float, FmaEngine<64>>(a, cfg);
+  if (a.D == 128) return launch_split<float, FmaEngine<128>>(a, cfg);
+  return launch_split<float, FmaEngine<256>>(a, cfg);
 }
 
 }  // namespace isk
