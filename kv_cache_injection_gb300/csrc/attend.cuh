@@ -1,0 +1,171 @@
+// What the kernels of is_attend share: the batch as they see it, the workspace
+// and the join of an item's parts.
+#pragma once
+
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace isk {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.f;             // how far a logit may pass the maximum in use
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two E4M3 bytes (the low half of x) as two fp16 values, exact.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// ---- the batch ------------------------------------------------------------------
+
+// One request as the kernel sees it.
+struct Req {
+  int32_t row0, n;       // first query row, query rows
+  int32_t seq;           // tokens in the cache
+  int32_t kb, ke;        // positions some row may see
+};
+
+// Requests whose rows or length make no sense have no rows.
+__device__ __forceinline__ Req read_request(const AttendArgs& a, int r, bool report) {
+  Req q;
+  const int32_t s0 = a.q_start ? a.q_start[r] : r, s1 = a.q_start ? a.q_start[r + 1] : r + 1;
+  const int32_t seq = a.seq_len[r];
+  const int64_t n = (int64_t)s1 - s0;
+  if (n < 0 || n > a.max_q || s0 < 0 || s1 > a.T || seq < 0 || seq > IS_MAX_POSITION) {
+    if (report) latch(a.status, IS_ST_COUNT);
+    q.row0 = q.n = q.seq = q.kb = q.ke = 0;
+    return q;
+  }
+  q.row0 = s0;
+  q.n = (int32_t)n;
+  q.seq = seq;
+  const int64_t cap = (int64_t)a.max_blocks * a.block_size;
+  q.ke = (int32_t)min((int64_t)seq, cap);
+  if (report && n > 0 && q.ke < seq) latch(a.status, IS_ST_BLOCK_TABLE);
+  q.kb = a.window > 0 ? max(0, (int32_t)max((int64_t)seq - n - a.window + 1, (int64_t)0)) : 0;
+  if (q.kb > q.ke) q.kb = q.ke;
+  return q;
+}
+
+// ---- workspace -------------------------------------------------------------------
+// [ctas] join records, then two partials per CTA: of the item its run begins
+// in (slot 2 c) and of the one it ends in (2 c + 1), when those cross its ends.
+struct JoinRecord {
+  int32_t parts;         // 0: nothing to join
+  int32_t slot0;         // the first part; part i > 0 is slot 2 * (cta + i)
+  int32_t row0;          // first query row of the request
+  int32_t head;          // KV head
+  int32_t rho0, rows;    // the item's first query row (token * G + head of the group) and their number
+};
+constexpr size_t kRecordBytes = 32;
+constexpr int kMaxCtas = 1024;
+template <int ROWS, int D>
+struct Partial {
+  float o[ROWS][D];
+  float m[ROWS], l[ROWS];
+};
+
+__device__ __forceinline__ JoinRecord* record_of(const AttendArgs& a, int cta) {
+  return reinterpret_cast<JoinRecord*>(a.workspace + (size_t)cta * kRecordBytes);
+}
+template <int ROWS, int D>
+__device__ __forceinline__ Partial<ROWS, D>* partial_of(const AttendArgs& a, int slot) {
+  return reinterpret_cast<Partial<ROWS, D>*>(a.workspace + (size_t)kMaxCtas * kRecordBytes) + slot;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_out(const AttendArgs& a, const Req& q, int head, int rho, int d, float x, float y) {
+  const int tok = rho / a.G;
+  T* p = reinterpret_cast<T*>(a.out) + ((size_t)(q.row0 + tok) * a.Hq + (size_t)head * a.G + (rho - tok * a.G)) * a.D + d;
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float2*>(p) = make_float2(x, y);
+  else
+    *reinterpret_cast<uint32_t*>(p) = Vec<T>::pack2(x, y);
+}
+__device__ __forceinline__ void store_lse(const AttendArgs& a, const Req& q, int head, int rho, float m, float l) {
+  if (!a.lse) return;
+  const int tok = rho / a.G;
+  a.lse[(size_t)(q.row0 + tok) * a.Hq + (size_t)head * a.G + (rho - tok * a.G)] =
+      l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Adds up the parts of an item that several CTAs worked on: one CTA per
+// (record, row) or several rows of a record, the threads splitting the parts
+// and the head dimension.
+constexpr int kJoinThreads = 256;
+
+template <typename T, int ROWS, int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a) {
+  constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
+  __shared__ float4 s_o[GROUPS][LANES];
+  __shared__ float s_m[GROUPS], s_l[GROUPS];
+  pdl_wait();
+  pdl_trigger();
+  const int cta = blockIdx.x;
+  const JoinRecord rec = *record_of(a, cta);
+  if (rec.parts == 0) return;
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  for (int row = blockIdx.y; row < rec.rows; row += gridDim.y) {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = group; i < rec.parts; i += GROUPS) {
+      const Partial<ROWS, D>* p = partial_of<ROWS, D>(a, i == 0 ? rec.slot0 : 2 * (cta + i));
+      const float pm = p->m[row], pl = p->l[row];
+      const float4 v = *reinterpret_cast<const float4*>(&p->o[row][lane * 4]);
+      const float mn = fmaxf(m, pm), mz = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2(m - mz), g = ex2(pm - mz);
+      o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
+      l = l * f + pl * g;
+      m = mn;
+    }
+    s_o[group][lane] = o;
+    if (lane == 0) {
+      s_m[group] = m;
+      s_l[group] = l;
+    }
+    __syncthreads();
+    if (group == 0) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) mx = fmaxf(mx, s_m[g]);
+      const float mz = mx == -INFINITY ? 0.f : mx;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+      l = 0.f;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        const float f = ex2(s_m[g] - mz);
+        const float4 v = s_o[g][lane];
+        o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
+        l = fmaf(f, s_l[g], l);
+      }
+      Req q;
+      q.row0 = rec.row0;
+      const float inv = l == 0.f ? 0.f : a.v_scale / l;
+      if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int rho = rec.rho0 + row;
+      store_out<T>(a, q, rec.head, rho, lane * 4, o.x * inv, o.y * inv);
+      store_out<T>(a, q, rec.head, rho, lane * 4 + 2, o.z * inv, o.w * inv);
+      if (lane == 0) store_lse(a, q, rec.head, rho, mx, l);
+    }
+    __syncthreads();                     // s_o is read before the next row's is written
+  }
+}
+
+}  // namespace isk

@@ -1,0 +1,705 @@
+// Softmax attention of many query rows per request over its paged cache
+// (is_attend with prompts), on the 5th-generation tensor cores.
+//
+// With n new tokens every key is used by up to n * G rows (G query heads share
+// a KV head), so the time is that of the two products, 4 * D flops per (row,
+// key) pair.  An item is (request, KV head, run of tokens whose rows fill two
+// 128-row tiles A and B); per 128 keys
+//   S = Q K^T   M 128 x N 128 keys x K D      (operands in shared memory)
+//   O += P V    M 128 x N D x K 128 keys      (P in tensor memory, over S)
+// Tile A's softmax runs while the tensor core works on tile B and the other way
+// round.  13 warps, each with one job:
+//   warps 0-3   softmax of tile A: one thread per row, so the row's maximum and
+//               sum need no exchange between threads
+//   warps 4-7   softmax of tile B
+//   warps 8-11  bring Q, K and V tiles into shared memory with 16-byte
+//               asynchronous copies, one row of the paged cache at a time: any
+//               block size works, rows past the end or of unnamed blocks are
+//               zero-filled; FP8 rows are converted on the way (exactly)
+//   warp 12     one thread issues the MMAs
+// Tensor memory (512 columns): S_A, S_B (128 each; P takes the first half of
+// its S as 16-bit pairs), O_A, O_B (D each).  Shared memory: Q (2 x 128 rows),
+// then a ring of 128-key tiles, K and V in turn.  Rows are stored as 64-element
+// halves of 128 bytes with the 128-byte swizzle: K-major for Q and K; V's
+// rows are keys, so it is the MN-major operand of the second product.
+//
+// As in the split kernel the items' keys are numbered in units of 128 over
+// the call and every CTA of a persistent grid (one per SM) takes one run of
+// them, so ragged and causal batches are balanced; items cut by a run's end
+// are joined from the workspace.  The running maximum moves only when a logit
+// passes it by 2^8; moving it rescales O in tensor memory, which the wait for
+// S already made safe: the MMA thread issued the previous O += P V before it.
+// Every wait is bounded (2 s): on time-out the CTA latches IS_ST_TIMEOUT,
+// lets its own work in flight end, frees its tensor memory and returns.
+#include <algorithm>
+#include <type_traits>
+
+#include "attend.cuh"
+#include "block_scan.cuh"
+#include "tcgen05.cuh"
+
+namespace isk {
+
+namespace prompt {
+
+constexpr int kThreads = 416;
+constexpr int kRows = 256;               // rows of an item, at most: tiles A and B
+constexpr int kKeys = 128;               // keys of a tile, and of a unit
+constexpr int kLoaderWarp = 8, kMmaWarp = 12;
+constexpr int kMinRun = 4;               // units of a CTA's run, at least
+constexpr int kMaskRing = 4;
+constexpr uint32_t kTmemAll = 512;
+
+template <int D>
+struct Shape {
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kHalfBytes = 128 * 128;           // 128 rows of 64 elements
+  static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
+  static constexpr int kRing = D == 128 ? 5 : 8;              // K and V tiles in flight
+  static constexpr int kLag = kRing - 2 < 4 ? kRing - 2 : 4;  // loads issued beyond the one being waited for
+  static constexpr size_t kSmem = 1024 + (2 + kRing) * (size_t)kTileBytes + 128 * 8;
+  static constexpr uint32_t kOCol = 256;                      // first column of O_A; O_B follows D columns on
+};
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Both operands in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A in tensor memory (lane = row, a column = two consecutive 16-bit elements of K).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of V for O += P V: K (keys) runs over 128-byte rows, eight to a
+// swizzle atom (stride byte offset 1024), N over the 64 elements of a row and
+// then the halves (leading byte offset).
+template <int D>
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(Shape<D>::kHalfBytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// kind::f16 instruction descriptor: D fp32 (bit 4), A and B fp16 or bf16
+// (bits 7, 10), B MN-major (bit 16) for V, N >> 3 at 17, M >> 4 at 24.
+template <typename T>
+__device__ constexpr uint32_t idesc_of(int n, bool mn_major_b) {
+  constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | ((mn_major_b ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+
+// Tile t of a request: its tokens, the positions its rows see, its units.
+struct Tile {
+  int32_t tok0, toks;
+  int32_t kb, ke, units;
+};
+__device__ __forceinline__ Tile tile_of(const AttendArgs& a, const Req& q, int per, int t) {
+  Tile x;
+  x.tok0 = t * per;
+  x.toks = min(per, q.n - x.tok0);
+  const int32_t p0 = q.seq - q.n + x.tok0;           // position of the first token
+  x.ke = min(q.ke, p0 + x.toks);
+  x.kb = a.window > 0 ? max(0, (int32_t)max((int64_t)p0 - a.window + 1, (int64_t)0)) : 0;
+  x.units = max(1, (x.ke - x.kb + kKeys - 1) / kKeys);
+  return x;
+}
+__device__ __forceinline__ int64_t units_of_request(const AttendArgs& a, const Req& q, int per) {
+  int64_t sum = 0;
+  for (int t = 0; t * per < q.n; ++t) sum += tile_of(a, q, per, t).units;
+  return sum * a.H;
+}
+
+// The segments of a CTA's run, walked the same way by every thread.
+struct Walk {
+  int64_t u, u_end, u_first, run, base;  // base: first unit of tile (r, t)
+  int r, t;
+  Req q;
+  Tile x;
+  // of the current segment
+  int head, k_lo, k_hi, rows;
+  int64_t item0;
+  bool whole, begins, at_start;
+
+  __device__ __forceinline__ bool next(const AttendArgs& a, int per) {
+    if (u >= u_end) return false;
+    while (true) {
+      if (t * per < q.n) {
+        const int64_t n = (int64_t)a.H * x.units;
+        if (u < base + n) break;
+        base += n;
+        ++t;
+      } else {
+        ++r;
+        t = 0;
+        q = read_request(a, r, false);
+      }
+      if (t * per < q.n) x = tile_of(a, q, per, t);
+    }
+    head = (int)((u - base) / x.units);
+    item0 = base + (int64_t)head * x.units;
+    const int ua = (int)(u - item0), ub = (int)min((int64_t)x.units, u_end - item0);
+    begins = ua == 0;
+    whole = begins && ub == x.units;
+    at_start = u == u_first;
+    k_lo = x.kb + ua * kKeys;
+    k_hi = min(x.ke, x.kb + ub * kKeys);
+    rows = x.toks * a.G;
+    u = item0 + ub;
+    return true;
+  }
+  __device__ __forceinline__ int tiles() const { return k_hi > k_lo ? (k_hi - k_lo + kKeys - 1) / kKeys : 0; }
+};
+
+struct Bars {
+  uint64_t q_full, q_empty, done;
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t mask_full[kMaskRing];
+};
+
+// Bits lo .. hi - 1 of a 32-bit word whose bit 0 is position `at`.
+__device__ __forceinline__ uint32_t bits_between(int at, int lo, int hi) {
+  const int l = max(lo - at, 0), h = min(hi - at, 32);
+  if (h <= l) return 0u;
+  return (h - l == 32 ? 0xffffffffu : ((1u << (h - l)) - 1u)) << l;
+}
+
+// Eight E4M3 bytes as eight 16-bit values, exact.
+template <typename T>
+__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
+  uint32_t w[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi), e4m3x2_f16x2(hi >> 16)};
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      w[i] = Vec<__nv_bfloat16>::pack2(f.x, f.y);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Where 16-byte chunk c (8 elements) of row `row` lies in a tile.
+template <int D>
+__device__ __forceinline__ uint32_t at_chunk(int row, int c) {
+  return (uint32_t)(c >> 3) * Shape<D>::kHalfBytes + (uint32_t)row * 128u + (uint32_t)(((c & 7) ^ (row & 7)) * 16);
+}
+
+template <typename T, bool F8, int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a, int per) {
+  using S = Shape<D>;
+  // FP8 values are exact in fp16 too, where the weights keep three more bits.
+  using W = typename std::conditional<F8, __half, T>::type;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) Bars bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ __align__(16) uint32_t s_mask[kMaskRing][4];
+  __shared__ int64_t scratch[33];
+  __shared__ int64_t s_base;
+  __shared__ int32_t s_req;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &s_abort;
+  const uint32_t tiles0 = (smem_addr(smem_raw) + 1023u) & ~1023u;     // Q_A, Q_B, then the ring
+  const uint32_t ring0 = tiles0 + 2 * S::kTileBytes;
+  long long* s_off = reinterpret_cast<long long*>(smem_raw + (ring0 - smem_addr(smem_raw)) + S::kRing * S::kTileBytes);
+
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(&s_tmem), kTmemAll);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    s_abort = 0;
+    mbar_init(smem_addr(&bars.q_full), 128);
+    mbar_init(smem_addr(&bars.q_empty), 1);
+    mbar_init(smem_addr(&bars.done), 1);
+    for (int i = 0; i < S::kRing; ++i) {
+      mbar_init(smem_addr(&bars.kv_full[i]), 128);
+      mbar_init(smem_addr(&bars.kv_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&bars.s_full[i]), 1);
+      mbar_init(smem_addr(&bars.p_full[i]), 128);
+      mbar_init(smem_addr(&bars.o_full[i]), 1);
+    }
+    for (int i = 0; i < kMaskRing; ++i) mbar_init(smem_addr(&bars.mask_full[i]), 128);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // This CTA's run of units.
+  const int share = (a.R + kThreads - 1) / kThreads;
+  const int r0 = min(a.R, tid * share), r1 = min(a.R, r0 + share);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) mine += units_of_request(a, read_request(a, r, blockIdx.x == 0), per);
+  int64_t total;
+  int64_t at = block_exclusive_scan(mine, scratch, &total);
+  Walk w;
+  w.run = max((int64_t)kMinRun, (total + gridDim.x - 1) / gridDim.x);
+  w.u = w.u_first = (int64_t)blockIdx.x * w.run;
+  w.u_end = min(total, w.u + w.run);
+  const bool idle = w.u >= w.u_end;
+  if (!idle && at <= w.u && w.u < at + mine) {
+    for (int r = r0; r < r1; ++r) {
+      const int64_t n = units_of_request(a, read_request(a, r, false), per);
+      if (w.u < at + n) {
+        s_req = r;
+        s_base = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  if (idle) {
+    if (tid == 0) record_of(a, blockIdx.x)->parts = 0;
+  } else {
+    w.r = s_req;
+    w.base = s_base;
+    w.t = 0;
+    w.q = read_request(a, w.r, false);
+    w.x = tile_of(a, w.q, per, 0);
+
+    if (warp < kLoaderWarp) {
+      // ---- softmax ------------------------------------------------------------
+      const int side = warp >> 2;                      // 0: tile A, 1: tile B
+      const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+      const uint32_t s_col = tmem + lanes + 128u * side, o_col = tmem + lanes + S::kOCol + (uint32_t)(D * side);
+      const float sc = a.scale * kLog2e;
+      uint32_t n_s = 0, n_o = 0, n_mask = 0;           // phases consumed
+      bool ok = true;
+      while (ok && w.next(a, per)) {
+        const int n_tiles = w.tiles();
+        const int row = side * 128 + (warp & 3) * 32 + lane;
+        const bool mine_has = side == 0 || w.rows > 128;   // the tile has rows
+        const int tok = row / a.G;
+        const int lim = row < w.rows ? w.q.seq - w.q.n + w.x.tok0 + tok : -1;
+        // the warp's first and last positions, for skipping the masks
+        const int lim_lo = __reduce_min_sync(0xffffffffu, row < w.rows ? lim : INT32_MAX);
+        const int lim_hi = __reduce_max_sync(0xffffffffu, lim);
+        const int64_t low = a.window > 0 ? (int64_t)lim - a.window + 1 : 0;
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < n_tiles; ++j, ++n_mask) {
+          if (!mine_has) continue;
+          const int slot = n_mask % kMaskRing;
+          ok = wait_or_abort(smem_addr(&bars.mask_full[slot]), (n_mask / kMaskRing) & 1u, abort_flag, kWaitBudgetNs) &&
+               wait_or_abort(smem_addr(&bars.s_full[side]), n_s & 1u, abort_flag, kWaitBudgetNs);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++n_s;
+          tc_fence_after();
+          const uint4 mw = *reinterpret_cast<const uint4*>(s_mask[slot]);
+          const uint32_t words[4] = {mw.x, mw.y, mw.z, mw.w};
+          const int key0 = w.k_lo + j * kKeys;
+          const bool check = (words[0] & words[1] & words[2] & words[3]) != 0xffffffffu || key0 + kKeys - 1 > lim_lo ||
+                             (a.window > 0 && (int64_t)key0 <= (int64_t)lim_hi - a.window);
+          // Bits of the keys this row sees.
+          uint32_t see[4];
+          if (check) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              see[c] = words[c] & bits_between(key0 + 32 * c, (int)max(low, (int64_t)0), lim + 1);
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld32(s_col + 32 * c, x);
+            tmem_wait_ld();
+            if (check) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((see[c] >> i) & 1u)) x[i] = 0xff800000u;
+            }
+            float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[1]);
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) {
+              m0 = fmaxf(m0, __uint_as_float(x[i]));
+              m1 = fmaxf(m1, __uint_as_float(x[i + 1]));
+            }
+            mx = fmaxf(mx, fmaxf(m0, m1));
+          }
+          mx *= sc;                                    // sc > 0
+          if (__any_sync(0xffffffffu, mx > m + kLazy)) {
+            const float mn = fmaxf(m, mx);
+            const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+            m = mn;
+            l *= f;
+            if (j > 0) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld32(o_col + 32 * c, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                tmem_st32(o_col + 32 * c, x);
+              }
+            }
+          }
+          const float mz = m == -INFINITY ? 0.f : m;
+          const unsigned long long sc2 = pk2(sc, sc), mz2 = pk2(-mz, -mz);
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32], p[16];
+            tmem_ld32(s_col + 32 * c, x);
+            tmem_wait_ld();
+            if (check) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((see[c] >> i) & 1u)) x[i] = 0xff800000u;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float y0, y1;
+              upk2(fma2_rn(pk2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, mz2), y0, y1);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              l0 += y0;
+              l1 += y1;
+              p[i] = Vec<W>::pack2(y0, y1);
+            }
+            tmem_st16(s_col + 16 * c, p);
+          }
+          l += l0 + l1;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_addr(&bars.p_full[side]));
+        }
+        if (!ok) break;
+        // The segment's output.
+        if (mine_has && n_tiles > 0) {
+          ok = __all_sync(0xffffffffu, wait_or_abort(smem_addr(&bars.o_full[side]), n_o & 1u, abort_flag, kWaitBudgetNs));
+          if (!ok) break;
+          ++n_o;
+          tc_fence_after();
+        }
+        Partial<kRows, D>* part =
+            w.whole ? nullptr : partial_of<kRows, D>(a, 2 * blockIdx.x + (w.at_start ? 0 : 1));
+        const int rho = w.x.tok0 * a.G + row;
+        const float inv = l == 0.f ? 0.f : a.v_scale / l;
+        if (mine_has) {
+          T* dst = nullptr;
+          if (row < w.rows)
+            dst = reinterpret_cast<T*>(a.out) +
+                  ((size_t)(w.q.row0 + w.x.tok0 + tok) * a.Hq + (size_t)w.head * a.G + (row - tok * a.G)) * D;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            if (n_tiles > 0) {
+              tmem_ld32(o_col + 32 * c, x);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = 0u;
+            }
+            if (row < w.rows) {
+              if (w.whole) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  float y[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) y[i] = l == 0.f ? 0.f : __uint_as_float(x[8 * v + i]) * inv;
+                  st_v4(dst + 32 * c + 8 * v, Vec<T>::pack(y));
+                }
+              } else {
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                  st_v4(&part->o[row][32 * c + 4 * v], make_uint4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]));
+              }
+            }
+          }
+          if (row < w.rows) {
+            if (w.whole) {
+              store_lse(a, w.q, w.head, rho, m, l);
+            } else {
+              part->m[row] = m;
+              part->l[row] = l;
+            }
+          }
+        }
+        // The next segment's first O += P V follows this side's next p_full, so O has been read by then.
+        tc_fence_before();
+        if (tid == 0 && w.begins && !w.whole) {
+          JoinRecord* rec = record_of(a, blockIdx.x);
+          rec->parts = (int32_t)((w.item0 + w.x.units - 1) / w.run - blockIdx.x) + 1;
+          rec->slot0 = 2 * blockIdx.x + (w.at_start ? 0 : 1);
+          rec->row0 = w.q.row0;
+          rec->head = w.head;
+          rec->rho0 = w.x.tok0 * a.G;
+          rec->rows = w.rows;
+        }
+        if (tid == 0 && w.u >= w.u_end && !(w.begins && !w.whole)) record_of(a, blockIdx.x)->parts = 0;
+      }
+      if (!ok) *abort_flag = 1;
+    } else if (warp < kMmaWarp) {
+      // ---- loads --------------------------------------------------------------
+      const int lt = tid - kLoaderWarp * 32;           // 0 .. 127
+      constexpr int EB = F8 ? 1 : 2;
+      const int64_t token_bytes = (int64_t)a.H * D * EB;
+      uint32_t n_load = 0, n_mask = 0, n_q = 0, n_told = 0;   // tiles issued, masks, query tiles, tiles signalled
+      bool ok = true;                                  // the same in all loaders once they have agreed()
+      auto agreed = [&](bool mine_ok) {                // also a barrier of the four warps
+        uint32_t r;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+            "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(r)
+            : "r"(mine_ok ? 1u : 0u)
+            : "memory");
+        return r != 0;
+      };
+      auto tell = [&](uint32_t upto) {                 // tiles up to here have landed
+        fence_proxy_async_smem();
+        for (; n_told < upto; ++n_told) mbar_arrive(smem_addr(&bars.kv_full[n_told % S::kRing]));
+      };
+      while (ok && w.next(a, per)) {
+        const int n_tiles = w.tiles();
+        if (n_tiles == 0) continue;
+        ok = agreed(wait_or_abort(smem_addr(&bars.q_empty), (n_q & 1u) ^ 1u, abort_flag, kWaitBudgetNs));
+        if (!ok) break;
+        {
+          constexpr int C = D / 8;                     // chunks of a row
+          for (int i = lt; i < kRows * C; i += 128) {
+            const int row = i / C, c = i % C, tok = row / a.G;
+            const bool in = row < w.rows;
+            const uint8_t* src = a.q + (int64_t)(w.q.row0 + w.x.tok0 + (in ? tok : 0)) * a.q_stride +
+                                 ((size_t)w.head * a.G + (in ? row - tok * a.G : 0)) * D * 2 + c * 16;
+            cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), src, in);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
+          mbar_arrive(smem_addr(&bars.q_full));
+          ++n_q;
+        }
+        const int32_t* table = a.block_table + (size_t)w.r * a.max_blocks;
+        const uint8_t* kbase = a.k_cache + (size_t)w.head * D * EB;
+        int32_t id = -1, off = 0;
+        auto look_up = [&](int j) {                    // this thread's key of tile j
+          const int p = w.k_lo + j * kKeys + lt;
+          id = -1;
+          if (j < n_tiles && p < w.k_hi) {
+            const int b = p / a.block_size;
+            off = p - b * a.block_size;
+            id = table[b];
+            if (id < 0 || id >= a.num_blocks) {
+              latch(a.status, IS_ST_BLOCK_ID);
+              id = -1;
+            }
+          }
+        };
+        look_up(0);
+        bool here = true;                              // this thread's waits
+        for (int j = 0; j < n_tiles; ++j) {
+          const long long at_key = id < 0 ? -1ll : ((long long)id * a.block_size + off) * token_bytes;
+          const uint32_t named = __ballot_sync(0xffffffffu, at_key >= 0);
+          ok = agreed(here);                           // and the last tile's offsets have been read
+          if (!ok) break;
+          s_off[lt] = at_key;
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          look_up(j + 1);
+          for (int kv = 0; kv < 2; ++kv, ++n_load) {
+            const int buf = n_load % S::kRing;
+            here = wait_or_abort(smem_addr(&bars.kv_empty[buf]), ((n_load / S::kRing) & 1u) ^ 1u, abort_flag, kWaitBudgetNs);
+            if (!here) break;
+            if (kv == 0) {
+              // The mask slot was last read four tiles ago: that tile's V has been released.
+              if (lane == 0) s_mask[n_mask % kMaskRing][warp - kLoaderWarp] = named;
+              mbar_arrive(smem_addr(&bars.mask_full[n_mask % kMaskRing]));
+              ++n_mask;
+            }
+            const uint32_t dst = ring0 + buf * S::kTileBytes;
+            const uint8_t* src0 = kbase + (kv ? a.v_offset : 0);
+            if constexpr (!F8) {
+              constexpr int C = D / 8, RP = 128 / C;   // chunks of a row; rows of one pass of the loaders
+#pragma unroll
+              for (int i = 0; i < 128 / RP; ++i) {
+                const int row = i * RP + lt / C, c = lt % C;
+                const long long o = s_off[row];
+                cp_async16(dst + at_chunk<D>(row, c), src0 + (o < 0 ? 0 : o) + c * 16, o >= 0);
+              }
+              cp_async_commit();
+              if (n_load - n_told >= (uint32_t)S::kLag) {
+                cp_async_wait<S::kLag>();
+                tell(n_load + 1 - S::kLag);
+              }
+            } else {
+              constexpr int C = D / 16, RP = 128 / C;  // 16-byte chunks of an FP8 row
+              uint4 x[128 / RP];
+#pragma unroll
+              for (int i = 0; i < 128 / RP; ++i) {
+                const long long o = s_off[i * RP + lt / C];
+                x[i] = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src0 + o + (lt % C) * 16);
+              }
+#pragma unroll
+              for (int i = 0; i < 128 / RP; ++i) {
+                const int row = i * RP + lt / C, c = lt % C;
+                st_shared_v4(dst + at_chunk<D>(row, 2 * c), kv ? widen8<W>(x[i].x, x[i].y) : widen8<T>(x[i].x, x[i].y));
+                st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), kv ? widen8<W>(x[i].z, x[i].w) : widen8<T>(x[i].z, x[i].w));
+              }
+              tell(n_load + 1);
+            }
+          }
+        }
+        ok = ok && agreed(here);
+        cp_async_wait<0>();
+        tell(n_load);
+      }
+      cp_async_wait<0>();
+      if (!ok) *abort_flag = 1;
+    } else if (lane == 0) {
+      // ---- MMAs ----------------------------------------------------------------
+      constexpr uint32_t kIdS = idesc_of<T>(128, false), kIdO = idesc_of<W>(D, true);
+      uint32_t n_kv = 0, n_q = 0, n_p[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && wait_or_abort(smem_addr(bar), parity, abort_flag, kWaitBudgetNs);
+        return ok;
+      };
+      auto scores = [&](int side, uint32_t k_tile) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = (uint32_t)(k >> 2) * S::kHalfBytes + 32u * (k & 3);
+          mma_ss(tmem + 128u * side, sw128_desc(tiles0 + side * S::kTileBytes + o), sw128_desc(k_tile + o), kIdS, k != 0);
+        }
+        mma_commit(smem_addr(&bars.s_full[side]));
+      };
+      while (ok && w.next(a, per)) {
+        const int n_tiles = w.tiles();
+        if (n_tiles == 0) continue;
+        const int sides = w.rows > 128 ? 2 : 1;
+        if (!wait(&bars.q_full, n_q & 1u)) break;
+        ++n_q;
+        if (!wait(&bars.kv_full[n_kv % S::kRing], (n_kv / S::kRing) & 1u)) break;
+        tc_fence_after();
+        for (int side = 0; side < sides; ++side) scores(side, ring0 + (n_kv % S::kRing) * S::kTileBytes);
+        mma_commit(smem_addr(&bars.kv_empty[n_kv % S::kRing]));
+        for (int j = 0; j < n_tiles && ok; ++j) {
+          const uint32_t nv = n_kv + 1, nk = n_kv + 2;   // V of this tile, K of the next
+          const uint32_t v_tile = ring0 + (nv % S::kRing) * S::kTileBytes;
+          if (!wait(&bars.kv_full[nv % S::kRing], (nv / S::kRing) & 1u)) break;
+          for (int side = 0; side < sides; ++side) {
+            if (!wait(&bars.p_full[side], n_p[side] & 1u)) break;
+            ++n_p[side];
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts(tmem + S::kOCol + (uint32_t)(D * side), tmem + 128u * side + 8u * k, v_desc<D>(v_tile + 2048u * k), kIdO,
+                     (j | k) != 0);
+            if (side == sides - 1) mma_commit(smem_addr(&bars.kv_empty[nv % S::kRing]));
+            if (j == n_tiles - 1) {
+              mma_commit(smem_addr(&bars.o_full[side]));
+            } else {
+              if (side == 0 && !wait(&bars.kv_full[nk % S::kRing], (nk / S::kRing) & 1u)) break;
+              if (side == 0) tc_fence_after();
+              scores(side, ring0 + (nk % S::kRing) * S::kTileBytes);
+              if (side == sides - 1) mma_commit(smem_addr(&bars.kv_empty[nk % S::kRing]));
+            }
+          }
+          n_kv += 2;
+        }
+        if (ok) mma_commit(smem_addr(&bars.q_empty));
+      }
+      if (!ok) *abort_flag = 1;
+      // Every MMA issued has ended before tensor and shared memory are let go.
+      mma_commit(smem_addr(&bars.done));
+      mbar_wait_bounded(smem_addr(&bars.done), 0, kWaitBudgetNs);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && s_abort) {
+    latch(a.status, IS_ST_TIMEOUT);
+    record_of(a, blockIdx.x)->parts = 0;
+  }
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemAll);
+  }
+}
+
+}  // namespace prompt
+
+// Prompts go here when the rows of a request fill a tensor-core tile better
+// than the split kernel's 16 rows (see launch_attend).
+template <typename T, bool F8, int D>
+static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
+  using S = prompt::Shape<D>;
+  auto* kern = prompt::attend_prompt_kernel<T, F8, D>;
+  static_assert(S::kSmem + 1024 <= 227 * 1024, "a CTA fits an SM");
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
+  if (e != cudaSuccess) return e;
+  constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - kMaxCtas * kRecordBytes) / (2 * sizeof(Partial<prompt::kRows, D>)));
+  const int grid = std::max(1, std::min({cfg.num_sms, kFit, kMaxCtas}));
+  const int per = prompt::kRows / a.G;   // tokens of an item
+  e = launch_ex(kern, dim3(grid), dim3(prompt::kThreads), S::kSmem, cfg.stream, cfg.pdl, a, per);
+  if (e != cudaSuccess) return e;
+  return launch_ex(attend_join_kernel<T, prompt::kRows, D>, dim3(grid, 8), dim3(kJoinThreads), 0, cfg.stream, cfg.pdl, a);
+}
+
+cudaError_t launch_attend_prompt(const AttendArgs& a, const LaunchCfg& cfg) {
+  if (a.dtype == IS_BF16) {
+    if (a.D == 64)
+      return a.fp8 ? launch_prompt_t<__nv_bfloat16, true, 64>(a, cfg) : launch_prompt_t<__nv_bfloat16, false, 64>(a, cfg);
+    return a.fp8 ? launch_prompt_t<__nv_bfloat16, true, 128>(a, cfg) : launch_prompt_t<__nv_bfloat16, false, 128>(a, cfg);
+  }
+  if (a.D == 64) return a.fp8 ? launch_prompt_t<__half, true, 64>(a, cfg) : launch_prompt_t<__half, false, 64>(a, cfg);
+  return a.fp8 ? launch_prompt_t<__half, true, 128>(a, cfg) : launch_prompt_t<__half, false, 128>(a, cfg);
+}
+
+}  // namespace isk

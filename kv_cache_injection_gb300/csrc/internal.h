@@ -93,6 +93,7 @@ cudaError_t launch_capture_layer(const CaptureArgs& a, const LaunchCfg& cfg);
 cudaError_t launch_extend(const is_extend_args_t& a, const LaunchCfg& cfg);
 cudaError_t launch_append(const AppendArgs& a, const AxisTurns& turns, const LaunchCfg& cfg);
 cudaError_t launch_attend(const AttendArgs& a, const LaunchCfg& cfg);
+cudaError_t launch_attend_prompt(const AttendArgs& a, const LaunchCfg& cfg);
 
 // Whether a row of row_bytes (K or V of one layer) and R requests fit the
 // inject kernel's shared-memory plan.
