@@ -168,4 +168,40 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
   }
 }
 
+// The same for items of many rows and few parts: D / 4 lanes take a row, all
+// parts of it.
+template <typename T, int ROWS, int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_rows_kernel(const AttendArgs a) {
+  constexpr int LANES = D / 4, AT_ONCE = kJoinThreads / LANES;
+  pdl_wait();
+  pdl_trigger();
+  const int cta = blockIdx.x;
+  const JoinRecord rec = *record_of(a, cta);
+  if (rec.parts == 0) return;
+  const int lane = threadIdx.x % LANES;
+  for (int row = blockIdx.y * AT_ONCE + threadIdx.x / LANES; row < rec.rows; row += gridDim.y * AT_ONCE) {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < rec.parts; ++i) {
+      const Partial<ROWS, D>* p = partial_of<ROWS, D>(a, i == 0 ? rec.slot0 : 2 * (cta + i));
+      const float pm = p->m[row], pl = p->l[row];
+      const float4 v = *reinterpret_cast<const float4*>(&p->o[row][lane * 4]);
+      const float mn = fmaxf(m, pm), mz = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2(m - mz), g = ex2(pm - mz);
+      o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
+      l = l * f + pl * g;
+      m = mn;
+    }
+    Req q;
+    q.row0 = rec.row0;
+    const float inv = l == 0.f ? 0.f : a.v_scale / l;
+    if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int rho = rec.rho0 + row;
+    store_out<T>(a, q, rec.head, rho, lane * 4, o.x * inv, o.y * inv);
+    store_out<T>(a, q, rec.head, rho, lane * 4 + 2, o.z * inv, o.w * inv);
+    if (lane == 0) store_lse(a, q, rec.head, rho, m, l);
+  }
+}
+
 }  // namespace isk

@@ -8,15 +8,16 @@
 //   S = Q K^T   M 128 x N 128 keys x K D      (operands in shared memory)
 //   O += P V    M 128 x N D x K 128 keys      (P in tensor memory, over S)
 // Tile A's softmax runs while the tensor core works on tile B and the other way
-// round.  13 warps, each with one job:
+// round.  12 warps, each with one job:
 //   warps 0-3   softmax of tile A: one thread per row, so the row's maximum and
 //               sum need no exchange between threads
 //   warps 4-7   softmax of tile B
-//   warps 8-11  bring Q, K and V tiles into shared memory with 16-byte
-//               asynchronous copies, one row of the paged cache at a time: any
-//               block size works, rows past the end or of unnamed blocks are
-//               zero-filled; FP8 rows are converted on the way (exactly)
-//   warp 12     one thread issues the MMAs
+//   warps 8-10  bring Q, K and V tiles into shared memory: whole tiles with
+//               bulk tensor copies, a block of the paged cache at a time; tiles
+//               with missing keys (zero-filled) and block sizes those do not
+//               fit with 16-byte asynchronous copies, row by row; FP8 rows
+//               through registers, widened on the way (exactly)
+//   warp 11     one thread issues the MMAs
 // Tensor memory (512 columns): S_A, S_B (128 each; P takes the first half of
 // its S as 16-bit pairs), O_A, O_B (D each).  Shared memory: Q (2 x 128 rows),
 // then a ring of 128-key tiles, K and V in turn.  Rows are stored as 64-element
@@ -31,7 +32,10 @@
 // S already made safe: the MMA thread issued the previous O += P V before it.
 // Every wait is bounded (2 s): on time-out the CTA latches IS_ST_TIMEOUT,
 // lets its own work in flight end, frees its tensor memory and returns.
+#include <cuda.h>
+
 #include <algorithm>
+#include <cstring>
 #include <type_traits>
 
 #include "attend.cuh"
@@ -42,10 +46,13 @@ namespace isk {
 
 namespace prompt {
 
-constexpr int kThreads = 416;
+constexpr int kThreads = 384;
 constexpr int kRows = 256;               // rows of an item, at most: tiles A and B
 constexpr int kKeys = 128;               // keys of a tile, and of a unit
-constexpr int kLoaderWarp = 8, kMmaWarp = 12;
+constexpr int kLoaderWarp = 8, kLoaders = 96, kMmaWarp = 11;
+// Registers a thread: 168 at launch (65,536 / 384); the softmax warps take what
+// a row of S needs, the other four give it: 2 * 208 + 88 = 3 * 168.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMinRun = 4;               // units of a CTA's run, at least
 constexpr int kMaskRing = 4;
 constexpr uint32_t kTmemAll = 512;
@@ -56,7 +63,6 @@ struct Shape {
   static constexpr uint32_t kHalfBytes = 128 * 128;           // 128 rows of 64 elements
   static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
   static constexpr int kRing = D == 128 ? 5 : 8;              // K and V tiles in flight
-  static constexpr int kLag = kRing - 2 < 4 ? kRing - 2 : 4;  // loads issued beyond the one being waited for
   static constexpr size_t kSmem = 1024 + (2 + kRing) * (size_t)kTileBytes + 128 * 8;
   static constexpr uint32_t kOCol = 256;                      // first column of O_A; O_B follows D columns on
 };
@@ -94,6 +100,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2_rn(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Rows of one half head: elements x .. x + 63 of head h of consecutive tokens from t on.
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int x, int h, int t, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t), "r"(bar)
+      : "memory");
+}
 
 // Both operands in shared memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -145,7 +170,8 @@ __device__ __forceinline__ Tile tile_of(const AttendArgs& a, const Req& q, int p
   x.toks = min(per, q.n - x.tok0);
   const int32_t p0 = q.seq - q.n + x.tok0;           // position of the first token
   x.ke = min(q.ke, p0 + x.toks);
-  x.kb = a.window > 0 ? max(0, (int32_t)max((int64_t)p0 - a.window + 1, (int64_t)0)) : 0;
+  // whole tiles from position 0 on, so that tiles line up with the cache's blocks
+  x.kb = a.window > 0 ? (int32_t)max((int64_t)p0 - a.window + 1, (int64_t)0) / kKeys * kKeys : 0;
   x.units = max(1, (x.ke - x.kb + kKeys - 1) / kKeys);
   return x;
 }
@@ -234,7 +260,8 @@ __device__ __forceinline__ uint32_t at_chunk(int row, int c) {
 }
 
 template <typename T, bool F8, int D>
-__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a, int per) {
+__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a, int per, int box,
+                                                                   const __grid_constant__ CUtensorMap rows_map) {
   using S = Shape<D>;
   // FP8 values are exact in fp16 too, where the weights keep three more bits.
   using W = typename std::conditional<F8, __half, T>::type;
@@ -258,11 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   }
   if (tid == 0) {
     s_abort = 0;
-    mbar_init(smem_addr(&bars.q_full), 128);
+    mbar_init(smem_addr(&bars.q_full), kLoaders);
     mbar_init(smem_addr(&bars.q_empty), 1);
     mbar_init(smem_addr(&bars.done), 1);
     for (int i = 0; i < S::kRing; ++i) {
-      mbar_init(smem_addr(&bars.kv_full[i]), 128);
+      mbar_init(smem_addr(&bars.kv_full[i]), 1);
       mbar_init(smem_addr(&bars.kv_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -270,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       mbar_init(smem_addr(&bars.p_full[i]), 128);
       mbar_init(smem_addr(&bars.o_full[i]), 1);
     }
-    for (int i = 0; i < kMaskRing; ++i) mbar_init(smem_addr(&bars.mask_full[i]), 128);
+    for (int i = 0; i < kMaskRing; ++i) mbar_init(smem_addr(&bars.mask_full[i]), 1);
     fence_mbar_init();
   }
   pdl_wait();
@@ -312,6 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     w.q = read_request(a, w.r, false);
     w.x = tile_of(a, w.q, per, 0);
 
+    if (warp < kLoaderWarp)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+
     if (warp < kLoaderWarp) {
       // ---- softmax ------------------------------------------------------------
       const int side = warp >> 2;                      // 0: tile A, 1: tile B
@@ -345,32 +377,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           const int key0 = w.k_lo + j * kKeys;
           const bool check = (words[0] & words[1] & words[2] & words[3]) != 0xffffffffu || key0 + kKeys - 1 > lim_lo ||
                              (a.window > 0 && (int64_t)key0 <= (int64_t)lim_hi - a.window);
-          // Bits of the keys this row sees.
-          uint32_t see[4];
+          uint32_t x[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, x[c]);
+          tmem_wait_ld();
           if (check) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              see[c] = words[c] & bits_between(key0 + 32 * c, (int)max(low, (int64_t)0), lim + 1);
-          }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tmem_ld32(s_col + 32 * c, x);
-            tmem_wait_ld();
-            if (check) {
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t see = words[c] & bits_between(key0 + 32 * c, (int)max(low, (int64_t)0), lim + 1);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (!((see[c] >> i) & 1u)) x[i] = 0xff800000u;
+                if (!((see >> i) & 1u)) x[c][i] = 0xff800000u;
             }
-            float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[1]);
-#pragma unroll
-            for (int i = 2; i < 32; i += 2) {
-              m0 = fmaxf(m0, __uint_as_float(x[i]));
-              m1 = fmaxf(m1, __uint_as_float(x[i + 1]));
-            }
-            mx = fmaxf(mx, fmaxf(m0, m1));
           }
+          float mx4[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            mx4[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
+#pragma unroll
+            for (int i = 3; i + 1 < 32; i += 2)
+              mx4[c] = max3(mx4[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+            mx4[c] = fmaxf(mx4[c], __uint_as_float(x[c][31]));
+          }
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           mx *= sc;                                    // sc > 0
           if (__any_sync(0xffffffffu, mx > m + kLazy)) {
             const float mn = fmaxf(m, mx);
@@ -380,40 +409,34 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             if (j > 0) {
 #pragma unroll
               for (int c = 0; c < D / 32; ++c) {
-                uint32_t x[32];
-                tmem_ld32(o_col + 32 * c, x);
+                uint32_t y[32];
+                tmem_ld32(o_col + 32 * c, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                tmem_st32(o_col + 32 * c, x);
+                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                tmem_st32(o_col + 32 * c, y);
               }
             }
           }
           const float mz = m == -INFINITY ? 0.f : m;
           const unsigned long long sc2 = pk2(sc, sc), mz2 = pk2(-mz, -mz);
-          float l0 = 0.f, l1 = 0.f;
+          unsigned long long sum = pk2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t x[32], p[16];
-            tmem_ld32(s_col + 32 * c, x);
-            tmem_wait_ld();
-            if (check) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((see[c] >> i) & 1u)) x[i] = 0xff800000u;
-            }
+            uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float y0, y1;
-              upk2(fma2_rn(pk2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, mz2), y0, y1);
+              upk2(fma2_rn(pk2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), sc2, mz2), y0, y1);
               y0 = ex2(y0);
               y1 = ex2(y1);
-              l0 += y0;
-              l1 += y1;
+              sum = add2_rn(sum, pk2(y0, y1));
               p[i] = Vec<W>::pack2(y0, y1);
             }
             tmem_st16(s_col + 16 * c, p);
           }
+          float l0, l1;
+          upk2(sum, l0, l1);
           l += l0 + l1;
           tmem_wait_st();
           tc_fence_before();
@@ -487,25 +510,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       if (!ok) *abort_flag = 1;
     } else if (warp < kMmaWarp) {
       // ---- loads --------------------------------------------------------------
-      const int lt = tid - kLoaderWarp * 32;           // 0 .. 127
+      const int lt = tid - kLoaderWarp * 32;           // 0 .. kLoaders - 1
       constexpr int EB = F8 ? 1 : 2;
       const int64_t token_bytes = (int64_t)a.H * D * EB;
-      uint32_t n_load = 0, n_mask = 0, n_q = 0, n_told = 0;   // tiles issued, masks, query tiles, tiles signalled
+      uint32_t n_load = 0, n_q = 0;                    // K and V tiles, query tiles
+      uint32_t bulk = 0;                               // ring places whose last load was a bulk copy
       bool ok = true;                                  // the same in all loaders once they have agreed()
-      auto agreed = [&](bool mine_ok) {                // also a barrier of the four warps
+      auto agreed = [&](bool mine_ok) {                // also a barrier of the three warps
         uint32_t r;
         asm volatile(
             "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-            "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+            "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
             : "=r"(r)
-            : "r"(mine_ok ? 1u : 0u)
+            : "r"(mine_ok ? 1u : 0u), "n"(kLoaders)
             : "memory");
         return r != 0;
       };
-      auto tell = [&](uint32_t upto) {                 // tiles up to here have landed
-        fence_proxy_async_smem();
-        for (; n_told < upto; ++n_told) mbar_arrive(smem_addr(&bars.kv_full[n_told % S::kRing]));
-      };
+      auto barrier_loaders = [] { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kLoaders) : "memory"); };
       while (ok && w.next(a, per)) {
         const int n_tiles = w.tiles();
         if (n_tiles == 0) continue;
@@ -513,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         if (!ok) break;
         {
           constexpr int C = D / 8;                     // chunks of a row
-          for (int i = lt; i < kRows * C; i += 128) {
+          for (int i = lt; i < kRows * C; i += kLoaders) {
             const int row = i / C, c = i % C, tok = row / a.G;
             const bool in = row < w.rows;
             const uint8_t* src = a.q + (int64_t)(w.q.row0 + w.x.tok0 + (in ? tok : 0)) * a.q_stride +
@@ -528,76 +549,138 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         }
         const int32_t* table = a.block_table + (size_t)w.r * a.max_blocks;
         const uint8_t* kbase = a.k_cache + (size_t)w.head * D * EB;
-        int32_t id = -1, off = 0;
-        auto look_up = [&](int j) {                    // this thread's key of tile j
-          const int p = w.k_lo + j * kKeys + lt;
-          id = -1;
-          if (j < n_tiles && p < w.k_hi) {
-            const int b = p / a.block_size;
-            off = p - b * a.block_size;
-            id = table[b];
-            if (id < 0 || id >= a.num_blocks) {
-              latch(a.status, IS_ST_BLOCK_ID);
-              id = -1;
+        // Block ids of this thread's keys of the next tile: lt, and lt + 96 for the first warp.
+        int32_t id[2];
+        auto look_up = [&](int j) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int p = w.k_lo + j * kKeys + lt + e * kLoaders;
+            id[e] = -1;
+            if (j < n_tiles && p < w.k_hi && lt + e * kLoaders < kKeys) {
+              id[e] = table[p / a.block_size];
+              if (id[e] < 0 || id[e] >= a.num_blocks) {
+                latch(a.status, IS_ST_BLOCK_ID);
+                id[e] = -1;
+              }
             }
           }
         };
         look_up(0);
         bool here = true;                              // this thread's waits
-        for (int j = 0; j < n_tiles; ++j) {
-          const long long at_key = id < 0 ? -1ll : ((long long)id * a.block_size + off) * token_bytes;
-          const uint32_t named = __ballot_sync(0xffffffffu, at_key >= 0);
-          ok = agreed(here);                           // and the last tile's offsets have been read
-          if (!ok) break;
-          s_off[lt] = at_key;
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          look_up(j + 1);
-          for (int kv = 0; kv < 2; ++kv, ++n_load) {
-            const int buf = n_load % S::kRing;
-            here = wait_or_abort(smem_addr(&bars.kv_empty[buf]), ((n_load / S::kRing) & 1u) ^ 1u, abort_flag, kWaitBudgetNs);
-            if (!here) break;
-            if (kv == 0) {
-              // The mask slot was last read four tiles ago: that tile's V has been released.
-              if (lane == 0) s_mask[n_mask % kMaskRing][warp - kLoaderWarp] = named;
-              mbar_arrive(smem_addr(&bars.mask_full[n_mask % kMaskRing]));
-              ++n_mask;
+        auto room = [&](uint32_t n) {                  // the ring's place of load n is free
+          here = here && wait_or_abort(smem_addr(&bars.kv_empty[n % S::kRing]), ((n / S::kRing) & 1u) ^ 1u, abort_flag,
+                                       kWaitBudgetNs);
+          return here;
+        };
+        for (int j = 0; j < n_tiles; ++j, n_load += 2) {
+          const int key0 = w.k_lo + j * kKeys;
+          const uint32_t slot = (n_load >> 1) % kMaskRing;   // last read four tiles ago: that tile's V has been released
+          const bool full = agreed(id[0] >= 0 && (id[1] >= 0 || lt >= kKeys - kLoaders)) && box > 0;
+          if (full) {
+            // Every key exists and is named: bulk tensor copies, `box` rows of 64 elements each.
+            look_up(j + 1);
+            if (warp == kLoaderWarp) {
+              const int groups = kKeys / box, g = lane / S::kHalves, half = lane % S::kHalves;
+              int64_t token = 0;
+              if (lane < groups * S::kHalves) {
+                const int p = key0 + g * box, b = p / a.block_size;
+                token = (int64_t)table[b] * a.block_size + (p - b * a.block_size);
+              }
+              for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t place = (n_load + kv) % S::kRing, bar = smem_addr(&bars.kv_full[place]);
+                if (!__all_sync(0xffffffffu, room(n_load + kv))) break;
+                if (lane == 0) {
+                  if (kv == 0) {
+                    *reinterpret_cast<uint4*>(s_mask[slot]) = make_uint4(~0u, ~0u, ~0u, ~0u);
+                    mbar_arrive(smem_addr(&bars.mask_full[slot]));
+                  }
+                  mbar_expect_tx(bar, S::kTileBytes);
+                }
+                __syncwarp();
+                if (lane < groups * S::kHalves)
+                  tma_load_rows(ring0 + place * S::kTileBytes + half * S::kHalfBytes + g * box * 128, &rows_map, half * 64,
+                                w.head, (int)(token + (kv ? (int64_t)a.num_blocks * a.block_size : 0)), bar);
+                bulk |= 1u << place;
+              }
             }
-            const uint32_t dst = ring0 + buf * S::kTileBytes;
-            const uint8_t* src0 = kbase + (kv ? a.v_offset : 0);
-            if constexpr (!F8) {
-              constexpr int C = D / 8, RP = 128 / C;   // chunks of a row; rows of one pass of the loaders
+            continue;
+          }
+          // A tile with missing keys, a block size the copies do not fit, or FP8 rows.
+          long long at_key[2];
+          uint32_t named[2];
 #pragma unroll
-              for (int i = 0; i < 128 / RP; ++i) {
-                const int row = i * RP + lt / C, c = lt % C;
+          for (int e = 0; e < 2; ++e) {
+            const int p = key0 + lt + e * kLoaders;
+            at_key[e] = id[e] < 0 ? -1ll : ((long long)id[e] * a.block_size + p % a.block_size) * token_bytes;
+            named[e] = __ballot_sync(0xffffffffu, at_key[e] >= 0);
+          }
+          ok = agreed(room(n_load));                   // and the last tile's offsets have been read
+          if (!ok) break;
+          s_off[lt] = at_key[0];
+          if (lt < kKeys - kLoaders) s_off[lt + kLoaders] = at_key[1];
+          if (lane == 0) s_mask[slot][warp - kLoaderWarp] = named[0];
+          if (lt == 0) s_mask[slot][3] = named[1];
+          look_up(j + 1);
+          barrier_loaders();
+          if (lt == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
+          for (int kv = 0; kv < 2; ++kv) {
+            if (kv == 1) {
+              ok = agreed(room(n_load + 1));
+              if (!ok) break;
+            }
+            const uint32_t place = (n_load + kv) % S::kRing, dst = ring0 + place * S::kTileBytes;
+            const uint8_t* src0 = kbase + (kv ? a.v_offset : 0);
+            bulk &= ~(1u << place);
+            if constexpr (!F8) {
+              constexpr int C = D / 8, RP = kLoaders / C;   // chunks of a row; rows of one pass of the loaders
+              const int c = lt % C;
+#pragma unroll 4
+              for (int row = lt / C; row < kKeys; row += RP) {
                 const long long o = s_off[row];
                 cp_async16(dst + at_chunk<D>(row, c), src0 + (o < 0 ? 0 : o) + c * 16, o >= 0);
               }
               cp_async_commit();
-              if (n_load - n_told >= (uint32_t)S::kLag) {
-                cp_async_wait<S::kLag>();
-                tell(n_load + 1 - S::kLag);
-              }
+              cp_async_wait<0>();
             } else {
-              constexpr int C = D / 16, RP = 128 / C;  // 16-byte chunks of an FP8 row
-              uint4 x[128 / RP];
+              constexpr int C = D / 16, RP = kLoaders / C;  // 16-byte chunks of an FP8 row
+              constexpr int N = (kKeys + RP - 1) / RP;
+              const int c = lt % C;
+              uint4 x[N];
 #pragma unroll
-              for (int i = 0; i < 128 / RP; ++i) {
-                const long long o = s_off[i * RP + lt / C];
-                x[i] = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src0 + o + (lt % C) * 16);
+              for (int i = 0; i < N; ++i) {
+                const int row = i * RP + lt / C;
+                const long long o = row < kKeys ? s_off[row] : -1ll;
+                x[i] = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src0 + o + c * 16);
               }
 #pragma unroll
-              for (int i = 0; i < 128 / RP; ++i) {
-                const int row = i * RP + lt / C, c = lt % C;
-                st_shared_v4(dst + at_chunk<D>(row, 2 * c), kv ? widen8<W>(x[i].x, x[i].y) : widen8<T>(x[i].x, x[i].y));
-                st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), kv ? widen8<W>(x[i].z, x[i].w) : widen8<T>(x[i].z, x[i].w));
+              for (int i = 0; i < N; ++i) {
+                const int row = i * RP + lt / C;
+                if (row < kKeys) {
+                  st_shared_v4(dst + at_chunk<D>(row, 2 * c), kv ? widen8<W>(x[i].x, x[i].y) : widen8<T>(x[i].x, x[i].y));
+                  st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), kv ? widen8<W>(x[i].z, x[i].w) : widen8<T>(x[i].z, x[i].w));
+                }
               }
-              tell(n_load + 1);
             }
+            fence_proxy_async_smem();
+            barrier_loaders();
+            if (lt == 0) mbar_arrive(smem_addr(&bars.kv_full[place]));
           }
+          if (!ok) break;
         }
         ok = ok && agreed(here);
-        cp_async_wait<0>();
-        tell(n_load);
+      }
+      // After a time-out bulk copies may be in flight that no MMA waited for:
+      // they land before shared memory is let go.
+      if (!ok && lt == 0) {
+        for (int i = 0; i < S::kRing; ++i) {
+          const uint32_t top = n_load + 1;             // no load beyond this one was issued
+          uint32_t n = top / S::kRing * S::kRing + i;
+          if (n > top) n -= S::kRing;
+          if ((bulk >> i) & 1u) {
+            mbar_wait_bounded(smem_addr(&bars.kv_full[i]), (n / S::kRing) & 1u, kWaitBudgetNs);
+            mbar_wait_bounded(smem_addr(&bars.kv_full[i]), ((n / S::kRing) & 1u) ^ 1u, kWaitBudgetNs / 64);
+          }
+        }
       }
       cp_async_wait<0>();
       if (!ok) *abort_flag = 1;
@@ -687,9 +770,20 @@ static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
   constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - kMaxCtas * kRecordBytes) / (2 * sizeof(Partial<prompt::kRows, D>)));
   const int grid = std::max(1, std::min({cfg.num_sms, kFit, kMaxCtas}));
   const int per = prompt::kRows / a.G;   // tokens of an item
-  e = launch_ex(kern, dim3(grid), dim3(prompt::kThreads), S::kSmem, cfg.stream, cfg.pdl, a, per);
+  // Bulk copies bring `box` rows at once: a block, or 128 rows of a longer one.
+  // They need blocks that divide a tile or consist of tiles, 8 rows at least (the
+  // swizzle's period), and 16-bit rows; other caches take the row copies.
+  int box = 0;
+  CUtensorMap map;
+  std::memset(&map, 0, sizeof map);
+  if (!F8 && a.block_size >= 8 && (prompt::kKeys % a.block_size == 0 || a.block_size % prompt::kKeys == 0)) {
+    box = std::min(a.block_size, prompt::kKeys);
+    if (!make_rows_map(&map, a.k_cache, a.D, a.H, 2LL * a.num_blocks * a.block_size, box, a.dtype)) box = 0;
+  }
+  e = launch_ex(kern, dim3(grid), dim3(prompt::kThreads), S::kSmem, cfg.stream, cfg.pdl, a, per, box, map);
   if (e != cudaSuccess) return e;
-  return launch_ex(attend_join_kernel<T, prompt::kRows, D>, dim3(grid, 8), dim3(kJoinThreads), 0, cfg.stream, cfg.pdl, a);
+  return launch_ex(attend_join_rows_kernel<T, prompt::kRows, D>, dim3(grid, 8), dim3(kJoinThreads), 0, cfg.stream,
+                   cfg.pdl, a);
 }
 
 cudaError_t launch_attend_prompt(const AttendArgs& a, const LaunchCfg& cfg) {
