@@ -17,7 +17,7 @@
 //               with missing keys (zero-filled) and block sizes those do not
 //               fit with 16-byte asynchronous copies, row by row; FP8 rows
 //               through registers, widened on the way (exactly)
-//   warp 11     one thread issues the MMAs
+//   warp 11     one elected thread issues the MMAs
 // Tensor memory (512 columns): S_A, S_B (128 each; P takes the first half of
 // its S as 16-bit pairs), O_A, O_B (D each).  Shared memory: Q (2 x 128 rows),
 // then a ring of 128-key tiles, K and V in turn.  Rows are stored as 64-element
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       constexpr int EB = F8 ? 1 : 2;
       const int64_t token_bytes = (int64_t)a.H * D * EB;
       uint32_t n_load = 0, n_q = 0;                    // K and V tiles, query tiles
-      uint32_t bulk = 0;                               // ring places whose last load was a bulk copy
+      uint32_t bulk = 0;                               // lane i: 1 + the last load of place i if that was a bulk copy
       bool ok = true;                                  // the same in all loaders once they have agreed()
       auto agreed = [&](bool mine_ok) {                // also a barrier of the three warps
         uint32_t r;
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 if (lane < groups * S::kHalves)
                   tma_load_rows(ring0 + place * S::kTileBytes + half * S::kHalfBytes + g * box * 128, &rows_map, half * 64,
                                 w.head, (int)(token + (kv ? (int64_t)a.num_blocks * a.block_size : 0)), bar);
-                bulk |= 1u << place;
+                if (lane == (int)place) bulk = n_load + kv + 1;
               }
             }
             continue;
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
             const uint32_t place = (n_load + kv) % S::kRing, dst = ring0 + place * S::kTileBytes;
             const uint8_t* src0 = kbase + (kv ? a.v_offset : 0);
-            bulk &= ~(1u << place);
+            if (lane == (int)place) bulk = 0;
             if constexpr (!F8) {
               constexpr int C = D / 8, RP = kLoaders / C;   // chunks of a row; rows of one pass of the loaders
               const int c = lt % C;
@@ -671,35 +671,45 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       }
       // After a time-out bulk copies may be in flight that no MMA waited for:
       // they land before shared memory is let go.
-      if (!ok && lt == 0) {
-        for (int i = 0; i < S::kRing; ++i) {
-          const uint32_t top = n_load + 1;             // no load beyond this one was issued
-          uint32_t n = top / S::kRing * S::kRing + i;
-          if (n > top) n -= S::kRing;
-          if ((bulk >> i) & 1u) {
-            mbar_wait_bounded(smem_addr(&bars.kv_full[i]), (n / S::kRing) & 1u, kWaitBudgetNs);
-            mbar_wait_bounded(smem_addr(&bars.kv_full[i]), ((n / S::kRing) & 1u) ^ 1u, kWaitBudgetNs / 64);
-          }
-        }
-      }
+      if (!ok && warp == kLoaderWarp && bulk > 0)
+        mbar_wait_bounded(smem_addr(&bars.kv_full[lane]), ((bulk - 1) / S::kRing) & 1u, kWaitBudgetNs);
+      __syncwarp();
       cp_async_wait<0>();
       if (!ok) *abort_flag = 1;
-    } else if (lane == 0) {
+    } else {
       // ---- MMAs ----------------------------------------------------------------
+      // The whole warp walks along and one elected lane issues: with the branch
+      // on elect.sync and descriptors that are sums of uniform values the
+      // compiler keeps them in uniform registers.  Branching on a lane number
+      // made one M128 N128 K16 MMA cost 72 to 97 clocks to issue; it takes 64.
       constexpr uint32_t kIdS = idesc_of<T>(128, false), kIdO = idesc_of<W>(D, true);
-      uint32_t n_kv = 0, n_q = 0, n_p[2] = {0, 0};
+      uint32_t leader;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), q_tile = __shfl_sync(0xffffffffu, tiles0, 0);
+      const uint64_t q_desc = sw128_desc(q_tile), k_desc = sw128_desc(q_tile + 2 * S::kTileBytes);
+      const uint64_t v_desc0 = v_desc<D>(q_tile + 2 * S::kTileBytes);
+      uint32_t n_q = 0, n_p[2] = {0, 0};
+      uint32_t place = 0, turn = 0;                    // of the next load: its place in the ring, and the ring's turn
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && wait_or_abort(smem_addr(bar), parity, abort_flag, kWaitBudgetNs);
+        ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, kWaitBudgetNs));
         return ok;
       };
-      auto scores = [&](int side, uint32_t k_tile) {
+      auto commit = [&](uint64_t* bar) {
+        if (leader) mma_commit(smem_addr(bar));
+      };
+      auto scores = [&](int side, uint32_t k_place) {
+        if (leader) {
+          const uint64_t qd = q_desc + (uint32_t)side * (S::kTileBytes >> 4), kd = k_desc + k_place * (S::kTileBytes >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = (uint32_t)(k >> 2) * S::kHalfBytes + 32u * (k & 3);
-          mma_ss(tmem + 128u * side, sw128_desc(tiles0 + side * S::kTileBytes + o), sw128_desc(k_tile + o), kIdS, k != 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = ((uint32_t)(k >> 2) * S::kHalfBytes + 32u * (k & 3)) >> 4;
+            mma_ss(tm + 128u * side, qd + o, kd + o, kIdS, k != 0);
+          }
+          mma_commit(smem_addr(&bars.s_full[side]));
         }
-        mma_commit(smem_addr(&bars.s_full[side]));
+        __syncwarp();
       };
       while (ok && w.next(a, per)) {
         const int n_tiles = w.tiles();
@@ -707,39 +717,51 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         const int sides = w.rows > 128 ? 2 : 1;
         if (!wait(&bars.q_full, n_q & 1u)) break;
         ++n_q;
-        if (!wait(&bars.kv_full[n_kv % S::kRing], (n_kv / S::kRing) & 1u)) break;
+        if (!wait(&bars.kv_full[place], turn)) break;
         tc_fence_after();
-        for (int side = 0; side < sides; ++side) scores(side, ring0 + (n_kv % S::kRing) * S::kTileBytes);
-        mma_commit(smem_addr(&bars.kv_empty[n_kv % S::kRing]));
+        for (int side = 0; side < sides; ++side) scores(side, place);
+        commit(&bars.kv_empty[place]);
         for (int j = 0; j < n_tiles && ok; ++j) {
-          const uint32_t nv = n_kv + 1, nk = n_kv + 2;   // V of this tile, K of the next
-          const uint32_t v_tile = ring0 + (nv % S::kRing) * S::kTileBytes;
-          if (!wait(&bars.kv_full[nv % S::kRing], (nv / S::kRing) & 1u)) break;
+          // V of this tile, then K of the next
+          if (++place == S::kRing) {
+            place = 0;
+            turn ^= 1u;
+          }
+          const uint32_t v_place = place;
+          if (!wait(&bars.kv_full[v_place], turn)) break;
+          if (++place == S::kRing) {
+            place = 0;
+            turn ^= 1u;
+          }
           for (int side = 0; side < sides; ++side) {
             if (!wait(&bars.p_full[side], n_p[side] & 1u)) break;
             ++n_p[side];
             tc_fence_after();
+            if (leader) {
+              const uint64_t vd = v_desc0 + v_place * (S::kTileBytes >> 4);
+              const uint32_t o_tm = tm + S::kOCol + (uint32_t)(D * side), p_tm = tm + 128u * side;
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmem + S::kOCol + (uint32_t)(D * side), tmem + 128u * side + 8u * k, v_desc<D>(v_tile + 2048u * k), kIdO,
-                     (j | k) != 0);
-            if (side == sides - 1) mma_commit(smem_addr(&bars.kv_empty[nv % S::kRing]));
+              for (int k = 0; k < kKeys / 16; ++k) mma_ts(o_tm, p_tm + 8u * k, vd + 128u * k, kIdO, (j | k) != 0);
+            }
+            __syncwarp();
+            if (side == sides - 1) commit(&bars.kv_empty[v_place]);
             if (j == n_tiles - 1) {
-              mma_commit(smem_addr(&bars.o_full[side]));
+              commit(&bars.o_full[side]);
             } else {
-              if (side == 0 && !wait(&bars.kv_full[nk % S::kRing], (nk / S::kRing) & 1u)) break;
-              if (side == 0) tc_fence_after();
-              scores(side, ring0 + (nk % S::kRing) * S::kTileBytes);
-              if (side == sides - 1) mma_commit(smem_addr(&bars.kv_empty[nk % S::kRing]));
+              if (side == 0) {
+                if (!wait(&bars.kv_full[place], turn)) break;
+                tc_fence_after();
+              }
+              scores(side, place);
+              if (side == sides - 1) commit(&bars.kv_empty[place]);
             }
           }
-          n_kv += 2;
         }
-        if (ok) mma_commit(smem_addr(&bars.q_empty));
+        if (ok) commit(&bars.q_empty);
       }
       if (!ok) *abort_flag = 1;
       // Every MMA issued has ended before tensor and shared memory are let go.
-      mma_commit(smem_addr(&bars.done));
+      commit(&bars.done);
       mbar_wait_bounded(smem_addr(&bars.done), 0, kWaitBudgetNs);
     }
     __syncwarp();
