@@ -60,8 +60,10 @@ constexpr uint32_t kTmemAll = 512;
 template <int D>
 struct Shape {
   static constexpr int kHalves = D / 64;
-  static constexpr uint32_t kHalfBytes = 128 * 128;           // 128 rows of 64 elements
-  static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
+  // A tile is 16 groups of 8 rows; a group holds the 64-element halves of its
+  // rows one after the other, 1024 bytes each (one swizzle atom).
+  static constexpr uint32_t kGroupBytes = kHalves * 1024;
+  static constexpr uint32_t kTileBytes = 16 * kGroupBytes;
   static constexpr int kRing = D == 128 ? 5 : 8;              // K and V tiles in flight
   static constexpr size_t kSmem = 1024 + (2 + kRing) * (size_t)kTileBytes + 128 * 8;
   static constexpr uint32_t kOCol = 256;                      // first column of O_A; O_B follows D columns on
@@ -112,11 +114,11 @@ __device__ __forceinline__ unsigned long long add2_rn(unsigned long long a, unsi
   return d;
 }
 
-// Rows of one half head: elements x .. x + 63 of head h of consecutive tokens from t on.
-__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int x, int h, int t, uint32_t bar) {
+// Groups of 8 tokens from group t8 on, all of head h (make_rows_map).
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int h, int t8, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t), "r"(bar)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], "
+      "[%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(h), "r"(t8), "r"(bar)
       : "memory");
 }
 
@@ -137,17 +139,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-// Descriptor of V for O += P V: K (keys) runs over 128-byte rows, eight to a
-// swizzle atom (stride byte offset 1024), N over the 64 elements of a row and
-// then the halves (leading byte offset).
+// Descriptors of 128-byte-swizzled tiles (version 1, layout type 2).  Q and K
+// are K-major: groups of 8 rows follow one another (stride byte offset).  For
+// O += P V the keys are K: again 8 to a group (stride byte offset), and N runs
+// over the 64 elements of a row and then the halves (leading byte offset).
 template <int D>
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(Shape<D>::kHalfBytes >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, uint32_t leading) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)leading << 16) |
+         ((uint64_t)(Shape<D>::kGroupBytes >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
 // kind::f16 instruction descriptor: D fp32 (bit 4), A and B fp16 or bf16
@@ -256,7 +255,8 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
 // Where 16-byte chunk c (8 elements) of row `row` lies in a tile.
 template <int D>
 __device__ __forceinline__ uint32_t at_chunk(int row, int c) {
-  return (uint32_t)(c >> 3) * Shape<D>::kHalfBytes + (uint32_t)row * 128u + (uint32_t)(((c & 7) ^ (row & 7)) * 16);
+  return (uint32_t)(row >> 3) * Shape<D>::kGroupBytes + (uint32_t)(c >> 3) * 1024u + (uint32_t)(row & 7) * 128u +
+         (uint32_t)(((c & 7) ^ (row & 7)) * 16);
 }
 
 template <typename T, bool F8, int D>
@@ -514,7 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       constexpr int EB = F8 ? 1 : 2;
       const int64_t token_bytes = (int64_t)a.H * D * EB;
       uint32_t n_load = 0, n_q = 0;                    // K and V tiles, query tiles
-      uint32_t bulk = 0;                               // lane i: 1 + the last load of place i if that was a bulk copy
+      uint32_t bulk = 0;                               // lane i: 1 + this warp's last load into place i if that was a bulk copy
+      uint32_t leader;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
       bool ok = true;                                  // the same in all loaders once they have agreed()
       auto agreed = [&](bool mine_ok) {                // also a barrier of the three warps
         uint32_t r;
@@ -549,7 +552,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         }
         const int32_t* table = a.block_table + (size_t)w.r * a.max_blocks;
         const uint8_t* kbase = a.k_cache + (size_t)w.head * D * EB;
-        // Block ids of this thread's keys of the next tile: lt, and lt + 96 for the first warp.
+        // Bulk copies: lane g of each warp finds the token of row group g (`box` rows) of a tile, one tile ahead;
+        // -1 if the tile is not whole.
+        const int groups = box > 0 ? kKeys / box : 0;
+        int64_t token = -1;
+        auto look_up_groups = [&](int j) {
+          const int key0 = w.k_lo + j * kKeys, p = key0 + lane * box;
+          token = -1;
+          if (lane < groups && j < n_tiles && key0 + kKeys <= w.k_hi) {
+            const int b = p / a.block_size;
+            const int32_t id = table[b];
+            if (id >= 0 && id < a.num_blocks) token = (int64_t)id * a.block_size + (p - b * a.block_size);
+          }
+        };
+        // Row copies: block ids of this thread's keys of a tile: lt, and lt + 96 for the first warp.
         int32_t id[2];
         auto look_up = [&](int j) {
 #pragma unroll
@@ -565,7 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
           }
         };
-        look_up(0);
+        if (box > 0) look_up_groups(0);
+        else look_up(0);
         bool here = true;                              // this thread's waits
         auto room = [&](uint32_t n) {                  // the ring's place of load n is free
           here = here && wait_or_abort(smem_addr(&bars.kv_empty[n % S::kRing]), ((n / S::kRing) & 1u) ^ 1u, abort_flag,
@@ -575,21 +592,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         for (int j = 0; j < n_tiles; ++j, n_load += 2) {
           const int key0 = w.k_lo + j * kKeys;
           const uint32_t slot = (n_load >> 1) % kMaskRing;   // last read four tiles ago: that tile's V has been released
-          const bool full = agreed(id[0] >= 0 && (id[1] >= 0 || lt >= kKeys - kLoaders)) && box > 0;
-          if (full) {
-            // Every key exists and is named: bulk tensor copies, `box` rows of 64 elements each.
-            look_up(j + 1);
-            if (warp == kLoaderWarp) {
-              const int groups = kKeys / box, g = lane / S::kHalves, half = lane % S::kHalves;
-              int64_t token = 0;
-              if (lane < groups * S::kHalves) {
-                const int p = key0 + g * box, b = p / a.block_size;
-                token = (int64_t)table[b] * a.block_size + (p - b * a.block_size);
-              }
-              for (int kv = 0; kv < 2; ++kv) {
+          if (box > 0) {
+            const int64_t from = token;
+            const bool whole_tile = agreed(lane >= groups || from >= 0);
+            look_up_groups(j + 1);
+            if (whole_tile) {
+              // The first loader warp brings K, the second V; one elected lane issues.
+              const int kv = warp - kLoaderWarp;
+              if (kv < 2 && __all_sync(0xffffffffu, room(n_load + kv))) {
                 const uint32_t place = (n_load + kv) % S::kRing, bar = smem_addr(&bars.kv_full[place]);
-                if (!__all_sync(0xffffffffu, room(n_load + kv))) break;
-                if (lane == 0) {
+                const int t8 = (int)((from + (kv ? (int64_t)a.num_blocks * a.block_size : 0)) >> 3);
+                if (leader) {
                   if (kv == 0) {
                     *reinterpret_cast<uint4*>(s_mask[slot]) = make_uint4(~0u, ~0u, ~0u, ~0u);
                     mbar_arrive(smem_addr(&bars.mask_full[slot]));
@@ -597,13 +610,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                   mbar_expect_tx(bar, S::kTileBytes);
                 }
                 __syncwarp();
-                if (lane < groups * S::kHalves)
-                  tma_load_rows(ring0 + place * S::kTileBytes + half * S::kHalfBytes + g * box * 128, &rows_map, half * 64,
-                                w.head, (int)(token + (kv ? (int64_t)a.num_blocks * a.block_size : 0)), bar);
+                const uint32_t step = (uint32_t)(box >> 3) * S::kGroupBytes;
+                uint32_t dst = ring0 + place * S::kTileBytes;
+                for (int g = 0; g < groups; ++g, dst += step) {
+                  const int at8 = __shfl_sync(0xffffffffu, t8, g);
+                  if (leader) tma_load_rows(dst, &rows_map, w.head, at8, bar);
+                }
                 if (lane == (int)place) bulk = n_load + kv + 1;
               }
+              continue;
             }
-            continue;
+            look_up(j);
           }
           // A tile with missing keys, a block size the copies do not fit, or FP8 rows.
           long long at_key[2];
@@ -620,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           if (lt < kKeys - kLoaders) s_off[lt + kLoaders] = at_key[1];
           if (lane == 0) s_mask[slot][warp - kLoaderWarp] = named[0];
           if (lt == 0) s_mask[slot][3] = named[1];
-          look_up(j + 1);
+          if (box == 0) look_up(j + 1);
           barrier_loaders();
           if (lt == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
           for (int kv = 0; kv < 2; ++kv) {
@@ -671,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       }
       // After a time-out bulk copies may be in flight that no MMA waited for:
       // they land before shared memory is let go.
-      if (!ok && warp == kLoaderWarp && bulk > 0)
+      if (!ok && bulk > 0)
         mbar_wait_bounded(smem_addr(&bars.kv_full[lane]), ((bulk - 1) / S::kRing) & 1u, kWaitBudgetNs);
       __syncwarp();
       cp_async_wait<0>();
@@ -687,8 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       asm volatile(
           "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), q_tile = __shfl_sync(0xffffffffu, tiles0, 0);
-      const uint64_t q_desc = sw128_desc(q_tile), k_desc = sw128_desc(q_tile + 2 * S::kTileBytes);
-      const uint64_t v_desc0 = v_desc<D>(q_tile + 2 * S::kTileBytes);
+      const uint64_t q_desc = tile_desc<D>(q_tile, 1), k_desc = tile_desc<D>(q_tile + 2 * S::kTileBytes, 1);
+      const uint64_t v_desc = tile_desc<D>(q_tile + 2 * S::kTileBytes, 1024 >> 4);
       uint32_t n_q = 0, n_p[2] = {0, 0};
       uint32_t place = 0, turn = 0;                    // of the next load: its place in the ring, and the ring's turn
       bool ok = true;
@@ -704,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           const uint64_t qd = q_desc + (uint32_t)side * (S::kTileBytes >> 4), kd = k_desc + k_place * (S::kTileBytes >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = ((uint32_t)(k >> 2) * S::kHalfBytes + 32u * (k & 3)) >> 4;
+            const uint32_t o = ((uint32_t)(k >> 2) * 1024u + 32u * (k & 3)) >> 4;
             mma_ss(tm + 128u * side, qd + o, kd + o, kIdS, k != 0);
           }
           mma_commit(smem_addr(&bars.s_full[side]));
@@ -738,10 +755,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             ++n_p[side];
             tc_fence_after();
             if (leader) {
-              const uint64_t vd = v_desc0 + v_place * (S::kTileBytes >> 4);
+              const uint64_t vd = v_desc + v_place * (S::kTileBytes >> 4);
               const uint32_t o_tm = tm + S::kOCol + (uint32_t)(D * side), p_tm = tm + 128u * side;
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k) mma_ts(o_tm, p_tm + 8u * k, vd + 128u * k, kIdO, (j | k) != 0);
+              for (int k = 0; k < kKeys / 16; ++k) mma_ts(o_tm, p_tm + 8u * k, vd + 2u * k * (S::kGroupBytes >> 4), kIdO, (j | k) != 0);
             }
             __syncwarp();
             if (side == sides - 1) commit(&bars.kv_empty[v_place]);

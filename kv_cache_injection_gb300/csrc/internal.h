@@ -73,8 +73,9 @@ cudaError_t launch_plan(const PlanArgs& a, const LaunchCfg& cfg);
 // the packed queries, and the three launches (grouping, contraction, top-k).
 size_t operand_map_bytes();
 bool make_operand_map(void* map_out, const void* base, int E, int64_t rows, int box_rows);
-// Tensor map of a layer cache's rows, K then V: boxes of 64 elements of one head
-// of box_rows consecutive tokens, 128-byte-swizzled.
+// Tensor map of a layer cache's rows, K then V: coordinates (element of a
+// 64-element half, token of 8, half, head, group of 8 tokens), boxes of all of
+// one head of box_rows consecutive tokens, 128-byte-swizzled.  16-bit elements.
 bool make_rows_map(void* map_out, const void* base, int D, int H, int64_t tokens, int box_rows, int dtype);
 cudaError_t launch_group(const GroupArgs& ga, const LaunchCfg& cfg);
 cudaError_t launch_sim_gemm(const GemmArgs& gg, const void* map_emb, const void* map_q, int Q,

@@ -360,13 +360,14 @@ bool make_operand_map(void* map_out, const void* base, int E, int64_t rows, int 
 
 bool make_rows_map(void* map_out, const void* base, int D, int H, int64_t tokens, int box_rows, int dtype) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (!fn || tokens <= 0 || tokens > INT32_MAX) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * H * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
-  const cuuint32_t estr[3] = {1, 1, 1};
+  if (!fn || tokens <= 0 || tokens % 8 != 0 || tokens / 8 > INT32_MAX) return false;
+  const cuuint64_t row = (cuuint64_t)D * H * 2;
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)D / 64, (cuuint64_t)H, (cuuint64_t)tokens / 8};
+  const cuuint64_t strides[4] = {row, 128, (cuuint64_t)D * 2, row * 8};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)D / 64, 1, (cuuint32_t)box_rows / 8};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(reinterpret_cast<CUtensorMap*>(map_out),
-                        dtype == IS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                        dtype == IS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
