@@ -83,14 +83,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -221,10 +220,24 @@ struct Walk {
   __device__ __forceinline__ int tiles() const { return k_hi > k_lo ? (k_hi - k_lo + kKeys - 1) / kKeys : 0; }
 };
 
+// One segment (a run's share of one item) as its workers need it, handed from
+// the loaders to the softmax and MMA warps through a ring in shared memory, so
+// that the walk costs those no registers.
+struct Segment {
+  int32_t tiles;         // -1: the run has ended
+  int32_t k_lo, rows;
+  int32_t lim0;          // position of the item's first token
+  int32_t head;
+  int32_t row0;          // first query row
+  int32_t slot;          // of the partial result; -1: the item is whole
+};
+constexpr int kSegments = 4;
+
 struct Bars {
   uint64_t q_full, q_empty, done;
+  uint64_t seg_full[kSegments], seg_empty[kSegments];
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];   // P in two halves of 64 keys
   uint64_t mask_full[kMaskRing];
 };
 
@@ -273,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   __shared__ int64_t scratch[33];
   __shared__ int64_t s_base;
   __shared__ int32_t s_req;
+  __shared__ Segment s_seg[kSegments];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &s_abort;
   const uint32_t tiles0 = (smem_addr(smem_raw) + 1023u) & ~1023u;     // Q_A, Q_B, then the ring
@@ -294,10 +308,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&bars.s_full[i]), 1);
-      mbar_init(smem_addr(&bars.p_full[i]), 128);
+      mbar_init(smem_addr(&bars.p_full[i][0]), 4);
+      mbar_init(smem_addr(&bars.p_full[i][1]), 4);
       mbar_init(smem_addr(&bars.o_full[i]), 1);
     }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(smem_addr(&bars.mask_full[i]), 1);
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(smem_addr(&bars.seg_full[i]), 1);
+      mbar_init(smem_addr(&bars.seg_empty[i]), 9);     // eight softmax warps, the MMA warp
+    }
     fence_mbar_init();
   }
   pdl_wait();
@@ -333,12 +352,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   if (idle) {
     if (tid == 0) record_of(a, blockIdx.x)->parts = 0;
   } else {
-    w.r = s_req;
-    w.base = s_base;
-    w.t = 0;
-    w.q = read_request(a, w.r, false);
-    w.x = tile_of(a, w.q, per, 0);
-
     if (warp < kLoaderWarp)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     else
@@ -350,77 +363,88 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
       const uint32_t s_col = tmem + lanes + 128u * side, o_col = tmem + lanes + S::kOCol + (uint32_t)(D * side);
       const float sc = a.scale * kLog2e;
+      const int row = side * 128 + (warp & 3) * 32 + lane, tok = row / a.G;
       uint32_t n_s = 0, n_o = 0, n_mask = 0;           // phases consumed
       bool ok = true;
-      while (ok && w.next(a, per)) {
-        const int n_tiles = w.tiles();
-        const int row = side * 128 + (warp & 3) * 32 + lane;
-        const bool mine_has = side == 0 || w.rows > 128;   // the tile has rows
-        const int tok = row / a.G;
-        const int lim = row < w.rows ? w.q.seq - w.q.n + w.x.tok0 + tok : -1;
-        // the warp's first and last positions, for skipping the masks
-        const int lim_lo = __reduce_min_sync(0xffffffffu, row < w.rows ? lim : INT32_MAX);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, kWaitBudgetNs));
+        return ok;
+      };
+      for (uint32_t n_seg = 0;; ++n_seg) {
+        if (!wait(&bars.seg_full[n_seg % kSegments], (n_seg / kSegments) & 1u)) break;
+        const Segment& g = s_seg[n_seg % kSegments];
+        const int n_tiles = g.tiles;
+        if (n_tiles < 0) break;
+        const bool has = g.rows > 128 * side;          // the side has rows
+        const bool live = row < g.rows;
+        // The row's last key, and the warp's smallest and largest, for skipping the masks.
+        const int lim = live ? g.lim0 + tok : -1;
+        const int lim_lo = __reduce_min_sync(0xffffffffu, live ? lim : INT32_MAX);
         const int lim_hi = __reduce_max_sync(0xffffffffu, lim);
-        const int64_t low = a.window > 0 ? (int64_t)lim - a.window + 1 : 0;
+        const int low = a.window > 0 ? (int)max((int64_t)lim - a.window + 1, (int64_t)0) : 0;
+        const int low_hi = a.window > 0 ? (int)max((int64_t)lim_hi - a.window + 1, (int64_t)0) : 0;
         float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < n_tiles; ++j, ++n_mask) {
-          if (!mine_has) continue;
+        if (!has) n_mask += n_tiles;
+        for (int j = 0, key0 = g.k_lo; has && j < n_tiles; ++j, ++n_mask, key0 += kKeys) {
           const int slot = n_mask % kMaskRing;
-          ok = wait_or_abort(smem_addr(&bars.mask_full[slot]), (n_mask / kMaskRing) & 1u, abort_flag, kWaitBudgetNs) &&
-               wait_or_abort(smem_addr(&bars.s_full[side]), n_s & 1u, abort_flag, kWaitBudgetNs);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          if (!wait(&bars.mask_full[slot], (n_mask / kMaskRing) & 1u) || !wait(&bars.s_full[side], n_s & 1u)) break;
           ++n_s;
           tc_fence_after();
-          const uint4 mw = *reinterpret_cast<const uint4*>(s_mask[slot]);
-          const uint32_t words[4] = {mw.x, mw.y, mw.z, mw.w};
-          const int key0 = w.k_lo + j * kKeys;
-          const bool check = (words[0] & words[1] & words[2] & words[3]) != 0xffffffffu || key0 + kKeys - 1 > lim_lo ||
-                             (a.window > 0 && (int64_t)key0 <= (int64_t)lim_hi - a.window);
           uint32_t x[4][32];
+          tmem_ld32(s_col, x[0]);
+          tmem_ld32(s_col + 32, x[1]);
+          const uint4 mw = *reinterpret_cast<const uint4*>(s_mask[slot]);
+          const bool check = (mw.x & mw.y & mw.z & mw.w) != 0xffffffffu || key0 + kKeys - 1 > lim_lo || key0 < low_hi;
+          auto hide = [&](uint32_t(&y)[32], uint32_t word, int at) {
+            const uint32_t see = word & bits_between(at, low, lim + 1);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, x[c]);
+            for (int i = 0; i < 32; ++i)
+              if (!((see >> i) & 1u)) y[i] = 0xff800000u;
+          };
+          auto top = [](const uint32_t(&y)[32]) {
+            float t0 = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
+            float t1 = max3(__uint_as_float(y[3]), __uint_as_float(y[4]), __uint_as_float(y[5]));
+#pragma unroll
+            for (int i = 6; i + 3 < 32; i += 4) {
+              t0 = max3(t0, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+              t1 = max3(t1, __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
+            }
+            return max3(max3(t0, t1, __uint_as_float(y[30])), __uint_as_float(y[31]), t0);
+          };
+          tmem_wait_ld();
+          tmem_ld32(s_col + 64, x[2]);
+          tmem_ld32(s_col + 96, x[3]);
+          if (check) {
+            hide(x[0], mw.x, key0);
+            hide(x[1], mw.y, key0 + 32);
+          }
+          float mx = fmaxf(top(x[0]), top(x[1]));
           tmem_wait_ld();
           if (check) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t see = words[c] & bits_between(key0 + 32 * c, (int)max(low, (int64_t)0), lim + 1);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((see >> i) & 1u)) x[c][i] = 0xff800000u;
-            }
+            hide(x[2], mw.z, key0 + 64);
+            hide(x[3], mw.w, key0 + 96);
           }
-          float mx4[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            mx4[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
-#pragma unroll
-            for (int i = 3; i + 1 < 32; i += 2)
-              mx4[c] = max3(mx4[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-            mx4[c] = fmaxf(mx4[c], __uint_as_float(x[c][31]));
-          }
-          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          mx *= sc;                                    // sc > 0
+          mx = fmaxf(mx, fmaxf(top(x[2]), top(x[3]))) * sc;   // sc > 0
           if (__any_sync(0xffffffffu, mx > m + kLazy)) {
             const float mn = fmaxf(m, mx);
             const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
             m = mn;
             l *= f;
             if (j > 0) {
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t y[32];
-                tmem_ld32(o_col + 32 * c, y);
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t y[16];
+                tmem_ld16(o_col + 16 * c, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-                tmem_st32(o_col + 32 * c, y);
+                for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                tmem_st16(o_col + 16 * c, y);
               }
             }
           }
           const float mz = m == -INFINITY ? 0.f : m;
           const unsigned long long sc2 = pk2(sc, sc), mz2 = pk2(-mz, -mz);
-          unsigned long long sum = pk2(0.f, 0.f);
+          unsigned long long sum = pk2(l, 0.f);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t p[16];
@@ -434,78 +458,67 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
               p[i] = Vec<W>::pack2(y0, y1);
             }
             tmem_st16(s_col + 16 * c, p);
+            if (c & 1) {                               // half of the keys: their part of O += P V can start
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&bars.p_full[side][c >> 1]));
+            }
           }
           float l0, l1;
           upk2(sum, l0, l1);
-          l += l0 + l1;
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(smem_addr(&bars.p_full[side]));
+          l = l0 + l1;
         }
         if (!ok) break;
         // The segment's output.
-        if (mine_has && n_tiles > 0) {
-          ok = __all_sync(0xffffffffu, wait_or_abort(smem_addr(&bars.o_full[side]), n_o & 1u, abort_flag, kWaitBudgetNs));
-          if (!ok) break;
+        if (has && n_tiles > 0) {
+          if (!wait(&bars.o_full[side], n_o & 1u)) break;
           ++n_o;
           tc_fence_after();
         }
-        Partial<kRows, D>* part =
-            w.whole ? nullptr : partial_of<kRows, D>(a, 2 * blockIdx.x + (w.at_start ? 0 : 1));
-        const int rho = w.x.tok0 * a.G + row;
-        const float inv = l == 0.f ? 0.f : a.v_scale / l;
-        if (mine_has) {
-          T* dst = nullptr;
-          if (row < w.rows)
-            dst = reinterpret_cast<T*>(a.out) +
-                  ((size_t)(w.q.row0 + w.x.tok0 + tok) * a.Hq + (size_t)w.head * a.G + (row - tok * a.G)) * D;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t x[32];
+        if (has) {
+          const int part_slot = g.slot;
+          const float inv = l == 0.f ? 0.f : a.v_scale / l;
+          T* dst = reinterpret_cast<T*>(a.out) +
+                   ((size_t)(g.row0 + (live ? tok : 0)) * a.Hq + (size_t)g.head * a.G + (live ? row - tok * a.G : 0)) * D;
+          Partial<kRows, D>* part = partial_of<kRows, D>(a, max(part_slot, 0));
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t y[16];
             if (n_tiles > 0) {
-              tmem_ld32(o_col + 32 * c, x);
+              tmem_ld16(o_col + 16 * c, y);
               tmem_wait_ld();
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = 0u;
+              for (int i = 0; i < 16; ++i) y[i] = 0u;
             }
-            if (row < w.rows) {
-              if (w.whole) {
+            if (live && part_slot < 0) {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                  float y[8];
+              for (int v = 0; v < 2; ++v) {
+                float z[8];
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) y[i] = l == 0.f ? 0.f : __uint_as_float(x[8 * v + i]) * inv;
-                  st_v4(dst + 32 * c + 8 * v, Vec<T>::pack(y));
-                }
-              } else {
-#pragma unroll
-                for (int v = 0; v < 8; ++v)
-                  st_v4(&part->o[row][32 * c + 4 * v], make_uint4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]));
+                for (int i = 0; i < 8; ++i) z[i] = l == 0.f ? 0.f : __uint_as_float(y[8 * v + i]) * inv;
+                st_v4(dst + 16 * c + 8 * v, Vec<T>::pack(z));
               }
+            } else if (live) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                st_v4(&part->o[row][16 * c + 4 * v], make_uint4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]));
             }
           }
-          if (row < w.rows) {
-            if (w.whole) {
-              store_lse(a, w.q, w.head, rho, m, l);
-            } else {
-              part->m[row] = m;
-              part->l[row] = l;
-            }
+          if (live && part_slot < 0) {
+            if (a.lse)
+              a.lse[(size_t)(g.row0 + tok) * a.Hq + (size_t)g.head * a.G + (row - tok * a.G)] =
+                  l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          } else if (live) {
+            part->m[row] = m;
+            part->l[row] = l;
           }
         }
         // The next segment's first O += P V follows this side's next p_full, so O has been read by then.
         tc_fence_before();
-        if (tid == 0 && w.begins && !w.whole) {
-          JoinRecord* rec = record_of(a, blockIdx.x);
-          rec->parts = (int32_t)((w.item0 + w.x.units - 1) / w.run - blockIdx.x) + 1;
-          rec->slot0 = 2 * blockIdx.x + (w.at_start ? 0 : 1);
-          rec->row0 = w.q.row0;
-          rec->head = w.head;
-          rec->rho0 = w.x.tok0 * a.G;
-          rec->rows = w.rows;
-        }
-        if (tid == 0 && w.u >= w.u_end && !(w.begins && !w.whole)) record_of(a, blockIdx.x)->parts = 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bars.seg_empty[n_seg % kSegments]));
       }
       if (!ok) *abort_flag = 1;
     } else if (warp < kMmaWarp) {
@@ -529,10 +542,46 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             : "memory");
         return r != 0;
       };
+      w.r = s_req;
+      w.base = s_base;
+      w.t = 0;
+      w.q = read_request(a, w.r, false);
+      w.x = tile_of(a, w.q, per, 0);
+      uint32_t n_seg = 0;
+      // Hands the current segment on (tiles -1: the end).
+      auto publish = [&](int tiles) {
+        const bool go = agreed(wait_or_abort(smem_addr(&bars.seg_empty[n_seg % kSegments]), ((n_seg / kSegments) & 1u) ^ 1u,
+                                             abort_flag, kWaitBudgetNs));
+        if (go && lt == 0) {
+          Segment& g = s_seg[n_seg % kSegments];
+          g.tiles = tiles;
+          g.k_lo = w.k_lo;
+          g.rows = w.rows;
+          g.lim0 = w.q.seq - w.q.n + w.x.tok0;
+          g.head = w.head;
+          g.row0 = w.q.row0 + w.x.tok0;
+          g.slot = w.whole ? -1 : 2 * blockIdx.x + (w.at_start ? 0 : 1);
+          mbar_arrive(smem_addr(&bars.seg_full[n_seg % kSegments]));
+        }
+        ++n_seg;
+        return go;
+      };
       auto barrier_loaders = [] { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kLoaders) : "memory"); };
+      bool crosses = false;                            // the run's last item began here and goes on in the next CTA
       while (ok && w.next(a, per)) {
         const int n_tiles = w.tiles();
-        if (n_tiles == 0) continue;
+        ok = publish(n_tiles);
+        crosses = w.begins && !w.whole;
+        if (crosses && lt == 0) {
+          JoinRecord* rec = record_of(a, blockIdx.x);
+          rec->parts = (int32_t)((w.item0 + w.x.units - 1) / w.run - blockIdx.x) + 1;
+          rec->slot0 = 2 * blockIdx.x + (w.at_start ? 0 : 1);
+          rec->row0 = w.q.row0;
+          rec->head = w.head;
+          rec->rho0 = w.x.tok0 * a.G;
+          rec->rows = w.rows;
+        }
+        if (!ok || n_tiles == 0) continue;
         ok = agreed(wait_or_abort(smem_addr(&bars.q_empty), (n_q & 1u) ^ 1u, abort_flag, kWaitBudgetNs));
         if (!ok) break;
         {
@@ -686,6 +735,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         }
         ok = ok && agreed(here);
       }
+      if (lt == 0 && !crosses) record_of(a, blockIdx.x)->parts = 0;
+      if (ok) ok = publish(-1);
       // After a time-out bulk copies may be in flight that no MMA waited for:
       // they land before shared memory is let go.
       if (!ok && bulk > 0)
@@ -728,10 +779,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         }
         __syncwarp();
       };
-      while (ok && w.next(a, per)) {
-        const int n_tiles = w.tiles();
+      for (uint32_t n_seg = 0; ok; ++n_seg) {
+        if (!wait(&bars.seg_full[n_seg % kSegments], (n_seg / kSegments) & 1u)) break;
+        const int n_tiles = s_seg[n_seg % kSegments].tiles, sides = s_seg[n_seg % kSegments].rows > 128 ? 2 : 1;
+        if (n_tiles < 0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bars.seg_empty[n_seg % kSegments]));
         if (n_tiles == 0) continue;
-        const int sides = w.rows > 128 ? 2 : 1;
         if (!wait(&bars.q_full, n_q & 1u)) break;
         ++n_q;
         if (!wait(&bars.kv_full[place], turn)) break;
@@ -751,16 +805,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             turn ^= 1u;
           }
           for (int side = 0; side < sides; ++side) {
-            if (!wait(&bars.p_full[side], n_p[side] & 1u)) break;
-            ++n_p[side];
-            tc_fence_after();
-            if (leader) {
-              const uint64_t vd = v_desc + v_place * (S::kTileBytes >> 4);
-              const uint32_t o_tm = tm + S::kOCol + (uint32_t)(D * side), p_tm = tm + 128u * side;
+            const uint64_t vd = v_desc + v_place * (S::kTileBytes >> 4);
+            const uint32_t o_tm = tm + S::kOCol + (uint32_t)(D * side), p_tm = tm + 128u * side;
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k) mma_ts(o_tm, p_tm + 8u * k, vd + 2u * k * (S::kGroupBytes >> 4), kIdO, (j | k) != 0);
+            for (int half = 0; half < 2; ++half) {
+              if (!wait(&bars.p_full[side][half], n_p[side] & 1u)) break;
+              tc_fence_after();
+              if (leader) {
+#pragma unroll
+                for (int k = 4 * half; k < 4 * half + 4; ++k)
+                  mma_ts(o_tm, p_tm + 8u * k, vd + 2u * k * (S::kGroupBytes >> 4), kIdO, (j | k) != 0);
+              }
+              __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
+            ++n_p[side];
             if (side == sides - 1) commit(&bars.kv_empty[v_place]);
             if (j == n_tiles - 1) {
               commit(&bars.o_full[side]);
