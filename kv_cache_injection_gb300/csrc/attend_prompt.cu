@@ -35,6 +35,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <cstring>
 #include <type_traits>
 
@@ -746,99 +747,95 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       if (!ok) *abort_flag = 1;
     } else {
       // ---- MMAs ----------------------------------------------------------------
-      // The whole warp walks along and one elected lane issues: with the branch
-      // on elect.sync and descriptors that are sums of uniform values the
-      // compiler keeps them in uniform registers.  Branching on a lane number
-      // made one M128 N128 K16 MMA cost 72 to 97 clocks to issue; it takes 64.
+      // One elected lane does it all.  With the branch on elect.sync and
+      // descriptors that are sums of uniform values the compiler keeps them in
+      // uniform registers: an M128 N128 K16 MMA is issued in the 64 clocks it
+      // takes, where a branch on the lane number cost 72 to 97.
       constexpr uint32_t kIdS = idesc_of<T>(128, false), kIdO = idesc_of<W>(D, true);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), q_tile = __shfl_sync(0xffffffffu, tiles0, 0);
+      const uint32_t bar0 = __shfl_sync(0xffffffffu, smem_addr(&bars), 0);
       uint32_t leader;
       asm volatile(
           "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), q_tile = __shfl_sync(0xffffffffu, tiles0, 0);
-      const uint64_t q_desc = tile_desc<D>(q_tile, 1), k_desc = tile_desc<D>(q_tile + 2 * S::kTileBytes, 1);
-      const uint64_t v_desc = tile_desc<D>(q_tile + 2 * S::kTileBytes, 1024 >> 4);
-      uint32_t n_q = 0, n_p[2] = {0, 0};
-      uint32_t place = 0, turn = 0;                    // of the next load: its place in the ring, and the ring's turn
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, kWaitBudgetNs));
-        return ok;
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (leader) mma_commit(smem_addr(bar));
-      };
-      auto scores = [&](int side, uint32_t k_place) {
-        if (leader) {
-          const uint64_t qd = q_desc + (uint32_t)side * (S::kTileBytes >> 4), kd = k_desc + k_place * (S::kTileBytes >> 4);
+      if (leader) {
+        const uint64_t q_desc = tile_desc<D>(q_tile, 1), k_desc = tile_desc<D>(q_tile + 2 * S::kTileBytes, 1);
+        const uint64_t v_desc = tile_desc<D>(q_tile + 2 * S::kTileBytes, 1024 >> 4);
+#define ISK_BAR(member) (bar0 + (uint32_t)offsetof(Bars, member))
+        uint32_t n_q = 0, p_turn[2] = {0, 0};
+        uint32_t place = 0, turn = 0;                  // of the next load: its place in the ring, and the ring's turn
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+          if (!mbar_try_wait(bar, parity)) ok = wait_or_abort(bar, parity, abort_flag, kWaitBudgetNs);
+          return ok;
+        };
+        auto next_place = [&] {
+          if (++place == S::kRing) {
+            place = 0;
+            turn ^= 1u;
+          }
+        };
+        auto scores = [&](uint32_t side, uint32_t k_place) {
+          const uint64_t qd = q_desc + side * (S::kTileBytes >> 4), kd = k_desc + k_place * (S::kTileBytes >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t o = ((uint32_t)(k >> 2) * 1024u + 32u * (k & 3)) >> 4;
             mma_ss(tm + 128u * side, qd + o, kd + o, kIdS, k != 0);
           }
-          mma_commit(smem_addr(&bars.s_full[side]));
-        }
-        __syncwarp();
-      };
-      for (uint32_t n_seg = 0; ok; ++n_seg) {
-        if (!wait(&bars.seg_full[n_seg % kSegments], (n_seg / kSegments) & 1u)) break;
-        const int n_tiles = s_seg[n_seg % kSegments].tiles, sides = s_seg[n_seg % kSegments].rows > 128 ? 2 : 1;
-        if (n_tiles < 0) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&bars.seg_empty[n_seg % kSegments]));
-        if (n_tiles == 0) continue;
-        if (!wait(&bars.q_full, n_q & 1u)) break;
-        ++n_q;
-        if (!wait(&bars.kv_full[place], turn)) break;
-        tc_fence_after();
-        for (int side = 0; side < sides; ++side) scores(side, place);
-        commit(&bars.kv_empty[place]);
-        for (int j = 0; j < n_tiles && ok; ++j) {
-          // V of this tile, then K of the next
-          if (++place == S::kRing) {
-            place = 0;
-            turn ^= 1u;
-          }
-          const uint32_t v_place = place;
-          if (!wait(&bars.kv_full[v_place], turn)) break;
-          if (++place == S::kRing) {
-            place = 0;
-            turn ^= 1u;
-          }
-          for (int side = 0; side < sides; ++side) {
+          mma_commit(ISK_BAR(s_full) + 8 * side);
+        };
+        for (uint32_t n_seg = 0; ok; ++n_seg) {
+          const uint32_t seg = n_seg % kSegments;
+          if (!wait(ISK_BAR(seg_full) + 8 * seg, (n_seg / kSegments) & 1u)) break;
+          const int n_tiles = s_seg[seg].tiles;
+          const uint32_t sides = s_seg[seg].rows > 128 ? 2 : 1;
+          if (n_tiles < 0) break;
+          mbar_arrive(ISK_BAR(seg_empty) + 8 * seg);
+          if (n_tiles == 0) continue;
+          if (!wait(ISK_BAR(q_full), n_q & 1u)) break;
+          ++n_q;
+          if (!wait(ISK_BAR(kv_full) + 8 * place, turn)) break;
+          tc_fence_after();
+          for (uint32_t side = 0; side < sides; ++side) scores(side, place);
+          mma_commit(ISK_BAR(kv_empty) + 8 * place);
+          for (int j = 0; j < n_tiles && ok; ++j) {
+            next_place();                              // V of this tile
+            const uint32_t v_place = place;
+            if (!wait(ISK_BAR(kv_full) + 8 * v_place, turn)) break;
+            next_place();                              // K of the next
             const uint64_t vd = v_desc + v_place * (S::kTileBytes >> 4);
-            const uint32_t o_tm = tm + S::kOCol + (uint32_t)(D * side), p_tm = tm + 128u * side;
+            for (uint32_t side = 0; side < sides; ++side) {
+              const uint32_t o_tm = tm + S::kOCol + (uint32_t)D * side, p_tm = tm + 128u * side;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (!wait(&bars.p_full[side][half], n_p[side] & 1u)) break;
-              tc_fence_after();
-              if (leader) {
+              for (int half = 0; half < 2; ++half) {
+                if (!wait(ISK_BAR(p_full) + 16 * side + 8 * half, p_turn[side])) break;
+                tc_fence_after();
 #pragma unroll
                 for (int k = 4 * half; k < 4 * half + 4; ++k)
                   mma_ts(o_tm, p_tm + 8u * k, vd + 2u * k * (S::kGroupBytes >> 4), kIdO, (j | k) != 0);
               }
-              __syncwarp();
-            }
-            if (!ok) break;
-            ++n_p[side];
-            if (side == sides - 1) commit(&bars.kv_empty[v_place]);
-            if (j == n_tiles - 1) {
-              commit(&bars.o_full[side]);
-            } else {
-              if (side == 0) {
-                if (!wait(&bars.kv_full[place], turn)) break;
-                tc_fence_after();
+              if (!ok) break;
+              p_turn[side] ^= 1u;
+              if (side == sides - 1) mma_commit(ISK_BAR(kv_empty) + 8 * v_place);
+              if (j == n_tiles - 1) {
+                mma_commit(ISK_BAR(o_full) + 8 * side);
+              } else {
+                if (side == 0) {
+                  if (!wait(ISK_BAR(kv_full) + 8 * place, turn)) break;
+                  tc_fence_after();
+                }
+                scores(side, place);
+                if (side == sides - 1) mma_commit(ISK_BAR(kv_empty) + 8 * place);
               }
-              scores(side, place);
-              if (side == sides - 1) commit(&bars.kv_empty[place]);
             }
           }
+          if (ok) mma_commit(ISK_BAR(q_empty));
         }
-        if (ok) commit(&bars.q_empty);
+        if (!ok) *abort_flag = 1;
+        // Every MMA issued has ended before tensor and shared memory are let go.
+        mma_commit(ISK_BAR(done));
+        mbar_wait_bounded(ISK_BAR(done), 0, kWaitBudgetNs);
+#undef ISK_BAR
       }
-      if (!ok) *abort_flag = 1;
-      // Every MMA issued has ended before tensor and shared memory are let go.
-      commit(&bars.done);
-      mbar_wait_bounded(smem_addr(&bars.done), 0, kWaitBudgetNs);
     }
     __syncwarp();
   }
