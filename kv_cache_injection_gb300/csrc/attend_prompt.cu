@@ -266,6 +266,21 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// Four lanes hold four vectors each; lane q ends with vector q of each of the four.
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4], int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {       // swap v[i + 1] of even lanes with v[i] of odd ones
+    const uint4 got = shfl_xor4(odd ? v[i] : v[i + 1], 1);
+    if (odd) v[i] = got; else v[i + 1] = got;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {          // and v[i + 2] of the lower pair with v[i] of the upper
+    const uint4 got = shfl_xor4(high ? v[i] : v[i + 2], 2);
+    if (high) v[i] = got; else v[i + 2] = got;
+  }
+}
+
 // Where 16-byte chunk c (8 elements) of row `row` lies in a tile.
 template <int D>
 __device__ __forceinline__ uint32_t at_chunk(int row, int c) {
@@ -480,31 +495,51 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         if (has) {
           const int part_slot = g.slot;
           const float inv = l == 0.f ? 0.f : a.v_scale / l;
-          T* dst = reinterpret_cast<T*>(a.out) +
-                   ((size_t)(g.row0 + (live ? tok : 0)) * a.Hq + (size_t)g.head * a.G + (live ? row - tok * a.G : 0)) * D;
+          // A thread holds a row; four lanes exchange 64-byte pieces so that each store of the warp writes eight
+          // rows' 64 consecutive bytes, not 32 rows' 16.
+          const int row4 = row & ~3, head0 = g.head * a.G;
+          T* dst[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = row4 + i, t = r / a.G;
+            dst[i] = r < g.rows ? reinterpret_cast<T*>(a.out) + ((size_t)(g.row0 + t) * a.Hq + head0 + (r - t * a.G)) * D : nullptr;
+          }
           Partial<kRows, D>* part = partial_of<kRows, D>(a, max(part_slot, 0));
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t y[16];
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t y[32];
             if (n_tiles > 0) {
-              tmem_ld16(o_col + 16 * c, y);
+              tmem_ld32(o_col + 32 * c, y);
               tmem_wait_ld();
             } else {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = 0u;
+              for (int i = 0; i < 32; ++i) y[i] = 0u;
             }
-            if (live && part_slot < 0) {
+            if (part_slot < 0) {
+              uint4 v[4];
 #pragma unroll
-              for (int v = 0; v < 2; ++v) {
+              for (int u = 0; u < 4; ++u) {
                 float z[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] = l == 0.f ? 0.f : __uint_as_float(y[8 * v + i]) * inv;
-                st_v4(dst + 16 * c + 8 * v, Vec<T>::pack(z));
+                for (int i = 0; i < 8; ++i) z[i] = l == 0.f ? 0.f : __uint_as_float(y[8 * u + i]) * inv;
+                v[u] = Vec<T>::pack(z);
               }
-            } else if (live) {
+              quad_transpose(v, lane);
 #pragma unroll
-              for (int v = 0; v < 4; ++v)
-                st_v4(&part->o[row][16 * c + 4 * v], make_uint4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]));
+              for (int i = 0; i < 4; ++i)
+                if (dst[i]) st_v4(dst[i] + 32 * c + 8 * (lane & 3), v[i]);
+            } else {
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  v[i] = make_uint4(y[16 * u + 4 * i], y[16 * u + 4 * i + 1], y[16 * u + 4 * i + 2], y[16 * u + 4 * i + 3]);
+                quad_transpose(v, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (dst[i]) st_v4(&part->o[row4 + i][32 * c + 16 * u + 4 * (lane & 3)], v[i]);
+              }
             }
           }
           if (live && part_slot < 0) {
@@ -583,23 +618,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           rec->rows = w.rows;
         }
         if (!ok || n_tiles == 0) continue;
-        ok = agreed(wait_or_abort(smem_addr(&bars.q_empty), (n_q & 1u) ^ 1u, abort_flag, kWaitBudgetNs));
-        if (!ok) break;
-        {
-          constexpr int C = D / 8;                     // chunks of a row
-          for (int i = lt; i < kRows * C; i += kLoaders) {
-            const int row = i / C, c = i % C, tok = row / a.G;
+        // Q once the last segment's logits are done; called after the first tile's loads are on their way.
+        auto load_q = [&] {
+          ok = agreed(wait_or_abort(smem_addr(&bars.q_empty), (n_q & 1u) ^ 1u, abort_flag, kWaitBudgetNs));
+          ++n_q;
+          if (!ok) return;
+          constexpr int C = D / 8, RP = kLoaders / C;  // chunks of a row; rows of one pass
+          const uint32_t g_inv = (65536u + a.G - 1) / a.G;   // row / G = row * g_inv >> 16 for row < 256, G <= 64
+          const int c = lt % C;
+          const uint8_t* src = a.q + (int64_t)(w.q.row0 + w.x.tok0) * a.q_stride + (size_t)w.head * a.G * D * 2 + c * 16;
+#pragma unroll 8
+          for (int row = lt / C; row < kRows; row += RP) {
+            const int tok = (int)((uint32_t)row * g_inv >> 16);
             const bool in = row < w.rows;
-            const uint8_t* src = a.q + (int64_t)(w.q.row0 + w.x.tok0 + (in ? tok : 0)) * a.q_stride +
-                                 ((size_t)w.head * a.G + (in ? row - tok * a.G : 0)) * D * 2 + c * 16;
-            cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), src, in);
+            cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c),
+                       in ? src + tok * a.q_stride + (row - tok * a.G) * (D * 2) : src, in);
           }
           cp_async_commit();
           cp_async_wait<0>();
           fence_proxy_async_smem();
           mbar_arrive(smem_addr(&bars.q_full));
-          ++n_q;
-        }
+        };
         const int32_t* table = a.block_table + (size_t)w.r * a.max_blocks;
         const uint8_t* kbase = a.k_cache + (size_t)w.head * D * EB;
         // Bulk copies: lane g of each warp finds the token of row group g (`box` rows) of a tile, one tile ahead;
@@ -668,6 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 }
                 if (lane == (int)place) bulk = n_load + kv + 1;
               }
+              if (j == 0) {
+                load_q();
+                if (!ok) break;
+              }
               continue;
             }
             look_up(j);
@@ -731,6 +774,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             fence_proxy_async_smem();
             barrier_loaders();
             if (lt == 0) mbar_arrive(smem_addr(&bars.kv_full[place]));
+            if (j == 0 && kv == 0) {
+              load_q();
+              if (!ok) break;
+            }
           }
           if (!ok) break;
         }
@@ -877,7 +924,7 @@ static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
   }
   e = launch_ex(kern, dim3(grid), dim3(prompt::kThreads), S::kSmem, cfg.stream, cfg.pdl, a, per, box, map);
   if (e != cudaSuccess) return e;
-  return launch_ex(attend_join_rows_kernel<T, prompt::kRows, D>, dim3(grid, 8), dim3(kJoinThreads), 0, cfg.stream,
+  return launch_ex(attend_join_rows_kernel<T, prompt::kRows, D>, dim3(grid, 32), dim3(kJoinThreads), 0, cfg.stream,
                    cfg.pdl, a);
 }
 
