@@ -18,18 +18,21 @@
 
 namespace isk {
 
-constexpr int kExtendThreads = 256;
-constexpr int kTokensPerCta = 2048;
+constexpr int kExtendThreads = 512;
+constexpr int kTokensPerThread = 4;
+constexpr int kTokensPerCta = kExtendThreads * kTokensPerThread;
+
+// Lengths and block sizes stay below 2^25 here, so 32-bit arithmetic suffices.
+__device__ __forceinline__ int32_t blocks_of(int32_t n, int32_t bs) { return (int32_t)((uint32_t)(n + bs - 1) / (uint32_t)bs); }
 
 __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_args_t a) {
   extern __shared__ int32_t sm[];
-  __shared__ int64_t scratch[33];
+  __shared__ int64_t scratch[2][kExtendThreads / 32];
   __shared__ int32_t s_used;
   const int R = a.num_requests, bs = a.block_size, tid = threadIdx.x;
   int32_t* s_start = sm;                 // [R + 1] first packed token, INT32_MAX at most
   int32_t* s_seq = sm + R + 1;           // [R] seq_len, or -1 if the request is refused
-  int32_t* s_new = s_seq + R;            // [R] tokens
-  int32_t* s_take = s_new + R;           // [R] free-list index of the request's table entry 0
+  int32_t* s_take = s_seq + R;           // [R] free-list index of the request's table entry 0
   pdl_wait();
   pdl_trigger();
   int32_t head = a.free_head ? a.free_head[0] : 0;
@@ -42,110 +45,133 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
   if (tid == 0) s_used = 0;
   const int per = (R + kExtendThreads - 1) / kExtendThreads;
   const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
+  // A thread's requests are consecutive (at most 8); all their lengths are loaded before any is used.
+  constexpr int kPer = (IS_MAX_REQUESTS + kExtendThreads - 1) / kExtendThreads;
+  int32_t len[kPer], add[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const bool in = r0 + i < r1;
+    len[i] = in ? a.seq_len[r0 + i] : 0;
+    add[i] = in ? a.new_len[r0 + i] : 0;
+  }
   int64_t tokens = 0, missing = 0;
-  for (int r = r0; r < r1; ++r) {
-    const int32_t n = a.seq_len[r], m = a.new_len[r];
-    const int32_t count = min(max(m, 0), IS_MAX_POSITION);
-    int32_t seq = n, miss = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (r0 + i >= r1) continue;
+    const int32_t n = len[i], m = add[i];
+    add[i] = min(max(m, 0), IS_MAX_POSITION);
+    int32_t miss = 0;
     if (n < 0 || m < 0) {
       bits |= IS_ST_COUNT;
-      seq = -1;
+      len[i] = -1;
     } else if ((int64_t)n + m > IS_MAX_POSITION) {
       bits |= IS_ST_POSITION;
-      seq = -1;
+      len[i] = -1;
     } else {
-      const int32_t have = (int32_t)(((int64_t)n + bs - 1) / bs), need = (int32_t)(((int64_t)n + m + bs - 1) / bs);
+      const int32_t need = blocks_of(n + m, bs);
       if (m > 0 && need > a.max_blocks_per_seq) {
         bits |= IS_ST_BLOCK_TABLE;
-        seq = -1;
+        len[i] = -1;
       } else {
-        miss = need - have;
+        miss = need - blocks_of(n, bs);
       }
     }
-    s_seq[r] = seq;
-    s_new[r] = count;
-    s_take[r] = miss;
-    tokens += count;
+    s_take[r0 + i] = miss;
+    tokens += add[i];
     missing += miss;
   }
   int64_t total, all_missing;
-  int64_t at = block_exclusive_scan(tokens, scratch, &total);
-  int64_t taken = block_exclusive_scan(missing, scratch, &all_missing);
-  for (int r = r0; r < r1; ++r) {
+  int64_t at = block_exclusive_scan_1bar<kExtendThreads / 32>(tokens, scratch[0], &total);
+  int64_t taken = block_exclusive_scan_1bar<kExtendThreads / 32>(missing, scratch[1], &all_missing);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int r = r0 + i;
+    if (r >= r1) continue;
     const int32_t miss = s_take[r];
     s_start[r] = (int32_t)min(at, (int64_t)INT32_MAX);
-    if (s_seq[r] >= 0 && miss > 0) {
+    if (len[i] >= 0 && miss > 0) {
       if (taken + miss > avail) {
         bits |= IS_ST_FREE_LIST;
-        s_seq[r] = -1;
+        len[i] = -1;
       } else {
         atomicMax(&s_used, (int32_t)(taken + miss));
       }
     }
-    // entry j >= have of the row is free_blocks[s_take + j]
-    s_take[r] = s_seq[r] < 0 ? 0 : head + (int32_t)taken - (s_seq[r] + bs - 1) / bs;
-    at += s_new[r];
+    s_seq[r] = len[i];
+    // entry j >= the blocks held of the row is free_blocks[s_take + j]
+    s_take[r] = len[i] < 0 ? 0 : head + (int32_t)taken - blocks_of(len[i], bs);
+    at += add[i];
     taken += miss;
   }
   if (tid == 0) s_start[R] = (int32_t)min(total, (int64_t)INT32_MAX);
   if (total > a.max_tokens) bits |= IS_ST_COUNT;
   __syncthreads();
 
-  // Table entries and per-request outputs: one warp per request.
-  const int lane = tid & 31, nwarps = kExtendThreads / 32;
-  for (int r = blockIdx.x * nwarps + (tid >> 5); r < R; r += gridDim.x * nwarps) {
-    const int32_t n = s_seq[r];
-    if (n >= 0) {
-      const int32_t have = (n + bs - 1) / bs, need = (int32_t)(((int64_t)n + s_new[r] + bs - 1) / bs);
-      int32_t* row = a.block_table + (size_t)r * a.max_blocks_per_seq;
-      for (int j = have + lane; j < need; j += 32) row[j] = a.free_blocks[s_take[r] + j];
-    }
-    if (lane == 0) {
-      if (a.seq_len_out) a.seq_len_out[r] = n >= 0 ? n + s_new[r] : a.seq_len[r];
-      if (a.token_start_out) {
-        a.token_start_out[r] = s_start[r];
-        if (r == R - 1) a.token_start_out[R] = s_start[R];
-      }
-    }
-  }
-  if (blockIdx.x == 0 && tid == 0 && a.free_head_out) a.free_head_out[0] = head + s_used;
-
-  // Slots and positions of this CTA's packed tokens.
-  const int64_t t_end = min((int64_t)a.max_tokens, ((int64_t)blockIdx.x + 1) * kTokensPerCta);
-  for (int64_t t = (int64_t)blockIdx.x * kTokensPerCta + tid; t < t_end; t += kExtendThreads) {
-    if (t >= s_start[R]) {
-      a.slot_mapping_out[t] = -1;
-      continue;
-    }
+  // Slots and positions of this CTA's packed tokens, a warp's 32 consecutive ones at a time: all searches, then all
+  // block ids, then all stores, so that their latencies overlap.
+  const int64_t t0 = (int64_t)blockIdx.x * kTokensPerCta + tid;
+  const int32_t end = s_start[R];
+  int32_t pos[kTokensPerThread], id[kTokensPerThread];
+#pragma unroll
+  for (int i = 0; i < kTokensPerThread; ++i) {
+    const int64_t t = t0 + i * kExtendThreads;
+    pos[i] = -1;
+    id[i] = -1;
+    if (t >= a.max_tokens || t >= end) continue;
     int lo = 0, hi = R;                  // last request that starts at or before t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (s_start[mid] <= t) lo = mid; else hi = mid;
     }
     const int32_t n = s_seq[lo];
+    if (n < 0) continue;
+    pos[i] = n + (int32_t)(t - s_start[lo]);
+    const int32_t j = (int32_t)((uint32_t)pos[i] / (uint32_t)bs);
+    const int32_t* src = j >= blocks_of(n, bs) ? a.free_blocks + (s_take[lo] + j)
+                                               : a.block_table + ((size_t)lo * a.max_blocks_per_seq + j);
+    id[i] = *src;
+  }
+#pragma unroll
+  for (int i = 0; i < kTokensPerThread; ++i) {
+    const int64_t t = t0 + i * kExtendThreads;
+    if (t >= a.max_tokens) continue;
     int64_t slot = -1;
-    int32_t p = -1;
-    if (n >= 0) {
-      p = n + (int32_t)(t - s_start[lo]);
-      const int j = p / bs;
-      const int32_t id = j >= (n + bs - 1) / bs ? a.free_blocks[s_take[lo] + j]
-                                               : a.block_table[(size_t)lo * a.max_blocks_per_seq + j];
-      if (id < 0 || id >= a.num_blocks)
+    if (pos[i] >= 0) {
+      if (id[i] < 0 || id[i] >= a.num_blocks)
         bits |= IS_ST_BLOCK_ID;
       else
-        slot = (int64_t)id * bs + (p - j * bs);
+        slot = (int64_t)id[i] * bs + (int32_t)((uint32_t)pos[i] % (uint32_t)bs);
     }
     a.slot_mapping_out[t] = slot;
-    if (a.positions_out) a.positions_out[t] = p;
+    if (t < end && a.positions_out) a.positions_out[t] = pos[i];
   }
+
+  // Table entries and per-request outputs: one warp per request.
+  const int lane = tid & 31, nwarps = kExtendThreads / 32;
+  for (int r = blockIdx.x * nwarps + (tid >> 5); r < R; r += gridDim.x * nwarps) {
+    const int32_t n = s_seq[r], m = a.new_len[r];
+    if (n >= 0) {
+      const int32_t need = blocks_of(n + m, bs);
+      int32_t* row = a.block_table + (size_t)r * a.max_blocks_per_seq;
+      for (int j = blocks_of(n, bs) + lane; j < need; j += 32) row[j] = a.free_blocks[s_take[r] + j];
+    }
+    if (lane == 0) {
+      if (a.seq_len_out) a.seq_len_out[r] = n >= 0 ? n + m : a.seq_len[r];
+      if (a.token_start_out) {
+        a.token_start_out[r] = s_start[r];
+        if (r == R - 1) a.token_start_out[R] = end;
+      }
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0 && a.free_head_out) a.free_head_out[0] = head + s_used;
   if (bits) latch(a.status_out, bits);
 }
 
 cudaError_t launch_extend(const is_extend_args_t& a, const LaunchCfg& cfg) {
-  const size_t smem = ((size_t)4 * a.num_requests + 1) * sizeof(int32_t);
+  const size_t smem = ((size_t)3 * a.num_requests + 1) * sizeof(int32_t);
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(extend_kernel), smem);
   if (e != cudaSuccess) return e;
-  const int grid = std::max(1, (int)(((int64_t)a.max_tokens + kTokensPerCta - 1) / kTokensPerCta));
+  const int grid = (int)(((int64_t)a.max_tokens + kTokensPerCta - 1) / kTokensPerCta);
   return launch_ex(extend_kernel, dim3(grid), dim3(kExtendThreads), smem, cfg.stream, cfg.pdl, a);
 }
 
