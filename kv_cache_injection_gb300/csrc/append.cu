@@ -3,142 +3,175 @@
 // Pair i of a head turns by the angle p_axis(i) * w_i (the turns are reduced
 // in fp32 as for the injected facts, see angle_turns): (a, b) becomes
 // (a cos - b sin, b cos + a sin), in fp32, rounded once to the output type.
-// The sines of a token depend on its positions alone, so a CTA takes one
-// token: half a head's worth of threads compute them once into shared memory,
-// and all heads use them.  A thread's 16-byte vectors of different heads share
-// one frequency group, whose sines it keeps in registers.  Bound by memory:
-// every input is read once and every output written once.
+// The sines of a token depend on its positions alone.  A warp works on one
+// token: its lanes compute the sines of all D / 2 pairs between them, exchange
+// them through the warp's shared memory, and go through the token's heads; a
+// lane's 16-byte vectors of different heads share one frequency group, whose
+// sines it keeps in registers.  With few tokens several warps share one, each
+// with its own heads (and its own copy of the sines: 2 a lane, less than a
+// block barrier costs), so that a single token is still one round of loads.
+// Bound by memory: every input is read once and every output written once.
 #include "common.cuh"
 #include "internal.h"
 
 namespace isk {
 
 constexpr int kAppendThreads = 128;
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kAppendBatch = 4;                  // vectors (or pairs) a lane loads before it uses any
 
-// Vectors a thread loads before the token's sines are known: as many rotated
-// items (a pair of vectors for half-split heads, else one) and plain ones.
-constexpr int kAppendAhead = 3;
+// One element of a parameter table, another one in each lane: through the
+// memory path, which serves a warp's 32 addresses together (the constant path
+// takes them one by one).
+__device__ __forceinline__ float ld_param(const float* p) {
+  float x;
+  asm("ld.f32 %0, [%1];" : "=f"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint32_t ld_param(const uint8_t* p) {
+  uint32_t x;
+  asm("ld.u8 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
 
 template <typename T, int STYLE, bool F8>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a, const __grid_constant__ AxisTurns at) {
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a, const __grid_constant__ AxisTurns at,
+                                                                int share) {
   constexpr int VE = Vec<T>::N;
   constexpr int NF = STYLE == 0 ? VE : VE / 2;   // frequencies of one vector
   constexpr int CB = F8 ? 1 : (int)sizeof(T);    // cache bytes per element
-  __shared__ float s_cos[kMaxHalfDim], s_sin[kMaxHalfDim];
-  __shared__ uint32_t s_bad;
-  const int tid = threadIdx.x, half = a.D / 2;
-  const int64_t t = blockIdx.x;
+  extern __shared__ float2 s_turn[];             // [warps][D / 2] (cos, sin)
+  const int lane = threadIdx.x & 31, half = a.D / 2;
+  const int64_t w = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  const int64_t t = w / share;                   // `share` warps to a token
+  const int first = (int)(w - t * share) * 32 + lane, step = share * 32;
+  float2* turn = s_turn + (threadIdx.x >> 5) * half;
   const int hv = a.D / VE;                       // vectors per head
-  const int gv = STYLE == 0 ? hv / 2 : hv;       // rotated items per head
-  const int f = tid % gv;                        // this thread's frequency group
-  const int h0 = tid / gv, hs = kAppendThreads / gv, heads = a.Hq + a.H;
+  const int gv = STYLE == 0 ? hv / 2 : hv;       // rotated items per head (a power of two, at most 32)
+  const int f = lane % gv;                       // this lane's frequency group
+  const int nr = (a.Hq + a.H) * gv, nv = a.H * hv;
+  pdl_wait();
+  pdl_trigger();
+  if (t >= a.T) return;
   const uint8_t* qrow = a.q + t * a.q_stride;
   const uint8_t* krow = a.k + t * a.k_stride;
   const uint8_t* vrow = a.v + t * a.v_stride;
-  if (tid == 0) s_bad = 0;
-  pdl_wait();
-  pdl_trigger();
 
-  // Everything that does not need the token's slot is under way before it is read.
-  const int64_t slot = a.slots[t];
-  auto item = [&](int h, bool second) -> const uint8_t* {
-    const uint8_t* row = h < a.Hq ? qrow + (size_t)h * hv * 16 : krow + (size_t)(h - a.Hq) * hv * 16;
-    return row + (size_t)(f + (second ? gv : 0)) * 16;
-  };
-  uint4 x0[kAppendAhead], x1[kAppendAhead], xv[kAppendAhead];
+  // Item i is head i / gv's vector (or pair of vectors) f = i % gv; byte offsets from the head 0 of q or k need no
+  // division.  The first batch is under way before the slot and the positions are read.
+  const int nq = a.Hq * gv;
+  const uint8_t* kbase = krow - (size_t)a.Hq * hv * 16;
+  auto offset = [&](int i) { return STYLE == 0 ? (2 * i - f) * 16 : i * 16; };
+  uint4 x0[kAppendBatch], x1[kAppendBatch];
+  auto load = [&](int i0) {
 #pragma unroll
-  for (int i = 0; i < kAppendAhead; ++i) {
-    const int h = h0 + i * hs, v = tid + i * kAppendThreads;
-    if (h < heads) {
-      x0[i] = *reinterpret_cast<const uint4*>(item(h, false));
-      if (STYLE == 0) x1[i] = *reinterpret_cast<const uint4*>(item(h, true));
+    for (int u = 0; u < kAppendBatch; ++u) {
+      const int i = i0 + u * step;
+      if (i < nr) {
+        const uint8_t* src = (i < nq ? qrow : kbase) + offset(i);
+        x0[u] = *reinterpret_cast<const uint4*>(src);
+        if (STYLE == 0) x1[u] = *reinterpret_cast<const uint4*>(src + gv * 16);
+      }
     }
-    if (v < a.H * hv) xv[i] = *reinterpret_cast<const uint4*>(vrow + (size_t)v * 16);
-  }
-  if (slot == -1) return;                        // padding: the whole CTA
-  __syncthreads();                               // s_bad is zero
+  };
+  const int64_t slot = a.slots[t];
+  const int32_t of_axis = lane < a.n_axes ? a.positions[(size_t)lane * a.T + t] : 0;
+  load(first);
+  if (slot == -1) return;                        // padding
   uint32_t bad = slot < 0 || slot >= a.n_slots ? IS_ST_BLOCK_ID : 0u;
-  if (tid < a.n_axes) {
-    const int32_t p = a.positions[(size_t)tid * a.T + t];
-    if (p < 0 || p >= IS_MAX_POSITION) bad |= IS_ST_POSITION;
-  }
-  if (bad) atomicOr(&s_bad, bad);
-  for (int i = tid; i < half; i += kAppendThreads) {
-    const float p = (float)a.positions[(size_t)at.axis[i] * a.T + t];
-    float sn, cs;
-    sincospif(2.0f * angle_turns(p, at.t.hi[i], at.t.lo[i]), &sn, &cs);
-    s_cos[i] = cs;
-    s_sin[i] = sn;
-  }
-  __syncthreads();
-  if (s_bad) {
-    if (tid == 0) latch(a.status, s_bad);
+  if (of_axis < 0 || of_axis >= IS_MAX_POSITION) bad |= IS_ST_POSITION;
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (bad) {
+    if (lane == 0) latch(a.status, bad);
     return;
   }
-  float cs[NF], sn[NF];
+  for (int i0 = 0; i0 < half; i0 += 32) {        // half may be 8 or 16: then lanes past it repeat pairs
+    const int i = (i0 + lane) % half;
+    const float p = (float)__shfl_sync(0xffffffffu, of_axis, ld_param(&at.axis[i]));
+    float sn, cs;
+    sincospif(2.0f * angle_turns(p, ld_param(&at.t.hi[i]), ld_param(&at.t.lo[i])), &sn, &cs);
+    turn[i] = make_float2(cs, sn);
+  }
+  __syncwarp();
+  // Two frequencies to a register pair: the paired multiply and fused
+  // multiply-add round each lane as the scalar forms do.
+  unsigned long long cs[NF / 2], sn[NF / 2], ns[NF / 2];
 #pragma unroll
-  for (int e = 0; e < NF; ++e) {
-    cs[e] = s_cos[f * NF + e];
-    sn[e] = s_sin[f * NF + e];
+  for (int e = 0; e < NF / 2; ++e) {
+    const float2 c0 = turn[f * NF + 2 * e], c1 = turn[f * NF + 2 * e + 1];
+    cs[e] = pk2(c0.x, c1.x);
+    sn[e] = pk2(c0.y, c1.y);
+    ns[e] = pk2(-c0.y, -c1.y);
   }
   uint8_t* qout = a.q_out + (size_t)t * a.Hq * a.D * sizeof(T);
   uint8_t* kout = a.k_cache + (size_t)slot * a.H * a.D * CB;
   uint8_t* vout = kout + a.v_offset;
-  auto put = [&](int h, int v, const float* y) {
-    if (h < a.Hq) st_v4(qout + ((size_t)h * hv + v) * 16, Vec<T>::pack(y));
-    else if (F8) st_v2(kout + ((size_t)(h - a.Hq) * hv + v) * 8, to_e4m3x8(y, a.k_inv));
-    else st_v4(kout + ((size_t)(h - a.Hq) * hv + v) * 16, Vec<T>::pack(y));
+  uint8_t* kput = kout - (size_t)a.Hq * a.D * CB;
+  auto put = [&](int i, int o, const float* y) {   // o: byte offset in 16-byte vectors' terms
+    if (i < nq) st_v4(qout + o, Vec<T>::pack(y));
+    else if (F8) st_v2(kput + o / 2, to_e4m3x8(y, a.k_inv));
+    else st_v4(kput + o, Vec<T>::pack(y));
   };
-  auto rotate = [&](int h, const uint4& u, const uint4& w) {
-    float x[VE], y[VE];
-    Vec<T>::unpack(u, x);
-    if (STYLE == 0) {
-      float z[VE], r[VE];
-      Vec<T>::unpack(w, z);
+  for (int i0 = first; i0 < nr; i0 += kAppendBatch * step) {
+    if (i0 != first) load(i0);
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        y[e] = fmaf(x[e], cs[e], -z[e] * sn[e]);
-        r[e] = fmaf(z[e], cs[e], x[e] * sn[e]);
+    for (int u = 0; u < kAppendBatch; ++u) {
+      const int i = i0 + u * step;
+      if (i >= nr) continue;
+      float x[VE], y[VE];
+      Vec<T>::unpack(x0[u], x);
+      if (STYLE == 0) {
+        float z[VE], r[VE];
+        Vec<T>::unpack(x1[u], z);
+#pragma unroll
+        for (int e = 0; e < VE / 2; ++e) {
+          const unsigned long long p = pk2(x[2 * e], x[2 * e + 1]), q = pk2(z[2 * e], z[2 * e + 1]);
+          upk2(fma2_rn(p, cs[e], mul2_rn(q, ns[e])), y[2 * e], y[2 * e + 1]);
+          upk2(fma2_rn(q, cs[e], mul2_rn(p, sn[e])), r[2 * e], r[2 * e + 1]);
+        }
+        put(i, offset(i), y);
+        put(i, offset(i) + gv * 16, r);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE / 4; ++e) {         // pairs 2 e and 2 e + 1
+          const unsigned long long p = pk2(x[4 * e], x[4 * e + 2]), q = pk2(x[4 * e + 1], x[4 * e + 3]);
+          upk2(fma2_rn(p, cs[e], mul2_rn(q, ns[e])), y[4 * e], y[4 * e + 2]);
+          upk2(fma2_rn(q, cs[e], mul2_rn(p, sn[e])), y[4 * e + 1], y[4 * e + 3]);
+        }
+        put(i, offset(i), y);
       }
-      put(h, f, y);
-      put(h, f + gv, r);
-    } else {
+    }
+  }
+  for (int i0 = first; i0 < nv; i0 += kAppendBatch * step) {
 #pragma unroll
-      for (int e = 0; e < VE / 2; ++e) {
-        y[2 * e] = fmaf(x[2 * e], cs[e], -x[2 * e + 1] * sn[e]);
-        y[2 * e + 1] = fmaf(x[2 * e + 1], cs[e], x[2 * e] * sn[e]);
+    for (int u = 0; u < kAppendBatch; ++u)
+      if (i0 + u * step < nv) x0[u] = *reinterpret_cast<const uint4*>(vrow + (size_t)(i0 + u * step) * 16);
+#pragma unroll
+    for (int u = 0; u < kAppendBatch; ++u) {
+      const int v = i0 + u * step;
+      if (v >= nv) continue;
+      if (F8) {
+        float y[VE];
+        Vec<T>::unpack(x0[u], y);
+        st_v2(vout + (size_t)v * 8, to_e4m3x8(y, a.v_inv));
+      } else {
+        st_v4(vout + (size_t)v * 16, x0[u]);
       }
-      put(h, f, y);
     }
-  };
-  auto copy = [&](int v, const uint4& x) {
-    if (F8) {
-      float y[VE];
-      Vec<T>::unpack(x, y);
-      st_v2(vout + (size_t)v * 8, to_e4m3x8(y, a.v_inv));
-    } else {
-      st_v4(vout + (size_t)v * 16, x);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < kAppendAhead; ++i) {
-    const int h = h0 + i * hs, v = tid + i * kAppendThreads;
-    if (h < heads) rotate(h, x0[i], x1[i]);
-    if (v < a.H * hv) copy(v, xv[i]);
   }
-  // Wider models' remaining heads.
-  for (int h = h0 + kAppendAhead * hs; h < heads; h += hs) {
-    const uint4 u = *reinterpret_cast<const uint4*>(item(h, false));
-    rotate(h, u, STYLE == 0 ? *reinterpret_cast<const uint4*>(item(h, true)) : u);
-  }
-  for (int v = tid + kAppendAhead * kAppendThreads; v < a.H * hv; v += kAppendThreads)
-    copy(v, *reinterpret_cast<const uint4*>(vrow + (size_t)v * 16));
 }
 
 template <typename T, bool F8>
 static cudaError_t launch_append_t(const AppendArgs& a, const AxisTurns& turns, const LaunchCfg& cfg) {
   auto* kern = a.style == 0 ? append_kernel<T, 0, F8> : append_kernel<T, 1, F8>;
-  return launch_ex(kern, dim3((unsigned)a.T), dim3(kAppendThreads), 0, cfg.stream, cfg.pdl, a, turns);
+  // Warps to a token: as many as keep a lane one batch busy while the SMs have room for 32 warps each.
+  const int gv = a.D * (int)sizeof(T) / 16 / (a.style == 0 ? 2 : 1);
+  const int64_t items = (int64_t)(a.Hq + a.H) * gv;
+  int share = 1;
+  while (share < 16 && (int64_t)a.T * share < 32LL * cfg.num_sms && (int64_t)share * 32 < items) share *= 2;
+  const int64_t ctas = ((int64_t)a.T * share + kAppendWarps - 1) / kAppendWarps;
+  return launch_ex(kern, dim3((unsigned)ctas), dim3(kAppendThreads), (size_t)kAppendWarps * a.D / 2 * sizeof(float2),
+                   cfg.stream, cfg.pdl, a, turns, share);
 }
 
 cudaError_t launch_append(const AppendArgs& a, const AxisTurns& turns, const LaunchCfg& cfg) {
