@@ -106,8 +106,9 @@ struct MmaEngine {
   static constexpr int kRowBytes = F8 ? D : 2 * D;
   static constexpr int kKeys = kRowBytes >= 256 ? 16 : 32;
   static constexpr int kMt = kKeys / 16;
-  static constexpr int kPitch = D + 4;
+  static constexpr int kPitch = kRows * (D + 4) * 4 <= 2 * kKeys * kRowBytes ? D + 4 : D;   // fits a tile
   static constexpr int kSharedQ = 0;
+  static constexpr int kMostPerSm = D * NT >= 256 ? 2 : 3;   // what the registers allow
   using M = typename std::conditional<F8, __half, T>::type;   // type of the products' operands
 
   uint32_t q[D / 16][NT][2];
@@ -337,6 +338,7 @@ struct FmaEngine {
   static constexpr int kPitch = D + 4;
   static constexpr int kSharedQ = kRows * D + kWarps * (kKeys * kRows + kRows);   // floats: q, then each warp's weights and factors
   static constexpr int kPer = kRows * kKeys / 32;
+  static constexpr int kMostPerSm = 3;
   static constexpr int kLaneChunks = D / 4 >= 32 ? D / 128 : 1;
   static constexpr int kGroups = D / 4 >= 32 ? 1 : 32 / (D / 4);   // lanes sharing a chunk, each with its keys
 
@@ -467,29 +469,104 @@ struct FmaEngine {
 
 // ---- the split kernel ----------------------------------------------------------------
 
+constexpr int kRingBytes = 16384;        // of a warp's ring
 template <class E>
 struct SplitShape {
   static constexpr int kUnit = kWarps * E::kKeys;                     // keys of a unit
   static constexpr int kTileBytes = 2 * E::kKeys * E::kRowBytes;      // K and V of a tile
-  static constexpr int kStages = 24576 / kTileBytes >= 3 ? 24576 / kTileBytes : 3;
+  static constexpr int kStages = kRingBytes / kTileBytes >= 2 ? kRingBytes / kTileBytes : 2;
   static constexpr int kWarpBytes = kStages * kTileBytes;
+  // A warp's output waits for the join in the last tile of its ring: the next
+  // segment's first loads take the others.
+  static constexpr int kJoinAt = (kStages - 1) * kTileBytes;
+  static_assert(E::kRows * E::kPitch * 4 <= kTileBytes, "the output fits a tile");
   static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes + (size_t)E::kSharedQ * 4;
-  static constexpr int kPerSm = 2 * (kSmem + 2048) <= 227 * 1024 ? 2 : 1;
-  static_assert(kSmem + 2048 <= 227 * 1024, "a CTA fits an SM");
-  static_assert(kWarpBytes >= E::kRows * E::kPitch * 4, "a warp's output is joined in its ring");
+  static constexpr int kFit = 227 * 1024 / (int)(kSmem + 2048);
+  static constexpr int kPerSm = kFit < E::kMostPerSm ? kFit : E::kMostPerSm;
+  static_assert(kPerSm >= 1, "a CTA fits an SM");
 };
-constexpr int kMinUnits = 4;             // units of a CTA's run, at least
+constexpr int kMinUnits = 1;             // units of a CTA's run, at least
+
+// A segment: a CTA's share of one item.
+struct SplitSeg {
+  int32_t r;                             // request; -1: the run has ended
+  int32_t row0, n, seq;
+  int32_t head, tile;
+  int32_t k_lo, k_hi;                    // keys
+  int32_t slot;                          // of the partial result; -1: the item is whole
+  int32_t parts;                         // of an item that begins here and goes on in other CTAs; else 0
+};
+
+// One thread's walk over the segments of its CTA's run.  What it reads of a
+// request is handed to the CTA through shared memory, so that the CTA agrees
+// on its segments whatever happens to the caller's arrays meanwhile; the next
+// request is read one step ahead.
+struct SplitWalk {
+  int64_t u, u_end, u_first, run, base;  // base: first unit of request r
+  int r;
+  Req q, ahead;
+
+  __device__ __forceinline__ void start(const AttendArgs& a, int r_, int64_t base_, int64_t u_, int64_t u_end_, int64_t run_) {
+    r = r_;
+    base = base_;
+    u = u_first = u_;
+    u_end = u_end_;
+    run = run_;
+    q = read_request(a, r, false);
+    look_ahead(a);
+  }
+  __device__ __forceinline__ void look_ahead(const AttendArgs& a) {
+    if (r + 1 < a.R) ahead = read_request(a, r + 1, false);
+    else ahead.n = 0;
+  }
+  template <int ROWS, int UNIT>
+  __device__ __forceinline__ void next(const AttendArgs& a, SplitSeg* out) {
+    out->r = -1;
+    if (u >= u_end) return;
+    while (true) {
+      const int tiles = tiles_of(a, q, ROWS), units = units_of(q, UNIT);
+      if (u >= base + (int64_t)a.H * tiles * units) {
+        base += (int64_t)a.H * tiles * units;
+        if (++r >= a.R) return;          // the arrays have changed under the call
+        q = ahead;
+        look_ahead(a);
+        continue;
+      }
+      const int item = (int)((u - base) / units);
+      const int64_t item0 = base + (int64_t)item * units;
+      const int ua = (int)(u - item0), ub = (int)min((int64_t)units, u_end - item0);
+      const int head = item / tiles, tile = item - head * tiles;
+      const int last_tok = min(q.n - 1, (tile * ROWS + ROWS - 1) / a.G);
+      out->row0 = q.row0;
+      out->n = q.n;
+      out->seq = q.seq;
+      out->head = head;
+      out->tile = tile;
+      out->k_lo = q.kb + ua * UNIT;
+      out->k_hi = min(min(q.ke, q.seq - q.n + last_tok + 1), q.kb + ub * UNIT);
+      out->slot = ua == 0 && ub == units ? -1 : 2 * blockIdx.x + (u == u_first ? 0 : 1);
+      out->parts = ua == 0 && ub < units ? (int)((item0 + units - 1) / run) - (int)blockIdx.x + 1 : 0;
+      out->r = r;
+      u = item0 + ub;
+      return;
+    }
+  }
+};
 
 template <typename T, class E>
-__global__ void __launch_bounds__(kAttendThreads) attend_split_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_split_kernel(const AttendArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   using S = SplitShape<E>;
   constexpr int ROWS = E::kRows, D = E::D, KT = E::kKeys, PITCH = E::kPitch;
-  __shared__ int64_t scratch[33];
+  __shared__ int64_t scratch[kWarps];
   __shared__ int64_t s_base;
   __shared__ int32_t s_req;
+  __shared__ SplitSeg s_seg[2];
   __shared__ float s_ml[kWarps][2 * ROWS];
+  __shared__ uint32_t s_valid[kWarps][S::kStages];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float* outs = reinterpret_cast<const float*>(smem + S::kJoinAt);
+  float* so = reinterpret_cast<float*>(smem + warp * S::kWarpBytes + S::kJoinAt);
   float* sq = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);
   pdl_wait();
   pdl_trigger();
@@ -503,19 +580,19 @@ __global__ void __launch_bounds__(kAttendThreads) attend_split_kernel(const Atte
     mine += (int64_t)a.H * tiles_of(a, q, ROWS) * units_of(q, S::kUnit);
   }
   int64_t total;
-  int64_t at = block_exclusive_scan(mine, scratch, &total);
+  int64_t at = block_exclusive_scan_1bar<kWarps>(mine, scratch, &total);
   const int64_t run = max((int64_t)kMinUnits, (total + gridDim.x - 1) / gridDim.x);
-  int64_t u = (int64_t)blockIdx.x * run;
-  const int64_t u_first = u, u_end = min(total, u + run);
+  const int64_t u = (int64_t)blockIdx.x * run, u_end = min(total, u + run);
   if (u >= u_end) {
     if (tid == 0) record_of(a, blockIdx.x)->parts = 0;
     return;
   }
+  SplitWalk walk;                        // thread 0's
   if (at <= u && u < at + mine) {
     for (int r = r0; r < r1; ++r) {
       const Req q = read_request(a, r, false);
       const int64_t n = (int64_t)a.H * tiles_of(a, q, ROWS) * units_of(q, S::kUnit);
-      if (u < at + n) {
+      if (u < at + n || r == r1 - 1) {
         s_req = r;
         s_base = at;
         break;
@@ -524,89 +601,88 @@ __global__ void __launch_bounds__(kAttendThreads) attend_split_kernel(const Atte
     }
   }
   __syncthreads();
-  int r = s_req;
-  int64_t base = s_base;                 // first unit of request r
-  bool crossed = false;                  // the last item goes on in the next CTA, and began here
+  if (tid == 0) {
+    walk.start(a, s_req, s_base, u, u_end, run);
+    walk.template next<ROWS, S::kUnit>(a, &s_seg[0]);
+  }
+  __syncthreads();
 
   const uint32_t ring = smem_addr(smem) + warp * S::kWarpBytes;
-  float* so = reinterpret_cast<float*>(smem + warp * S::kWarpBytes);
   const int64_t token_bytes = (int64_t)a.H * E::kRowBytes;
 
-  while (u < u_end) {
-    Req q = read_request(a, r, false);
-    const int tiles = tiles_of(a, q, ROWS), units = units_of(q, S::kUnit);
-    if (u >= base + (int64_t)a.H * tiles * units) {
-      base += (int64_t)a.H * tiles * units;
-      ++r;
-      continue;
+  // Loads of the current segment's tiles of this warp: tile warp + i * kWarps.  Lane i < KT looks up key i of a tile,
+  // one tile ahead of its loads.
+  int k_lo = 0, k_hi = 0, n_mine = 0;
+  const int32_t* table = nullptr;
+  const uint8_t* kbase = nullptr;
+  int32_t id_next = -1, off_next = 0;
+  auto look_up = [&](int i) {
+    const int j = k_lo + (warp + i * kWarps) * KT + lane;
+    id_next = -1;
+    if (i < n_mine && lane < KT && j < k_hi) {
+      const int b = j / a.block_size;
+      off_next = j - b * a.block_size;
+      id_next = table[b];
+      if (id_next < 0 || id_next >= a.num_blocks) {
+        latch(a.status, IS_ST_BLOCK_ID);
+        id_next = -1;
+      }
     }
-    const int item = (int)((u - base) / units);
-    const int head = item / tiles, tile = item - head * tiles;
-    const int64_t item0 = base + (int64_t)item * units;
-    const int ua = (int)(u - item0);
-    const int ub = (int)min((int64_t)units, u_end - item0);
-    const bool whole = ua == 0 && ub == units;
-    // Keys of this segment that some row of the tile sees.
-    const int last_tok = min(q.n - 1, (tile * ROWS + ROWS - 1) / a.G), first_tok = tile * ROWS / a.G;
-    const int p_first = q.seq - q.n + first_tok, p_last = q.seq - q.n + last_tok;
-    const int k_lo = q.kb + ua * S::kUnit;
-    const int k_hi = min(min(q.ke, p_last + 1), q.kb + ub * S::kUnit);
+  };
+  auto issue = [&](int i, int stage) {
+    if (i < n_mine) {
+      const long long off = id_next < 0 ? -1ll : ((long long)id_next * a.block_size + off_next) * token_bytes;
+      const uint32_t valid = __ballot_sync(0xffffffffu, off >= 0);
+      if (lane == 0) s_valid[warp][stage] = valid;
+      look_up(i + 1);
+      constexpr int CPR = E::kRowBytes / 16;             // chunks of a row
+      constexpr int RPI = CPR >= 32 ? 1 : 32 / CPR;      // rows of one pass of the warp
+      constexpr int PASS = CPR >= 32 ? CPR / 32 : 1;     // passes of one row
+      const uint32_t kd = ring + stage * S::kTileBytes, vd = kd + KT * E::kRowBytes;
+#pragma unroll
+      for (int x = 0; x < KT; x += RPI) {
+        const int row = x + (RPI > 1 ? lane / CPR : 0);
+        const long long o = __shfl_sync(0xffffffffu, off, row);
+        const bool in = o >= 0;
+#pragma unroll
+        for (int y = 0; y < PASS; ++y) {
+          const int c = (RPI > 1 ? lane % CPR : lane) + 32 * y;
+          const uint8_t* src = kbase + (in ? o : 0) + c * 16;
+          const uint32_t dst = chunk_at<E::kRowBytes>(row, c);
+          cp_async16(kd + dst, src, in);
+          cp_async16(vd + dst, src + a.v_offset, in);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  auto open = [&](const SplitSeg& g) {
+    k_lo = g.k_lo;
+    k_hi = g.k_hi;
+    table = a.block_table + (size_t)g.r * a.max_blocks;
+    kbase = a.k_cache + (size_t)g.head * E::kRowBytes;
+    const int n_tiles = k_hi > k_lo ? (k_hi - k_lo + KT - 1) / KT : 0;
+    n_mine = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
+    look_up(0);
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) issue(s, s);
+  };
+
+  bool crossed = false;                  // the run's last item began here and goes on in the next CTA
+  if (s_seg[0].r >= 0) open(s_seg[0]);
+  for (int k = 0; s_seg[k & 1].r >= 0; ++k) {
+    const SplitSeg& g = s_seg[k & 1];
+    if (tid == 0) walk.template next<ROWS, S::kUnit>(a, &s_seg[(k + 1) & 1]);
+    Req q;
+    q.row0 = g.row0;
+    q.n = g.n;
+    q.seq = g.seq;
+    const int head = g.head, tile = g.tile;
+    const int p_first = q.seq - q.n + tile * ROWS / a.G;
+    const int p_last = q.seq - q.n + min(q.n - 1, (tile * ROWS + ROWS - 1) / a.G);
 
     E e;
     e.begin(a, q, head, tile, sq);
-    const int n_tiles = k_hi > k_lo ? (k_hi - k_lo + KT - 1) / KT : 0;
-    const int n_mine = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
-    const int32_t* table = a.block_table + (size_t)r * a.max_blocks;
-    const uint8_t* kbase = a.k_cache + (size_t)head * E::kRowBytes;
-
-    // Lane i < KT looks up key i of a tile, one tile ahead of its loads.
-    int32_t id_next = 0, off_next = 0;
-    auto look_up = [&](int i) {
-      const int j = k_lo + (warp + i * kWarps) * KT + lane;
-      id_next = -1;
-      if (i < n_mine && lane < KT && j < k_hi) {
-        const int b = j / a.block_size;
-        off_next = j - b * a.block_size;
-        id_next = table[b];
-        if (id_next < 0 || id_next >= a.num_blocks) {
-          latch(a.status, IS_ST_BLOCK_ID);
-          id_next = -1;
-        }
-      }
-    };
-    uint32_t valid_of[S::kStages];
-    auto issue = [&](int i, int stage) {
-      uint32_t valid = 0;
-      if (i < n_mine) {
-        const long long off = id_next < 0 ? -1ll : ((long long)id_next * a.block_size + off_next) * token_bytes;
-        valid = __ballot_sync(0xffffffffu, off >= 0);
-        look_up(i + 1);
-        constexpr int CPR = E::kRowBytes / 16;             // chunks of a row
-        constexpr int RPI = CPR >= 32 ? 1 : 32 / CPR;      // rows of one pass of the warp
-        constexpr int PASS = CPR >= 32 ? CPR / 32 : 1;     // passes of one row
-        const uint32_t kd = ring + stage * S::kTileBytes, vd = kd + KT * E::kRowBytes;
-#pragma unroll
-        for (int x = 0; x < KT; x += RPI) {
-          const int row = x + (RPI > 1 ? lane / CPR : 0);
-          const long long o = __shfl_sync(0xffffffffu, off, row);
-          const bool in = o >= 0;
-#pragma unroll
-          for (int y = 0; y < PASS; ++y) {
-            const int c = (RPI > 1 ? lane % CPR : lane) + 32 * y;
-            const uint8_t* src = kbase + (in ? o : 0) + c * 16;
-            const uint32_t dst = chunk_at<E::kRowBytes>(row, c);
-            cp_async16(kd + dst, src, in);
-            cp_async16(vd + dst, src + a.v_offset, in);
-          }
-        }
-      }
-      cp_async_commit();
-      return valid;
-    };
-    look_up(0);
-#pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) valid_of[s] = issue(s, s);
-    valid_of[S::kStages - 1] = 0;
     for (int i0 = 0; i0 < n_mine; i0 += S::kStages) {
 #pragma unroll
       for (int s = 0; s < S::kStages; ++s) {
@@ -614,27 +690,28 @@ __global__ void __launch_bounds__(kAttendThreads) attend_split_kernel(const Atte
         if (i < n_mine) {
           cp_async_wait<S::kStages - 2>();
           __syncwarp();                  // every lane's part of tile i has landed, and all are done with tile i - 1
-          const uint32_t valid = valid_of[s];
-          valid_of[(s + S::kStages - 1) % S::kStages] = issue(i + S::kStages - 1, (s + S::kStages - 1) % S::kStages);
           TileMask tm;
+          tm.valid = s_valid[warp][s];
+          issue(i + S::kStages - 1, (s + S::kStages - 1) % S::kStages);
           tm.key0 = k_lo + (warp + i * kWarps) * KT;
-          tm.valid = valid;
           constexpr uint32_t kFull = KT == 32 ? 0xffffffffu : (1u << KT) - 1u;
-          tm.check = valid != kFull || tm.key0 + KT - 1 > p_first || (a.window > 0 && tm.key0 <= p_last - a.window);
+          tm.check = tm.valid != kFull || tm.key0 + KT - 1 > p_first || (a.window > 0 && tm.key0 <= p_last - a.window);
           const uint32_t kd = ring + s * S::kTileBytes;
           e.step(a, kd, kd + KT * E::kRowBytes, tm, sq);
         }
       }
     }
     cp_async_wait<0>();
-    __syncwarp();
+    __syncwarp();                        // every lane is done with the ring
     e.finish(so, s_ml[warp]);
     __syncthreads();
+    // The next segment's first tiles are on their way while this one's output is joined.
+    if (s_seg[(k + 1) & 1].r >= 0) open(s_seg[(k + 1) & 1]);
 
     // Join the warps.  Every thread takes pairs of elements.
     const int rho0 = tile * ROWS, rows = min(ROWS, q.n * a.G - rho0);
-    Partial<ROWS, D>* part = whole ? nullptr : partial_of<ROWS, D>(a, 2 * blockIdx.x + (u == u_first ? 0 : 1));
-    const float* all = reinterpret_cast<const float*>(smem);
+    const int slot = g.slot;
+    Partial<ROWS, D>* part = partial_of<ROWS, D>(a, max(slot, 0));
     for (int x = tid; x < rows * (D / 2); x += kAttendThreads) {
       const int row = x / (D / 2), d = (x % (D / 2)) * 2;
       float mx = -INFINITY;
@@ -645,12 +722,12 @@ __global__ void __launch_bounds__(kAttendThreads) attend_split_kernel(const Atte
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2(s_ml[w][row] - m0);
-        const float2 v = *reinterpret_cast<const float2*>(all + (size_t)w * (S::kWarpBytes / 4) + row * PITCH + d);
+        const float2 v = *reinterpret_cast<const float2*>(outs + (size_t)w * (S::kWarpBytes / 4) + row * PITCH + d);
         ox = fmaf(f, v.x, ox);
         oy = fmaf(f, v.y, oy);
         l = fmaf(f, s_ml[w][ROWS + row], l);
       }
-      if (whole) {
+      if (slot < 0) {
         const float inv = l == 0.f ? 0.f : a.v_scale / l;
         store_out<T>(a, q, head, rho0 + row, d, l == 0.f ? 0.f : ox * inv, l == 0.f ? 0.f : oy * inv);
         if (d == 0) store_lse(a, q, head, rho0 + row, mx, l);
@@ -662,19 +739,18 @@ __global__ void __launch_bounds__(kAttendThreads) attend_split_kernel(const Atte
         }
       }
     }
-    if (!whole && ua == 0 && tid == 0) {
-      // The item begins here and ends in a later CTA: this CTA's record names its parts.
+    if (slot >= 0 && g.parts > 0 && tid == 0) {
+      // The item begins here and goes on in other CTAs: this CTA's record names its parts.
       JoinRecord* rec = record_of(a, blockIdx.x);
-      rec->parts = (int32_t)((item0 + units - 1) / run - blockIdx.x) + 1;
-      rec->slot0 = 2 * blockIdx.x + (u == u_first ? 0 : 1);
+      rec->parts = g.parts;
+      rec->slot0 = slot;
       rec->row0 = q.row0;
       rec->head = head;
       rec->rho0 = rho0;
       rec->rows = rows;
     }
-    crossed = !whole && ua == 0;
-    u = item0 + ub;
-    __syncthreads();                     // the ring and s_ml are free again
+    crossed = slot >= 0 && g.parts > 0;
+    __syncthreads();                     // s_ml and the warps' outputs are free again
   }
   if (!crossed && tid == 0) record_of(a, blockIdx.x)->parts = 0;
 }
@@ -687,7 +763,7 @@ static cudaError_t launch_split(const AttendArgs& a, const LaunchCfg& cfg) {
   auto* kern = attend_split_kernel<T, E>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
-  static_assert(kMaxCtas * (kRecordBytes + 2 * sizeof(Partial<E::kRows, E::D>)) <= IS_ATTEND_WORKSPACE_BYTES,
+  static_assert(partials_offset() + kMaxCtas * 2 * sizeof(Partial<E::kRows, E::D>) <= IS_ATTEND_WORKSPACE_BYTES,
                 "the workspace holds every partial");
   // As many CTAs as the SMs hold; fewer when the table's reach shows that there are fewer runs.
   const int64_t keys = (int64_t)a.max_blocks * a.block_size;

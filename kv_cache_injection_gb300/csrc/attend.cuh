@@ -75,6 +75,7 @@ struct JoinRecord {
 };
 constexpr size_t kRecordBytes = 32;
 constexpr int kMaxCtas = 1024;
+constexpr size_t partials_offset() { return kMaxCtas * kRecordBytes; }
 template <int ROWS, int D>
 struct Partial {
   float o[ROWS][D];
@@ -86,7 +87,7 @@ __device__ __forceinline__ JoinRecord* record_of(const AttendArgs& a, int cta) {
 }
 template <int ROWS, int D>
 __device__ __forceinline__ Partial<ROWS, D>* partial_of(const AttendArgs& a, int slot) {
-  return reinterpret_cast<Partial<ROWS, D>*>(a.workspace + (size_t)kMaxCtas * kRecordBytes) + slot;
+  return reinterpret_cast<Partial<ROWS, D>*>(a.workspace + partials_offset()) + slot;
 }
 
 template <typename T>

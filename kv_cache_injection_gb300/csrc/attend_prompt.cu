@@ -909,7 +909,7 @@ static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
   static_assert(S::kSmem + 1024 <= 227 * 1024, "a CTA fits an SM");
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
-  constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - kMaxCtas * kRecordBytes) / (2 * sizeof(Partial<prompt::kRows, D>)));
+  constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - partials_offset()) / (2 * sizeof(Partial<prompt::kRows, D>)));
   const int grid = std::max(1, std::min({cfg.num_sms, kFit, kMaxCtas}));
   const int per = prompt::kRows / a.G;   // tokens of an item
   // Bulk copies bring `box` rows at once: a block, or 128 rows of a longer one.
