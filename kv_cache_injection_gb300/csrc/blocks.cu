@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
   int64_t total, all_missing;
   int64_t at = block_exclusive_scan_1bar<kExtendThreads / 32>(tokens, scratch[0], &total);
   int64_t taken = block_exclusive_scan_1bar<kExtendThreads / 32>(missing, scratch[1], &all_missing);
+  int32_t used = 0;                      // blocks taken up to this thread's last request
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int r = r0 + i;
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
         bits |= IS_ST_FREE_LIST;
         len[i] = -1;
       } else {
-        atomicMax(&s_used, (int32_t)(taken + miss));
+        used = (int32_t)(taken + miss);
       }
     }
     s_seq[r] = len[i];
@@ -103,6 +104,8 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
     at += add[i];
     taken += miss;
   }
+  used = __reduce_max_sync(0xffffffffu, used);
+  if ((tid & 31) == 0) atomicMax(&s_used, used);
   if (tid == 0) s_start[R] = (int32_t)min(total, (int64_t)INT32_MAX);
   if (total > a.max_tokens) bits |= IS_ST_COUNT;
   __syncthreads();
