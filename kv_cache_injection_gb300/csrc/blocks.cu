@@ -18,21 +18,44 @@
 
 namespace isk {
 
-constexpr int kExtendThreads = 512;
+// Few requests: small CTAs, two requests a thread at most.  Many: large ones,
+// since each CTA goes over all requests (4096 requests with 614,000 tokens:
+// 14.1 us with 512 threads a CTA, 12.1 us with 1024).
+constexpr int kFewRequests = 512, kFewThreads = 256, kManyThreads = 1024;
 constexpr int kTokensPerThread = 4;
-constexpr int kTokensPerCta = kExtendThreads * kTokensPerThread;
 
-// Lengths and block sizes stay below 2^25 here, so 32-bit arithmetic suffices.
-__device__ __forceinline__ int32_t blocks_of(int32_t n, int32_t bs) { return (int32_t)((uint32_t)(n + bs - 1) / (uint32_t)bs); }
+// Division by the block size as a multiplication: with 2^(k-1) < bs <= 2^k and
+// mul = ceil(2^(26+k) / bs), x / bs = x * mul >> (26 + k) for every x < 2^26
+// (mul overshoots 2^(26+k) / bs by less than 1, so x * mul / 2^(26+k) by less
+// than 2^-k <= 1 / bs, which carries no quotient over the next whole number).
+// Lengths stay below 2^24 + 1 and block sizes at most 2^24, so x < 2^26.
+struct BlockDiv {
+  uint32_t mul, shift;
+};
+static BlockDiv block_div(int32_t bs) {
+  uint32_t k = 0;
+  while ((1ll << k) < bs) ++k;
+  return {(uint32_t)(((1ull << (26 + k)) + (uint64_t)bs - 1) / (uint64_t)bs), 26 + k};
+}
+__device__ __forceinline__ int32_t div_bs(int32_t x, const BlockDiv& d) {
+  return (int32_t)(((uint64_t)(uint32_t)x * d.mul) >> d.shift);
+}
+__device__ __forceinline__ int32_t blocks_of(int32_t n, int32_t bs, const BlockDiv& d) { return div_bs(n + bs - 1, d); }
 
-__global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_args_t a) {
+// Request r's place in the shared tables: threads that walk 2 or 4 consecutive
+// requests each then hit different banks.
+__host__ __device__ constexpr int at(int r) { return r + (r >> 5); }
+
+template <int kExtendThreads, int kPer>
+__global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_args_t a, const BlockDiv div) {
   extern __shared__ int32_t sm[];
   __shared__ int64_t scratch[2][kExtendThreads / 32];
   __shared__ int32_t s_used;
   const int R = a.num_requests, bs = a.block_size, tid = threadIdx.x;
+  const int pitch = at(R) + 1;
   int32_t* s_start = sm;                 // [R + 1] first packed token, INT32_MAX at most
-  int32_t* s_seq = sm + R + 1;           // [R] seq_len, or -1 if the request is refused
-  int32_t* s_take = s_seq + R;           // [R] free-list index of the request's table entry 0
+  int32_t* s_seq = sm + pitch;           // [R] seq_len, or -1 if the request is refused
+  int32_t* s_take = s_seq + pitch;       // [R] free-list index of the request's table entry 0
   pdl_wait();
   pdl_trigger();
   int32_t head = a.free_head ? a.free_head[0] : 0;
@@ -43,10 +66,9 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
   }
   const int32_t avail = a.num_free - head;
   if (tid == 0) s_used = 0;
-  const int per = (R + kExtendThreads - 1) / kExtendThreads;
-  const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
-  // A thread's requests are consecutive (at most 8); all their lengths are loaded before any is used.
-  constexpr int kPer = (IS_MAX_REQUESTS + kExtendThreads - 1) / kExtendThreads;
+  constexpr int kTokensPerCta = kExtendThreads * kTokensPerThread;
+  // A thread's requests are consecutive; all their lengths are loaded before any is used.
+  const int r0 = min(R, tid * kPer), r1 = min(R, r0 + kPer);
   int32_t len[kPer], add[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -54,6 +76,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
     len[i] = in ? a.seq_len[r0 + i] : 0;
     add[i] = in ? a.new_len[r0 + i] : 0;
   }
+  int32_t lack[kPer];                    // blocks missing
   int64_t tokens = 0, missing = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -68,28 +91,28 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
       bits |= IS_ST_POSITION;
       len[i] = -1;
     } else {
-      const int32_t need = blocks_of(n + m, bs);
+      const int32_t need = blocks_of(n + m, bs, div);
       if (m > 0 && need > a.max_blocks_per_seq) {
         bits |= IS_ST_BLOCK_TABLE;
         len[i] = -1;
       } else {
-        miss = need - blocks_of(n, bs);
+        miss = need - blocks_of(n, bs, div);
       }
     }
-    s_take[r0 + i] = miss;
+    lack[i] = miss;
     tokens += add[i];
     missing += miss;
   }
   int64_t total, all_missing;
-  int64_t at = block_exclusive_scan_1bar<kExtendThreads / 32>(tokens, scratch[0], &total);
+  int64_t first = block_exclusive_scan_1bar<kExtendThreads / 32>(tokens, scratch[0], &total);
   int64_t taken = block_exclusive_scan_1bar<kExtendThreads / 32>(missing, scratch[1], &all_missing);
   int32_t used = 0;                      // blocks taken up to this thread's last request
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int r = r0 + i;
     if (r >= r1) continue;
-    const int32_t miss = s_take[r];
-    s_start[r] = (int32_t)min(at, (int64_t)INT32_MAX);
+    const int32_t miss = lack[i];
+    s_start[at(r)] = (int32_t)min(first, (int64_t)INT32_MAX);
     if (len[i] >= 0 && miss > 0) {
       if (taken + miss > avail) {
         bits |= IS_ST_FREE_LIST;
@@ -98,22 +121,22 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
         used = (int32_t)(taken + miss);
       }
     }
-    s_seq[r] = len[i];
+    s_seq[at(r)] = len[i];
     // entry j >= the blocks held of the row is free_blocks[s_take + j]
-    s_take[r] = len[i] < 0 ? 0 : head + (int32_t)taken - blocks_of(len[i], bs);
-    at += add[i];
+    s_take[at(r)] = len[i] < 0 ? 0 : head + (int32_t)taken - blocks_of(len[i], bs, div);
+    first += add[i];
     taken += miss;
   }
   used = __reduce_max_sync(0xffffffffu, used);
   if ((tid & 31) == 0) atomicMax(&s_used, used);
-  if (tid == 0) s_start[R] = (int32_t)min(total, (int64_t)INT32_MAX);
+  if (tid == 0) s_start[at(R)] = (int32_t)min(total, (int64_t)INT32_MAX);
   if (total > a.max_tokens) bits |= IS_ST_COUNT;
   __syncthreads();
 
   // Slots and positions of this CTA's packed tokens, a warp's 32 consecutive ones at a time: all searches, then all
   // block ids, then all stores, so that their latencies overlap.
   const int64_t t0 = (int64_t)blockIdx.x * kTokensPerCta + tid;
-  const int32_t end = s_start[R];
+  const int32_t end = s_start[at(R)];
   int32_t pos[kTokensPerThread], id[kTokensPerThread];
 #pragma unroll
   for (int i = 0; i < kTokensPerThread; ++i) {
@@ -124,13 +147,13 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
     int lo = 0, hi = R;                  // last request that starts at or before t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s_start[mid] <= t) lo = mid; else hi = mid;
+      if (s_start[at(mid)] <= t) lo = mid; else hi = mid;
     }
-    const int32_t n = s_seq[lo];
+    const int32_t n = s_seq[at(lo)];
     if (n < 0) continue;
-    pos[i] = n + (int32_t)(t - s_start[lo]);
-    const int32_t j = (int32_t)((uint32_t)pos[i] / (uint32_t)bs);
-    const int32_t* src = j >= blocks_of(n, bs) ? a.free_blocks + (s_take[lo] + j)
+    pos[i] = n + (int32_t)(t - s_start[at(lo)]);
+    const int32_t j = div_bs(pos[i], div);
+    const int32_t* src = j >= blocks_of(n, bs, div) ? a.free_blocks + (s_take[at(lo)] + j)
                                                : a.block_table + ((size_t)lo * a.max_blocks_per_seq + j);
     id[i] = *src;
   }
@@ -143,7 +166,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
       if (id[i] < 0 || id[i] >= a.num_blocks)
         bits |= IS_ST_BLOCK_ID;
       else
-        slot = (int64_t)id[i] * bs + (int32_t)((uint32_t)pos[i] % (uint32_t)bs);
+        slot = (int64_t)id[i] * bs + (pos[i] - div_bs(pos[i], div) * bs);
     }
     a.slot_mapping_out[t] = slot;
     if (t < end && a.positions_out) a.positions_out[t] = pos[i];
@@ -152,16 +175,16 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
   // Table entries and per-request outputs: one warp per request.
   const int lane = tid & 31, nwarps = kExtendThreads / 32;
   for (int r = blockIdx.x * nwarps + (tid >> 5); r < R; r += gridDim.x * nwarps) {
-    const int32_t n = s_seq[r], m = a.new_len[r];
+    const int32_t n = s_seq[at(r)], m = a.new_len[r];
     if (n >= 0) {
-      const int32_t need = blocks_of(n + m, bs);
+      const int32_t need = blocks_of(n + m, bs, div);
       int32_t* row = a.block_table + (size_t)r * a.max_blocks_per_seq;
-      for (int j = blocks_of(n, bs) + lane; j < need; j += 32) row[j] = a.free_blocks[s_take[r] + j];
+      for (int j = blocks_of(n, bs, div) + lane; j < need; j += 32) row[j] = a.free_blocks[s_take[at(r)] + j];
     }
     if (lane == 0) {
       if (a.seq_len_out) a.seq_len_out[r] = n >= 0 ? n + m : a.seq_len[r];
       if (a.token_start_out) {
-        a.token_start_out[r] = s_start[r];
+        a.token_start_out[r] = s_start[at(r)];
         if (r == R - 1) a.token_start_out[R] = end;
       }
     }
@@ -170,12 +193,20 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
   if (bits) latch(a.status_out, bits);
 }
 
-cudaError_t launch_extend(const is_extend_args_t& a, const LaunchCfg& cfg) {
-  const size_t smem = ((size_t)3 * a.num_requests + 1) * sizeof(int32_t);
-  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(extend_kernel), smem);
+template <int THREADS, int PER>
+static cudaError_t launch_extend_t(const is_extend_args_t& a, const LaunchCfg& cfg) {
+  auto* kern = extend_kernel<THREADS, PER>;
+  const size_t smem = (size_t)3 * (at(a.num_requests) + 1) * sizeof(int32_t);
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int grid = (int)(((int64_t)a.max_tokens + kTokensPerCta - 1) / kTokensPerCta);
-  return launch_ex(extend_kernel, dim3(grid), dim3(kExtendThreads), smem, cfg.stream, cfg.pdl, a);
+  constexpr int per_cta = THREADS * kTokensPerThread;
+  const int grid = (int)(((int64_t)a.max_tokens + per_cta - 1) / per_cta);
+  return launch_ex(kern, dim3(grid), dim3(THREADS), smem, cfg.stream, cfg.pdl, a, block_div(a.block_size));
+}
+
+cudaError_t launch_extend(const is_extend_args_t& a, const LaunchCfg& cfg) {
+  static_assert(kFewRequests <= kFewThreads * 2 && IS_MAX_REQUESTS <= kManyThreads * 4, "every request has a thread");
+  return a.num_requests <= kFewRequests ? launch_extend_t<kFewThreads, 2>(a, cfg) : launch_extend_t<kManyThreads, 4>(a, cfg);
 }
 
 }  // namespace isk

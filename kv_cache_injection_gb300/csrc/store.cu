@@ -20,8 +20,8 @@ namespace isk {
 
 void prefer_max_shared(const void* kern) {
   static std::mutex mu;
-  static const void* done_kern[64];
-  static int done_dev[64];
+  static const void* done_kern[256];
+  static int done_dev[256];
   static int n_done = 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return;
@@ -30,7 +30,7 @@ void prefer_max_shared(const void* kern) {
     if (done_kern[i] == kern && done_dev[i] == dev) return;
   cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                        (int)cudaSharedmemCarveoutMaxShared);
-  if (n_done < 64) {
+  if (n_done < 256) {
     done_kern[n_done] = kern;
     done_dev[n_done] = dev;
     ++n_done;
@@ -39,9 +39,9 @@ void prefer_max_shared(const void* kern) {
 
 cudaError_t ensure_dynamic_smem(const void* kern, size_t bytes) {
   static std::mutex mu;
-  static const void* kern_set[64];
-  static int dev_set[64];
-  static size_t bytes_set[64];
+  static const void* kern_set[256];
+  static int dev_set[256];
+  static size_t bytes_set[256];
   static int n_set = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -53,7 +53,7 @@ cudaError_t ensure_dynamic_smem(const void* kern, size_t bytes) {
   if (slot >= 0 && bytes_set[slot] >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  if (slot < 0 && n_set < 64) slot = n_set++;
+  if (slot < 0 && n_set < 256) slot = n_set++;
   if (slot >= 0) {
     kern_set[slot] = kern;
     dev_set[slot] = dev;
