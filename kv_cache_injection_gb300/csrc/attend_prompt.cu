@@ -55,7 +55,7 @@ constexpr int kLoaderWarp = 8, kLoaders = 96, kMmaWarp = 11;
 // a row of S needs, the other four give it: 2 * 208 + 88 = 3 * 168.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMinRun = 4;               // units of a CTA's run, at least
-constexpr int kMaskRing = 4;
+constexpr int kMaskRing = 8;
 constexpr uint32_t kTmemAll = 512;
 
 template <int D>
@@ -66,6 +66,9 @@ struct Shape {
   static constexpr uint32_t kGroupBytes = kHalves * 1024;
   static constexpr uint32_t kTileBytes = 16 * kGroupBytes;
   static constexpr int kRing = D == 128 ? 5 : 8;              // K and V tiles in flight
+  // A tile's mask is written when its K has a place, that is once load 2 t - kRing has been released; the mask it
+  // replaces has been read once V of tile t - kMaskRing, load 2 (t - kMaskRing) + 1, has been released.
+  static_assert(2 * kMaskRing >= kRing + 1, "a mask is read before its place is used again");
   static constexpr size_t kSmem = 1024 + (2 + kRing) * (size_t)kTileBytes + 128 * 8;
   static constexpr uint32_t kOCol = 256;                      // first column of O_A; O_B follows D columns on
 };
@@ -680,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         };
         for (int j = 0; j < n_tiles; ++j, n_load += 2) {
           const int key0 = w.k_lo + j * kKeys;
-          const uint32_t slot = (n_load >> 1) % kMaskRing;   // last read four tiles ago: that tile's V has been released
+          const uint32_t slot = (n_load >> 1) % kMaskRing;
           if (box > 0) {
             const int64_t from = token;
             const bool whole_tile = agreed(lane >= groups || from >= 0);

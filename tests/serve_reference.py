@@ -89,28 +89,27 @@ def attend(q, seq, k, v, named, scale, window):
     (the table names the position).  Returns out, lse, sum_j p_j |v_j|, and the largest
     sum_d |q_d k_d| * scale and number of keys seen per (row, head)."""
     n, Hq, D = q.shape
-    H = k.shape[1]
-    out = torch.zeros(n, Hq, D, dtype=torch.float64)
+    S, H = k.shape[0], k.shape[1]
+    G = Hq // H
+    p = torch.arange(seq - n, seq)[:, None]
+    j = torch.arange(S)[None]
+    see = (j <= p) & named[None]
+    if window:
+        see &= j > p - window
+    seen = see.sum(1).to(torch.float64)
     lse = torch.full((n, Hq), -math.inf, dtype=torch.float64)
-    spread = torch.zeros(n, Hq, D, dtype=torch.float64)
+    out, spread = torch.zeros(n, Hq, D, dtype=torch.float64), torch.zeros(n, Hq, D, dtype=torch.float64)
     heft = torch.zeros(n, Hq, dtype=torch.float64)
-    seen = torch.zeros(n, dtype=torch.float64)
-    for i in range(n):
-        p = seq - n + i
-        lo = max(0, p - window + 1) if window else 0
-        js = [j for j in range(lo, p + 1) if j < len(named) and named[j]]
-        seen[i] = len(js)
-        if not js:
-            continue
-        kk, vv = k[js], v[js]
-        for h in range(Hq):
-            g = h // (Hq // H)
-            s = kk[:, g] @ q[i, h] * scale
-            lse[i, h] = torch.logsumexp(s, 0)
-            w = torch.exp(s - lse[i, h])
-            out[i, h] = w @ vv[:, g]
-            spread[i, h] = w @ vv[:, g].abs()
-            heft[i, h] = (kk[:, g].abs() @ q[i, h].abs()).max() * abs(scale)
+    if S == 0:
+        return out, lse, spread, heft, seen
+    some = seen > 0
+    for h in range(Hq):
+        kk, vv = k[:, h // G], v[:, h // G]
+        s = (q[:, h] @ kk.T * scale).masked_fill(~see, -math.inf)
+        lse[:, h] = torch.logsumexp(s, 1)
+        w = torch.where(some[:, None], torch.exp(s - lse[:, h, None]), torch.zeros(()).double())
+        out[:, h], spread[:, h] = w @ vv, w @ vv.abs()
+        heft[:, h] = (q[:, h].abs() @ kk.abs().T).masked_fill(~see, 0.0).amax(1) * abs(scale)
     return out, lse, spread, heft, seen
 
 

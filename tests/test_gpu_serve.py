@@ -396,6 +396,16 @@ def test_few_and_many_rows(Hq, H, D, dtype, cache):
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("Hq,H,D,bs,window", [(4, 1, 64, 16, 0), (7, 1, 64, 24, 0), (4, 2, 128, 16, 0), (4, 1, 128, 5, 0),
+                                              (2, 1, 256, 16, 0), (4, 1, 64, 8, 700), (4, 1, 128, 128, 900)])
+def test_long_prompts(Hq, H, D, bs, window, dtype, cache):
+    """Dozens of key tiles a request, so that every ring of the pipeline goes round many times; several items a CTA
+    and items cut between CTAs."""
+    sc = SCALES.get(cache, (1.0, 1.0))
+    attend_case([(3333, 200), (70, 70), (5000, 129), (1999, 1)], Hq, H, D, dtype, cache, bs=bs, window=window, scales=sc)
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
 def test_rows_that_see_nothing(dtype, cache):
     """More rows than tokens: the first ones stand before position 0.  Empty caches."""
     sc = SCALES.get(cache, (1.0, 1.0))
