@@ -16,7 +16,7 @@
 //               bulk tensor copies, a block of the paged cache at a time; tiles
 //               with missing keys (zero-filled) and block sizes those do not
 //               fit with 16-byte asynchronous copies, row by row; FP8 rows
-//               through registers, widened on the way (exactly)
+//               likewise, as bytes, and widened to fp16 from there (exactly)
 //   warp 11     one elected thread issues the MMAs
 // Tensor memory (512 columns): S_A, S_B (128 each; P takes the first half of
 // its S as 16-bit pairs), O_A, O_B (D each).  Shared memory: Q (2 x 128 rows),
@@ -58,18 +58,21 @@ constexpr int kMinRun = 4;               // units of a CTA's run, at least
 constexpr int kMaskRing = 8;
 constexpr uint32_t kTmemAll = 512;
 
-template <int D>
+template <int D, bool F8>
 struct Shape {
   static constexpr int kHalves = D / 64;
   // A tile is 16 groups of 8 rows; a group holds the 64-element halves of its
   // rows one after the other, 1024 bytes each (one swizzle atom).
   static constexpr uint32_t kGroupBytes = kHalves * 1024;
   static constexpr uint32_t kTileBytes = 16 * kGroupBytes;
-  static constexpr int kRing = D == 128 ? 5 : 8;              // K and V tiles in flight
+  static constexpr int kRing = F8 ? (D == 128 ? 3 : 5) : D == 128 ? 5 : 8;   // K and V tiles in shared memory
+  // FP8 rows are copied as they are, kRaw tiles ahead, and widened from there.
+  static constexpr int kRaw = D == 128 ? 3 : 4;
+  static constexpr uint32_t kRawBytes = F8 ? 128 * D : 0;
   // A tile's mask is written when its K has a place, that is once load 2 t - kRing has been released; the mask it
   // replaces has been read once V of tile t - kMaskRing, load 2 (t - kMaskRing) + 1, has been released.
   static_assert(2 * kMaskRing >= kRing + 1, "a mask is read before its place is used again");
-  static constexpr size_t kSmem = 1024 + (2 + kRing) * (size_t)kTileBytes + 128 * 8;
+  static constexpr size_t kSmem = 1024 + (2 + kRing) * (size_t)kTileBytes + kRaw * (size_t)kRawBytes + 128 * 8;
   static constexpr uint32_t kOCol = 256;                      // first column of O_A; O_B follows D columns on
 };
 
@@ -146,10 +149,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 // are K-major: groups of 8 rows follow one another (stride byte offset).  For
 // O += P V the keys are K: again 8 to a group (stride byte offset), and N runs
 // over the 64 elements of a row and then the halves (leading byte offset).
-template <int D>
+template <int D, bool F8>
 __device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, uint32_t leading) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)leading << 16) |
-         ((uint64_t)(Shape<D>::kGroupBytes >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+         ((uint64_t)(Shape<D, F8>::kGroupBytes >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
 // kind::f16 instruction descriptor: D fp32 (bit 4), A and B fp16 or bf16
@@ -252,18 +255,9 @@ __device__ __forceinline__ uint32_t bits_between(int at, int lo, int hi) {
   return (h - l == 32 ? 0xffffffffu : ((1u << (h - l)) - 1u)) << l;
 }
 
-// Eight E4M3 bytes as eight 16-bit values, exact.
-template <typename T>
+// Eight E4M3 bytes as eight fp16 values, exact.
 __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
-  uint32_t w[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi), e4m3x2_f16x2(hi >> 16)};
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      w[i] = Vec<__nv_bfloat16>::pack2(f.x, f.y);
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(e4m3x2_f16x2(lo), e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi), e4m3x2_f16x2(hi >> 16));
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -287,21 +281,25 @@ __device__ __forceinline__ void quad_transpose(uint4 (&v)[4], int lane) {
 // Where 16-byte chunk c (8 elements) of row `row` lies in a tile.
 template <int D>
 __device__ __forceinline__ uint32_t at_chunk(int row, int c) {
-  return (uint32_t)(row >> 3) * Shape<D>::kGroupBytes + (uint32_t)(c >> 3) * 1024u + (uint32_t)(row & 7) * 128u +
+  return (uint32_t)(row >> 3) * Shape<D, false>::kGroupBytes + (uint32_t)(c >> 3) * 1024u + (uint32_t)(row & 7) * 128u +
          (uint32_t)(((c & 7) ^ (row & 7)) * 16);
 }
 
 template <typename T, bool F8, int D>
 __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a, int per, int box,
                                                                    const __grid_constant__ CUtensorMap rows_map) {
-  using S = Shape<D>;
-  // FP8 values are exact in fp16 too, where the weights keep three more bits.
+  using S = Shape<D, F8>;
+  // FP8 keys and values are exact in fp16, and so is a bf16 query row scaled by a power of two (undone in the logits):
+  // with an FP8 cache both products are taken in fp16.
   using W = typename std::conditional<F8, __half, T>::type;
+  constexpr bool kShift = F8 && std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(16) uint32_t s_mask[kMaskRing][4];
+  __shared__ uint32_t s_raw_mask[S::kRaw][4];
+  __shared__ float s_unscale[kShift ? kRows : 1];
   __shared__ int64_t scratch[33];
   __shared__ int64_t s_base;
   __shared__ int32_t s_req;
@@ -310,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   volatile int* abort_flag = &s_abort;
   const uint32_t tiles0 = (smem_addr(smem_raw) + 1023u) & ~1023u;     // Q_A, Q_B, then the ring
   const uint32_t ring0 = tiles0 + 2 * S::kTileBytes;
-  long long* s_off = reinterpret_cast<long long*>(smem_raw + (ring0 - smem_addr(smem_raw)) + S::kRing * S::kTileBytes);
+  long long* s_off = reinterpret_cast<long long*>(smem_raw + (ring0 - smem_addr(smem_raw)) + S::kRing * S::kTileBytes + S::kRaw * S::kRawBytes);
 
   if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&s_tmem), kTmemAll);
@@ -381,9 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       const int side = warp >> 2;                      // 0: tile A, 1: tile B
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
       const uint32_t s_col = tmem + lanes + 128u * side, o_col = tmem + lanes + S::kOCol + (uint32_t)(D * side);
-      const float sc = a.scale * kLog2e;
+      const float sc0 = a.scale * kLog2e;
       const int row = side * 128 + (warp & 3) * 32 + lane, tok = row / a.G;
-      uint32_t n_s = 0, n_o = 0, n_mask = 0;           // phases consumed
+      uint32_t n_s = 0, n_o = 0, n_mask = 0, n_q = 0;  // phases consumed
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, kWaitBudgetNs));
@@ -402,7 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         const int lim_hi = __reduce_max_sync(0xffffffffu, lim);
         const int low = a.window > 0 ? (int)max((int64_t)lim - a.window + 1, (int64_t)0) : 0;
         const int low_hi = a.window > 0 ? (int)max((int64_t)lim_hi - a.window + 1, (int64_t)0) : 0;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, sc = sc0;
+        if (kShift && n_tiles > 0) {
+          if (!wait(&bars.q_full, n_q & 1u)) break;
+          ++n_q;
+          sc = sc0 * s_unscale[row];
+        }
         if (!has) n_mask += n_tiles;
         for (int j = 0, key0 = g.k_lo; has && j < n_tiles; ++j, ++n_mask, key0 += kKeys) {
           const int slot = n_mask % kMaskRing;
@@ -630,15 +633,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           const uint32_t g_inv = (65536u + a.G - 1) / a.G;   // row / G = row * g_inv >> 16 for row < 256, G <= 64
           const int c = lt % C;
           const uint8_t* src = a.q + (int64_t)(w.q.row0 + w.x.tok0) * a.q_stride + (size_t)w.head * a.G * D * 2 + c * 16;
-#pragma unroll 8
-          for (int row = lt / C; row < kRows; row += RP) {
+          auto from = [&](int row) {
             const int tok = (int)((uint32_t)row * g_inv >> 16);
-            const bool in = row < w.rows;
-            cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c),
-                       in ? src + tok * a.q_stride + (row - tok * a.G) * (D * 2) : src, in);
+            return row < w.rows ? src + tok * a.q_stride + (row - tok * a.G) * (D * 2) : src;
+          };
+          if constexpr (!kShift) {
+#pragma unroll 8
+            for (int row = lt / C; row < kRows; row += RP)
+              cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), from(row), row < w.rows);
+            cp_async_commit();
+            cp_async_wait<0>();
+          } else {
+            // bf16 to fp16: the C lanes of a row scale it by a power of two that brings its largest element to
+            // [2^14, 2^15), and leave the inverse for the softmax.
+            constexpr int N = 4;
+            for (int r0 = 0; r0 < kRows; r0 += N * RP) {
+              uint4 x[N];
+#pragma unroll
+              for (int i = 0; i < N; ++i) {
+                const int row = r0 + i * RP + lt / C;
+                x[i] = row < w.rows ? *reinterpret_cast<const uint4*>(from(row)) : make_uint4(0, 0, 0, 0);
+              }
+#pragma unroll
+              for (int i = 0; i < N; ++i) {
+                const int row = r0 + i * RP + lt / C;
+                float f[8], big = 0.f;
+                Vec<__nv_bfloat16>::unpack(x[i], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
+#pragma unroll
+                for (int d = C / 2; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+                const int shift =
+                    big > 0.f && big < INFINITY ? min(14 - (int)(((__float_as_uint(big) >> 23) & 255u) - 127), 120) : 0;
+                const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] *= up;
+                if (row < kRows) {
+                  st_shared_v4(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), Vec<__half>::pack(f));
+                  if (c == 0) s_unscale[row] = __uint_as_float((uint32_t)(127 - shift) << 23);
+                }
+              }
+            }
           }
-          cp_async_commit();
-          cp_async_wait<0>();
           fence_proxy_async_smem();
           mbar_arrive(smem_addr(&bars.q_full));
         };
@@ -675,12 +711,86 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         };
         if (box > 0) look_up_groups(0);
         else look_up(0);
+        // Byte offsets of the tile's keys, for the row copies; -1: no such key.  Returns this thread's keys' mask words.
+        auto find_rows = [&](int j, uint32_t(&named)[2]) {
+          long long at_key[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int p = w.k_lo + j * kKeys + lt + e * kLoaders;
+            at_key[e] = id[e] < 0 ? -1ll : ((long long)id[e] * a.block_size + p % a.block_size) * token_bytes;
+            named[e] = __ballot_sync(0xffffffffu, at_key[e] >= 0);
+          }
+          s_off[lt] = at_key[0];
+          if (lt < kKeys - kLoaders) s_off[lt + kLoaders] = at_key[1];
+        };
         bool here = true;                              // this thread's waits
         auto room = [&](uint32_t n) {                  // the ring's place of load n is free
           here = here && wait_or_abort(smem_addr(&bars.kv_empty[n % S::kRing]), ((n / S::kRing) & 1u) ^ 1u, abort_flag,
                                        kWaitBudgetNs);
           return here;
         };
+        if constexpr (F8) {
+          // Loads K0, V0, K1, ...: copied as bytes three loads ahead, then each thread widens the chunks that it copied.
+          constexpr int C = D / 16, RP = kLoaders / C, N = (kKeys + RP - 1) / RP;   // 16-byte chunks of a row, rows of a pass
+          const int c = lt % C, row0 = lt / C, n_loads = 2 * n_tiles;
+          const uint32_t raw0 = ring0 + S::kRing * S::kTileBytes + (uint32_t)row0 * D + c * 16;
+          auto copy_raw = [&](int i) {
+            if (i < n_loads) {
+              const int j = i >> 1;
+              if ((i & 1) == 0) {
+                agreed(true);                          // the last tile's offsets have been read
+                uint32_t named[2];
+                find_rows(j, named);
+                if (lane == 0) s_raw_mask[j % S::kRaw][warp - kLoaderWarp] = named[0];
+                if (lt == 0) s_raw_mask[j % S::kRaw][3] = named[1];
+                look_up(j + 1);
+                barrier_loaders();
+              }
+              const uint8_t* src = kbase + ((i & 1) ? a.v_offset : 0) + c * 16;
+              const uint32_t dst = raw0 + ((n_load + i) % S::kRaw) * S::kRawBytes;
+              long long o[N];
+#pragma unroll
+              for (int k = 0; k < N; ++k) o[k] = row0 + k * RP < kKeys ? s_off[row0 + k * RP] : -1ll;
+#pragma unroll
+              for (int k = 0; k < N; ++k)
+                if (row0 + k * RP < kKeys) cp_async16(dst + k * RP * D, src + (o[k] < 0 ? 0 : o[k]), o[k] >= 0);
+            }
+            cp_async_commit();
+          };
+#pragma unroll
+          for (int i = 0; i < S::kRaw - 1; ++i) copy_raw(i);
+          for (int i = 0; i < n_loads; ++i) {
+            copy_raw(i + S::kRaw - 1);
+            const uint32_t n = n_load + i, slot = (n >> 1) % kMaskRing;
+            here = room(n);
+            cp_async_wait<S::kRaw - 1>();
+            const uint32_t src = raw0 + (n % S::kRaw) * S::kRawBytes, dst = ring0 + (n % S::kRing) * S::kTileBytes;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+              const int row = row0 + k * RP;
+              if (row < kKeys) {
+                const uint4 x = ld_shared_v4(src + k * RP * D);
+                st_shared_v4(dst + at_chunk<D>(row, 2 * c), widen8(x.x, x.y));
+                st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), widen8(x.z, x.w));
+              }
+            }
+            if ((i & 1) == 0 && lt < 4) s_mask[slot][lt] = s_raw_mask[(i >> 1) % S::kRaw][lt];
+            fence_proxy_async_smem();
+            ok = agreed(here);
+            if (!ok) break;
+            if (lt == 0) {
+              if ((i & 1) == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
+              mbar_arrive(smem_addr(&bars.kv_full[n % S::kRing]));
+            }
+            if (i == 0) {
+              load_q();
+              if (!ok) break;
+            }
+          }
+          n_load += n_loads;
+          if (!ok) break;
+          continue;
+        }
         for (int j = 0; j < n_tiles; ++j, n_load += 2) {
           const int key0 = w.k_lo + j * kKeys;
           const uint32_t slot = (n_load >> 1) % kMaskRing;
@@ -718,19 +828,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
             look_up(j);
           }
-          // A tile with missing keys, a block size the copies do not fit, or FP8 rows.
-          long long at_key[2];
-          uint32_t named[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int p = key0 + lt + e * kLoaders;
-            at_key[e] = id[e] < 0 ? -1ll : ((long long)id[e] * a.block_size + p % a.block_size) * token_bytes;
-            named[e] = __ballot_sync(0xffffffffu, at_key[e] >= 0);
-          }
+          // A tile with missing keys, or a block size the bulk copies do not fit.
           ok = agreed(room(n_load));                   // and the last tile's offsets have been read
           if (!ok) break;
-          s_off[lt] = at_key[0];
-          if (lt < kKeys - kLoaders) s_off[lt + kLoaders] = at_key[1];
+          uint32_t named[2];
+          find_rows(j, named);
           if (lane == 0) s_mask[slot][warp - kLoaderWarp] = named[0];
           if (lt == 0) s_mask[slot][3] = named[1];
           if (box == 0) look_up(j + 1);
@@ -744,36 +846,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             const uint32_t place = (n_load + kv) % S::kRing, dst = ring0 + place * S::kTileBytes;
             const uint8_t* src0 = kbase + (kv ? a.v_offset : 0);
             if (lane == (int)place) bulk = 0;
-            if constexpr (!F8) {
-              constexpr int C = D / 8, RP = kLoaders / C;   // chunks of a row; rows of one pass of the loaders
-              const int c = lt % C;
+            constexpr int C = D / 8, RP = kLoaders / C;   // chunks of a row; rows of one pass of the loaders
+            const int c = lt % C;
 #pragma unroll 4
-              for (int row = lt / C; row < kKeys; row += RP) {
-                const long long o = s_off[row];
-                cp_async16(dst + at_chunk<D>(row, c), src0 + (o < 0 ? 0 : o) + c * 16, o >= 0);
-              }
-              cp_async_commit();
-              cp_async_wait<0>();
-            } else {
-              constexpr int C = D / 16, RP = kLoaders / C;  // 16-byte chunks of an FP8 row
-              constexpr int N = (kKeys + RP - 1) / RP;
-              const int c = lt % C;
-              uint4 x[N];
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const int row = i * RP + lt / C;
-                const long long o = row < kKeys ? s_off[row] : -1ll;
-                x[i] = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src0 + o + c * 16);
-              }
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const int row = i * RP + lt / C;
-                if (row < kKeys) {
-                  st_shared_v4(dst + at_chunk<D>(row, 2 * c), kv ? widen8<W>(x[i].x, x[i].y) : widen8<T>(x[i].x, x[i].y));
-                  st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), kv ? widen8<W>(x[i].z, x[i].w) : widen8<T>(x[i].z, x[i].w));
-                }
-              }
+            for (int row = lt / C; row < kKeys; row += RP) {
+              const long long o = s_off[row];
+              cp_async16(dst + at_chunk<D>(row, c), src0 + (o < 0 ? 0 : o) + c * 16, o >= 0);
             }
+            cp_async_commit();
+            cp_async_wait<0>();
             fence_proxy_async_smem();
             barrier_loaders();
             if (lt == 0) mbar_arrive(smem_addr(&bars.kv_full[place]));
@@ -801,15 +882,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       // descriptors that are sums of uniform values the compiler keeps them in
       // uniform registers: an M128 N128 K16 MMA is issued in the 64 clocks it
       // takes, where a branch on the lane number cost 72 to 97.
-      constexpr uint32_t kIdS = idesc_of<T>(128, false), kIdO = idesc_of<W>(D, true);
+      constexpr uint32_t kIdS = idesc_of<W>(128, false), kIdO = idesc_of<W>(D, true);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), q_tile = __shfl_sync(0xffffffffu, tiles0, 0);
       const uint32_t bar0 = __shfl_sync(0xffffffffu, smem_addr(&bars), 0);
       uint32_t leader;
       asm volatile(
           "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
       if (leader) {
-        const uint64_t q_desc = tile_desc<D>(q_tile, 1), k_desc = tile_desc<D>(q_tile + 2 * S::kTileBytes, 1);
-        const uint64_t v_desc = tile_desc<D>(q_tile + 2 * S::kTileBytes, 1024 >> 4);
+        const uint64_t q_desc = tile_desc<D, F8>(q_tile, 1), k_desc = tile_desc<D, F8>(q_tile + 2 * S::kTileBytes, 1);
+        const uint64_t v_desc = tile_desc<D, F8>(q_tile + 2 * S::kTileBytes, 1024 >> 4);
 #define ISK_BAR(member) (bar0 + (uint32_t)offsetof(Bars, member))
         uint32_t n_q = 0, p_turn[2] = {0, 0};
         uint32_t place = 0, turn = 0;                  // of the next load: its place in the ring, and the ring's turn
@@ -907,9 +988,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 // than the split kernel's 16 rows (see launch_attend).
 template <typename T, bool F8, int D>
 static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
-  using S = prompt::Shape<D>;
+  using S = prompt::Shape<D, F8>;
   auto* kern = prompt::attend_prompt_kernel<T, F8, D>;
-  static_assert(S::kSmem + 1024 <= 227 * 1024, "a CTA fits an SM");
+  static_assert(S::kSmem + (F8 ? 2048 : 1024) <= 227 * 1024, "a CTA fits an SM");
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
   constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - partials_offset()) / (2 * sizeof(Partial<prompt::kRows, D>)));
