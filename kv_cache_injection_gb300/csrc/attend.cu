@@ -795,7 +795,7 @@ static cudaError_t launch_mma(const AttendArgs& a, const LaunchCfg& cfg) {
 cudaError_t launch_attend(const AttendArgs& a, const LaunchCfg& cfg) {
   // Many rows: the kernel of attend_prompt.cu.  It takes the maximum of the
   // unscaled logits, so the scale has to be positive.
-  if (a.dtype != IS_F32 && a.D <= 128 && a.G <= 64 && (int64_t)a.max_q * a.G > 32 && a.scale > 0.f)
+  if (a.dtype != IS_F32 && (a.D <= 128 || !a.fp8) && a.G <= 64 && (int64_t)a.max_q * a.G > 32 && a.scale > 0.f)
     return launch_attend_prompt(a, cfg);
   if (a.dtype == IS_BF16)
     return a.fp8 ? launch_mma<__nv_bfloat16, true>(a, cfg) : launch_mma<__nv_bfloat16, false>(a, cfg);

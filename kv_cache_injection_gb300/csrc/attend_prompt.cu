@@ -48,7 +48,6 @@ namespace isk {
 namespace prompt {
 
 constexpr int kThreads = 384;
-constexpr int kRows = 256;               // rows of an item, at most: tiles A and B
 constexpr int kKeys = 128;               // keys of a tile, and of a unit
 constexpr int kLoaderWarp = 8, kLoaders = 96, kMmaWarp = 11;
 // Registers a thread: 168 at launch (65,536 / 384); the softmax warps take what
@@ -60,19 +59,22 @@ constexpr uint32_t kTmemAll = 512;
 
 template <int D, bool F8>
 struct Shape {
+  // Rows of an item, at most: tiles A and B; at head_dim 256 tensor memory has room for O of one.
+  static constexpr int kRows = D == 256 ? 128 : 256;
+  static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kHalves = D / 64;
-  // A tile is 16 groups of 8 rows; a group holds the 64-element halves of its
+  // A tile is 16 groups of 8 rows; a group holds the 64-element parts of its
   // rows one after the other, 1024 bytes each (one swizzle atom).
   static constexpr uint32_t kGroupBytes = kHalves * 1024;
   static constexpr uint32_t kTileBytes = 16 * kGroupBytes;
-  static constexpr int kRing = F8 ? (D == 128 ? 3 : 5) : D == 128 ? 5 : 8;   // K and V tiles in shared memory
+  static constexpr int kRing = D == 256 ? 2 : F8 ? (D == 128 ? 3 : 5) : D == 128 ? 5 : 8;   // K and V tiles in shared memory
   // FP8 rows are copied as they are, kRaw tiles ahead, and widened from there.
   static constexpr int kRaw = D == 128 ? 3 : 4;
   static constexpr uint32_t kRawBytes = F8 ? 128 * D : 0;
   // A tile's mask is written when its K has a place, that is once load 2 t - kRing has been released; the mask it
   // replaces has been read once V of tile t - kMaskRing, load 2 (t - kMaskRing) + 1, has been released.
   static_assert(2 * kMaskRing >= kRing + 1, "a mask is read before its place is used again");
-  static constexpr size_t kSmem = 1024 + (2 + kRing) * (size_t)kTileBytes + kRaw * (size_t)kRawBytes + 128 * 8;
+  static constexpr size_t kSmem = 1024 + kQBytes + kRing * (size_t)kTileBytes + kRaw * (size_t)kRawBytes + 128 * 8;
   static constexpr uint32_t kOCol = 256;                      // first column of O_A; O_B follows D columns on
 };
 
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   __shared__ int s_abort;
   __shared__ __align__(16) uint32_t s_mask[kMaskRing][4];
   __shared__ uint32_t s_raw_mask[S::kRaw][4];
-  __shared__ float s_unscale[kShift ? kRows : 1];
+  __shared__ float s_unscale[kShift ? S::kRows : 1];
   __shared__ int64_t scratch[33];
   __shared__ int64_t s_base;
   __shared__ int32_t s_req;
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &s_abort;
   const uint32_t tiles0 = (smem_addr(smem_raw) + 1023u) & ~1023u;     // Q_A, Q_B, then the ring
-  const uint32_t ring0 = tiles0 + 2 * S::kTileBytes;
+  const uint32_t ring0 = tiles0 + S::kQBytes;
   long long* s_off = reinterpret_cast<long long*>(smem_raw + (ring0 - smem_addr(smem_raw)) + S::kRing * S::kTileBytes + S::kRaw * S::kRawBytes);
 
   if (warp == kMmaWarp) {
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             const int r = row4 + i, t = r / a.G;
             dst[i] = r < g.rows ? reinterpret_cast<T*>(a.out) + ((size_t)(g.row0 + t) * a.Hq + head0 + (r - t * a.G)) * D : nullptr;
           }
-          Partial<kRows, D>* part = partial_of<kRows, D>(a, max(part_slot, 0));
+          Partial<S::kRows, D>* part = partial_of<S::kRows, D>(a, max(part_slot, 0));
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t y[32];
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           };
           if constexpr (!kShift) {
 #pragma unroll 8
-            for (int row = lt / C; row < kRows; row += RP)
+            for (int row = lt / C; row < S::kRows; row += RP)
               cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), from(row), row < w.rows);
             cp_async_commit();
             cp_async_wait<0>();
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             // bf16 to fp16: the C lanes of a row scale it by a power of two that brings its largest element to
             // [2^14, 2^15), and leave the inverse for the softmax.
             constexpr int N = 4;
-            for (int r0 = 0; r0 < kRows; r0 += N * RP) {
+            for (int r0 = 0; r0 < S::kRows; r0 += N * RP) {
               uint4 x[N];
 #pragma unroll
               for (int i = 0; i < N; ++i) {
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] *= up;
-                if (row < kRows) {
+                if (row < S::kRows) {
                   st_shared_v4(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), Vec<__half>::pack(f));
                   if (c == 0) s_unscale[row] = __uint_as_float((uint32_t)(127 - shift) << 23);
                 }
@@ -889,8 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       asm volatile(
           "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
       if (leader) {
-        const uint64_t q_desc = tile_desc<D, F8>(q_tile, 1), k_desc = tile_desc<D, F8>(q_tile + 2 * S::kTileBytes, 1);
-        const uint64_t v_desc = tile_desc<D, F8>(q_tile + 2 * S::kTileBytes, 1024 >> 4);
+        const uint64_t q_desc = tile_desc<D, F8>(q_tile, 1), k_desc = tile_desc<D, F8>(q_tile + S::kQBytes, 1);
+        const uint64_t v_desc = tile_desc<D, F8>(q_tile + S::kQBytes, 1024 >> 4);
 #define ISK_BAR(member) (bar0 + (uint32_t)offsetof(Bars, member))
         uint32_t n_q = 0, p_turn[2] = {0, 0};
         uint32_t place = 0, turn = 0;                  // of the next load: its place in the ring, and the ring's turn
@@ -993,9 +995,9 @@ static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
   static_assert(S::kSmem + (F8 ? 2048 : 1024) <= 227 * 1024, "a CTA fits an SM");
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
-  constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - partials_offset()) / (2 * sizeof(Partial<prompt::kRows, D>)));
+  constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - partials_offset()) / (2 * sizeof(Partial<S::kRows, D>)));
   const int grid = std::max(1, std::min({cfg.num_sms, kFit, kMaxCtas}));
-  const int per = prompt::kRows / a.G;   // tokens of an item
+  const int per = S::kRows / a.G;   // tokens of an item
   // Bulk copies bring `box` rows at once: a block, or 128 rows of a longer one.
   // They need blocks that divide a tile or consist of tiles, 8 rows at least (the
   // swizzle's period), and 16-bit rows; other caches take the row copies.
@@ -1008,11 +1010,12 @@ static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
   }
   e = launch_ex(kern, dim3(grid), dim3(prompt::kThreads), S::kSmem, cfg.stream, cfg.pdl, a, per, box, map);
   if (e != cudaSuccess) return e;
-  return launch_ex(attend_join_rows_kernel<T, prompt::kRows, D>, dim3(grid, 32), dim3(kJoinThreads), 0, cfg.stream,
+  return launch_ex(attend_join_rows_kernel<T, S::kRows, D>, dim3(grid, 32), dim3(kJoinThreads), 0, cfg.stream,
                    cfg.pdl, a);
 }
 
 cudaError_t launch_attend_prompt(const AttendArgs& a, const LaunchCfg& cfg) {
+  if (a.D == 256) return a.dtype == IS_BF16 ? launch_prompt_t<__nv_bfloat16, false, 256>(a, cfg) : launch_prompt_t<__half, false, 256>(a, cfg);
   if (a.dtype == IS_BF16) {
     if (a.D == 64)
       return a.fp8 ? launch_prompt_t<__nv_bfloat16, true, 64>(a, cfg) : launch_prompt_t<__nv_bfloat16, false, 64>(a, cfg);
