@@ -593,9 +593,9 @@ typedef struct {
   const int32_t* seq_len;      /* [R] */
   const int32_t* block_table;  /* [R][max_blocks_per_seq] */
   const void* layer_cache;     /* [2][num_blocks][block_size][num_kv_heads][head_dim] */
-  void* out;                   /* [num_tokens][num_q_heads][head_dim] */
+  void* out;                   /* [num_tokens][num_q_heads][head_dim], 32-byte aligned */
   float* lse_out;              /* [num_tokens][num_q_heads] or NULL */
-  void* workspace;             /* 16-byte aligned */
+  void* workspace;             /* 32-byte aligned */
   int64_t workspace_bytes;     /* >= IS_ATTEND_WORKSPACE_BYTES */
   uint32_t* status_out;
   is_cache_desc_t cache;       /* dtype: the call's, or IS_FP8_E4M3 with a 16-bit one */

@@ -12,11 +12,11 @@
 //   warps 0-3   softmax of tile A: one thread per row, so the row's maximum and
 //               sum need no exchange between threads
 //   warps 4-7   softmax of tile B
-//   warps 8-10  bring Q, K and V tiles into shared memory: whole tiles with
-//               bulk tensor copies, a block of the paged cache at a time; tiles
-//               with missing keys (zero-filled) and block sizes those do not
-//               fit with 16-byte asynchronous copies, row by row; FP8 rows
-//               likewise, as bytes, and widened to fp16 from there (exactly)
+//   warps 8-10  bring Q, K and V tiles into shared memory: with bulk tensor
+//               copies, a block of the paged cache at a time; where those do not
+//               fit the block size with 16-byte asynchronous copies, row by row;
+//               FP8 rows likewise, as bytes, and widened to fp16 from there
+//               (exactly).  Rows of no key are zero
 //   warp 11     one elected thread issues the MMAs
 // Tensor memory (512 columns): S_A, S_B (128 each; P takes the first half of
 // its S as 16-bit pairs), O_A, O_B (D each).  Shared memory: Q (2 x 128 rows),
@@ -54,6 +54,9 @@ constexpr int kLoaderWarp = 8, kLoaders = 96, kMmaWarp = 11;
 // a row of S needs, the other four give it: 2 * 208 + 88 = 3 * 168.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMinRun = 4;               // units of a CTA's run, at least
+// Starting and ending an item costs a CTA about as much as this many units, so
+// an item counts as so many more, before its first.
+constexpr int kItemCost = 6;
 constexpr int kMaskRing = 8;
 constexpr uint32_t kTmemAll = 512;
 
@@ -179,7 +182,7 @@ __device__ __forceinline__ Tile tile_of(const AttendArgs& a, const Req& q, int p
   x.ke = min(q.ke, p0 + x.toks);
   // whole tiles from position 0 on, so that tiles line up with the cache's blocks
   x.kb = a.window > 0 ? (int32_t)max((int64_t)p0 - a.window + 1, (int64_t)0) / kKeys * kKeys : 0;
-  x.units = max(1, (x.ke - x.kb + kKeys - 1) / kKeys);
+  x.units = kItemCost + max(1, (x.ke - x.kb + kKeys - 1) / kKeys);
   return x;
 }
 __device__ __forceinline__ int64_t units_of_request(const AttendArgs& a, const Req& q, int per) {
@@ -188,53 +191,59 @@ __device__ __forceinline__ int64_t units_of_request(const AttendArgs& a, const R
   return sum * a.H;
 }
 
-// The segments of a CTA's run, walked the same way by every thread.
+// The segments of a CTA's run, walked by one thread.
 struct Walk {
   int64_t u, u_end, u_first, run, base;  // base: first unit of tile (r, t)
   int r, t;
   Req q;
   Tile x;
   // of the current segment
-  int head, k_lo, k_hi, rows;
-  int64_t item0;
+  int head, k_lo, k_hi, rows, parts;
   bool whole, begins, at_start;
 
   __device__ __forceinline__ bool next(const AttendArgs& a, int per) {
-    if (u >= u_end) return false;
-    while (true) {
-      if (t * per < q.n) {
-        const int64_t n = (int64_t)a.H * x.units;
-        if (u < base + n) break;
-        base += n;
-        ++t;
-      } else {
-        ++r;
-        t = 0;
-        q = read_request(a, r, false);
+    while (u < u_end) {
+      // the tile that unit u lies in
+      while (true) {
+        if (t * per < q.n) {
+          const int64_t n = (int64_t)a.H * x.units;
+          if (u < base + n) break;
+          base += n;
+          ++t;
+        } else {
+          if (++r >= a.R) return false;  // the lengths have changed under the call
+          t = 0;
+          q = read_request(a, r, false);
+        }
+        if (t * per < q.n) x = tile_of(a, q, per, t);
       }
-      if (t * per < q.n) x = tile_of(a, q, per, t);
+      head = (int)((u - base) / x.units);
+      const int64_t item0 = base + (int64_t)head * x.units;
+      const int ua = max((int)(u - item0) - kItemCost, 0), ub = (int)min((int64_t)x.units, u_end - item0) - kItemCost;
+      at_start = u == u_first;
+      u = item0 + ub + kItemCost;
+      if (ub <= 0) continue;             // none of its keys yet: the item begins in the next CTA
+      begins = ua == 0;
+      whole = begins && ub == x.units - kItemCost;
+      parts = (int)((item0 + x.units - 1) / run) - (int)blockIdx.x + 1;
+      k_lo = x.kb + ua * kKeys;
+      k_hi = min(x.ke, x.kb + ub * kKeys);
+      rows = x.toks * a.G;
+      return true;
     }
-    head = (int)((u - base) / x.units);
-    item0 = base + (int64_t)head * x.units;
-    const int ua = (int)(u - item0), ub = (int)min((int64_t)x.units, u_end - item0);
-    begins = ua == 0;
-    whole = begins && ub == x.units;
-    at_start = u == u_first;
-    k_lo = x.kb + ua * kKeys;
-    k_hi = min(x.ke, x.kb + ub * kKeys);
-    rows = x.toks * a.G;
-    u = item0 + ub;
-    return true;
+    return false;
   }
   __device__ __forceinline__ int tiles() const { return k_hi > k_lo ? (k_hi - k_lo + kKeys - 1) / kKeys : 0; }
 };
 
 // One segment (a run's share of one item) as its workers need it, handed from
-// the loaders to the softmax and MMA warps through a ring in shared memory, so
-// that the walk costs those no registers.
+// one loader thread to all warps through a ring in shared memory: the walk costs
+// the others no registers, and the CTA agrees on its segments whatever happens
+// to the caller's arrays meanwhile.
 struct Segment {
   int32_t tiles;         // -1: the run has ended
-  int32_t k_lo, rows;
+  int32_t k_lo, k_hi, rows;
+  int32_t r;
   int32_t lim0;          // position of the item's first token
   int32_t head;
   int32_t row0;          // first query row
@@ -243,7 +252,7 @@ struct Segment {
 constexpr int kSegments = 4;
 
 struct Bars {
-  uint64_t q_full, q_empty, done;
+  uint64_t q_full, q_empty, done, v_tail;
   uint64_t seg_full[kSegments], seg_empty[kSegments];
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_full[2][2], o_full[2];   // P in two halves of 64 keys
@@ -265,19 +274,11 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Four lanes hold four vectors each; lane q ends with vector q of each of the four.
-__device__ __forceinline__ void quad_transpose(uint4 (&v)[4], int lane) {
-  const bool odd = lane & 1, high = lane & 2;
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {       // swap v[i + 1] of even lanes with v[i] of odd ones
-    const uint4 got = shfl_xor4(odd ? v[i] : v[i + 1], 1);
-    if (odd) v[i] = got; else v[i + 1] = got;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {          // and v[i + 2] of the lower pair with v[i] of the upper
-    const uint4 got = shfl_xor4(high ? v[i] : v[i + 2], 2);
-    if (high) v[i] = got; else v[i + 2] = got;
-  }
+// 32 bytes to a 32-byte-aligned address.
+__device__ __forceinline__ void st_sector(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // Where 16-byte chunk c (8 elements) of row `row` lies in a tile.
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     mbar_init(smem_addr(&bars.q_full), kLoaders);
     mbar_init(smem_addr(&bars.q_empty), 1);
     mbar_init(smem_addr(&bars.done), 1);
+    mbar_init(smem_addr(&bars.v_tail), 1);
     for (int i = 0; i < S::kRing; ++i) {
       mbar_init(smem_addr(&bars.kv_full[i]), 1);
       mbar_init(smem_addr(&bars.kv_empty[i]), 1);
@@ -348,15 +350,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   for (int r = r0; r < r1; ++r) mine += units_of_request(a, read_request(a, r, blockIdx.x == 0), per);
   int64_t total;
   int64_t at = block_exclusive_scan(mine, scratch, &total);
-  Walk w;
-  w.run = max((int64_t)kMinRun, (total + gridDim.x - 1) / gridDim.x);
-  w.u = w.u_first = (int64_t)blockIdx.x * w.run;
-  w.u_end = min(total, w.u + w.run);
-  const bool idle = w.u >= w.u_end;
-  if (!idle && at <= w.u && w.u < at + mine) {
+  const int64_t run = max((int64_t)kMinRun, (total + gridDim.x - 1) / gridDim.x);
+  const int64_t u0 = (int64_t)blockIdx.x * run, u1 = min(total, u0 + run);
+  const bool idle = u0 >= u1;
+  if (!idle && at <= u0 && u0 < at + mine) {
     for (int r = r0; r < r1; ++r) {
       const int64_t n = units_of_request(a, read_request(a, r, false), per);
-      if (w.u < at + n) {
+      if (u0 < at + n || r == r1 - 1) {
         s_req = r;
         s_base = at;
         break;
@@ -503,15 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         if (has) {
           const int part_slot = g.slot;
           const float inv = l == 0.f ? 0.f : a.v_scale / l;
-          // A thread holds a row; four lanes exchange 64-byte pieces so that each store of the warp writes eight
-          // rows' 64 consecutive bytes, not 32 rows' 16.
-          const int row4 = row & ~3, head0 = g.head * a.G;
-          T* dst[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = row4 + i, t = r / a.G;
-            dst[i] = r < g.rows ? reinterpret_cast<T*>(a.out) + ((size_t)(g.row0 + t) * a.Hq + head0 + (r - t * a.G)) * D : nullptr;
-          }
+          // A thread holds a row and writes it in whole 32-byte sectors.  (Exchanging pieces between four lanes so that a
+          // store covers 64 bytes of eight rows took four times as long: the shuffles cost more than the sectors.)
+          T* dst = reinterpret_cast<T*>(a.out) +
+                   ((size_t)(g.row0 + (live ? tok : 0)) * a.Hq + (size_t)g.head * a.G + (live ? row - tok * a.G : 0)) * D;
           Partial<S::kRows, D>* part = partial_of<S::kRows, D>(a, max(part_slot, 0));
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -523,32 +518,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 #pragma unroll
               for (int i = 0; i < 32; ++i) y[i] = 0u;
             }
-            if (part_slot < 0) {
-              uint4 v[4];
+            if (live && part_slot < 0) {
+              uint32_t z[16];
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                float z[8];
+              for (int i = 0; i < 16; ++i)
+                z[i] = l == 0.f ? 0u : Vec<T>::pack2(__uint_as_float(y[2 * i]) * inv, __uint_as_float(y[2 * i + 1]) * inv);
+              st_sector(dst + 32 * c, z);
+              st_sector(dst + 32 * c + 16, z + 8);
+            } else if (live) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] = l == 0.f ? 0.f : __uint_as_float(y[8 * u + i]) * inv;
-                v[u] = Vec<T>::pack(z);
-              }
-              quad_transpose(v, lane);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (dst[i]) st_v4(dst[i] + 32 * c + 8 * (lane & 3), v[i]);
-            } else {
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                uint4 v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  v[i] = make_uint4(y[16 * u + 4 * i], y[16 * u + 4 * i + 1], y[16 * u + 4 * i + 2], y[16 * u + 4 * i + 3]);
-                quad_transpose(v, lane);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (dst[i]) st_v4(&part->o[row4 + i][32 * c + 16 * u + 4 * (lane & 3)], v[i]);
-              }
+              for (int v = 0; v < 4; ++v) st_sector(&part->o[row][32 * c + 8 * v], y + 8 * v);
             }
+            __syncwarp();
           }
           if (live && part_slot < 0) {
             if (a.lse)
@@ -570,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       const int lt = tid - kLoaderWarp * 32;           // 0 .. kLoaders - 1
       constexpr int EB = F8 ? 1 : 2;
       const int64_t token_bytes = (int64_t)a.H * D * EB;
-      uint32_t n_load = 0, n_q = 0;                    // K and V tiles, query tiles
+      uint32_t n_load = 0, n_q = 0, n_tail = 0;        // K and V tiles, query tiles, cleared V tiles
       uint32_t bulk = 0;                               // lane i: 1 + this warp's last load into place i if that was a bulk copy
       uint32_t leader;
       asm volatile(
@@ -586,46 +567,57 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             : "memory");
         return r != 0;
       };
-      w.r = s_req;
-      w.base = s_base;
-      w.t = 0;
-      w.q = read_request(a, w.r, false);
-      w.x = tile_of(a, w.q, per, 0);
-      uint32_t n_seg = 0;
-      // Hands the current segment on (tiles -1: the end).
-      auto publish = [&](int tiles) {
-        const bool go = agreed(wait_or_abort(smem_addr(&bars.seg_empty[n_seg % kSegments]), ((n_seg / kSegments) & 1u) ^ 1u,
-                                             abort_flag, kWaitBudgetNs));
-        if (go && lt == 0) {
-          Segment& g = s_seg[n_seg % kSegments];
-          g.tiles = tiles;
-          g.k_lo = w.k_lo;
-          g.rows = w.rows;
-          g.lim0 = w.q.seq - w.q.n + w.x.tok0;
-          g.head = w.head;
-          g.row0 = w.q.row0 + w.x.tok0;
-          g.slot = w.whole ? -1 : 2 * blockIdx.x + (w.at_start ? 0 : 1);
-          mbar_arrive(smem_addr(&bars.seg_full[n_seg % kSegments]));
-        }
-        ++n_seg;
-        return go;
-      };
       auto barrier_loaders = [] { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kLoaders) : "memory"); };
+      Walk w;                                          // the first thread's
       bool crosses = false;                            // the run's last item began here and goes on in the next CTA
-      while (ok && w.next(a, per)) {
-        const int n_tiles = w.tiles();
-        ok = publish(n_tiles);
-        crosses = w.begins && !w.whole;
-        if (crosses && lt == 0) {
-          JoinRecord* rec = record_of(a, blockIdx.x);
-          rec->parts = (int32_t)((w.item0 + w.x.units - 1) / w.run - blockIdx.x) + 1;
-          rec->slot0 = 2 * blockIdx.x + (w.at_start ? 0 : 1);
-          rec->row0 = w.q.row0;
-          rec->head = w.head;
-          rec->rho0 = w.x.tok0 * a.G;
-          rec->rows = w.rows;
+      if (lt == 0) {
+        w.run = run;
+        w.u = w.u_first = u0;
+        w.u_end = u1;
+        w.r = s_req;
+        w.base = s_base;
+        w.t = 0;
+        w.q = read_request(a, w.r, false);
+        w.x = tile_of(a, w.q, per, 0);
+      }
+      for (uint32_t n_seg = 0;; ++n_seg) {
+        const uint32_t seg = n_seg % kSegments;
+        ok = agreed(wait_or_abort(smem_addr(&bars.seg_empty[seg]), ((n_seg / kSegments) & 1u) ^ 1u, abort_flag, kWaitBudgetNs));
+        if (!ok) break;
+        Segment& g = s_seg[seg];
+        if (lt == 0) {
+          if (w.next(a, per)) {
+            g.tiles = w.tiles();
+            g.k_lo = w.k_lo;
+            g.k_hi = w.k_hi;
+            g.rows = w.rows;
+            g.r = w.r;
+            g.lim0 = w.q.seq - w.q.n + w.x.tok0;
+            g.head = w.head;
+            g.row0 = w.q.row0 + w.x.tok0;
+            g.slot = w.whole ? -1 : 2 * blockIdx.x + (w.at_start ? 0 : 1);
+            crosses = w.begins && !w.whole;
+            if (crosses) {
+              JoinRecord* rec = record_of(a, blockIdx.x);
+              rec->parts = w.parts;
+              rec->slot0 = g.slot;
+              rec->row0 = w.q.row0;
+              rec->head = w.head;
+              rec->rho0 = w.x.tok0 * a.G;
+              rec->rows = w.rows;
+            }
+          } else {
+            g.tiles = -1;
+            if (!crosses) record_of(a, blockIdx.x)->parts = 0;
+          }
         }
-        if (!ok || n_tiles == 0) continue;
+        barrier_loaders();
+        const int n_tiles = g.tiles, k_lo = g.k_lo, k_hi = g.k_hi, rows = g.rows, head = g.head, row_at = g.row0;
+        const int32_t* table = a.block_table + (size_t)g.r * a.max_blocks;
+        const uint8_t* kbase = a.k_cache + (size_t)head * D * EB;
+        if (lt == 0) mbar_arrive(smem_addr(&bars.seg_full[seg]));
+        if (n_tiles < 0) break;
+        if (n_tiles == 0) continue;
         // Q once the last segment's logits are done; called after the first tile's loads are on their way.
         auto load_q = [&] {
           ok = agreed(wait_or_abort(smem_addr(&bars.q_empty), (n_q & 1u) ^ 1u, abort_flag, kWaitBudgetNs));
@@ -634,15 +626,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           constexpr int C = D / 8, RP = kLoaders / C;  // chunks of a row; rows of one pass
           const uint32_t g_inv = (65536u + a.G - 1) / a.G;   // row / G = row * g_inv >> 16 for row < 256, G <= 64
           const int c = lt % C;
-          const uint8_t* src = a.q + (int64_t)(w.q.row0 + w.x.tok0) * a.q_stride + (size_t)w.head * a.G * D * 2 + c * 16;
+          const uint8_t* src = a.q + (int64_t)row_at * a.q_stride + (size_t)head * a.G * D * 2 + c * 16;
           auto from = [&](int row) {
             const int tok = (int)((uint32_t)row * g_inv >> 16);
-            return row < w.rows ? src + tok * a.q_stride + (row - tok * a.G) * (D * 2) : src;
+            return row < rows ? src + tok * a.q_stride + (row - tok * a.G) * (D * 2) : src;
           };
           if constexpr (!kShift) {
 #pragma unroll 8
             for (int row = lt / C; row < S::kRows; row += RP)
-              cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), from(row), row < w.rows);
+              cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), from(row), row < rows);
             cp_async_commit();
             cp_async_wait<0>();
           } else {
@@ -654,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 #pragma unroll
               for (int i = 0; i < N; ++i) {
                 const int row = r0 + i * RP + lt / C;
-                x[i] = row < w.rows ? *reinterpret_cast<const uint4*>(from(row)) : make_uint4(0, 0, 0, 0);
+                x[i] = row < rows ? *reinterpret_cast<const uint4*>(from(row)) : make_uint4(0, 0, 0, 0);
               }
 #pragma unroll
               for (int i = 0; i < N; ++i) {
@@ -680,19 +672,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           fence_proxy_async_smem();
           mbar_arrive(smem_addr(&bars.q_full));
         };
-        const int32_t* table = a.block_table + (size_t)w.r * a.max_blocks;
-        const uint8_t* kbase = a.k_cache + (size_t)w.head * D * EB;
-        // Bulk copies: lane g of each warp finds the token of row group g (`box` rows) of a tile, one tile ahead;
-        // -1 if the tile is not whole.
+        // Bulk copies: lane g of each warp finds the token of row group g (`box` rows) of a tile, one tile ahead; -1 if
+        // it has no key or the table does not name it (the copy then starts behind the cache and reads zeros).
         const int groups = box > 0 ? kKeys / box : 0;
         int64_t token = -1;
         auto look_up_groups = [&](int j) {
-          const int key0 = w.k_lo + j * kKeys, p = key0 + lane * box;
+          const int key0 = k_lo + j * kKeys, p = key0 + lane * box;
           token = -1;
-          if (lane < groups && j < n_tiles && key0 + kKeys <= w.k_hi) {
+          if (lane < groups && j < n_tiles && p < k_hi) {
             const int b = p / a.block_size;
             const int32_t id = table[b];
             if (id >= 0 && id < a.num_blocks) token = (int64_t)id * a.block_size + (p - b * a.block_size);
+            else latch(a.status, IS_ST_BLOCK_ID);
           }
         };
         // Row copies: block ids of this thread's keys of a tile: lt, and lt + 96 for the first warp.
@@ -700,9 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         auto look_up = [&](int j) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int p = w.k_lo + j * kKeys + lt + e * kLoaders;
+            const int p = k_lo + j * kKeys + lt + e * kLoaders;
             id[e] = -1;
-            if (j < n_tiles && p < w.k_hi && lt + e * kLoaders < kKeys) {
+            if (j < n_tiles && p < k_hi && lt + e * kLoaders < kKeys) {
               id[e] = table[p / a.block_size];
               if (id[e] < 0 || id[e] >= a.num_blocks) {
                 latch(a.status, IS_ST_BLOCK_ID);
@@ -718,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           long long at_key[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int p = w.k_lo + j * kKeys + lt + e * kLoaders;
+            const int p = k_lo + j * kKeys + lt + e * kLoaders;
             at_key[e] = id[e] < 0 ? -1ll : ((long long)id[e] * a.block_size + p % a.block_size) * token_bytes;
             named[e] = __ballot_sync(0xffffffffu, at_key[e] >= 0);
           }
@@ -794,50 +785,64 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           continue;
         }
         for (int j = 0; j < n_tiles; ++j, n_load += 2) {
-          const int key0 = w.k_lo + j * kKeys;
+          const int key0 = k_lo + j * kKeys;
           const uint32_t slot = (n_load >> 1) % kMaskRing;
           if (box > 0) {
             const int64_t from = token;
-            const bool whole_tile = agreed(lane >= groups || from >= 0);
             look_up_groups(j + 1);
-            if (whole_tile) {
-              // The first loader warp brings K, the second V; one elected lane issues.
-              const int kv = warp - kLoaderWarp;
-              if (kv < 2 && __all_sync(0xffffffffu, room(n_load + kv))) {
-                const uint32_t place = (n_load + kv) % S::kRing, bar = smem_addr(&bars.kv_full[place]);
-                const int t8 = (int)((from + (kv ? (int64_t)a.num_blocks * a.block_size : 0)) >> 3);
-                if (leader) {
-                  if (kv == 0) {
-                    *reinterpret_cast<uint4*>(s_mask[slot]) = make_uint4(~0u, ~0u, ~0u, ~0u);
-                    mbar_arrive(smem_addr(&bars.mask_full[slot]));
-                  }
-                  mbar_expect_tx(bar, S::kTileBytes);
+            // The first loader warp brings K, the second V; one elected lane issues.
+            const int kv = warp - kLoaderWarp;
+            if (kv < 2 && __all_sync(0xffffffffu, room(n_load + kv))) {
+              const uint32_t place = (n_load + kv) % S::kRing, full = smem_addr(&bars.kv_full[place]);
+              // Behind the last key V has to be zero, whatever its block holds there (0 * NaN): those rows are cleared
+              // before the tile is handed on.
+              const int keys = min(kKeys, k_hi - key0);
+              const bool clear = kv == 1 && keys % box != 0;
+              const uint32_t bar = clear ? smem_addr(&bars.v_tail) : full;
+              const int64_t rows_of_k = (int64_t)a.num_blocks * a.block_size;
+              const int t8 = (int)((from < 0 ? 2 * rows_of_k : from + (kv ? rows_of_k : 0)) >> 3);
+              if (kv == 0) {
+                const uint32_t named = __ballot_sync(0xffffffffu, lane < groups && from >= 0);
+                for (int word = 0; word < 4; ++word) {
+                  const int key = 32 * word + lane;
+                  const uint32_t bits = __ballot_sync(0xffffffffu, key < keys && ((named >> (key / box)) & 1u));
+                  if (lane == 0) s_mask[slot][word] = bits;
                 }
+                if (lane == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
+              }
+              if (leader) mbar_expect_tx(bar, S::kTileBytes);
+              __syncwarp();
+              const uint32_t step = (uint32_t)(box >> 3) * S::kGroupBytes, dst = ring0 + place * S::kTileBytes;
+              for (int g = 0; g < groups; ++g) {
+                const int at8 = __shfl_sync(0xffffffffu, t8, g);
+                if (leader) tma_load_rows(dst + g * step, &rows_map, head, at8, bar);
+              }
+              if (lane == (int)place) bulk = n_load + kv + 1;
+              if (clear) {
+                here = here && __all_sync(0xffffffffu, mbar_wait_bounded(bar, n_tail & 1u, kWaitBudgetNs));
+                ++n_tail;
+                const int end = (keys + box - 1) / box * box;
+                for (int x = lane; x < (end - keys) * (D / 8); x += 32)
+                  st_shared_v4(dst + at_chunk<D>(keys + x / (D / 8), x % (D / 8)), make_uint4(0, 0, 0, 0));
+                fence_proxy_async_smem();
                 __syncwarp();
-                const uint32_t step = (uint32_t)(box >> 3) * S::kGroupBytes;
-                uint32_t dst = ring0 + place * S::kTileBytes;
-                for (int g = 0; g < groups; ++g, dst += step) {
-                  const int at8 = __shfl_sync(0xffffffffu, t8, g);
-                  if (leader) tma_load_rows(dst, &rows_map, w.head, at8, bar);
-                }
-                if (lane == (int)place) bulk = n_load + kv + 1;
+                if (lane == 0) mbar_arrive(full);
               }
-              if (j == 0) {
-                load_q();
-                if (!ok) break;
-              }
-              continue;
             }
-            look_up(j);
+            if (j == 0) {
+              load_q();
+              if (!ok) break;
+            }
+            continue;
           }
-          // A tile with missing keys, or a block size the bulk copies do not fit.
+          // A block size that the bulk copies do not fit.
           ok = agreed(room(n_load));                   // and the last tile's offsets have been read
           if (!ok) break;
           uint32_t named[2];
           find_rows(j, named);
           if (lane == 0) s_mask[slot][warp - kLoaderWarp] = named[0];
           if (lt == 0) s_mask[slot][3] = named[1];
-          if (box == 0) look_up(j + 1);
+          look_up(j + 1);
           barrier_loaders();
           if (lt == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
           for (int kv = 0; kv < 2; ++kv) {
@@ -868,9 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           if (!ok) break;
         }
         ok = ok && agreed(here);
+        if (!ok) break;
       }
-      if (lt == 0 && !crosses) record_of(a, blockIdx.x)->parts = 0;
-      if (ok) ok = publish(-1);
       // After a time-out bulk copies may be in flight that no MMA waited for:
       // they land before shared memory is let go.
       if (!ok && bulk > 0)

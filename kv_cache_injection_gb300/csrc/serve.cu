@@ -284,8 +284,10 @@ extern "C" is_status_t is_attend(const is_attend_args_t* a, cudaStream_t stream)
   const int64_t qrow = (int64_t)Hq * D, row = (int64_t)H * D;
   if (T > 1 && a->q_stride < qrow) return refuse(IS_ERR_INVALID_ARG, "q_stride is smaller than a row");
   const int64_t qs = a->q_stride * e;
-  if ((T > 1 && (qs & 15)) || !aligned16(a->q) || !aligned16(a->out) || !aligned16(a->workspace))
-    return refuse(IS_ERR_INVALID_ARG, "rows of q, out and workspace must be 16-byte aligned");
+  if ((T > 1 && (qs & 15)) || !aligned16(a->q))
+    return refuse(IS_ERR_INVALID_ARG, "rows of q must be 16-byte aligned");
+  if (((uintptr_t)a->out | (uintptr_t)a->workspace) & 31)
+    return refuse(IS_ERR_INVALID_ARG, "out and workspace must be 32-byte aligned");
   const int c = a->cache.dtype == IS_FP8_E4M3 ? 1 : e;
   const int64_t slots = (int64_t)a->cache.num_blocks * a->cache.block_size;
   const Span ins[] = {{"q", a->q, (T - 1) * qs + qrow * e}, {"q_start", a->q_start, 4LL * (R + 1)},

@@ -118,6 +118,7 @@ def test_attend_needs_its_pointers(lib, field):
     (dict(window=-1), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(head_dim=32), UNSUPPORTED), (dict(head_dim=512), UNSUPPORTED), (dict(q_stride=508), INVALID),
     (dict(q=addr(0) + 8), INVALID), (dict(out=addr(5) + 4), INVALID), (dict(workspace=addr(7) + 8), INVALID),
+    (dict(out=addr(5) + 16), INVALID), (dict(workspace=addr(7) + 16), INVALID),
     (dict(workspace_bytes=_lib.IS_ATTEND_WORKSPACE_BYTES - 1), INVALID), (dict(out=addr(0)), INVALID),
     (dict(lse_out=addr(5)), INVALID), (dict(workspace=addr(4)), INVALID), (dict(reserved=2), INVALID),
     (dict(q_start=None, num_requests=4), INVALID), (dict(cache=api.make_cache_desc(16, 8, "f32")), INVALID),
