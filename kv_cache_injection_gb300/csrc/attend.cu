@@ -773,10 +773,10 @@ static cudaError_t launch_split(const AttendArgs& a, const LaunchCfg& cfg) {
   const int grid = (int)std::min<int64_t>(std::min<int64_t>(runs, (int64_t)S::kPerSm * cfg.num_sms), kMaxCtas);
   e = launch_ex(kern, dim3(grid), dim3(kAttendThreads), S::kSmem, cfg.stream, cfg.pdl, a);
   if (e != cudaSuccess) return e;
-  // Few parts an item: a CTA joins all rows of a record; else a CTA per row splits the parts.
-  if (items * 2 >= grid)
+  // Few parts an item: a CTA joins all rows of a record; else four CTAs, each splitting the parts of a row at a time.
+  if (items * 4 >= grid)
     return launch_ex(attend_join_rows_kernel<T, E::kRows, E::D>, dim3(grid, 1), dim3(kJoinThreads), 0, cfg.stream, cfg.pdl, a);
-  return launch_ex(attend_join_kernel<T, E::kRows, E::D>, dim3(grid, E::kRows), dim3(kJoinThreads), 0, cfg.stream,
+  return launch_ex(attend_join_kernel<T, E::kRows, E::D>, dim3(grid, 4), dim3(kJoinThreads), 0, cfg.stream,
                    cfg.pdl, a);
 }
 

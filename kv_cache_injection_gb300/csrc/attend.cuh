@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_rows_kernel(const At
   for (int row = blockIdx.y * AT_ONCE + threadIdx.x / LANES; row < rec.rows; row += gridDim.y * AT_ONCE) {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 8
     for (int i = 0; i < rec.parts; ++i) {
       const Partial<ROWS, D>* p = partial_of<ROWS, D>(a, i == 0 ? rec.slot0 : 2 * (cta + i));
       const float pm = p->m[row], pl = p->l[row];

@@ -35,6 +35,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cstddef>
 #include <cstring>
 #include <type_traits>
@@ -381,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       const int side = warp >> 2;                      // 0: tile A, 1: tile B
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
       const uint32_t s_col = tmem + lanes + 128u * side, o_col = tmem + lanes + S::kOCol + (uint32_t)(D * side);
+      // Never 0: a hidden logit is -inf times it.  (Below the smallest normal number every weight is 1 in any case.)
       const float sc0 = a.scale * kLog2e;
       const int row = side * 128 + (warp & 3) * 32 + lane, tok = row / a.G;
       uint32_t n_s = 0, n_o = 0, n_mask = 0, n_q = 0;  // phases consumed
@@ -402,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         const int lim_hi = __reduce_max_sync(0xffffffffu, lim);
         const int low = a.window > 0 ? (int)max((int64_t)lim - a.window + 1, (int64_t)0) : 0;
         const int low_hi = a.window > 0 ? (int)max((int64_t)lim_hi - a.window + 1, (int64_t)0) : 0;
-        float m = -INFINITY, l = 0.f, sc = sc0;
+        float m = -INFINITY, l = 0.f, sc = fmaxf(sc0, FLT_MIN);
         if (kShift && n_tiles > 0) {
           if (!wait(&bars.q_full, n_q & 1u)) break;
           ++n_q;
-          sc = sc0 * s_unscale[row];
+          sc = fmaxf(sc0 * s_unscale[row], FLT_MIN);
         }
         if (!has) n_mask += n_tiles;
         for (int j = 0, key0 = g.k_lo; has && j < n_tiles; ++j, ++n_mask, key0 += kKeys) {

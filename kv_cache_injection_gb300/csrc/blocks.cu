@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
   const int pitch = at(R) + 1;
   int32_t* s_start = sm;                 // [R + 1] first packed token, INT32_MAX at most
   int32_t* s_seq = sm + pitch;           // [R] seq_len, or -1 if the request is refused
-  int32_t* s_take = s_seq + pitch;       // [R] free-list index of the request's table entry 0
+  int32_t* s_taken = s_seq + pitch;      // [R] blocks taken before the request (what matters of it is at most num_free)
   pdl_wait();
   pdl_trigger();
   int32_t head = a.free_head ? a.free_head[0] : 0;
@@ -122,8 +122,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
       }
     }
     s_seq[at(r)] = len[i];
-    // entry j >= the blocks held of the row is free_blocks[s_take + j]
-    s_take[at(r)] = len[i] < 0 ? 0 : head + (int32_t)taken - blocks_of(len[i], bs, div);
+    s_taken[at(r)] = (int32_t)min(taken, (int64_t)INT32_MAX);
     first += add[i];
     taken += miss;
   }
@@ -153,8 +152,9 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
     if (n < 0) continue;
     pos[i] = n + (int32_t)(t - s_start[at(lo)]);
     const int32_t j = div_bs(pos[i], div);
-    const int32_t* src = j >= blocks_of(n, bs, div) ? a.free_blocks + (s_take[at(lo)] + j)
-                                               : a.block_table + ((size_t)lo * a.max_blocks_per_seq + j);
+    const int32_t have = blocks_of(n, bs, div);
+    const int32_t* src = j >= have ? a.free_blocks + (head + s_taken[at(lo)] + (j - have))
+                                   : a.block_table + ((size_t)lo * a.max_blocks_per_seq + j);
     id[i] = *src;
   }
 #pragma unroll
@@ -172,21 +172,24 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
     if (t < end && a.positions_out) a.positions_out[t] = pos[i];
   }
 
-  // Table entries and per-request outputs: one warp per request.
-  const int lane = tid & 31, nwarps = kExtendThreads / 32;
-  for (int r = blockIdx.x * nwarps + (tid >> 5); r < R; r += gridDim.x * nwarps) {
-    const int32_t n = s_seq[at(r)], m = a.new_len[r];
-    if (n >= 0) {
-      const int32_t need = blocks_of(n + m, bs, div);
-      int32_t* row = a.block_table + (size_t)r * a.max_blocks_per_seq;
-      for (int j = blocks_of(n, bs, div) + lane; j < need; j += 32) row[j] = a.free_blocks[s_take[at(r)] + j];
+  // Table entries: the blocks taken are the free list's next s_used, one thread each.
+  const int32_t all_used = s_used;
+  for (int32_t i = blockIdx.x * kExtendThreads + tid; i < all_used; i += gridDim.x * kExtendThreads) {
+    int lo = 0, hi = R;                  // last request with at most i blocks taken before it: the one that takes block i
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_taken[at(mid)] <= i) lo = mid; else hi = mid;
     }
-    if (lane == 0) {
-      if (a.seq_len_out) a.seq_len_out[r] = n >= 0 ? n + m : a.seq_len[r];
-      if (a.token_start_out) {
-        a.token_start_out[r] = s_start[at(r)];
-        if (r == R - 1) a.token_start_out[R] = end;
-      }
+    a.block_table[(size_t)lo * a.max_blocks_per_seq + blocks_of(s_seq[at(lo)], bs, div) + (i - s_taken[at(lo)])] =
+        a.free_blocks[head + i];
+  }
+  // Per-request outputs.
+  for (int r = blockIdx.x * kExtendThreads + tid; r < R; r += gridDim.x * kExtendThreads) {
+    const int32_t n = s_seq[at(r)];
+    if (a.seq_len_out) a.seq_len_out[r] = n >= 0 ? n + a.new_len[r] : a.seq_len[r];
+    if (a.token_start_out) {
+      a.token_start_out[r] = s_start[at(r)];
+      if (r == R - 1) a.token_start_out[R] = end;
     }
   }
   if (blockIdx.x == 0 && tid == 0 && a.free_head_out) a.free_head_out[0] = head + s_used;
