@@ -49,7 +49,7 @@ __host__ __device__ constexpr int at(int r) { return r + (r >> 5); }
 template <int kExtendThreads, int kPer>
 __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_args_t a, const BlockDiv div) {
   extern __shared__ int32_t sm[];
-  __shared__ int64_t scratch[2][kExtendThreads / 32];
+  __shared__ int64_t scratch[33];
   __shared__ int32_t s_used;
   const int R = a.num_requests, bs = a.block_size, tid = threadIdx.x;
   const int pitch = at(R) + 1;
@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
     missing += miss;
   }
   int64_t total, all_missing;
-  int64_t first = block_exclusive_scan_1bar<kExtendThreads / 32>(tokens, scratch[0], &total);
-  int64_t taken = block_exclusive_scan_1bar<kExtendThreads / 32>(missing, scratch[1], &all_missing);
+  int64_t first = block_exclusive_scan(tokens, scratch, &total);
+  int64_t taken = block_exclusive_scan(missing, scratch, &all_missing);
   int32_t used = 0;                      // blocks taken up to this thread's last request
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -132,25 +132,40 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
   if (total > a.max_tokens) bits |= IS_ST_COUNT;
   __syncthreads();
 
-  // Slots and positions of this CTA's packed tokens, a warp's 32 consecutive ones at a time: all searches, then all
-  // block ids, then all stores, so that their latencies overlap.
-  const int64_t t0 = (int64_t)blockIdx.x * kTokensPerCta + tid;
+  // Slots and positions of this CTA's packed tokens.  A warp has consecutive ones and finds the requests of its first
+  // and last together, 32 probes at a time; each lane's request lies between the two.  All block ids are loaded before
+  // any is used.
+  const int lane = tid & 31;
   const int32_t end = s_start[at(R)];
+  const int64_t tw = (int64_t)blockIdx.x * kTokensPerCta + (int64_t)(tid >> 5) * 32 * kTokensPerThread;   // the warp's first
+  auto find_warp = [&](int32_t t) {      // last request that starts at or before t
+    int lo = 0, hi = R;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) >> 5, idx = lo + lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, idx < hi && s_start[at(idx)] <= t);   // lane 0 probes lo, which qualifies
+      lo += (31 - __clz(m)) * step;
+      hi = min(hi, lo + step);
+    }
+    return lo;
+  };
   int32_t pos[kTokensPerThread], id[kTokensPerThread];
+  const int32_t t_last = (int32_t)min(min((int64_t)end, (int64_t)a.max_tokens) - 1, tw + 32 * kTokensPerThread - 1);
+  const int r_first = tw <= t_last ? find_warp((int32_t)tw) : 0, r_last = tw <= t_last ? find_warp(t_last) : 0;
 #pragma unroll
   for (int i = 0; i < kTokensPerThread; ++i) {
-    const int64_t t = t0 + i * kExtendThreads;
+    const int64_t t64 = tw + i * 32 + lane;
     pos[i] = -1;
     id[i] = -1;
-    if (t >= a.max_tokens || t >= end) continue;
-    int lo = 0, hi = R;                  // last request that starts at or before t
+    if (t64 > t_last) continue;
+    const int32_t t = (int32_t)t64;
+    int lo = r_first, hi = r_last + 1;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (s_start[at(mid)] <= t) lo = mid; else hi = mid;
     }
     const int32_t n = s_seq[at(lo)];
     if (n < 0) continue;
-    pos[i] = n + (int32_t)(t - s_start[at(lo)]);
+    pos[i] = n + (t - s_start[at(lo)]);
     const int32_t j = div_bs(pos[i], div);
     const int32_t have = blocks_of(n, bs, div);
     const int32_t* src = j >= have ? a.free_blocks + (head + s_taken[at(lo)] + (j - have))
@@ -159,7 +174,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
   }
 #pragma unroll
   for (int i = 0; i < kTokensPerThread; ++i) {
-    const int64_t t = t0 + i * kExtendThreads;
+    const int64_t t = tw + i * 32 + lane;
     if (t >= a.max_tokens) continue;
     int64_t slot = -1;
     if (pos[i] >= 0) {
