@@ -563,8 +563,10 @@ is_status_t is_append(const is_append_args_t* args, cudaStream_t stream);
  *   lse = log sum_j w_j.
  * Query head h uses KV head h / (num_q_heads / num_kv_heads).  A row that sees
  * no key gives out 0 and lse -inf.  Rows of no request are left as they were.
- * Keys and values behind seq_len are not read into any row, whatever they
- * hold.  A position whose block the table does not name (an id outside
+ * Positions that none of its rows see, before the window or behind seq_len,
+ * do not touch a request, whatever the cache holds there; a value that is not
+ * finite at a position that some of its rows see may reach its other rows
+ * too.  A position whose block the table does not name (an id outside
  * [0, num_blocks): IS_ST_BLOCK_ID; past the row's end: IS_ST_BLOCK_TABLE) is
  * hidden from every row.  A request whose rows leave [0, num_tokens), are more
  * than max_q_len or fewer than 0, or whose seq_len is outside
@@ -574,7 +576,10 @@ is_status_t is_append(const is_append_args_t* args, cudaStream_t stream);
  *               IS_ATTEND_WORKSPACE_BYTES is enough for every call;
  *               its contents need no initialisation and mean nothing later.
  * Products are summed in fp32; with a 16-bit q the weights w_j are rounded to
- * 16 bits before they multiply the values.  head_dim is 64, 128 or 256. */
+ * 16 bits before they multiply the values.  head_dim is 64, 128 or 256.
+ * The kernel for many rows waits on its own copies and products with a limit
+ * of 2 s, after which it latches IS_ST_TIMEOUT; the call's outputs are then
+ * undefined.  Calls with equal arguments and contents give equal bits. */
 #define IS_ATTEND_WORKSPACE_BYTES 67108864
 typedef struct {
   int32_t num_requests;        /* R: 1 .. IS_MAX_REQUESTS */

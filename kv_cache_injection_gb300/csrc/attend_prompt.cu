@@ -173,6 +173,7 @@ __device__ constexpr uint32_t idesc_of(int n, bool mn_major_b) {
 // Tile t of a request: its tokens, the positions its rows see, its units.
 struct Tile {
   int32_t tok0, toks;
+  int32_t see;           // first position that some row sees
   int32_t kb, ke, units;
 };
 __device__ __forceinline__ Tile tile_of(const AttendArgs& a, const Req& q, int per, int t) {
@@ -182,7 +183,8 @@ __device__ __forceinline__ Tile tile_of(const AttendArgs& a, const Req& q, int p
   const int32_t p0 = q.seq - q.n + x.tok0;           // position of the first token
   x.ke = min(q.ke, p0 + x.toks);
   // whole tiles from position 0 on, so that tiles line up with the cache's blocks
-  x.kb = a.window > 0 ? (int32_t)max((int64_t)p0 - a.window + 1, (int64_t)0) / kKeys * kKeys : 0;
+  x.see = a.window > 0 ? (int32_t)max((int64_t)p0 - a.window + 1, (int64_t)0) : 0;
+  x.kb = x.see / kKeys * kKeys;
   x.units = kItemCost + max(1, (x.ke - x.kb + kKeys - 1) / kKeys);
   return x;
 }
@@ -244,6 +246,7 @@ struct Walk {
 struct Segment {
   int32_t tiles;         // -1: the run has ended
   int32_t k_lo, k_hi, rows;
+  int32_t k_see;         // first key that some row of the item sees
   int32_t r;
   int32_t lim0;          // position of the item's first token
   int32_t head;
@@ -592,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             g.tiles = w.tiles();
             g.k_lo = w.k_lo;
             g.k_hi = w.k_hi;
+            g.k_see = w.x.see;
             g.rows = w.rows;
             g.r = w.r;
             g.lim0 = w.q.seq - w.q.n + w.x.tok0;
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           }
         }
         barrier_loaders();
-        const int n_tiles = g.tiles, k_lo = g.k_lo, k_hi = g.k_hi, rows = g.rows, head = g.head, row_at = g.row0;
+        const int n_tiles = g.tiles, k_lo = g.k_lo, k_hi = g.k_hi, k_see = g.k_see, rows = g.rows, head = g.head, row_at = g.row0;
         const int32_t* table = a.block_table + (size_t)g.r * a.max_blocks;
         const uint8_t* kbase = a.k_cache + (size_t)head * D * EB;
         if (lt == 0) mbar_arrive(smem_addr(&bars.seg_full[seg]));
@@ -695,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           for (int e = 0; e < 2; ++e) {
             const int p = k_lo + j * kKeys + lt + e * kLoaders;
             id[e] = -1;
-            if (j < n_tiles && p < k_hi && lt + e * kLoaders < kKeys) {
+            if (j < n_tiles && p >= k_see && p < k_hi && lt + e * kLoaders < kKeys) {
               id[e] = table[p / a.block_size];
               if (id[e] < 0 || id[e] >= a.num_blocks) {
                 latch(a.status, IS_ST_BLOCK_ID);
@@ -796,10 +800,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             const int kv = warp - kLoaderWarp;
             if (kv < 2 && __all_sync(0xffffffffu, room(n_load + kv))) {
               const uint32_t place = (n_load + kv) % S::kRing, full = smem_addr(&bars.kv_full[place]);
-              // Behind the last key V has to be zero, whatever its block holds there (0 * NaN): those rows are cleared
-              // before the tile is handed on.
-              const int keys = min(kKeys, k_hi - key0);
-              const bool clear = kv == 1 && keys % box != 0;
+              // Before the first key that a row sees and behind the last V has to be zero, whatever its blocks hold
+              // there (0 * NaN): those rows are cleared before the tile is handed on.
+              const int keys = min(kKeys, k_hi - key0), skip = max(0, k_see - key0);
+              const bool clear = kv == 1 && (keys % box != 0 || skip > 0);
               const uint32_t bar = clear ? smem_addr(&bars.v_tail) : full;
               const int64_t rows_of_k = (int64_t)a.num_blocks * a.block_size;
               const int t8 = (int)((from < 0 ? 2 * rows_of_k : from + (kv ? rows_of_k : 0)) >> 3);
@@ -826,6 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 const int end = (keys + box - 1) / box * box;
                 for (int x = lane; x < (end - keys) * (D / 8); x += 32)
                   st_shared_v4(dst + at_chunk<D>(keys + x / (D / 8), x % (D / 8)), make_uint4(0, 0, 0, 0));
+                for (int x = lane; x < skip * (D / 8); x += 32)
+                  st_shared_v4(dst + at_chunk<D>(x / (D / 8), x % (D / 8)), make_uint4(0, 0, 0, 0));
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full);

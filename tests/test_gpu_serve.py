@@ -442,6 +442,75 @@ def test_large_logits(dtype, cache):
     attend_case([(200, 1)], 4, 2, 128, dtype, cache, scale=0.0, scales=SCALES.get(cache, (1.0, 1.0)))
 
 
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("bs", [16, 24])
+def test_nan_before_the_window(bs, dtype, cache):
+    """Positions before the window of every row hold NaN: single tokens and a prompt."""
+    g = torch.Generator().manual_seed(11)
+    H, Hq, D, n, sc = 2, 8, 64, 700, SCALES.get(cache, (1.0, 1.0))
+    nb = -(-n // bs)
+    for rows, window in ((1, 90), (20, 250)):
+        store = nan_cache((2, nb, bs, H, D), cache)
+        flat = store.view(2, nb * bs, H, D)
+        see = slice(n - rows - window + 1, n)
+        x = [torch.zeros(n, H, D, dtype=torch.float64) for _ in range(2)]
+        for i in range(2):
+            flat[i, see] = quantise(torch.randn(rows + window - 1, H, D, generator=g), cache, sc[i])
+            x[i][see] = ref.stored_values(cache, flat[i, see]) * sc[i]
+        q = torch.randn(rows, Hq, D, generator=g).to(ref.TORCH[dtype])
+        out, lse, status = torch.empty_like(q, device=DEV), torch.empty(rows, Hq, device=DEV), ints([0])
+        api.is_attend(q.to(DEV), ints([n]), ints([list(range(nb))]), api.make_cache_desc(bs, nb, cache, *sc), store.to(DEV), out,
+                      api.attend_workspace(), status, q_start=ints([0, rows]), max_q_len=rows, window=window, lse_out=lse)
+        o, ls, spread, heft, seen = ref.attend(q.double(), n, *x, torch.ones(n, dtype=torch.bool), D ** -0.5, window)
+        tol, ltol = ref.attend_tolerance(dtype, cache, D, o, ls, spread, heft, seen, float(x[1].abs().max()))
+        assert bool(((out.cpu().double() - o).abs() <= tol).all()) and bool(((lse.cpu().double() - ls).abs() <= ltol).all())
+        assert status.tolist() == [0]
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("Hq,H", [(64, 1), (100, 1), (33, 3)])
+def test_wide_groups(Hq, H, dtype, cache):
+    sc = SCALES.get(cache, (1.0, 1.0))
+    attend_case([(200, 1), (33, 3), (150, 9)], Hq, H, 64, dtype, cache, scales=sc)
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-40, 1e-30])
+def test_odd_scales(scale, dtype, cache):
+    sc = SCALES.get(cache, (1.0, 1.0))
+    attend_case([(200, 60), (130, 1)], 4, 2, 64, dtype, cache, scales=sc, scale=scale)
+
+
+@pytest.mark.parametrize("rows", [1, 50])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_rows_of_any_magnitude(rows, cache):
+    """bf16 query rows from 1e-35 to 1e30, and zeros: an FP8 cache's products are taken in fp16, on scaled rows."""
+    g = torch.Generator().manual_seed(12)
+    H, Hq, D, n, bs, sc = 1, 4, 64, 300, 16, SCALES.get(cache, (1.0, 1.0))
+    nb = -(-n // bs)
+    store = nan_cache((2, nb, bs, H, D), cache)
+    flat, x = store.view(2, nb * bs, H, D), []
+    for i in range(2):
+        flat[i, :n] = quantise(torch.randn(n, H, D, generator=g), cache, sc[i])
+        x.append(ref.stored_values(cache, flat[i, :n]) * sc[i])
+    size = torch.tensor([1e-35, 1e-3, 0.0, 1e30])
+    for scale in (1e-30, 1.0):
+        q = (torch.randn(rows, Hq, D, generator=g) * size[:, None]).to(torch.bfloat16)
+        out, lse, status = torch.empty_like(q, device=DEV), torch.empty(rows, Hq, device=DEV), ints([0])
+        api.is_attend(q.to(DEV), ints([n]), ints([list(range(nb))]), api.make_cache_desc(bs, nb, cache, *sc), store.to(DEV), out,
+                      api.attend_workspace(), status, q_start=ints([0, rows]), max_q_len=rows, scale=scale, lse_out=lse)
+        use = slice(0, 4 if scale < 1 else 3)         # 1e30 at scale 1: one key takes all, ties of 2^100 apart decided in fp32
+        o, ls, spread, heft, seen = ref.attend(q.double(), n, *x, torch.ones(n, dtype=torch.bool), scale, 0)
+        tol, ltol = ref.attend_tolerance("bf16", cache, D, o, ls, spread, heft, seen, float(x[1].abs().max()))
+        assert bool(((out.cpu().double() - o).abs() <= tol)[:, use].all())
+        assert bool(((lse.cpu().double() - ls).abs() <= ltol)[:, use].all()) and status.tolist() == [0]
+
+
+def test_thousands_of_requests():
+    attend_case([(1 + (53 * r) % 40, (r * 7) % 3) for r in range(2500)], 2, 1, 64, "bf16", "bf16")
+    attend_case([(1 + (53 * r) % 40, (r * 7) % 19) for r in range(600)], 4, 1, 64, "f16", "f16")
+
+
 def test_many_requests_without_q_start_and_strided_q():
     attend_case([(1 + (37 * r) % 90, 1) for r in range(300)], 4, 2, 64, "bf16", "bf16", use_start=False)
     attend_case([(50, 3), (20, 20)], 4, 2, 64, "bf16", "bf16", spread_q=True)
