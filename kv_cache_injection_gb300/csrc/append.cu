@@ -11,6 +11,13 @@
 // with its own heads (and its own copy of the sines: 2 a lane, less than a
 // block barrier costs), so that a single token is still one round of loads.
 // Bound by memory: every input is read once and every output written once.
+//
+// Measured: 8192 tokens, 32 + 8 heads of 128, bf16, three axes, 201 MB: 38 us =
+// 5.3 TB/s, 78 % of a plain copy.  A CTA per token with block barriers took 44.7
+// us, rows loaded before the slot was known 40.5; a division per vector and the
+// table read through the constant path (one address at a time) cost 10 us of a
+// first warp-per-token form.  Batches of 3 to 10 vectors and smaller register
+// budgets measured the same or worse.  One token: 3 us, the launch.
 #include "common.cuh"
 #include "internal.h"
 

@@ -13,16 +13,24 @@
 //   found from the lengths on the device: a long request is spread over many
 //   CTAs, short ones share one, whatever the batch looks like.  An item that
 //   crosses CTAs leaves an unnormalised partial (m, l, O) per CTA in the
-//   workspace and attend_join_kernel adds them up in CTA order, so results do
-//   not depend on timing.
+//   workspace and a second kernel adds them up in CTA order, so results do not
+//   depend on timing.  (Joining in the CTA that finishes last instead, counted
+//   with atomics, measured the same at 100 requests and 17 us instead of 9 at
+//   one, where a dozen CTAs meet on one counter.)
 // - Inside a CTA every warp runs alone on its own tiles of KT keys, with its
 //   own cp.async ring in shared memory (no block barrier in the loop) and its
-//   own running maximum m, sum l and output O, joined once at the end.
+//   own running maximum m, sum l and output O, joined once at the end, under
+//   the first loads of the CTA's next item.  Three CTAs of 64 KB rings fit an SM:
+//   12 warps with a tile of 8 KB on its way each.  (Two CTAs with three tiles a
+//   warp: 100 requests 51.5 us, 48.5 with three CTAs of two; a ring with K and V
+//   released separately, so that half a tile more is in flight: 4 % slower, for
+//   the second pass over the rows' addresses.)
 // - The tensor cores take the transposed products S^T = K Q^T and
 //   O^T = V^T P^T (mma.m16n8k16): the keys and the head dimension fill the
 //   16-row side and the query rows the 8-column side, so a group of 4 to 8
 //   query heads wastes little.  tcgen05 wants 128 (or 64) rows and gains
-//   nothing here: the products take a tenth of the time the loads take.
+//   nothing here: the SMs issue in a fifth of their slots (bf16) while the
+//   memory is the limit.
 // - The maximum moves only when a logit passes it by more than 2^8 (in the
 //   base-2 exponent): the weights stay below 2^8, far from overflow in bf16
 //   and fp16, and the usual tile costs one vote instead of a reduction.
@@ -32,6 +40,14 @@
 // values are exact in fp16, so that path computes in fp16, a bf16 query row
 // being scaled by a power of two into fp16's range (exact, undone in fp32).
 // fp32 caches use fp32 fused multiply-adds throughout.
+//
+// Measured (H = 8, D = 128, bf16 unless said): 4 requests of 60,000-131,000
+// tokens 264 us, 6.8 TB/s, the rate of a plain copy; 64 requests of 500-8000
+// tokens 170 us (6.3 TB/s), with an FP8 cache 101 us (5.3 TB/s, where the
+// conversions fill 44 % of the issue slots); 100 requests of 300-2048 tokens
+// (H = 4) 46.6 us against 34.3 for their bytes, the rest being the start
+// (2 us to find the runs, 3 more until the first tile has landed), the last
+// tiles and the join.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -506,13 +522,14 @@ struct SplitWalk {
   int r;
   Req q, ahead;
 
-  __device__ __forceinline__ void start(const AttendArgs& a, int r_, int64_t base_, int64_t u_, int64_t u_end_, int64_t run_) {
+  __device__ __forceinline__ void start(const AttendArgs& a, int r_, const Req& q_, int64_t base_, int64_t u_, int64_t u_end_,
+                                        int64_t run_) {
     r = r_;
+    q = q_;
     base = base_;
     u = u_first = u_;
     u_end = u_end_;
     run = run_;
-    q = read_request(a, r, false);
     look_ahead(a);
   }
   __device__ __forceinline__ void look_ahead(const AttendArgs& a) {
@@ -532,7 +549,7 @@ struct SplitWalk {
         look_ahead(a);
         continue;
       }
-      const int item = (int)((u - base) / units);
+      const int item = (int)div_small(u - base, units);
       const int64_t item0 = base + (int64_t)item * units;
       const int ua = (int)(u - item0), ub = (int)min((int64_t)units, u_end - item0);
       const int head = item / tiles, tile = item - head * tiles;
@@ -544,8 +561,8 @@ struct SplitWalk {
       out->tile = tile;
       out->k_lo = q.kb + ua * UNIT;
       out->k_hi = min(min(q.ke, q.seq - q.n + last_tok + 1), q.kb + ub * UNIT);
-      out->slot = ua == 0 && ub == units ? -1 : 2 * blockIdx.x + (u == u_first ? 0 : 1);
-      out->parts = ua == 0 && ub < units ? (int)((item0 + units - 1) / run) - (int)blockIdx.x + 1 : 0;
+      out->slot = ua == 0 && ub == units ? -1 : 2 * (int)blockIdx.x + (u == u_first ? 0 : 1);
+      out->parts = ua == 0 && ub < units ? (int)div_small(item0 + units - 1, run) - (int)blockIdx.x + 1 : 0;
       out->r = r;
       u = item0 + ub;
       return;
@@ -559,8 +576,6 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
   using S = SplitShape<E>;
   constexpr int ROWS = E::kRows, D = E::D, KT = E::kKeys, PITCH = E::kPitch;
   __shared__ int64_t scratch[kWarps];
-  __shared__ int64_t s_base;
-  __shared__ int32_t s_req;
   __shared__ SplitSeg s_seg[2];
   __shared__ float s_ml[kWarps][2 * ROWS];
   __shared__ uint32_t s_valid[kWarps][S::kStages];
@@ -581,28 +596,25 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
   }
   int64_t total;
   int64_t at = block_exclusive_scan_1bar<kWarps>(mine, scratch, &total);
-  const int64_t run = max((int64_t)kMinUnits, (total + gridDim.x - 1) / gridDim.x);
+  const int64_t run = max((int64_t)kMinUnits, div_small(total + gridDim.x - 1, gridDim.x));
   const int64_t u = (int64_t)blockIdx.x * run, u_end = min(total, u + run);
   if (u >= u_end) {
     if (tid == 0) record_of(a, blockIdx.x)->parts = 0;
     return;
   }
-  SplitWalk walk;                        // thread 0's
-  if (at <= u && u < at + mine) {
+  // The thread whose requests the run begins in walks along it.
+  SplitWalk walk;
+  const bool walker = at <= u && u < at + mine;
+  if (walker) {
     for (int r = r0; r < r1; ++r) {
       const Req q = read_request(a, r, false);
       const int64_t n = (int64_t)a.H * tiles_of(a, q, ROWS) * units_of(q, S::kUnit);
       if (u < at + n || r == r1 - 1) {
-        s_req = r;
-        s_base = at;
+        walk.start(a, r, q, at, u, u_end, run);
         break;
       }
       at += n;
     }
-  }
-  __syncthreads();
-  if (tid == 0) {
-    walk.start(a, s_req, s_base, u, u_end, run);
     walk.template next<ROWS, S::kUnit>(a, &s_seg[0]);
   }
   __syncthreads();
@@ -672,7 +684,7 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
   if (s_seg[0].r >= 0) open(s_seg[0]);
   for (int k = 0; s_seg[k & 1].r >= 0; ++k) {
     const SplitSeg& g = s_seg[k & 1];
-    if (tid == 0) walk.template next<ROWS, S::kUnit>(a, &s_seg[(k + 1) & 1]);
+    if (walker) walk.template next<ROWS, S::kUnit>(a, &s_seg[(k + 1) & 1]);
     Req q;
     q.row0 = g.row0;
     q.n = g.n;

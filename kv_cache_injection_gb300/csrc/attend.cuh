@@ -63,6 +63,11 @@ __device__ __forceinline__ Req read_request(const AttendArgs& a, int r, bool rep
   return q;
 }
 
+// x / d for non-negative operands, in 32-bit arithmetic when both fit.
+__device__ __forceinline__ int64_t div_small(int64_t x, int64_t d) {
+  return ((x | d) >> 31) == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
+}
+
 // ---- workspace -------------------------------------------------------------------
 // [ctas] join records, then two partials per CTA: of the item its run begins
 // in (slot 2 c) and of the one it ends in (2 c + 1), when those cross its ends.

@@ -8,8 +8,10 @@
 // most IS_MAX_REQUESTS requests, 32 KB of input: every CTA computes them for
 // itself instead of waiting for another, so the call is one launch and no CTA
 // depends on what another writes (a new token's block id comes from the free
-// list, not from the table entry).  Bound by latency at few tokens, by the 12
-// bytes written per token at many.
+// list, not from the table entry).  Bound by latency at few tokens (100
+// requests of one token: 3.6 us) and by the instructions of going over all
+// requests in every CTA at many (4096 requests, 614,000 tokens, 7.7 MB: 8.5
+// us; 45 with 64-bit divisions and a search per token).
 #include <algorithm>
 
 #include "block_scan.cuh"
@@ -18,11 +20,11 @@
 
 namespace isk {
 
-// Few requests: small CTAs, two requests a thread at most.  Many: large ones,
-// since each CTA goes over all requests (4096 requests with 614,000 tokens:
-// 14.1 us with 512 threads a CTA, 12.1 us with 1024).
+// Few requests: small CTAs, one token and at most two requests a thread.  Many:
+// large ones, since each CTA goes over all requests (4096 requests: 14.1 us
+// with 512 threads a CTA, 12.1 with 1024).
 constexpr int kFewRequests = 512, kFewThreads = 256, kManyThreads = 1024;
-constexpr int kTokensPerThread = 4;
+constexpr int kFewTokens = 1, kManyTokens = 4;   // tokens a thread
 
 // Division by the block size as a multiplication: with 2^(k-1) < bs <= 2^k and
 // mul = ceil(2^(26+k) / bs), x / bs = x * mul >> (26 + k) for every x < 2^26
@@ -46,10 +48,10 @@ __device__ __forceinline__ int32_t blocks_of(int32_t n, int32_t bs, const BlockD
 // requests each then hit different banks.
 __host__ __device__ constexpr int at(int r) { return r + (r >> 5); }
 
-template <int kExtendThreads, int kPer>
+template <int kExtendThreads, int kPer, int kTokensPerThread>
 __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_args_t a, const BlockDiv div) {
   extern __shared__ int32_t sm[];
-  __shared__ int64_t scratch[33];
+  __shared__ int64_t scratch[2][33];
   __shared__ int32_t s_used;
   const int R = a.num_requests, bs = a.block_size, tid = threadIdx.x;
   const int pitch = at(R) + 1;
@@ -104,8 +106,13 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
     missing += miss;
   }
   int64_t total, all_missing;
-  int64_t first = block_exclusive_scan(tokens, scratch, &total);
-  int64_t taken = block_exclusive_scan(missing, scratch, &all_missing);
+  // One barrier a sum while adding up the warps' totals is cheap, three with many warps.
+  auto scan = [](int64_t x, int64_t* scratch_, int64_t* sum) {
+    if constexpr (kExtendThreads <= 256) return block_exclusive_scan_1bar<kExtendThreads / 32>(x, scratch_, sum);
+    else return block_exclusive_scan(x, scratch_, sum);
+  };
+  int64_t first = scan(tokens, scratch[0], &total);
+  int64_t taken = scan(missing, scratch[1], &all_missing);
   int32_t used = 0;                      // blocks taken up to this thread's last request
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -211,20 +218,21 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
   if (bits) latch(a.status_out, bits);
 }
 
-template <int THREADS, int PER>
+template <int THREADS, int PER, int TOKENS>
 static cudaError_t launch_extend_t(const is_extend_args_t& a, const LaunchCfg& cfg) {
-  auto* kern = extend_kernel<THREADS, PER>;
+  auto* kern = extend_kernel<THREADS, PER, TOKENS>;
   const size_t smem = (size_t)3 * (at(a.num_requests) + 1) * sizeof(int32_t);
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  constexpr int per_cta = THREADS * kTokensPerThread;
+  constexpr int per_cta = THREADS * TOKENS;
   const int grid = (int)(((int64_t)a.max_tokens + per_cta - 1) / per_cta);
   return launch_ex(kern, dim3(grid), dim3(THREADS), smem, cfg.stream, cfg.pdl, a, block_div(a.block_size));
 }
 
 cudaError_t launch_extend(const is_extend_args_t& a, const LaunchCfg& cfg) {
   static_assert(kFewRequests <= kFewThreads * 2 && IS_MAX_REQUESTS <= kManyThreads * 4, "every request has a thread");
-  return a.num_requests <= kFewRequests ? launch_extend_t<kFewThreads, 2>(a, cfg) : launch_extend_t<kManyThreads, 4>(a, cfg);
+  return a.num_requests <= kFewRequests ? launch_extend_t<kFewThreads, 2, kFewTokens>(a, cfg)
+                                        : launch_extend_t<kManyThreads, 4, kManyTokens>(a, cfg);
 }
 
 }  // namespace isk

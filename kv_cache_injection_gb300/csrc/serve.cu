@@ -270,8 +270,8 @@ extern "C" is_status_t is_attend(const is_attend_args_t* a, cudaStream_t stream)
   if (a->reserved != 0) return refuse(IS_ERR_INVALID_ARG, "reserved must be 0");
   if (!std::isfinite(a->scale)) return refuse(IS_ERR_INVALID_ARG, "scale must be finite");
   if (D != 64 && D != 128 && D != 256) return refuse(IS_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
-  if (Hq > (1 << 16) || (int64_t)T * Hq > INT32_MAX)
-    return refuse(IS_ERR_UNSUPPORTED, "at most 65536 heads, and num_tokens * num_q_heads below 2^31");
+  if (Hq > (1 << 16) || (int64_t)T * Hq > (1 << 30))
+    return refuse(IS_ERR_UNSUPPORTED, "at most 65536 heads and 2^30 rows (num_tokens * num_q_heads)");
   is_status_t st = check_layer_cache(a->cache, a->dtype, a->layer_cache);
   if (st != IS_OK) return st;
   if (!a->q_start && T < R) return refuse(IS_ERR_INVALID_ARG, "without q_start there is one row per request");
