@@ -584,7 +584,8 @@ is_status_t is_append(const is_append_args_t* args, cudaStream_t stream);
 typedef struct {
   int32_t num_requests;        /* R: 1 .. IS_MAX_REQUESTS */
   int32_t num_tokens;          /* rows of q, out, lse_out */
-  int32_t max_q_len;           /* largest number of query rows of a request, >= 1 */
+  int32_t max_q_len;           /* largest number of query rows of a request, >= 1: chooses the kernel,
+                                  so a step of single tokens should say 1 */
   int32_t num_q_heads;         /* a multiple of num_kv_heads */
   int32_t num_kv_heads;
   int32_t head_dim;

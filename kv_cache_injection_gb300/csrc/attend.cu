@@ -562,7 +562,10 @@ struct SplitWalk {
       out->k_lo = q.kb + ua * UNIT;
       out->k_hi = min(min(q.ke, q.seq - q.n + last_tok + 1), q.kb + ub * UNIT);
       out->slot = ua == 0 && ub == units ? -1 : 2 * (int)blockIdx.x + (u == u_first ? 0 : 1);
-      out->parts = ua == 0 && ub < units ? (int)div_small(item0 + units - 1, run) - (int)blockIdx.x + 1 : 0;
+      // Within the grid, whatever became of the lengths since they were added up.
+      out->parts = ua == 0 && ub < units
+                       ? (int)(min(div_small(item0 + units - 1, run), (int64_t)gridDim.x - 1) - (int64_t)blockIdx.x) + 1
+                       : 0;
       out->r = r;
       u = item0 + ub;
       return;

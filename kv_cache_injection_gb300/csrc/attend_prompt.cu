@@ -242,7 +242,8 @@ struct Walk {
       if (ub <= 0) continue;             // none of its keys yet: the item begins in the next CTA
       begins = ua == 0;
       whole = begins && ub == x.units - kItemCost;
-      parts = (int)((item0 + x.units - 1) / run) - (int)blockIdx.x + 1;
+      // within the grid, whatever became of the lengths since they were added up
+      parts = (int)(min(div_small(item0 + x.units - 1, run), (int64_t)gridDim.x - 1) - (int64_t)blockIdx.x) + 1;
       k_lo = x.kb + ua * kKeys;
       k_hi = min(x.ke, x.kb + ub * kKeys);
       rows = x.toks * a.G;

@@ -481,6 +481,15 @@ def test_odd_scales(scale, dtype, cache):
     attend_case([(200, 60), (130, 1)], 4, 2, 64, dtype, cache, scales=sc, scale=scale)
 
 
+@pytest.mark.parametrize("dtype,cache", TYPES)
+def test_single_tokens_under_a_large_bound(dtype, cache):
+    """max_q_len far above the rows there are."""
+    sc = SCALES.get(cache, (1.0, 1.0))
+    attend_case([(n, 1) for n in (1, 16, 17, 127, 128, 129, 400, 2000, 3, 0, 77, 256, 600)], 4, 1, 128, dtype, cache, scales=sc,
+                max_q=1000)
+    attend_case([(900, 1)] * 20, 8, 2, 64, dtype, cache, scales=sc, max_q=64, use_start=True, window=100)
+
+
 @pytest.mark.parametrize("rows", [1, 50])
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_rows_of_any_magnitude(rows, cache):
