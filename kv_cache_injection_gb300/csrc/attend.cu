@@ -223,8 +223,9 @@ struct MmaEngine {
           ldmatrix4(ks + chunk_at<kRowBytes>(row, c + (mat >> 1)), b);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint32_t lo = b[2 * u], hi = b[2 * u + 1];
-            const uint32_t k[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(hi), e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi >> 16)};
+            uint32_t k[4];
+            e4m3x4_f16x4(b[2 * u], k[0], k[2]);
+            e4m3x4_f16x4(b[2 * u + 1], k[1], k[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816<M>(s[mt][nt], k, q[c + u][nt][0], q[c + u][nt][1]);
           }
@@ -308,8 +309,9 @@ struct MmaEngine {
           ldmatrix4_t(vs + chunk_at<kRowBytes>(row, c + (mat >> 1)), b);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint32_t lo = __byte_perm(b[2 * u], 0, 0x3120), hi = __byte_perm(b[2 * u + 1], 0, 0x3120);
-            const uint32_t v[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi), e4m3x2_f16x2(hi >> 16)};
+            uint32_t v[4];
+            e4m3x4_f16x4(__byte_perm(b[2 * u], 0, 0x3120), v[0], v[1]);
+            e4m3x4_f16x4(__byte_perm(b[2 * u + 1], 0, 0x3120), v[2], v[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816<M>(o[c + u][nt], v, p[mt][nt][0], p[mt][nt][1]);
           }
@@ -635,7 +637,7 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
     const int j = k_lo + (warp + i * kWarps) * KT + lane;
     id_next = -1;
     if (i < n_mine && lane < KT && j < k_hi) {
-      const int b = j / a.block_size;
+      const int b = block_of(a, j);
       off_next = j - b * a.block_size;
       id_next = table[b];
       if (id_next < 0 || id_next >= a.num_blocks) {

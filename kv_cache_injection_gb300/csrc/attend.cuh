@@ -25,11 +25,15 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two E4M3 bytes (the low half of x) as two fp16 values, exact.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(x));
-  return r;
+// Four E4M3 bytes as fp16 values, exact: lo of bytes 0 and 1, hi of bytes 2 and 3.
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+// Block of position p: a shift where the block size is a power of two.
+__device__ __forceinline__ int32_t block_of(const AttendArgs& a, int32_t p) {
+  return a.block_shift >= 0 ? p >> a.block_shift : p / a.block_size;
 }
 
 // ---- the batch ------------------------------------------------------------------

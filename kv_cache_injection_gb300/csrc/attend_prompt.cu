@@ -287,7 +287,10 @@ __device__ __forceinline__ uint32_t bits_between(int at, int lo, int hi) {
 
 // Eight E4M3 bytes as eight fp16 values, exact.
 __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
-  return make_uint4(e4m3x2_f16x2(lo), e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi), e4m3x2_f16x2(hi >> 16));
+  uint4 r;
+  e4m3x4_f16x4(lo, r.x, r.y);
+  e4m3x4_f16x4(hi, r.z, r.w);
+  return r;
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -701,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           const int key0 = k_lo + j * kKeys, p = key0 + lane * box;
           token = -1;
           if (lane < groups && j < n_tiles && p < k_hi) {
-            const int b = p / a.block_size;
+            const int b = block_of(a, p);
             const int32_t id = table[b];
             if (id >= 0 && id < a.num_blocks) token = (int64_t)id * a.block_size + (p - b * a.block_size);
             else latch(a.status, IS_ST_BLOCK_ID);
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             const int p = k_lo + j * kKeys + lt + e * kLoaders;
             id[e] = -1;
             if (j < n_tiles && p >= k_see && p < k_hi && lt + e * kLoaders < kKeys) {
-              id[e] = table[p / a.block_size];
+              id[e] = table[block_of(a, p)];
               if (id[e] < 0 || id[e] >= a.num_blocks) {
                 latch(a.status, IS_ST_BLOCK_ID);
                 id[e] = -1;
@@ -731,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int p = k_lo + j * kKeys + lt + e * kLoaders;
-            at_key[e] = id[e] < 0 ? -1ll : ((long long)id[e] * a.block_size + p % a.block_size) * token_bytes;
+            at_key[e] = id[e] < 0 ? -1ll : ((long long)id[e] * a.block_size + (p - block_of(a, p) * a.block_size)) * token_bytes;
             named[e] = __ballot_sync(0xffffffffu, at_key[e] >= 0);
           }
           s_off[lt] = at_key[0];

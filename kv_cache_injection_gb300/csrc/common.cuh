@@ -161,6 +161,7 @@ struct AttendArgs {
   uint8_t* workspace;
   uint32_t* status;
   int32_t R, T, max_q, Hq, H, G, D, max_blocks, block_size, num_blocks;
+  int32_t block_shift;          // log2(block_size), or -1 if that is no whole number
   int32_t window;               // 0: none
   float scale;                  // softmax scale times the K scale of an FP8 cache
   float v_scale;

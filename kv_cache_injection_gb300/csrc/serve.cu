@@ -324,6 +324,9 @@ extern "C" is_status_t is_attend(const is_attend_args_t* a, cudaStream_t stream)
   p.max_blocks = a->max_blocks_per_seq;
   p.block_size = a->cache.block_size;
   p.num_blocks = a->cache.num_blocks;
+  p.block_shift = -1;
+  for (int s = 0; s <= 24; ++s)
+    if (a->cache.block_size == 1 << s) p.block_shift = s;
   p.window = a->window;
   p.dtype = a->dtype;
   p.fp8 = a->cache.dtype == IS_FP8_E4M3;
