@@ -66,8 +66,9 @@ constexpr int kThreads = 384;
 constexpr int kKeys = 128;               // keys of a tile, and of a unit
 constexpr int kLoaderWarp = 8, kLoaders = 96, kMmaWarp = 11;
 // Registers a thread: 168 at launch (65,536 / 384); the softmax warps take what
-// a row of S needs, the other four give it: 2 * 208 + 88 = 3 * 168.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// a row of S needs, the other four give it: 2 * 192 + 120 = 3 * 168.  (208 and 88:
+// the loaders and the MMA thread spill, and the long prompts take 426 us, not 406.)
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 constexpr int kMinRun = 4;               // units of a CTA's run, at least
 // Starting and ending an item costs a CTA about as much as this many units, so
 // an item counts as so many more, before its first.
@@ -924,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         const uint64_t q_desc = tile_desc<D, F8>(q_tile, 1), k_desc = tile_desc<D, F8>(q_tile + S::kQBytes, 1);
         const uint64_t v_desc = tile_desc<D, F8>(q_tile + S::kQBytes, 1024 >> 4);
 #define ISK_BAR(member) (bar0 + (uint32_t)offsetof(Bars, member))
-        uint32_t n_q = 0, p_turn[2] = {0, 0};
+        uint32_t n_q = 0, p_turn0 = 0, p_turn1 = 0;
         uint32_t place = 0, turn = 0;                  // of the next load: its place in the ring, and the ring's turn
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -937,7 +938,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             turn ^= 1u;
           }
         };
-        auto scores = [&](uint32_t side, uint32_t k_place) {
+        // Each side is code of its own, so that its addresses are constants.
+        auto scores = [&](auto side_, uint32_t k_place) {
+          constexpr uint32_t side = decltype(side_)::value;
           const uint64_t qd = q_desc + side * (S::kTileBytes >> 4), kd = k_desc + k_place * (S::kTileBytes >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -946,11 +949,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           }
           mma_commit(ISK_BAR(s_full) + 8 * side);
         };
+        auto values = [&](auto side_, uint64_t vd, uint32_t& p_turn, bool first) {
+          constexpr uint32_t side = decltype(side_)::value;
+          constexpr uint32_t o_at = S::kOCol + (uint32_t)D * side, p_at = 128u * side;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!wait(ISK_BAR(p_full) + 16 * side + 8 * half, p_turn)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              mma_ts(tm + o_at, tm + p_at + 8u * k, vd + 2u * k * (S::kGroupBytes >> 4), kIdO, k != 0 || !first);
+          }
+          p_turn ^= 1u;
+        };
+        constexpr std::integral_constant<uint32_t, 0> A{};
+        constexpr std::integral_constant<uint32_t, 1> B{};
         for (uint32_t n_seg = 0; ok; ++n_seg) {
           const uint32_t seg = n_seg % kSegments;
           if (!wait(ISK_BAR(seg_full) + 8 * seg, (n_seg / kSegments) & 1u)) break;
           const int n_tiles = s_seg[seg].tiles;
-          const uint32_t sides = s_seg[seg].rows > 128 ? 2 : 1;
+          const bool both = s_seg[seg].rows > 128;
           if (n_tiles < 0) break;
           mbar_arrive(ISK_BAR(seg_empty) + 8 * seg);
           if (n_tiles == 0) continue;
@@ -958,38 +976,34 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           ++n_q;
           if (!wait(ISK_BAR(kv_full) + 8 * place, turn)) break;
           tc_fence_after();
-          for (uint32_t side = 0; side < sides; ++side) scores(side, place);
+          scores(A, place);
+          if (both) scores(B, place);
           mma_commit(ISK_BAR(kv_empty) + 8 * place);
-          for (int j = 0; j < n_tiles && ok; ++j) {
+          for (int j = 0; j < n_tiles; ++j) {
             next_place();                              // V of this tile
             const uint32_t v_place = place;
             if (!wait(ISK_BAR(kv_full) + 8 * v_place, turn)) break;
             next_place();                              // K of the next
             const uint64_t vd = v_desc + v_place * (S::kTileBytes >> 4);
-            for (uint32_t side = 0; side < sides; ++side) {
-              const uint32_t o_tm = tm + S::kOCol + (uint32_t)D * side, p_tm = tm + 128u * side;
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                if (!wait(ISK_BAR(p_full) + 16 * side + 8 * half, p_turn[side])) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 4 * half; k < 4 * half + 4; ++k)
-                  mma_ts(o_tm, p_tm + 8u * k, vd + 2u * k * (S::kGroupBytes >> 4), kIdO, (j | k) != 0);
-              }
-              if (!ok) break;
-              p_turn[side] ^= 1u;
-              if (side == sides - 1) mma_commit(ISK_BAR(kv_empty) + 8 * v_place);
-              if (j == n_tiles - 1) {
-                mma_commit(ISK_BAR(o_full) + 8 * side);
-              } else {
-                if (side == 0) {
-                  if (!wait(ISK_BAR(kv_full) + 8 * place, turn)) break;
-                  tc_fence_after();
-                }
-                scores(side, place);
-                if (side == sides - 1) mma_commit(ISK_BAR(kv_empty) + 8 * place);
-              }
+            const bool last = j == n_tiles - 1;
+            values(A, vd, p_turn0, j == 0);
+            if (!ok) break;
+            if (!both) mma_commit(ISK_BAR(kv_empty) + 8 * v_place);
+            if (last) {
+              mma_commit(ISK_BAR(o_full));
+            } else {
+              if (!wait(ISK_BAR(kv_full) + 8 * place, turn)) break;
+              tc_fence_after();
+              scores(A, place);
             }
+            if (both) {
+              values(B, vd, p_turn1, j == 0);
+              if (!ok) break;
+              mma_commit(ISK_BAR(kv_empty) + 8 * v_place);
+              if (last) mma_commit(ISK_BAR(o_full) + 8);
+              else scores(B, place);
+            }
+            if (!last) mma_commit(ISK_BAR(kv_empty) + 8 * place);
           }
           if (ok) mma_commit(ISK_BAR(q_empty));
         }
