@@ -828,11 +828,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
               const int t8 = (int)((from < 0 ? 2 * rows_of_k : from + (kv ? rows_of_k : 0)) >> 3);
               if (kv == 0) {
                 const uint32_t named = __ballot_sync(0xffffffffu, lane < groups && from >= 0);
-                for (int word = 0; word < 4; ++word) {
-                  const int key = 32 * word + lane;
-                  const uint32_t bits = __ballot_sync(0xffffffffu, key < keys && ((named >> (key / box)) & 1u));
-                  if (lane == 0) s_mask[slot][word] = bits;
+                uint4 bits = make_uint4(~0u, ~0u, ~0u, ~0u);
+                if (keys < kKeys || __popc(named) < groups) {
+                  auto word = [&](int key) {
+                    return __ballot_sync(0xffffffffu, key < keys && ((named >> (key / box)) & 1u));
+                  };
+                  bits = make_uint4(word(lane), word(32 + lane), word(64 + lane), word(96 + lane));
                 }
+                if (lane == 0) *reinterpret_cast<uint4*>(s_mask[slot]) = bits;
                 if (lane == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
               }
               if (leader) mbar_expect_tx(bar, S::kTileBytes);
