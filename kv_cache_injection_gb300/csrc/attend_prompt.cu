@@ -37,15 +37,17 @@
 // B's place.
 //
 // Measured (H = 8, G = 4, D = 128, bf16): two prompts of 2000-2500 tokens
-// behind up to 8192, 538 GFLOP, 427 us = 1.26 PFLOP/s, 66 % of the burst rate of
+// behind up to 8192, 538 GFLOP, 399 us = 1.35 PFLOP/s, 71 % of the burst rate of
 // a plain library product.  128 keys of a pair of tiles are 2048 clocks of MMAs
-// (64 each for M 128, N 128, K 16) and take 3300.  Leaving out the exponentials
+// (64 each for M 128, N 128, K 16) and take 2900.  Leaving out the exponentials
 // changes nothing; half the S products save 3 %, half the O products 2 %, half
 // of the loaded bytes 8 %: shared memory feeds the MMAs (S alone reads 128
 // bytes a clock) while it takes in the next tiles, and a tile's next S waits
-// for its softmax (1400 clocks) and the other tile's products.  16 requests with 20-100 new tokens
-// over 900-2000: 61 us; the start and end of an item (its first tiles, 64 KB of
-// output or 128 KB of partial) cost as much as about six key tiles.
+// for its softmax (1400 clocks) and the other tile's products.  16 requests with
+// 20-100 new tokens over 900-2000: 57 us; the start and end of an item (its first
+// tiles, 64 KB of output or 128 KB of partial) cost as much as about six key
+// tiles.  One request, 100 new tokens over 400: 22 us, the latency of this kernel
+// (2 us to the first run, 4 to the first softmax, 6 of output) and of the join.
 #include <cuda.h>
 
 #include <algorithm>
@@ -69,7 +71,9 @@ constexpr int kLoaderWarp = 8, kLoaders = 96, kMmaWarp = 11;
 // a row of S needs, the other four give it: 2 * 192 + 120 = 3 * 168.  (208 and 88:
 // the loaders and the MMA thread spill, and the long prompts take 426 us, not 406.)
 constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
-constexpr int kMinRun = 4;               // units of a CTA's run, at least
+// Units of a CTA's run, at least.  4: one request's 100 tokens over 400 take 23.1
+// us, not 21.7, over 1313 26.6, not 26.0; larger batches have longer runs anyway.
+constexpr int kMinRun = 2;
 // Starting and ending an item costs a CTA about as much as this many units, so
 // an item counts as so many more, before its first.
 constexpr int kItemCost = 6;
@@ -235,7 +239,7 @@ struct Walk {
         }
         if (t * per < q.n) x = tile_of(a, q, per, t);
       }
-      head = (int)((u - base) / x.units);
+      head = (int)div_small(u - base, x.units);
       const int64_t item0 = base + (int64_t)head * x.units;
       const int ua = max((int)(u - item0) - kItemCost, 0), ub = (int)min((int64_t)x.units, u_end - item0) - kItemCost;
       at_start = u == u_first;
@@ -362,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       mbar_init(smem_addr(&bars.seg_empty[i]), 9);     // eight softmax warps, the MMA warp
     }
     fence_mbar_init();
+    if (box > 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&rows_map)) : "memory");
   }
   pdl_wait();
   pdl_trigger();
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   for (int r = r0; r < r1; ++r) mine += units_of_request(a, read_request(a, r, blockIdx.x == 0), per);
   int64_t total;
   int64_t at = block_exclusive_scan(mine, scratch, &total);
-  const int64_t run = max((int64_t)kMinRun, (total + gridDim.x - 1) / gridDim.x);
+  const int64_t run = max((int64_t)kMinRun, div_small(total + gridDim.x - 1, gridDim.x));
   const int64_t u0 = (int64_t)blockIdx.x * run, u1 = min(total, u0 + run);
   const bool idle = u0 >= u1;
   if (!idle && at <= u0 && u0 < at + mine) {
