@@ -47,7 +47,7 @@
 // 20-100 new tokens over 900-2000: 57 us; the start and end of an item (its first
 // tiles, 64 KB of output or 128 KB of partial) cost as much as about six key
 // tiles.  One request, 100 new tokens over 400: 22 us, the latency of this kernel
-// (2 us to the first run, 4 to the first softmax, 6 of output) and of the join.
+// (1 us to its run, 4 to the first S, 2 for the tiles, 3.5 of output) and the join.
 #include <cuda.h>
 
 #include <algorithm>
