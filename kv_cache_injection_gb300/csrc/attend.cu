@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
     // Join the warps.  Every thread takes pairs of elements.
     const int rho0 = tile * ROWS, rows = min(ROWS, q.n * a.G - rho0);
     const int slot = g.slot;
-    Partial<ROWS, D>* part = partial_of<ROWS, D>(a, max(slot, 0));
+    Partial<ROWS, D>* part = partial_of<Partial<ROWS, D>>(a, max(slot, 0));
     for (int x = tid; x < rows * (D / 2); x += kAttendThreads) {
       const int row = x / (D / 2), d = (x % (D / 2)) * 2;
       float mx = -INFINITY;
@@ -792,7 +792,7 @@ static cudaError_t launch_split(const AttendArgs& a, const LaunchCfg& cfg) {
   if (e != cudaSuccess) return e;
   // Few parts an item: a CTA joins all rows of a record; else four CTAs, each splitting the parts of a row at a time.
   if (items * 4 >= grid)
-    return launch_ex(attend_join_rows_kernel<T, E::kRows, E::D>, dim3(grid, 1), dim3(kJoinThreads), 0, cfg.stream, cfg.pdl, a);
+    return launch_ex(attend_join_rows_kernel<T, E::kRows, E::D, false>, dim3(grid, 1), dim3(kJoinThreads), 0, cfg.stream, cfg.pdl, a);
   return launch_ex(attend_join_kernel<T, E::kRows, E::D>, dim3(grid, 4), dim3(kJoinThreads), 0, cfg.stream,
                    cfg.pdl, a);
 }

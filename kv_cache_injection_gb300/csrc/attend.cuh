@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -90,13 +91,20 @@ struct Partial {
   float o[ROWS][D];
   float m[ROWS], l[ROWS];
 };
+// The same where a thread writes whole rows (the prompt kernel): by columns of
+// eight, so that the 32 lanes' rows of a store lie behind one another.
+template <int ROWS, int D>
+struct PartialByEights {
+  float o[D / 8][ROWS][8];
+  float m[ROWS], l[ROWS];
+};
 
 __device__ __forceinline__ JoinRecord* record_of(const AttendArgs& a, int cta) {
   return reinterpret_cast<JoinRecord*>(a.workspace + (size_t)cta * kRecordBytes);
 }
-template <int ROWS, int D>
-__device__ __forceinline__ Partial<ROWS, D>* partial_of(const AttendArgs& a, int slot) {
-  return reinterpret_cast<Partial<ROWS, D>*>(a.workspace + partials_offset()) + slot;
+template <typename P>
+__device__ __forceinline__ P* partial_of(const AttendArgs& a, int slot) {
+  return reinterpret_cast<P*>(a.workspace + partials_offset()) + slot;
 }
 
 template <typename T>
@@ -136,7 +144,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = group; i < rec.parts; i += GROUPS) {
-      const Partial<ROWS, D>* p = partial_of<ROWS, D>(a, i == 0 ? rec.slot0 : 2 * (cta + i));
+      const Partial<ROWS, D>* p = partial_of<Partial<ROWS, D>>(a, i == 0 ? rec.slot0 : 2 * (cta + i));
       const float pm = p->m[row], pl = p->l[row];
       const float4 v = *reinterpret_cast<const float4*>(&p->o[row][lane * 4]);
       const float mn = fmaxf(m, pm), mz = mn == -INFINITY ? 0.f : mn;
@@ -179,8 +187,9 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
 }
 
 // The same for items of many rows and few parts: D / 4 lanes take a row, all
-// parts of it.
-template <typename T, int ROWS, int D>
+// parts of it.  By eights a warp takes 32 columns of four rows, so that it reads
+// 128 bytes at a time.
+template <typename T, int ROWS, int D, bool EIGHTS>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_rows_kernel(const AttendArgs a) {
   constexpr int LANES = D / 4, AT_ONCE = kJoinThreads / LANES;
   pdl_wait();
@@ -188,15 +197,22 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_rows_kernel(const At
   const int cta = blockIdx.x;
   const JoinRecord rec = *record_of(a, cta);
   if (rec.parts == 0) return;
-  const int lane = threadIdx.x % LANES;
-  for (int row = blockIdx.y * AT_ONCE + threadIdx.x / LANES; row < rec.rows; row += gridDim.y * AT_ONCE) {
+  using P = std::conditional_t<EIGHTS, PartialByEights<ROWS, D>, Partial<ROWS, D>>;
+  const int warp = threadIdx.x / 32, in_warp = threadIdx.x % 32;
+  const int lane = EIGHTS ? warp % (D / 32) * 8 + in_warp / 8 * 2 + in_warp % 2 : threadIdx.x % LANES;
+  const int first = EIGHTS ? warp / (D / 32) * 4 + in_warp / 2 % 4 : threadIdx.x / LANES;
+  for (int row = blockIdx.y * AT_ONCE + first; row < rec.rows; row += gridDim.y * AT_ONCE) {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int i = 0; i < rec.parts; ++i) {
-      const Partial<ROWS, D>* p = partial_of<ROWS, D>(a, i == 0 ? rec.slot0 : 2 * (cta + i));
+      const P* p = partial_of<P>(a, i == 0 ? rec.slot0 : 2 * (cta + i));
       const float pm = p->m[row], pl = p->l[row];
-      const float4 v = *reinterpret_cast<const float4*>(&p->o[row][lane * 4]);
+      float4 v;
+      if constexpr (EIGHTS)
+        v = *reinterpret_cast<const float4*>(&p->o[lane / 2][row][lane % 2 * 4]);
+      else
+        v = *reinterpret_cast<const float4*>(&p->o[row][lane * 4]);
       const float mn = fmaxf(m, pm), mz = mn == -INFINITY ? 0.f : mn;
       const float f = ex2(m - mz), g = ex2(pm - mz);
       o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);

@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           // store covers 64 bytes of eight rows took four times as long: the shuffles cost more than the sectors.)
           T* dst = reinterpret_cast<T*>(a.out) +
                    ((size_t)(g.row0 + (live ? tok : 0)) * a.Hq + (size_t)g.head * a.G + (live ? row - tok * a.G : 0)) * D;
-          Partial<S::kRows, D>* part = partial_of<S::kRows, D>(a, max(part_slot, 0));
+          auto* part = partial_of<PartialByEights<S::kRows, D>>(a, max(part_slot, 0));
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t y[32];
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
               st_sector(dst + 32 * c + 16, z + 8);
             } else if (live) {
 #pragma unroll
-              for (int v = 0; v < 4; ++v) st_sector(&part->o[row][32 * c + 8 * v], y + 8 * v);
+              for (int v = 0; v < 4; ++v) st_sector(part->o[4 * c + v][row], y + 8 * v);
             }
             __syncwarp();
           }
@@ -1047,7 +1047,7 @@ static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
   static_assert(S::kSmem + (F8 ? 2048 : 1024) <= 227 * 1024, "a CTA fits an SM");
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
-  constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - partials_offset()) / (2 * sizeof(Partial<S::kRows, D>)));
+  constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - partials_offset()) / (2 * sizeof(PartialByEights<S::kRows, D>)));
   const int grid = std::max(1, std::min({cfg.num_sms, kFit, kMaxCtas}));
   const int per = S::kRows / a.G;   // tokens of an item
   // Bulk copies bring `box` rows at once: a block, or 128 rows of a longer one.
@@ -1062,7 +1062,7 @@ static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
   }
   e = launch_ex(kern, dim3(grid), dim3(prompt::kThreads), S::kSmem, cfg.stream, cfg.pdl, a, per, box, map);
   if (e != cudaSuccess) return e;
-  return launch_ex(attend_join_rows_kernel<T, S::kRows, D>, dim3(grid, 32), dim3(kJoinThreads), 0, cfg.stream,
+  return launch_ex(attend_join_rows_kernel<T, S::kRows, D, true>, dim3(grid, 32), dim3(kJoinThreads), 0, cfg.stream,
                    cfg.pdl, a);
 }
 
