@@ -97,7 +97,7 @@ struct Shape {
   // A tile's mask is written when its K has a place, that is once load 2 t - kRing has been released; the mask it
   // replaces has been read once V of tile t - kMaskRing, load 2 (t - kMaskRing) + 1, has been released.
   static_assert(2 * kMaskRing >= kRing + 1, "a mask is read before its place is used again");
-  static constexpr size_t kSmem = 1024 + kQBytes + kRing * (size_t)kTileBytes + kRaw * (size_t)kRawBytes + 128 * 8;
+  static constexpr size_t kSmem = 1024 + kQBytes + kRing * (size_t)kTileBytes + kRaw * (size_t)kRawBytes + (F8 ? 2 : 1) * 128 * 8;
   static constexpr uint32_t kOCol = 256;                      // first column of O_A; O_B follows D columns on
 };
 
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     mbar_init(smem_addr(&bars.done), 1);
     mbar_init(smem_addr(&bars.v_tail), 1);
     for (int i = 0; i < S::kRing; ++i) {
-      mbar_init(smem_addr(&bars.kv_full[i]), 1);
+      mbar_init(smem_addr(&bars.kv_full[i]), F8 ? kLoaders / 32 : 1);
       mbar_init(smem_addr(&bars.kv_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -661,42 +661,54 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             const int tok = (int)((uint32_t)row * g_inv >> 16);
             return row < rows ? src + tok * a.q_stride + (row - tok * a.G) * (D * 2) : src;
           };
-          if constexpr (!kShift) {
 #pragma unroll 8
-            for (int row = lt / C; row < S::kRows; row += RP)
-              cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), from(row), row < rows);
-            cp_async_commit();
-            cp_async_wait<0>();
-          } else {
-            // bf16 to fp16: the C lanes of a row scale it by a power of two that brings its largest element to
-            // [2^14, 2^15), and leave the inverse for the softmax.
-            constexpr int N = 4;
-            for (int r0 = 0; r0 < S::kRows; r0 += N * RP) {
-              uint4 x[N];
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const int row = r0 + i * RP + lt / C;
-                x[i] = row < rows ? *reinterpret_cast<const uint4*>(from(row)) : make_uint4(0, 0, 0, 0);
-              }
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const int row = r0 + i * RP + lt / C;
-                float f[8], big = 0.f;
-                Vec<__nv_bfloat16>::unpack(x[i], f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
-#pragma unroll
-                for (int d = C / 2; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+          for (int row = lt / C; row < S::kRows; row += RP)
+            cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), from(row), row < rows);
+          cp_async_commit();
+          cp_async_wait<0>();
+          if constexpr (kShift) {
+            // bf16 to fp16, in place: a thread scales a row by a power of two that brings its largest element to
+            // [2^14, 2^15), and leaves the inverse for the softmax.  (A row to 16 lanes, with shuffles for the largest:
+            // 5 us an item, 82 us for the 16 requests' prompts over FP8 where this takes 72.)
+            barrier_loaders();                         // the others' chunks have landed
+            for (int row = lt; row < S::kRows; row += kLoaders) {
+              float down = 1.f;
+              if (row < rows) {
+                const uint32_t tile = tiles0 + (row >> 7) * S::kTileBytes;
+                __nv_bfloat162 big(0.f, 0.f);
+                auto larger = [&](uint32_t w) {
+                  w &= 0x7fff7fffu;
+                  big = __hmax2(big, *reinterpret_cast<const __nv_bfloat162*>(&w));
+                };
+#pragma unroll 4
+                for (int k = 0; k < C; ++k) {
+                  const uint4 x = ld_shared_v4(tile + at_chunk<D>(row & 127, k));
+                  larger(x.x);
+                  larger(x.y);
+                  larger(x.z);
+                  larger(x.w);
+                }
+                const float most = fmaxf(__low2float(big), __high2float(big));
                 const int shift =
-                    big > 0.f && big < INFINITY ? min(14 - (int)(((__float_as_uint(big) >> 23) & 255u) - 127), 120) : 0;
+                    most > 0.f && most < INFINITY ? min(14 - (int)(((__float_as_uint(most) >> 23) & 255u) - 127), 120) : 0;
                 const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+                down = __uint_as_float((uint32_t)(127 - shift) << 23);
+#pragma unroll 1
+                for (int k0 = 0; k0 < C; k0 += 4) {
+                  uint4 x[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] *= up;
-                if (row < S::kRows) {
-                  st_shared_v4(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, c), Vec<__half>::pack(f));
-                  if (c == 0) s_unscale[row] = __uint_as_float((uint32_t)(127 - shift) << 23);
+                  for (int k = 0; k < 4; ++k) x[k] = ld_shared_v4(tile + at_chunk<D>(row & 127, k0 + k));
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    float f[8];
+                    Vec<__nv_bfloat16>::unpack(x[k], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] *= up;
+                    st_shared_v4(tile + at_chunk<D>(row & 127, k0 + k), Vec<__half>::pack(f));
+                  }
                 }
               }
+              s_unscale[row] = down;
             }
           }
           fence_proxy_async_smem();
@@ -735,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         if (box > 0) look_up_groups(0);
         else look_up(0);
         // Byte offsets of the tile's keys, for the row copies; -1: no such key.  Returns this thread's keys' mask words.
-        auto find_rows = [&](int j, uint32_t(&named)[2]) {
+        auto find_rows = [&](int j, long long* off, uint32_t(&named)[2]) {
           long long at_key[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -743,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             at_key[e] = id[e] < 0 ? -1ll : ((long long)id[e] * a.block_size + (p - block_of(a, p) * a.block_size)) * token_bytes;
             named[e] = __ballot_sync(0xffffffffu, at_key[e] >= 0);
           }
-          s_off[lt] = at_key[0];
-          if (lt < kKeys - kLoaders) s_off[lt + kLoaders] = at_key[1];
+          off[lt] = at_key[0];
+          if (lt < kKeys - kLoaders) off[lt + kLoaders] = at_key[1];
         };
         bool here = true;                              // this thread's waits
         auto room = [&](uint32_t n) {                  // the ring's place of load n is free
@@ -753,27 +765,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           return here;
         };
         if constexpr (F8) {
-          // Loads K0, V0, K1, ...: copied as bytes three loads ahead, then each thread widens the chunks that it copied.
+          // Loads K0, V0, K1, ...: copied as bytes kRaw - 1 loads ahead, then each thread widens the chunks that it copied,
+          // so that the three warps meet once a tile only, over the keys' offsets and bits: two tiles' offsets are kept,
+          // and a tile's are written when all have passed the tile before it.
           constexpr int C = D / 16, RP = kLoaders / C, N = (kKeys + RP - 1) / RP;   // 16-byte chunks of a row, rows of a pass
+          constexpr int kAhead = 6;
           const int c = lt % C, row0 = lt / C, n_loads = 2 * n_tiles;
           const uint32_t raw0 = ring0 + S::kRing * S::kTileBytes + (uint32_t)row0 * D + c * 16;
           auto copy_raw = [&](int i) {
             if (i < n_loads) {
               const int j = i >> 1;
+              const long long* off = s_off + (j & 1) * kKeys;
               if ((i & 1) == 0) {
-                agreed(true);                          // the last tile's offsets have been read
                 uint32_t named[2];
-                find_rows(j, named);
+                find_rows(j, s_off + (j & 1) * kKeys, named);
                 if (lane == 0) s_raw_mask[j % S::kRaw][warp - kLoaderWarp] = named[0];
                 if (lt == 0) s_raw_mask[j % S::kRaw][3] = named[1];
                 look_up(j + 1);
-                barrier_loaders();
+                ok = agreed(here);
               }
               const uint8_t* src = kbase + ((i & 1) ? a.v_offset : 0) + c * 16;
               const uint32_t dst = raw0 + ((n_load + i) % S::kRaw) * S::kRawBytes;
               long long o[N];
 #pragma unroll
-              for (int k = 0; k < N; ++k) o[k] = row0 + k * RP < kKeys ? s_off[row0 + k * RP] : -1ll;
+              for (int k = 0; k < N; ++k) o[k] = row0 + k * RP < kKeys ? off[row0 + k * RP] : -1ll;
 #pragma unroll
               for (int k = 0; k < N; ++k)
                 if (row0 + k * RP < kKeys) cp_async16(dst + k * RP * D, src + (o[k] < 0 ? 0 : o[k]), o[k] >= 0);
@@ -784,33 +799,40 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           for (int i = 0; i < S::kRaw - 1; ++i) copy_raw(i);
           for (int i = 0; i < n_loads; ++i) {
             copy_raw(i + S::kRaw - 1);
+            if (!ok) break;
             const uint32_t n = n_load + i, slot = (n >> 1) % kMaskRing;
             here = room(n);
             cp_async_wait<S::kRaw - 1>();
             const uint32_t src = raw0 + (n % S::kRaw) * S::kRawBytes, dst = ring0 + (n % S::kRing) * S::kTileBytes;
+            // Some chunks are read before any is written: one at a time, each waits for the one before (the two long
+            // prompts over FP8: 669 us, not 611).
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-              const int row = row0 + k * RP;
-              if (row < kKeys) {
-                const uint4 x = ld_shared_v4(src + k * RP * D);
-                st_shared_v4(dst + at_chunk<D>(row, 2 * c), widen8(x.x, x.y));
-                st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), widen8(x.z, x.w));
+            for (int k0 = 0; k0 < N; k0 += kAhead) {
+              uint4 x[kAhead];
+#pragma unroll
+              for (int k = k0; k < k0 + kAhead && k < N; ++k)
+                if (row0 + k * RP < kKeys) x[k - k0] = ld_shared_v4(src + k * RP * D);
+#pragma unroll
+              for (int k = k0; k < k0 + kAhead && k < N; ++k) {
+                const int row = row0 + k * RP;
+                if (row < kKeys) {
+                  st_shared_v4(dst + at_chunk<D>(row, 2 * c), widen8(x[k - k0].x, x[k - k0].y));
+                  st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), widen8(x[k - k0].z, x[k - k0].w));
+                }
               }
             }
             if ((i & 1) == 0 && lt < 4) s_mask[slot][lt] = s_raw_mask[(i >> 1) % S::kRaw][lt];
             fence_proxy_async_smem();
-            ok = agreed(here);
-            if (!ok) break;
-            if (lt == 0) {
-              if ((i & 1) == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
-              mbar_arrive(smem_addr(&bars.kv_full[n % S::kRing]));
-            }
+            __syncwarp();
+            if (lt == 0 && (i & 1) == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
+            if (lane == 0) mbar_arrive(smem_addr(&bars.kv_full[n % S::kRing]));
             if (i == 0) {
               load_q();
               if (!ok) break;
             }
           }
           n_load += n_loads;
+          ok = ok && agreed(here);
           if (!ok) break;
           continue;
         }
@@ -874,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           ok = agreed(room(n_load));                   // and the last tile's offsets have been read
           if (!ok) break;
           uint32_t named[2];
-          find_rows(j, named);
+          find_rows(j, s_off, named);
           if (lane == 0) s_mask[slot][warp - kLoaderWarp] = named[0];
           if (lt == 0) s_mask[slot][3] = named[1];
           look_up(j + 1);
