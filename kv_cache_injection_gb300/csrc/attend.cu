@@ -816,7 +816,7 @@ cudaError_t launch_attend(const AttendArgs& a, const LaunchCfg& cfg) {
   // with 4 new ones, 28 rows: 98 us here, 71 there; at head_dim 256, 16 rows: 176
   // and 97; 4 requests of up to 131,000 tokens, 32 rows: 528 and 273; a single
   // one of 1313: 18 and 21.  FP8 rows are widened faster here, so there they go
-  // from 33 on (32 rows, 64 requests of 500-8000 tokens: 257 and 336 us).
+  // from 33 on (32 rows, 64 requests of 500-8000 tokens: 258 and 295 us).
   // Maxima there are of unscaled logits, so the scale has to be positive.
   const int most = a.fp8 ? 32 : a.D == 256 ? 8 : 16;
   if (a.dtype != IS_F32 && (a.D <= 128 || !a.fp8) && a.G <= 64 && (int64_t)a.max_q * a.G > most && a.scale > 0.f)

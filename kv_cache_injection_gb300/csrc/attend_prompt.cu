@@ -44,10 +44,12 @@
 // of the loaded bytes 8 %: shared memory feeds the MMAs (S alone reads 128
 // bytes a clock) while it takes in the next tiles, and a tile's next S waits
 // for its softmax (1400 clocks) and the other tile's products.  16 requests with
-// 20-100 new tokens over 900-2000: 57 us; the start and end of an item (its first
+// 20-100 new tokens over 900-2000: 54 us; the start and end of an item (its first
 // tiles, 64 KB of output or 128 KB of partial) cost as much as about six key
-// tiles.  One request, 100 new tokens over 400: 22 us, the latency of this kernel
-// (1 us to its run, 4 to the first S, 2 for the tiles, 3.5 of output) and the join.
+// tiles.  One request, 100 new tokens over 400: 20 us, the latency of this kernel
+// (1 us to its run, 4 to the first S, 2 for the tiles, 2 of output) and the join.
+// Over an FP8 cache the two long prompts take 569 us, 0.95 PFLOP/s: the three
+// loader warps that widen the rows are the limit.
 #include <cuda.h>
 
 #include <algorithm>
