@@ -45,7 +45,7 @@
 // tokens 264 us, 6.8 TB/s, the rate of a plain copy; 64 requests of 500-8000
 // tokens 170 us (6.3 TB/s), with an FP8 cache 101 us (5.3 TB/s, where the
 // conversions fill 44 % of the issue slots); 100 requests of 300-2048 tokens
-// (H = 4) 46.6 us against 34.3 for their bytes, the rest being the start
+// (H = 4) 46.2 us against 34.3 for their bytes, the rest being the start
 // (2 us to find the runs, 3 more until the first tile has landed), the last
 // tiles and the join.
 #include <algorithm>

@@ -37,7 +37,7 @@
 // B's place.
 //
 // Measured (H = 8, G = 4, D = 128, bf16): two prompts of 2000-2500 tokens
-// behind up to 8192, 538 GFLOP, 396 us = 1.36 PFLOP/s, 71 % of the burst rate of
+// behind up to 8192, 538 GFLOP, 392 us = 1.37 PFLOP/s, 72 % of the burst rate of
 // a plain library product.  128 keys of a pair of tiles are 2048 clocks of MMAs
 // (64 each for M 128, N 128, K 16) and take 2900.  Leaving out the exponentials
 // changes nothing; half the S products save 3 %, half the O products 2 %, half
