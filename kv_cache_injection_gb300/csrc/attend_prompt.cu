@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   if (tid == 0) {
     s_abort = 0;
     mbar_init(smem_addr(&bars.q_full), kLoaders);
-    mbar_init(smem_addr(&bars.q_empty), 1);
+    mbar_init(smem_addr(&bars.q_empty), kShift ? 9 : 1);   // the last logits; eight softmax warps that read s_unscale
     mbar_init(smem_addr(&bars.done), 1);
     mbar_init(smem_addr(&bars.v_tail), 1);
     for (int i = 0; i < S::kRing; ++i) {
@@ -438,6 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           if (!wait(&bars.q_full, n_q & 1u)) break;
           ++n_q;
           sc = fmaxf(sc0 * s_unscale[row], FLT_MIN);
+          // A segment of one tile may have its logits before these warps, still at the last one's output, come here:
+          // the next query rows' factors, and the next phase of q_full, have to wait for them.
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&bars.q_empty));
         }
         if (!has) n_mask += n_tiles;
         for (int j = 0, key0 = g.k_lo; has && j < n_tiles; ++j, ++n_mask, key0 += kKeys) {

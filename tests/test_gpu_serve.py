@@ -515,6 +515,38 @@ def test_rows_of_any_magnitude(rows, cache):
         assert bool(((lse.cpu().double() - ls).abs() <= ltol)[:, use].all()) and status.tolist() == [0]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_short_prompts_of_different_magnitudes(D, dtype):
+    """Items of one or two key tiles behind one another in a CTA, over an FP8 cache, each request's query rows of
+    a magnitude of their own."""
+    g = torch.Generator().manual_seed(5)
+    R, H, Hq, bs, m, n, sc = 1200, 1, 4, 16, 20, 128, SCALES["e4m3"]
+    nb = R * (n // bs)
+    store = nan_cache((2, nb, bs, H, D), "e4m3")
+    flat = store.view(2, nb * bs, H, D)
+    x = []
+    for i in range(2):
+        flat[i] = quantise(torch.randn(nb * bs, H, D, generator=g), "e4m3", sc[i])
+        x.append(ref.stored_values("e4m3", flat[i]) * sc[i])
+    table = torch.arange(nb, dtype=torch.int32).reshape(R, n // bs)
+    size = 2.0 ** ((torch.arange(R) * 5) % 8 - 7).double()          # 2^-7 .. 1
+    q = (torch.randn(R * m, Hq, D, generator=g) * size.repeat_interleave(m)[:, None, None]).to(ref.TORCH[dtype])
+    out, lse, status = torch.empty_like(q, device=DEV), torch.empty(R * m, Hq, device=DEV), ints([0])
+    api.is_attend(q.to(DEV), ints([n] * R), table.to(DEV), api.make_cache_desc(bs, nb, "e4m3", *sc), store.to(DEV), out,
+                  api.attend_workspace(), status, q_start=ints([m * r for r in range(R + 1)]), max_q_len=m, scale=D ** -0.5,
+                  lse_out=lse)
+    assert status.tolist() == [0]
+    out, lse = out.cpu().double(), lse.cpu().double()
+    for r in range(R):
+        rows, keys = slice(m * r, m * r + m), slice(n * r, n * r + n)
+        k, v = x[0][keys], x[1][keys]
+        o, ls, spread, heft, seen = ref.attend(q[rows].double(), n, k, v, torch.ones(n, dtype=torch.bool), D ** -0.5, 0)
+        tol, ltol = ref.attend_tolerance(dtype, "e4m3", D, o, ls, spread, heft, seen, float(v.abs().max()))
+        assert bool(((out[rows] - o).abs() <= tol).all()), r
+        assert bool(((lse[rows] - ls).abs() <= ltol).all()), r
+
+
 def test_thousands_of_requests():
     attend_case([(1 + (53 * r) % 40, (r * 7) % 3) for r in range(2500)], 2, 1, 64, "bf16", "bf16")
     attend_case([(1 + (53 * r) % 40, (r * 7) % 19) for r in range(600)], 4, 1, 64, "f16", "f16")
