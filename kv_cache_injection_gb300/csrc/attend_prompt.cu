@@ -721,13 +721,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           mbar_arrive(smem_addr(&bars.q_full));
         };
         // Bulk copies: lane g of each warp finds the token of row group g (`box` rows) of a tile, one tile ahead; -1 if
-        // it has no key or the table does not name it (the copy then starts behind the cache and reads zeros).
+        // it has no key that a row sees (the blocks before a window may be gone from the table) or the table does not
+        // name it (the copy then starts behind the cache and reads zeros).
         const int groups = box > 0 ? kKeys / box : 0;
         int64_t token = -1;
         auto look_up_groups = [&](int j) {
           const int key0 = k_lo + j * kKeys, p = key0 + lane * box;
           token = -1;
-          if (lane < groups && j < n_tiles && p < k_hi) {
+          if (lane < groups && j < n_tiles && p + box > k_see && p < k_hi) {
             const int b = block_of(a, p);
             const int32_t id = table[b];
             if (id >= 0 && id < a.num_blocks) token = (int64_t)id * a.block_size + (p - b * a.block_size);

@@ -1,0 +1,58 @@
+"""The serving step's calls at their edges, against the plain 64-bit definitions."""
+import pytest
+import torch
+
+from kv_cache_injection_gb300 import _lib, api
+from tests import gpu_helpers as gh
+from tests import serve_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TYPES = [("bf16", "bf16"), ("f16", "f16"), ("f32", "f32"), ("bf16", "e4m3"), ("f16", "e4m3")]
+SCALES = {"e4m3": (0.02, 0.05)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    gh.ensure_built()
+
+
+def ints(x, dtype=torch.int32):
+    return torch.tensor(x, dtype=dtype, device=DEV)
+
+
+def stored(x, cache, scale):
+    """x as the cache holds it, and the fp64 values that stands for."""
+    if cache == "e4m3":
+        x = (x / scale).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        x = x.to(ref.TORCH[cache])
+    return x, ref.stored_values(cache, x) * scale
+
+
+# ---------------------------------------------------------------- blocks freed behind a window
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("bs", [8, 16, 24, 128])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_blocks_before_the_window_need_no_name(D, bs, dtype, cache):
+    """An engine takes back the blocks that lie before every row's window and leaves -1, or an id of no block, in the
+    table: single tokens and prompts answer as if they were there, and report nothing."""
+    g = torch.Generator().manual_seed(21)
+    H, Hq, n, sc = 2, 8, 700, SCALES.get(cache, (1.0, 1.0))
+    nb = -(-n // bs)
+    for rows, window in ((1, 90), (1, 300), (20, 250), (70, 5), (200, 40)):
+        kv = [stored(torch.randn(nb * bs, H, D, generator=g), cache, sc[i]) for i in range(2)]
+        lc = torch.stack([s for s, _ in kv]).view(2, nb, bs, H, D)
+        table = torch.arange(nb, dtype=torch.int32)
+        first = n - rows - window + 1                  # the first position that a row sees
+        table[: first // bs: 2], table[1: first // bs: 2] = -1, nb + 5
+        q = torch.randn(rows, Hq, D, generator=g).to(ref.TORCH[dtype])
+        out, lse, status = torch.empty_like(q, device=DEV), torch.empty(rows, Hq, device=DEV), ints([0])
+        api.is_attend(q.to(DEV), ints([n]), table[None].to(DEV), api.make_cache_desc(bs, nb, cache, *sc), lc.to(DEV), out,
+                      api.attend_workspace(), status, q_start=ints([0, rows]), max_q_len=rows, window=window, lse_out=lse)
+        k, v = (x[:n] for _, x in kv)
+        o, ls, spread, heft, seen = ref.attend(q.double(), n, k, v, torch.ones(n, dtype=torch.bool), D ** -0.5, window)
+        tol, ltol = ref.attend_tolerance(dtype, cache, D, o, ls, spread, heft, seen, float(v.abs().max()))
+        assert status.tolist() == [0], (rows, window)
+        assert bool(((out.cpu().double() - o).abs() <= tol).all()) and bool(((lse.cpu().double() - ls).abs() <= ltol).all())
