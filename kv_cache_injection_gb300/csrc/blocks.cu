@@ -194,9 +194,12 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
     if (t < end && a.positions_out) a.positions_out[t] = pos[i];
   }
 
-  // Table entries: the blocks taken are the free list's next s_used, one thread each.
+  // Table entries: the blocks taken are the free list's next s_used, one thread each.  (64-bit steps: slot maps of
+  // almost 2^31 entries have 2^31 threads.)
   const int32_t all_used = s_used;
-  for (int32_t i = blockIdx.x * kExtendThreads + tid; i < all_used; i += gridDim.x * kExtendThreads) {
+  const int64_t threads = (int64_t)gridDim.x * kExtendThreads, me = (int64_t)blockIdx.x * kExtendThreads + tid;
+  for (int64_t i64 = me; i64 < all_used; i64 += threads) {
+    const int32_t i = (int32_t)i64;
     int lo = 0, hi = R;                  // last request with at most i blocks taken before it: the one that takes block i
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -206,7 +209,8 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const is_extend_
         a.free_blocks[head + i];
   }
   // Per-request outputs.
-  for (int r = blockIdx.x * kExtendThreads + tid; r < R; r += gridDim.x * kExtendThreads) {
+  for (int64_t r64 = me; r64 < R; r64 += threads) {
+    const int r = (int)r64;
     const int32_t n = s_seq[at(r)];
     if (a.seq_len_out) a.seq_len_out[r] = n >= 0 ? n + a.new_len[r] : a.seq_len[r];
     if (a.token_start_out) {

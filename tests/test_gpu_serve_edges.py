@@ -56,3 +56,24 @@ def test_blocks_before_the_window_need_no_name(D, bs, dtype, cache):
         tol, ltol = ref.attend_tolerance(dtype, cache, D, o, ls, spread, heft, seen, float(v.abs().max()))
         assert status.tolist() == [0], (rows, window)
         assert bool(((out.cpu().double() - o).abs() <= tol).all()) and bool(((lse.cpu().double() - ls).abs() <= ltol).all())
+
+
+# ---------------------------------------------------------------- the largest slot map
+
+@pytest.mark.parametrize("requests", [3, 600])
+def test_slot_map_of_2_31_entries(requests):
+    """The largest slot map that max_tokens can name (17 GB), nearly all of it padding: the kernel has as many threads."""
+    bs, cap = 16, (1 << 31) - 1
+    lens, news = [7 * r % 50 for r in range(requests)], [1 + 5 * r % 40 for r in range(requests)]
+    need = [-(-(n + m) // bs) for n, m in zip(lens, news)]
+    have = [-(-n // bs) for n in lens]
+    ids = list(range(sum(need) + 3))[::-1]
+    table = [[ids.pop() if j < have[r] else -1 for j in range(7)] for r in range(requests)]
+    want = ref.extend(lens, news, ids, 0, table, bs, len(ids) + sum(have), sum(news))
+    t, status, head = ints(table), ints([0]), ints([-9])
+    slots = torch.full((cap,), -9, dtype=torch.int64, device=DEV)
+    api.is_extend_block_table(ints(lens), ints(news), ints(ids), bs, len(ids) + sum(have), t, slots, status_out=status,
+                              free_head_out=head)
+    assert t.tolist() == want[0] and head.tolist() == [want[5]] and status.tolist() == [0]
+    assert slots[: sum(news)].tolist() == want[1]
+    assert all(bool((slots[i: i + (1 << 28)] == -1).all()) for i in range(sum(news), cap, 1 << 28))
