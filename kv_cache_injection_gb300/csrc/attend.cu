@@ -32,8 +32,8 @@
 //   nothing here: the SMs issue in a fifth of their slots (bf16) while the
 //   memory is the limit.
 // - The maximum moves only when a logit passes it by more than 2^8 (in the
-//   base-2 exponent): the weights stay below 2^8, far from overflow in bf16
-//   and fp16, and the usual tile costs one vote instead of a reduction.
+//   base-2 exponent), so the usual tile costs one vote instead of a reduction;
+//   fp16 weights are raised by 2^7 (see kRaise).
 //
 // Sums, maxima and O are fp32; the weights are rounded to 16 bits for the
 // second product (relative 2^-8 or 2^-11, like the output).  FP8 keys and
@@ -234,6 +234,11 @@ struct MmaEngine {
     }
     // Scaled logits (base 2), hidden keys at -inf.
     bool over = false;
+    float bound[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) bound[nt][i] = lazy_bound<M>(m[nt][i]);
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
@@ -248,7 +253,7 @@ struct MmaEngine {
             if (!see) x = -INFINITY;
           }
           s[mt][nt][e] = x;
-          over |= x > m[nt][e & 1] + kLazy;
+          over |= x > bound[nt][e & 1];
         }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -261,7 +266,7 @@ struct MmaEngine {
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          const float mn = fmaxf(m[nt][i], x);
+          const float mn = fmaxf(m[nt][i], x - kRaise<M>);
           const float f = mn == -INFINITY ? 1.f : ex2(m[nt][i] - mn);
           m[nt][i] = mn;
           l[nt][i] *= f;
@@ -412,7 +417,7 @@ struct FmaEngine {
       s[i] *= sc;
       const int j = tm.key0 + key;
       if (tm.check && !(((tm.valid >> key) & 1u) && j <= lim[i] && (a.window == 0 || j > lim[i] - a.window))) s[i] = -INFINITY;
-      over |= s[i] > m[i] + kLazy;
+      over |= s[i] > lazy_bound<float>(m[i]);
     }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll

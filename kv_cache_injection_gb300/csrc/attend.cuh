@@ -12,7 +12,24 @@ namespace isk {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.f;             // how far a logit may pass the maximum in use
+
+// The reference m of a row, in the base-2 exponent: a weight is 2^(x - m), and m
+// moves only when a logit passes it by more than kLazy + kRaise, to kRaise
+// below that logit.  So the largest weight is at least 2^kRaise and none passes
+// 2^(kLazy + kRaise).  fp16 weights are raised by 7, to 2^15 at most (fp16 ends
+// at 65504): the faintest steps, 2^-24, are then 2^-31 of the largest weight, and
+// weights keep 11 bits down to 2^-21 of it.  (Unraised, of what 2999 keys at
+// 2^-26 add beside a strong one, such as a prompt's first token, a seventh to
+// a fifth was lost.)  bf16 and fp32 have the exponents.
+constexpr float kLazy = 8.f;
+template <typename M>
+constexpr float kRaise = std::is_same<M, __half>::value ? 7.f : 0.f;
+// What a logit has to pass to move m; rounded down, so that it holds where a
+// step of m is larger than the bound.
+template <typename M>
+__device__ __forceinline__ float lazy_bound(float m) {
+  return __fadd_rd(m, kLazy + kRaise<M>);
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");

@@ -28,7 +28,7 @@
 // the call and every CTA of a persistent grid (one per SM) takes one run of
 // them, so ragged and causal batches are balanced; items cut by a run's end
 // are joined from the workspace.  The running maximum moves only when a logit
-// passes it by 2^8; moving it rescales O in tensor memory, which the wait for
+// passes it by 2^8 (see kRaise); moving it rescales O in tensor memory, which the wait for
 // S already made safe: the MMA thread issued the previous O += P V before it.
 // Every wait is bounded (2 s): on time-out the CTA latches IS_ST_TIMEOUT,
 // lets its own work in flight end, frees its tensor memory and returns.
@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             hide(x[3], mw.w, key0 + 96);
           }
           mx = fmaxf(mx, fmaxf(top(x[2]), top(x[3]))) * sc;   // sc > 0
-          if (__any_sync(0xffffffffu, mx > m + kLazy)) {
-            const float mn = fmaxf(m, mx);
+          if (__any_sync(0xffffffffu, mx > lazy_bound<W>(m))) {
+            const float mn = fmaxf(m, mx - kRaise<W>);
             const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
             m = mn;
             l *= f;

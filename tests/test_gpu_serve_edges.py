@@ -77,3 +77,43 @@ def test_slot_map_of_2_31_entries(requests):
     assert t.tolist() == want[0] and head.tolist() == [want[5]] and status.tolist() == [0]
     assert slots[: sum(news)].tolist() == want[1]
     assert all(bool((slots[i: i + (1 << 28)] == -1).all()) for i in range(sum(news), cap, 1 << 28))
+
+
+# ---------------------------------------------------------------- faint weights
+
+@pytest.mark.parametrize("rows", [1, 20])
+@pytest.mark.parametrize("dtype,cache", [("f16", "f16"), ("bf16", "e4m3"), ("f16", "e4m3")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_faint_weights_beside_a_strong_one(D, dtype, cache, rows):
+    """A first key that takes nearly all weight and whose value is 0: the output is what the other 2999 keys add, each
+    with about 2^-26 of the first one's weight.  Weights are kept in fp16 with at least 2^7 for the largest, so that
+    a step of the smallest ones is 2^-24, half of it 2^-32 of the largest: that times |v| a key is the bound on what
+    their rounding may change."""
+    g = torch.Generator().manual_seed(31)
+    H, Hq, n, bs, R, sc = 1, 4, 3000, 16, 600 if rows == 1 else 64, SCALES.get(cache, (1.0, 1.0))
+    nb = -(-n // bs)
+    k = 0.3 * torch.randn(nb * bs, H, D, generator=g) * (64 / D) ** 0.5
+    k[:, :, 0] = 0.0
+    k[0] = 0.0
+    k[0, :, 0] = 2.28125
+    v = 1.0 + 0.2 * torch.randn(nb * bs, H, D, generator=g)
+    v[0] = 0.0
+    (ks, k), (vs, v) = stored(k, cache, sc[0]), stored(v, cache, sc[1])
+    k, v = k[:n], v[:n]
+    q = 0.25 * torch.randn(R * rows, Hq, D, generator=g)
+    q[:, :, 0] = 8.0
+    q = q.to(ref.TORCH[dtype])
+    out, lse, status = torch.empty_like(q, device=DEV), torch.empty(R * rows, Hq, device=DEV), ints([0])
+    api.is_attend(q.to(DEV), ints([n] * R), torch.arange(nb, dtype=torch.int32).repeat(R, 1).to(DEV),
+                  api.make_cache_desc(bs, nb, cache, *sc), torch.stack([ks, vs]).view(2, nb, bs, H, D).to(DEV), out,
+                  api.attend_workspace(), status, q_start=ints([rows * r for r in range(R + 1)]), max_q_len=rows, scale=1.0,
+                  lse_out=lse)
+    assert status.tolist() == [0]
+    out, lse = out.cpu().double(), lse.cpu().double()
+    for r in range(0, R, 1 if rows == 1 else 4):
+        mine = slice(rows * r, rows * (r + 1))
+        o, ls, spread, heft, seen = ref.attend(q[mine].double(), n, k, v, torch.ones(n, dtype=torch.bool), 1.0, 0)
+        tol, ltol = ref.attend_tolerance(dtype, cache, D, o, ls, spread, heft, seen, float(v.abs().max()) * 2.0 ** -7)
+        err = (out[mine] - o).abs()
+        assert bool((err <= tol).all()), (r, float((err / tol).max()), float((err / o.abs()).max()))
+        assert bool(((lse[mine] - ls).abs() <= ltol).all())
