@@ -245,7 +245,7 @@ struct MmaEngine {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float x = s[mt][nt][e] * sc[nt][e & 1];
+          float x = __fmul_rn(s[mt][nt][e], sc[nt][e & 1]);   // not fused with - m: far logits
           if (tm.check) {
             const int key = mt * 16 + (lane >> 2) + (e >> 1) * 8, j = tm.key0 + key;
             const bool see = ((tm.valid >> key) & 1u) && j <= lim[nt][e & 1] &&
@@ -414,7 +414,7 @@ struct FmaEngine {
     bool over = false;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      s[i] *= sc;
+      s[i] = __fmul_rn(s[i], sc);         // not fused with - m: far logits
       const int j = tm.key0 + key;
       if (tm.check && !(((tm.valid >> key) & 1u) && j <= lim[i] && (a.window == 0 || j > lim[i] - a.window))) s[i] = -INFINITY;
       over |= s[i] > lazy_bound<float>(m[i]);

@@ -80,6 +80,11 @@ constexpr int kMinRun = 2;
 // an item counts as so many more, before its first.
 constexpr int kItemCost = 6;
 constexpr int kMaskRing = 8;
+// The exponents are x * sc - m in one rounding, so that they keep the error of
+// the product that m was rounded by: half a step of m.  That passes a weight's
+// range where m is past 2^24 (fp16) or 2^30: past this, far_weights rounds the
+// product first, as it was for m.
+constexpr float kFar = 4194304.f;
 constexpr uint32_t kTmemAll = 512;
 
 template <int D, bool F8>
@@ -317,6 +322,42 @@ __device__ __forceinline__ uint32_t at_chunk(int row, int c) {
          (uint32_t)(((c & 7) ^ (row & 7)) * 16);
 }
 
+// The weights of a tile with rows past kFar: S (logits before their scale) once
+// more from tensor memory, weights over it and their sum added to l.  Of 32
+// logits S is read before the 16 columns of their weights, which lie before the
+// next ones', are written.  A function of its own, since inside the loop it costs
+// the other rows registers: the long prompts take 403 us instead of 392.
+template <typename W>
+__device__ __noinline__ float far_weights(uint32_t s_col, float sc, float m, float l, uint4 named, int key0, int low, int end,
+                                          uint32_t p_full, int lane) {
+  const float mz = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t y[32], p[16];
+    tmem_ld32(s_col + 32 * c, y);
+    tmem_wait_ld();
+    const uint32_t word = c == 0 ? named.x : c == 1 ? named.y : c == 2 ? named.z : named.w;
+    const uint32_t see = word & bits_between(key0 + 32 * c, low, end);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float w[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        w[e] = (see >> (2 * i + e)) & 1u ? ex2(__fsub_rn(__fmul_rn(__uint_as_float(y[2 * i + e]), sc), mz)) : 0.f;
+      l += w[0] + w[1];
+      p[i] = Vec<W>::pack2(w[0], w[1]);
+    }
+    tmem_st16(s_col + 16 * c, p);
+    tmem_wait_st();
+    if (c & 1) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + 8 * (c >> 1));
+    }
+  }
+  return l;
+}
+
 template <typename T, bool F8, int D>
 __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a, int per, int box,
                                                                    const __grid_constant__ CUtensorMap rows_map) {
@@ -483,8 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             hide(x[2], mw.z, key0 + 64);
             hide(x[3], mw.w, key0 + 96);
           }
-          mx = fmaxf(mx, fmaxf(top(x[2]), top(x[3]))) * sc;   // sc > 0
-          if (__any_sync(0xffffffffu, mx > lazy_bound<W>(m))) {
+          mx = __fmul_rn(fmaxf(mx, fmaxf(top(x[2]), top(x[3]))), sc);   // sc > 0
+          // A logit past the bound moves m; far rows come here with every tile.
+          if (__any_sync(0xffffffffu, mx > (fabsf(m) > kFar ? -INFINITY : lazy_bound<W>(m)))) {
             const float mn = fmaxf(m, mx - kRaise<W>);
             const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
             m = mn;
@@ -499,6 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
                 tmem_st16(o_col + 16 * c, y);
               }
+            }
+            if (__any_sync(0xffffffffu, fabsf(m) > kFar && m > -INFINITY)) {
+              l = far_weights<W>(s_col, sc, m, l, mw, key0, low, lim + 1, smem_addr(&bars.p_full[side][0]), lane);
+              continue;
             }
           }
           const float mz = m == -INFINITY ? 0.f : m;

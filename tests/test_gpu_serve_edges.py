@@ -117,3 +117,31 @@ def test_faint_weights_beside_a_strong_one(D, dtype, cache, rows):
         err = (out[mine] - o).abs()
         assert bool((err <= tol).all()), (r, float((err / tol).max()), float((err / o.abs()).max()))
         assert bool(((lse[mine] - ls).abs() <= ltol).all())
+
+# ---------------------------------------------------------------- logits without bounds
+
+@pytest.mark.parametrize("rows", [1, 5, 60])
+@pytest.mark.parametrize("dtype,cache,size", [("bf16", "bf16", 1e30), ("bf16", "e4m3", 1e30), ("f32", "f32", 1e30),
+                                              ("f16", "f16", 6e4), ("f16", "e4m3", 6e4), ("bf16", "bf16", 1e9)])
+def test_logits_past_every_step(dtype, cache, size, rows):
+    """Logits of 2^24 to 2^110, whose fp32 steps are larger than any softmax is wide.  One key's is positive and all
+    others' are negative, so that one takes all weight: the output is its value, rounded."""
+    g = torch.Generator().manual_seed(51)
+    H, Hq, D, n, bs, sc = 1, 4, 64, 400, 16, SCALES.get(cache, (1.0, 1.0))
+    nb = -(-n // bs)
+    big = 900.0 if cache == "f16" else 4.0
+    k = -big * torch.rand(nb * bs, H, D, generator=g)
+    k[17] = -k[17]
+    (ks, k), (vs, v) = stored(k, cache, sc[0]), stored(torch.randn(nb * bs, H, D, generator=g), cache, sc[1])
+    q = (size * (0.5 + 0.5 * torch.rand(rows, Hq, D, generator=g))).to(ref.TORCH[dtype])
+    out, lse, status = torch.empty_like(q, device=DEV), torch.empty(rows, Hq, device=DEV), ints([0])
+    api.is_attend(q.to(DEV), ints([n]), ints([list(range(nb))]), api.make_cache_desc(bs, nb, cache, *sc),
+                  torch.stack([ks, vs]).view(2, nb, bs, H, D).to(DEV), out, api.attend_workspace(), status,
+                  q_start=ints([0, rows]), max_q_len=rows, scale=1.0, lse_out=lse)
+    o, ls, spread, heft, seen = ref.attend(q.double(), n, k[:n], v[:n], torch.ones(n, dtype=torch.bool), 1.0, 0)
+    # The others' weights are exactly 0, so only the value's scale, its weight (1 over itself) and the output round.
+    tol = (ref.U[dtype] * 1.01 + 2.0 ** -20) * o.abs() + (2.0 ** -25 if dtype == "f16" else 0.0)
+    lse_tol = (D + 16) * 2.0 ** -24 * heft + 2.0 ** -22 * ls.abs()
+    assert status.tolist() == [0]
+    assert bool(((out.cpu().double() - o).abs() <= tol).all())
+    assert bool(((lse.cpu().double() - ls).abs() <= lse_tol).all())
