@@ -609,6 +609,14 @@ typedef struct {
 } is_attend_args_t;
 is_status_t is_attend(const is_attend_args_t* args, cudaStream_t stream);
 
+/* is_attend with the limit of each wait, 0 <= budget_ns <= 2 s, instead of the
+ * 2 s (see is_set_wait_budget, which does this for a store's calls).  With 0 a
+ * wait looks once and gives up at once, which is how the tests exercise the
+ * time-out path.  The waits that let copies in flight land before the kernel ends
+ * keep 2 s, and the kernel for few rows has none.
+ * Errors: those of is_attend; IS_ERR_INVALID_ARG for a budget outside that range. */
+is_status_t is_attend_within(const is_attend_args_t* args, int64_t budget_ns, cudaStream_t stream);
+
 /* ---- is_set_retrieval_mode -----------------------------------------------------
  * How the similarity is computed.  IS_RETRIEVAL_PER_QUERY: one launch in
  * which each query's CTAs stream its user's embedding tiles and the last CTA

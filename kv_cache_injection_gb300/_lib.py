@@ -130,6 +130,7 @@ SIGNATURES = {
     "is_extend_block_table": [POINTER(ExtendArgs), c_void_p],
     "is_append": [POINTER(AppendArgs), c_void_p],
     "is_attend": [POINTER(AttendArgs), c_void_p],
+    "is_attend_within": [POINTER(AttendArgs), c_int64, c_void_p],
     "is_get_status": [c_void_p, c_void_p, POINTER(c_uint32)],
     "is_last_error_message": [],
     "is_status_string": [c_int],

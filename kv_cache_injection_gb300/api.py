@@ -353,7 +353,7 @@ def _layer_cache(cache: CacheDesc, layer_cache, heads, dim, dtype: str, device):
     return _typed("layer_cache", layer_cache, dtype, (2, cache.num_blocks, cache.block_size, heads, dim), device)
 
 
-def _prepared(fn_name: str, args, keep, stream, device):
+def _prepared(fn_name: str, args, keep, stream, device, *more):
     """A callable that issues the call on the bound buffers (contents may change between calls)."""
     fn = getattr(_lib.load(), fn_name)
     ref = byref(args)
@@ -363,7 +363,7 @@ def _prepared(fn_name: str, args, keep, stream, device):
     st = c_void_p(_stream(stream))
 
     def call():
-        status = fn(ref, st)
+        status = fn(ref, *more, st)
         if status != _lib.IS_OK:
             _check(status)
     call.keep = (args, keep)                  # the struct and the bound tensors must outlive the callable
@@ -442,9 +442,11 @@ def attend_workspace(device=None):
 
 
 def prepare_attend(q, seq_len, block_table, cache: CacheDesc, layer_cache, out, workspace, status_out, q_start=None,
-                   max_q_len: int = 1, scale: float | None = None, window: int = 0, lse_out=None, stream=None):
+                   max_q_len: int = 1, scale: float | None = None, window: int = 0, lse_out=None, stream=None,
+                   budget_ns: int | None = None):
     """is_attend with every argument marshalled once.  q [T][Hq][D] may be a
-    view with any token stride; scale None: head_dim ** -0.5."""
+    view with any token stride; scale None: head_dim ** -0.5; budget_ns: the
+    limit of each wait (is_attend_within)."""
     dt, code = _float_code("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens][heads][head_dim]")
@@ -462,8 +464,10 @@ def prepare_attend(q, seq_len, block_table, cache: CacheDesc, layer_cache, out, 
                       float(D ** -0.5 if scale is None else scale), int(q.stride(0)), q.data_ptr(), _ptr(q_start),
                       _ptr(seq_len), _ptr(block_table), _ptr(layer_cache), _ptr(out), _ptr(lse_out), _ptr(workspace),
                       int(workspace.shape[0]), _ptr(_typed("status_out", status_out, "int32", (1,), dev)), cache, 0)
-    return _prepared("is_attend", args, (q, q_start, seq_len, block_table, layer_cache, out, lse_out, workspace,
-                                         status_out), stream, dev)
+    keep = (q, q_start, seq_len, block_table, layer_cache, out, lse_out, workspace, status_out)
+    if budget_ns is None:
+        return _prepared("is_attend", args, keep, stream, dev)
+    return _prepared("is_attend_within", args, keep, stream, dev, c_int64(budget_ns))
 
 
 def is_attend(*args, **kw) -> None:

@@ -30,8 +30,9 @@
 // are joined from the workspace.  The running maximum moves only when a logit
 // passes it by 2^8 (see kRaise); moving it rescales O in tensor memory, which the wait for
 // S already made safe: the MMA thread issued the previous O += P V before it.
-// Every wait is bounded (2 s): on time-out the CTA latches IS_ST_TIMEOUT,
-// lets its own work in flight end, frees its tensor memory and returns.
+// Every wait is bounded (2 s, or the call's limit): on time-out the CTA latches
+// IS_ST_TIMEOUT, lets its own work in flight end, for which it waits 2 s whatever
+// the limit, frees its tensor memory and returns.
 //
 // At head_dim 256 an item is one 128-row tile: O takes 256 columns, and tile
 // B's place.
@@ -358,10 +359,12 @@ __device__ __noinline__ float far_weights(uint32_t s_col, float sc, float m, flo
   return l;
 }
 
-template <typename T, bool F8, int D>
+// LIMITED: the limit of the waits is the call's.  (As a variable in the ordinary form it costs 16 prompts 1.2 us of 53.4.)
+template <typename T, bool F8, int D, bool LIMITED>
 __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a, int per, int box,
                                                                    const __grid_constant__ CUtensorMap rows_map) {
   using S = Shape<D, F8>;
+  const uint64_t limit_ns = LIMITED ? a.wait_ns : kWaitBudgetNs;
   // FP8 keys and values are exact in fp16, and so is a bf16 query row scaled by a power of two (undone in the logits):
   // with an FP8 cache both products are taken in fp16.
   using W = typename std::conditional<F8, __half, T>::type;
@@ -370,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   __shared__ __align__(8) Bars bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ uint32_t s_bulk[8];                       // of both loader warps' `bulk` the larger, after a time-out
   __shared__ __align__(16) uint32_t s_mask[kMaskRing][4];
   __shared__ uint32_t s_raw_mask[S::kRaw][4];
   __shared__ float s_unscale[kShift ? S::kRows : 1];
@@ -389,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   }
   if (tid == 0) {
     s_abort = 0;
+    for (int i = 0; i < 8; ++i) s_bulk[i] = 0;
     mbar_init(smem_addr(&bars.q_full), kLoaders);
     mbar_init(smem_addr(&bars.q_empty), kShift ? 9 : 1);   // the last logits; eight softmax warps that read s_unscale
     mbar_init(smem_addr(&bars.done), 1);
@@ -458,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       uint32_t n_s = 0, n_o = 0, n_mask = 0, n_q = 0;  // phases consumed
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, kWaitBudgetNs));
+        ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, limit_ns));
         return ok;
       };
       for (uint32_t n_seg = 0;; ++n_seg) {
@@ -633,10 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       constexpr int EB = F8 ? 1 : 2;
       const int64_t token_bytes = (int64_t)a.H * D * EB;
       uint32_t n_load = 0, n_q = 0, n_tail = 0;        // K and V tiles, query tiles, cleared V tiles
-      uint32_t bulk = 0;                               // lane i: 1 + this warp's last load into place i if that was a bulk copy
       uint32_t leader;
       asm volatile(
           "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
+      uint32_t bulk = 0;                               // lane i: 1 + this warp's last load into place i if that was a bulk copy
       bool ok = true;                                  // the same in all loaders once they have agreed()
       auto agreed = [&](bool mine_ok) {                // also a barrier of the three warps
         uint32_t r;
@@ -663,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       }
       for (uint32_t n_seg = 0;; ++n_seg) {
         const uint32_t seg = n_seg % kSegments;
-        ok = agreed(wait_or_abort(smem_addr(&bars.seg_empty[seg]), ((n_seg / kSegments) & 1u) ^ 1u, abort_flag, kWaitBudgetNs));
+        ok = agreed(wait_or_abort(smem_addr(&bars.seg_empty[seg]), ((n_seg / kSegments) & 1u) ^ 1u, abort_flag, limit_ns));
         if (!ok) break;
         Segment& g = s_seg[seg];
         if (lt == 0) {
@@ -702,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         if (n_tiles == 0) continue;
         // Q once the last segment's logits are done; called after the first tile's loads are on their way.
         auto load_q = [&] {
-          ok = agreed(wait_or_abort(smem_addr(&bars.q_empty), (n_q & 1u) ^ 1u, abort_flag, kWaitBudgetNs));
+          ok = agreed(wait_or_abort(smem_addr(&bars.q_empty), (n_q & 1u) ^ 1u, abort_flag, limit_ns));
           ++n_q;
           if (!ok) return;
           constexpr int C = D / 8, RP = kLoaders / C;  // chunks of a row; rows of one pass
@@ -814,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         bool here = true;                              // this thread's waits
         auto room = [&](uint32_t n) {                  // the ring's place of load n is free
           here = here && wait_or_abort(smem_addr(&bars.kv_empty[n % S::kRing]), ((n / S::kRing) & 1u) ^ 1u, abort_flag,
-                                       kWaitBudgetNs);
+                                       limit_ns);
           return here;
         };
         if constexpr (F8) {
@@ -962,7 +967,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
             const uint32_t place = (n_load + kv) % S::kRing, dst = ring0 + place * S::kTileBytes;
             const uint8_t* src0 = kbase + (kv ? a.v_offset : 0);
-            if (lane == (int)place) bulk = 0;
             constexpr int C = D / 8, RP = kLoaders / C;   // chunks of a row; rows of one pass of the loaders
             const int c = lt % C;
 #pragma unroll 4
@@ -986,9 +990,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         if (!ok) break;
       }
       // After a time-out bulk copies may be in flight that no MMA waited for:
-      // they land before shared memory is let go.
-      if (!ok && bulk > 0)
-        mbar_wait_bounded(smem_addr(&bars.kv_full[lane]), ((bulk - 1) / S::kRing) & 1u, kWaitBudgetNs);
+      // they land before shared memory is let go.  Both warps' copies go into a
+      // place of an odd ring in turn: the last one is waited for, as those before
+      // it have landed (and their phase's parity comes again two phases later).
+      if (!ok) {
+        if (bulk > 0) atomicMax(&s_bulk[lane], bulk);
+        barrier_loaders();
+        const uint32_t last = lane < S::kRing ? s_bulk[lane] : 0u;
+        if (last > 0) mbar_wait_bounded(smem_addr(&bars.kv_full[lane]), ((last - 1) / S::kRing) & 1u, kWaitBudgetNs);
+      }
       __syncwarp();
       cp_async_wait<0>();
       if (!ok) *abort_flag = 1;
@@ -1012,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         uint32_t place = 0, turn = 0;                  // of the next load: its place in the ring, and the ring's turn
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
-          if (!mbar_try_wait(bar, parity)) ok = wait_or_abort(bar, parity, abort_flag, kWaitBudgetNs);
+          if (!mbar_try_wait(bar, parity)) ok = wait_or_abort(bar, parity, abort_flag, limit_ns);
           return ok;
         };
         auto next_place = [&] {
@@ -1118,7 +1128,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 template <typename T, bool F8, int D>
 static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
   using S = prompt::Shape<D, F8>;
-  auto* kern = prompt::attend_prompt_kernel<T, F8, D>;
+  auto* kern = a.wait_ns < kWaitBudgetNs ? prompt::attend_prompt_kernel<T, F8, D, true> : prompt::attend_prompt_kernel<T, F8, D, false>;
   static_assert(S::kSmem + (F8 ? 2048 : 1024) <= 227 * 1024, "a CTA fits an SM");
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;

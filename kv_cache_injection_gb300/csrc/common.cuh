@@ -166,6 +166,7 @@ struct AttendArgs {
   float scale;                  // softmax scale times the K scale of an FP8 cache
   float v_scale;
   int32_t dtype, fp8;
+  uint64_t wait_ns;             // limit of each wait of the kernel for prompts
 };
 
 // Uniform bins of the cosine in [-1, 1] used by the top-k's first pass.

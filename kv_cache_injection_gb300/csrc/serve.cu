@@ -258,8 +258,14 @@ extern "C" is_status_t is_append(const is_append_args_t* a, cudaStream_t stream)
   return launched(launch_append(p, *turns, LaunchCfg{stream, sms_of(dev), true}), "is_append launch");
 }
 
-extern "C" is_status_t is_attend(const is_attend_args_t* a, cudaStream_t stream) {
+extern "C" is_status_t is_attend(const is_attend_args_t* args, cudaStream_t stream) {
+  return is_attend_within(args, (int64_t)kWaitBudgetNs, stream);
+}
+
+extern "C" is_status_t is_attend_within(const is_attend_args_t* a, int64_t budget_ns, cudaStream_t stream) {
   if (!a) return refuse(IS_ERR_INVALID_ARG, "args are NULL");
+  if (budget_ns < 0 || budget_ns > (int64_t)kWaitBudgetNs)
+    return refuse(IS_ERR_INVALID_ARG, "budget_ns must be in [0, %llu]", (unsigned long long)kWaitBudgetNs);
   const int R = a->num_requests, T = a->num_tokens, Hq = a->num_q_heads, H = a->num_kv_heads, D = a->head_dim;
   if (R < 1 || R > IS_MAX_REQUESTS) return refuse(IS_ERR_INVALID_ARG, "num_requests must be in [1, IS_MAX_REQUESTS]");
   if (T < 0 || a->max_q_len < 1 || a->max_blocks_per_seq < 1 || a->window < 0)
@@ -332,6 +338,7 @@ extern "C" is_status_t is_attend(const is_attend_args_t* a, cudaStream_t stream)
   p.fp8 = a->cache.dtype == IS_FP8_E4M3;
   p.scale = p.fp8 ? a->scale * a->cache.k_scale : a->scale;
   p.v_scale = p.fp8 ? a->cache.v_scale : 1.f;
+  p.wait_ns = (uint64_t)budget_ns;
   DeviceGuard g(dev);
   return launched(launch_attend(p, LaunchCfg{stream, sms_of(dev), true}), "is_attend launch");
 }

@@ -1,4 +1,6 @@
 """The serving step's calls at their edges, against the plain 64-bit definitions."""
+import time
+
 import pytest
 import torch
 
@@ -145,3 +147,49 @@ def test_logits_past_every_step(dtype, cache, size, rows):
     assert status.tolist() == [0]
     assert bool(((out.cpu().double() - o).abs() <= tol).all())
     assert bool(((lse.cpu().double() - ls).abs() <= lse_tol).all())
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("dtype,cache,D,bs,window", [
+    ("bf16", "bf16", 64, 16, 0), ("bf16", "bf16", 128, 16, 0), ("f16", "f16", 128, 8, 250), ("bf16", "bf16", 128, 24, 0),
+    ("f16", "f16", 256, 16, 0), ("bf16", "e4m3", 128, 16, 0), ("f16", "e4m3", 64, 16, 0)])
+def test_waits_that_run_out(dtype, cache, D, bs, window):
+    """An ordinary prompt with limits of its waits that it cannot keep: the call ends at once (its own copies in flight
+    have landed by then), reports IS_ST_TIMEOUT and nothing else, and the next call on the same stream and workspace,
+    which needs the tensor memory back, gives the bits that it gave before."""
+    g = torch.Generator().manual_seed(61)
+    H, Hq, lens, rows, sc = 2, 8, [3333, 900, 70], [200, 100, 70], SCALES.get(cache, (1.0, 1.0))
+    need = [-(-n // bs) for n in lens]
+    nb = sum(need)
+    table, at = torch.full((3, max(need)), -1, dtype=torch.int32), 0
+    for r, n in enumerate(need):
+        table[r, :n] = torch.arange(at, at + n)
+        at += n
+    lc = torch.stack([stored(torch.randn(nb * bs, H, D, generator=g), cache, sc[i])[0] for i in range(2)])
+    q = torch.randn(sum(rows), Hq, D, generator=g).to(ref.TORCH[dtype]).to(DEV)
+    start = [0, 200, 300, 370]
+    args = (q, ints(lens), table.to(DEV), api.make_cache_desc(bs, nb, cache, *sc), lc.view(2, nb, bs, H, D).to(DEV))
+    ws, status = api.attend_workspace(), ints([0])
+
+    def call(**kw):
+        out = torch.zeros_like(q)
+        torch.cuda.synchronize()
+        t = time.perf_counter()
+        api.is_attend(*args, out, ws, status, q_start=ints(start), max_q_len=200, window=window, **kw)
+        torch.cuda.synchronize()
+        bits = status.item()
+        status.zero_()
+        return out.cpu(), bits, time.perf_counter() - t
+
+    want, bits, _ = call()
+    assert bits == 0 and bool(want.isfinite().all())
+    seen = 0
+    for budget in (0, 0, 500, 2000, 10000, 100000):
+        out, bits, took = call(budget_ns=budget)
+        assert bits in (0, _lib.IS_ST_TIMEOUT) and took < 1.0
+        assert bits or torch.equal(out, want)
+        seen |= bits
+        out, bits, _ = call()
+        assert bits == 0 and torch.equal(out, want)
+    assert seen == _lib.IS_ST_TIMEOUT
