@@ -442,11 +442,14 @@ def attend_workspace(device=None):
 
 
 def prepare_attend(q, seq_len, block_table, cache: CacheDesc, layer_cache, out, workspace, status_out, q_start=None,
-                   max_q_len: int = 1, scale: float | None = None, window: int = 0, lse_out=None, stream=None,
+                   max_q_len: int | None = None, scale: float | None = None, window: int = 0, lse_out=None, stream=None,
                    budget_ns: int | None = None):
     """is_attend with every argument marshalled once.  q [T][Hq][D] may be a
     view with any token stride; scale None: head_dim ** -0.5; budget_ns: the
-    limit of each wait (is_attend_within)."""
+    limit of each wait (is_attend_within).  max_q_len None: one row a request
+    without q_start, with it up to all of q's.  That answers every request, but
+    chooses the kernel for prompts: a step of few rows a request should say
+    how many."""
     dt, code = _float_code("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens][heads][head_dim]")
@@ -460,6 +463,8 @@ def prepare_attend(q, seq_len, block_table, cache: CacheDesc, layer_cache, out, 
     _typed("out", out, dt, (T, Hq, D), dev)
     _typed("lse_out", lse_out, "float32", (T, Hq), dev, True)
     _typed("workspace", workspace, "uint8", (None,), dev)
+    if max_q_len is None:
+        max_q_len = 1 if q_start is None else max(1, T)
     args = AttendArgs(R, T, int(max_q_len), Hq, H, D, code, int(block_table.shape[1]), int(window),
                       float(D ** -0.5 if scale is None else scale), int(q.stride(0)), q.data_ptr(), _ptr(q_start),
                       _ptr(seq_len), _ptr(block_table), _ptr(layer_cache), _ptr(out), _ptr(lse_out), _ptr(workspace),

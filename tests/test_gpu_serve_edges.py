@@ -193,3 +193,23 @@ def test_waits_that_run_out(dtype, cache, D, bs, window):
         out, bits, _ = call()
         assert bits == 0 and torch.equal(out, want)
     assert seen == _lib.IS_ST_TIMEOUT
+
+
+# ---------------------------------------------------------------- arguments left out
+
+def test_q_start_without_max_q_len():
+    """Requests of several rows are answered although their largest number is not given."""
+    g = torch.Generator().manual_seed(41)
+    H, Hq, D, bs, nb = 1, 2, 64, 16, 6
+    lc = torch.randn(2, nb, bs, H, D, generator=g)
+    q = torch.randn(24, Hq, D, generator=g)
+    for starts, lens in (([0, 5, 24], [30, 40]), ([0, 1, 2], [30, 40]), ([0, 0, 24], [9, 24])):
+        got = []
+        for kw in (dict(), dict(max_q_len=24)):
+            out, status = torch.full((24, Hq, D), 7.0, device=DEV), ints([0])
+            api.is_attend(q.to(DEV), ints(lens), ints([[0, 1, 2], [3, 4, 5]]), api.make_cache_desc(bs, nb, "f32"), lc.to(DEV),
+                          out, api.attend_workspace(), status, q_start=ints(starts), **kw)
+            assert status.tolist() == [0]
+            got.append(out.cpu())
+        assert torch.equal(*got)
+        assert bool((got[0][: starts[-1]] != 7.0).all()) and bool((got[0][starts[-1]:] == 7.0).all())
