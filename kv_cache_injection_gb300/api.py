@@ -374,7 +374,10 @@ def prepare_extend_block_table(seq_len, new_len, free_blocks, block_size: int, n
                                slot_mapping_out, positions_out=None, token_start_out=None, seq_len_out=None,
                                status_out=None, free_head=None, free_head_out=None, stream=None):
     """is_extend_block_table with every argument marshalled once: a callable for
-    serving loops that reuse their buffers."""
+    serving loops that reuse their buffers.  status_out (int32 [1]) is required:
+    refused requests show nowhere else."""
+    if status_out is None:
+        raise ValueError("status_out is required: an int32 tensor [1] that collects the IS_ST_* bits")
     dev = _typed("seq_len", seq_len, "int32", (None,)).device
     R, T = int(seq_len.shape[0]), int(slot_mapping_out.shape[0])
     args = ExtendArgs(
@@ -396,7 +399,7 @@ def prepare_extend_block_table(seq_len, new_len, free_blocks, block_size: int, n
 
 def is_extend_block_table(*args, **kw) -> None:
     """Blocks, slots and positions of a step's new tokens; arguments as in the
-    prepared form.  status_out (int32 [1]) collects the IS_ST_* bits."""
+    prepared form.  status_out (int32 [1], required) collects the IS_ST_* bits."""
     prepare_extend_block_table(*args, **kw)()
 
 

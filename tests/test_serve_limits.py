@@ -3,7 +3,7 @@ import ctypes
 
 import pytest
 
-from kv_cache_injection_gb300 import _lib, build
+from kv_cache_injection_gb300 import _lib, api, build
 from tests.test_serve_refusals import INVALID, attend_args
 
 
@@ -24,3 +24,8 @@ def test_attend_within_takes_its_range(lib):
     args = attend_args(num_tokens=0)
     assert [lib.is_attend_within(ctypes.byref(args), b, None) for b in (0, 1, 2_000_000_000)] == [0, 0, 0]
     assert lib.is_attend_within(None, 0, None) == INVALID
+
+
+def test_extend_says_that_it_needs_a_status_word():
+    with pytest.raises(ValueError, match="status_out is required"):
+        api.is_extend_block_table(None, None, None, 16, 4, None, None)
