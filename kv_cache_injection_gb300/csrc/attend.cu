@@ -38,7 +38,9 @@
 // Sums, maxima and O are fp32; the weights are rounded to 16 bits for the
 // second product (relative 2^-8 or 2^-11, like the output).  FP8 keys and
 // values are exact in fp16, so that path computes in fp16, a bf16 query row
-// being scaled by a power of two into fp16's range (exact, undone in fp32).
+// being scaled by a power of two that brings its largest element to [2^14,
+// 2^15) (undone in fp32).  That is exact for elements down to 2^-31 of the
+// largest; fainter ones are rounded by 2^-39 of the largest at most.
 // fp32 caches use fp32 fused multiply-adds throughout.
 //
 // Measured (H = 8, D = 128, bf16 unless said): 4 requests of 60,000-131,000

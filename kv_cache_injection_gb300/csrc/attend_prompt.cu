@@ -365,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                                                                    const __grid_constant__ CUtensorMap rows_map) {
   using S = Shape<D, F8>;
   const uint64_t limit_ns = LIMITED ? a.wait_ns : kWaitBudgetNs;
-  // FP8 keys and values are exact in fp16, and so is a bf16 query row scaled by a power of two (undone in the logits):
-  // with an FP8 cache both products are taken in fp16.
+  // FP8 keys and values are exact in fp16, and a bf16 query row scaled by a power of two (undone in the logits) loses
+  // 2^-39 of its largest element at most: with an FP8 cache both products are taken in fp16.
   using W = typename std::conditional<F8, __half, T>::type;
   constexpr bool kShift = F8 && std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ uint8_t smem_raw[];

@@ -213,3 +213,35 @@ def test_q_start_without_max_q_len():
             got.append(out.cpu())
         assert torch.equal(*got)
         assert bool((got[0][: starts[-1]] != 7.0).all()) and bool((got[0][starts[-1]:] == 7.0).all())
+
+
+# ---------------------------------------------------------------- query rows of a wide spread
+
+@pytest.mark.parametrize("rows", [1, 50])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("scale,zero", [(0.125, True), (2.0 ** -26, False)])
+def test_one_large_element_a_query_row(D, rows, scale, zero):
+    """bf16 rows with one element of 2^26 over an FP8 cache, whose keys are 0 there (the others decide) or not.  The
+    products are taken in fp16 with the largest element in [2^14, 2^15), where rounding changes an element by half of
+    the smallest step, 2^-25, at most: 2^-39 of the largest element, times |k| and the scale in a logit."""
+    g = torch.Generator().manual_seed(71)
+    H, Hq, n, bs, sc = 1, 4, 500, 16, SCALES["e4m3"]
+    nb = -(-n // bs)
+    k = torch.randn(nb * bs, H, D, generator=g)
+    if zero:
+        k[:, :, 0] = 0.0
+    (ks, k), (vs, v) = stored(k, "e4m3", sc[0]), stored(torch.randn(nb * bs, H, D, generator=g), "e4m3", sc[1])
+    k, v = k[:n], v[:n]
+    q = torch.randn(rows, Hq, D, generator=g)
+    q[:, :, 0] = 2.0 ** 26
+    q = q.to(torch.bfloat16)
+    out, lse, status = torch.empty_like(q, device=DEV), torch.empty(rows, Hq, device=DEV), ints([0])
+    api.is_attend(q.to(DEV), ints([n]), ints([list(range(nb))]), api.make_cache_desc(bs, nb, "e4m3", *sc),
+                  torch.stack([ks, vs]).view(2, nb, bs, H, D).to(DEV), out, api.attend_workspace(), status,
+                  q_start=ints([0, rows]), max_q_len=rows, scale=scale, lse_out=lse)
+    o, ls, spread, heft, seen = ref.attend(q.double(), n, k, v, torch.ones(n, dtype=torch.bool), scale, 0)
+    lost = 2.0 ** -39 * 2.0 ** 26 * float(k.abs().sum(-1).max()) * scale
+    tol, ltol = ref.attend_tolerance("bf16", "e4m3", D, o, ls, spread, heft + lost / ((D + 8) * 2.0 ** -24), seen,
+                                     float(v.abs().max()))
+    assert status.tolist() == [0] and lost < 0.01
+    assert bool(((out.cpu().double() - o).abs() <= tol).all()) and bool(((lse.cpu().double() - ls).abs() <= ltol).all())
