@@ -576,7 +576,8 @@ is_status_t is_append(const is_append_args_t* args, cudaStream_t stream);
  *               IS_ATTEND_WORKSPACE_BYTES is enough for every call;
  *               its contents need no initialisation and mean nothing later.
  * Products are summed in fp32; with a 16-bit q the weights w_j are rounded to
- * 16 bits before they multiply the values.  Over an FP8 cache an element of a
+ * 16 bits before they multiply the values (in the kernel for at most 8 rows a
+ * request and KV head to twice the bits, bf16 over an FP8 cache to fp16's).  Over an FP8 cache an element of a
  * bf16 query row is rounded by 2^-39 of the row's largest at most (exact down
  * to 2^-31 of it).  head_dim is 64, 128 or 256.
  * The kernel for many rows waits on its own copies and products with a limit

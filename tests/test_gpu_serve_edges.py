@@ -245,3 +245,31 @@ def test_one_large_element_a_query_row(D, rows, scale, zero):
                                      float(v.abs().max()))
     assert status.tolist() == [0] and lost < 0.01
     assert bool(((out.cpu().double() - o).abs() <= tol).all()) and bool(((lse.cpu().double() - ls).abs() <= ltol).all())
+
+
+# ---------------------------------------------------------------- single tokens' weights
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("f16", "f16"), ("f16", "e4m3")])
+@pytest.mark.parametrize("Hq,H,D", [(8, 2, 64), (7, 1, 128), (4, 2, 256)])
+def test_single_tokens_weights_keep_their_bits(Hq, H, D, dtype, cache):
+    """A single token's weights are multiplied with what their rounding took off: they keep 2^-16 (bf16) or 2^-22 (fp16;
+    2^-32 of the largest among the faintest), so that the output's rounding is all that 16 bits cost."""
+    g = torch.Generator().manual_seed(81)
+    lens, bs, sc = [1, 17, 130, 900, 2500] * 20, 16, SCALES.get(cache, (1.0, 1.0))
+    nb = -(-max(lens) // bs)
+    kv = [stored(torch.randn(nb * bs, H, D, generator=g), cache, sc[i]) for i in range(2)]
+    k, v = (x for _, x in kv)
+    q = torch.randn(len(lens), Hq, D, generator=g).to(ref.TORCH[dtype])
+    out, status = torch.empty_like(q, device=DEV), ints([0])
+    api.is_attend(q.to(DEV), ints(lens), torch.arange(nb, dtype=torch.int32).repeat(len(lens), 1).to(DEV),
+                  api.make_cache_desc(bs, nb, cache, *sc), torch.stack([s for s, _ in kv]).view(2, nb, bs, H, D).to(DEV), out,
+                  api.attend_workspace(), status)
+    assert status.tolist() == [0]
+    for r, n in enumerate(lens):
+        o, ls, spread, heft, seen = ref.attend(q[r: r + 1].double(), n, k[:n], v[:n], torch.ones(n, dtype=torch.bool), D ** -0.5, 0)
+        tol, _ = ref.attend_tolerance("f32", "f32", D, o, ls, spread, heft, seen, 0.0)
+        tol = tol + (2.0 ** -16 if dtype == "bf16" else 2.0 ** -22) * 1.01 * spread + ref.U[dtype] * 1.01 * o.abs()
+        if dtype == "f16":
+            tol = tol + n * 2.0 ** -32 * float(v[:n].abs().max()) + 2.0 ** -25
+        err = (out[r: r + 1].cpu().double() - o).abs()
+        assert bool((err <= tol).all()), (r, float((err / tol).max()))
