@@ -455,12 +455,14 @@ is_status_t is_inject_noalloc(const void* kv_arena, int64_t arena_tokens,
  * is_extend_block_table makes room for a step's new tokens, is_append rotates
  * their queries and keys and writes their K/V behind the segment, and
  * is_attend attends from them over the whole paged cache, segment included.
- * The three need no store, allocate nothing and keep nothing between calls:
- * every buffer is the caller's, and device-detected errors are OR-ed into the
- * caller's status word, as in is_inject_noalloc.  Each takes its arguments in
- * a struct that is read before the call returns, so a serving loop fills it
- * once.  The device is the one that owns the call's buffers (the current
- * device is put back afterwards) and the stream must belong to it.  All
+ * The three need no store, allocate nothing and keep nothing of a call's data
+ * (is_append keeps the calling thread's last rotation table, by value, which
+ * depends on rope, axes and head_dim alone): every buffer is the caller's, and
+ * device-detected errors are OR-ed into the caller's status word, as in
+ * is_inject_noalloc.  Each takes its arguments in a struct that is read before
+ * the call returns, so a serving loop fills it once.  The device is the one
+ * that owns the call's buffers (the current device is put back afterwards) and
+ * the stream must belong to it.  All
  * pointers are device (or managed) memory; outputs overlap neither one another
  * nor any input unless said.  The kernels may start before the previous
  * kernel of the stream has ended and wait for it before they touch memory. */

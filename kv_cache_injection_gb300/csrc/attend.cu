@@ -29,8 +29,8 @@
 //   O^T = V^T P^T (mma.m16n8k16): the keys and the head dimension fill the
 //   16-row side and the query rows the 8-column side, so a group of 4 to 8
 //   query heads wastes little.  tcgen05 wants 128 (or 64) rows and gains
-//   nothing here: the SMs issue in a fifth of their slots (bf16) while the
-//   memory is the limit.
+//   nothing here: the SMs issue in 28 % of their slots (bf16) while the memory
+//   is the limit.
 // - The maximum moves only when a logit passes it by more than 2^8 (in the
 //   base-2 exponent), so the usual tile costs one vote instead of a reduction;
 //   fp16 weights are raised by 2^7 (see kRaise).
@@ -46,12 +46,12 @@
 // fp32 caches use fp32 fused multiply-adds throughout.
 //
 // Measured (H = 8, D = 128, bf16 unless said): 4 requests of 60,000-131,000
-// tokens 264 us, 6.8 TB/s, the rate of a plain copy; 64 requests of 500-8000
-// tokens 170 us (6.3 TB/s), with an FP8 cache 101 us (5.3 TB/s, where the
-// conversions fill 44 % of the issue slots); 100 requests of 300-2048 tokens
-// (H = 4) 46.2 us against 34.3 for their bytes, the rest being the start
-// (2 us to find the runs, 3 more until the first tile has landed), the last
-// tiles and the join.
+// tokens 260 us on one GPU and 268 on another, 6.7 to 6.9 TB/s, the rate of a
+// plain copy; 64 requests of 500-8000 tokens 173 us (6.2 TB/s), with an FP8 cache
+// 92 and 101 us (5.9 and 5.3 TB/s, the SMs issuing in 34 % of their slots); 100
+// requests of 300-2048 tokens (H = 4) 46.2 and 46.8 us against 34.3 for their
+// bytes, the rest being the start (2 us to find the runs, 3 more until the first
+// tile has landed), the last tiles and the join.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -844,10 +844,14 @@ cudaError_t launch_attend(const AttendArgs& a, const LaunchCfg& cfg) {
   // Many rows go to the kernel of attend_prompt.cu, which reads the keys once
   // for 256 rows (128 at head_dim 256), from the number of rows on at which the
   // kernel here would read them more than once.  100 requests of 300-2048 tokens
-  // with 4 new ones, 28 rows: 98 us here, 71 there; at head_dim 256, 16 rows: 176
-  // and 97; 4 requests of up to 131,000 tokens, 32 rows: 528 and 273; a single
-  // one of 1313: 18 and 21.  FP8 rows are widened faster here, so there they go
-  // from 33 on (32 rows, 64 requests of 500-8000 tokens: 258 and 295 us).
+  // with 4 new ones, 28 rows: 98 us here, 68 there; at head_dim 256, 16 rows: 178
+  // and 98; 4 requests of up to 131,000 tokens, 32 rows: 542 and 278; a single
+  // one of 1313: 18.1 and 17.3.  FP8 rows are widened faster here, so there they go
+  // from 33 on (32 rows, 64 requests of 500-8000 tokens: 259 and 293 us), and not
+  // at all at head_dim 256, where the other kernel's shared memory has no room for
+  // them: 64 KB of Q and two widened tiles of 64 KB leave 35 KB, one tile of raw
+  // rows and none ahead of it.  (Two prompts of 2000-2500 tokens behind up to 8192,
+  // H = 4, G = 2: 2100 us here over FP8, 255 there over bf16.)
   // Maxima there are of unscaled logits, so the scale has to be positive.
   const int most = a.fp8 ? 32 : a.D == 256 ? 8 : 16;
   if (a.dtype != IS_F32 && (a.D <= 128 || !a.fp8) && a.G <= 64 && (int64_t)a.max_q * a.G > most && a.scale > 0.f)

@@ -38,19 +38,21 @@
 // B's place.
 //
 // Measured (H = 8, G = 4, D = 128, bf16): two prompts of 2000-2500 tokens
-// behind up to 8192, 538 GFLOP, 392 us = 1.37 PFLOP/s, 72 % of the burst rate of
+// behind up to 8192, 538 GFLOP, 385 us = 1.40 PFLOP/s, 74 % of the burst rate of
 // a plain library product.  128 keys of a pair of tiles are 2048 clocks of MMAs
 // (64 each for M 128, N 128, K 16) and take 2900.  Leaving out the exponentials
 // changes nothing; half the S products save 3 %, half the O products 2 %, half
 // of the loaded bytes 8 %: shared memory feeds the MMAs (S alone reads 128
 // bytes a clock) while it takes in the next tiles, and a tile's next S waits
 // for its softmax (1400 clocks) and the other tile's products.  16 requests with
-// 20-100 new tokens over 900-2000: 54 us; the start and end of an item (its first
+// 20-100 new tokens over 900-2000: 51.6 us; the start and end of an item (its first
 // tiles, 64 KB of output or 128 KB of partial) cost as much as about six key
-// tiles.  One request, 100 new tokens over 400: 20 us, the latency of this kernel
+// tiles.  One request, 100 new tokens over 400: 19.5 us, the latency of this kernel
 // (1 us to its run, 4 to the first S, 2 for the tiles, 2 of output) and the join.
-// Over an FP8 cache the two long prompts take 569 us, 0.95 PFLOP/s: the three
-// loader warps that widen the rows are the limit.
+// Over an FP8 cache the two long prompts take 560 us, 0.96 PFLOP/s: the three
+// loader warps that widen the rows are the limit.  At head_dim 256 (bf16, twice
+// the operations) 947 us, 1.14 PFLOP/s: with one tile, its products and its softmax
+// take turns.
 #include <cuda.h>
 
 #include <algorithm>

@@ -10,7 +10,7 @@
 // depends on what another writes (a new token's block id comes from the free
 // list, not from the table entry).  Bound by latency at few tokens (100
 // requests of one token: 3.6 us) and by the instructions of going over all
-// requests in every CTA at many (4096 requests, 614,000 tokens, 7.7 MB: 8.5
+// requests in every CTA at many (4096 requests, 614,000 tokens, 7.7 MB: 8.6
 // us; 45 with 64-bit divisions and a search per token).
 #include <algorithm>
 
@@ -21,8 +21,8 @@
 namespace isk {
 
 // Few requests: small CTAs, one token and at most two requests a thread.  Many:
-// large ones, since each CTA goes over all requests (4096 requests: 14.1 us
-// with 512 threads a CTA, 12.1 with 1024).
+// large ones, since each CTA goes over all requests (4096 requests: 11.5 us
+// with 512 threads a CTA, 8.6 with 1024).
 constexpr int kFewRequests = 512, kFewThreads = 256, kManyThreads = 1024;
 constexpr int kFewTokens = 1, kManyTokens = 4;   // tokens a thread
 

@@ -1,5 +1,6 @@
 // C ABI of the serving step around the segment: argument checks and launches of
-// is_extend_block_table, is_append and is_attend.  They keep no state: the
+// is_extend_block_table, is_append and is_attend.  They keep no state but a
+// thread's last rotation table, which its parameters determine (axis_turns): the
 // device comes from the call's buffers, everything else from its arguments.
 #include <cmath>
 #include <cstdarg>
