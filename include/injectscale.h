@@ -79,11 +79,13 @@ typedef enum {
 #define IS_ST_COUNT        0x40u  /* n_ids[r] < 0 or > ids_stride */
 #define IS_ST_TIMEOUT      0x80u  /* a bounded device wait gave up */
 #define IS_ST_FREE_LIST    0x100u /* the free list has too few blocks, or its head is outside it */
+#define IS_ST_SCALE        0x200u /* a scaled cache's block has a scale outside [2^-40, 2^40] */
 
 /* IS_FP8_E4M3 is a paged-cache type only (never a store type): 8-bit floats
  * in the OCP E4M3 format (no infinities, largest finite 448), the 8-bit KV
- * cache of vLLM, the engine InferScale injects into. */
-typedef enum { IS_F32 = 0, IS_BF16 = 1, IS_F16 = 2, IS_FP8_E4M3 = 3 } is_dtype_t;
+ * cache of vLLM, the engine InferScale injects into.  IS_INT8 (two's
+ * complement, -127 .. 127) is a type of scaled caches only (is_append_scaled). */
+typedef enum { IS_F32 = 0, IS_BF16 = 1, IS_F16 = 2, IS_FP8_E4M3 = 3, IS_INT8 = 4 } is_dtype_t;
 
 /* Where the store's K/V arena lives (is_store_config_t.kv_placement).
  * InferScale ("Résultats", Scalabilité) offloads the KV store to host DRAM to go past the
@@ -621,6 +623,96 @@ is_status_t is_attend(const is_attend_args_t* args, cudaStream_t stream);
  * keep 2 s, and the kernel for few rows has none.
  * Errors: those of is_attend; IS_ERR_INVALID_ARG for a budget outside that range. */
 is_status_t is_attend_within(const is_attend_args_t* args, int64_t budget_ns, cudaStream_t stream);
+
+/* ---- the serving step over a scaled cache ---------------------------------------
+ * A scaled cache holds one layer's K and V in 8 bits with a scale for each
+ * block and KV head that follows the data, so nothing is calibrated:
+ *   layer_cache  codes [2][num_blocks][block_size][H][D], IS_INT8 or IS_FP8_E4M3
+ *   scales       float [2][num_blocks][H]: an element is its code times the scale
+ *                of its block, head and K or V; each in [2^-40, 2^40]
+ * Its is_cache_desc_t has k_scale = v_scale = 1.  The block table and slots are
+ * those of any paged cache (is_extend_block_table).  Conventions are those of
+ * the serving step above: no store, no allocation, the caller's status word,
+ * and the device of the call's buffers.
+ *
+ * What is written: the tokens of a call that lie in one block are adjacent in
+ * the batch (a packed batch's are).  With A the largest magnitude of their
+ * finite elements of a head, K or V, and qmax 127 (INT8) or 448 (E4M3), the
+ * block's scale becomes fp32(A / qmax), at least 2^-40 and at most 2^40; unless
+ * row 0 of the block is among the tokens' rows, the rows below the lowest of
+ * them are held already and the scale is not made smaller than it was.  Where
+ * it grows, those rows' codes become round(code * fp32(old / new)).  The new
+ * codes are round(y * fp32(1 / scale)), to nearest even and saturated; y is the
+ * key rotated in fp32 or the raw value.  Infinities saturate; NaN is 0 in INT8 and NaN
+ * in E4M3.  Rows behind the tokens' are left as they are and mean nothing.  A
+ * block whose earlier rows count but whose scale is out of range keeps its
+ * codes, and the tokens' K or V of that head are not written (IS_ST_SCALE). */
+
+/* is_append_scaled: is_append into a scaled cache (args->cache of IS_INT8 or
+ * IS_FP8_E4M3, any args->dtype).  q_out is that of is_append.  A refused token's
+ * slot, if it lies in the cache, still counts as one of the call's rows. */
+is_status_t is_append_scaled(const is_append_args_t* args, float* scales, cudaStream_t stream);
+
+/* is_move_scaled: tokens of one layer of a plain cache (what is_inject wrote, for
+ * instance: a segment's keys are rotated already) into a scaled one, from slot
+ * from_slots[i] to slot slot_mapping[i].  A token with -1 in either is skipped;
+ * so is, with IS_ST_BLOCK_ID, one with any other slot outside its cache. */
+typedef struct {
+  int32_t num_tokens;          /* >= 0 */
+  int32_t num_kv_heads;
+  int32_t head_dim;            /* power of two, 16 .. IS_MAX_HEAD_DIM (fp32: 256) */
+  int32_t dtype;               /* of from_cache: IS_F32, IS_BF16 or IS_F16 */
+  const int64_t* from_slots;   /* [num_tokens] */
+  const int64_t* slot_mapping; /* [num_tokens] */
+  const void* from_cache;      /* [2][from.num_blocks][from.block_size][num_kv_heads][head_dim] */
+  void* layer_cache;
+  float* scales;
+  uint32_t* status_out;
+  is_cache_desc_t from;
+  is_cache_desc_t cache;       /* of layer_cache */
+  int32_t reserved[2];         /* must be 0 */
+} is_move_args_t;
+is_status_t is_move_scaled(const is_move_args_t* args, cudaStream_t stream);
+
+/* is_read_scaled: tokens of a scaled cache back as rows, elements multiplied out in
+ * fp32 and rounded once.  With unrotate 1 the keys are turned back by their
+ * positions first, which gives keys before RoPE as is_store_add_facts and
+ * is_store_capture_layer take them: what a request wrote can become facts.
+ * A token with slot -1 is skipped: its rows are left as they were.  So is, with
+ * its status bit, one with any other slot outside the cache (IS_ST_BLOCK_ID) or
+ * a position outside [0, IS_MAX_POSITION) (IS_ST_POSITION), and a head's row
+ * whose block has a scale out of range (IS_ST_SCALE). */
+typedef struct {
+  int32_t num_tokens;          /* >= 0 */
+  int32_t num_kv_heads;
+  int32_t head_dim;            /* power of two, 16 .. IS_MAX_HEAD_DIM (fp32: 256); limits of is_rope_params_t */
+  int32_t dtype;               /* of k_out and v_out: IS_F32, IS_BF16 or IS_F16 */
+  int32_t unrotate;            /* 0 or 1; rope, axes and positions are read with 1 only */
+  int32_t reserved;            /* must be 0 */
+  const int64_t* slot_mapping; /* [num_tokens] */
+  const int32_t* positions;    /* [n_axes][num_tokens] */
+  const void* layer_cache;
+  const float* scales;
+  void* k_out;                 /* [num_tokens][num_kv_heads][head_dim], or NULL */
+  void* v_out;                 /* or NULL (one of the two is given) */
+  uint32_t* status_out;
+  is_rope_params_t rope;
+  is_rope_axes_t axes;
+  is_cache_desc_t cache;
+  int32_t reserved2;           /* must be 0 */
+} is_read_args_t;
+is_status_t is_read_scaled(const is_read_args_t* args, cudaStream_t stream);
+
+/* is_attend_scaled: is_attend over a scaled cache, for 16-bit queries; the rows,
+ * masks, outputs and the workspace are those of is_attend.  A block with a
+ * scale out of range is hidden like one that the table does not name
+ * (IS_ST_SCALE).  Products are taken in fp16, in which every code is exact, and
+ * a bf16 query row as over an FP8 cache of is_attend; the weights are rounded to
+ * fp16 (for fp16 queries, in the kernel for at most 8 rows, to twice the bits).
+ * is_attend_scaled_within: with the limit of each wait (is_attend_within). */
+is_status_t is_attend_scaled(const is_attend_args_t* args, const float* scales, cudaStream_t stream);
+is_status_t is_attend_scaled_within(const is_attend_args_t* args, const float* scales, int64_t budget_ns,
+                                    cudaStream_t stream);
 
 /* ---- is_set_retrieval_mode -----------------------------------------------------
  * How the similarity is computed.  IS_RETRIEVAL_PER_QUERY: one launch in

@@ -12,10 +12,10 @@ IS_OK = 0
 STATUS_NAMES = {0: "IS_OK", 1: "IS_ERR_INVALID_ARG", 2: "IS_ERR_OOM", 3: "IS_ERR_CAPACITY",
                 4: "IS_ERR_OUT_OF_RANGE", 5: "IS_ERR_CUDA", 6: "IS_ERR_TIMEOUT", 7: "IS_ERR_DEVICE",
                 8: "IS_ERR_UNSUPPORTED"}
-IS_F32, IS_BF16, IS_F16, IS_FP8_E4M3 = 0, 1, 2, 3
+IS_F32, IS_BF16, IS_F16, IS_FP8_E4M3, IS_INT8 = 0, 1, 2, 3, 4
 IS_ST_FACT_RANGE, IS_ST_FACT_USER, IS_ST_BLOCK_TABLE, IS_ST_BLOCK_ID = 0x01, 0x02, 0x04, 0x08
 IS_ST_USER_RANGE, IS_ST_POSITION, IS_ST_COUNT, IS_ST_TIMEOUT = 0x10, 0x20, 0x40, 0x80
-IS_ST_FREE_LIST = 0x100
+IS_ST_FREE_LIST, IS_ST_SCALE = 0x100, 0x200
 IS_STAGE_SIMILARITY, IS_STAGE_TOPK, IS_STAGE_PLAN, IS_STAGE_INJECT = 0, 1, 2, 3
 IS_MAX_K, IS_MAX_QUERIES, IS_MAX_REQUESTS, IS_EMB_TILE = 1024, 1024, 4096, 128
 IS_NOALLOC_MAX_REQUESTS, IS_NOALLOC_MAX_FACTS = 256, 256
@@ -89,6 +89,22 @@ class AttendArgs(ctypes.Structure):
                 ("reserved", c_int32)]
 
 
+class MoveArgs(ctypes.Structure):
+    _fields_ = [("num_tokens", c_int32), ("num_kv_heads", c_int32), ("head_dim", c_int32),
+                ("dtype", c_int32), ("from_slots", c_void_p), ("slot_mapping", c_void_p),
+                ("from_cache", c_void_p), ("layer_cache", c_void_p), ("scales", c_void_p),
+                ("status_out", c_void_p), ("from_", CacheDesc), ("cache", CacheDesc),
+                ("reserved", c_int32 * 2)]
+
+
+class ReadArgs(ctypes.Structure):
+    _fields_ = [("num_tokens", c_int32), ("num_kv_heads", c_int32), ("head_dim", c_int32),
+                ("dtype", c_int32), ("unrotate", c_int32), ("reserved", c_int32),
+                ("slot_mapping", c_void_p), ("positions", c_void_p), ("layer_cache", c_void_p),
+                ("scales", c_void_p), ("k_out", c_void_p), ("v_out", c_void_p), ("status_out", c_void_p),
+                ("rope", RopeParams), ("axes", RopeAxes), ("cache", CacheDesc), ("reserved2", c_int32)]
+
+
 # name -> argtypes (restype is is_status_t unless listed in _RESTYPES)
 SIGNATURES = {
     "is_store_create": [POINTER(StoreConfig), c_int, c_void_p, POINTER(c_void_p)],
@@ -131,6 +147,11 @@ SIGNATURES = {
     "is_append": [POINTER(AppendArgs), c_void_p],
     "is_attend": [POINTER(AttendArgs), c_void_p],
     "is_attend_within": [POINTER(AttendArgs), c_int64, c_void_p],
+    "is_append_scaled": [POINTER(AppendArgs), c_void_p, c_void_p],
+    "is_move_scaled": [POINTER(MoveArgs), c_void_p],
+    "is_read_scaled": [POINTER(ReadArgs), c_void_p],
+    "is_attend_scaled": [POINTER(AttendArgs), c_void_p, c_void_p],
+    "is_attend_scaled_within": [POINTER(AttendArgs), c_void_p, c_int64, c_void_p],
     "is_get_status": [c_void_p, c_void_p, POINTER(c_uint32)],
     "is_last_error_message": [],
     "is_status_string": [c_int],

@@ -12,9 +12,11 @@ from ctypes import byref, c_double, c_int64, c_uint32, c_void_p
 import numpy as np
 
 from . import _lib
-from ._lib import AppendArgs, AttendArgs, CacheDesc, ExtendArgs, RopeAxes, RopeParams, StoreConfig, StoreInfo
+from ._lib import (AppendArgs, AttendArgs, CacheDesc, ExtendArgs, MoveArgs, ReadArgs, RopeAxes, RopeParams, StoreConfig,
+                   StoreInfo)
 
-DTYPE_CODES = {"f32": _lib.IS_F32, "bf16": _lib.IS_BF16, "f16": _lib.IS_F16, "e4m3": _lib.IS_FP8_E4M3}
+DTYPE_CODES = {"f32": _lib.IS_F32, "bf16": _lib.IS_BF16, "f16": _lib.IS_F16, "e4m3": _lib.IS_FP8_E4M3,
+               "int8": _lib.IS_INT8}
 
 
 class ISError(RuntimeError):
@@ -88,7 +90,8 @@ def make_rope(theta: float, style: int = 0, scaling: int = 0, factor: float = 1.
 
 def make_cache_desc(block_size: int, num_blocks: int, dtype, k_scale: float = 1.0,
                     v_scale: float = 1.0) -> CacheDesc:
-    """dtype "e4m3" (IS_FP8_E4M3): an FP8 cache holding K / k_scale and V / v_scale."""
+    """dtype "e4m3" (IS_FP8_E4M3): an FP8 cache holding K / k_scale and V / v_scale.
+    A scaled cache ("int8" or "e4m3") has scales of its own and leaves these at 1."""
     return CacheDesc(block_size, num_blocks, DTYPE_CODES[dtype] if isinstance(dtype, str) else dtype,
                      k_scale, v_scale)
 
@@ -403,11 +406,8 @@ def is_extend_block_table(*args, **kw) -> None:
     prepare_extend_block_table(*args, **kw)()
 
 
-def prepare_append(q, k, v, positions, slot_mapping, rope: RopeParams, cache: CacheDesc, layer_cache, q_out,
-                   status_out, axes: RopeAxes | None = None, stream=None):
-    """is_append with every argument marshalled once.  q [T][Hq][D], k and v
-    [T][H][D] may be views with any token stride (q and q_out None: keys and
-    values only); positions int32 [n_axes][T] or [T]; q_out may be q."""
+def _append_args(q, k, v, positions, slot_mapping, rope, cache, layer_cache, q_out, status_out, axes, scaled: bool):
+    """The struct of is_append and is_append_scaled, and the tensors' device and KV heads."""
     axes = make_axes() if axes is None else axes
     dt, code = _float_code("k", k)
     if k.dim() != 3:
@@ -424,11 +424,20 @@ def prepare_append(q, k, v, positions, slot_mapping, rope: RopeParams, cache: Ca
         raise ValueError("q_out without q")
     _typed("positions", positions, "int32", (T,) if axes.n_axes == 1 and positions.dim() == 1 else (axes.n_axes, T), dev)
     _typed("slot_mapping", slot_mapping, "int64", (T,), dev)
-    _layer_cache(cache, layer_cache, H, D, dt, dev)
+    (_scaled_cache if scaled else _layer_cache)(cache, layer_cache, H, D, dt, dev)
     args = AppendArgs(T, Hq, H, D, code, 0, int(q.stride(0)) if Hq else 0, int(k.stride(0)), int(v.stride(0)),
                       q.data_ptr() if Hq else None, k.data_ptr(), v.data_ptr(), _ptr(positions), _ptr(slot_mapping),
                       _ptr(q_out) if Hq else None, _ptr(layer_cache),
                       _ptr(_typed("status_out", status_out, "int32", (1,), dev)), rope, axes, cache, 0)
+    return args, dev, H
+
+
+def prepare_append(q, k, v, positions, slot_mapping, rope: RopeParams, cache: CacheDesc, layer_cache, q_out,
+                   status_out, axes: RopeAxes | None = None, stream=None):
+    """is_append with every argument marshalled once.  q [T][Hq][D], k and v
+    [T][H][D] may be views with any token stride (q and q_out None: keys and
+    values only); positions int32 [n_axes][T] or [T]; q_out may be q."""
+    args, dev, _ = _append_args(q, k, v, positions, slot_mapping, rope, cache, layer_cache, q_out, status_out, axes, False)
     return _prepared("is_append", args, (q, k, v, positions, slot_mapping, layer_cache, q_out, status_out), stream, dev)
 
 
@@ -444,15 +453,9 @@ def attend_workspace(device=None):
                        device="cuda" if device is None else device)
 
 
-def prepare_attend(q, seq_len, block_table, cache: CacheDesc, layer_cache, out, workspace, status_out, q_start=None,
-                   max_q_len: int | None = None, scale: float | None = None, window: int = 0, lse_out=None, stream=None,
-                   budget_ns: int | None = None):
-    """is_attend with every argument marshalled once.  q [T][Hq][D] may be a
-    view with any token stride; scale None: head_dim ** -0.5; budget_ns: the
-    limit of each wait (is_attend_within).  max_q_len None: one row a request
-    without q_start, with it up to all of q's.  That answers every request, but
-    chooses the kernel for prompts: a step of few rows a request should say
-    how many."""
+def _attend_args(q, seq_len, block_table, cache, layer_cache, out, workspace, status_out, q_start, max_q_len, scale, window,
+                 lse_out, scaled: bool):
+    """The struct of is_attend and is_attend_scaled, and the tensors' device and KV heads."""
     dt, code = _float_code("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens][heads][head_dim]")
@@ -462,7 +465,7 @@ def prepare_attend(q, seq_len, block_table, cache: CacheDesc, layer_cache, out, 
     _typed("block_table", block_table, "int32", (R, None), dev)
     _typed("q_start", q_start, "int32", (R + 1,), dev, True)
     H = int(layer_cache.shape[3]) if layer_cache.dim() == 5 else 0
-    _layer_cache(cache, layer_cache, H, D, dt, dev)
+    (_scaled_cache if scaled else _layer_cache)(cache, layer_cache, H, D, dt, dev)
     _typed("out", out, dt, (T, Hq, D), dev)
     _typed("lse_out", lse_out, "float32", (T, Hq), dev, True)
     _typed("workspace", workspace, "uint8", (None,), dev)
@@ -472,6 +475,20 @@ def prepare_attend(q, seq_len, block_table, cache: CacheDesc, layer_cache, out, 
                       float(D ** -0.5 if scale is None else scale), int(q.stride(0)), q.data_ptr(), _ptr(q_start),
                       _ptr(seq_len), _ptr(block_table), _ptr(layer_cache), _ptr(out), _ptr(lse_out), _ptr(workspace),
                       int(workspace.shape[0]), _ptr(_typed("status_out", status_out, "int32", (1,), dev)), cache, 0)
+    return args, dev, H
+
+
+def prepare_attend(q, seq_len, block_table, cache: CacheDesc, layer_cache, out, workspace, status_out, q_start=None,
+                   max_q_len: int | None = None, scale: float | None = None, window: int = 0, lse_out=None, stream=None,
+                   budget_ns: int | None = None):
+    """is_attend with every argument marshalled once.  q [T][Hq][D] may be a
+    view with any token stride; scale None: head_dim ** -0.5; budget_ns: the
+    limit of each wait (is_attend_within).  max_q_len None: one row a request
+    without q_start, with it up to all of q's.  That answers every request, but
+    chooses the kernel for prompts: a step of few rows a request should say
+    how many."""
+    args, dev, _ = _attend_args(q, seq_len, block_table, cache, layer_cache, out, workspace, status_out, q_start, max_q_len,
+                                scale, window, lse_out, False)
     keep = (q, q_start, seq_len, block_table, layer_cache, out, lse_out, workspace, status_out)
     if budget_ns is None:
         return _prepared("is_attend", args, keep, stream, dev)
@@ -481,6 +498,112 @@ def prepare_attend(q, seq_len, block_table, cache: CacheDesc, layer_cache, out, 
 def is_attend(*args, **kw) -> None:
     """Attention of each request's last tokens over its paged cache; arguments as in the prepared form."""
     prepare_attend(*args, **kw)()
+
+
+def _scaled_cache(cache: CacheDesc, layer_cache, heads, dim, dtype: str, device):
+    """The codes of a scaled cache [2][num_blocks][block_size][heads][dim]: int8, or FP8 as uint8 or float8_e4m3fn."""
+    want = "int8"
+    if cache.dtype == _lib.IS_FP8_E4M3:
+        want = "float8_e4m3fn" if "float8_e4m3fn" in str(getattr(layer_cache, "dtype", "")) else "uint8"
+    return _typed("layer_cache", layer_cache, want, (2, cache.num_blocks, cache.block_size, heads, dim), device)
+
+
+def _scales(scales, cache: CacheDesc, heads: int, device):
+    return c_void_p(_ptr(_typed("scales", scales, "float32", (2, cache.num_blocks, heads), device)))
+
+
+def prepare_append_scaled(q, k, v, positions, slot_mapping, rope: RopeParams, cache: CacheDesc, layer_cache, scales, q_out,
+                          status_out, axes: RopeAxes | None = None, stream=None):
+    """is_append_scaled with every argument marshalled once: as prepare_append,
+    into a scaled cache (dtype "int8" or "e4m3"); scales float32
+    [2][num_blocks][heads], in and out."""
+    args, dev, H = _append_args(q, k, v, positions, slot_mapping, rope, cache, layer_cache, q_out, status_out, axes, True)
+    keep = (q, k, v, positions, slot_mapping, layer_cache, scales, q_out, status_out)
+    return _prepared("is_append_scaled", args, keep, stream, dev, _scales(scales, cache, H, dev))
+
+
+def is_append_scaled(*args, **kw) -> None:
+    """Rotate a step's queries and keys and write its K/V quantised; arguments as in the prepared form."""
+    prepare_append_scaled(*args, **kw)()
+
+
+def prepare_move_scaled(from_desc: CacheDesc, from_cache, from_slots, cache: CacheDesc, layer_cache, scales, slot_mapping,
+                        status_out, stream=None):
+    """is_move_scaled with every argument marshalled once: tokens at from_slots
+    (int64 [T]) of the plain layer cache from_cache, to slot_mapping (int64 [T])
+    of the scaled cache layer_cache, scales."""
+    dt, code = _float_code("from_cache", from_cache)
+    if from_cache.dim() != 5:
+        raise ValueError("from_cache must be [2][num_blocks][block_size][heads][head_dim]")
+    H, D = int(from_cache.shape[3]), int(from_cache.shape[4])
+    dev = _layer_cache(from_desc, from_cache, H, D, dt, None).device
+    T = int(_typed("from_slots", from_slots, "int64", (None,), dev).shape[0])
+    _typed("slot_mapping", slot_mapping, "int64", (T,), dev)
+    _scaled_cache(cache, layer_cache, H, D, dt, dev)
+    args = MoveArgs(T, H, D, code, _ptr(from_slots), _ptr(slot_mapping), _ptr(from_cache), _ptr(layer_cache),
+                    _scales(scales, cache, H, dev), _ptr(_typed("status_out", status_out, "int32", (1,), dev)),
+                    from_desc, cache, (ctypes.c_int32 * 2)(0, 0))
+    keep = (from_cache, from_slots, layer_cache, scales, slot_mapping, status_out)
+    return _prepared("is_move_scaled", args, keep, stream, dev)
+
+
+def is_move_scaled(*args, **kw) -> None:
+    """Tokens of a plain paged cache into a scaled one; arguments as in the prepared form."""
+    prepare_move_scaled(*args, **kw)()
+
+
+def prepare_read_scaled(slot_mapping, cache: CacheDesc, layer_cache, scales, k_out, v_out, status_out, positions=None,
+                        rope: RopeParams | None = None, axes: RopeAxes | None = None, stream=None):
+    """is_read_scaled with every argument marshalled once: the tokens at
+    slot_mapping (int64 [T]) as rows k_out and v_out [T][heads][head_dim] (one
+    may be None).  With positions (int32 [n_axes][T] or [T]) and rope the keys
+    are turned back to what they were before the rotation."""
+    like = k_out if k_out is not None else v_out
+    dt, code = _float_code("k_out", like)
+    if like.dim() != 3:
+        raise ValueError("k_out and v_out must be [tokens][heads][head_dim]")
+    T, H, D = (int(n) for n in like.shape)
+    dev = _typed("k_out", k_out, dt, (T, H, D), None, True)
+    dev = (dev if dev is not None else _typed("v_out", v_out, dt, (T, H, D))).device
+    _typed("v_out", v_out, dt, (T, H, D), dev, True)
+    _typed("slot_mapping", slot_mapping, "int64", (T,), dev)
+    _scaled_cache(cache, layer_cache, H, D, dt, dev)
+    if (positions is None) != (rope is None) or (positions is None and axes is not None):
+        raise ValueError("positions and rope go together, axes with them")
+    if positions is not None:
+        axes = make_axes() if axes is None else axes
+        _typed("positions", positions, "int32", (T,) if axes.n_axes == 1 and positions.dim() == 1 else (axes.n_axes, T), dev)
+    args = ReadArgs(T, H, D, code, 0 if rope is None else 1, 0, _ptr(slot_mapping), _ptr(positions), _ptr(layer_cache),
+                    _scales(scales, cache, H, dev), _ptr(k_out), _ptr(v_out),
+                    _ptr(_typed("status_out", status_out, "int32", (1,), dev)), RopeParams() if rope is None else rope,
+                    RopeAxes() if axes is None else axes, cache, 0)
+    keep = (slot_mapping, positions, layer_cache, scales, k_out, v_out, status_out)
+    return _prepared("is_read_scaled", args, keep, stream, dev)
+
+
+def is_read_scaled(*args, **kw) -> None:
+    """Tokens of a scaled cache back as rows; arguments as in the prepared form."""
+    prepare_read_scaled(*args, **kw)()
+
+
+def prepare_attend_scaled(q, seq_len, block_table, cache: CacheDesc, layer_cache, scales, out, workspace, status_out,
+                          q_start=None, max_q_len: int | None = None, scale: float | None = None, window: int = 0,
+                          lse_out=None, stream=None, budget_ns: int | None = None):
+    """is_attend_scaled with every argument marshalled once: as prepare_attend,
+    over a scaled cache (dtype "int8" or "e4m3"); scales float32
+    [2][num_blocks][heads]."""
+    args, dev, H = _attend_args(q, seq_len, block_table, cache, layer_cache, out, workspace, status_out, q_start, max_q_len,
+                                scale, window, lse_out, True)
+    keep = (q, q_start, seq_len, block_table, layer_cache, scales, out, lse_out, workspace, status_out)
+    at = _scales(scales, cache, H, dev)
+    if budget_ns is None:
+        return _prepared("is_attend_scaled", args, keep, stream, dev, at)
+    return _prepared("is_attend_scaled_within", args, keep, stream, dev, at, c_int64(budget_ns))
+
+
+def is_attend_scaled(*args, **kw) -> None:
+    """Attention of each request's last tokens over a scaled cache; arguments as in the prepared form."""
+    prepare_attend_scaled(*args, **kw)()
 
 
 def is_get_status(store: Store, stream=None) -> int:

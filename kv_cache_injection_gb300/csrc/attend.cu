@@ -4,18 +4,6 @@
 
 namespace isk {
 
-template <typename T, bool F8>
-static cudaError_t launch_mma(const AttendArgs& a, const LaunchCfg& cfg) {
-  // Two column tiles when a request has more than 8 rows: the keys are then
-  // read once for 16 rows.  At head_dim 256 their output would not fit the registers.
-  const bool two = (int64_t)a.max_q * a.G > 8;
-  if (a.D == 64)
-    return two ? launch_split<T, MmaEngine<T, F8, 64, 2>>(a, cfg) : launch_split<T, MmaEngine<T, F8, 64, 1>>(a, cfg);
-  if (a.D == 128)
-    return two ? launch_split<T, MmaEngine<T, F8, 128, 2>>(a, cfg) : launch_split<T, MmaEngine<T, F8, 128, 1>>(a, cfg);
-  return launch_split<T, MmaEngine<T, F8, 256, 1>>(a, cfg);
-}
-
 cudaError_t launch_attend(const AttendArgs& a, const LaunchCfg& cfg) {
   // Many rows go to the kernel of attend_prompt.cu, which reads the keys once
   // for 256 rows (128 at head_dim 256), from the number of rows on at which the
@@ -33,8 +21,8 @@ cudaError_t launch_attend(const AttendArgs& a, const LaunchCfg& cfg) {
   if (a.dtype != IS_F32 && (a.D <= 128 || !a.fp8) && a.G <= 64 && (int64_t)a.max_q * a.G > most && a.scale > 0.f)
     return launch_attend_prompt(a, cfg);
   if (a.dtype == IS_BF16)
-    return a.fp8 ? launch_mma<__nv_bfloat16, true>(a, cfg) : launch_mma<__nv_bfloat16, false>(a, cfg);
-  if (a.dtype == IS_F16) return a.fp8 ? launch_mma<__half, true>(a, cfg) : launch_mma<__half, false>(a, cfg);
+    return a.fp8 ? launch_mma<__nv_bfloat16, kCacheE4m3>(a, cfg) : launch_mma<__nv_bfloat16, kCachePlain>(a, cfg);
+  if (a.dtype == IS_F16) return a.fp8 ? launch_mma<__half, kCacheE4m3>(a, cfg) : launch_mma<__half, kCachePlain>(a, cfg);
   if (a.D == 64) return launch_split<float, FmaEngine<64>>(a, cfg);
   if (a.D == 128) return launch_split<float, FmaEngine<128>>(a, cfg);
   return launch_split<float, FmaEngine<256>>(a, cfg);

@@ -55,6 +55,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -117,6 +118,7 @@ struct TileMask {
   int key0;              // position of the tile's first key
   uint32_t valid;        // keys that are read (in range and named by the table)
   bool check;            // some row does not see some valid key, or a key is not valid
+  const float4* key;     // scaled cache: each key's K scale, log2 of its V scale, and 1 / V scale
 };
 
 // 16-byte chunk c of row `row`: rows of 128 bytes or more rotate their chunks
@@ -127,8 +129,11 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
   return (uint32_t)row * ROWB + (uint32_t)((ROWB >= 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) * 16);
 }
 
-template <typename T, bool F8, int D_, int NT>
+template <typename T, CacheKind KIND, int D_, int NT>
 struct MmaEngine {
+  static constexpr bool F8 = KIND != kCachePlain;               // 8-bit elements
+  static constexpr bool kInt8 = KIND == kCacheScaledInt8;
+  static constexpr bool kScaled = KIND == kCacheScaledE4m3 || KIND == kCacheScaledInt8;
   static constexpr int D = D_;
   static constexpr int kRows = 8 * NT;
   static constexpr int kRowBytes = F8 ? D : 2 * D;
@@ -240,15 +245,22 @@ struct MmaEngine {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             uint32_t k[4];
-            e4m3x4_f16x4(b[2 * u], k[0], k[2]);
-            e4m3x4_f16x4(b[2 * u + 1], k[1], k[3]);
+            codes_f16x4<kInt8>(b[2 * u], k[0], k[2]);
+            codes_f16x4<kInt8>(b[2 * u + 1], k[1], k[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816<M>(s[mt][nt], k, q[c + u][nt][0], q[c + u][nt][1]);
           }
         }
       }
     }
-    // Scaled logits (base 2), hidden keys at -inf.
+    // Scaled logits (base 2), hidden keys at -inf.  Over a scaled cache x is the logit plus log2 of the key's V scale.
+    float4 sk[kMt][2];                   // of keys mt * 16 + lane / 4 and that + 8
+    if constexpr (kScaled) {
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) sk[mt][h] = tm.key[mt * 16 + (lane >> 2) + 8 * h];
+    }
     bool over = false;
     float bound[NT][2];
 #pragma unroll
@@ -261,7 +273,13 @@ struct MmaEngine {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float x = __fmul_rn(s[mt][nt][e], sc[nt][e & 1]);   // not fused with - m: far logits
+          float x;
+          if constexpr (kScaled) {       // the product of the scales stays finite, so that 0 times it is 0
+            const float4 k = sk[mt][e >> 1];
+            x = fmaf(s[mt][nt][e], fminf(fmaxf(sc[nt][e & 1] * k.x, -FLT_MAX), FLT_MAX), k.y);
+          } else {
+            x = __fmul_rn(s[mt][nt][e], sc[nt][e & 1]);   // not fused with - m: far logits
+          }
           if (tm.check) {
             const int key = mt * 16 + (lane >> 2) + (e >> 1) * 8, j = tm.key0 + key;
             const bool see = ((tm.valid >> key) & 1u) && j <= lim[nt][e & 1] &&
@@ -301,8 +319,13 @@ struct MmaEngine {
       for (int mt = 0; mt < kMt; ++mt) {
         const float p0 = ex2(s[mt][nt][0] - m0), p1 = ex2(s[mt][nt][1] - m1);
         const float p2 = ex2(s[mt][nt][2] - m0), p3 = ex2(s[mt][nt][3] - m1);
-        l[nt][0] += p0 + p2;
-        l[nt][1] += p1 + p3;
+        if constexpr (kScaled) {         // p holds the V scale
+          l[nt][0] += fmaf(p0, sk[mt][0].z, p2 * sk[mt][1].z);
+          l[nt][1] += fmaf(p1, sk[mt][0].z, p3 * sk[mt][1].z);
+        } else {
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+        }
         // [key][row] pairs to the product's [row][key] pairs
         const uint32_t h0 = Vec<M>::pack2(p0, p1), h1 = Vec<M>::pack2(p2, p3);
         p[mt][nt][0] = movmatrix_t(h0);
@@ -340,8 +363,8 @@ struct MmaEngine {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             uint32_t v[4];
-            e4m3x4_f16x4(__byte_perm(b[2 * u], 0, 0x3120), v[0], v[1]);
-            e4m3x4_f16x4(__byte_perm(b[2 * u + 1], 0, 0x3120), v[2], v[3]);
+            codes_f16x4_even_odd<kInt8>(b[2 * u], v[0], v[1]);
+            codes_f16x4_even_odd<kInt8>(b[2 * u + 1], v[2], v[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma16816<M>(o[c + u][nt], v, p[mt][nt][0], p[mt][nt][1]);
@@ -382,6 +405,7 @@ struct MmaEngine {
 // memory.
 template <int D_>
 struct FmaEngine {
+  static constexpr bool kScaled = false;
   static constexpr int D = D_;
   static constexpr int kRows = 8;
   static constexpr int kRowBytes = 4 * D;
@@ -532,7 +556,8 @@ struct SplitShape {
   static constexpr int kJoinAt = (kStages - 1) * kTileBytes;
   static_assert(E::kRows * E::kPitch * 4 <= kTileBytes, "the output fits a tile");
   static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes + (size_t)E::kSharedQ * 4;
-  static constexpr int kFit = 227 * 1024 / (int)(kSmem + 2048);
+  static constexpr int kScaleBytes = E::kScaled ? kWarps * E::kKeys * (kStages * 8 + 16) : 0;   // static shared memory
+  static constexpr int kFit = 227 * 1024 / (int)(kSmem + 2048 + kScaleBytes);
   static constexpr int kPerSm = kFit < E::kMostPerSm ? kFit : E::kMostPerSm;
   static_assert(kPerSm >= 1, "a CTA fits an SM");
 };
@@ -617,6 +642,8 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
   __shared__ SplitSeg s_seg[2];
   __shared__ float s_ml[kWarps][2 * ROWS];
   __shared__ uint32_t s_valid[kWarps][S::kStages];
+  __shared__ float s_scale[E::kScaled ? kWarps : 1][S::kStages][2][E::kScaled ? KT : 1];   // the tiles' K and V scales
+  __shared__ float4 s_key[E::kScaled ? kWarps : 1][E::kScaled ? KT : 1];                   // TileMask::key
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float* outs = reinterpret_cast<const float*>(smem + S::kJoinAt);
   float* so = reinterpret_cast<float*>(smem + warp * S::kWarpBytes + S::kJoinAt);
@@ -665,6 +692,7 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
   int k_lo = 0, k_hi = 0, n_mine = 0;
   const int32_t* table = nullptr;
   const uint8_t* kbase = nullptr;
+  const float* scale_base = nullptr;
   int32_t id_next = -1, off_next = 0;
   auto look_up = [&](int i) {
     const int j = k_lo + (warp + i * kWarps) * KT + lane;
@@ -684,6 +712,13 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
       const long long off = id_next < 0 ? -1ll : ((long long)id_next * a.block_size + off_next) * token_bytes;
       const uint32_t valid = __ballot_sync(0xffffffffu, off >= 0);
       if (lane == 0) s_valid[warp][stage] = valid;
+      if constexpr (E::kScaled) {
+        if (lane < KT) {
+          const float* at = scale_base + (off < 0 ? 0 : (int64_t)id_next * a.H);
+          cp_async4(smem_addr(&s_scale[warp][stage][0][lane]), at, off >= 0);
+          cp_async4(smem_addr(&s_scale[warp][stage][1][lane]), at + (int64_t)a.num_blocks * a.H, off >= 0);
+        }
+      }
       look_up(i + 1);
       constexpr int CPR = E::kRowBytes / 16;             // chunks of a row
       constexpr int RPI = CPR >= 32 ? 1 : 32 / CPR;      // rows of one pass of the warp
@@ -711,6 +746,7 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
     k_hi = g.k_hi;
     table = a.block_table + (size_t)g.r * a.max_blocks;
     kbase = a.k_cache + (size_t)g.head * E::kRowBytes;
+    if constexpr (E::kScaled) scale_base = a.scales + g.head;
     const int n_tiles = k_hi > k_lo ? (k_hi - k_lo + KT - 1) / KT : 0;
     n_mine = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
     look_up(0);
@@ -742,6 +778,18 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
           __syncwarp();                  // every lane's part of tile i has landed, and all are done with tile i - 1
           TileMask tm;
           tm.valid = s_valid[warp][s];
+          if constexpr (E::kScaled) {    // lane i has key i; one whose scales are out of range is hidden
+            const float ks = lane < KT ? s_scale[warp][s][0][lane] : 1.f, vs = lane < KT ? s_scale[warp][s][1][lane] : 1.f;
+            const bool ok = scale_ok(ks) && scale_ok(vs);
+            const uint32_t good = __ballot_sync(0xffffffffu, ok);
+            if (tm.valid & ~good) {
+              if (lane == 0) latch(a.status, IS_ST_SCALE);
+              tm.valid &= good;
+            }
+            if (lane < KT) s_key[warp][lane] = ok ? make_float4(ks, log2f(vs), 1.f / vs, 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
+            __syncwarp();
+            tm.key = s_key[warp];
+          }
           issue(i + S::kStages - 1, (s + S::kStages - 1) % S::kStages);
           tm.key0 = k_lo + (warp + i * kWarps) * KT;
           constexpr uint32_t kFull = KT == 32 ? 0xffffffffu : (1u << KT) - 1u;
@@ -828,6 +876,19 @@ static cudaError_t launch_split(const AttendArgs& a, const LaunchCfg& cfg) {
     return launch_ex(attend_join_rows_kernel<T, E::kRows, E::D, false>, dim3(grid, 1), dim3(kJoinThreads), 0, cfg.stream, cfg.pdl, a);
   return launch_ex(attend_join_kernel<T, E::kRows, E::D>, dim3(grid, 4), dim3(kJoinThreads), 0, cfg.stream,
                    cfg.pdl, a);
+}
+
+// The split kernel's forms for 16-bit queries.
+template <typename T, CacheKind KIND>
+static cudaError_t launch_mma(const AttendArgs& a, const LaunchCfg& cfg) {
+  // Two column tiles when a request has more than 8 rows: the keys are then
+  // read once for 16 rows.  At head_dim 256 their output would not fit the registers.
+  const bool two = (int64_t)a.max_q * a.G > 8;
+  if (a.D == 64)
+    return two ? launch_split<T, MmaEngine<T, KIND, 64, 2>>(a, cfg) : launch_split<T, MmaEngine<T, KIND, 64, 1>>(a, cfg);
+  if (a.D == 128)
+    return two ? launch_split<T, MmaEngine<T, KIND, 128, 2>>(a, cfg) : launch_split<T, MmaEngine<T, KIND, 128, 1>>(a, cfg);
+  return launch_split<T, MmaEngine<T, KIND, 256, 1>>(a, cfg);
 }
 
 }  // namespace isk

@@ -167,6 +167,40 @@ struct AttendArgs {
   float v_scale;
   int32_t dtype, fp8;
   uint64_t wait_ns;             // limit of each wait of the kernel for prompts
+  const float* scales;          // scaled cache: [2][num_blocks][H]
+};
+
+// What a cache holds (is_attend and is_attend_scaled): the call's own type, E4M3
+// bytes under one scale, or codes with a scale for each block and head.
+enum CacheKind { kCachePlain = 0, kCacheE4m3 = 1, kCacheScaledE4m3 = 2, kCacheScaledInt8 = 3 };
+
+// Scales of blocks that are used; a block with another one counts as not there.
+constexpr float kSmallestScale = 9.094947017729282e-13f, kLargestScale = 1099511627776.f;   // 2^-40, 2^40
+__device__ __forceinline__ bool scale_ok(float s) { return s >= kSmallestScale && s <= kLargestScale; }
+
+// is_append_scaled and is_move_scaled with their checks done.
+struct ScaledWriteArgs {
+  AppendArgs a;                 // a move has no q, and k, v and strides of the cache it reads
+  const int64_t* from;          // [T] rows of k and v that the tokens take; null: row t
+  int64_t n_from;
+  float* scales;                // [2][num_blocks][H]
+  int64_t v_scales;             // num_blocks * H
+  int32_t block_size, block_shift;
+  int32_t int8, rotate;
+};
+
+// is_read_scaled with its checks done.
+struct ScaledReadArgs {
+  const uint8_t* k_cache;
+  int64_t v_offset, n_slots;
+  const float* scales;
+  int64_t v_scales;
+  const int64_t* slots;         // [T]
+  const int32_t* positions;     // [n_axes][T], or null: keys as they are
+  uint8_t* k_out;               // or null
+  uint8_t* v_out;
+  uint32_t* status;
+  int32_t T, H, D, n_axes, dtype, style, int8, block_size, block_shift;
 };
 
 // Uniform bins of the cosine in [-1, 1] used by the top-k's first pass.
@@ -331,6 +365,60 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float* x, float r) {
     }
   }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// Eight fp32 values times r into eight INT8 codes: nearest even, saturated to
+// +-127; NaN gives 0.
+__device__ __forceinline__ uint2 to_int8x8(const float* x, float r) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = max(__float2int_rn(__fmul_rn(x[4 * h + e], r)), -127);
+    uint32_t hi;
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"(c[3]), "r"(c[2]), "r"(0));
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w[h]) : "r"(c[1]), "r"(c[0]), "r"(hi));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Four E4M3 bytes as fp16 values, exact: lo of bytes 0 and 1, hi of bytes 2 and 3.
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+
+// Two INT8 codes (bytes A and B of x + 128, four of them in a register) as fp16
+// values: under the exponent of 1024 a byte adds itself, and 1152 comes off; exact.
+template <int A, int B>
+__device__ __forceinline__ uint32_t biased_f16x2(uint32_t x) {
+  const uint32_t w = __byte_perm(x, 0x64646464u, A | 0x40 | (B << 8) | 0x4000), off = 0x64806480u;
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&off));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Four codes as fp16 values: lo of bytes 0 and 1, hi of bytes 2 and 3.
+template <bool I8>
+__device__ __forceinline__ void codes_f16x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  if constexpr (I8) {
+    const uint32_t u = x ^ 0x80808080u;
+    lo = biased_f16x2<0, 1>(u);
+    hi = biased_f16x2<2, 3>(u);
+  } else {
+    e4m3x4_f16x4(x, lo, hi);
+  }
+}
+// The same with lo of bytes 0 and 2, hi of bytes 1 and 3.
+template <bool I8>
+__device__ __forceinline__ void codes_f16x4_even_odd(uint32_t x, uint32_t& even, uint32_t& odd) {
+  if constexpr (I8) {
+    const uint32_t u = x ^ 0x80808080u;
+    even = biased_f16x2<0, 2>(u);
+    odd = biased_f16x2<1, 3>(u);
+  } else {
+    e4m3x4_f16x4(__byte_perm(x, 0, 0x3120), even, odd);
+  }
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) {

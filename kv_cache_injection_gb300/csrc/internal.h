@@ -99,6 +99,11 @@ cudaError_t launch_append(const AppendArgs& a, const AxisTurns& turns, const Lau
 cudaError_t launch_attend(const AttendArgs& a, const LaunchCfg& cfg);
 cudaError_t launch_attend_prompt(const AttendArgs& a, const LaunchCfg& cfg);
 
+// The same over a cache with a scale for each block and head.
+cudaError_t launch_scaled_write(const ScaledWriteArgs& p, const AxisTurns& turns, const LaunchCfg& cfg);
+cudaError_t launch_scaled_read(const ScaledReadArgs& a, const AxisTurns& turns, const LaunchCfg& cfg);
+cudaError_t launch_attend_scaled(const AttendArgs& a, bool int8, const LaunchCfg& cfg);
+
 // Whether a row of row_bytes (K or V of one layer) and R requests fit the
 // inject kernel's shared-memory plan.
 bool inject_shape_ok(int row_bytes, int R);

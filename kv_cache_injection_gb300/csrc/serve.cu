@@ -1,7 +1,9 @@
 // C ABI of the serving step around the segment: argument checks and launches of
-// is_extend_block_table, is_append and is_attend.  They keep no state but a
-// thread's last rotation table, which its parameters determine (axis_turns): the
-// device comes from the call's buffers, everything else from its arguments.
+// is_extend_block_table, is_append and is_attend, and of their forms over a cache
+// with a scale for each block (is_append_scaled, is_move_scaled, is_read_scaled,
+// is_attend_scaled).  They keep no state but a thread's last rotation table,
+// which its parameters determine (axis_turns): the device comes from the call's
+// buffers, everything else from its arguments.
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -87,6 +89,24 @@ is_status_t check_layer_cache(const is_cache_desc_t& c, int dtype, const void* l
   }
   if (!aligned16(layer_cache)) return refuse(IS_ERR_INVALID_ARG, "layer_cache must be 16-byte aligned");
   return IS_OK;
+}
+
+// A scaled cache goes with every type of the call; the scales are the blocks' own.
+is_status_t check_scaled_cache(const is_cache_desc_t& c, const void* layer_cache) {
+  if (c.block_size < 1 || c.block_size > IS_MAX_POSITION || c.num_blocks < 1)
+    return refuse(IS_ERR_INVALID_ARG, "block_size must be in [1, IS_MAX_POSITION], num_blocks >= 1");
+  if (c.dtype != IS_INT8 && c.dtype != IS_FP8_E4M3)
+    return refuse(IS_ERR_INVALID_ARG, "a scaled cache is IS_INT8 or IS_FP8_E4M3, not %d", c.dtype);
+  if (c.k_scale != 1.f || c.v_scale != 1.f)
+    return refuse(IS_ERR_INVALID_ARG, "k_scale and v_scale must be 1: a scaled cache has the blocks' scales");
+  if (!aligned16(layer_cache)) return refuse(IS_ERR_INVALID_ARG, "layer_cache must be 16-byte aligned");
+  return IS_OK;
+}
+
+int shift_of(int32_t block_size) {
+  for (int s = 0; s <= 24; ++s)
+    if (block_size == 1 << s) return s;
+  return -1;
 }
 
 bool valid_dtype(int dt) { return dt == IS_F32 || dt == IS_BF16 || dt == IS_F16; }
@@ -182,7 +202,11 @@ extern "C" is_status_t is_extend_block_table(const is_extend_args_t* a, cudaStre
   return launched(launch_extend(*a, LaunchCfg{stream, sms_of(dev), true}), "is_extend_block_table launch");
 }
 
-extern "C" is_status_t is_append(const is_append_args_t* a, cudaStream_t stream) {
+// The checks of is_append, or with `scaled` of is_append_scaled; *p is filled
+// unless there are no tokens (p->T 0).
+static is_status_t check_append(const is_append_args_t* a, bool scaled, const float* scales, AppendArgs* out,
+                                const AxisTurns** turns_out, int* dev) {
+  out->T = 0;
   if (!a) return refuse(IS_ERR_INVALID_ARG, "args are NULL");
   const int T = a->num_tokens, Hq = a->num_q_heads, H = a->num_kv_heads, D = a->head_dim;
   if (T < 0 || Hq < 0 || H < 1) return refuse(IS_ERR_INVALID_ARG, "num_tokens, num_q_heads >= 0, num_kv_heads >= 1");
@@ -191,11 +215,10 @@ extern "C" is_status_t is_append(const is_append_args_t* a, cudaStream_t stream)
   if (D < 16 || D > IS_MAX_HEAD_DIM || (D & (D - 1)) != 0)
     return refuse(IS_ERR_UNSUPPORTED, "head_dim must be a power of two in [16, IS_MAX_HEAD_DIM]");
   if (Hq > (1 << 16) || H > (1 << 16)) return refuse(IS_ERR_UNSUPPORTED, "at most 65536 heads");
-  is_status_t st = check_layer_cache(a->cache, a->dtype, a->layer_cache);
+  is_status_t st = scaled ? check_scaled_cache(a->cache, a->layer_cache) : check_layer_cache(a->cache, a->dtype, a->layer_cache);
   if (st != IS_OK) return st;
   const int e = a->dtype == IS_F32 ? 4 : 2, ve = 16 / e;
-  const AxisTurns* turns = nullptr;
-  st = axis_turns(a->rope, a->axes, D, &turns);
+  st = axis_turns(a->rope, a->axes, D, turns_out);
   if (st != IS_OK) return st;
   const int vecs = a->rope.style == 0 ? D / 2 / ve : D / ve;
   if (vecs < 1 || vecs > 32)
@@ -203,7 +226,7 @@ extern "C" is_status_t is_append(const is_append_args_t* a, cudaStream_t stream)
                   a->rope.style == 0 ? "half head (max 32)" : "head (max 32)");
   if (T == 0) return IS_OK;
   if (!a->k || !a->v || !a->positions || !a->slot_mapping || !a->layer_cache || !a->status_out ||
-      (Hq > 0 && (!a->q || !a->q_out)))
+      (Hq > 0 && (!a->q || !a->q_out)) || (scaled && !scales))
     return refuse(IS_ERR_INVALID_ARG, "a required pointer is NULL");
   const int64_t qrow = (int64_t)Hq * D, row = (int64_t)H * D;
   if ((Hq > 0 && T > 1 && a->q_stride < qrow) || (T > 1 && (a->k_stride < row || a->v_stride < row)))
@@ -212,24 +235,22 @@ extern "C" is_status_t is_append(const is_append_args_t* a, cudaStream_t stream)
   if ((T > 1 && ((qs | ks | vs) & 15)) || !aligned16(a->k) || !aligned16(a->v) ||
       (Hq > 0 && (!aligned16(a->q) || !aligned16(a->q_out))))
     return refuse(IS_ERR_INVALID_ARG, "rows of q, k, v and q_out must be 16-byte aligned");
-  const int c = a->cache.dtype == IS_FP8_E4M3 ? 1 : e;
+  const int c = scaled || a->cache.dtype == IS_FP8_E4M3 ? 1 : e;
   const int64_t slots = (int64_t)a->cache.num_blocks * a->cache.block_size;
   const Span sq("q", Hq > 0 ? a->q : nullptr, (T - 1) * qs + qrow * e);
   const Span ins[] = {{"k", a->k, (T - 1) * ks + row * e}, {"v", a->v, (T - 1) * vs + row * e},
                       {"positions", a->positions, 4LL * T * a->axes.n_axes}, {"slot_mapping", a->slot_mapping, 8LL * T},
                       sq};
   const Span outs[] = {{"layer_cache", a->layer_cache, 2 * slots * row * c}, {"status_out", a->status_out, 4},
-                       {"q_out", Hq > 0 ? a->q_out : nullptr, T * qrow * e}};
+                       {"scales", scales, 8LL * a->cache.num_blocks * H}, {"q_out", Hq > 0 ? a->q_out : nullptr, T * qrow * e}};
   const bool in_place = Hq > 0 && a->q == a->q_out && (T == 1 || a->q_stride == qrow);
-  st = check_apart(outs, 2, ins, 5);
-  if (st == IS_OK) st = check_apart(outs + 2, 1, ins, in_place ? 4 : 5);
-  if (st == IS_OK) st = check_apart(outs, 3, nullptr, 0);
-  if (st != IS_OK) return st;
-  int dev = 0;
-  st = device_of(a->layer_cache, "layer_cache", &dev);
+  st = check_apart(outs, 3, ins, 5);
+  if (st == IS_OK) st = check_apart(outs + 3, 1, ins, in_place ? 4 : 5);
+  if (st == IS_OK) st = check_apart(outs, 4, nullptr, 0);
+  if (st == IS_OK) st = device_of(a->layer_cache, "layer_cache", dev);
   if (st != IS_OK) return st;
 
-  AppendArgs p{};
+  AppendArgs& p = *out;
   p.q = static_cast<const uint8_t*>(a->q);
   p.k = static_cast<const uint8_t*>(a->k);
   p.v = static_cast<const uint8_t*>(a->v);
@@ -255,15 +276,147 @@ extern "C" is_status_t is_append(const is_append_args_t* a, cudaStream_t stream)
     p.k_inv = (float)(1.0 / (double)a->cache.k_scale);
     p.v_inv = (float)(1.0 / (double)a->cache.v_scale);
   }
+  return IS_OK;
+}
+
+extern "C" is_status_t is_append(const is_append_args_t* a, cudaStream_t stream) {
+  AppendArgs p{};
+  const AxisTurns* turns = nullptr;
+  int dev = 0;
+  const is_status_t st = check_append(a, false, nullptr, &p, &turns, &dev);
+  if (st != IS_OK || p.T == 0) return st;
   DeviceGuard g(dev);
   return launched(launch_append(p, *turns, LaunchCfg{stream, sms_of(dev), true}), "is_append launch");
 }
 
-extern "C" is_status_t is_attend(const is_attend_args_t* args, cudaStream_t stream) {
-  return is_attend_within(args, (int64_t)kWaitBudgetNs, stream);
+extern "C" is_status_t is_append_scaled(const is_append_args_t* a, float* scales, cudaStream_t stream) {
+  ScaledWriteArgs w{};
+  const AxisTurns* turns = nullptr;
+  int dev = 0;
+  const is_status_t st = check_append(a, true, scales, &w.a, &turns, &dev);
+  if (st != IS_OK || w.a.T == 0) return st;
+  w.scales = scales;
+  w.v_scales = (int64_t)a->cache.num_blocks * w.a.H;
+  w.block_size = a->cache.block_size;
+  w.block_shift = shift_of(w.block_size);
+  w.int8 = a->cache.dtype == IS_INT8;
+  w.rotate = 1;
+  DeviceGuard g(dev);
+  return launched(launch_scaled_write(w, *turns, LaunchCfg{stream, sms_of(dev), true}), "is_append_scaled launch");
 }
 
-extern "C" is_status_t is_attend_within(const is_attend_args_t* a, int64_t budget_ns, cudaStream_t stream) {
+// Tokens, heads and head_dim of a call that moves or reads rows of a scaled cache.
+static is_status_t check_rows(int T, int H, int D, int dtype) {
+  if (T < 0 || H < 1) return refuse(IS_ERR_INVALID_ARG, "num_tokens >= 0, num_kv_heads >= 1");
+  if (!valid_dtype(dtype)) return refuse(IS_ERR_INVALID_ARG, "bad dtype");
+  if (D < 16 || D > IS_MAX_HEAD_DIM || (D & (D - 1)) != 0)
+    return refuse(IS_ERR_UNSUPPORTED, "head_dim must be a power of two in [16, IS_MAX_HEAD_DIM]");
+  if (H > (1 << 16)) return refuse(IS_ERR_UNSUPPORTED, "at most 65536 heads");
+  if (D * (dtype == IS_F32 ? 4 : 2) > 1024) return refuse(IS_ERR_UNSUPPORTED, "head_dim %d is too wide for fp32", D);
+  return IS_OK;
+}
+
+extern "C" is_status_t is_move_scaled(const is_move_args_t* a, cudaStream_t stream) {
+  if (!a) return refuse(IS_ERR_INVALID_ARG, "args are NULL");
+  const int T = a->num_tokens, H = a->num_kv_heads, D = a->head_dim;
+  is_status_t st = check_rows(T, H, D, a->dtype);
+  if (st == IS_OK && (a->reserved[0] | a->reserved[1]) != 0) st = refuse(IS_ERR_INVALID_ARG, "reserved must be 0");
+  if (st == IS_OK && a->from.dtype == IS_FP8_E4M3) st = refuse(IS_ERR_UNSUPPORTED, "from_cache must be f32, bf16 or f16");
+  if (st == IS_OK) st = check_layer_cache(a->from, a->dtype, a->from_cache);
+  if (st == IS_OK) st = check_scaled_cache(a->cache, a->layer_cache);
+  if (st != IS_OK || T == 0) return st;
+  if (!a->from_slots || !a->slot_mapping || !a->from_cache || !a->layer_cache || !a->scales || !a->status_out)
+    return refuse(IS_ERR_INVALID_ARG, "a required pointer is NULL");
+  const int64_t row = (int64_t)H * D, e = a->dtype == IS_F32 ? 4 : 2;
+  const int64_t slots = (int64_t)a->cache.num_blocks * a->cache.block_size;
+  const int64_t from_slots = (int64_t)a->from.num_blocks * a->from.block_size;
+  const Span ins[] = {{"from_slots", a->from_slots, 8LL * T}, {"slot_mapping", a->slot_mapping, 8LL * T},
+                      {"from_cache", a->from_cache, 2 * from_slots * row * e}};
+  const Span outs[] = {{"layer_cache", a->layer_cache, 2 * slots * row}, {"scales", a->scales, 8LL * a->cache.num_blocks * H},
+                       {"status_out", a->status_out, 4}};
+  st = check_apart(outs, 3, ins, 3);
+  int dev = 0;
+  if (st == IS_OK) st = device_of(a->layer_cache, "layer_cache", &dev);
+  if (st != IS_OK) return st;
+  ScaledWriteArgs w{};
+  w.a.k = static_cast<const uint8_t*>(a->from_cache);
+  w.a.v = w.a.k + from_slots * row * e;
+  w.a.k_stride = w.a.v_stride = row * e;
+  w.a.slots = a->slot_mapping;
+  w.a.k_cache = static_cast<uint8_t*>(a->layer_cache);
+  w.a.v_offset = slots * row;
+  w.a.n_slots = slots;
+  w.a.status = a->status_out;
+  w.a.T = T;
+  w.a.H = H;
+  w.a.D = D;
+  w.a.dtype = a->dtype;
+  w.from = a->from_slots;
+  w.n_from = from_slots;
+  w.scales = a->scales;
+  w.v_scales = (int64_t)a->cache.num_blocks * H;
+  w.block_size = a->cache.block_size;
+  w.block_shift = shift_of(w.block_size);
+  w.int8 = a->cache.dtype == IS_INT8;
+  static const AxisTurns none{};
+  DeviceGuard g(dev);
+  return launched(launch_scaled_write(w, none, LaunchCfg{stream, sms_of(dev), true}), "is_move_scaled launch");
+}
+
+extern "C" is_status_t is_read_scaled(const is_read_args_t* a, cudaStream_t stream) {
+  if (!a) return refuse(IS_ERR_INVALID_ARG, "args are NULL");
+  const int T = a->num_tokens, H = a->num_kv_heads, D = a->head_dim;
+  is_status_t st = check_rows(T, H, D, a->dtype);
+  if (st == IS_OK && (a->reserved | a->reserved2) != 0) st = refuse(IS_ERR_INVALID_ARG, "reserved must be 0");
+  if (st == IS_OK && a->unrotate != 0 && a->unrotate != 1) st = refuse(IS_ERR_INVALID_ARG, "unrotate must be 0 or 1");
+  if (st == IS_OK) st = check_scaled_cache(a->cache, a->layer_cache);
+  static const AxisTurns none{};
+  const AxisTurns* turns = &none;
+  if (st == IS_OK && a->unrotate) st = axis_turns(a->rope, a->axes, D, &turns);
+  if (st != IS_OK) return st;
+  const int64_t row = (int64_t)H * D, e = a->dtype == IS_F32 ? 4 : 2;
+  if (a->unrotate && a->rope.style == 1 && D * e > 512)
+    return refuse(IS_ERR_UNSUPPORTED, "head_dim %d with this dtype is too wide for interleaved pairs", D);
+  if (T == 0) return IS_OK;
+  if (!a->slot_mapping || !a->layer_cache || !a->scales || !a->status_out || (!a->k_out && !a->v_out) ||
+      (a->unrotate && !a->positions))
+    return refuse(IS_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(a->k_out) || !aligned16(a->v_out)) return refuse(IS_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  const int64_t slots = (int64_t)a->cache.num_blocks * a->cache.block_size;
+  const Span ins[] = {{"slot_mapping", a->slot_mapping, 8LL * T},
+                      {"positions", a->unrotate ? a->positions : nullptr, 4LL * T * (a->unrotate ? a->axes.n_axes : 0)},
+                      {"layer_cache", a->layer_cache, 2 * slots * row}, {"scales", a->scales, 8LL * a->cache.num_blocks * H}};
+  const Span outs[] = {{"k_out", a->k_out, T * row * e}, {"v_out", a->v_out, T * row * e}, {"status_out", a->status_out, 4}};
+  st = check_apart(outs, 3, ins, 4);
+  int dev = 0;
+  if (st == IS_OK) st = device_of(a->layer_cache, "layer_cache", &dev);
+  if (st != IS_OK) return st;
+  ScaledReadArgs r{};
+  r.k_cache = static_cast<const uint8_t*>(a->layer_cache);
+  r.v_offset = slots * row;
+  r.n_slots = slots;
+  r.scales = a->scales;
+  r.v_scales = (int64_t)a->cache.num_blocks * H;
+  r.slots = a->slot_mapping;
+  r.positions = a->unrotate ? a->positions : nullptr;
+  r.k_out = static_cast<uint8_t*>(a->k_out);
+  r.v_out = static_cast<uint8_t*>(a->v_out);
+  r.status = a->status_out;
+  r.T = T;
+  r.H = H;
+  r.D = D;
+  r.n_axes = a->unrotate ? a->axes.n_axes : 0;
+  r.dtype = a->dtype;
+  r.style = a->rope.style;
+  r.int8 = a->cache.dtype == IS_INT8;
+  r.block_size = a->cache.block_size;
+  r.block_shift = shift_of(r.block_size);
+  DeviceGuard g(dev);
+  return launched(launch_scaled_read(r, *turns, LaunchCfg{stream, sms_of(dev), true}), "is_read_scaled launch");
+}
+
+// is_attend_within, or with `scaled` is_attend_scaled_within.
+static is_status_t attend(const is_attend_args_t* a, bool scaled, const float* scales, int64_t budget_ns, cudaStream_t stream) {
   if (!a) return refuse(IS_ERR_INVALID_ARG, "args are NULL");
   if (budget_ns < 0 || budget_ns > (int64_t)kWaitBudgetNs)
     return refuse(IS_ERR_INVALID_ARG, "budget_ns must be in [0, %llu]", (unsigned long long)kWaitBudgetNs);
@@ -279,11 +432,13 @@ extern "C" is_status_t is_attend_within(const is_attend_args_t* a, int64_t budge
   if (D != 64 && D != 128 && D != 256) return refuse(IS_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
   if (Hq > (1 << 16) || (int64_t)T * Hq > (1 << 30))
     return refuse(IS_ERR_UNSUPPORTED, "at most 65536 heads and 2^30 rows (num_tokens * num_q_heads)");
-  is_status_t st = check_layer_cache(a->cache, a->dtype, a->layer_cache);
+  is_status_t st = scaled ? check_scaled_cache(a->cache, a->layer_cache) : check_layer_cache(a->cache, a->dtype, a->layer_cache);
+  if (st == IS_OK && scaled && a->dtype == IS_F32) st = refuse(IS_ERR_UNSUPPORTED, "a scaled cache is attended with bf16 or fp16");
   if (st != IS_OK) return st;
   if (!a->q_start && T < R) return refuse(IS_ERR_INVALID_ARG, "without q_start there is one row per request");
   if (T == 0) return IS_OK;
-  if (!a->q || !a->seq_len || !a->block_table || !a->layer_cache || !a->out || !a->workspace || !a->status_out)
+  if (!a->q || !a->seq_len || !a->block_table || !a->layer_cache || !a->out || !a->workspace || !a->status_out ||
+      (scaled && !scales))
     return refuse(IS_ERR_INVALID_ARG, "a required pointer is NULL");
   if (a->workspace_bytes < IS_ATTEND_WORKSPACE_BYTES)
     return refuse(IS_ERR_INVALID_ARG, "workspace must hold IS_ATTEND_WORKSPACE_BYTES");
@@ -295,14 +450,14 @@ extern "C" is_status_t is_attend_within(const is_attend_args_t* a, int64_t budge
     return refuse(IS_ERR_INVALID_ARG, "rows of q must be 16-byte aligned");
   if (((uintptr_t)a->out | (uintptr_t)a->workspace) & 31)
     return refuse(IS_ERR_INVALID_ARG, "out and workspace must be 32-byte aligned");
-  const int c = a->cache.dtype == IS_FP8_E4M3 ? 1 : e;
+  const int c = scaled || a->cache.dtype == IS_FP8_E4M3 ? 1 : e;
   const int64_t slots = (int64_t)a->cache.num_blocks * a->cache.block_size;
   const Span ins[] = {{"q", a->q, (T - 1) * qs + qrow * e}, {"q_start", a->q_start, 4LL * (R + 1)},
                       {"seq_len", a->seq_len, 4LL * R}, {"block_table", a->block_table, 4LL * R * a->max_blocks_per_seq},
-                      {"layer_cache", a->layer_cache, 2 * slots * row * c}};
+                      {"layer_cache", a->layer_cache, 2 * slots * row * c}, {"scales", scales, 8LL * a->cache.num_blocks * H}};
   const Span outs[] = {{"out", a->out, T * qrow * e}, {"lse_out", a->lse_out, 4LL * T * Hq},
                        {"workspace", a->workspace, IS_ATTEND_WORKSPACE_BYTES}, {"status_out", a->status_out, 4}};
-  st = check_apart(outs, 4, ins, 5);
+  st = check_apart(outs, 4, ins, 6);
   if (st != IS_OK) return st;
   int dev = 0;
   st = device_of(a->out, "out", &dev);
@@ -331,15 +486,33 @@ extern "C" is_status_t is_attend_within(const is_attend_args_t* a, int64_t budge
   p.max_blocks = a->max_blocks_per_seq;
   p.block_size = a->cache.block_size;
   p.num_blocks = a->cache.num_blocks;
-  p.block_shift = -1;
-  for (int s = 0; s <= 24; ++s)
-    if (a->cache.block_size == 1 << s) p.block_shift = s;
+  p.block_shift = shift_of(p.block_size);
   p.window = a->window;
   p.dtype = a->dtype;
   p.fp8 = a->cache.dtype == IS_FP8_E4M3;
   p.scale = p.fp8 ? a->scale * a->cache.k_scale : a->scale;
   p.v_scale = p.fp8 ? a->cache.v_scale : 1.f;
   p.wait_ns = (uint64_t)budget_ns;
+  p.scales = scales;
   DeviceGuard g(dev);
-  return launched(launch_attend(p, LaunchCfg{stream, sms_of(dev), true}), "is_attend launch");
+  const LaunchCfg cfg{stream, sms_of(dev), true};
+  if (scaled) return launched(launch_attend_scaled(p, a->cache.dtype == IS_INT8, cfg), "is_attend_scaled launch");
+  return launched(launch_attend(p, cfg), "is_attend launch");
+}
+
+extern "C" is_status_t is_attend(const is_attend_args_t* args, cudaStream_t stream) {
+  return attend(args, false, nullptr, (int64_t)kWaitBudgetNs, stream);
+}
+
+extern "C" is_status_t is_attend_within(const is_attend_args_t* args, int64_t budget_ns, cudaStream_t stream) {
+  return attend(args, false, nullptr, budget_ns, stream);
+}
+
+extern "C" is_status_t is_attend_scaled(const is_attend_args_t* args, const float* scales, cudaStream_t stream) {
+  return attend(args, true, scales, (int64_t)kWaitBudgetNs, stream);
+}
+
+extern "C" is_status_t is_attend_scaled_within(const is_attend_args_t* args, const float* scales, int64_t budget_ns,
+                                               cudaStream_t stream) {
+  return attend(args, true, scales, budget_ns, stream);
 }
