@@ -302,13 +302,20 @@ __device__ __forceinline__ uint32_t bits_between(int at, int lo, int hi) {
   return (h - l == 32 ? 0xffffffffu : ((1u << (h - l)) - 1u)) << l;
 }
 
-// Eight E4M3 bytes as eight fp16 values, exact.
+// Eight 8-bit elements as eight fp16 values, exact.
+template <bool I8>
 __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
   uint4 r;
-  e4m3x4_f16x4(lo, r.x, r.y);
-  e4m3x4_f16x4(hi, r.z, r.w);
+  codes_f16x4<I8>(lo, r.x, r.y);
+  codes_f16x4<I8>(hi, r.z, r.w);
   return r;
 }
+
+// Scaled cache: what eight keys of a block share is K scale, log2 of the V scale
+// and 1 / V scale.  A row's factor to their logits stays finite, so that 0 times
+// it is 0; sc > 0.
+constexpr int kGroup = 8;
+__device__ __forceinline__ float group_factor(float sc, float ks) { return fminf(sc * ks, FLT_MAX); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -332,9 +339,9 @@ __device__ __forceinline__ uint32_t at_chunk(int row, int c) {
 // logits S is read before the 16 columns of their weights, which lie before the
 // next ones', are written.  A function of its own, since inside the loop it costs
 // the other rows registers: the long prompts take 403 us instead of 392.
-template <typename W>
+template <typename W, bool SC>
 __device__ __noinline__ float far_weights(uint32_t s_col, float sc, float m, float l, uint4 named, int key0, int low, int end,
-                                          uint32_t p_full, int lane) {
+                                          uint32_t p_full, int lane, const float4* groups) {
   const float mz = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -346,10 +353,18 @@ __device__ __noinline__ float far_weights(uint32_t s_col, float sc, float m, flo
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float w[2];
+      if constexpr (SC) {
+        const float4 k = groups[(32 * c + 2 * i) / kGroup];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        w[e] = (see >> (2 * i + e)) & 1u ? ex2(__fsub_rn(__fmul_rn(__uint_as_float(y[2 * i + e]), sc), mz)) : 0.f;
-      l += w[0] + w[1];
+        for (int e = 0; e < 2; ++e)
+          w[e] = (see >> (2 * i + e)) & 1u ? ex2(__fsub_rn(fmaf(__uint_as_float(y[2 * i + e]), group_factor(sc, k.x), k.y), mz)) : 0.f;
+        l = fmaf(w[0] + w[1], k.z, l);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          w[e] = (see >> (2 * i + e)) & 1u ? ex2(__fsub_rn(__fmul_rn(__uint_as_float(y[2 * i + e]), sc), mz)) : 0.f;
+        l += w[0] + w[1];
+      }
       p[i] = Vec<W>::pack2(w[0], w[1]);
     }
     tmem_st16(s_col + 16 * c, p);
@@ -364,9 +379,11 @@ __device__ __noinline__ float far_weights(uint32_t s_col, float sc, float m, flo
 }
 
 // LIMITED: the limit of the waits is the call's.  (As a variable in the ordinary form it costs 16 prompts 1.2 us of 53.4.)
-template <typename T, bool F8, int D, bool LIMITED>
+template <typename T, CacheKind KIND, int D, bool LIMITED>
 __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a, int per, int box,
                                                                    const __grid_constant__ CUtensorMap rows_map) {
+  constexpr bool F8 = KIND != kCachePlain, kInt8 = KIND == kCacheScaledInt8;   // F8: 8-bit elements
+  constexpr bool kScaled = KIND == kCacheScaledE4m3 || KIND == kCacheScaledInt8;
   using S = Shape<D, F8>;
   const uint64_t limit_ns = LIMITED ? a.wait_ns : kWaitBudgetNs;
   // FP8 keys and values are exact in fp16, and a bf16 query row scaled by a power of two (undone in the logits) loses
@@ -381,6 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   __shared__ __align__(16) uint32_t s_mask[kMaskRing][4];
   __shared__ uint32_t s_raw_mask[S::kRaw][4];
   __shared__ float s_unscale[kShift ? S::kRows : 1];
+  // Scaled cache, by groups of eight keys: K and V scales as they are found, and what the softmax takes of them.
+  __shared__ float2 s_raw_group[kScaled ? S::kRaw : 1][kScaled ? kKeys / kGroup : 1];
+  __shared__ float4 s_group[kScaled ? kMaskRing : 1][kScaled ? kKeys / kGroup : 1];
   __shared__ int64_t scratch[33];
   __shared__ int64_t s_base;
   __shared__ int32_t s_req;
@@ -394,6 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&s_tmem), kTmemAll);
     tmem_relinquish();
+  }
+  if constexpr (kScaled) {               // groups without a key in use keep scales that are numbers
+    for (int i = tid; i < S::kRaw * (kKeys / kGroup); i += kThreads) s_raw_group[0][i] = make_float2(1.f, 1.f);
   }
   if (tid == 0) {
     s_abort = 0;
@@ -520,6 +543,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
             return max3(max3(t0, t1, __uint_as_float(y[30])), __uint_as_float(y[31]), t0);
           };
+          // Scaled cache: the largest of logit + log2 of the V scale, which grows with the logits of a group.
+          const float4* groups = s_group[kScaled ? slot : 0];
+          auto top_scaled = [&](const uint32_t(&y)[32], int c) {
+            float most = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 32 / kGroup; ++g) {
+              const float4 k = groups[c * (32 / kGroup) + g];
+              const uint32_t* v = y + g * kGroup;
+              float x0 = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+              const float x1 = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+              x0 = max3(x0, __uint_as_float(v[6]), __uint_as_float(v[7]));
+              most = fmaxf(most, fmaf(fmaxf(x0, x1), group_factor(sc, k.x), k.y));
+            }
+            return most;
+          };
           tmem_wait_ld();
           tmem_ld32(s_col + 64, x[2]);
           tmem_ld32(s_col + 96, x[3]);
@@ -527,13 +565,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             hide(x[0], mw.x, key0);
             hide(x[1], mw.y, key0 + 32);
           }
-          float mx = fmaxf(top(x[0]), top(x[1]));
+          float mx;
+          if constexpr (kScaled) {
+            mx = fmaxf(top_scaled(x[0], 0), top_scaled(x[1], 1));
+          } else {
+            mx = fmaxf(top(x[0]), top(x[1]));
+          }
           tmem_wait_ld();
           if (check) {
             hide(x[2], mw.z, key0 + 64);
             hide(x[3], mw.w, key0 + 96);
           }
-          mx = __fmul_rn(fmaxf(mx, fmaxf(top(x[2]), top(x[3]))), sc);   // sc > 0
+          if constexpr (kScaled) {
+            mx = fmaxf(mx, fmaxf(top_scaled(x[2], 2), top_scaled(x[3], 3)));
+          } else {
+            mx = __fmul_rn(fmaxf(mx, fmaxf(top(x[2]), top(x[3]))), sc);   // sc > 0
+          }
           // A logit past the bound moves m; far rows come here with every tile.
           if (__any_sync(0xffffffffu, mx > (fabsf(m) > kFar ? -INFINITY : lazy_bound<W>(m)))) {
             const float mn = fmaxf(m, mx - kRaise<W>);
@@ -552,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
               }
             }
             if (__any_sync(0xffffffffu, fabsf(m) > kFar && m > -INFINITY)) {
-              l = far_weights<W>(s_col, sc, m, l, mw, key0, low, lim + 1, smem_addr(&bars.p_full[side][0]), lane);
+              l = far_weights<W, kScaled>(s_col, sc, m, l, mw, key0, low, lim + 1, smem_addr(&bars.p_full[side][0]), lane, groups);
               continue;
             }
           }
@@ -562,14 +609,34 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t p[16];
+            if constexpr (kScaled) {                   // a weight holds its key's V scale, which the sum takes back
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float y0, y1;
-              upk2(fma2_rn(pk2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), sc2, mz2), y0, y1);
-              y0 = ex2(y0);
-              y1 = ex2(y1);
-              sum = add2_rn(sum, pk2(y0, y1));
-              p[i] = Vec<W>::pack2(y0, y1);
+              for (int g = 0; g < 32 / kGroup; ++g) {
+                const float4 k = groups[c * (32 / kGroup) + g];
+                const float factor = group_factor(sc, k.x), off = k.y - mz;
+                const unsigned long long factor2 = pk2(factor, factor), off2 = pk2(off, off);
+                unsigned long long of_group = pk2(0.f, 0.f);
+#pragma unroll
+                for (int i = g * kGroup / 2; i < (g + 1) * kGroup / 2; ++i) {
+                  float y0, y1;
+                  upk2(fma2_rn(pk2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), factor2, off2), y0, y1);
+                  y0 = ex2(y0);
+                  y1 = ex2(y1);
+                  of_group = add2_rn(of_group, pk2(y0, y1));
+                  p[i] = Vec<W>::pack2(y0, y1);
+                }
+                sum = fma2_rn(of_group, pk2(k.z, k.z), sum);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float y0, y1;
+                upk2(fma2_rn(pk2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), sc2, mz2), y0, y1);
+                y0 = ex2(y0);
+                y1 = ex2(y1);
+                sum = add2_rn(sum, pk2(y0, y1));
+                p[i] = Vec<W>::pack2(y0, y1);
+              }
             }
             tmem_st16(s_col + 16 * c, p);
             if (c & 1) {                               // half of the keys: their part of O += P V can start
@@ -806,8 +873,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
           }
         };
+        // Scaled cache: the scales of this thread's keys, once their block is known; a key whose block has one out of range
+        // counts as not named.
+        float2 scale_of[2];
+        auto look_up_scales = [&] {
+          if constexpr (kScaled) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              scale_of[e] = make_float2(1.f, 1.f);
+              if (id[e] >= 0) {
+                const float* at = a.scales + (int64_t)id[e] * a.H + head;
+                scale_of[e] = make_float2(at[0], at[(int64_t)a.num_blocks * a.H]);
+              }
+            }
+          }
+        };
         if (box > 0) look_up_groups(0);
         else look_up(0);
+        look_up_scales();
         // Byte offsets of the tile's keys, for the row copies; -1: no such key.  Returns this thread's keys' mask words.
         auto find_rows = [&](int j, long long* off, uint32_t(&named)[2]) {
           long long at_key[2];
@@ -840,11 +923,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
               const long long* off = s_off + (j & 1) * kKeys;
               if ((i & 1) == 0) {
                 uint32_t named[2];
+                if constexpr (kScaled) {
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    if (id[e] < 0) continue;
+                    if (scale_ok(scale_of[e].x) && scale_ok(scale_of[e].y)) {   // the same from every key of a group
+                      s_raw_group[j % S::kRaw][(lt + e * kLoaders) / kGroup] = scale_of[e];
+                    } else {
+                      latch(a.status, IS_ST_SCALE);
+                      id[e] = -1;
+                    }
+                  }
+                }
                 find_rows(j, s_off + (j & 1) * kKeys, named);
                 if (lane == 0) s_raw_mask[j % S::kRaw][warp - kLoaderWarp] = named[0];
                 if (lt == 0) s_raw_mask[j % S::kRaw][3] = named[1];
                 look_up(j + 1);
                 ok = agreed(here);
+              } else {
+                look_up_scales();                      // of the next tile's keys
               }
               const uint8_t* src = kbase + ((i & 1) ? a.v_offset : 0) + c * 16;
               const uint32_t dst = raw0 + ((n_load + i) % S::kRaw) * S::kRawBytes;
@@ -878,12 +975,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
               for (int k = k0; k < k0 + kAhead && k < N; ++k) {
                 const int row = row0 + k * RP;
                 if (row < kKeys) {
-                  st_shared_v4(dst + at_chunk<D>(row, 2 * c), widen8(x[k - k0].x, x[k - k0].y));
-                  st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), widen8(x[k - k0].z, x[k - k0].w));
+                  st_shared_v4(dst + at_chunk<D>(row, 2 * c), widen8<kInt8>(x[k - k0].x, x[k - k0].y));
+                  st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), widen8<kInt8>(x[k - k0].z, x[k - k0].w));
                 }
               }
             }
             if ((i & 1) == 0 && lt < 4) s_mask[slot][lt] = s_raw_mask[(i >> 1) % S::kRaw][lt];
+            if constexpr (kScaled) {
+              if ((i & 1) == 0 && lt < kKeys / kGroup) {
+                const float2 s = s_raw_group[(i >> 1) % S::kRaw][lt];
+                s_group[slot][lt] = make_float4(s.x, log2f(s.y), 1.f / s.y, 0.f);
+              }
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lt == 0 && (i & 1) == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
@@ -1129,11 +1232,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 
 // Prompts go here when the rows of a request fill a tensor-core tile better
 // than the split kernel's 16 rows (see launch_attend).
-template <typename T, bool F8, int D>
+template <typename T, CacheKind KIND, int D>
 static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
+  constexpr bool F8 = KIND != kCachePlain;
   using S = prompt::Shape<D, F8>;
-  auto* kern = a.wait_ns < kWaitBudgetNs ? prompt::attend_prompt_kernel<T, F8, D, true> : prompt::attend_prompt_kernel<T, F8, D, false>;
-  static_assert(S::kSmem + (F8 ? 2048 : 1024) <= 227 * 1024, "a CTA fits an SM");
+  auto* kern = a.wait_ns < kWaitBudgetNs ? prompt::attend_prompt_kernel<T, KIND, D, true> : prompt::attend_prompt_kernel<T, KIND, D, false>;
+  static_assert(S::kSmem + (F8 ? 6144 : 1024) <= 227 * 1024, "a CTA fits an SM");
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
   constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - partials_offset()) / (2 * sizeof(PartialByEights<S::kRows, D>)));

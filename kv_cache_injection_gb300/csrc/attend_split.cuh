@@ -782,10 +782,13 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
             const float ks = lane < KT ? s_scale[warp][s][0][lane] : 1.f, vs = lane < KT ? s_scale[warp][s][1][lane] : 1.f;
             const bool ok = scale_ok(ks) && scale_ok(vs);
             const uint32_t good = __ballot_sync(0xffffffffu, ok);
-            if (tm.valid & ~good) {
+            for (uint32_t bad = tm.valid & ~good; bad; bad &= bad - 1) {   // its values, whatever they are, become 0
               if (lane == 0) latch(a.status, IS_ST_SCALE);
-              tm.valid &= good;
+              const uint32_t row = ring + s * S::kTileBytes + (KT + __ffs(bad) - 1) * E::kRowBytes;
+              for (int c = lane; c < E::kRowBytes / 16; c += 32)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(row + c * 16), "r"(0) : "memory");
             }
+            tm.valid &= good;
             if (lane < KT) s_key[warp][lane] = ok ? make_float4(ks, log2f(vs), 1.f / vs, 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
             __syncwarp();
             tm.key = s_key[warp];

@@ -362,6 +362,7 @@ def attend_case(reqs, Hq, H, D, dtype, cache, bs=16, window=0, scale=None, seed=
     used = torch.cat(used[1:]) if sum(n for n, _ in reqs) else used[0]
     for r, b, kv, s in bad:
         scales[kv, table[r, b]] = s
+        codes[:, table[r, b]] = 127                      # E4M3: NaN
         named[r][b * bs: (b + 1) * bs] = False
         want_bits |= _lib.IS_ST_SCALE
     for r, b, i in holes:
@@ -713,3 +714,42 @@ def test_step_behind_an_injected_segment(cache_dtype):
         half = {"int8": 0.5, "e4m3": 16.0}[cache_dtype] * 5 * math.sqrt(2)
         size = want.abs().amax(-1, keepdim=True) * math.sqrt(2) + half * unit
         assert bool(((got - want).abs() <= half * unit + 3 * 2.0 ** -8 * size).all())
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("dtype,cache,D,bs", [("bf16", "int8", 128, 16), ("f16", "e4m3", 64, 8), ("bf16", "e4m3", 64, 16), ("f16", "int8", 128, 40)])
+def test_waits_that_run_out(dtype, cache, D, bs):
+    """A prompt with limits of its waits that it cannot keep ends with IS_ST_TIMEOUT and nothing else, and the next call on
+    the same stream and workspace gives the bits that it gave before."""
+    g = torch.Generator().manual_seed(61)
+    H, Hq, lens, start = 2, 8, [3333, 900, 70], [0, 200, 300, 370]
+    need = [-(-n // bs) for n in lens]
+    nb = sum(need)
+    table, at = torch.full((3, max(need)), -1, dtype=torch.int32), 0
+    for r, n in enumerate(need):
+        table[r, :n] = torch.arange(at, at + n)
+        at += n
+    codes, scales = random_cache(cache, nb, bs, H, D, g)
+    q = torch.randn(start[-1], Hq, D, generator=g).to(ref.TORCH[dtype]).to(DEV)
+    args = (q, ints(lens), table.to(DEV), api.make_cache_desc(bs, nb, cache), codes.to(DEV), scales.to(DEV))
+    ws, status = api.attend_workspace(), ints([0])
+
+    def call(**kw):
+        out = torch.zeros_like(q)
+        api.is_attend_scaled(*args, out, ws, status, q_start=ints(start), max_q_len=200, **kw)
+        torch.cuda.synchronize()
+        bits = status.item()
+        status.zero_()
+        return out.cpu(), bits
+
+    want, bits = call()
+    assert bits == 0 and bool(want.isfinite().all())
+    seen = 0
+    for budget in (0, 0, 500, 2000, 10000, 100000):
+        out, bits = call(budget_ns=budget)
+        assert bits in (0, _lib.IS_ST_TIMEOUT) and (bits or torch.equal(out, want))
+        seen |= bits
+        out, bits = call()
+        assert bits == 0 and torch.equal(out, want)
+    assert seen == _lib.IS_ST_TIMEOUT
