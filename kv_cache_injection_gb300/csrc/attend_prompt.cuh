@@ -73,7 +73,7 @@ namespace prompt {
 
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;               // keys of a tile, and of a unit
-constexpr int kLoaderWarp = 8, kLoaders = 96, kMmaWarp = 11;
+constexpr int kLoaderWarp = 8, kLoaders = 96;
 // Registers a thread: 168 at launch (65,536 / 384); the softmax warps take what
 // a row of S needs, the other four give it: 2 * 192 + 120 = 3 * 168.  (208 and 88:
 // the loaders and the MMA thread spill, and the long prompts take 426 us, not 406.)
@@ -85,6 +85,11 @@ constexpr int kMinRun = 2;
 // an item counts as so many more, before its first.
 constexpr int kItemCost = 6;
 constexpr int kMaskRing = 8;
+// The form over a scaled cache has 16 warps: 0-7 softmax, 8 finds the tiles'
+// blocks and scales, 9-11 bring K, 12-14 V, 15 issues the MMAs; 128 registers a thread.
+constexpr int kScaledThreads = 512;
+constexpr int kCodeWarps = 3;            // that bring K, and that bring V
+constexpr int kCodeThreads = 2 * 32 * kCodeWarps;
 // The exponents are x * sc - m in one rounding, so that they keep the error of
 // the product that m was rounded by: half a step of m.  That passes a weight's
 // range where m is past 2^24 (fp16) or 2^30: past this, far_weights rounds the
@@ -92,7 +97,7 @@ constexpr int kMaskRing = 8;
 constexpr float kFar = 4194304.f;
 constexpr uint32_t kTmemAll = 512;
 
-template <int D, bool F8>
+template <int D, bool F8, bool SCALED = false>
 struct Shape {
   // Rows of an item, at most: tiles A and B; at head_dim 256 tensor memory has room for O of one.
   static constexpr int kRows = D == 256 ? 128 : 256;
@@ -102,14 +107,16 @@ struct Shape {
   // rows one after the other, 1024 bytes each (one swizzle atom).
   static constexpr uint32_t kGroupBytes = kHalves * 1024;
   static constexpr uint32_t kTileBytes = 16 * kGroupBytes;
-  static constexpr int kRing = D == 256 ? 2 : F8 ? (D == 128 ? 3 : 5) : D == 128 ? 5 : 8;   // K and V tiles in shared memory
+  static constexpr int kRing =           // K and V tiles in shared memory
+      D == 256 ? 2 : SCALED ? (D == 128 ? 4 : 8) : F8 ? (D == 128 ? 3 : 5) : D == 128 ? 5 : 8;
   // FP8 rows are copied as they are, kRaw tiles ahead, and widened from there.
   static constexpr int kRaw = D == 128 ? 3 : 4;
-  static constexpr uint32_t kRawBytes = F8 ? 128 * D : 0;
+  static constexpr uint32_t kRawBytes = F8 && !SCALED ? 128 * D : 0;
   // A tile's mask is written when its K has a place, that is once load 2 t - kRing has been released; the mask it
   // replaces has been read once V of tile t - kMaskRing, load 2 (t - kMaskRing) + 1, has been released.
   static_assert(2 * kMaskRing >= kRing + 1, "a mask is read before its place is used again");
-  static constexpr size_t kSmem = 1024 + kQBytes + kRing * (size_t)kTileBytes + kRaw * (size_t)kRawBytes + (F8 ? 2 : 1) * 128 * 8;
+  static constexpr size_t kSmem = 1024 + kQBytes + kRing * (size_t)kTileBytes + kRaw * (size_t)kRawBytes +
+                                  (SCALED ? 0 : F8 ? 2 : 1) * 128 * 8;
   static constexpr uint32_t kOCol = 256;                      // first column of O_A; O_B follows D columns on
 };
 
@@ -126,6 +133,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+// Waits for this thread's loads from tensor memory, r's among them.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32], uint32_t (&s)[32]) {
+  tmem_wait_ld32(r);
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(s[i]), "+r"(s[i + 1]), "+r"(s[i + 2]), "+r"(s[i + 3]), "+r"(s[i + 4]), "+r"(s[i + 5]), "+r"(s[i + 6]), "+r"(s[i + 7]));
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -294,6 +317,9 @@ struct Bars {
   uint64_t s_full[2], p_full[2][2], o_full[2];   // P in two halves of 64 keys
   uint64_t mask_full[kMaskRing];
 };
+struct ScaledBars {      // beside them, over a scaled cache
+  uint64_t tile_empty[kMaskRing], q_raw;
+};
 
 // Bits lo .. hi - 1 of a 32-bit word whose bit 0 is position `at`.
 __device__ __forceinline__ uint32_t bits_between(int at, int lo, int hi) {
@@ -314,7 +340,16 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
 // Scaled cache: what eight keys of a block share is K scale, log2 of the V scale
 // and 1 / V scale.  A row's factor to their logits stays finite, so that 0 times
 // it is 0; sc > 0.
-constexpr int kGroup = 8;
+constexpr int kGroup = 8, kGroups = kKeys / kGroup;
+// A tile of keys as its loaders need it.  The tiles of a CTA's run follow one
+// another here whatever their segments, so that a tile's codes are on their way
+// while those of the tile before it are widened.
+struct TileInfo {
+  int64_t at[kGroups];   // first K row of the group, in bytes; -1: no block of it counts
+  int32_t lo, hi;        // its keys that some row may see
+  int32_t rows;          // query rows of the segment that it begins, 0: goes on with one; -1: the run has ended
+  int32_t row0, head;    // of that segment
+};
 __device__ __forceinline__ float group_factor(float sc, float ks) { return fminf(sc * ks, FLT_MAX); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -334,14 +369,56 @@ __device__ __forceinline__ uint32_t at_chunk(int row, int c) {
          (uint32_t)(((c & 7) ^ (row & 7)) * 16);
 }
 
+// A query row, bf16 in a tile, becomes fp16 times a power of two that brings its
+// largest element to [2^14, 2^15); *unscale is the inverse.
+template <int D>
+__device__ __forceinline__ void scale_query_row(uint32_t tile, int row, bool live, float* unscale) {
+  constexpr int C = D / 8;
+  float down = 1.f;
+  if (live) {
+    __nv_bfloat162 big(0.f, 0.f);
+    auto larger = [&](uint32_t w) {
+      w &= 0x7fff7fffu;
+      big = __hmax2(big, *reinterpret_cast<const __nv_bfloat162*>(&w));
+    };
+#pragma unroll 4
+    for (int k = 0; k < C; ++k) {
+      const uint4 x = ld_shared_v4(tile + at_chunk<D>(row, k));
+      larger(x.x);
+      larger(x.y);
+      larger(x.z);
+      larger(x.w);
+    }
+    const float most = fmaxf(__low2float(big), __high2float(big));
+    const int shift = most > 0.f && most < INFINITY ? min(14 - (int)(((__float_as_uint(most) >> 23) & 255u) - 127), 120) : 0;
+    const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+    down = __uint_as_float((uint32_t)(127 - shift) << 23);
+#pragma unroll 1
+    for (int k0 = 0; k0 < C; k0 += 4) {
+      uint4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = ld_shared_v4(tile + at_chunk<D>(row, k0 + k));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float f[8];
+        Vec<__nv_bfloat16>::unpack(x[k], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= up;
+        st_shared_v4(tile + at_chunk<D>(row, k0 + k), Vec<__half>::pack(f));
+      }
+    }
+  }
+  *unscale = down;
+}
+
 // The weights of a tile with rows past kFar: S (logits before their scale) once
 // more from tensor memory, weights over it and their sum added to l.  Of 32
 // logits S is read before the 16 columns of their weights, which lie before the
 // next ones', are written.  A function of its own, since inside the loop it costs
 // the other rows registers: the long prompts take 403 us instead of 392.
-template <typename W, bool SC>
+template <typename W>
 __device__ __noinline__ float far_weights(uint32_t s_col, float sc, float m, float l, uint4 named, int key0, int low, int end,
-                                          uint32_t p_full, int lane, const float4* groups) {
+                                          uint32_t p_full, int lane) {
   const float mz = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -353,18 +430,10 @@ __device__ __noinline__ float far_weights(uint32_t s_col, float sc, float m, flo
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float w[2];
-      if constexpr (SC) {
-        const float4 k = groups[(32 * c + 2 * i) / kGroup];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          w[e] = (see >> (2 * i + e)) & 1u ? ex2(__fsub_rn(fmaf(__uint_as_float(y[2 * i + e]), group_factor(sc, k.x), k.y), mz)) : 0.f;
-        l = fmaf(w[0] + w[1], k.z, l);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          w[e] = (see >> (2 * i + e)) & 1u ? ex2(__fsub_rn(__fmul_rn(__uint_as_float(y[2 * i + e]), sc), mz)) : 0.f;
-        l += w[0] + w[1];
-      }
+      for (int e = 0; e < 2; ++e)
+        w[e] = (see >> (2 * i + e)) & 1u ? ex2(__fsub_rn(__fmul_rn(__uint_as_float(y[2 * i + e]), sc), mz)) : 0.f;
+      l += w[0] + w[1];
       p[i] = Vec<W>::pack2(w[0], w[1]);
     }
     tmem_st16(s_col + 16 * c, p);
@@ -378,13 +447,172 @@ __device__ __noinline__ float far_weights(uint32_t s_col, float sc, float m, flo
   return l;
 }
 
+// Scaled cache, one tile of a row: S (logits before their scale) becomes weights
+// over it.  A weight holds its key's V scale, x = logit + log2 of it, and the sum
+// takes that back by groups of eight.  S is read twice, 32 columns ahead of their
+// use, for the maximum of x and for the weights: keeping all 128 between the two
+// takes registers that the loaders need.  Of 32 logits S is read before the 16
+// columns of their weights, which lie before the next ones', are written.  The
+// groups' scales are read ahead with them.
+template <int D>
+struct ScaledTile;
+template <typename W, int D>
+__device__ float far_scaled_weights(ScaledTile<D> t, float mz, float l);
+template <int D>
+struct ScaledTile {
+  uint32_t s_col;
+  float sc;
+  uint4 named;
+  const float4* groups;
+  int key0, low, end;
+  bool check;
+  uint32_t p_full;
+  int lane;
+
+  __device__ __forceinline__ void hide(uint32_t (&y)[32], int c) const {
+    if (!check) return;
+    const uint32_t word = c == 0 ? named.x : c == 1 ? named.y : c == 2 ? named.z : named.w;
+    const uint32_t see = word & bits_between(key0 + 32 * c, low, end);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!((see >> i) & 1u)) y[i] = 0xff800000u;
+  }
+  struct Scales {
+    float4 k[32 / kGroup];
+  };
+  __device__ __forceinline__ Scales scales(int c) const {
+    Scales s;
+#pragma unroll
+    for (int g = 0; g < 32 / kGroup; ++g) s.k[g] = groups[c * (32 / kGroup) + g];
+    return s;
+  }
+  __device__ __forceinline__ float top(uint32_t (&y)[32], int c, const Scales& s) const {
+    hide(y, c);
+    float x[32 / kGroup];
+#pragma unroll
+    for (int g = 0; g < 32 / kGroup; ++g) {
+      const uint32_t* v = y + g * kGroup;
+      float x0 = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+      const float x1 = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+      x0 = max3(x0, __uint_as_float(v[6]), __uint_as_float(v[7]));
+      x[g] = fmaf(fmaxf(x0, x1), group_factor(sc, s.k[g].x), s.k[g].y);   // grows with the logits of a group
+    }
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  }
+  // FAR: exponents rounded as they were for the maximum (see kFar).
+  template <typename W, bool FAR>
+  __device__ __forceinline__ void weights(uint32_t (&y)[32], int c, const Scales& s, float mz, unsigned long long& sum) const {
+    hide(y, c);
+    uint32_t p[16];
+#pragma unroll
+    for (int g = 0; g < 32 / kGroup; ++g) {
+      const float4 k = s.k[g];
+      const float factor = group_factor(sc, k.x), off = FAR ? k.y : k.y - mz;
+      const unsigned long long factor2 = pk2(factor, factor), off2 = pk2(off, off);
+      unsigned long long of_group = 0ull;
+#pragma unroll
+      for (int i = g * kGroup / 2; i < (g + 1) * kGroup / 2; ++i) {
+        float y0, y1;
+        upk2(fma2_rn(pk2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), factor2, off2), y0, y1);
+        y0 = ex2(FAR ? __fsub_rn(y0, mz) : y0);
+        y1 = ex2(FAR ? __fsub_rn(y1, mz) : y1);
+        of_group = i == g * kGroup / 2 ? pk2(y0, y1) : add2_rn(of_group, pk2(y0, y1));
+        p[i] = Vec<W>::pack2(y0, y1);
+      }
+      sum = fma2_rn(of_group, pk2(k.z, k.z), sum);
+    }
+    tmem_st16(s_col + 16 * c, p);
+    if (c & 1) {                         // half of the keys: their part of O += P V can start
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + 8 * (c >> 1));
+    }
+  }
+  // The tile's weights for maximum m and sum l, both brought up to date with O.
+  template <typename W>
+  __device__ __forceinline__ float run(uint32_t o_col, bool has_o, float& m, float l) const {
+    uint32_t a[32], b[32];
+    tmem_ld32(s_col, a);
+    tmem_ld32(s_col + 32, b);
+    Scales sa = scales(0), sb = scales(1);
+    tmem_wait_ld32(a, b);
+    float most = top(a, 0, sa);
+    tmem_ld32(s_col + 64, a);
+    sa = scales(2);
+    most = fmaxf(most, top(b, 1, sb));
+    tmem_ld32(s_col + 96, b);
+    sb = scales(3);
+    tmem_wait_ld32(a, b);
+    most = fmaxf(most, top(a, 2, sa));
+    tmem_ld32(s_col, a);
+    sa = scales(0);
+    most = fmaxf(most, top(b, 3, sb));
+    tmem_ld32(s_col + 32, b);
+    sb = scales(1);
+    // A logit past the bound moves m; far rows come here with every tile.
+    if (__any_sync(0xffffffffu, most > (fabsf(m) > kFar ? -INFINITY : lazy_bound<W>(m)))) {
+      const float mn = fmaxf(m, most - kRaise<W>);
+      const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+      m = mn;
+      l *= f;
+      if (has_o) {
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t y[16];
+          tmem_ld16(o_col + 16 * c, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+          tmem_st16(o_col + 16 * c, y);
+        }
+      }
+      if (__any_sync(0xffffffffu, fabsf(m) > kFar && m > -INFINITY)) return far_scaled_weights<W, D>(*this, m == -INFINITY ? 0.f : m, l);
+    }
+    const float mz = m == -INFINITY ? 0.f : m;
+    unsigned long long sum = pk2(l, 0.f);
+    tmem_wait_ld32(a, b);
+    weights<W, false>(a, 0, sa, mz, sum);
+    tmem_ld32(s_col + 64, a);
+    sa = scales(2);
+    weights<W, false>(b, 1, sb, mz, sum);
+    tmem_ld32(s_col + 96, b);
+    sb = scales(3);
+    tmem_wait_ld32(a, b);
+    weights<W, false>(a, 2, sa, mz, sum);
+    weights<W, false>(b, 3, sb, mz, sum);
+    float l0, l1;
+    upk2(sum, l0, l1);
+    return l0 + l1;
+  }
+};
+
+template <typename W, int D>
+__device__ __noinline__ float far_scaled_weights(ScaledTile<D> t, float mz, float l) {
+  unsigned long long sum = pk2(l, 0.f);
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t y[32];
+    tmem_ld32(t.s_col + 32 * c, y);
+    const typename ScaledTile<D>::Scales s = t.scales(c);
+    tmem_wait_ld32(y);
+    t.template weights<W, true>(y, c, s, mz, sum);
+  }
+  float l0, l1;
+  upk2(sum, l0, l1);
+  return l0 + l1;
+}
+
+constexpr int threads_of(CacheKind kind) { return kind == kCacheScaledE4m3 || kind == kCacheScaledInt8 ? kScaledThreads : kThreads; }
+
 // LIMITED: the limit of the waits is the call's.  (As a variable in the ordinary form it costs 16 prompts 1.2 us of 53.4.)
 template <typename T, CacheKind KIND, int D, bool LIMITED>
-__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a, int per, int box,
-                                                                   const __grid_constant__ CUtensorMap rows_map) {
+__global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(const AttendArgs a, int per, int box,
+                                                                           const __grid_constant__ CUtensorMap rows_map) {
   constexpr bool F8 = KIND != kCachePlain, kInt8 = KIND == kCacheScaledInt8;   // F8: 8-bit elements
   constexpr bool kScaled = KIND == kCacheScaledE4m3 || KIND == kCacheScaledInt8;
-  using S = Shape<D, F8>;
+  using S = Shape<D, F8, kScaled>;
+  constexpr int kThreads = threads_of(KIND), kMmaWarp = kThreads / 32 - 1;
   const uint64_t limit_ns = LIMITED ? a.wait_ns : kWaitBudgetNs;
   // FP8 keys and values are exact in fp16, and a bf16 query row scaled by a power of two (undone in the logits) loses
   // 2^-39 of its largest element at most: with an FP8 cache both products are taken in fp16.
@@ -398,9 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   __shared__ __align__(16) uint32_t s_mask[kMaskRing][4];
   __shared__ uint32_t s_raw_mask[S::kRaw][4];
   __shared__ float s_unscale[kShift ? S::kRows : 1];
-  // Scaled cache, by groups of eight keys: K and V scales as they are found, and what the softmax takes of them.
-  __shared__ float2 s_raw_group[kScaled ? S::kRaw : 1][kScaled ? kKeys / kGroup : 1];
-  __shared__ float4 s_group[kScaled ? kMaskRing : 1][kScaled ? kKeys / kGroup : 1];
+  __shared__ float4 s_group[kScaled ? kMaskRing : 1][kScaled ? kGroups : 1];
+  __shared__ TileInfo s_tile[kScaled ? kMaskRing : 1];
+  __shared__ __align__(8) ScaledBars more;             // the plain forms, which fill an SM's shared memory, use none of the three
   __shared__ int64_t scratch[33];
   __shared__ int64_t s_base;
   __shared__ int32_t s_req;
@@ -415,13 +643,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     tmem_alloc(smem_addr(&s_tmem), kTmemAll);
     tmem_relinquish();
   }
-  if constexpr (kScaled) {               // groups without a key in use keep scales that are numbers
-    for (int i = tid; i < S::kRaw * (kKeys / kGroup); i += kThreads) s_raw_group[0][i] = make_float2(1.f, 1.f);
-  }
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < 8; ++i) s_bulk[i] = 0;
-    mbar_init(smem_addr(&bars.q_full), kLoaders);
+    mbar_init(smem_addr(&bars.q_full), kScaled ? kCodeThreads : kLoaders);
+    if constexpr (kScaled) {
+      mbar_init(smem_addr(&more.q_raw), kCodeThreads);
+      for (int i = 0; i < kMaskRing; ++i) mbar_init(smem_addr(&more.tile_empty[i]), 1);
+    }
     mbar_init(smem_addr(&bars.q_empty), kShift ? 9 : 1);   // the last logits; eight softmax warps that read s_unscale
     mbar_init(smem_addr(&bars.done), 1);
     mbar_init(smem_addr(&bars.v_tail), 1);
@@ -474,10 +703,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
   if (idle) {
     if (tid == 0) record_of(a, blockIdx.x)->parts = 0;
   } else {
-    if (warp < kLoaderWarp)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if constexpr (!kScaled) {
+      if (warp < kLoaderWarp)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+      else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    }
 
     if (warp < kLoaderWarp) {
       // ---- softmax ------------------------------------------------------------
@@ -522,6 +753,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
           if (!wait(&bars.mask_full[slot], (n_mask / kMaskRing) & 1u) || !wait(&bars.s_full[side], n_s & 1u)) break;
           ++n_s;
           tc_fence_after();
+          if constexpr (kScaled) {
+            const uint4 named = *reinterpret_cast<const uint4*>(s_mask[slot]);
+            const bool check = (named.x & named.y & named.z & named.w) != 0xffffffffu || key0 + kKeys - 1 > lim_lo || key0 < low_hi;
+            const ScaledTile<D> tile{s_col, sc, named, s_group[slot], key0, low, lim + 1, check, smem_addr(&bars.p_full[side][0]), lane};
+            l = tile.template run<W>(o_col, j > 0, m, l);
+            continue;
+          }
           uint32_t x[4][32];
           tmem_ld32(s_col, x[0]);
           tmem_ld32(s_col + 32, x[1]);
@@ -543,21 +781,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
             return max3(max3(t0, t1, __uint_as_float(y[30])), __uint_as_float(y[31]), t0);
           };
-          // Scaled cache: the largest of logit + log2 of the V scale, which grows with the logits of a group.
-          const float4* groups = s_group[kScaled ? slot : 0];
-          auto top_scaled = [&](const uint32_t(&y)[32], int c) {
-            float most = -INFINITY;
-#pragma unroll
-            for (int g = 0; g < 32 / kGroup; ++g) {
-              const float4 k = groups[c * (32 / kGroup) + g];
-              const uint32_t* v = y + g * kGroup;
-              float x0 = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-              const float x1 = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
-              x0 = max3(x0, __uint_as_float(v[6]), __uint_as_float(v[7]));
-              most = fmaxf(most, fmaf(fmaxf(x0, x1), group_factor(sc, k.x), k.y));
-            }
-            return most;
-          };
           tmem_wait_ld();
           tmem_ld32(s_col + 64, x[2]);
           tmem_ld32(s_col + 96, x[3]);
@@ -565,22 +788,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             hide(x[0], mw.x, key0);
             hide(x[1], mw.y, key0 + 32);
           }
-          float mx;
-          if constexpr (kScaled) {
-            mx = fmaxf(top_scaled(x[0], 0), top_scaled(x[1], 1));
-          } else {
-            mx = fmaxf(top(x[0]), top(x[1]));
-          }
+          float mx = fmaxf(top(x[0]), top(x[1]));
           tmem_wait_ld();
           if (check) {
             hide(x[2], mw.z, key0 + 64);
             hide(x[3], mw.w, key0 + 96);
           }
-          if constexpr (kScaled) {
-            mx = fmaxf(mx, fmaxf(top_scaled(x[2], 2), top_scaled(x[3], 3)));
-          } else {
-            mx = __fmul_rn(fmaxf(mx, fmaxf(top(x[2]), top(x[3]))), sc);   // sc > 0
-          }
+          mx = __fmul_rn(fmaxf(mx, fmaxf(top(x[2]), top(x[3]))), sc);   // sc > 0
           // A logit past the bound moves m; far rows come here with every tile.
           if (__any_sync(0xffffffffu, mx > (fabsf(m) > kFar ? -INFINITY : lazy_bound<W>(m)))) {
             const float mn = fmaxf(m, mx - kRaise<W>);
@@ -599,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
               }
             }
             if (__any_sync(0xffffffffu, fabsf(m) > kFar && m > -INFINITY)) {
-              l = far_weights<W, kScaled>(s_col, sc, m, l, mw, key0, low, lim + 1, smem_addr(&bars.p_full[side][0]), lane, groups);
+              l = far_weights<W>(s_col, sc, m, l, mw, key0, low, lim + 1, smem_addr(&bars.p_full[side][0]), lane);
               continue;
             }
           }
@@ -609,34 +823,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t p[16];
-            if constexpr (kScaled) {                   // a weight holds its key's V scale, which the sum takes back
 #pragma unroll
-              for (int g = 0; g < 32 / kGroup; ++g) {
-                const float4 k = groups[c * (32 / kGroup) + g];
-                const float factor = group_factor(sc, k.x), off = k.y - mz;
-                const unsigned long long factor2 = pk2(factor, factor), off2 = pk2(off, off);
-                unsigned long long of_group = pk2(0.f, 0.f);
-#pragma unroll
-                for (int i = g * kGroup / 2; i < (g + 1) * kGroup / 2; ++i) {
-                  float y0, y1;
-                  upk2(fma2_rn(pk2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), factor2, off2), y0, y1);
-                  y0 = ex2(y0);
-                  y1 = ex2(y1);
-                  of_group = add2_rn(of_group, pk2(y0, y1));
-                  p[i] = Vec<W>::pack2(y0, y1);
-                }
-                sum = fma2_rn(of_group, pk2(k.z, k.z), sum);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float y0, y1;
-                upk2(fma2_rn(pk2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), sc2, mz2), y0, y1);
-                y0 = ex2(y0);
-                y1 = ex2(y1);
-                sum = add2_rn(sum, pk2(y0, y1));
-                p[i] = Vec<W>::pack2(y0, y1);
-              }
+            for (int i = 0; i < 16; ++i) {
+              float y0, y1;
+              upk2(fma2_rn(pk2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), sc2, mz2), y0, y1);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              sum = add2_rn(sum, pk2(y0, y1));
+              p[i] = Vec<W>::pack2(y0, y1);
             }
             tmem_st16(s_col + 16 * c, p);
             if (c & 1) {                               // half of the keys: their part of O += P V can start
@@ -703,7 +897,243 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         if (lane == 0) mbar_arrive(smem_addr(&bars.seg_empty[n_seg % kSegments]));
       }
       if (!ok) *abort_flag = 1;
-    } else if (warp < kMmaWarp) {
+    } else if (kScaled && warp == kLoaderWarp) {
+      // ---- scaled cache: segments, and the tiles' blocks, masks and scales ---------
+      if constexpr (kScaled) {
+        Walk w;                                        // the first lane's
+        bool crosses = false, ok = true;
+        if (lane == 0) {
+          w.run = run;
+          w.u = w.u_first = u0;
+          w.u_end = u1;
+          w.r = s_req;
+          w.base = s_base;
+          w.t = 0;
+          w.q = read_request(a, w.r, false);
+          w.x = tile_of(a, w.q, per, 0);
+        }
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, limit_ns));
+          return ok;
+        };
+        uint32_t n_tile = 0;
+        for (uint32_t n_seg = 0;; ++n_seg) {
+          const uint32_t seg = n_seg % kSegments;
+          if (!wait(&bars.seg_empty[seg], ((n_seg / kSegments) & 1u) ^ 1u)) break;
+          Segment& g = s_seg[seg];
+          if (lane == 0) {
+            if (w.next(a, per)) {
+              g.tiles = w.tiles();
+              g.k_lo = w.k_lo;
+              g.k_hi = w.k_hi;
+              g.k_see = w.x.see;
+              g.rows = w.rows;
+              g.r = w.r;
+              g.lim0 = w.q.seq - w.q.n + w.x.tok0;
+              g.head = w.head;
+              g.row0 = w.q.row0 + w.x.tok0;
+              g.slot = w.whole ? -1 : 2 * blockIdx.x + (w.at_start ? 0 : 1);
+              crosses = w.begins && !w.whole;
+              if (crosses) {
+                JoinRecord* rec = record_of(a, blockIdx.x);
+                rec->parts = w.parts;
+                rec->slot0 = g.slot;
+                rec->row0 = w.q.row0;
+                rec->head = w.head;
+                rec->rho0 = w.x.tok0 * a.G;
+                rec->rows = w.rows;
+              }
+            } else {
+              g.tiles = -1;
+              if (!crosses) record_of(a, blockIdx.x)->parts = 0;
+            }
+          }
+          __syncwarp();
+          const int n_tiles = g.tiles, k_lo = g.k_lo, k_hi = g.k_hi, k_see = g.k_see, rows = g.rows, head = g.head, row_at = g.row0;
+          const int32_t* table = a.block_table + (size_t)g.r * a.max_blocks;
+          if (lane == 0) mbar_arrive(smem_addr(&bars.seg_full[seg]));
+          if (n_tiles < 0) break;
+          // Two tiles at a time: half a warp each, a lane to a group.
+          const int half = lane >> 4, grp = lane & 15;
+          for (int j0 = 0; j0 < n_tiles; j0 += 2) {
+            const int j = j0 + half, key0 = k_lo + j * kKeys, p = key0 + grp * kGroup;
+            int64_t at = -1;
+            float ks = 1.f, vs = 1.f;
+            if (j < n_tiles && p + kGroup > k_see && p < k_hi) {
+              const int b = block_of(a, p);
+              const int32_t id = table[b];
+              if (id >= 0 && id < a.num_blocks) {
+                const float* s = a.scales + (int64_t)id * a.H + head;
+                ks = s[0];
+                vs = s[(int64_t)a.num_blocks * a.H];
+                at = (((int64_t)id * a.block_size + (p - b * a.block_size)) * a.H + head) * D;
+              } else {
+                latch(a.status, IS_ST_BLOCK_ID);
+              }
+            }
+            if (!scale_ok(ks) || !scale_ok(vs)) {      // hidden, as if the table did not name it
+              latch(a.status, IS_ST_SCALE);
+              at = -1;
+              ks = vs = 1.f;
+            }
+            const uint32_t named = __ballot_sync(0xffffffffu, at >= 0) >> (16 * half);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (j0 + h >= n_tiles) break;
+              const uint32_t slot = n_tile % kMaskRing;
+              if (!wait(&more.tile_empty[slot], ((n_tile / kMaskRing) & 1u) ^ 1u)) break;
+              if (half == h) {
+                TileInfo& info = s_tile[slot];
+                const int lo = max(0, k_see - key0), hi = min(kKeys, k_hi - key0);
+                info.at[grp] = at;
+                s_group[slot][grp] = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
+                if (grp < 4) {                         // a bit a key of 32: four groups' bits to bytes, and the range
+                  const uint32_t four = (named >> (4 * grp)) & 15u;
+                  s_mask[slot][grp] = ((four * 0x00204081u) & 0x01010101u) * 0xffu & bits_between(32 * grp, lo, hi);
+                }
+                if (grp == 0) {
+                  info.lo = lo;
+                  info.hi = hi;
+                  info.rows = j0 + h == 0 ? rows : 0;
+                  info.row0 = row_at;
+                  info.head = head;
+                }
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
+              ++n_tile;
+            }
+            if (!ok) break;
+          }
+          if (!ok) break;
+        }
+        const uint32_t slot = n_tile % kMaskRing;
+        if (ok && wait(&more.tile_empty[slot], ((n_tile / kMaskRing) & 1u) ^ 1u)) {
+          if (lane == 0) {
+            s_tile[slot].rows = -1;
+            mbar_arrive(smem_addr(&bars.mask_full[slot]));
+          }
+        }
+        if (!ok) *abort_flag = 1;
+      }
+    } else if (kScaled && warp < kMmaWarp) {
+      // ---- scaled cache: codes from the cache to fp16 tiles --------------------------
+      // Three warps bring K, three V.  A lane holds one 16-byte chunk of each of its rows in registers; when it has
+      // widened and stored one, it asks for the same chunk of the next tile, which so has a tile's time to arrive.
+      // Eight lanes of a store (a phase of the shared memory) are four even chunks of a row and of its neighbour, whose
+      // swizzle brings them to the odd places: no bank twice.
+      if constexpr (kScaled) {
+        constexpr int C = D / 16, RW = 32 / C, N = (kKeys / RW + kCodeWarps - 1) / kCodeWarps;   // chunks of a row; a warp's rows
+        const int kv = warp >= kLoaderWarp + 1 + kCodeWarps, w = (warp - kLoaderWarp - 1) % kCodeWarps;
+        const int lt = tid - (kLoaderWarp + 1) * 32;   // 0 .. kCodeThreads - 1
+        const int c = (lane & 3) + (C == 8 ? (lane >> 3 & 1) * 4 : 0);
+        const int rw = (lane >> 2 & 1) + (C == 8 ? lane >> 4 : lane >> 3) * 2;       // row of the warp's RW
+        // Unit u = w + 3 k of RW rows.  With RW 4 two units are a group of 8: units of odd k lie in the other half of one.
+        const int64_t token_bytes = (int64_t)a.H * D;
+        const uint8_t* src = a.k_cache + (kv ? a.v_offset : 0) + c * 16;
+        const int64_t row_off[2] = {(rw + (RW == 4 ? 4 * (w & 1) : 0)) * token_bytes, (rw + 4 * (~w & 1)) * token_bytes};
+        const int in_group[2] = {rw + (RW == 4 ? 4 * (w & 1) : 0), RW == 4 ? rw + 4 * (~w & 1) : rw};
+        const int group0[2] = {RW == 4 ? w >> 1 : w, (w + 3) >> 1};                  // of k = 0 and, with RW 4, k = 1
+        uint32_t put[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) put[x] = group0[x] * S::kGroupBytes + at_chunk<D>(in_group[x], 2 * c);
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, limit_ns));
+          return ok;
+        };
+        uint4 code[N];
+        // Chunks k0 .. k0 + kBatch - 1, together: chunk k has the place x of the pairs above and lies some groups on.
+        constexpr int kBatch = 4;
+        auto fetch = [&](const TileInfo& t, bool whole, int k0) {
+          int64_t at[kBatch];
+#pragma unroll
+          for (int k = k0; k < k0 + kBatch && k < N; ++k)
+            at[k - k0] = w + kCodeWarps * k < kKeys / RW ? t.at[group0[RW == 4 ? k & 1 : 0] + (RW == 4 ? (k >> 1) * 3 : k * 3)] : -1;
+#pragma unroll
+          for (int k = k0; k < k0 + kBatch && k < N; ++k) {
+            const int x = RW == 4 ? k & 1 : 0, row = (group0[x] + (RW == 4 ? (k >> 1) * 3 : k * 3)) * kGroup + in_group[x];
+            code[k] = make_uint4(0, 0, 0, 0);
+            if (at[k - k0] >= 0 && (whole || (row >= t.lo && row < t.hi)))
+              asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(code[k].x), "=r"(code[k].y), "=r"(code[k].z), "=r"(code[k].w)
+                           : "l"(src + at[k - k0] + row_off[x]));
+          }
+        };
+        auto load_q = [&](const TileInfo& t, uint32_t n_q) {
+          if (!wait(&bars.q_empty, (n_q & 1u) ^ 1u)) return;
+          const int rows = t.rows;
+          constexpr int QC = D / 8, QP = kCodeThreads / QC;   // chunks of a row; rows of one pass
+          const uint32_t g_inv = (65536u + a.G - 1) / a.G;     // row / G = row * g_inv >> 16 for row < 256, G <= 64
+          const int qc = lt % QC;
+          const uint8_t* q = a.q + (int64_t)t.row0 * a.q_stride + (size_t)t.head * a.G * D * 2 + qc * 16;
+#pragma unroll 4
+          for (int row = lt / QC; row < S::kRows; row += QP) {
+            const int tok = (int)((uint32_t)row * g_inv >> 16);
+            cp_async16(tiles0 + (row >> 7) * S::kTileBytes + at_chunk<D>(row & 127, qc),
+                       row < rows ? q + tok * a.q_stride + (row - tok * a.G) * (D * 2) : q, row < rows);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          if constexpr (kShift) {
+            // bf16 to fp16, in place, as over an FP8 cache: a thread scales a row so that its largest element comes to
+            // [2^14, 2^15), and leaves the inverse for the softmax.
+            mbar_arrive(smem_addr(&more.q_raw));
+            if (!wait(&more.q_raw, n_q & 1u)) return;  // the others' chunks have landed
+            for (int row = lt; row < S::kRows; row += kCodeThreads) scale_query_row<D>(tiles0 + (row >> 7) * S::kTileBytes, row & 127, row < rows, &s_unscale[row]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(smem_addr(&bars.q_full));
+        };
+        uint32_t n_tile = 0, n_q = 0;
+        if (wait(&bars.mask_full[0], 0)) {
+          const TileInfo& t = s_tile[0];
+          if (t.rows >= 0) {
+#pragma unroll
+            for (int k = 0; k < N; k += kBatch) fetch(t, false, k);
+          }
+          for (;; ++n_tile) {
+            const TileInfo& t = s_tile[n_tile % kMaskRing];
+            const int rows = t.rows;
+            if (rows < 0) break;
+            if (kv == 1 && rows > 0) load_q(t, n_q);
+            const uint32_t n = 2 * n_tile + kv, next = (n_tile + 1) % kMaskRing;
+            if (!ok || !wait(&bars.mask_full[next], ((n_tile + 1) / kMaskRing) & 1u) ||
+                !wait(&bars.kv_empty[n % S::kRing], ((n / S::kRing) & 1u) ^ 1u))
+              break;
+            const TileInfo& ahead = s_tile[next];
+            const bool more = ahead.rows >= 0, whole = ahead.lo == 0 && ahead.hi == kKeys;
+            const uint32_t dst = ring0 + (n % S::kRing) * S::kTileBytes;
+#pragma unroll
+            for (int k0 = 0; k0 < N; k0 += kBatch) {
+              uint4 wide[kBatch][2];
+#pragma unroll
+              for (int k = k0; k < k0 + kBatch && k < N; ++k) {
+                wide[k - k0][0] = widen8<kInt8>(code[k].x, code[k].y);
+                wide[k - k0][1] = widen8<kInt8>(code[k].z, code[k].w);
+              }
+              if (more) fetch(ahead, whole, k0);
+#pragma unroll
+              for (int k = k0; k < k0 + kBatch && k < N; ++k) {
+                const uint32_t to = dst + put[RW == 4 ? k & 1 : 0] + (RW == 4 ? (k >> 1) * 3 : k * 3) * S::kGroupBytes;
+                if (w + kCodeWarps * k < kKeys / RW) {
+                  st_shared_v4(to, wide[k - k0][0]);
+                  st_shared_v4(to ^ 16u, wide[k - k0][1]);
+                }
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&bars.kv_full[n % S::kRing]));
+            if (kv == 0 && rows > 0) load_q(t, n_q);
+            n_q += rows > 0;
+            if (!ok) break;
+          }
+        }
+        cp_async_wait<0>();
+        if (!ok) *abort_flag = 1;
+      }
+    } else if (!kScaled && warp < kMmaWarp) {
       // ---- loads --------------------------------------------------------------
       const int lt = tid - kLoaderWarp * 32;           // 0 .. kLoaders - 1
       constexpr int EB = F8 ? 1 : 2;
@@ -799,45 +1229,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             // [2^14, 2^15), and leaves the inverse for the softmax.  (A row to 16 lanes, with shuffles for the largest:
             // 5 us an item, 82 us for the 16 requests' prompts over FP8 where this takes 72.)
             barrier_loaders();                         // the others' chunks have landed
-            for (int row = lt; row < S::kRows; row += kLoaders) {
-              float down = 1.f;
-              if (row < rows) {
-                const uint32_t tile = tiles0 + (row >> 7) * S::kTileBytes;
-                __nv_bfloat162 big(0.f, 0.f);
-                auto larger = [&](uint32_t w) {
-                  w &= 0x7fff7fffu;
-                  big = __hmax2(big, *reinterpret_cast<const __nv_bfloat162*>(&w));
-                };
-#pragma unroll 4
-                for (int k = 0; k < C; ++k) {
-                  const uint4 x = ld_shared_v4(tile + at_chunk<D>(row & 127, k));
-                  larger(x.x);
-                  larger(x.y);
-                  larger(x.z);
-                  larger(x.w);
-                }
-                const float most = fmaxf(__low2float(big), __high2float(big));
-                const int shift =
-                    most > 0.f && most < INFINITY ? min(14 - (int)(((__float_as_uint(most) >> 23) & 255u) - 127), 120) : 0;
-                const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
-                down = __uint_as_float((uint32_t)(127 - shift) << 23);
-#pragma unroll 1
-                for (int k0 = 0; k0 < C; k0 += 4) {
-                  uint4 x[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) x[k] = ld_shared_v4(tile + at_chunk<D>(row & 127, k0 + k));
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    float f[8];
-                    Vec<__nv_bfloat16>::unpack(x[k], f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] *= up;
-                    st_shared_v4(tile + at_chunk<D>(row & 127, k0 + k), Vec<__half>::pack(f));
-                  }
-                }
-              }
-              s_unscale[row] = down;
-            }
+            for (int row = lt; row < S::kRows; row += kLoaders)
+              scale_query_row<D>(tiles0 + (row >> 7) * S::kTileBytes, row & 127, row < rows, &s_unscale[row]);
           }
           fence_proxy_async_smem();
           mbar_arrive(smem_addr(&bars.q_full));
@@ -873,24 +1266,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
           }
         };
-        // Scaled cache: the scales of this thread's keys, once their block is known; a key whose block has one out of range
-        // counts as not named.
-        float2 scale_of[2];
-        auto look_up_scales = [&] {
-          if constexpr (kScaled) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              scale_of[e] = make_float2(1.f, 1.f);
-              if (id[e] >= 0) {
-                const float* at = a.scales + (int64_t)id[e] * a.H + head;
-                scale_of[e] = make_float2(at[0], at[(int64_t)a.num_blocks * a.H]);
-              }
-            }
-          }
-        };
         if (box > 0) look_up_groups(0);
         else look_up(0);
-        look_up_scales();
         // Byte offsets of the tile's keys, for the row copies; -1: no such key.  Returns this thread's keys' mask words.
         auto find_rows = [&](int j, long long* off, uint32_t(&named)[2]) {
           long long at_key[2];
@@ -923,25 +1300,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
               const long long* off = s_off + (j & 1) * kKeys;
               if ((i & 1) == 0) {
                 uint32_t named[2];
-                if constexpr (kScaled) {
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    if (id[e] < 0) continue;
-                    if (scale_ok(scale_of[e].x) && scale_ok(scale_of[e].y)) {   // the same from every key of a group
-                      s_raw_group[j % S::kRaw][(lt + e * kLoaders) / kGroup] = scale_of[e];
-                    } else {
-                      latch(a.status, IS_ST_SCALE);
-                      id[e] = -1;
-                    }
-                  }
-                }
                 find_rows(j, s_off + (j & 1) * kKeys, named);
                 if (lane == 0) s_raw_mask[j % S::kRaw][warp - kLoaderWarp] = named[0];
                 if (lt == 0) s_raw_mask[j % S::kRaw][3] = named[1];
                 look_up(j + 1);
                 ok = agreed(here);
-              } else {
-                look_up_scales();                      // of the next tile's keys
               }
               const uint8_t* src = kbase + ((i & 1) ? a.v_offset : 0) + c * 16;
               const uint32_t dst = raw0 + ((n_load + i) % S::kRaw) * S::kRawBytes;
@@ -975,18 +1338,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
               for (int k = k0; k < k0 + kAhead && k < N; ++k) {
                 const int row = row0 + k * RP;
                 if (row < kKeys) {
-                  st_shared_v4(dst + at_chunk<D>(row, 2 * c), widen8<kInt8>(x[k - k0].x, x[k - k0].y));
-                  st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), widen8<kInt8>(x[k - k0].z, x[k - k0].w));
+                  st_shared_v4(dst + at_chunk<D>(row, 2 * c), widen8<false>(x[k - k0].x, x[k - k0].y));
+                  st_shared_v4(dst + at_chunk<D>(row, 2 * c + 1), widen8<false>(x[k - k0].z, x[k - k0].w));
                 }
               }
             }
             if ((i & 1) == 0 && lt < 4) s_mask[slot][lt] = s_raw_mask[(i >> 1) % S::kRaw][lt];
-            if constexpr (kScaled) {
-              if ((i & 1) == 0 && lt < kKeys / kGroup) {
-                const float2 s = s_raw_group[(i >> 1) % S::kRaw][lt];
-                s_group[slot][lt] = make_float4(s.x, log2f(s.y), 1.f / s.y, 0.f);
-              }
-            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lt == 0 && (i & 1) == 0) mbar_arrive(smem_addr(&bars.mask_full[slot]));
@@ -1118,6 +1475,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
       constexpr uint32_t kIdS = idesc_of<W>(128, false), kIdO = idesc_of<W>(D, true);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), q_tile = __shfl_sync(0xffffffffu, tiles0, 0);
       const uint32_t bar0 = __shfl_sync(0xffffffffu, smem_addr(&bars), 0);
+      const uint32_t tiles_done = kScaled ? __shfl_sync(0xffffffffu, smem_addr(&more.tile_empty[0]), 0) : 0u;
       uint32_t leader;
       asm volatile(
           "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
@@ -1126,6 +1484,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         const uint64_t v_desc = tile_desc<D, F8>(q_tile + S::kQBytes, 1024 >> 4);
 #define ISK_BAR(member) (bar0 + (uint32_t)offsetof(Bars, member))
         uint32_t n_q = 0, p_turn0 = 0, p_turn1 = 0;
+        uint32_t n_tile = 0;
         uint32_t place = 0, turn = 0;                  // of the next load: its place in the ring, and the ring's turn
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -1204,6 +1563,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
               else scores(B, place);
             }
             if (!last) mma_commit(ISK_BAR(kv_empty) + 8 * place);
+            if constexpr (kScaled) mma_commit(tiles_done + 8 * (n_tile++ % kMaskRing));
           }
           if (ok) mma_commit(ISK_BAR(q_empty));
         }
@@ -1235,9 +1595,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 template <typename T, CacheKind KIND, int D>
 static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
   constexpr bool F8 = KIND != kCachePlain;
-  using S = prompt::Shape<D, F8>;
+  constexpr bool kScaled = KIND == kCacheScaledE4m3 || KIND == kCacheScaledInt8;
+  using S = prompt::Shape<D, F8, kScaled>;
   auto* kern = a.wait_ns < kWaitBudgetNs ? prompt::attend_prompt_kernel<T, KIND, D, true> : prompt::attend_prompt_kernel<T, KIND, D, false>;
-  static_assert(S::kSmem + (F8 ? 6144 : 1024) <= 227 * 1024, "a CTA fits an SM");
+  static_assert(S::kSmem + (kScaled ? 8192 : F8 ? 2048 : 1024) <= 227 * 1024, "a CTA fits an SM");
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
   constexpr int kFit = (int)((IS_ATTEND_WORKSPACE_BYTES - partials_offset()) / (2 * sizeof(PartialByEights<S::kRows, D>)));
@@ -1253,7 +1614,7 @@ static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
     box = std::min(a.block_size, prompt::kKeys);
     if (!make_rows_map(&map, a.k_cache, a.D, a.H, 2LL * a.num_blocks * a.block_size, box, a.dtype)) box = 0;
   }
-  e = launch_ex(kern, dim3(grid), dim3(prompt::kThreads), S::kSmem, cfg.stream, cfg.pdl, a, per, box, map);
+  e = launch_ex(kern, dim3(grid), dim3(prompt::threads_of(KIND)), S::kSmem, cfg.stream, cfg.pdl, a, per, box, map);
   if (e != cudaSuccess) return e;
   return launch_ex(attend_join_rows_kernel<T, S::kRows, D, true>, dim3(grid, 32), dim3(kJoinThreads), 0, cfg.stream,
                    cfg.pdl, a);
