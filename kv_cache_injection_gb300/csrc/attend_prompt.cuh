@@ -108,15 +108,18 @@ struct Shape {
   static constexpr uint32_t kGroupBytes = kHalves * 1024;
   static constexpr uint32_t kTileBytes = 16 * kGroupBytes;
   static constexpr int kRing =           // K and V tiles in shared memory
-      D == 256 ? 2 : SCALED ? (D == 128 ? 4 : 8) : F8 ? (D == 128 ? 3 : 5) : D == 128 ? 5 : 8;
+      D == 256 ? 2 : SCALED ? (D == 128 ? 3 : 8) : F8 ? (D == 128 ? 3 : 5) : D == 128 ? 5 : 8;
   // FP8 rows are copied as they are, kRaw tiles ahead, and widened from there.
   static constexpr int kRaw = D == 128 ? 3 : 4;
   static constexpr uint32_t kRawBytes = F8 && !SCALED ? 128 * D : 0;
+  // Scaled cache: batches of four chunks that bring a thread's part of a tile, and the place of two tiles of them.
+  static constexpr int kBatches = D == 128 ? 3 : 2;
+  static constexpr size_t kCodeBytes = SCALED ? 2 * kBatches * 4 * 32 * kCodeWarps * 16 : 0;
   // A tile's mask is written when its K has a place, that is once load 2 t - kRing has been released; the mask it
   // replaces has been read once V of tile t - kMaskRing, load 2 (t - kMaskRing) + 1, has been released.
   static_assert(2 * kMaskRing >= kRing + 1, "a mask is read before its place is used again");
   static constexpr size_t kSmem = 1024 + kQBytes + kRing * (size_t)kTileBytes + kRaw * (size_t)kRawBytes +
-                                  (SCALED ? 0 : F8 ? 2 : 1) * 128 * 8;
+                                  kCodeBytes + (SCALED ? 0 : F8 ? 2 : 1) * 128 * 8;
   static constexpr uint32_t kOCol = 256;                      // first column of O_A; O_B follows D columns on
 };
 
@@ -449,20 +452,17 @@ __device__ __noinline__ float far_weights(uint32_t s_col, float sc, float m, flo
 
 // Scaled cache, one tile of a row: S (logits before their scale) becomes weights
 // over it.  A weight holds its key's V scale, x = logit + log2 of it, and the sum
-// takes that back by groups of eight.  S is read twice, 32 columns ahead of their
-// use, for the maximum of x and for the weights: keeping all 128 between the two
-// takes registers that the loaders need.  Of 32 logits S is read before the 16
-// columns of their weights, which lie before the next ones', are written.  The
-// groups' scales are read ahead with them.
-template <int D>
-struct ScaledTile;
-template <typename W, int D>
-__device__ float far_scaled_weights(ScaledTile<D> t, float mz, float l);
+// takes that back by groups of eight.  S is read twice, for the maximum of x and
+// for the weights, in loops of 64 and 32 columns: with all 128 unrolled between one
+// read and its use the warps of an SM, each in a part of the code of its own,
+// waited for instructions in a quarter of their time.  Of 32 logits S is read
+// before the 16 columns of their weights, which lie before the next ones', are
+// written.
 template <int D>
 struct ScaledTile {
   uint32_t s_col;
   float sc;
-  uint4 named;
+  const uint32_t* named;
   const float4* groups;
   int key0, low, end;
   bool check;
@@ -471,85 +471,86 @@ struct ScaledTile {
 
   __device__ __forceinline__ void hide(uint32_t (&y)[32], int c) const {
     if (!check) return;
-    const uint32_t word = c == 0 ? named.x : c == 1 ? named.y : c == 2 ? named.z : named.w;
-    const uint32_t see = word & bits_between(key0 + 32 * c, low, end);
+    const uint32_t see = named[c] & bits_between(key0 + 32 * c, low, end);
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       if (!((see >> i) & 1u)) y[i] = 0xff800000u;
   }
-  struct Scales {
-    float4 k[32 / kGroup];
-  };
-  __device__ __forceinline__ Scales scales(int c) const {
-    Scales s;
-#pragma unroll
-    for (int g = 0; g < 32 / kGroup; ++g) s.k[g] = groups[c * (32 / kGroup) + g];
-    return s;
-  }
-  __device__ __forceinline__ float top(uint32_t (&y)[32], int c, const Scales& s) const {
+  __device__ __forceinline__ float top(uint32_t (&y)[32], int c) const {
     hide(y, c);
     float x[32 / kGroup];
 #pragma unroll
     for (int g = 0; g < 32 / kGroup; ++g) {
+      const float4 k = groups[c * (32 / kGroup) + g];
       const uint32_t* v = y + g * kGroup;
       float x0 = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
       const float x1 = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
       x0 = max3(x0, __uint_as_float(v[6]), __uint_as_float(v[7]));
-      x[g] = fmaf(fmaxf(x0, x1), group_factor(sc, s.k[g].x), s.k[g].y);   // grows with the logits of a group
+      x[g] = fmaf(fmaxf(x0, x1), group_factor(sc, k.x), k.y);   // grows with the logits of a group
     }
     return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
   }
-  // FAR: exponents rounded as they were for the maximum (see kFar).
+  // The weights of all columns, the first 32 of which are on their way to y, and their sum on top of l.  FAR: exponents
+  // rounded as they were for the maximum (see kFar).
   template <typename W, bool FAR>
-  __device__ __forceinline__ void weights(uint32_t (&y)[32], int c, const Scales& s, float mz, unsigned long long& sum) const {
-    hide(y, c);
-    uint32_t p[16];
+  __device__ __forceinline__ float weights(uint32_t (&y)[32], float mz, float l) const {
+    unsigned long long sum = pk2(l, 0.f);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      float4 k[32 / kGroup];
 #pragma unroll
-    for (int g = 0; g < 32 / kGroup; ++g) {
-      const float4 k = s.k[g];
-      const float factor = group_factor(sc, k.x), off = FAR ? k.y : k.y - mz;
-      const unsigned long long factor2 = pk2(factor, factor), off2 = pk2(off, off);
-      unsigned long long of_group = 0ull;
+      for (int g = 0; g < 32 / kGroup; ++g) k[g] = groups[c * (32 / kGroup) + g];
+      tmem_wait_ld32(y);
+      hide(y, c);
+      float x[32];
 #pragma unroll
-      for (int i = g * kGroup / 2; i < (g + 1) * kGroup / 2; ++i) {
-        float y0, y1;
-        upk2(fma2_rn(pk2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), factor2, off2), y0, y1);
-        y0 = ex2(FAR ? __fsub_rn(y0, mz) : y0);
-        y1 = ex2(FAR ? __fsub_rn(y1, mz) : y1);
-        of_group = i == g * kGroup / 2 ? pk2(y0, y1) : add2_rn(of_group, pk2(y0, y1));
-        p[i] = Vec<W>::pack2(y0, y1);
+      for (int g = 0; g < 32 / kGroup; ++g) {
+        const float factor = group_factor(sc, k[g].x), off = FAR ? k[g].y : k[g].y - mz;
+        const unsigned long long factor2 = pk2(factor, factor), off2 = pk2(off, off);
+#pragma unroll
+        for (int i = g * kGroup; i < (g + 1) * kGroup; i += 2)
+          upk2(fma2_rn(pk2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), factor2, off2), x[i], x[i + 1]);
       }
-      sum = fma2_rn(of_group, pk2(k.z, k.z), sum);
+      if (c < 3) tmem_ld32(s_col + 32 * (c + 1), y);
+      uint32_t p[16];
+#pragma unroll
+      for (int g = 0; g < 32 / kGroup; ++g) {
+        unsigned long long of_group = 0ull;
+#pragma unroll
+        for (int i = g * kGroup; i < (g + 1) * kGroup; i += 2) {
+          const float y0 = ex2(FAR ? __fsub_rn(x[i], mz) : x[i]), y1 = ex2(FAR ? __fsub_rn(x[i + 1], mz) : x[i + 1]);
+          of_group = i == g * kGroup ? pk2(y0, y1) : add2_rn(of_group, pk2(y0, y1));
+          p[i / 2] = Vec<W>::pack2(y0, y1);
+        }
+        sum = fma2_rn(of_group, pk2(k[g].z, k[g].z), sum);
+      }
+      tmem_st16(s_col + 16 * c, p);
+      if (c & 1) {                       // half of the keys: their part of O += P V can start
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * (c >> 1));
+      }
     }
-    tmem_st16(s_col + 16 * c, p);
-    if (c & 1) {                         // half of the keys: their part of O += P V can start
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + 8 * (c >> 1));
-    }
+    float l0, l1;
+    upk2(sum, l0, l1);
+    return l0 + l1;
   }
   // The tile's weights for maximum m and sum l, both brought up to date with O.
   template <typename W>
   __device__ __forceinline__ float run(uint32_t o_col, bool has_o, float& m, float l) const {
     uint32_t a[32], b[32];
+    float most = -INFINITY;
     tmem_ld32(s_col, a);
     tmem_ld32(s_col + 32, b);
-    Scales sa = scales(0), sb = scales(1);
-    tmem_wait_ld32(a, b);
-    float most = top(a, 0, sa);
-    tmem_ld32(s_col + 64, a);
-    sa = scales(2);
-    most = fmaxf(most, top(b, 1, sb));
-    tmem_ld32(s_col + 96, b);
-    sb = scales(3);
-    tmem_wait_ld32(a, b);
-    most = fmaxf(most, top(a, 2, sa));
-    tmem_ld32(s_col, a);
-    sa = scales(0);
-    most = fmaxf(most, top(b, 3, sb));
-    tmem_ld32(s_col + 32, b);
-    sb = scales(1);
+#pragma unroll 1
+    for (int c = 0; c < 4; c += 2) {
+      tmem_wait_ld32(a, b);
+      most = fmaxf(most, top(a, c));
+      tmem_ld32(s_col + (c ? 0 : 64), a);
+      most = fmaxf(most, top(b, c + 1));
+      if (c == 0) tmem_ld32(s_col + 96, b);
+    }
     // A logit past the bound moves m; far rows come here with every tile.
     if (__any_sync(0xffffffffu, most > (fabsf(m) > kFar ? -INFINITY : lazy_bound<W>(m)))) {
       const float mn = fmaxf(m, most - kRaise<W>);
@@ -567,41 +568,11 @@ struct ScaledTile {
           tmem_st16(o_col + 16 * c, y);
         }
       }
-      if (__any_sync(0xffffffffu, fabsf(m) > kFar && m > -INFINITY)) return far_scaled_weights<W, D>(*this, m == -INFINITY ? 0.f : m, l);
+      if (__any_sync(0xffffffffu, fabsf(m) > kFar && m > -INFINITY)) return weights<W, true>(a, m == -INFINITY ? 0.f : m, l);
     }
-    const float mz = m == -INFINITY ? 0.f : m;
-    unsigned long long sum = pk2(l, 0.f);
-    tmem_wait_ld32(a, b);
-    weights<W, false>(a, 0, sa, mz, sum);
-    tmem_ld32(s_col + 64, a);
-    sa = scales(2);
-    weights<W, false>(b, 1, sb, mz, sum);
-    tmem_ld32(s_col + 96, b);
-    sb = scales(3);
-    tmem_wait_ld32(a, b);
-    weights<W, false>(a, 2, sa, mz, sum);
-    weights<W, false>(b, 3, sb, mz, sum);
-    float l0, l1;
-    upk2(sum, l0, l1);
-    return l0 + l1;
+    return weights<W, false>(a, m == -INFINITY ? 0.f : m, l);
   }
 };
-
-template <typename W, int D>
-__device__ __noinline__ float far_scaled_weights(ScaledTile<D> t, float mz, float l) {
-  unsigned long long sum = pk2(l, 0.f);
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t y[32];
-    tmem_ld32(t.s_col + 32 * c, y);
-    const typename ScaledTile<D>::Scales s = t.scales(c);
-    tmem_wait_ld32(y);
-    t.template weights<W, true>(y, c, s, mz, sum);
-  }
-  float l0, l1;
-  upk2(sum, l0, l1);
-  return l0 + l1;
-}
 
 constexpr int threads_of(CacheKind kind) { return kind == kCacheScaledE4m3 || kind == kCacheScaledInt8 ? kScaledThreads : kThreads; }
 
@@ -756,7 +727,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
           if constexpr (kScaled) {
             const uint4 named = *reinterpret_cast<const uint4*>(s_mask[slot]);
             const bool check = (named.x & named.y & named.z & named.w) != 0xffffffffu || key0 + kKeys - 1 > lim_lo || key0 < low_hi;
-            const ScaledTile<D> tile{s_col, sc, named, s_group[slot], key0, low, lim + 1, check, smem_addr(&bars.p_full[side][0]), lane};
+            const ScaledTile<D> tile{s_col, sc, s_mask[slot], s_group[slot], key0, low, lim + 1, check, smem_addr(&bars.p_full[side][0]), lane};
             l = tile.template run<W>(o_col, j > 0, m, l);
             continue;
           }
@@ -1018,46 +989,49 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
       }
     } else if (kScaled && warp < kMmaWarp) {
       // ---- scaled cache: codes from the cache to fp16 tiles --------------------------
-      // Three warps bring K, three V.  A lane holds one 16-byte chunk of each of its rows in registers; when it has
-      // widened and stored one, it asks for the same chunk of the next tile, which so has a tile's time to arrive.
+      // Three warps bring K, three V.  A lane has one 16-byte chunk of each of its rows in a place of its own in shared
+      // memory; when it has widened and stored four, it asks for the same four of the next tile, which so have a tile's
+      // time to arrive.  (In registers they would have no second trip, but would have to be unrolled: see ScaledTile.)
       // Eight lanes of a store (a phase of the shared memory) are four even chunks of a row and of its neighbour, whose
       // swizzle brings them to the odd places: no bank twice.
       if constexpr (kScaled) {
-        constexpr int C = D / 16, RW = 32 / C, N = (kKeys / RW + kCodeWarps - 1) / kCodeWarps;   // chunks of a row; a warp's rows
+        constexpr int C = D / 16, RW = 32 / C, kUnits = kKeys / RW;   // chunks of a row; a warp's rows
+        constexpr int kBatch = 4, kBatches = S::kBatches, kCodeGroup = 32 * kCodeWarps;
         const int kv = warp >= kLoaderWarp + 1 + kCodeWarps, w = (warp - kLoaderWarp - 1) % kCodeWarps;
         const int lt = tid - (kLoaderWarp + 1) * 32;   // 0 .. kCodeThreads - 1
         const int c = (lane & 3) + (C == 8 ? (lane >> 3 & 1) * 4 : 0);
         const int rw = (lane >> 2 & 1) + (C == 8 ? lane >> 4 : lane >> 3) * 2;       // row of the warp's RW
-        // Unit u = w + 3 k of RW rows.  With RW 4 two units are a group of 8: units of odd k lie in the other half of one.
-        const int64_t token_bytes = (int64_t)a.H * D;
-        const uint8_t* src = a.k_cache + (kv ? a.v_offset : 0) + c * 16;
-        const int64_t row_off[2] = {(rw + (RW == 4 ? 4 * (w & 1) : 0)) * token_bytes, (rw + 4 * (~w & 1)) * token_bytes};
-        const int in_group[2] = {rw + (RW == 4 ? 4 * (w & 1) : 0), RW == 4 ? rw + 4 * (~w & 1) : rw};
-        const int group0[2] = {RW == 4 ? w >> 1 : w, (w + 3) >> 1};                  // of k = 0 and, with RW 4, k = 1
-        uint32_t put[2];
+        // Unit u = w + 3 k of RW rows, k = 4 b + i.  With RW 4 two units are a group of 8: units of odd k lie in the other
+        // half of one.  Of pair x = i % 2: row in its group, first group (b = i / 2 = 0), bytes from the group to the chunk.
+        constexpr int X = RW == 4 ? 2 : 1, kGroupStep = RW == 4 ? 3 : 3;             // groups from i to i + X
+        int in_group[X];
+        uint32_t put[X], row_off[X];
+        int group0[X];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) put[x] = group0[x] * S::kGroupBytes + at_chunk<D>(in_group[x], 2 * c);
+        for (int x = 0; x < X; ++x) {
+          in_group[x] = RW == 4 ? rw + 4 * ((w + x) & 1) : rw;
+          group0[x] = RW == 4 ? (w + 3 * x) >> 1 : w;
+          put[x] = group0[x] * S::kGroupBytes + at_chunk<D>(in_group[x], 2 * c);
+          row_off[x] = (uint32_t)(in_group[x] * a.H * D) + c * 16;
+        }
+        const uint8_t* src = a.k_cache + (kv ? a.v_offset : 0);
+        // A thread's chunks as they are, 16 bytes for each k.
+        const uint32_t raw = ring0 + S::kRing * S::kTileBytes + (kv * kBatches * kBatch * kCodeGroup + lt % kCodeGroup) * 16;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, limit_ns));
           return ok;
         };
-        uint4 code[N];
-        // Chunks k0 .. k0 + kBatch - 1, together: chunk k has the place x of the pairs above and lies some groups on.
-        constexpr int kBatch = 4;
-        auto fetch = [&](const TileInfo& t, bool whole, int k0) {
-          int64_t at[kBatch];
+        // Asks for batch b of a tile.
+        auto fetch = [&](const TileInfo& t, bool whole, int b) {
 #pragma unroll
-          for (int k = k0; k < k0 + kBatch && k < N; ++k)
-            at[k - k0] = w + kCodeWarps * k < kKeys / RW ? t.at[group0[RW == 4 ? k & 1 : 0] + (RW == 4 ? (k >> 1) * 3 : k * 3)] : -1;
-#pragma unroll
-          for (int k = k0; k < k0 + kBatch && k < N; ++k) {
-            const int x = RW == 4 ? k & 1 : 0, row = (group0[x] + (RW == 4 ? (k >> 1) * 3 : k * 3)) * kGroup + in_group[x];
-            code[k] = make_uint4(0, 0, 0, 0);
-            if (at[k - k0] >= 0 && (whole || (row >= t.lo && row < t.hi)))
-              asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(code[k].x), "=r"(code[k].y), "=r"(code[k].z), "=r"(code[k].w)
-                           : "l"(src + at[k - k0] + row_off[x]));
+          for (int i = 0; i < kBatch; ++i) {
+            const int x = i % X, group = group0[x] + (b * (kBatch / X) + i / X) * kGroupStep;
+            const bool mine = w + kCodeWarps * (kBatch * b + i) < kUnits;
+            const int64_t at = mine ? t.at[group] : -1;
+            const int row = group * kGroup + in_group[x];
+            const bool in = at >= 0 && (whole || (row >= t.lo && row < t.hi));
+            cp_async16(raw + (kBatch * b + i) * kCodeGroup * 16, in ? src + at + row_off[x] : src, in);
           }
         };
         auto load_q = [&](const TileInfo& t, uint32_t n_q) {
@@ -1088,9 +1062,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
         uint32_t n_tile = 0, n_q = 0;
         if (wait(&bars.mask_full[0], 0)) {
           const TileInfo& t = s_tile[0];
-          if (t.rows >= 0) {
-#pragma unroll
-            for (int k = 0; k < N; k += kBatch) fetch(t, false, k);
+#pragma unroll 1
+          for (int b = 0; b < kBatches; ++b) {
+            if (t.rows >= 0) fetch(t, false, b);
+            cp_async_commit();
           }
           for (;; ++n_tile) {
             const TileInfo& t = s_tile[n_tile % kMaskRing];
@@ -1104,23 +1079,27 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
             const TileInfo& ahead = s_tile[next];
             const bool more = ahead.rows >= 0, whole = ahead.lo == 0 && ahead.hi == kKeys;
             const uint32_t dst = ring0 + (n % S::kRing) * S::kTileBytes;
+#pragma unroll 1
+            for (int b = 0; b < kBatches; ++b) {
+              cp_async_wait<kBatches - 1>();
+              uint4 code[kBatch];
 #pragma unroll
-            for (int k0 = 0; k0 < N; k0 += kBatch) {
+              for (int i = 0; i < kBatch; ++i) code[i] = ld_shared_v4(raw + (kBatch * b + i) * kCodeGroup * 16);
               uint4 wide[kBatch][2];
 #pragma unroll
-              for (int k = k0; k < k0 + kBatch && k < N; ++k) {
-                wide[k - k0][0] = widen8<kInt8>(code[k].x, code[k].y);
-                wide[k - k0][1] = widen8<kInt8>(code[k].z, code[k].w);
+              for (int i = 0; i < kBatch; ++i) {
+                wide[i][0] = widen8<kInt8>(code[i].x, code[i].y);
+                wide[i][1] = widen8<kInt8>(code[i].z, code[i].w);
               }
-              if (more) fetch(ahead, whole, k0);
 #pragma unroll
-              for (int k = k0; k < k0 + kBatch && k < N; ++k) {
-                const uint32_t to = dst + put[RW == 4 ? k & 1 : 0] + (RW == 4 ? (k >> 1) * 3 : k * 3) * S::kGroupBytes;
-                if (w + kCodeWarps * k < kKeys / RW) {
-                  st_shared_v4(to, wide[k - k0][0]);
-                  st_shared_v4(to ^ 16u, wide[k - k0][1]);
+              for (int i = 0; i < kBatch; ++i)
+                if (w + kCodeWarps * (kBatch * b + i) < kUnits) {
+                  const uint32_t to = dst + put[i % X] + (b * (kBatch / X) + i / X) * kGroupStep * S::kGroupBytes;
+                  st_shared_v4(to, wide[i][0]);
+                  st_shared_v4(to ^ 16u, wide[i][1]);
                 }
-              }
+              if (more) fetch(ahead, whole, b);
+              cp_async_commit();
             }
             fence_proxy_async_smem();
             __syncwarp();
