@@ -16,6 +16,8 @@
 // Longer groups go through twice, once for the scale and once for the codes.
 // The queries are rotated by CTAs of their own, a warp or several to a token.
 // Bound by memory; each input is read once and each code written once.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -50,30 +52,67 @@ __device__ __forceinline__ float2 turn_of(const AxisTurns& at, int i, float p, f
   return make_float2(cs, sign * sn);
 }
 
-// Rotates the pair of vectors f and f + gv of a head: NeoX pairs element e of one
-// with element e of the other, interleaved pairs neighbours.
+// The sines of a lane's pairs: NeoX vectors f and f + gv of a head rotate element
+// e of one with element e of the other, interleaved ones neighbours within each.
+// Either way a lane has VE pairs; pair_of(f, e) is the e-th one's number.
+template <int VE, int STYLE>
+__device__ __forceinline__ int pair_of(int f, int e, int gv) {
+  return STYLE == 0 ? f * VE + e : (e < VE / 2 ? f : f + gv) * (VE / 2) + e % (VE / 2);
+}
+template <int VE>
+struct Turn {
+  float cs[VE], sn[VE];
+};
+// A row's sines in shared memory: by pieces of four, cosines then sines, a piece of
+// all lanes after the other, so that eight lanes' 16 bytes lie in different banks.
+template <int VE>
+__device__ __forceinline__ int turn_at(int f, int e, int gv) { return ((e / 4) * gv + f) * 4 + e % 4; }
+template <int VE>
+__device__ __forceinline__ Turn<VE> load_turn(const float* row, int f, int gv) {
+  Turn<VE> t;
+#pragma unroll
+  for (int q = 0; q < VE / 4; ++q) {
+    const float4 c = *reinterpret_cast<const float4*>(row + (q * gv + f) * 4);
+    const float4 s = *reinterpret_cast<const float4*>(row + ((q + VE / 4) * gv + f) * 4);
+    t.cs[4 * q] = c.x, t.cs[4 * q + 1] = c.y, t.cs[4 * q + 2] = c.z, t.cs[4 * q + 3] = c.w;
+    t.sn[4 * q] = s.x, t.sn[4 * q + 1] = s.y, t.sn[4 * q + 2] = s.z, t.sn[4 * q + 3] = s.w;
+  }
+  return t;
+}
 template <typename T, int STYLE>
-__device__ __forceinline__ void rotate_pair(const float2* turn, int f, int gv, float (&x)[Vec<T>::N], float (&z)[Vec<T>::N]) {
+__device__ __forceinline__ void rotate_pair(const Turn<Vec<T>::N>& t, float (&x)[Vec<T>::N], float (&z)[Vec<T>::N]) {
   constexpr int VE = Vec<T>::N;
   if constexpr (STYLE == 0) {
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const float2 t = turn[f * VE + e];
       const float a = x[e], b = z[e];
-      x[e] = fmaf(a, t.x, -__fmul_rn(b, t.y));
-      z[e] = fmaf(b, t.x, __fmul_rn(a, t.y));
+      x[e] = fmaf(a, t.cs[e], -__fmul_rn(b, t.sn[e]));
+      z[e] = fmaf(b, t.cs[e], __fmul_rn(a, t.sn[e]));
     }
   } else {
 #pragma unroll
     for (int e = 0; e < VE / 2; ++e) {
-      const float2 t = turn[f * (VE / 2) + e], u = turn[(f + gv) * (VE / 2) + e];
       const float a = x[2 * e], b = x[2 * e + 1], c = z[2 * e], d = z[2 * e + 1];
-      x[2 * e] = fmaf(a, t.x, -__fmul_rn(b, t.y));
-      x[2 * e + 1] = fmaf(b, t.x, __fmul_rn(a, t.y));
-      z[2 * e] = fmaf(c, u.x, -__fmul_rn(d, u.y));
-      z[2 * e + 1] = fmaf(d, u.x, __fmul_rn(c, u.y));
+      x[2 * e] = fmaf(a, t.cs[e], -__fmul_rn(b, t.sn[e]));
+      x[2 * e + 1] = fmaf(b, t.cs[e], __fmul_rn(a, t.sn[e]));
+      z[2 * e] = fmaf(c, t.cs[VE / 2 + e], -__fmul_rn(d, t.sn[VE / 2 + e]));
+      z[2 * e + 1] = fmaf(d, t.cs[VE / 2 + e], __fmul_rn(c, t.sn[VE / 2 + e]));
     }
   }
+}
+// The sines of one token's pairs, computed by a warp and kept by each lane for its f.
+template <typename T, int STYLE>
+__device__ __forceinline__ Turn<Vec<T>::N> warp_turn(const AxisTurns& at, float* row, int half, int gv, int f, int32_t of_axis, float sign) {
+  constexpr int VE = Vec<T>::N;
+  const int lane = threadIdx.x & 31;
+  for (int i0 = 0; i0 < half; i0 += 32) {        // half may be 8 or 16: then lanes past it repeat pairs
+    const int i = (i0 + lane) % half, g = i / VE, e = i % VE, j = pair_of<VE, STYLE>(g, e, gv);
+    const float2 v = turn_of(at, j, (float)__shfl_sync(0xffffffffu, of_axis, ld_table(&at.axis[j])), sign);
+    row[turn_at<VE>(g, e, gv)] = v.x;
+    row[turn_at<VE>(g, e + VE, gv)] = v.y;
+  }
+  __syncwarp();
+  return load_turn<VE>(row, f, gv);
 }
 
 __device__ __forceinline__ float larger_finite(float most, float x) {
@@ -118,7 +157,7 @@ __device__ __forceinline__ uint4 again(const uint4& c, float ratio) {
 
 // The queries of a token, one or `share` warps to it; a refused token's row is left as it was.
 template <typename T, int STYLE>
-__device__ void rotate_queries(const AppendArgs& a, const AxisTurns& at, float2* turn, int64_t w, int share) {
+__device__ void rotate_queries(const AppendArgs& a, const AxisTurns& at, float* row, int64_t w, int share) {
   constexpr int VE = Vec<T>::N, kBatch = 4;
   const int lane = threadIdx.x & 31, half = a.D / 2, gv = a.D / VE / 2;
   const int64_t t = w / share;
@@ -141,11 +180,7 @@ __device__ void rotate_queries(const AppendArgs& a, const AxisTurns& at, float2*
   load(first);
   if (slot < 0 || slot >= a.n_slots) return;     // padding, or reported by the CTA that looks at the token's block
   if (__any_sync(0xffffffffu, of_axis < 0 || of_axis >= IS_MAX_POSITION)) return;
-  for (int i0 = 0; i0 < half; i0 += 32) {        // half may be 8 or 16: then lanes past it repeat pairs
-    const int i = (i0 + lane) % half;
-    turn[i] = turn_of(at, i, (float)__shfl_sync(0xffffffffu, of_axis, ld_table(&at.axis[i])), 1.f);
-  }
-  __syncwarp();
+  const Turn<VE> turn = warp_turn<T, STYLE>(at, row, half, gv, f, of_axis, 1.f);
   uint8_t* dst = a.q_out + (size_t)t * a.Hq * a.D * sizeof(T);
   for (int i0 = first; i0 < n; i0 += kBatch * step) {
     if (i0 != first) load(i0);
@@ -156,7 +191,7 @@ __device__ void rotate_queries(const AppendArgs& a, const AxisTurns& at, float2*
       float x[VE], z[VE];
       Vec<T>::unpack(x0[u], x);
       Vec<T>::unpack(x1[u], z);
-      rotate_pair<T, STYLE>(turn, f, gv, x, z);
+      rotate_pair<T, STYLE>(turn, x, z);
       st_v4(dst + offset(i), Vec<T>::pack(x));
       st_v4(dst + offset(i) + gv * 16, Vec<T>::pack(z));
     }
@@ -166,51 +201,69 @@ __device__ void rotate_queries(const AppendArgs& a, const AxisTurns& at, float2*
 // STYLE -1: no rotation (a move).
 template <typename T, int STYLE, bool I8>
 __global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledWriteArgs p, const __grid_constant__ AxisTurns at,
-                                                                  int64_t group_ctas, int splits, int share) {
+                                                                  int64_t group_ctas, int window, int splits, int share) {
   constexpr int VE = Vec<T>::N;
   const AppendArgs& a = p.a;
-  extern __shared__ float2 s_turn[];             // the group's tile [rows][D / 2], or a query warp's [D / 2] each
+  extern __shared__ __align__(16) float s_turn[];   // the group's tile [rows][D], or a query warp's [D] each
   __shared__ int32_t s_row[kRowsOfTile];         // row of the block; -1: the token is skipped
   __shared__ int64_t s_from[kRowsOfTile];
+  __shared__ uint32_t s_leaders;
+  __shared__ struct { int64_t block, n; int32_t low; } s_group;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = a.D / 2;
   pdl_wait();
   pdl_trigger();
   if ((int64_t)blockIdx.x >= group_ctas) {
     if constexpr (STYLE >= 0) {
-      rotate_queries<T, STYLE>(a, at, s_turn + warp * half, ((int64_t)blockIdx.x - group_ctas) * kWarps + warp, share);
+      rotate_queries<T, STYLE>(a, at, s_turn + warp * a.D, ((int64_t)blockIdx.x - group_ctas) * kWarps + warp, share);
     }
     return;
   }
-  const int64_t t0 = blockIdx.x / splits;
-  const int head0 = (int)(blockIdx.x - t0 * splits) * kHeadsPerCta, heads = min(kHeadsPerCta, a.H - head0);
-
-  // The group: every warp finds it for itself, 31 tokens at a time.
+  const int64_t begin = blockIdx.x / splits * (int64_t)window;
+  const int head0 = (int)(blockIdx.x % splits) * kHeadsPerCta, heads = min(kHeadsPerCta, a.H - head0);
   auto block_at = [&](int64_t t) -> int64_t {
     if (t < 0 || t >= a.T) return -1;
     const int64_t slot = a.slots[t];
     return slot < 0 || slot >= a.n_slots ? -1 : block_of_slot(slot, p.block_size, p.block_shift);
   };
-  const int64_t mine = block_at(t0 - 1 + lane);
-  const int64_t block = __shfl_sync(0xffffffffu, mine, 1);
-  if (block < 0) {
-    if (tid == 0 && head0 == 0 && a.slots[t0] != -1) latch(a.status, IS_ST_BLOCK_ID);
-    return;
+  // The groups that begin in this CTA's tokens begin .. begin + window - 1 (window <= 16): lane i looks at token begin - 1 + i.
+  // One warp looks, so that the CTA agrees on its groups whatever happens to the caller's slots meanwhile.
+  int64_t mine = -1;
+  if (warp == 0) {
+    mine = block_at(begin - 1 + lane);
+    const int64_t before = __shfl_up_sync(0xffffffffu, mine, 1);
+    const bool ours = lane >= 1 && lane <= window && begin - 1 + lane < a.T;
+    const uint32_t found = __ballot_sync(0xffffffffu, ours && mine >= 0 && mine != before);
+    if (head0 == 0 && ours && mine < 0 && a.slots[begin - 1 + lane] != -1) latch(a.status, IS_ST_BLOCK_ID);
+    if (lane == 0) s_leaders = found;
   }
-  const uint32_t same = __ballot_sync(0xffffffffu, mine == block);
-  if (same & 1u) return;                         // the token before it is of the same block
-  int64_t n = __ffs(~(same >> 1)) - 1;           // bit 31 of same >> 1 is 0
-  while (n % 31 == 0) {
-    const uint32_t more = __ballot_sync(0xffffffffu, lane < 31 && block_at(t0 + n + lane) == block);
-    n += __ffs(~more) - 1;
-    if ((more & 0x7fffffffu) != 0x7fffffffu) break;
+  __syncthreads();
+  for (uint32_t leaders = s_leaders; leaders; leaders &= leaders - 1) {
+  const int first = __ffs(leaders) - 1;
+  const int64_t t0 = begin - 1 + first;
+  if (warp == 0) {
+    const int64_t block = __shfl_sync(0xffffffffu, mine, first);
+    int64_t n = 0;                               // its tokens, 31 at a time
+    int32_t low = p.block_size;                  // the lowest of their rows: below it the block is held already
+    for (uint32_t more = ~0u; n % 31 == 0 && more != 0;) {
+      const int64_t t = t0 + n + lane;
+      const bool in = lane < 31 && block_at(t) == block;
+      if (in) low = min(low, (int32_t)max(a.slots[t] - block * p.block_size, (int64_t)0));
+      more = __ballot_sync(0xffffffffu, in);
+      n += __ffs(~more) - 1;             // bit 31 is 0
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) {
+      s_group.block = block;
+      s_group.n = max(n, (int64_t)1);
+      s_group.low = low;
+    }
   }
-  int32_t low = INT32_MAX;                       // the lowest of the group's rows: below it the block is held already
-  for (int64_t i = lane; i < n; i += 32) low = min(low, (int32_t)(a.slots[t0 + i] - block * p.block_size));
-  low = __reduce_min_sync(0xffffffffu, low);
-
+  __syncthreads();
+  const int64_t block = s_group.block, n = s_group.n;
+  const int32_t low = s_group.low;
   const int gv = a.D / VE / 2, f = lane % gv, tile_rows = kRowsOfTile / gv, row_step = 32 / gv;
   const int units = 2 * heads;                   // keys of each head, then values
-  // Tokens t0 + i0 .. of the group: their rows, sources and sines.
+  // Tokens t0 + i0 .. of the group: their rows and sources, and their keys' sines.
   bool any = false;                              // some token is not skipped
   auto stage = [&](int64_t i0) {
     const int cnt = (int)min((int64_t)tile_rows, n - i0);
@@ -218,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledW
     __syncthreads();
     for (int i = tid; i < cnt; i += kThreads) {
       const int64_t t = t0 + i0 + i;
-      int32_t row = (int32_t)(a.slots[t] - block * p.block_size);
+      const int64_t in_block = a.slots[t] - block * p.block_size;
+      int32_t row = in_block >= 0 && in_block < p.block_size ? (int32_t)in_block : -1;
       int64_t from = t;
       if (p.from) {
         from = p.from[t];
@@ -240,46 +294,54 @@ __global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledW
       s_from[i] = from;
       put |= row >= 0;
     }
-    if constexpr (STYLE >= 0) {
-      for (int x = tid; x < cnt * half; x += kThreads) {
-        const int i = x / half, j = x - i * half;
-        const int32_t pos = a.positions[(size_t)ld_table(&at.axis[j]) * a.T + t0 + i0 + i];
-        s_turn[x] = turn_of(at, j, (float)pos, 1.f);
-      }
-    }
     any |= __syncthreads_or(put) != 0;
     return cnt;
   };
-  uint4 x0[kPairs], x1[kPairs];
-  auto load = [&](int unit, int cnt) {
+  auto stage_turns = [&](int64_t i0, int cnt) {
+    if constexpr (STYLE >= 0) {
+      for (int x = tid; x < cnt * half; x += kThreads) {
+        const int i = x / half, g = (x - i * half) / VE, e = x % VE, j = pair_of<VE, STYLE>(g, e, gv);
+        const float2 v = turn_of(at, j, (float)a.positions[(size_t)ld_table(&at.axis[j]) * a.T + t0 + i0 + i], 1.f);
+        s_turn[i * a.D + turn_at<VE>(g, e, gv)] = v.x;
+        s_turn[i * a.D + turn_at<VE>(g, e + VE, gv)] = v.y;
+      }
+      __syncthreads();
+    }
+  };
+  constexpr int kMine = 2 * kHeadsPerCta / kWarps;   // units of a warp, at most
+  uint4 x0[kMine][kPairs], x1[kMine][kPairs];
+  auto load = [&](int m, int cnt) {
+    const int unit = warp + m * kWarps;
+    if (unit >= units) return;
     const int head = head0 + unit % heads;
     const uint8_t* src = (unit < heads ? a.k : a.v) + ((size_t)head * a.D) * sizeof(T) + f * 16;
     const int64_t stride = unit < heads ? a.k_stride : a.v_stride;
 #pragma unroll
     for (int u = 0; u < kPairs; ++u) {
       const int i = lane / gv + u * row_step;
-      x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
+      x0[m][u] = x1[m][u] = make_uint4(0, 0, 0, 0);
       if (i < cnt && s_row[i] >= 0) {
         const uint8_t* r = src + s_from[i] * stride;
-        x0[u] = *reinterpret_cast<const uint4*>(r);
-        x1[u] = *reinterpret_cast<const uint4*>(r + gv * 16);
+        x0[m][u] = *reinterpret_cast<const uint4*>(r);
+        x1[m][u] = *reinterpret_cast<const uint4*>(r + gv * 16);
       }
     }
   };
-  auto values = [&](int unit, int u, float (&x)[VE], float (&z)[VE]) {
-    Vec<T>::unpack(x0[u], x);
-    Vec<T>::unpack(x1[u], z);
+  auto values = [&](int m, int u, float (&x)[VE], float (&z)[VE]) {
+    Vec<T>::unpack(x0[m][u], x);
+    Vec<T>::unpack(x1[m][u], z);
     if constexpr (STYLE >= 0) {
-      if (unit < heads) rotate_pair<T, STYLE>(s_turn + (lane / gv + u * row_step) * half, f, gv, x, z);
+      if (warp + m * kWarps < heads)
+        rotate_pair<T, STYLE>(load_turn<VE>(s_turn + (lane / gv + u * row_step) * a.D, f, gv), x, z);
     }
   };
-  auto largest = [&](int unit, int cnt, float most) {
+  auto largest = [&](int m, int cnt, float most) {
 #pragma unroll
     for (int u = 0; u < kPairs; ++u) {
       const int i = lane / gv + u * row_step;
       if (i < cnt && s_row[i] >= 0) {
         float x[VE], z[VE];
-        values(unit, u, x, z);
+        values(m, u, x, z);
 #pragma unroll
         for (int e = 0; e < VE; ++e) most = larger_finite(larger_finite(most, x[e]), z[e]);
       }
@@ -317,7 +379,8 @@ __global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledW
     if (lane == 0) *at_scale = s;
     return s;
   };
-  auto put = [&](int unit, int cnt, float s) {
+  auto put = [&](int m, int cnt, float s) {
+    const int unit = warp + m * kWarps;
     const float r = 1.f / s;
     uint8_t* codes = codes_of(unit) + f * VE;
 #pragma unroll
@@ -325,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledW
       const int i = lane / gv + u * row_step;
       if (i < cnt && s_row[i] >= 0) {
         float x[VE], z[VE];
-        values(unit, u, x, z);
+        values(m, u, x, z);
         uint8_t* c = codes + s_row[i] * row_bytes;
         store_codes<VE, I8>(c, x, r);
         store_codes<VE, I8>(c + gv * VE, z, r);
@@ -334,38 +397,44 @@ __global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledW
   };
   if (n <= tile_rows) {
     const int cnt = stage(0);
-    if (!any) return;
-    for (int unit = warp; unit < units; unit += kWarps) {
-      load(unit, cnt);
-      const float s = settle(unit, largest(unit, cnt, 0.f));
-      if (s > 0.f) put(unit, cnt, s);
-    }
-    return;
+    if (!any) continue;
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) load(m, cnt);    // under way while the sines are computed
+    stage_turns(0, cnt);
+#pragma unroll
+    for (int m = 0; m < kMine; ++m)
+      if (warp + m * kWarps < units) {
+        const float s = settle(warp + m * kWarps, largest(m, cnt, 0.f));
+        if (s > 0.f) put(m, cnt, s);
+      }
+    continue;
   }
-  constexpr int kMine = 2 * kHeadsPerCta / kWarps;   // units of a warp, at most
   float most[kMine], scale[kMine];
 #pragma unroll
   for (int m = 0; m < kMine; ++m) most[m] = 0.f;
   for (int64_t i0 = 0; i0 < n; i0 += tile_rows) {
     const int cnt = stage(i0);
+    stage_turns(i0, cnt);
 #pragma unroll
     for (int m = 0; m < kMine; ++m)
       if (warp + m * kWarps < units) {
-        load(warp + m * kWarps, cnt);
-        most[m] = largest(warp + m * kWarps, cnt, most[m]);
+        load(m, cnt);
+        most[m] = largest(m, cnt, most[m]);
       }
   }
-  if (!any) return;
+  if (!any) continue;
 #pragma unroll
   for (int m = 0; m < kMine; ++m) scale[m] = warp + m * kWarps < units ? settle(warp + m * kWarps, most[m]) : 0.f;
   for (int64_t i0 = 0; i0 < n; i0 += tile_rows) {
     const int cnt = stage(i0);
+    stage_turns(i0, cnt);
 #pragma unroll
     for (int m = 0; m < kMine; ++m)
       if (scale[m] > 0.f) {
-        load(warp + m * kWarps, cnt);
-        put(warp + m * kWarps, cnt, scale[m]);
+        load(m, cnt);
+        put(m, cnt, scale[m]);
       }
+  }
   }
 }
 
@@ -379,10 +448,9 @@ template <typename T, int STYLE, bool I8>
 __global__ void __launch_bounds__(kReadThreads) scaled_read_kernel(const ScaledReadArgs a, const __grid_constant__ AxisTurns at,
                                                                    int share) {
   constexpr int VE = Vec<T>::N;
-  extern __shared__ float2 s_turn[];             // [warps][D / 2]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = a.D / 2, gv = a.D / VE / 2;
+  extern __shared__ __align__(16) float s_turn[];   // [warps][D]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = a.D / 2, gv = a.D / VE / 2, f = lane % gv;
   const int64_t w = (int64_t)blockIdx.x * (kReadThreads / 32) + warp, t = w / share;
-  float2* turn = s_turn + warp * half;
   pdl_wait();
   pdl_trigger();
   if (t >= a.T) return;
@@ -397,14 +465,11 @@ __global__ void __launch_bounds__(kReadThreads) scaled_read_kernel(const ScaledR
     return;
   }
   const int64_t block = block_of_slot(slot, a.block_size, a.block_shift);
+  Turn<VE> turn;
   if constexpr (STYLE >= 0) {
-    for (int i0 = 0; i0 < half; i0 += 32) {
-      const int i = (i0 + lane) % half;
-      turn[i] = turn_of(at, i, (float)__shfl_sync(0xffffffffu, of_axis, ld_table(&at.axis[i])), -1.f);
-    }
-    __syncwarp();
+    turn = warp_turn<T, STYLE>(at, s_turn + warp * a.D, half, gv, f, of_axis, -1.f);
   }
-  const int f = lane % gv, n = a.H * gv;
+  const int n = a.H * gv;
   const uint8_t* krow = a.k_cache + (size_t)slot * a.H * a.D;
   auto load_codes = [&](const uint8_t* p) {
     if constexpr (VE == 8) return *reinterpret_cast<const uint2*>(p);
@@ -455,7 +520,7 @@ __global__ void __launch_bounds__(kReadThreads) scaled_read_kernel(const ScaledR
         widen(c0[u], s[u], x);
         widen(c1[u], s[u], z);
         if constexpr (STYLE >= 0) {
-          if (kv == 0) rotate_pair<T, STYLE>(turn, f, gv, x, z);
+          if (kv == 0) rotate_pair<T, STYLE>(turn, x, z);
         }
         st_v4(out + (2 * i - f) * 16, Vec<T>::pack(x));
         st_v4(out + (2 * i - f) * 16 + gv * 16, Vec<T>::pack(z));
@@ -469,17 +534,20 @@ cudaError_t launch_write_t(const ScaledWriteArgs& p, const AxisTurns& turns, con
   constexpr int VE = Vec<T>::N;
   const AppendArgs& a = p.a;
   const int splits = (a.H + kHeadsPerCta - 1) / kHeadsPerCta;
-  const int64_t group_ctas = (int64_t)a.T * splits;
+  // One token a CTA up to 16 CTAs an SM, then several: most tokens of a prompt begin no group, and their CTAs, though they
+  // end at once, hold up the others (8000 tokens: 74.6 us with one token a CTA).
+  const int window = (int)std::min<int64_t>(16, (a.T + 16LL * cfg.num_sms - 1) / (16LL * cfg.num_sms));
+  const int64_t group_ctas = ((int64_t)a.T + window - 1) / window * splits;
   // Warps to a token's queries: as many as keep a lane one batch busy while the SMs have room for 32 warps each.
   const int64_t items = (int64_t)a.Hq * (a.D / VE / 2);
   int share = 1;
   while (share < 16 && (int64_t)a.T * share < 32LL * cfg.num_sms && (int64_t)share * 32 < items) share *= 2;
   const int64_t q_ctas = a.Hq > 0 ? ((int64_t)a.T * share + kWarps - 1) / kWarps : 0;
   if (group_ctas + q_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const size_t tile = STYLE >= 0 ? (size_t)kRowsOfTile * VE * sizeof(float2) : 0;   // kRowsOfTile / gv rows of D / 2
+  const size_t tile = STYLE >= 0 ? (size_t)kRowsOfTile * VE * sizeof(float2) : 0;   // kRowsOfTile / gv rows of D floats
   const size_t queries = STYLE >= 0 ? (size_t)kWarps * a.D / 2 * sizeof(float2) : 0;
   return launch_ex(scaled_write_kernel<T, STYLE, I8>, dim3((unsigned)(group_ctas + q_ctas)), dim3(kThreads),
-                   tile > queries ? tile : queries, cfg.stream, cfg.pdl, p, turns, group_ctas, splits, share);
+                   tile > queries ? tile : queries, cfg.stream, cfg.pdl, p, turns, group_ctas, window, splits, share);
 }
 
 template <typename T, bool I8>
