@@ -8,15 +8,17 @@
 // or 448,
 //   s = A / qmax, in [2^-40, 2^40]; beside earlier rows no smaller than their scale;
 //   code = round(y * (1 / s)), and earlier rows' codes round(code * s_old / s) if s grew.
-// A CTA whose token begins a group takes it for up to 8 heads (other CTAs look
-// at two slots and end): it computes the sines of the group's keys once, then
-// each warp takes one head's keys or values.  A warp holds up to 128 pairs of
-// 16-byte vectors, which is a block of 16 rows at head_dim 128 in 16 bits: loaded
-// once, the largest found by shuffles, quantised and stored from registers.
-// Longer groups go through twice, once for the scale and once for the codes.
+// A CTA takes the groups that begin in its tokens, as many at a time as there is
+// room for: their rows are loaded, each head's keys or values by a warp (longer
+// blocks: two), while the sines of the keys are computed once for all heads; the
+// largest element of each group is found by shuffles, and the rows are quantised
+// and stored from registers.  Groups that do not fit go through twice, once for
+// the scale and once for the codes.
 // The queries are rotated by CTAs of their own, a warp or several to a token.
 // Bound by memory; each input is read once and each code written once.
 #include <algorithm>
+#include <cfloat>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -27,9 +29,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeadsPerCta = 8;
-constexpr int kPairs = 4;                        // pairs of vectors a lane holds
-constexpr int kRowsOfTile = 32 * kPairs;         // rows of a warp's tile with one pair a row
 
 __device__ __forceinline__ float ld_table(const float* p) {   // see ld_param in append.cu
   float x;
@@ -61,7 +60,7 @@ __device__ __forceinline__ int pair_of(int f, int e, int gv) {
 }
 template <int VE>
 struct Turn {
-  float cs[VE], sn[VE];
+  unsigned long long cs[VE / 2], sn[VE / 2];   // two pairs' to a register pair: the paired operations round as the single ones
 };
 // A row's sines in shared memory: by pieces of four, cosines then sines, a piece of
 // all lanes after the other, so that eight lanes' 16 bytes lie in different banks.
@@ -74,29 +73,28 @@ __device__ __forceinline__ Turn<VE> load_turn(const float* row, int f, int gv) {
   for (int q = 0; q < VE / 4; ++q) {
     const float4 c = *reinterpret_cast<const float4*>(row + (q * gv + f) * 4);
     const float4 s = *reinterpret_cast<const float4*>(row + ((q + VE / 4) * gv + f) * 4);
-    t.cs[4 * q] = c.x, t.cs[4 * q + 1] = c.y, t.cs[4 * q + 2] = c.z, t.cs[4 * q + 3] = c.w;
-    t.sn[4 * q] = s.x, t.sn[4 * q + 1] = s.y, t.sn[4 * q + 2] = s.z, t.sn[4 * q + 3] = s.w;
+    t.cs[2 * q] = pk2(c.x, c.y), t.cs[2 * q + 1] = pk2(c.z, c.w);
+    t.sn[2 * q] = pk2(s.x, s.y), t.sn[2 * q + 1] = pk2(s.z, s.w);
   }
   return t;
 }
+__device__ __forceinline__ unsigned long long neg2(unsigned long long x) { return x ^ 0x8000000080000000ull; }
 template <typename T, int STYLE>
 __device__ __forceinline__ void rotate_pair(const Turn<Vec<T>::N>& t, float (&x)[Vec<T>::N], float (&z)[Vec<T>::N]) {
   constexpr int VE = Vec<T>::N;
+  auto turn = [](float& a0, float& a1, float& b0, float& b1, unsigned long long cs, unsigned long long sn) {
+    const unsigned long long a = pk2(a0, a1), b = pk2(b0, b1);
+    upk2(fma2_rn(a, cs, mul2_rn(b, neg2(sn))), a0, a1);
+    upk2(fma2_rn(b, cs, mul2_rn(a, sn)), b0, b1);
+  };
   if constexpr (STYLE == 0) {
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const float a = x[e], b = z[e];
-      x[e] = fmaf(a, t.cs[e], -__fmul_rn(b, t.sn[e]));
-      z[e] = fmaf(b, t.cs[e], __fmul_rn(a, t.sn[e]));
-    }
+    for (int e = 0; e < VE / 2; ++e) turn(x[2 * e], x[2 * e + 1], z[2 * e], z[2 * e + 1], t.cs[e], t.sn[e]);
   } else {
 #pragma unroll
-    for (int e = 0; e < VE / 2; ++e) {
-      const float a = x[2 * e], b = x[2 * e + 1], c = z[2 * e], d = z[2 * e + 1];
-      x[2 * e] = fmaf(a, t.cs[e], -__fmul_rn(b, t.sn[e]));
-      x[2 * e + 1] = fmaf(b, t.cs[e], __fmul_rn(a, t.sn[e]));
-      z[2 * e] = fmaf(c, t.cs[VE / 2 + e], -__fmul_rn(d, t.sn[VE / 2 + e]));
-      z[2 * e + 1] = fmaf(d, t.cs[VE / 2 + e], __fmul_rn(c, t.sn[VE / 2 + e]));
+    for (int e = 0; e < VE / 4; ++e) {           // pairs 2 e and 2 e + 1 of each vector
+      turn(x[4 * e], x[4 * e + 2], x[4 * e + 1], x[4 * e + 3], t.cs[e], t.sn[e]);
+      turn(z[4 * e], z[4 * e + 2], z[4 * e + 1], z[4 * e + 3], t.cs[VE / 4 + e], t.sn[VE / 4 + e]);
     }
   }
 }
@@ -115,18 +113,57 @@ __device__ __forceinline__ Turn<Vec<T>::N> warp_turn(const AxisTurns& at, float*
   return load_turn<VE>(row, f, gv);
 }
 
+// The magnitudes of a vector's elements as whole numbers, which order as they do
+// and put what is not finite on top: the largest so far.
+template <typename T>
+__device__ __forceinline__ uint32_t larger_bits(uint32_t most, const uint4& v) {
+  if constexpr (sizeof(T) == 4)
+    return max(max(max(most, v.x & 0x7fffffffu), max(v.y & 0x7fffffffu, v.z & 0x7fffffffu)), v.w & 0x7fffffffu);
+  else
+    return __vimax3_s16x2(__vimax3_s16x2(most, v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(T) == 4) return max(a, b);
+  else return __vmaxs2(a, b);
+}
+// The magnitude itself; inf or NaN if one of the elements was.
+template <typename T>
+__device__ __forceinline__ float magnitude(uint32_t most) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(most);
+  const uint32_t m = max(most & 0xffffu, most >> 16);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(m << 16);
+  else return __half2float(__ushort_as_half((unsigned short)m));
+}
+
 __device__ __forceinline__ float larger_finite(float most, float x) {
   const float a = fabsf(x);
   return a < INFINITY ? fmaxf(most, a) : most;   // false for NaN
 }
 
-// N codes (4 or 8) of a vector.
+// Four INT8 codes of finite elements whose codes are known to be in range: added
+// to 1.5 * 2^23 a product is rounded to a whole number, whose low byte is the code.
+__device__ __forceinline__ uint32_t int8x4_in_range(const float* y, unsigned long long r2) {
+  const unsigned long long magic = pk2(12582912.f, 12582912.f);
+  float a, b, c, d;
+  upk2(fma2_rn(pk2(y[0], y[1]), r2, magic), a, b);
+  upk2(fma2_rn(pk2(y[2], y[3]), r2, magic), c, d);
+  return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040),
+                     __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
+}
+// N codes (4 or 8) of a vector.  odd: its row has elements that are not finite, or past the largest scale's range.
 template <int N, bool I8>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float (&y)[N], float r) {
-  float w[8];
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&y)[N], float r, bool odd) {
+  uint2 c;
+  if (I8 && !odd) {
+    const unsigned long long r2 = pk2(r, r);
+    c = make_uint2(int8x4_in_range(y, r2), N == 8 ? int8x4_in_range(y + N - 4, r2) : 0u);
+  } else {
+    float w[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = e < N ? y[e % N] : 0.f;
-  const uint2 c = I8 ? to_int8x8(w, r) : to_e4m3x8(w, r);
+    for (int e = 0; e < 8; ++e) w[e] = e < N ? y[e % N] : 0.f;
+    c = I8 ? to_int8x8(w, r) : to_e4m3x8(w, r);
+  }
   if constexpr (N == 8) st_v2(p, c);
   else *reinterpret_cast<uint32_t*>(p) = c.x;
 }
@@ -198,243 +235,334 @@ __device__ void rotate_queries(const AppendArgs& a, const AxisTurns& at, float* 
   }
 }
 
+// A group of a CTA's round.
+struct Group {
+  int64_t block, t0, n;
+  int32_t row0;          // of its first token among the round's rows
+  int32_t low;           // the lowest of its rows in the block: below it the block is held already
+  int32_t live;          // some token is not skipped
+};
+constexpr int kWindow = 16;              // tokens of a CTA, and groups of a round, at most
+constexpr int kMaxRows = 128;            // of a round
+constexpr int kDataBytes = 65536;        // of a round's rows: keys and values of the CTA's heads
+constexpr int kMaxUnits = 16;            // a head's keys, or its values
+
+// Rows of a round of a CTA with `heads_of` heads.
+__host__ __device__ inline int rows_of_round(int heads_of, int D, int bytes) {
+  const int n = kDataBytes / (2 * heads_of * D * bytes);
+  return n < kMaxRows ? n : kMaxRows;
+}
+
 // STYLE -1: no rotation (a move).
 template <typename T, int STYLE, bool I8>
 __global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledWriteArgs p, const __grid_constant__ AxisTurns at,
-                                                                  int64_t group_ctas, int window, int splits, int share) {
+                                                                  int64_t group_ctas, int window, int heads_of, int share) {
   constexpr int VE = Vec<T>::N;
   const AppendArgs& a = p.a;
-  extern __shared__ __align__(16) float s_turn[];   // the group's tile [rows][D], or a query warp's [D] each
-  __shared__ int32_t s_row[kRowsOfTile];         // row of the block; -1: the token is skipped
-  __shared__ int64_t s_from[kRowsOfTile];
-  __shared__ uint32_t s_leaders;
-  __shared__ struct { int64_t block, n; int32_t low; } s_group;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int32_t s_row[kMaxRows];            // row of the block; -1: the token is skipped
+  __shared__ int64_t s_from[kMaxRows];
+  __shared__ uint8_t s_of[kMaxRows];             // group
+  __shared__ Group s_group[kWindow];
+  __shared__ float s_scale[kWindow * kMaxUnits], s_ratio[kWindow * kMaxUnits];   // 0: no scale; 0: it did not grow
+  __shared__ int32_t s_groups;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = a.D / 2;
   pdl_wait();
   pdl_trigger();
   if ((int64_t)blockIdx.x >= group_ctas) {
     if constexpr (STYLE >= 0) {
-      rotate_queries<T, STYLE>(a, at, s_turn + warp * a.D, ((int64_t)blockIdx.x - group_ctas) * kWarps + warp, share);
+      rotate_queries<T, STYLE>(a, at, reinterpret_cast<float*>(smem) + warp * a.D,
+                               ((int64_t)blockIdx.x - group_ctas) * kWarps + warp, share);
     }
     return;
   }
+  const int splits = (a.H + heads_of - 1) / heads_of;
   const int64_t begin = blockIdx.x / splits * (int64_t)window;
-  const int head0 = (int)(blockIdx.x % splits) * kHeadsPerCta, heads = min(kHeadsPerCta, a.H - head0);
+  const int head0 = (int)(blockIdx.x % splits) * heads_of, heads = min(heads_of, a.H - head0), units = 2 * heads;
+  const int gv = a.D / VE / 2, f = tid % gv, cap = rows_of_round(heads_of, a.D, (int)sizeof(T));
+  const int head_bytes = a.D * (int)sizeof(T), part_bytes = heads * head_bytes;   // of a row's keys, or values
+  const size_t row_bytes = (size_t)a.H * a.D;    // of the cache
+  float* s_turn = reinterpret_cast<float*>(smem + (size_t)2 * cap * heads_of * head_bytes);   // [rows][D]
+  float* s_most = s_turn + (STYLE >= 0 ? cap * a.D : 0);                                       // [units][rows]
   auto block_at = [&](int64_t t) -> int64_t {
     if (t < 0 || t >= a.T) return -1;
     const int64_t slot = a.slots[t];
     return slot < 0 || slot >= a.n_slots ? -1 : block_of_slot(slot, p.block_size, p.block_shift);
   };
-  // The groups that begin in this CTA's tokens begin .. begin + window - 1 (window <= 16): lane i looks at token begin - 1 + i.
-  // One warp looks, so that the CTA agrees on its groups whatever happens to the caller's slots meanwhile.
+
+  // The groups that begin in this CTA's tokens begin .. begin + window - 1: lane i of the first warp looks at token begin -
+  // 1 + i and hands them on, so that the CTA agrees on them whatever happens to the caller's slots meanwhile.
   int64_t mine = -1;
+  int32_t mine_row = 0;
+  uint32_t leaders = 0, ends = 0;
   if (warp == 0) {
-    mine = block_at(begin - 1 + lane);
+    const int64_t t = begin - 1 + lane;
+    mine = block_at(t);
+    if (mine >= 0) mine_row = (int32_t)max(a.slots[t] - mine * p.block_size, (int64_t)0);
     const int64_t before = __shfl_up_sync(0xffffffffu, mine, 1);
-    const bool ours = lane >= 1 && lane <= window && begin - 1 + lane < a.T;
-    const uint32_t found = __ballot_sync(0xffffffffu, ours && mine >= 0 && mine != before);
-    if (head0 == 0 && ours && mine < 0 && a.slots[begin - 1 + lane] != -1) latch(a.status, IS_ST_BLOCK_ID);
-    if (lane == 0) s_leaders = found;
+    const bool ours = lane >= 1 && lane <= window && t < a.T;
+    leaders = __ballot_sync(0xffffffffu, ours && mine >= 0 && mine != before);
+    ends = __ballot_sync(0xffffffffu, lane >= 1 && mine != before);
+    if (head0 == 0 && ours && mine < 0 && a.slots[t] != -1) latch(a.status, IS_ST_BLOCK_ID);
   }
-  __syncthreads();
-  for (uint32_t leaders = s_leaders; leaders; leaders &= leaders - 1) {
-  const int first = __ffs(leaders) - 1;
-  const int64_t t0 = begin - 1 + first;
-  if (warp == 0) {
-    const int64_t block = __shfl_sync(0xffffffffu, mine, first);
-    int64_t n = 0;                               // its tokens, 31 at a time
-    int32_t low = p.block_size;                  // the lowest of their rows: below it the block is held already
-    for (uint32_t more = ~0u; n % 31 == 0 && more != 0;) {
-      const int64_t t = t0 + n + lane;
-      const bool in = lane < 31 && block_at(t) == block;
-      if (in) low = min(low, (int32_t)max(a.slots[t] - block * p.block_size, (int64_t)0));
-      more = __ballot_sync(0xffffffffu, in);
-      n += __ffs(~more) - 1;             // bit 31 is 0
-    }
-    low = __reduce_min_sync(0xffffffffu, low);
-    if (lane == 0) {
-      s_group.block = block;
-      s_group.n = max(n, (int64_t)1);
-      s_group.low = low;
-    }
-  }
-  __syncthreads();
-  const int64_t block = s_group.block, n = s_group.n;
-  const int32_t low = s_group.low;
-  const int gv = a.D / VE / 2, f = lane % gv, tile_rows = kRowsOfTile / gv, row_step = 32 / gv;
-  const int units = 2 * heads;                   // keys of each head, then values
-  // Tokens t0 + i0 .. of the group: their rows and sources, and their keys' sines.
-  bool any = false;                              // some token is not skipped
-  auto stage = [&](int64_t i0) {
-    const int cnt = (int)min((int64_t)tile_rows, n - i0);
-    bool put = false;
-    __syncthreads();
-    for (int i = tid; i < cnt; i += kThreads) {
-      const int64_t t = t0 + i0 + i;
-      const int64_t in_block = a.slots[t] - block * p.block_size;
-      int32_t row = in_block >= 0 && in_block < p.block_size ? (int32_t)in_block : -1;
-      int64_t from = t;
-      if (p.from) {
-        from = p.from[t];
-        if (from < 0 || from >= p.n_from) {
-          if (from != -1) latch(a.status, IS_ST_BLOCK_ID);
-          row = -1;
+  while (true) {
+    if (warp == 0) {                             // as many groups as have room
+      int64_t total = 0;
+      int ng = 0;
+      while (leaders && total < cap) {
+        const int first = __ffs(leaders) - 1;
+        const int64_t block = __shfl_sync(0xffffffffu, mine, first);
+        const uint32_t after = ends & ~((2u << first) - 1u);
+        const int last = after ? __ffs(after) - 1 : 32;   // lane behind its last
+        int64_t n = last - first;
+        int32_t low = lane >= first && lane < last ? mine_row : p.block_size;
+        for (bool more = last == 32; more;) {    // on past this warp's tokens, 32 at a time
+          const int64_t t = begin - 1 + first + n + lane;
+          const bool in = block_at(t) == block;
+          const uint32_t got = __ballot_sync(0xffffffffu, in);
+          const int count = got == ~0u ? 32 : __ffs(~got) - 1;
+          if (lane < count) low = min(low, (int32_t)max(a.slots[t] - block * p.block_size, (int64_t)0));
+          n += count;
+          more = count == 32;
         }
+        if (ng > 0 && total + n > cap) break;
+        low = __reduce_min_sync(0xffffffffu, low);
+        if (lane == 0) s_group[ng] = {block, begin - 1 + first, n, (int32_t)total, low, 0};
+        ++ng;
+        total += n;
+        leaders &= leaders - 1;
       }
-      if constexpr (STYLE >= 0) {
-        for (int x = 0; x < a.n_axes; ++x) {
-          const int32_t pos = a.positions[(size_t)x * a.T + t];
-          if (pos < 0 || pos >= IS_MAX_POSITION) {
-            latch(a.status, IS_ST_POSITION);
+      if (lane == 0) s_groups = ng;
+    }
+    __syncthreads();
+    const int ng = s_groups;
+    if (ng == 0) return;
+    const int64_t total = s_group[ng - 1].row0 + s_group[ng - 1].n;   // past cap: one long group, which goes through twice
+
+    // Rows i0 .. i0 + cnt - 1 of the round: their places, their elements and their keys' sines.
+    auto stage = [&](int64_t i0, int cnt) {
+      for (int i = tid; i < cnt; i += kThreads) {
+        int g = ng - 1;
+        while (g > 0 && s_group[g].row0 > i) --g;
+        const int64_t t = s_group[g].t0 + (i0 + i - s_group[g].row0);
+        const int64_t in_block = a.slots[t] - s_group[g].block * p.block_size;
+        int32_t row = in_block >= 0 && in_block < p.block_size ? (int32_t)in_block : -1;
+        int64_t from = t;
+        if (p.from) {
+          from = p.from[t];
+          if (from < 0 || from >= p.n_from) {
+            if (from != -1) latch(a.status, IS_ST_BLOCK_ID);
             row = -1;
           }
         }
-      }
-      s_row[i] = row;
-      s_from[i] = from;
-      put |= row >= 0;
-    }
-    any |= __syncthreads_or(put) != 0;
-    return cnt;
-  };
-  auto stage_turns = [&](int64_t i0, int cnt) {
-    if constexpr (STYLE >= 0) {
-      for (int x = tid; x < cnt * half; x += kThreads) {
-        const int i = x / half, g = (x - i * half) / VE, e = x % VE, j = pair_of<VE, STYLE>(g, e, gv);
-        const float2 v = turn_of(at, j, (float)a.positions[(size_t)ld_table(&at.axis[j]) * a.T + t0 + i0 + i], 1.f);
-        s_turn[i * a.D + turn_at<VE>(g, e, gv)] = v.x;
-        s_turn[i * a.D + turn_at<VE>(g, e + VE, gv)] = v.y;
+        if constexpr (STYLE >= 0) {
+          for (int x = 0; x < a.n_axes; ++x) {
+            const int32_t pos = a.positions[(size_t)x * a.T + t];
+            if (pos < 0 || pos >= IS_MAX_POSITION) {
+              latch(a.status, IS_ST_POSITION);
+              row = -1;
+            }
+          }
+        }
+        s_row[i] = row;
+        s_from[i] = from;
+        s_of[i] = (uint8_t)g;
+        if (row >= 0) s_group[g].live = 1;
       }
       __syncthreads();
-    }
-  };
-  constexpr int kMine = 2 * kHeadsPerCta / kWarps;   // units of a warp, at most
-  uint4 x0[kMine][kPairs], x1[kMine][kPairs];
-  auto load = [&](int m, int cnt) {
-    const int unit = warp + m * kWarps;
-    if (unit >= units) return;
-    const int head = head0 + unit % heads;
-    const uint8_t* src = (unit < heads ? a.k : a.v) + ((size_t)head * a.D) * sizeof(T) + f * 16;
-    const int64_t stride = unit < heads ? a.k_stride : a.v_stride;
-#pragma unroll
-    for (int u = 0; u < kPairs; ++u) {
-      const int i = lane / gv + u * row_step;
-      x0[m][u] = x1[m][u] = make_uint4(0, 0, 0, 0);
-      if (i < cnt && s_row[i] >= 0) {
-        const uint8_t* r = src + s_from[i] * stride;
-        x0[m][u] = *reinterpret_cast<const uint4*>(r);
-        x1[m][u] = *reinterpret_cast<const uint4*>(r + gv * 16);
+      for (int x = warp; x < 2 * cnt; x += kWarps) {
+        const int i = x < cnt ? x : x - cnt;
+        if (s_row[i] < 0) continue;
+        const uint8_t* src = (x < cnt ? a.k + s_from[i] * a.k_stride : a.v + s_from[i] * a.v_stride) + (size_t)head0 * head_bytes;
+        const uint32_t dst = smem_addr(smem) + (uint32_t)x * part_bytes;
+        for (int c = lane * 16; c < part_bytes; c += 512) cp_async16(dst + c, src + c, true);
       }
-    }
-  };
-  auto values = [&](int m, int u, float (&x)[VE], float (&z)[VE]) {
-    Vec<T>::unpack(x0[m][u], x);
-    Vec<T>::unpack(x1[m][u], z);
-    if constexpr (STYLE >= 0) {
-      if (warp + m * kWarps < heads)
-        rotate_pair<T, STYLE>(load_turn<VE>(s_turn + (lane / gv + u * row_step) * a.D, f, gv), x, z);
-    }
-  };
-  auto largest = [&](int m, int cnt, float most) {
-#pragma unroll
-    for (int u = 0; u < kPairs; ++u) {
-      const int i = lane / gv + u * row_step;
-      if (i < cnt && s_row[i] >= 0) {
-        float x[VE], z[VE];
-        values(m, u, x, z);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) most = larger_finite(larger_finite(most, x[e]), z[e]);
-      }
-    }
-    return most;
-  };
-  auto codes_of = [&](int unit) {                // row 0 of the block, this head
-    return a.k_cache + (unit < heads ? 0 : a.v_offset) + ((size_t)block * p.block_size * a.H + head0 + unit % heads) * a.D;
-  };
-  const size_t row_bytes = (size_t)a.H * a.D;
-  // The block's scale, and what it holds already rounded anew; 0: the block's scale is none.
-  auto settle = [&](int unit, float most) -> float {
-    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-    float* at_scale = p.scales + (unit < heads ? 0 : p.v_scales) + block * a.H + head0 + unit % heads;
-    float s = fminf(fmaxf(most / (I8 ? 127.f : 448.f), kSmallestScale), kLargestScale);
-    if (low > 0) {
-      const float old = *at_scale;
-      if (!scale_ok(old)) {
-        if (lane == 0) latch(a.status, IS_ST_SCALE);
-        return 0.f;
-      }
-      if (s > old) {
-        const float ratio = old / s;
-        uint8_t* codes = codes_of(unit);
-        const int chunks = a.D / 16;
-        for (int64_t x = lane; x < (int64_t)low * chunks; x += 32) {
-          uint4* c = reinterpret_cast<uint4*>(codes + x / chunks * row_bytes + x % chunks * 16);
-          *c = again<I8>(*c, ratio);
+      cp_async_commit();
+      if constexpr (STYLE >= 0) {                // s_from is the token
+        for (int x = tid; x < cnt * half; x += kThreads) {
+          const int i = x / half, g = (x - i * half) / VE, e = x % VE, j = pair_of<VE, STYLE>(g, e, gv);
+          const float2 v = turn_of(at, j, (float)a.positions[(size_t)ld_table(&at.axis[j]) * a.T + s_from[i]], 1.f);
+          s_turn[i * a.D + turn_at<VE>(g, e, gv)] = v.x;
+          s_turn[i * a.D + turn_at<VE>(g, e + VE, gv)] = v.y;
         }
-      } else {
-        s = old;
+      }
+      cp_async_wait<0>();
+      __syncthreads();
+    };
+    // A warp takes a unit, gv lanes a row of it: vectors f and f + gv of the head.
+    const int step = 32 / gv;
+    auto unit_rows = [&](int unit, int cnt) {
+      return smem + (size_t)(unit < heads ? 0 : cnt) * part_bytes + (unit < heads ? unit : unit - heads) * head_bytes + f * 16;
+    };
+    auto values = [&](bool key, int i, const uint4& x0, const uint4& z0, float (&x)[VE], float (&z)[VE]) {
+      Vec<T>::unpack(x0, x);
+      Vec<T>::unpack(z0, z);
+      if constexpr (STYLE >= 0) {
+        if (key) rotate_pair<T, STYLE>(load_turn<VE>(s_turn + i * a.D, f, gv), x, z);
+      }
+    };
+    auto signed_most = [](float most, bool odd) { return odd ? -most - FLT_MIN : most; };
+    // The largest finite magnitude of a unit's rows of one group, or of each of its rows; negative if some element is not
+    // finite.
+    auto find_most = [&](int cnt, bool by_row) {
+      for (int unit = warp; unit < units; unit += kWarps) {
+        const uint8_t* rows = unit_rows(unit, cnt);
+        const bool key = unit < heads;
+        float most = 0.f;
+        uint32_t bits = 0;
+        bool odd = false;
+        auto slow = [&](int i, const uint4& x0, const uint4& z0) {
+          float x[VE], z[VE];
+          values(key, i, x0, z0, x, z);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) most = larger_finite(larger_finite(most, x[e]), z[e]);
+        };
+        for (int i0 = 0; i0 < cnt; i0 += step) {
+          const int i = i0 + lane / gv;
+          if (i < cnt && s_row[i] >= 0) {
+            const uint4 x0 = *reinterpret_cast<const uint4*>(rows + (size_t)i * part_bytes);
+            const uint4 z0 = *reinterpret_cast<const uint4*>(rows + (size_t)i * part_bytes + gv * 16);
+            const uint32_t mine = larger_bits<T>(larger_bits<T>(0u, x0), z0);
+            if (!(magnitude<T>(mine) < INFINITY)) {
+              odd = true;
+              slow(i, x0, z0);
+            } else if (STYLE >= 0 && key) {
+              float x[VE], z[VE], top = 0.f;
+              values(true, i, x0, z0, x, z);
+#pragma unroll
+              for (int e = 0; e < VE; ++e) top = fmaxf(fmaxf(top, fabsf(x[e])), fabsf(z[e]));
+              if (top == INFINITY) {
+                odd = true;
+                slow(i, x0, z0);
+              } else {
+                most = fmaxf(most, top);
+              }
+            } else {
+              bits = max_bits<T>(bits, mine);
+            }
+          }
+          if (by_row) {
+            most = fmaxf(most, magnitude<T>(bits));
+            for (int d = 1; d < gv; d <<= 1) {
+              most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+              odd |= __shfl_xor_sync(0xffffffffu, (int)odd, d) != 0;
+            }
+            if (f == 0 && i < cnt) s_most[unit * cap + i] = signed_most(most, odd);
+            most = 0.f;
+            bits = 0;
+            odd = false;
+          }
+        }
+        if (!by_row) {
+          most = fmaxf(most, magnitude<T>(bits));
+          most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+          odd = __any_sync(0xffffffffu, odd);
+          if (lane == 0) s_most[unit * cap] = signed_most(most, odd);
+        }
+      }
+      __syncthreads();
+    };
+    auto store = [&](int cnt) {
+      for (int unit = warp; unit < units; unit += kWarps) {
+        const uint8_t* rows = unit_rows(unit, cnt);
+        const bool key = unit < heads;
+        uint8_t* to = a.k_cache + (key ? 0 : a.v_offset) + (size_t)(head0 + (key ? unit : unit - heads)) * a.D + f * VE;
+        int group = -1;
+        bool odd = false;
+        float r = 0.f;
+        uint8_t* block = nullptr;
+        for (int i = lane / gv; i < cnt; i += step) {
+          const int row = s_row[i], g = s_of[i];
+          if (row < 0) continue;
+          if (g != group) {
+            const float s = s_scale[g * kMaxUnits + unit];
+            group = g;
+            r = s == 0.f ? 0.f : 1.f / fabsf(s);
+            odd = s < 0.f;
+            block = to + (size_t)s_group[g].block * p.block_size * row_bytes;
+          }
+          if (r == 0.f) continue;
+          const uint4 x0 = *reinterpret_cast<const uint4*>(rows + (size_t)i * part_bytes);
+          const uint4 z0 = *reinterpret_cast<const uint4*>(rows + (size_t)i * part_bytes + gv * 16);
+          float x[VE], z[VE];
+          values(key, i, x0, z0, x, z);
+          uint8_t* c = block + row * row_bytes;
+          store_codes<VE, I8>(c, x, r, odd);
+          store_codes<VE, I8>(c + gv * VE, z, r, odd);
+        }
+      }
+    };
+    // Thread x settles unit x % kMaxUnits of group x / kMaxUnits: its block's scale there.
+    static_assert(kWindow * kMaxUnits == kThreads, "a thread to each");
+    const int my_group = tid / kMaxUnits, my_unit = tid % kMaxUnits;
+    const bool settles = my_group < ng && my_unit < units;
+    const int64_t my_scale = settles ? (my_unit < heads ? 0 : p.v_scales) + s_group[my_group].block * a.H + head0 +
+                                           (my_unit < heads ? my_unit : my_unit - heads) : 0;
+    const float old = settles ? p.scales[my_scale] : 0.f;
+    float most = 0.f;
+    bool odd = false;
+    auto gather = [&](bool by_row) {
+      if (!settles) return;
+      const int first = by_row ? s_group[my_group].row0 : 0, n = by_row ? (int)s_group[my_group].n : 1;
+      for (int i = first; i < first + n; ++i) {
+        const float x = s_most[my_unit * cap + i];
+        most = fmaxf(most, fabsf(x));
+        odd |= x < 0.f;
+      }
+    };
+    auto settle = [&] {
+      float s = 0.f, ratio = 0.f;
+      if (settles && s_group[my_group].live) {
+        s = fminf(fmaxf(most / (I8 ? 127.f : 448.f), kSmallestScale), kLargestScale);
+        if (s_group[my_group].low > 0) {
+          if (!scale_ok(old)) {
+            latch(a.status, IS_ST_SCALE);
+            s = 0.f;
+          } else if (s > old) {
+            ratio = old / s;
+          } else {
+            s = old;
+          }
+        }
+        if (s > 0.f) p.scales[my_scale] = s;
+      }
+      s_scale[tid] = odd || s == kLargestScale ? -s : s;   // negative: elements past the codes' range, or none of it
+      s_ratio[tid] = ratio;
+      __syncthreads();
+      for (int x = warp; x < ng * kMaxUnits; x += kWarps) {   // what blocks held already, rounded anew
+        const float r = s_ratio[x];
+        if (r == 0.f) continue;
+        const int g = x / kMaxUnits, unit = x % kMaxUnits, chunks = a.D / 16;
+        uint8_t* codes = a.k_cache + (unit < heads ? 0 : a.v_offset) + (size_t)s_group[g].block * p.block_size * row_bytes +
+                         (size_t)(head0 + (unit < heads ? unit : unit - heads)) * a.D;
+        for (int64_t y = lane; y < (int64_t)s_group[g].low * chunks; y += 32) {
+          uint4* c = reinterpret_cast<uint4*>(codes + y / chunks * row_bytes + y % chunks * 16);
+          *c = again<I8>(*c, r);
+        }
+      }
+    };
+    if (total <= cap) {
+      stage(0, (int)total);
+      find_most((int)total, ng > 1);
+      gather(ng > 1);
+      settle();
+      store((int)total);
+    } else {
+      auto rows_from = [&](int64_t i0) { return (int)min((int64_t)cap, total - i0); };
+      for (int64_t i0 = 0; i0 < total; i0 += cap) {
+        stage(i0, rows_from(i0));
+        find_most(rows_from(i0), false);
+        gather(false);
+        __syncthreads();                         // before the next rows are staged
+      }
+      settle();
+      for (int64_t i0 = 0; i0 < total; i0 += cap) {
+        stage(i0, rows_from(i0));
+        store(rows_from(i0));
+        __syncthreads();
       }
     }
-    __syncwarp();
-    if (lane == 0) *at_scale = s;
-    return s;
-  };
-  auto put = [&](int m, int cnt, float s) {
-    const int unit = warp + m * kWarps;
-    const float r = 1.f / s;
-    uint8_t* codes = codes_of(unit) + f * VE;
-#pragma unroll
-    for (int u = 0; u < kPairs; ++u) {
-      const int i = lane / gv + u * row_step;
-      if (i < cnt && s_row[i] >= 0) {
-        float x[VE], z[VE];
-        values(m, u, x, z);
-        uint8_t* c = codes + s_row[i] * row_bytes;
-        store_codes<VE, I8>(c, x, r);
-        store_codes<VE, I8>(c + gv * VE, z, r);
-      }
-    }
-  };
-  if (n <= tile_rows) {
-    const int cnt = stage(0);
-    if (!any) continue;
-#pragma unroll
-    for (int m = 0; m < kMine; ++m) load(m, cnt);    // under way while the sines are computed
-    stage_turns(0, cnt);
-#pragma unroll
-    for (int m = 0; m < kMine; ++m)
-      if (warp + m * kWarps < units) {
-        const float s = settle(warp + m * kWarps, largest(m, cnt, 0.f));
-        if (s > 0.f) put(m, cnt, s);
-      }
-    continue;
-  }
-  float most[kMine], scale[kMine];
-#pragma unroll
-  for (int m = 0; m < kMine; ++m) most[m] = 0.f;
-  for (int64_t i0 = 0; i0 < n; i0 += tile_rows) {
-    const int cnt = stage(i0);
-    stage_turns(i0, cnt);
-#pragma unroll
-    for (int m = 0; m < kMine; ++m)
-      if (warp + m * kWarps < units) {
-        load(m, cnt);
-        most[m] = largest(m, cnt, most[m]);
-      }
-  }
-  if (!any) continue;
-#pragma unroll
-  for (int m = 0; m < kMine; ++m) scale[m] = warp + m * kWarps < units ? settle(warp + m * kWarps, most[m]) : 0.f;
-  for (int64_t i0 = 0; i0 < n; i0 += tile_rows) {
-    const int cnt = stage(i0);
-    stage_turns(i0, cnt);
-#pragma unroll
-    for (int m = 0; m < kMine; ++m)
-      if (scale[m] > 0.f) {
-        load(m, cnt);
-        put(m, cnt, scale[m]);
-      }
-  }
+    __syncthreads();                             // the round's rows and groups have been read
   }
 }
 
@@ -533,10 +661,13 @@ template <typename T, int STYLE, bool I8>
 cudaError_t launch_write_t(const ScaledWriteArgs& p, const AxisTurns& turns, const LaunchCfg& cfg) {
   constexpr int VE = Vec<T>::N;
   const AppendArgs& a = p.a;
-  const int splits = (a.H + kHeadsPerCta - 1) / kHeadsPerCta;
-  // One token a CTA up to 16 CTAs an SM, then several: most tokens of a prompt begin no group, and their CTAs, though they
-  // end at once, hold up the others (8000 tokens: 74.6 us with one token a CTA).
-  const int window = (int)std::min<int64_t>(16, (a.T + 16LL * cfg.num_sms - 1) / (16LL * cfg.num_sms));
+  // Heads of a CTA: 8, fewer where a block's rows would not fit a round otherwise.
+  int heads_of = kMaxUnits / 2;
+  while (heads_of > 2 && rows_of_round(heads_of, a.D, (int)sizeof(T)) < std::min(p.block_size, kMaxRows)) heads_of /= 2;
+  const int splits = (a.H + heads_of - 1) / heads_of;
+  // Tokens of a CTA: one while every SM gets one, then up to 16.  Most tokens of a prompt begin no group, and CTAs that end
+  // at once still hold up the others (8000 tokens with one a CTA: 74.6 us).
+  const int window = (int)std::min<int64_t>(kWindow, std::max<int64_t>(1, a.T / cfg.num_sms));
   const int64_t group_ctas = ((int64_t)a.T + window - 1) / window * splits;
   // Warps to a token's queries: as many as keep a lane one batch busy while the SMs have room for 32 warps each.
   const int64_t items = (int64_t)a.Hq * (a.D / VE / 2);
@@ -544,10 +675,13 @@ cudaError_t launch_write_t(const ScaledWriteArgs& p, const AxisTurns& turns, con
   while (share < 16 && (int64_t)a.T * share < 32LL * cfg.num_sms && (int64_t)share * 32 < items) share *= 2;
   const int64_t q_ctas = a.Hq > 0 ? ((int64_t)a.T * share + kWarps - 1) / kWarps : 0;
   if (group_ctas + q_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const size_t tile = STYLE >= 0 ? (size_t)kRowsOfTile * VE * sizeof(float2) : 0;   // kRowsOfTile / gv rows of D floats
-  const size_t queries = STYLE >= 0 ? (size_t)kWarps * a.D / 2 * sizeof(float2) : 0;
+  const size_t rows = rows_of_round(heads_of, a.D, (int)sizeof(T));
+  const size_t smem = rows * (2 * heads_of * (a.D * sizeof(T) + sizeof(float)) + (STYLE >= 0 ? a.D * sizeof(float) : 0));
+  const size_t queries = STYLE >= 0 ? (size_t)kWarps * a.D * sizeof(float) : 0;
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(&scaled_write_kernel<T, STYLE, I8>), std::max(smem, queries));
+  if (e != cudaSuccess) return e;
   return launch_ex(scaled_write_kernel<T, STYLE, I8>, dim3((unsigned)(group_ctas + q_ctas)), dim3(kThreads),
-                   tile > queries ? tile : queries, cfg.stream, cfg.pdl, p, turns, group_ctas, window, splits, share);
+                   std::max(smem, queries), cfg.stream, cfg.pdl, p, turns, group_ctas, window, heads_of, share);
 }
 
 template <typename T, bool I8>

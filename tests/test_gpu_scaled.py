@@ -753,3 +753,16 @@ def test_waits_that_run_out(dtype, cache, D, bs):
         out, bits = call()
         assert bits == 0 and torch.equal(out, want)
     assert seen == _lib.IS_ST_TIMEOUT
+
+
+# ---------------------------------------------------------------- many short groups in a call
+
+@pytest.mark.parametrize("cache,D,bs", [("int8", 64, 16), ("e4m3", 128, 16), ("int8", 128, 32), ("int8", 128, 64), ("e4m3", 256, 8)])
+def test_append_many_requests(cache, D, bs):
+    """Hundreds of requests with one to a few new tokens each, so that a CTA has many groups, some in new blocks and some
+    that raise a block's scale, with padding between requests."""
+    reqs = [(1 + (37 * i) % 90, 1 + (i % 7 == 0) * (i % 5)) for i in range(700)]
+    reqs = [(n, min(n, m)) for n, m in reqs]
+    at = np.cumsum([0] + [m for _, m in reqs])
+    skip = [int(at[r]) for r in range(0, 700, 53) if reqs[r][1] == 1]       # a block's tokens stay adjacent
+    append_case(reqs, 4, 3, D, "bf16", cache, bs=bs, skip=skip)
