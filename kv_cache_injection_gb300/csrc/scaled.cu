@@ -27,7 +27,9 @@ namespace isk {
 
 namespace {
 
-constexpr int kThreads = 256;
+// 128 threads and 32 KB of rows, five CTAs an SM: the steps of a CTA wait for one another, other CTAs fill the gaps (46,000
+// moved tokens 84 us, 101 with 256 threads and 64 KB, 116 with 64 and 16).
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ float ld_table(const float* p) {   // see ld_param in append.cu
@@ -242,10 +244,11 @@ struct Group {
   int32_t low;           // the lowest of its rows in the block: below it the block is held already
   int32_t live;          // some token is not skipped
 };
-constexpr int kWindow = 16;              // tokens of a CTA, and groups of a round, at most
+constexpr int kWindow = 30;              // tokens of a CTA, at most (a warp looks at them and a neighbour)
+constexpr int kMaxGroups = 16;           // of a round
 constexpr int kMaxRows = 128;            // of a round
-constexpr int kDataBytes = 65536;        // of a round's rows: keys and values of the CTA's heads
-constexpr int kMaxUnits = 16;            // a head's keys, or its values
+constexpr int kDataBytes = 32768;        // of a round's rows: keys and values of the CTA's heads
+constexpr int kMaxUnits = 8;             // a head's keys, or its values
 
 // Rows of a round of a CTA with `heads_of` heads.
 __host__ __device__ inline int rows_of_round(int heads_of, int D, int bytes) {
@@ -255,7 +258,7 @@ __host__ __device__ inline int rows_of_round(int heads_of, int D, int bytes) {
 
 // STYLE -1: no rotation (a move).
 template <typename T, int STYLE, bool I8>
-__global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledWriteArgs p, const __grid_constant__ AxisTurns at,
+__global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledWriteArgs p, const __grid_constant__ AxisTurns at,
                                                                   int64_t group_ctas, int window, int heads_of, int share) {
   constexpr int VE = Vec<T>::N;
   const AppendArgs& a = p.a;
@@ -263,8 +266,8 @@ __global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledW
   __shared__ int32_t s_row[kMaxRows];            // row of the block; -1: the token is skipped
   __shared__ int64_t s_from[kMaxRows];
   __shared__ uint8_t s_of[kMaxRows];             // group
-  __shared__ Group s_group[kWindow];
-  __shared__ float s_scale[kWindow * kMaxUnits], s_ratio[kWindow * kMaxUnits];   // 0: no scale; 0: it did not grow
+  __shared__ Group s_group[kMaxGroups];
+  __shared__ float s_scale[kMaxGroups * kMaxUnits], s_ratio[kMaxGroups * kMaxUnits];   // 0: no scale; 0: it did not grow
   __shared__ int32_t s_groups;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = a.D / 2;
   pdl_wait();
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledW
     if (warp == 0) {                             // as many groups as have room
       int64_t total = 0;
       int ng = 0;
-      while (leaders && total < cap) {
+      while (leaders && total < cap && ng < kMaxGroups) {
         const int first = __ffs(leaders) - 1;
         const int64_t block = __shfl_sync(0xffffffffu, mine, first);
         const uint32_t after = ends & ~((2u << first) - 1u);
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 2) scaled_write_kernel(const ScaledW
       }
     };
     // Thread x settles unit x % kMaxUnits of group x / kMaxUnits: its block's scale there.
-    static_assert(kWindow * kMaxUnits == kThreads, "a thread to each");
+    static_assert(kMaxGroups * kMaxUnits == kThreads, "a thread to each");
     const int my_group = tid / kMaxUnits, my_unit = tid % kMaxUnits;
     const bool settles = my_group < ng && my_unit < units;
     const int64_t my_scale = settles ? (my_unit < heads ? 0 : p.v_scales) + s_group[my_group].block * a.H + head0 +
@@ -661,13 +664,13 @@ template <typename T, int STYLE, bool I8>
 cudaError_t launch_write_t(const ScaledWriteArgs& p, const AxisTurns& turns, const LaunchCfg& cfg) {
   constexpr int VE = Vec<T>::N;
   const AppendArgs& a = p.a;
-  // Heads of a CTA: 8, fewer where a block's rows would not fit a round otherwise.
+  // Heads of a CTA: 4, 2 where a block's rows would not fit a round otherwise.
   int heads_of = kMaxUnits / 2;
   while (heads_of > 2 && rows_of_round(heads_of, a.D, (int)sizeof(T)) < std::min(p.block_size, kMaxRows)) heads_of /= 2;
   const int splits = (a.H + heads_of - 1) / heads_of;
-  // Tokens of a CTA: one while every SM gets one, then up to 16.  Most tokens of a prompt begin no group, and CTAs that end
-  // at once still hold up the others (8000 tokens with one a CTA: 74.6 us).
-  const int window = (int)std::min<int64_t>(kWindow, std::max<int64_t>(1, a.T / cfg.num_sms));
+  // Tokens of a CTA: one while every SM gets one, then up to 16 or a block.  Most tokens of a prompt begin no group, and CTAs
+  // that end at once still hold up the others (8000 tokens with one a CTA: 74.6 us).
+  const int window = (int)std::min<int64_t>(std::min(kWindow, std::max(16, p.block_size)), std::max<int64_t>(1, a.T / cfg.num_sms));
   const int64_t group_ctas = ((int64_t)a.T + window - 1) / window * splits;
   // Warps to a token's queries: as many as keep a lane one batch busy while the SMs have room for 32 warps each.
   const int64_t items = (int64_t)a.Hq * (a.D / VE / 2);
