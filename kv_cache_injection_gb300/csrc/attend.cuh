@@ -36,6 +36,17 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// What the attention takes of the scales of a key (scaled cache): K scale, log2 of
+// the V scale and its reciprocal.  The hardware's log2 is off by 2^-22 near 1, so
+// the exponent is taken off first; the reciprocal is off by one step.
+__device__ __forceinline__ float4 key_scales(float ks, float vs) {
+  const int e = (__float_as_int(vs) - 0x3f400000) >> 23;   // vs = 2^e f, f in [0.75, 1.5)
+  float l, r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(l) : "f"(__int_as_float(__float_as_int(vs) - (e << 23))));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(vs));
+  return make_float4(ks, (float)e + l, r, 0.f);
+}
+
 // Block of position p: a shift where the block size is a power of two.
 __device__ __forceinline__ int32_t block_of(const AttendArgs& a, int32_t p) {
   return a.block_shift >= 0 ? p >> a.block_shift : p / a.block_size;

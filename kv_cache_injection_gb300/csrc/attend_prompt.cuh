@@ -957,7 +957,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
                 TileInfo& info = s_tile[slot];
                 const int lo = max(0, k_see - key0), hi = min(kKeys, k_hi - key0);
                 info.at[grp] = at;
-                s_group[slot][grp] = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
+                s_group[slot][grp] = key_scales(ks, vs);
                 if (grp < 4) {                         // a bit a key of 32: four groups' bits to bytes, and the range
                   const uint32_t four = (named >> (4 * grp)) & 15u;
                   s_mask[slot][grp] = ((four * 0x00204081u) & 0x01010101u) * 0xffu & bits_between(32 * grp, lo, hi);

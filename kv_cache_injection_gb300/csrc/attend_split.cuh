@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(kAttendThreads, SplitShape<E>::kPerSm) attend_
                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(row + c * 16), "r"(0) : "memory");
             }
             tm.valid &= good;
-            if (lane < KT) s_key[warp][lane] = ok ? make_float4(ks, log2f(vs), 1.f / vs, 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
+            if (lane < KT) s_key[warp][lane] = ok ? key_scales(ks, vs) : make_float4(1.f, 0.f, 1.f, 0.f);
             __syncwarp();
             tm.key = s_key[warp];
           }
