@@ -348,7 +348,8 @@ constexpr int kGroup = 8, kGroups = kKeys / kGroup;
 // another here whatever their segments, so that a tile's codes are on their way
 // while those of the tile before it are widened.
 struct TileInfo {
-  int64_t at[kGroups];   // first K row of the group, in bytes; -1: no block of it counts
+  int64_t at[kGroups];   // first K row of the group, in bytes; 0 where no block of it counts
+  uint32_t named;        // a bit a group: one does
   int32_t lo, hi;        // its keys that some row may see
   int32_t rows;          // query rows of the segment that it begins, 0: goes on with one; -1: the run has ended
   int32_t row0, head;    // of that segment
@@ -956,13 +957,14 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
               if (half == h) {
                 TileInfo& info = s_tile[slot];
                 const int lo = max(0, k_see - key0), hi = min(kKeys, k_hi - key0);
-                info.at[grp] = at;
+                info.at[grp] = max(at, (int64_t)0);
                 s_group[slot][grp] = key_scales(ks, vs);
                 if (grp < 4) {                         // a bit a key of 32: four groups' bits to bytes, and the range
                   const uint32_t four = (named >> (4 * grp)) & 15u;
                   s_mask[slot][grp] = ((four * 0x00204081u) & 0x01010101u) * 0xffu & bits_between(32 * grp, lo, hi);
                 }
                 if (grp == 0) {
+                  info.named = named & 0xffffu;
                   info.lo = lo;
                   info.hi = hi;
                   info.rows = j0 + h == 0 ? rows : 0;
@@ -1022,16 +1024,19 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
           ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, limit_ns));
           return ok;
         };
-        // Asks for batch b of a tile.
-        auto fetch = [&](const TileInfo& t, bool whole, int b) {
+        // Asks for batch b of a tile; `named` and `whole` are the tile's.  (A group without a block stands at 0 and is not
+        // read; blocks are whole eights, so there are eight rows.)
+        auto fetch = [&](const TileInfo& t, uint32_t named, bool whole, int b) {
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
             const int x = i % X, group = group0[x] + (b * (kBatch / X) + i / X) * kGroupStep;
-            const bool mine = w + kCodeWarps * (kBatch * b + i) < kUnits;
-            const int64_t at = mine ? t.at[group] : -1;
-            const int row = group * kGroup + in_group[x];
-            const bool in = at >= 0 && (whole || (row >= t.lo && row < t.hi));
-            cp_async16(raw + (kBatch * b + i) * kCodeGroup * 16, in ? src + at + row_off[x] : src, in);
+            if (w + kCodeWarps * (kBatch * b + i) >= kUnits) break;
+            bool in = (named >> group) & 1u;
+            if (!whole) {
+              const int row = group * kGroup + in_group[x];
+              in = in && row >= t.lo && row < t.hi;
+            }
+            cp_async16(raw + (kBatch * b + i) * kCodeGroup * 16, src + t.at[group] + row_off[x], in);
           }
         };
         auto load_q = [&](const TileInfo& t, uint32_t n_q) {
@@ -1064,7 +1069,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
           const TileInfo& t = s_tile[0];
 #pragma unroll 1
           for (int b = 0; b < kBatches; ++b) {
-            if (t.rows >= 0) fetch(t, false, b);
+            if (t.rows >= 0) fetch(t, t.named, false, b);
             cp_async_commit();
           }
           for (;; ++n_tile) {
@@ -1078,6 +1083,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
               break;
             const TileInfo& ahead = s_tile[next];
             const bool more = ahead.rows >= 0, whole = ahead.lo == 0 && ahead.hi == kKeys;
+            const uint32_t named = ahead.named;
             const uint32_t dst = ring0 + (n % S::kRing) * S::kTileBytes;
 #pragma unroll 1
             for (int b = 0; b < kBatches; ++b) {
@@ -1098,7 +1104,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
                   st_shared_v4(to, wide[i][0]);
                   st_shared_v4(to ^ 16u, wide[i][1]);
                 }
-              if (more) fetch(ahead, whole, b);
+              if (more) fetch(ahead, named, whole, b);
               cp_async_commit();
             }
             fence_proxy_async_smem();
