@@ -6,6 +6,12 @@
 // as they are, one maximum (of y) and one exponential a logit serve both sums,
 // and no weight leaves the range of its 16 bits whatever the blocks' scales are
 // to one another (a weight times a scale of its own would, for blocks 2^15 apart).
+//
+// Measured (bf16 queries): 4 requests of 60,000-131,000 tokens over INT8 (H = 8, D =
+// 128, 904 MB) 159 us = 5.7 TB/s, 84 % of a plain copy; 100 requests of 300-2048 tokens
+// (H = 4, 117 MB) 38 us over INT8 and 35 over E4M3, 17 for their bytes: a tile of 32 keys
+// is about 1000 instructions of a warp, a third of them the widening, 12 warps an SM;
+// one request of 1313 tokens 9.1 us, the latency of two kernels.
 #include "attend_split.cuh"
 
 namespace isk {

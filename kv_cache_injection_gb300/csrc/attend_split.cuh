@@ -45,6 +45,11 @@
 // largest; fainter ones are rounded by 2^-39 of the largest at most.
 // fp32 caches use fp32 fused multiply-adds throughout.
 //
+// Over a scaled cache (is_attend_scaled) a key's scales come to shared memory with
+// its rows, 4 bytes each by asynchronous copies; a lane makes them K scale, log2 of
+// the V scale and its reciprocal once a key.  The V scale goes into the exponent,
+// so the second product takes the codes as they are (see attend_scaled.cu).
+//
 // Measured (H = 8, D = 128, bf16 unless said): 4 requests of 60,000-131,000
 // tokens 260 us on one GPU and 268 on another, 6.7 to 6.9 TB/s, the rate of a
 // plain copy; 64 requests of 500-8000 tokens 173 us (6.2 TB/s), with an FP8 cache

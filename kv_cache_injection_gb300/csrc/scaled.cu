@@ -9,13 +9,25 @@
 //   s = A / qmax, in [2^-40, 2^40]; beside earlier rows no smaller than their scale;
 //   code = round(y * (1 / s)), and earlier rows' codes round(code * s_old / s) if s grew.
 // A CTA takes the groups that begin in its tokens, as many at a time as there is
-// room for: their rows are loaded, each head's keys or values by a warp (longer
-// blocks: two), while the sines of the keys are computed once for all heads; the
-// largest element of each group is found by shuffles, and the rows are quantised
-// and stored from registers.  Groups that do not fit go through twice, once for
-// the scale and once for the codes.
-// The queries are rotated by CTAs of their own, a warp or several to a token.
-// Bound by memory; each input is read once and each code written once.
+// room for (a round): their rows are copied to shared memory while the sines of
+// their keys are computed once for all heads; each warp finds the largest elements
+// of one head's keys or values at a time, a thread settles each block's scale, and
+// the warps go through the rows once more for the codes.  Groups that do not fit
+// are brought twice.  The queries are rotated by CTAs of their own, a warp or
+// several to a token.
+//
+// The bytes would take 27 and 40 us in the two large cases below; the steps of a
+// round wait for one another and for memory, and what overlaps them is other CTAs
+// (a fifth of the issue slots are used, DRAM at 40 to 60 %).  Short loops matter
+// more than registers: rows kept in registers and unrolled took 56 and 165 us, each
+// CTA running once through code that it has to fetch first.
+//
+// Measured: 8000 tokens, 32 + 8 heads of 128, bf16 to INT8, 183 MB: 44 us = 4.1
+// TB/s, 61 % of a plain copy (without the search and the codes 36); 46,000 moved
+// tokens, 8 heads, bf16 to E4M3 in blocks of 32, 271 MB: 80 us = 3.4 TB/s, blocks of
+// 16 73 us; 1276 tokens moved 8.8 us; 1000 requests' single tokens 11.1 us; one token
+// 5.8 us, the latency of its steps.  Reading 54,000 tokens back (E4M3 to bf16, 223 MB)
+// 40 us = 5.5 TB/s; 700 tokens with their keys turned back 3.9 us.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>

@@ -76,6 +76,7 @@ is_status_t check_apart(const Span* outs, int n_out, const Span* ins, int n_in) 
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3) == 0; }
 
 is_status_t check_layer_cache(const is_cache_desc_t& c, int dtype, const void* layer_cache) {
   if (c.block_size < 1 || c.block_size > IS_MAX_POSITION || c.num_blocks < 1)
@@ -92,11 +93,12 @@ is_status_t check_layer_cache(const is_cache_desc_t& c, int dtype, const void* l
 }
 
 // A scaled cache goes with every type of the call; the scales are the blocks' own.
-is_status_t check_scaled_cache(const is_cache_desc_t& c, const void* layer_cache) {
+is_status_t check_scaled_cache(const is_cache_desc_t& c, const void* layer_cache, const float* scales) {
   if (c.block_size < 1 || c.block_size > IS_MAX_POSITION || c.num_blocks < 1)
     return refuse(IS_ERR_INVALID_ARG, "block_size must be in [1, IS_MAX_POSITION], num_blocks >= 1");
   if (c.dtype != IS_INT8 && c.dtype != IS_FP8_E4M3)
     return refuse(IS_ERR_INVALID_ARG, "a scaled cache is IS_INT8 or IS_FP8_E4M3, not %d", c.dtype);
+  if (!aligned4(scales)) return refuse(IS_ERR_INVALID_ARG, "scales must be 4-byte aligned");
   if (c.k_scale != 1.f || c.v_scale != 1.f)
     return refuse(IS_ERR_INVALID_ARG, "k_scale and v_scale must be 1: a scaled cache has the blocks' scales");
   if (!aligned16(layer_cache)) return refuse(IS_ERR_INVALID_ARG, "layer_cache must be 16-byte aligned");
@@ -215,7 +217,7 @@ static is_status_t check_append(const is_append_args_t* a, bool scaled, const fl
   if (D < 16 || D > IS_MAX_HEAD_DIM || (D & (D - 1)) != 0)
     return refuse(IS_ERR_UNSUPPORTED, "head_dim must be a power of two in [16, IS_MAX_HEAD_DIM]");
   if (Hq > (1 << 16) || H > (1 << 16)) return refuse(IS_ERR_UNSUPPORTED, "at most 65536 heads");
-  is_status_t st = scaled ? check_scaled_cache(a->cache, a->layer_cache) : check_layer_cache(a->cache, a->dtype, a->layer_cache);
+  is_status_t st = scaled ? check_scaled_cache(a->cache, a->layer_cache, scales) : check_layer_cache(a->cache, a->dtype, a->layer_cache);
   if (st != IS_OK) return st;
   const int e = a->dtype == IS_F32 ? 4 : 2, ve = 16 / e;
   st = axis_turns(a->rope, a->axes, D, turns_out);
@@ -323,7 +325,7 @@ extern "C" is_status_t is_move_scaled(const is_move_args_t* a, cudaStream_t stre
   if (st == IS_OK && (a->reserved[0] | a->reserved[1]) != 0) st = refuse(IS_ERR_INVALID_ARG, "reserved must be 0");
   if (st == IS_OK && a->from.dtype == IS_FP8_E4M3) st = refuse(IS_ERR_UNSUPPORTED, "from_cache must be f32, bf16 or f16");
   if (st == IS_OK) st = check_layer_cache(a->from, a->dtype, a->from_cache);
-  if (st == IS_OK) st = check_scaled_cache(a->cache, a->layer_cache);
+  if (st == IS_OK) st = check_scaled_cache(a->cache, a->layer_cache, a->scales);
   if (st != IS_OK || T == 0) return st;
   if (!a->from_slots || !a->slot_mapping || !a->from_cache || !a->layer_cache || !a->scales || !a->status_out)
     return refuse(IS_ERR_INVALID_ARG, "a required pointer is NULL");
@@ -369,7 +371,7 @@ extern "C" is_status_t is_read_scaled(const is_read_args_t* a, cudaStream_t stre
   is_status_t st = check_rows(T, H, D, a->dtype);
   if (st == IS_OK && (a->reserved | a->reserved2) != 0) st = refuse(IS_ERR_INVALID_ARG, "reserved must be 0");
   if (st == IS_OK && a->unrotate != 0 && a->unrotate != 1) st = refuse(IS_ERR_INVALID_ARG, "unrotate must be 0 or 1");
-  if (st == IS_OK) st = check_scaled_cache(a->cache, a->layer_cache);
+  if (st == IS_OK) st = check_scaled_cache(a->cache, a->layer_cache, a->scales);
   static const AxisTurns none{};
   const AxisTurns* turns = &none;
   if (st == IS_OK && a->unrotate) st = axis_turns(a->rope, a->axes, D, &turns);
@@ -432,7 +434,7 @@ static is_status_t attend(const is_attend_args_t* a, bool scaled, const float* s
   if (D != 64 && D != 128 && D != 256) return refuse(IS_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
   if (Hq > (1 << 16) || (int64_t)T * Hq > (1 << 30))
     return refuse(IS_ERR_UNSUPPORTED, "at most 65536 heads and 2^30 rows (num_tokens * num_q_heads)");
-  is_status_t st = scaled ? check_scaled_cache(a->cache, a->layer_cache) : check_layer_cache(a->cache, a->dtype, a->layer_cache);
+  is_status_t st = scaled ? check_scaled_cache(a->cache, a->layer_cache, scales) : check_layer_cache(a->cache, a->dtype, a->layer_cache);
   if (st == IS_OK && scaled && a->dtype == IS_F32) st = refuse(IS_ERR_UNSUPPORTED, "a scaled cache is attended with bf16 or fp16");
   if (st != IS_OK) return st;
   if (!a->q_start && T < R) return refuse(IS_ERR_INVALID_ARG, "without q_start there is one row per request");

@@ -18,10 +18,12 @@ using namespace isk;
 // Launch helpers shared by every kernel launch (declared in internal.h).
 namespace isk {
 
+constexpr int kLaunchTable = 512;        // (kernel, device) pairs remembered; the library has about 230 kernels
+
 void prefer_max_shared(const void* kern) {
   static std::mutex mu;
-  static const void* done_kern[256];
-  static int done_dev[256];
+  static const void* done_kern[kLaunchTable];
+  static int done_dev[kLaunchTable];
   static int n_done = 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return;
@@ -30,7 +32,7 @@ void prefer_max_shared(const void* kern) {
     if (done_kern[i] == kern && done_dev[i] == dev) return;
   cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                        (int)cudaSharedmemCarveoutMaxShared);
-  if (n_done < 256) {
+  if (n_done < kLaunchTable) {
     done_kern[n_done] = kern;
     done_dev[n_done] = dev;
     ++n_done;
@@ -39,9 +41,9 @@ void prefer_max_shared(const void* kern) {
 
 cudaError_t ensure_dynamic_smem(const void* kern, size_t bytes) {
   static std::mutex mu;
-  static const void* kern_set[256];
-  static int dev_set[256];
-  static size_t bytes_set[256];
+  static const void* kern_set[kLaunchTable];
+  static int dev_set[kLaunchTable];
+  static size_t bytes_set[kLaunchTable];
   static int n_set = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -53,7 +55,7 @@ cudaError_t ensure_dynamic_smem(const void* kern, size_t bytes) {
   if (slot >= 0 && bytes_set[slot] >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  if (slot < 0 && n_set < 256) slot = n_set++;
+  if (slot < 0 && n_set < kLaunchTable) slot = n_set++;
   if (slot >= 0) {
     kern_set[slot] = kern;
     dev_set[slot] = dev;

@@ -71,6 +71,7 @@ def check_write(cache, bs, slots, refused, rows, err, before, after):
         same_scale[:, b] = False
         for kv in range(2):
             y, e = rows[kv, live], err[kv, live]
+            e = torch.where(y.isfinite(), e, torch.zeros(()).double())   # the others have no error: they saturate, or are NaN
             finite = torch.where(y.isfinite(), y.abs(), torch.zeros(()).double())
             top = finite.amax((0, 2))                                # [H]
             new = (top / QMAX[cache]).clamp(SMALLEST, LARGEST)

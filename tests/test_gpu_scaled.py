@@ -161,6 +161,30 @@ def test_append_what_is_not_finite(cache):
         v[1, 0, 3], v[2, 1, 5], v[3, 0, 0] = math.inf, -math.inf, math.nan
     append_case([(12, 8)], 2, 2, 64, "bf16", cache, values=spoil)
 
+    def spoil_keys(qkv, Hq, H):                          # of head 0: what head 1 gets is as ever
+        k = qkv[:, Hq: Hq + H]
+        k[1, 0, 3], k[2, 0, 40], k[5, 0, 0] = math.inf, -math.inf, math.nan
+    append_case([(12, 8)], 2, 2, 64, "bf16", cache, values=spoil_keys)
+    append_case([(40, 40)], 2, 2, 64, "f16", cache, values=spoil_keys, bs=8)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_append_rows_in_any_order(cache):
+    """The tokens of a block in another order than its rows; the lowest row says what is held."""
+    g = torch.Generator().manual_seed(13)
+    bs, H, D, nb = 16, 2, 64, 3
+    rows = [21, 19, 24, 22] + [32 + r for r in (7, 0, 3)]          # block 1 from row 3 on, block 2 afresh
+    slots, T = torch.tensor(rows), len(rows)
+    k, v = (torch.randn(T, H, D, generator=g) for _ in range(2))
+    c0, s0 = random_cache(cache, nb, bs, H, D, g)
+    codes, scales, status = c0.to(DEV), s0.to(DEV), ints([0])
+    api.is_append_scaled(None, k.to(DEV), v.to(DEV), ints([0] * T), slots.to(DEV), rope_of(PLAIN), api.make_cache_desc(bs, nb, cache),
+                         codes, scales, None, status)
+    both = torch.stack([k, v]).double()
+    sref.check_write(cache, bs, slots, torch.zeros(T, dtype=torch.bool), both, torch.zeros_like(both), (c0, s0),
+                     (codes.cpu(), scales.cpu()))
+    assert status.tolist() == [0]
+
 
 @pytest.mark.parametrize("cache", CACHES)
 def test_append_token_by_token(cache):

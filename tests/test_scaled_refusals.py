@@ -83,6 +83,10 @@ def test_append_refuses(lib, kw, status):
 
 
 def test_scales_are_needed(lib):
+    assert call(lib, "is_append_scaled", append_args(cache=CODES), SCALES + 2) == INVALID
+    assert call(lib, "is_attend_scaled", attend_args(cache=CODES), SCALES + 1) == INVALID
+    assert call(lib, "is_move_scaled", move_args(scales=SCALES + 2)) == INVALID
+    assert call(lib, "is_read_scaled", read_args(scales=SCALES + 2)) == INVALID
     assert call(lib, "is_append_scaled", append_args(cache=CODES), None) == INVALID
     assert call(lib, "is_attend_scaled", attend_args(cache=CODES), None) == INVALID
     assert call(lib, "is_attend_scaled", attend_args(cache=CODES, out=SCALES)) == INVALID
