@@ -23,10 +23,10 @@
 // CTA running once through code that it has to fetch first.
 //
 // Measured: 8000 tokens, 32 + 8 heads of 128, bf16 to INT8, 183 MB: 44 us = 4.1
-// TB/s, 61 % of a plain copy (without the search and the codes 36); 46,000 moved
+// TB/s, 61 % of a plain copy (without the search and the codes 36); 44,000 moved
 // tokens, 8 heads, bf16 to E4M3 in blocks of 32, 271 MB: 80 us = 3.4 TB/s, blocks of
 // 16 73 us; 1276 tokens moved 8.8 us; 1000 requests' single tokens 11.1 us; one token
-// 5.8 us, the latency of its steps.  Reading 54,000 tokens back (E4M3 to bf16, 223 MB)
+// 5.8 us, the latency of its steps.  Reading 36,000 tokens back (E4M3 to bf16, 223 MB)
 // 40 us = 5.5 TB/s; 700 tokens with their keys turned back 3.9 us.
 #include <algorithm>
 #include <cfloat>
@@ -39,7 +39,7 @@ namespace isk {
 
 namespace {
 
-// 128 threads and 32 KB of rows, five CTAs an SM: the steps of a CTA wait for one another, other CTAs fill the gaps (46,000
+// 128 threads and 32 KB of rows, five CTAs an SM: the steps of a CTA wait for one another, other CTAs fill the gaps (44,000
 // moved tokens 84 us, 101 with 256 threads and 64 KB, 116 with 64 and 16).
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
