@@ -27,7 +27,7 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-
                      "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]
 SOURCES = ["store.cu", "retrieve.cu", "inject.cu", "simgemm.cu", "capture.cu", "serve.cu", "blocks.cu",
            "append.cu", "attend.cu", "attend_prompt.cu", "scaled.cu", "attend_scaled.cu",
-           "attend_prompt_scaled.cu"]
+           "attend_prompt_scaled.cu", "attend_prompt_scaled_f16.cu"]
 HEADERS = [os.path.join(INCLUDE, "injectscale.h")] + [
     os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
 

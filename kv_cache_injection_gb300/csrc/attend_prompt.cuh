@@ -91,8 +91,9 @@ constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 // us, not 21.7, over 1313 26.6, not 26.0; larger batches have longer runs anyway.
 constexpr int kMinRun = 2;
 // Starting and ending an item costs a CTA about as much as this many units, so
-// an item counts as so many more, before its first.
-constexpr int kItemCost = 6;
+// an item counts as so many more, before its first.  Over a scaled cache a unit
+// takes twice as long (3: 16 requests' prompts 68.7 us; 2: 70.0, 4 and 6: 71.9).
+constexpr int kItemCost = 6, kScaledItemCost = 3;
 constexpr int kMaskRing = 8;
 // The form over a scaled cache has 16 warps: 0-7 softmax, 8 finds the tiles'
 // blocks and scales, 9-11 bring K, 12-14 V, 15 issues the MMAs; 128 registers a thread.
@@ -242,6 +243,7 @@ struct Tile {
   int32_t see;           // first position that some row sees
   int32_t kb, ke, units;
 };
+template <int COST>
 __device__ __forceinline__ Tile tile_of(const AttendArgs& a, const Req& q, int per, int t) {
   Tile x;
   x.tok0 = t * per;
@@ -251,16 +253,18 @@ __device__ __forceinline__ Tile tile_of(const AttendArgs& a, const Req& q, int p
   // whole tiles from position 0 on, so that tiles line up with the cache's blocks
   x.see = a.window > 0 ? (int32_t)max((int64_t)p0 - a.window + 1, (int64_t)0) : 0;
   x.kb = x.see / kKeys * kKeys;
-  x.units = kItemCost + max(1, (x.ke - x.kb + kKeys - 1) / kKeys);
+  x.units = COST + max(1, (x.ke - x.kb + kKeys - 1) / kKeys);
   return x;
 }
+template <int COST>
 __device__ __forceinline__ int64_t units_of_request(const AttendArgs& a, const Req& q, int per) {
   int64_t sum = 0;
-  for (int t = 0; t * per < q.n; ++t) sum += tile_of(a, q, per, t).units;
+  for (int t = 0; t * per < q.n; ++t) sum += tile_of<COST>(a, q, per, t).units;
   return sum * a.H;
 }
 
 // The segments of a CTA's run, walked by one thread.
+template <int COST>
 struct Walk {
   int64_t u, u_end, u_first, run, base;  // base: first unit of tile (r, t)
   int r, t;
@@ -284,16 +288,16 @@ struct Walk {
           t = 0;
           q = read_request(a, r, false);
         }
-        if (t * per < q.n) x = tile_of(a, q, per, t);
+        if (t * per < q.n) x = tile_of<COST>(a, q, per, t);
       }
       head = (int)div_small(u - base, x.units);
       const int64_t item0 = base + (int64_t)head * x.units;
-      const int ua = max((int)(u - item0) - kItemCost, 0), ub = (int)min((int64_t)x.units, u_end - item0) - kItemCost;
+      const int ua = max((int)(u - item0) - COST, 0), ub = (int)min((int64_t)x.units, u_end - item0) - COST;
       at_start = u == u_first;
-      u = item0 + ub + kItemCost;
+      u = item0 + ub + COST;
       if (ub <= 0) continue;             // none of its keys yet: the item begins in the next CTA
       begins = ua == 0;
-      whole = begins && ub == x.units - kItemCost;
+      whole = begins && ub == x.units - COST;
       // within the grid, whatever became of the lengths since they were added up
       parts = (int)(min(div_small(item0 + x.units - 1, run), (int64_t)gridDim.x - 1) - (int64_t)blockIdx.x) + 1;
       k_lo = x.kb + ua * kKeys;
@@ -462,13 +466,14 @@ __device__ __noinline__ float far_weights(uint32_t s_col, float sc, float m, flo
 
 // Scaled cache, one tile of a row: S (logits before their scale) becomes weights
 // over it.  A weight holds its key's V scale, x = logit + log2 of it, and the sum
-// takes that back by groups of eight.  S is read twice, for the maximum of x and
+// takes that back by groups of GROUP: sixteen where blocks are whole sixteens (606 us
+// at the long prompts' sizes, 624 with eight).  S is read twice, for the maximum of x and
 // for the weights, in loops of 64 and 32 columns: with all 128 unrolled between one
 // read and its use the warps of an SM, each in a part of the code of its own,
 // waited for instructions in a quarter of their time.  Of 32 logits S is read
 // before the 16 columns of their weights, which lie before the next ones', are
 // written.
-template <int D>
+template <int D, int GROUP>
 struct ScaledTile {
   uint32_t s_col;
   float sc;
@@ -488,17 +493,22 @@ struct ScaledTile {
   }
   __device__ __forceinline__ float top(uint32_t (&y)[32], int c) const {
     hide(y, c);
-    float x[32 / kGroup];
+    float x[32 / GROUP];
 #pragma unroll
-    for (int g = 0; g < 32 / kGroup; ++g) {
-      const float4 k = groups[c * (32 / kGroup) + g];
-      const uint32_t* v = y + g * kGroup;
+    for (int g = 0; g < 32 / GROUP; ++g) {
+      const float4 k = groups[(c * 32 + g * GROUP) / kGroup];
+      const uint32_t* v = y + g * GROUP;
       float x0 = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
       const float x1 = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
       x0 = max3(x0, __uint_as_float(v[6]), __uint_as_float(v[7]));
+#pragma unroll
+      for (int i = 8; i < GROUP; i += 2) x0 = max3(x0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
       x[g] = fmaf(fmaxf(x0, x1), group_factor(sc, k.x), k.y);   // grows with the logits of a group
     }
-    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    float most = x[0];
+#pragma unroll
+    for (int g = 1; g < 32 / GROUP; ++g) most = fmaxf(most, x[g]);
+    return most;
   }
   // The weights of all columns, the first 32 of which are on their way to y, and their sum on top of l.  FAR: exponents
   // rounded as they were for the maximum (see kFar).
@@ -507,29 +517,29 @@ struct ScaledTile {
     unsigned long long sum = pk2(l, 0.f);
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
-      float4 k[32 / kGroup];
+      float4 k[32 / GROUP];
 #pragma unroll
-      for (int g = 0; g < 32 / kGroup; ++g) k[g] = groups[c * (32 / kGroup) + g];
+      for (int g = 0; g < 32 / GROUP; ++g) k[g] = groups[(c * 32 + g * GROUP) / kGroup];
       tmem_wait_ld32(y);
       hide(y, c);
       float x[32];
 #pragma unroll
-      for (int g = 0; g < 32 / kGroup; ++g) {
+      for (int g = 0; g < 32 / GROUP; ++g) {
         const float factor = group_factor(sc, k[g].x), off = FAR ? k[g].y : k[g].y - mz;
         const unsigned long long factor2 = pk2(factor, factor), off2 = pk2(off, off);
 #pragma unroll
-        for (int i = g * kGroup; i < (g + 1) * kGroup; i += 2)
+        for (int i = g * GROUP; i < (g + 1) * GROUP; i += 2)
           upk2(fma2_rn(pk2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), factor2, off2), x[i], x[i + 1]);
       }
       if (c < 3) tmem_ld32(s_col + 32 * (c + 1), y);
       uint32_t p[16];
 #pragma unroll
-      for (int g = 0; g < 32 / kGroup; ++g) {
+      for (int g = 0; g < 32 / GROUP; ++g) {
         unsigned long long of_group = 0ull;
 #pragma unroll
-        for (int i = g * kGroup; i < (g + 1) * kGroup; i += 2) {
+        for (int i = g * GROUP; i < (g + 1) * GROUP; i += 2) {
           const float y0 = ex2(FAR ? __fsub_rn(x[i], mz) : x[i]), y1 = ex2(FAR ? __fsub_rn(x[i + 1], mz) : x[i + 1]);
-          of_group = i == g * kGroup ? pk2(y0, y1) : add2_rn(of_group, pk2(y0, y1));
+          of_group = i == g * GROUP ? pk2(y0, y1) : add2_rn(of_group, pk2(y0, y1));
           p[i / 2] = Vec<W>::pack2(y0, y1);
         }
         sum = fma2_rn(of_group, pk2(k[g].z, k[g].z), sum);
@@ -587,12 +597,13 @@ struct ScaledTile {
 constexpr int threads_of(CacheKind kind) { return kind == kCacheScaledE4m3 || kind == kCacheScaledInt8 ? kScaledThreads : kThreads; }
 
 // LIMITED: the limit of the waits is the call's.  (As a variable in the ordinary form it costs 16 prompts 1.2 us of 53.4.)
-template <typename T, CacheKind KIND, int D, bool LIMITED>
+template <typename T, CacheKind KIND, int D, bool LIMITED, int GROUP>
 __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(const AttendArgs a, int per, int box,
                                                                            const __grid_constant__ CUtensorMap rows_map) {
   constexpr bool F8 = KIND != kCachePlain, kInt8 = KIND == kCacheScaledInt8;   // F8: 8-bit elements
   constexpr bool kScaled = KIND == kCacheScaledE4m3 || KIND == kCacheScaledInt8;
   using S = Shape<D, F8, kScaled>;
+  constexpr int kCost = kScaled ? kScaledItemCost : kItemCost;
   constexpr int kThreads = threads_of(KIND), kMmaWarp = kThreads / 32 - 1;
   const uint64_t limit_ns = LIMITED ? a.wait_ns : kWaitBudgetNs;
   // FP8 keys and values are exact in fp16, and a bf16 query row scaled by a power of two (undone in the logits) loses
@@ -660,7 +671,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
   const int share = (a.R + kThreads - 1) / kThreads;
   const int r0 = min(a.R, tid * share), r1 = min(a.R, r0 + share);
   int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) mine += units_of_request(a, read_request(a, r, blockIdx.x == 0), per);
+  for (int r = r0; r < r1; ++r) mine += units_of_request<kCost>(a, read_request(a, r, blockIdx.x == 0), per);
   int64_t total;
   int64_t at = block_exclusive_scan(mine, scratch, &total);
   const int64_t run = max((int64_t)kMinRun, div_small(total + gridDim.x - 1, gridDim.x));
@@ -668,7 +679,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
   const bool idle = u0 >= u1;
   if (!idle && at <= u0 && u0 < at + mine) {
     for (int r = r0; r < r1; ++r) {
-      const int64_t n = units_of_request(a, read_request(a, r, false), per);
+      const int64_t n = units_of_request<kCost>(a, read_request(a, r, false), per);
       if (u0 < at + n || r == r1 - 1) {
         s_req = r;
         s_base = at;
@@ -737,7 +748,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
           if constexpr (kScaled) {
             const uint4 named = *reinterpret_cast<const uint4*>(s_mask[slot]);
             const bool check = (named.x & named.y & named.z & named.w) != 0xffffffffu || key0 + kKeys - 1 > lim_lo || key0 < low_hi;
-            const ScaledTile<D> tile{s_col, sc, s_mask[slot], s_group[slot], key0, low, lim + 1, check, smem_addr(&bars.p_full[side][0]), lane};
+            const ScaledTile<D, GROUP> tile{s_col, sc, s_mask[slot], s_group[slot], key0, low, lim + 1, check, smem_addr(&bars.p_full[side][0]), lane};
             l = tile.template run<W>(o_col, j > 0, m, l);
             continue;
           }
@@ -881,7 +892,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
     } else if (kScaled && warp == kLoaderWarp) {
       // ---- scaled cache: segments, and the tiles' blocks, masks and scales ---------
       if constexpr (kScaled) {
-        Walk w;                                        // the first lane's
+        Walk<kCost> w;                                 // the first lane's
         bool crosses = false, ok = true;
         if (lane == 0) {
           w.run = run;
@@ -891,7 +902,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
           w.base = s_base;
           w.t = 0;
           w.q = read_request(a, w.r, false);
-          w.x = tile_of(a, w.q, per, 0);
+          w.x = tile_of<kCost>(a, w.q, per, 0);
         }
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, limit_ns));
@@ -940,7 +951,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
             const int j = j0 + half, key0 = k_lo + j * kKeys, p = key0 + grp * kGroup;
             int64_t at = -1;
             float ks = 1.f, vs = 1.f;
-            if (j < n_tiles && p + kGroup > k_see && p < k_hi) {
+            // (of a group of which any key is seen, all eights: the first's scales are the group's)
+            if (j < n_tiles && (p & -GROUP) + GROUP > k_see && p < k_hi) {
               const int b = block_of(a, p);
               const int32_t id = table[b];
               if (id >= 0 && id < a.num_blocks) {
@@ -1149,7 +1161,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
         return r != 0;
       };
       auto barrier_loaders = [] { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kLoaders) : "memory"); };
-      Walk w;                                          // the first thread's
+      Walk<kCost> w;                                   // the first thread's
       bool crosses = false;                            // the run's last item began here and goes on in the next CTA
       if (lt == 0) {
         w.run = run;
@@ -1159,7 +1171,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
         w.base = s_base;
         w.t = 0;
         w.q = read_request(a, w.r, false);
-        w.x = tile_of(a, w.q, per, 0);
+        w.x = tile_of<kCost>(a, w.q, per, 0);
       }
       for (uint32_t n_seg = 0;; ++n_seg) {
         const uint32_t seg = n_seg % kSegments;
@@ -1586,12 +1598,13 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
 
 // Prompts go here when the rows of a request fill a tensor-core tile better
 // than the split kernel's 16 rows (see launch_attend).
-template <typename T, CacheKind KIND, int D>
+template <typename T, CacheKind KIND, int D, int GROUP = prompt::kGroup>
 static cudaError_t launch_prompt_t(const AttendArgs& a, const LaunchCfg& cfg) {
   constexpr bool F8 = KIND != kCachePlain;
   constexpr bool kScaled = KIND == kCacheScaledE4m3 || KIND == kCacheScaledInt8;
   using S = prompt::Shape<D, F8, kScaled>;
-  auto* kern = a.wait_ns < kWaitBudgetNs ? prompt::attend_prompt_kernel<T, KIND, D, true> : prompt::attend_prompt_kernel<T, KIND, D, false>;
+  auto* kern = a.wait_ns < kWaitBudgetNs ? prompt::attend_prompt_kernel<T, KIND, D, true, GROUP>
+                                         : prompt::attend_prompt_kernel<T, KIND, D, false, GROUP>;
   static_assert(S::kSmem + (kScaled ? 8192 : F8 ? 2048 : 1024) <= 227 * 1024, "a CTA fits an SM");
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;

@@ -21,7 +21,7 @@ cudaError_t launch_attend_scaled(const AttendArgs& a, bool int8, const LaunchCfg
   // kernel where its shared memory has room and the scale is positive.  It takes
   // a block's scales once for eight keys, so blocks have to be whole eights.
   if (a.D <= 128 && a.block_size % 8 == 0 && a.G <= 64 && (int64_t)a.max_q * a.G > 32 && a.scale > 0.f)
-    return launch_attend_prompt_scaled(a, int8, cfg);
+    return a.dtype == IS_BF16 ? launch_attend_prompt_scaled_bf16(a, int8, cfg) : launch_attend_prompt_scaled_f16(a, int8, cfg);
   if (a.dtype == IS_BF16)
     return int8 ? launch_mma<__nv_bfloat16, kCacheScaledInt8>(a, cfg) : launch_mma<__nv_bfloat16, kCacheScaledE4m3>(a, cfg);
   return int8 ? launch_mma<__half, kCacheScaledInt8>(a, cfg) : launch_mma<__half, kCacheScaledE4m3>(a, cfg);

@@ -103,7 +103,8 @@ cudaError_t launch_attend_prompt(const AttendArgs& a, const LaunchCfg& cfg);
 cudaError_t launch_scaled_write(const ScaledWriteArgs& p, const AxisTurns& turns, const LaunchCfg& cfg);
 cudaError_t launch_scaled_read(const ScaledReadArgs& a, const AxisTurns& turns, const LaunchCfg& cfg);
 cudaError_t launch_attend_scaled(const AttendArgs& a, bool int8, const LaunchCfg& cfg);
-cudaError_t launch_attend_prompt_scaled(const AttendArgs& a, bool int8, const LaunchCfg& cfg);
+cudaError_t launch_attend_prompt_scaled_bf16(const AttendArgs& a, bool int8, const LaunchCfg& cfg);
+cudaError_t launch_attend_prompt_scaled_f16(const AttendArgs& a, bool int8, const LaunchCfg& cfg);
 
 // Whether a row of row_bytes (K or V of one layer) and R requests fit the
 // inject kernel's shared-memory plan.
