@@ -55,6 +55,8 @@ __device__ __forceinline__ uint32_t ld_table(const uint8_t* p) {
   return x;
 }
 
+__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ int64_t block_of_slot(int64_t slot, int32_t size, int32_t shift) {
   return shift >= 0 ? slot >> shift : slot / size;
 }
@@ -271,29 +273,40 @@ __host__ __device__ inline int rows_of_round(int heads_of, int D, int bytes) {
 // STYLE -1: no rotation (a move).
 template <typename T, int STYLE, bool I8>
 __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledWriteArgs p, const __grid_constant__ AxisTurns at,
-                                                                  int64_t group_ctas, int window, int heads_of, int share) {
+                                                                  int group_ctas, int turns_of, int window, int heads_of, int share) {
   constexpr int VE = Vec<T>::N;
   const AppendArgs& a = p.a;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int32_t s_row[kMaxRows];            // row of the block; -1: the token is skipped
-  __shared__ int64_t s_from[kMaxRows];
+  __shared__ int32_t s_token[STYLE >= 0 ? kMaxRows : 1];
   __shared__ uint8_t s_of[kMaxRows];             // group
   __shared__ Group s_group[kMaxGroups];
   __shared__ float s_scale[kMaxGroups * kMaxUnits], s_ratio[kMaxGroups * kMaxUnits];   // 0: no scale; 0: it did not grow
   __shared__ int32_t s_groups;
+  __shared__ uint64_t s_landed;                  // a stage's rows
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = a.D / 2;
+  // The first 2 turns_of CTAs are a group's and the queries' in turn, then come what is left of the groups' and of the queries'.
+  const int at_grid = blockIdx.x, later = at_grid - turns_of;
+  const int cta = at_grid >= 2 * turns_of ? (later < group_ctas ? later : at_grid)
+                  : at_grid & 1           ? group_ctas + at_grid / 2 : at_grid / 2;
   pdl_wait();
   pdl_trigger();
-  if ((int64_t)blockIdx.x >= group_ctas) {
+  if (cta >= group_ctas) {
     if constexpr (STYLE >= 0) {
       rotate_queries<T, STYLE>(a, at, reinterpret_cast<float*>(smem) + warp * a.D,
-                               ((int64_t)blockIdx.x - group_ctas) * kWarps + warp, share);
+                               (int64_t)(cta - group_ctas) * kWarps + warp, share);
     }
     return;
   }
+  const uint32_t landed = smem_addr(&s_landed);
+  uint32_t n_stage = 0;
+  if (tid == 0) {
+    mbar_init(landed, kThreads);
+    fence_mbar_init();
+  }
   const int splits = (a.H + heads_of - 1) / heads_of;
-  const int64_t begin = blockIdx.x / splits * (int64_t)window;
-  const int head0 = (int)(blockIdx.x % splits) * heads_of, heads = min(heads_of, a.H - head0), units = 2 * heads;
+  const int64_t begin = cta / splits * (int64_t)window;
+  const int head0 = cta % splits * heads_of, heads = min(heads_of, a.H - head0), units = 2 * heads;
   const int gv = a.D / VE / 2, f = tid % gv, cap = rows_of_round(heads_of, a.D, (int)sizeof(T));
   const int head_bytes = a.D * (int)sizeof(T), part_bytes = heads * head_bytes;   // of a row's keys, or values
   const size_t row_bytes = (size_t)a.H * a.D;    // of the cache
@@ -319,6 +332,12 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
     leaders = __ballot_sync(0xffffffffu, ours && mine >= 0 && mine != before);
     ends = __ballot_sync(0xffffffffu, lane >= 1 && mine != before);
     if (head0 == 0 && ours && mine < 0 && a.slots[t] != -1) latch(a.status, IS_ST_BLOCK_ID);
+  }
+  if (warp == 1 && lane < window && begin + lane < a.T) {   // what the rows' threads will read next
+    if (p.from) prefetch(p.from + begin + lane);
+    if constexpr (STYLE >= 0) {
+      for (int x = 0; x < a.n_axes; ++x) prefetch(a.positions + (size_t)x * a.T + begin + lane);
+    }
   }
   while (true) {
     if (warp == 0) {                             // as many groups as have room
@@ -354,9 +373,13 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
     if (ng == 0) return;
     const int64_t total = s_group[ng - 1].row0 + s_group[ng - 1].n;   // past cap: one long group, which goes through twice
 
-    // Rows i0 .. i0 + cnt - 1 of the round: their places, their elements and their keys' sines.
+    // Rows i0 .. i0 + cnt - 1 of the round: their places, their elements and their keys' sines.  A row's keys and values are a
+    // bulk copy each, and a thread issues one (a warp issues its lanes' one after the other, so neighbours go to other
+    // warps: 44,000 moved tokens 63 us, 70 with a warp's lanes side by side, 79 with 16 bytes a thread).  False: the copies
+    // did not arrive in time.
     auto stage = [&](int64_t i0, int cnt) {
-      for (int i = tid; i < cnt; i += kThreads) {
+      for (int x = lane * kWarps + warp; x < 2 * cnt; x += kThreads) {
+        const int i = x >> 1, value = x & 1;
         int g = ng - 1;
         while (g > 0 && s_group[g].row0 > i) --g;
         const int64_t t = s_group[g].t0 + (i0 + i - s_group[g].row0);
@@ -379,30 +402,31 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
             }
           }
         }
-        s_row[i] = row;
-        s_from[i] = from;
-        s_of[i] = (uint8_t)g;
-        if (row >= 0) s_group[g].live = 1;
+        if (value == 0) {
+          s_row[i] = row;
+          s_of[i] = (uint8_t)g;
+          if (STYLE >= 0) s_token[i] = (int32_t)t;
+          if (row >= 0) s_group[g].live = 1;
+        }
+        if (row >= 0) {
+          const uint8_t* src = (value ? a.v + from * a.v_stride : a.k + from * a.k_stride) + (size_t)head0 * head_bytes;
+          mbar_add_tx(landed, part_bytes);
+          bulk_load(smem_addr(smem) + (uint32_t)(value ? cnt + i : i) * part_bytes, src, part_bytes, landed);
+        }
       }
-      __syncthreads();
-      for (int x = warp; x < 2 * cnt; x += kWarps) {
-        const int i = x < cnt ? x : x - cnt;
-        if (s_row[i] < 0) continue;
-        const uint8_t* src = (x < cnt ? a.k + s_from[i] * a.k_stride : a.v + s_from[i] * a.v_stride) + (size_t)head0 * head_bytes;
-        const uint32_t dst = smem_addr(smem) + (uint32_t)x * part_bytes;
-        for (int c = lane * 16; c < part_bytes; c += 512) cp_async16(dst + c, src + c, true);
-      }
-      cp_async_commit();
-      if constexpr (STYLE >= 0) {                // s_from is the token
+      mbar_arrive(landed);
+      if constexpr (STYLE >= 0) {
+        __syncthreads();
         for (int x = tid; x < cnt * half; x += kThreads) {
           const int i = x / half, g = (x - i * half) / VE, e = x % VE, j = pair_of<VE, STYLE>(g, e, gv);
-          const float2 v = turn_of(at, j, (float)a.positions[(size_t)ld_table(&at.axis[j]) * a.T + s_from[i]], 1.f);
+          const float2 v = turn_of(at, j, (float)a.positions[(size_t)ld_table(&at.axis[j]) * a.T + s_token[i]], 1.f);
           s_turn[i * a.D + turn_at<VE>(g, e, gv)] = v.x;
           s_turn[i * a.D + turn_at<VE>(g, e + VE, gv)] = v.y;
         }
       }
-      cp_async_wait<0>();
-      __syncthreads();
+      const bool in_time = __syncthreads_and(mbar_wait_bounded(landed, n_stage++ & 1u, kWaitBudgetNs));
+      if (!in_time && tid == 0) latch(a.status, IS_ST_TIMEOUT);
+      return in_time;
     };
     // A warp takes a unit, gv lanes a row of it: vectors f and f + gv of the head.
     const int step = 32 / gv;
@@ -423,56 +447,59 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
       for (int unit = warp; unit < units; unit += kWarps) {
         const uint8_t* rows = unit_rows(unit, cnt);
         const bool key = unit < heads;
-        float most = 0.f;
-        uint32_t bits = 0;
+        const bool turned = STYLE >= 0 && key;
+        const int first = lane / gv;
+        float most = 0.f;                        // of rotated elements
+        uint32_t bits = 0;                       // of elements as they came
         bool odd = false;
-        auto slow = [&](int i, const uint4& x0, const uint4& z0) {
-          float x[VE], z[VE];
-          values(key, i, x0, z0, x, z);
+        // The largest finite magnitude of the lane's elements since the last time, which are those of rows from, from +
+        // step, ... below end: looked at one by one if one of them is not finite (odd).
+        auto flush = [&](int from, int end) {
+          const float came = magnitude<T>(bits);
+          float m = turned ? most : came;
+          odd = !(came < INFINITY) || m == INFINITY;
+          if (odd) {
+            m = 0.f;
+#pragma unroll 1
+            for (int i = from; i < end; i += step) {
+              if (s_row[i] < 0) continue;
+              float x[VE], z[VE];
+              values(key, i, *reinterpret_cast<const uint4*>(rows + (size_t)i * part_bytes),
+                     *reinterpret_cast<const uint4*>(rows + (size_t)i * part_bytes + gv * 16), x, z);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) most = larger_finite(larger_finite(most, x[e]), z[e]);
+              for (int e = 0; e < VE; ++e) m = larger_finite(larger_finite(m, x[e]), z[e]);
+            }
+          }
+          most = 0.f;
+          bits = 0;
+          return m;
         };
         for (int i0 = 0; i0 < cnt; i0 += step) {
-          const int i = i0 + lane / gv;
+          const int i = i0 + first;
           if (i < cnt && s_row[i] >= 0) {
             const uint4 x0 = *reinterpret_cast<const uint4*>(rows + (size_t)i * part_bytes);
             const uint4 z0 = *reinterpret_cast<const uint4*>(rows + (size_t)i * part_bytes + gv * 16);
-            const uint32_t mine = larger_bits<T>(larger_bits<T>(0u, x0), z0);
-            if (!(magnitude<T>(mine) < INFINITY)) {
-              odd = true;
-              slow(i, x0, z0);
-            } else if (STYLE >= 0 && key) {
-              float x[VE], z[VE], top = 0.f;
+            bits = larger_bits<T>(larger_bits<T>(bits, x0), z0);
+            if (turned) {
+              float x[VE], z[VE];
               values(true, i, x0, z0, x, z);
 #pragma unroll
-              for (int e = 0; e < VE; ++e) top = fmaxf(fmaxf(top, fabsf(x[e])), fabsf(z[e]));
-              if (top == INFINITY) {
-                odd = true;
-                slow(i, x0, z0);
-              } else {
-                most = fmaxf(most, top);
-              }
-            } else {
-              bits = max_bits<T>(bits, mine);
+              for (int e = 0; e < VE; ++e) most = fmaxf(fmaxf(most, fabsf(x[e])), fabsf(z[e]));
             }
           }
           if (by_row) {
-            most = fmaxf(most, magnitude<T>(bits));
-            for (int d = 1; d < gv; d <<= 1) {
-              most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-              odd |= __shfl_xor_sync(0xffffffffu, (int)odd, d) != 0;
+            float m = flush(i, min(cnt, i + 1));
+            for (int d = 1; d < gv; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            if (__any_sync(0xffffffffu, odd)) {
+              for (int d = 1; d < gv; d <<= 1) odd |= __shfl_xor_sync(0xffffffffu, (int)odd, d) != 0;
             }
-            if (f == 0 && i < cnt) s_most[unit * cap + i] = signed_most(most, odd);
-            most = 0.f;
-            bits = 0;
-            odd = false;
+            if (f == 0 && i < cnt) s_most[unit * cap + i] = signed_most(m, odd);
           }
         }
         if (!by_row) {
-          most = fmaxf(most, magnitude<T>(bits));
-          most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+          const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(flush(first, cnt))));
           odd = __any_sync(0xffffffffu, odd);
-          if (lane == 0) s_most[unit * cap] = signed_most(most, odd);
+          if (lane == 0) s_most[unit * cap] = signed_most(m, odd);
         }
       }
       __syncthreads();
@@ -557,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
       }
     };
     if (total <= cap) {
-      stage(0, (int)total);
+      if (!stage(0, (int)total)) return;
       find_most((int)total, ng > 1);
       gather(ng > 1);
       settle();
@@ -565,14 +592,14 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
     } else {
       auto rows_from = [&](int64_t i0) { return (int)min((int64_t)cap, total - i0); };
       for (int64_t i0 = 0; i0 < total; i0 += cap) {
-        stage(i0, rows_from(i0));
+        if (!stage(i0, rows_from(i0))) return;
         find_most(rows_from(i0), false);
         gather(false);
         __syncthreads();                         // before the next rows are staged
       }
       settle();
       for (int64_t i0 = 0; i0 < total; i0 += cap) {
-        stage(i0, rows_from(i0));
+        if (!stage(i0, rows_from(i0))) return;
         store(rows_from(i0));
         __syncthreads();
       }
@@ -690,13 +717,16 @@ cudaError_t launch_write_t(const ScaledWriteArgs& p, const AxisTurns& turns, con
   while (share < 16 && (int64_t)a.T * share < 32LL * cfg.num_sms && (int64_t)share * 32 < items) share *= 2;
   const int64_t q_ctas = a.Hq > 0 ? ((int64_t)a.T * share + kWarps - 1) / kWarps : 0;
   if (group_ctas + q_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  // Queries' CTAs wait for memory and groups' for their steps: where not all fit at once they take turns (8000 tokens 41.3 us
+  // with the groups' first, 37.6 in turn; 100 tokens 5.7 and 6.1).
+  const int turns_of = group_ctas + q_ctas > 5LL * cfg.num_sms ? (int)std::min(group_ctas, q_ctas) : 0;
   const size_t rows = rows_of_round(heads_of, a.D, (int)sizeof(T));
   const size_t smem = rows * (2 * heads_of * (a.D * sizeof(T) + sizeof(float)) + (STYLE >= 0 ? a.D * sizeof(float) : 0));
   const size_t queries = STYLE >= 0 ? (size_t)kWarps * a.D * sizeof(float) : 0;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(&scaled_write_kernel<T, STYLE, I8>), std::max(smem, queries));
   if (e != cudaSuccess) return e;
   return launch_ex(scaled_write_kernel<T, STYLE, I8>, dim3((unsigned)(group_ctas + q_ctas)), dim3(kThreads),
-                   std::max(smem, queries), cfg.stream, cfg.pdl, p, turns, group_ctas, window, heads_of, share);
+                   std::max(smem, queries), cfg.stream, cfg.pdl, p, turns, (int)group_ctas, turns_of, window, heads_of, share);
 }
 
 template <typename T, bool I8>
