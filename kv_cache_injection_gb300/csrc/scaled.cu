@@ -9,7 +9,7 @@
 //   s = A / qmax, in [2^-40, 2^40]; beside earlier rows no smaller than their scale;
 //   code = round(y * (1 / s)), and earlier rows' codes round(code * s_old / s) if s grew.
 // A CTA takes the groups that begin in its tokens, as many at a time as there is
-// room for (a round): their rows are copied to shared memory while the sines of
+// room for (a round): their rows come to shared memory by bulk copies while the sines of
 // their keys are computed once for all heads; each warp finds the largest elements
 // of one head's keys or values at a time, a thread settles each block's scale, and
 // the warps go through the rows once more for the codes.  Groups that do not fit
@@ -18,16 +18,19 @@
 //
 // The bytes would take 27 and 40 us in the two large cases below; the steps of a
 // round wait for one another and for memory, and what overlaps them is other CTAs
-// (a fifth of the issue slots are used, DRAM at 40 to 60 %).  Short loops matter
-// more than registers: rows kept in registers and unrolled took 56 and 165 us, each
-// CTA running once through code that it has to fetch first.
+// (the SMs issue in half of their slots).  Of the 63 us of the second case 18 are
+// the codes, 7 the search and 38 the way to the rows and the rows themselves.
+// Short loops matter more than registers: rows kept in registers and unrolled took
+// 56 and 165 us, each CTA running once through code that it has to fetch first.
+// Bringing a piece of a CTA's heads while the one before is quantised, 16 KB each,
+// took 40 and 68 us: more steps for each byte.
 //
-// Measured: 8000 tokens, 32 + 8 heads of 128, bf16 to INT8, 183 MB: 44 us = 4.1
-// TB/s, 61 % of a plain copy (without the search and the codes 36); 44,000 moved
-// tokens, 8 heads, bf16 to E4M3 in blocks of 32, 271 MB: 80 us = 3.4 TB/s, blocks of
-// 16 73 us; 1276 tokens moved 8.8 us; 1000 requests' single tokens 11.1 us; one token
-// 5.8 us, the latency of its steps.  Reading 36,000 tokens back (E4M3 to bf16, 223 MB)
-// 40 us = 5.5 TB/s; 700 tokens with their keys turned back 3.9 us.
+// Measured: 8000 tokens, 32 + 8 heads of 128, bf16 to INT8, 183 MB: 37 us = 4.9
+// TB/s, 72 % of a plain copy (the queries alone 26); 44,000 moved tokens, 8 heads,
+// bf16 to E4M3 in blocks of 32, 271 MB: 63 us = 4.3 TB/s, blocks of 16 62 us; 1276
+// tokens moved 6.9 us; 1000 requests' single tokens 11.3 us; one token 5.0 us, the
+// latency of its steps.  Reading 36,000 tokens back (E4M3 to bf16, 223 MB) 40 us =
+// 5.5 TB/s; 700 tokens with their keys turned back 3.9 us.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -39,8 +42,8 @@ namespace isk {
 
 namespace {
 
-// 128 threads and 32 KB of rows, five CTAs an SM: the steps of a CTA wait for one another, other CTAs fill the gaps (44,000
-// moved tokens 84 us, 101 with 256 threads and 64 KB, 116 with 64 and 16).
+// 128 threads and 32 KB of rows, five CTAs an SM: the steps of a CTA wait for one another, other CTAs fill the gaps (8000
+// tokens 37 us, 51 with 256 threads and 64 KB, 45 with 128 threads and 16 KB).
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
@@ -706,11 +709,14 @@ cudaError_t launch_write_t(const ScaledWriteArgs& p, const AxisTurns& turns, con
   // Heads of a CTA: 4, 2 where a block's rows would not fit a round otherwise.
   int heads_of = kMaxUnits / 2;
   while (heads_of > 2 && rows_of_round(heads_of, a.D, (int)sizeof(T)) < std::min(p.block_size, kMaxRows)) heads_of /= 2;
-  const int splits = (a.H + heads_of - 1) / heads_of;
   // Tokens of a CTA: one while every SM gets one, then up to 16 or a block.  Most tokens of a prompt begin no group, and CTAs
   // that end at once still hold up the others (8000 tokens with one a CTA: 74.6 us).
   const int window = (int)std::min<int64_t>(std::min(kWindow, std::max(16, p.block_size)), std::max<int64_t>(1, a.T / cfg.num_sms));
-  const int64_t group_ctas = ((int64_t)a.T + window - 1) / window * splits;
+  // Two heads too while all CTAs fit at once: one token 5.5 -> 5.0 us, 1276 moved tokens 7.9 -> 6.9, a prompt of 1600 16.9 ->
+  // 15.3 (1000 single tokens 10.6 -> 11.3).
+  const int64_t windows = ((int64_t)a.T + window - 1) / window, at_once = 5LL * cfg.num_sms;
+  while (heads_of > 2 && windows * ((a.H + heads_of / 2 - 1) / (heads_of / 2)) <= at_once) heads_of /= 2;
+  const int64_t group_ctas = windows * ((a.H + heads_of - 1) / heads_of);
   // Warps to a token's queries: as many as keep a lane one batch busy while the SMs have room for 32 warps each.
   const int64_t items = (int64_t)a.Hq * (a.D / VE / 2);
   int share = 1;
@@ -719,7 +725,7 @@ cudaError_t launch_write_t(const ScaledWriteArgs& p, const AxisTurns& turns, con
   if (group_ctas + q_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   // Queries' CTAs wait for memory and groups' for their steps: where not all fit at once they take turns (8000 tokens 41.3 us
   // with the groups' first, 37.6 in turn; 100 tokens 5.7 and 6.1).
-  const int turns_of = group_ctas + q_ctas > 5LL * cfg.num_sms ? (int)std::min(group_ctas, q_ctas) : 0;
+  const int turns_of = group_ctas + q_ctas > at_once ? (int)std::min(group_ctas, q_ctas) : 0;
   const size_t rows = rows_of_round(heads_of, a.D, (int)sizeof(T));
   const size_t smem = rows * (2 * heads_of * (a.D * sizeof(T) + sizeof(float)) + (STYLE >= 0 ? a.D * sizeof(float) : 0));
   const size_t queries = STYLE >= 0 ? (size_t)kWarps * a.D * sizeof(float) : 0;
