@@ -646,7 +646,9 @@ is_status_t is_attend_within(const is_attend_args_t* args, int64_t budget_ns, cu
  * key rotated in fp32 or the raw value.  Infinities saturate; NaN is 0 in INT8 and NaN
  * in E4M3.  Rows behind the tokens' are left as they are and mean nothing.  A
  * block whose earlier rows count but whose scale is out of range keeps its
- * codes, and the tokens' K or V of that head are not written (IS_ST_SCALE). */
+ * codes, and the tokens' K or V of that head are not written (IS_ST_SCALE).
+ * A call waits at most 2 s for its copies of rows, then leaves tokens out
+ * (IS_ST_TIMEOUT). */
 
 /* is_append_scaled: is_append into a scaled cache (args->cache of IS_INT8 or
  * IS_FP8_E4M3, any args->dtype).  q_out is that of is_append.  A refused token's

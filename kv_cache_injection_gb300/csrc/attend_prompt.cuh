@@ -58,10 +58,10 @@
 // Over an FP8 cache the two long prompts take 560 us, 0.96 PFLOP/s: the three
 // loader warps that widen the rows are the limit.  At head_dim 256 (bf16, twice
 // the operations) 947 us, 1.14 PFLOP/s: with one tile, its products and its softmax
-// take turns.  Over a scaled cache 628 us (INT8) and 600 us (E4M3), 0.86 and 0.90
-// PFLOP/s: instructions, 11,000 a pair of tiles at half of the issue slots, two
-// thirds of them the softmax (a group of eight keys costs as much for its scales as
-// for two of its weights), one third the loaders; 16 requests' prompts 71 us.
+// take turns.  Over a scaled cache 606 us (INT8) and 574 us (E4M3), 0.89 and 0.94
+// PFLOP/s: instructions, about 10,000 a pair of tiles at half of the issue slots, two
+// thirds of them the softmax (what a group of keys shares costs as much as two of its
+// weights), one third the loaders; 16 requests' prompts 67.5 us.
 #pragma once
 
 #include <cuda.h>

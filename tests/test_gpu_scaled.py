@@ -790,3 +790,9 @@ def test_append_many_requests(cache, D, bs):
     at = np.cumsum([0] + [m for _, m in reqs])
     skip = [int(at[r]) for r in range(0, 700, 53) if reqs[r][1] == 1]       # a block's tokens stay adjacent
     append_case(reqs, 4, 3, D, "bf16", cache, bs=bs, skip=skip)
+
+
+@pytest.mark.parametrize("Hq,H,D", [(2, 32, 64), (33, 9, 64), (4, 3, 128)])
+def test_append_long_prompts(Hq, H, D):
+    """More CTAs than fit at once, of which those of the queries are fewer or more than those of the groups."""
+    append_case([(1700, 1650), (90, 1), (1301, 1300), (2000, 1999)], Hq, H, D, "bf16", "int8")
