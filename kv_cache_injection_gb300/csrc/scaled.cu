@@ -60,6 +60,9 @@ __device__ __forceinline__ uint32_t ld_table(const uint8_t* p) {
 
 __device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
+// Of a power of two.  (What divides here mostly is one; a division by a variable takes 20 instructions, 64 bits wide 80.)
+__device__ __forceinline__ int log2_of(int x) { return 31 - __clz(x); }
+
 __device__ __forceinline__ int64_t block_of_slot(int64_t slot, int32_t size, int32_t shift) {
   return shift >= 0 ? slot >> shift : slot / size;
 }
@@ -123,7 +126,7 @@ __device__ __forceinline__ Turn<Vec<T>::N> warp_turn(const AxisTurns& at, float*
   constexpr int VE = Vec<T>::N;
   const int lane = threadIdx.x & 31;
   for (int i0 = 0; i0 < half; i0 += 32) {        // half may be 8 or 16: then lanes past it repeat pairs
-    const int i = (i0 + lane) % half, g = i / VE, e = i % VE, j = pair_of<VE, STYLE>(g, e, gv);
+    const int i = (i0 + lane) & (half - 1), g = i / VE, e = i % VE, j = pair_of<VE, STYLE>(g, e, gv);
     const float2 v = turn_of(at, j, (float)__shfl_sync(0xffffffffu, of_axis, ld_table(&at.axis[j])), sign);
     row[turn_at<VE>(g, e, gv)] = v.x;
     row[turn_at<VE>(g, e + VE, gv)] = v.y;
@@ -216,9 +219,9 @@ template <typename T, int STYLE>
 __device__ void rotate_queries(const AppendArgs& a, const AxisTurns& at, float* row, int64_t w, int share) {
   constexpr int VE = Vec<T>::N, kBatch = 4;
   const int lane = threadIdx.x & 31, half = a.D / 2, gv = a.D / VE / 2;
-  const int64_t t = w / share;
+  const int64_t t = w >> log2_of(share);
   if (t >= a.T) return;
-  const int first = (int)(w - t * share) * 32 + lane, step = share * 32, f = lane % gv, n = a.Hq * gv;
+  const int first = (int)(w - t * share) * 32 + lane, step = share * 32, f = lane & (gv - 1), n = a.Hq * gv;
   const uint8_t* src = a.q + t * a.q_stride;
   auto offset = [&](int i) { return (2 * i - f) * 16; };          // head i / gv, vector f
   uint4 x0[kBatch], x1[kBatch];
@@ -268,7 +271,7 @@ constexpr int kDataBytes = 32768;        // of a round's rows: keys and values o
 constexpr int kMaxUnits = 8;             // a head's keys, or its values
 
 // Rows of a round of a CTA with `heads_of` heads.
-__host__ __device__ inline int rows_of_round(int heads_of, int D, int bytes) {
+inline int rows_of_round(int heads_of, int D, int bytes) {
   const int n = kDataBytes / (2 * heads_of * D * bytes);
   return n < kMaxRows ? n : kMaxRows;
 }
@@ -276,7 +279,7 @@ __host__ __device__ inline int rows_of_round(int heads_of, int D, int bytes) {
 // STYLE -1: no rotation (a move).
 template <typename T, int STYLE, bool I8>
 __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledWriteArgs p, const __grid_constant__ AxisTurns at,
-                                                                  int group_ctas, int turns_of, int window, int heads_of, int share) {
+                                                                  int group_ctas, int turns_of, int window, int heads_of, int cap, int share) {
   constexpr int VE = Vec<T>::N;
   const AppendArgs& a = p.a;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -308,9 +311,10 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
     fence_mbar_init();
   }
   const int splits = (a.H + heads_of - 1) / heads_of;
-  const int64_t begin = cta / splits * (int64_t)window;
-  const int head0 = cta % splits * heads_of, heads = min(heads_of, a.H - head0), units = 2 * heads;
-  const int gv = a.D / VE / 2, f = tid % gv, cap = rows_of_round(heads_of, a.D, (int)sizeof(T));
+  const int of_window = cta / splits;
+  const int64_t begin = of_window * (int64_t)window;
+  const int head0 = (cta - of_window * splits) * heads_of, heads = min(heads_of, a.H - head0), units = 2 * heads;
+  const int gv = a.D / VE / 2, gv_bits = log2_of(gv), f = tid & (gv - 1);
   const int head_bytes = a.D * (int)sizeof(T), part_bytes = heads * head_bytes;   // of a row's keys, or values
   const size_t row_bytes = (size_t)a.H * a.D;    // of the cache
   float* s_turn = reinterpret_cast<float*>(smem + (size_t)2 * cap * heads_of * head_bytes);   // [rows][D]
@@ -421,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
       if constexpr (STYLE >= 0) {
         __syncthreads();
         for (int x = tid; x < cnt * half; x += kThreads) {
-          const int i = x / half, g = (x - i * half) / VE, e = x % VE, j = pair_of<VE, STYLE>(g, e, gv);
+          const int i = x >> log2_of(half), g = (x & (half - 1)) / VE, e = x % VE, j = pair_of<VE, STYLE>(g, e, gv);
           const float2 v = turn_of(at, j, (float)a.positions[(size_t)ld_table(&at.axis[j]) * a.T + s_token[i]], 1.f);
           s_turn[i * a.D + turn_at<VE>(g, e, gv)] = v.x;
           s_turn[i * a.D + turn_at<VE>(g, e + VE, gv)] = v.y;
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
       return in_time;
     };
     // A warp takes a unit, gv lanes a row of it: vectors f and f + gv of the head.
-    const int step = 32 / gv;
+    const int step = 32 >> gv_bits;
     auto unit_rows = [&](int unit, int cnt) {
       return smem + (size_t)(unit < heads ? 0 : cnt) * part_bytes + (unit < heads ? unit : unit - heads) * head_bytes + f * 16;
     };
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
         const uint8_t* rows = unit_rows(unit, cnt);
         const bool key = unit < heads;
         const bool turned = STYLE >= 0 && key;
-        const int first = lane / gv;
+        const int first = lane >> gv_bits;
         float most = 0.f;                        // of rotated elements
         uint32_t bits = 0;                       // of elements as they came
         bool odd = false;
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
         bool odd = false;
         float r = 0.f;
         uint8_t* block = nullptr;
-        for (int i = lane / gv; i < cnt; i += step) {
+        for (int i = lane >> gv_bits; i < cnt; i += step) {
           const int row = s_row[i], g = s_of[i];
           if (row < 0) continue;
           if (g != group) {
@@ -622,8 +626,8 @@ __global__ void __launch_bounds__(kReadThreads) scaled_read_kernel(const ScaledR
                                                                    int share) {
   constexpr int VE = Vec<T>::N;
   extern __shared__ __align__(16) float s_turn[];   // [warps][D]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = a.D / 2, gv = a.D / VE / 2, f = lane % gv;
-  const int64_t w = (int64_t)blockIdx.x * (kReadThreads / 32) + warp, t = w / share;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = a.D / 2, gv = a.D / VE / 2, gv_bits = log2_of(gv), f = lane & (gv - 1);
+  const int64_t w = (int64_t)blockIdx.x * (kReadThreads / 32) + warp, t = w >> log2_of(share);
   pdl_wait();
   pdl_trigger();
   if (t >= a.T) return;
@@ -678,7 +682,7 @@ __global__ void __launch_bounds__(kReadThreads) scaled_read_kernel(const ScaledR
         if (i < n) {
           c0[u] = load_codes(codes + (2 * i - f) * VE);
           c1[u] = load_codes(codes + (2 * i - f) * VE + gv * VE);
-          s[u] = scales[i / gv];
+          s[u] = scales[i >> gv_bits];
         }
       }
 #pragma unroll
@@ -726,13 +730,13 @@ cudaError_t launch_write_t(const ScaledWriteArgs& p, const AxisTurns& turns, con
   // Queries' CTAs wait for memory and groups' for their steps: where not all fit at once they take turns (8000 tokens 41.3 us
   // with the groups' first, 37.6 in turn; 100 tokens 5.7 and 6.1).
   const int turns_of = group_ctas + q_ctas > at_once ? (int)std::min(group_ctas, q_ctas) : 0;
-  const size_t rows = rows_of_round(heads_of, a.D, (int)sizeof(T));
-  const size_t smem = rows * (2 * heads_of * (a.D * sizeof(T) + sizeof(float)) + (STYLE >= 0 ? a.D * sizeof(float) : 0));
+  const int rows = rows_of_round(heads_of, a.D, (int)sizeof(T));
+  const size_t smem = (size_t)rows * (2 * heads_of * (a.D * sizeof(T) + sizeof(float)) + (STYLE >= 0 ? a.D * sizeof(float) : 0));
   const size_t queries = STYLE >= 0 ? (size_t)kWarps * a.D * sizeof(float) : 0;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(&scaled_write_kernel<T, STYLE, I8>), std::max(smem, queries));
   if (e != cudaSuccess) return e;
   return launch_ex(scaled_write_kernel<T, STYLE, I8>, dim3((unsigned)(group_ctas + q_ctas)), dim3(kThreads),
-                   std::max(smem, queries), cfg.stream, cfg.pdl, p, turns, (int)group_ctas, turns_of, window, heads_of, share);
+                   std::max(smem, queries), cfg.stream, cfg.pdl, p, turns, (int)group_ctas, turns_of, window, heads_of, rows, share);
 }
 
 template <typename T, bool I8>
