@@ -25,12 +25,12 @@
 // Bringing a piece of a CTA's heads while the one before is quantised, 16 KB each,
 // took 40 and 68 us: more steps for each byte.
 //
-// Measured: 8000 tokens, 32 + 8 heads of 128, bf16 to INT8, 183 MB: 37 us = 4.9
-// TB/s, 72 % of a plain copy (the queries alone 26); 44,000 moved tokens, 8 heads,
+// Measured: 8000 tokens, 32 + 8 heads of 128, bf16 to INT8, 183 MB: 36.6 us = 5.0
+// TB/s, 73 % of a plain copy (the queries alone 26); 44,000 moved tokens, 8 heads,
 // bf16 to E4M3 in blocks of 32, 271 MB: 63 us = 4.3 TB/s, blocks of 16 62 us; 1276
-// tokens moved 6.9 us; 1000 requests' single tokens 11.3 us; one token 5.0 us, the
-// latency of its steps.  Reading 36,000 tokens back (E4M3 to bf16, 223 MB) 40 us =
-// 5.5 TB/s; 700 tokens with their keys turned back 3.9 us.
+// tokens moved 6.9 us; 1000 requests' single tokens 11.3 us; one token 4.7 us, the
+// latency of its steps.  Reading 36,000 tokens back (E4M3 to bf16, 223 MB) 35.7 us
+// = 6.3 TB/s, 92 % of a copy; 700 tokens with their keys turned back 3.4 us.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -617,8 +617,10 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
 
 // ---- reading back -----------------------------------------------------------------------
 
-constexpr int kReadThreads = 256;
-constexpr int kReadBatch = 4;
+// Pairs of vectors that a lane has on their way at once, and small CTAs: more of them leave room for other warps' instead
+// (36,000 tokens 35.7 us; pairs by four 37.5, with 256 threads 38.7, by eight 46).
+constexpr int kReadThreads = 64;
+constexpr int kReadBatch = 2;
 
 // A warp to a token: items are pairs of vectors, keys' then values'.
 template <typename T, int STYLE, bool I8>
