@@ -25,10 +25,10 @@
 // Bringing a piece of a CTA's heads while the one before is quantised, 16 KB each,
 // took 40 and 68 us: more steps for each byte.
 //
-// Measured: 8000 tokens, 32 + 8 heads of 128, bf16 to INT8, 183 MB: 36.6 us = 5.0
+// Measured: 8000 tokens, 32 + 8 heads of 128, bf16 to INT8, 183 MB: 36.4 us = 5.0
 // TB/s, 73 % of a plain copy (the queries alone 26); 44,000 moved tokens, 8 heads,
 // bf16 to E4M3 in blocks of 32, 271 MB: 63 us = 4.3 TB/s, blocks of 16 62 us; 1276
-// tokens moved 6.9 us; 1000 requests' single tokens 11.3 us; one token 4.7 us, the
+// tokens moved 6.7 us; 1000 requests' single tokens 11.3 us; one token 4.7 us, the
 // latency of its steps.  Reading 36,000 tokens back (E4M3 to bf16, 223 MB) 35.7 us
 // = 6.3 TB/s, 92 % of a copy; 700 tokens with their keys turned back 3.4 us.
 #include <algorithm>
@@ -435,8 +435,9 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
       if (!in_time && tid == 0) latch(a.status, IS_ST_TIMEOUT);
       return in_time;
     };
-    // A warp takes a unit, gv lanes a row of it: vectors f and f + gv of the head.
-    const int step = 32 >> gv_bits;
+    // A warp takes a unit, or two warps where there are two, and gv lanes a row of it: vectors f and f + gv of the head.
+    const int sharers = units == 2 ? kWarps / 2 : 1, part = warp & (sharers - 1);
+    const int rows_of_warp = 32 >> gv_bits, first_row = part * rows_of_warp + (lane >> gv_bits), step = rows_of_warp * sharers;
     auto unit_rows = [&](int unit, int cnt) {
       return smem + (size_t)(unit < heads ? 0 : cnt) * part_bytes + (unit < heads ? unit : unit - heads) * head_bytes + f * 16;
     };
@@ -451,11 +452,10 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
     // The largest finite magnitude of a unit's rows of one group, or of each of its rows; negative if some element is not
     // finite.
     auto find_most = [&](int cnt, bool by_row) {
-      for (int unit = warp; unit < units; unit += kWarps) {
+      for (int unit = warp / sharers; unit < units; unit += kWarps / sharers) {
         const uint8_t* rows = unit_rows(unit, cnt);
         const bool key = unit < heads;
         const bool turned = STYLE >= 0 && key;
-        const int first = lane >> gv_bits;
         float most = 0.f;                        // of rotated elements
         uint32_t bits = 0;                       // of elements as they came
         bool odd = false;
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
           return m;
         };
         for (int i0 = 0; i0 < cnt; i0 += step) {
-          const int i = i0 + first;
+          const int i = i0 + first_row;
           if (i < cnt && s_row[i] >= 0) {
             const uint4 x0 = *reinterpret_cast<const uint4*>(rows + (size_t)i * part_bytes);
             const uint4 z0 = *reinterpret_cast<const uint4*>(rows + (size_t)i * part_bytes + gv * 16);
@@ -504,15 +504,15 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
           }
         }
         if (!by_row) {
-          const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(flush(first, cnt))));
+          const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(flush(first_row, cnt))));
           odd = __any_sync(0xffffffffu, odd);
-          if (lane == 0) s_most[unit * cap] = signed_most(m, odd);
+          if (lane == 0) s_most[unit * cap + part] = signed_most(m, odd);
         }
       }
       __syncthreads();
     };
     auto store = [&](int cnt) {
-      for (int unit = warp; unit < units; unit += kWarps) {
+      for (int unit = warp / sharers; unit < units; unit += kWarps / sharers) {
         const uint8_t* rows = unit_rows(unit, cnt);
         const bool key = unit < heads;
         uint8_t* to = a.k_cache + (key ? 0 : a.v_offset) + (size_t)(head0 + (key ? unit : unit - heads)) * a.D + f * VE;
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
         bool odd = false;
         float r = 0.f;
         uint8_t* block = nullptr;
-        for (int i = lane >> gv_bits; i < cnt; i += step) {
+        for (int i = first_row; i < cnt; i += step) {
           const int row = s_row[i], g = s_of[i];
           if (row < 0) continue;
           if (g != group) {
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
     bool odd = false;
     auto gather = [&](bool by_row) {
       if (!settles) return;
-      const int first = by_row ? s_group[my_group].row0 : 0, n = by_row ? (int)s_group[my_group].n : 1;
+      const int first = by_row ? s_group[my_group].row0 : 0, n = by_row ? (int)s_group[my_group].n : sharers;
       for (int i = first; i < first + n; ++i) {
         const float x = s_most[my_unit * cap + i];
         most = fmaxf(most, fabsf(x));
@@ -722,6 +722,12 @@ cudaError_t launch_write_t(const ScaledWriteArgs& p, const AxisTurns& turns, con
   // 15.3 (1000 single tokens 10.6 -> 11.3).
   const int64_t windows = ((int64_t)a.T + window - 1) / window, at_once = 5LL * cfg.num_sms;
   while (heads_of > 2 && windows * ((a.H + heads_of / 2 - 1) / (heads_of / 2)) <= at_once) heads_of /= 2;
+  // One head where two heads' rows of a block do not fit a round, CTAs have several tokens and no more than two times as many
+  // CTAs (most of which have no group then): 1276 tokens moved into blocks of 64 15.2 -> 9.7 us (8000 tokens would take 64,
+  // not 56, and 100 single ones 6.2, not 5.4).
+  if (heads_of == 2 && window > 1 && windows * a.H <= 2 * at_once &&
+      rows_of_round(2, a.D, (int)sizeof(T)) < std::min(p.block_size, kMaxRows))
+    heads_of = 1;
   const int64_t group_ctas = windows * ((a.H + heads_of - 1) / heads_of);
   // Warps to a token's queries: as many as keep a lane one batch busy while the SMs have room for 32 warps each.
   const int64_t items = (int64_t)a.Hq * (a.D / VE / 2);
