@@ -352,7 +352,8 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
 
 // Scaled cache: what eight keys of a block share is K scale, log2 of the V scale
 // and 1 / V scale.  A row's factor to their logits stays finite, so that 0 times
-// it is 0; sc > 0.
+// it is 0, and at the smallest normal number or above, so that a hidden logit, -inf,
+// times it is -inf (sc > 0; a smaller factor makes every weight 1 in any case).
 constexpr int kGroup = 8, kGroups = kKeys / kGroup;
 // A tile of keys as its loaders need it.  The tiles of a CTA's run follow one
 // another here whatever their segments, so that a tile's codes are on their way
@@ -364,7 +365,7 @@ struct TileInfo {
   int32_t rows;          // query rows of the segment that it begins, 0: goes on with one; -1: the run has ended
   int32_t row0, head;    // of that segment
 };
-__device__ __forceinline__ float group_factor(float sc, float ks) { return fminf(sc * ks, FLT_MAX); }
+__device__ __forceinline__ float group_factor(float sc, float ks) { return fminf(fmaxf(sc * ks, FLT_MIN), FLT_MAX); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
