@@ -636,7 +636,8 @@ is_status_t is_attend_within(const is_attend_args_t* args, int64_t budget_ns, cu
  * and the device of the call's buffers.
  *
  * What is written: the tokens of a call that lie in one block are adjacent in
- * the batch (a packed batch's are).  With A the largest magnitude of their
+ * the batch (a packed batch's are), but for skipped ones, of which any number
+ * may lie between them.  Slots of one call must be distinct.  With A the largest magnitude of their
  * finite elements of a head, K or V, and qmax 127 (INT8) or 448 (E4M3), the
  * block's scale becomes fp32(A / qmax), at least 2^-40 and at most 2^40; unless
  * row 0 of the block is among the tokens' rows, the rows below the lowest of

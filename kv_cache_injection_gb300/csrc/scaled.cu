@@ -3,7 +3,8 @@
 // and values apart.
 //
 // The rows that a call puts into one block share one scale per head, so the unit
-// of work is a group: the adjacent tokens of one block.  With A the largest
+// of work is a group: the tokens of one block, between which others may lie that
+// have no slot.  With A the largest
 // finite magnitude of a head's new elements (keys rotated in fp32) and qmax 127
 // or 448,
 //   s = A / qmax, in [2^-40, 2^40]; beside earlier rows no smaller than their scale;
@@ -265,6 +266,7 @@ struct Group {
   int32_t live;          // some token is not skipped
 };
 constexpr int kWindow = 30;              // tokens of a CTA, at most (a warp looks at them and a neighbour)
+constexpr int kLook = 16;                // tokens that a thread looks at at once, far from them
 constexpr int kMaxGroups = 16;           // of a round
 constexpr int kMaxRows = 128;            // of a round
 constexpr int kDataBytes = 32768;        // of a round's rows: keys and values of the CTA's heads
@@ -288,7 +290,9 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
   __shared__ uint8_t s_of[kMaxRows];             // group
   __shared__ Group s_group[kMaxGroups];
   __shared__ float s_scale[kMaxGroups * kMaxUnits], s_ratio[kMaxGroups * kMaxUnits];   // 0: no scale; 0: it did not grow
-  __shared__ int32_t s_groups;
+  __shared__ int32_t s_groups;                   // -1: the first warp asks for the nearest token with a slot
+  __shared__ int64_t s_from;
+  __shared__ int32_t s_way, s_near[kWarps];
   __shared__ uint64_t s_landed;                  // a stage's rows
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = a.D / 2;
   // The first 2 turns_of CTAs are a group's and the queries' in turn, then come what is left of the groups' and of the queries'.
@@ -319,26 +323,61 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
   const size_t row_bytes = (size_t)a.H * a.D;    // of the cache
   float* s_turn = reinterpret_cast<float*>(smem + (size_t)2 * cap * heads_of * head_bytes);   // [rows][D]
   float* s_most = s_turn + (STYLE >= 0 ? cap * a.D : 0);                                       // [units][rows]
-  auto block_at = [&](int64_t t) -> int64_t {
-    if (t < 0 || t >= a.T) return -1;
-    const int64_t slot = a.slots[t];
-    return slot < 0 || slot >= a.n_slots ? -1 : block_of_slot(slot, p.block_size, p.block_shift);
+  // The slot of a token, negative if it has none in the cache.  (A load in any case, so that several are under way at once.)
+  auto slot_at = [&](int64_t t) -> int64_t {
+    const int64_t u = min(max(t, (int64_t)0), (int64_t)a.T - 1), slot = a.slots[u];
+    return t == u && slot < a.n_slots ? slot : -1;
+  };
+  auto block_of = [&](int64_t slot) -> int64_t { return slot < 0 ? -1 : block_of_slot(slot, p.block_size, p.block_shift); };
+  // The nearest token from `from` on, one way or the other, that has a slot; -1: none.  The whole CTA looks: behind the last
+  // token of a padded batch there may be thousands without one (100 tokens of 8192 18.4 us; by a warp, 128 at a time, 64).
+  auto nearest = [&](int64_t from, int way) -> int64_t {
+    for (int64_t d0 = 0; way > 0 ? from + d0 < a.T : from - d0 >= 0; d0 += kThreads * kLook) {
+      int64_t slot[kLook];
+#pragma unroll
+      for (int u = 0; u < kLook; ++u) slot[u] = slot_at(from + way * (d0 + u * kThreads + tid));
+      int32_t near = INT32_MAX;
+#pragma unroll
+      for (int u = kLook - 1; u >= 0; --u) near = slot[u] >= 0 ? u * kThreads + tid : near;
+      near = __reduce_min_sync(0xffffffffu, near);
+      __syncthreads();                           // the last turn's have been read
+      if (lane == 0) s_near[warp] = near;
+      __syncthreads();
+      for (int w = 0; w < kWarps; ++w) near = min(near, s_near[w]);
+      if (near < INT32_MAX) return from + way * (d0 + near);
+    }
+    return -1;
   };
 
   // The groups that begin in this CTA's tokens begin .. begin + window - 1: lane i of the first warp looks at token begin -
-  // 1 + i and hands them on, so that the CTA agrees on them whatever happens to the caller's slots meanwhile.
-  int64_t mine = -1;
+  // 1 + i and hands them on, so that the CTA agrees on them whatever happens to the caller's slots meanwhile.  A token
+  // begins a group if the one before it that has a slot has it in another block.  What precedes the first leader and where
+  // the last group ends may lie further off: the 32 tokens on either side are looked at in the same trip to memory.
+  int64_t mine = -1, ahead = -1;                 // block of the lane's token; slot of token next + lane
   int32_t mine_row = 0;
-  uint32_t leaders = 0, ends = 0;
+  uint32_t present = 0, leaders = 0, starts = 0; // starts: leaders, and first tokens of groups of the next CTA
+  int ask = 0;                                   // the whole CTA has to look, backwards (-1) or forwards (1)
+  int64_t next = begin + 31, tail = 0;           // the last group, while it is open, goes on from here; its tokens so far
+  int32_t tail_low = 0;
+  bool open = false;
   if (warp == 0) {
-    const int64_t t = begin - 1 + lane;
-    mine = block_at(t);
-    if (mine >= 0) mine_row = (int32_t)max(a.slots[t] - mine * p.block_size, (int64_t)0);
-    const int64_t before = __shfl_up_sync(0xffffffffu, mine, 1);
-    const bool ours = lane >= 1 && lane <= window && t < a.T;
-    leaders = __ballot_sync(0xffffffffu, ours && mine >= 0 && mine != before);
-    ends = __ballot_sync(0xffffffffu, lane >= 1 && mine != before);
-    if (head0 == 0 && ours && mine < 0 && a.slots[t] != -1) latch(a.status, IS_ST_BLOCK_ID);
+    const int64_t t = begin - 1 + lane, slot = slot_at(t), behind = slot_at(t - 32);
+    ahead = slot_at(t + 32);
+    mine = block_of(slot);
+    mine_row = (int32_t)(slot - mine * p.block_size);
+    present = __ballot_sync(0xffffffffu, mine >= 0);
+    const uint32_t earlier = present & ((1u << lane) - 1u), of_window = ((2u << window) - 1u) & ~1u;
+    const int64_t before = __shfl_sync(0xffffffffu, mine, earlier ? 31 - __clz(earlier) : 0);
+    starts = __ballot_sync(0xffffffffu, lane >= 1 && mine >= 0 && (!earlier || mine != before));
+    if ((starts & of_window) && !(present & 1u)) {
+      const uint32_t some = __ballot_sync(0xffffffffu, behind >= 0);
+      const int64_t last = __shfl_sync(0xffffffffu, behind, some ? 31 - __clz(some) : 0);
+      if (some && block_of(last) == __shfl_sync(0xffffffffu, mine, __ffs(present) - 1)) starts &= starts - 1u;
+      if (!some && begin >= 34) ask = -1;
+    }
+    leaders = starts & of_window;
+    open = next < a.T;
+    if (head0 == 0 && ((of_window >> lane) & 1u) && t < a.T && slot < 0 && a.slots[t] != -1) latch(a.status, IS_ST_BLOCK_ID);
   }
   if (warp == 1 && lane < window && begin + lane < a.T) {   // what the rows' threads will read next
     if (p.from) prefetch(p.from + begin + lane);
@@ -347,25 +386,43 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
     }
   }
   while (true) {
-    if (warp == 0) {                             // as many groups as have room
+    if (warp == 0 && ask == 0 && open) {         // where the last group ends
+      const int first = leaders ? 31 - __clz(leaders) : 0;
+      const int64_t block = __shfl_sync(0xffffffffu, mine, first);
+      open = leaders && !(starts >> first >> 1);
+      if (open && tail == 0) {
+        tail = 32 - __clz(present) - first;
+        tail_low = lane >= first && mine >= 0 ? mine_row : p.block_size;
+      }
+      while (open && ask == 0) {
+        const int64_t b = block_of(ahead);
+        const uint32_t some = __ballot_sync(0xffffffffu, b >= 0), other = __ballot_sync(0xffffffffu, b >= 0 && b != block);
+        const uint32_t same = some & ~other & (other ? (other & -other) - 1u : ~0u);
+        if (same) tail = next + 32 - __clz(same) - (begin - 1 + first);
+        if ((same >> lane) & 1u) tail_low = min(tail_low, (int32_t)(ahead - block * p.block_size));
+        next += 32;
+        open = !other && next < a.T;
+        if (open && !some && a.T - next > 96) ask = 1;   // (for fewer the CTA's look takes as long)
+        else if (open) ahead = slot_at(next + lane);
+      }
+    }
+    if (warp == 0 && ask != 0) {
+      if (lane == 0) {
+        s_groups = -1;
+        s_from = ask < 0 ? begin - 34 : next;
+        s_way = ask;
+      }
+    } else if (warp == 0) {                      // as many groups as have room
       int64_t total = 0;
       int ng = 0;
       while (leaders && total < cap && ng < kMaxGroups) {
         const int first = __ffs(leaders) - 1;
         const int64_t block = __shfl_sync(0xffffffffu, mine, first);
-        const uint32_t after = ends & ~((2u << first) - 1u);
-        const int last = after ? __ffs(after) - 1 : 32;   // lane behind its last
-        int64_t n = last - first;
-        int32_t low = lane >= first && lane < last ? mine_row : p.block_size;
-        for (bool more = last == 32; more;) {    // on past this warp's tokens, 32 at a time
-          const int64_t t = begin - 1 + first + n + lane;
-          const bool in = block_at(t) == block;
-          const uint32_t got = __ballot_sync(0xffffffffu, in);
-          const int count = got == ~0u ? 32 : __ffs(~got) - 1;
-          if (lane < count) low = min(low, (int32_t)max(a.slots[t] - block * p.block_size, (int64_t)0));
-          n += count;
-          more = count == 32;
-        }
+        const uint32_t after = starts & ~((2u << first) - 1u);
+        const uint32_t in_group = present & ~((1u << first) - 1u) & ((after & -after) - 1u);
+        const bool on = !after && tail;          // past this warp's tokens
+        const int64_t n = on ? tail : 32 - __clz(in_group) - first;   // to its last token
+        int32_t low = on ? tail_low : (in_group >> lane) & 1u ? mine_row : p.block_size;
         if (ng > 0 && total + n > cap) break;
         low = __reduce_min_sync(0xffffffffu, low);
         if (lane == 0) s_group[ng] = {block, begin - 1 + first, n, (int32_t)total, low, 0};
@@ -378,6 +435,23 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
     __syncthreads();
     const int ng = s_groups;
     if (ng == 0) return;
+    if (ng < 0) {
+      const int64_t found = nearest(s_from, s_way);
+      if (warp == 0) {
+        const int64_t slot = found < 0 ? -1 : slot_at(found + (ask > 0 ? lane : 0));
+        if (ask > 0) {
+          open = found >= 0;
+          next = found;
+          ahead = slot;
+        } else if (slot >= 0 && block_of(slot) == __shfl_sync(0xffffffffu, mine, __ffs(present) - 1)) {
+          starts &= starts - 1u;
+          leaders &= leaders - 1u;
+        }
+        ask = 0;
+      }
+      __syncthreads();                           // the question has been read
+      continue;
+    }
     const int64_t total = s_group[ng - 1].row0 + s_group[ng - 1].n;   // past cap: one long group, which goes through twice
 
     // Rows i0 .. i0 + cnt - 1 of the round: their places, their elements and their keys' sines.  A row's keys and values are a
@@ -396,12 +470,12 @@ __global__ void __launch_bounds__(kThreads, 5) scaled_write_kernel(const ScaledW
         if (p.from) {
           from = p.from[t];
           if (from < 0 || from >= p.n_from) {
-            if (from != -1) latch(a.status, IS_ST_BLOCK_ID);
+            if (row >= 0 && from != -1) latch(a.status, IS_ST_BLOCK_ID);
             row = -1;
           }
         }
         if constexpr (STYLE >= 0) {
-          for (int x = 0; x < a.n_axes; ++x) {
+          for (int x = 0; x < a.n_axes && row >= 0; ++x) {
             const int32_t pos = a.positions[(size_t)x * a.T + t];
             if (pos < 0 || pos >= IS_MAX_POSITION) {
               latch(a.status, IS_ST_POSITION);

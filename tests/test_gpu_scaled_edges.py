@@ -68,3 +68,90 @@ def test_zero_keys_under_the_smallest_factor(dtype, cache, D, bs, window, scale,
         o, ls, spread, heft, seen = ref.attend(q[rng].double(), n, k, v, torch.ones(n, dtype=torch.bool), scale, window)
         tol, ltol = sref.attend_tolerance(dtype, D, o, ls, spread, heft, seen, scales[1, b], sref.QMAX[cache])
         assert bool(((out[rng].cpu().double() - o).abs() <= tol).all()) and bool(((lse[rng].cpu().double() - ls).abs() <= ltol).all())
+
+
+# ---------------------------------------------------------------- tokens left out inside a block
+
+def with_holes(n, holes, pad, g):
+    """Where n tokens come to lie when holes[i] skipped ones follow token i, and the length with `pad` in front."""
+    at, t = [], pad
+    for i in range(n):
+        at.append(t)
+        t += 1 + holes.get(i, 0)
+    return torch.tensor(at), t
+
+
+def cache_of(cache, nb, bs, H, D, g):
+    codes, scales = sref.quantised(cache, torch.randn(2, nb, bs, H, D, generator=g).double() * 0.5)
+    return codes.to(DEV), scales.to(DEV)
+
+
+HOLES = [{2: 1}, {0: 29}, {0: 30}, {0: 31}, {5: 32}, {3: 95}, {3: 127}, {3: 128}, {3: 129}, {7: 700}, {i: 1 for i in range(60)},
+         {i: (i * 7) % 5 for i in range(60)}, {i: 40 for i in range(0, 60, 3)}, {59: 300}, {10: 3, 11: 33, 12: 130, 40: 600}]
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("bs", [1, 7, 16, 64, 1000])
+@pytest.mark.parametrize("pad", [0, 1, 40, 500])
+def test_skipped_tokens_between_those_of_a_block(cache, bs, pad):
+    """However many tokens without a slot, or with a slot outside the cache, lie between a block's tokens, the call writes
+    what it writes without them."""
+    g = torch.Generator().manual_seed(bs + pad)
+    H, Hq, D, n, nb = 3, 4, 64, 61, 64 if bs < 64 else 3
+    order = torch.randperm(nb, generator=g)
+    first = 3 if bs > 3 else 0                           # the first block holds rows already
+    p = first + torch.arange(n)
+    slots = order[p // bs] * bs + p % bs
+    x = (3 * torch.randn(n, Hq + 2 * H, D, generator=g)).to(torch.bfloat16).to(DEV)
+    rope, cd = api.make_rope(1e4), api.make_cache_desc(bs, nb, cache)
+    source = torch.randn(2, 8, 16, H, D, generator=g).to(torch.bfloat16).to(DEV)
+    from_slots = torch.randperm(128, generator=g)[:n].to(DEV)
+    c0, s0 = cache_of(cache, nb, bs, H, D, g)
+
+    def append(at, T, bad):
+        codes, scales, status = c0.clone(), s0.clone(), ints([0])
+        rows = torch.full((T, Hq + 2 * H, D), math.nan, dtype=torch.bfloat16, device=DEV)
+        where = torch.full((T,), bad, dtype=torch.int64)
+        pos = torch.full((T,), -7, dtype=torch.int32)    # what is skipped may have any position
+        rows[at.to(DEV)], where[at], pos[at] = x, slots, p.to(torch.int32)
+        q = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=DEV)
+        api.is_append_scaled(rows[:, :Hq], rows[:, Hq: Hq + H], rows[:, Hq + H:], pos.to(DEV), where.to(DEV), rope, cd, codes, scales,
+                             q, status)
+        return codes, scales, q[at.to(DEV)], status
+
+    def move(at, T, bad):
+        codes, scales, status = c0.clone(), s0.clone(), ints([0])
+        where, source_at = torch.full((T,), bad, dtype=torch.int64), torch.full((T,), 5, dtype=torch.int64, device=DEV)
+        where[at], source_at[at.to(DEV)] = slots, from_slots
+        api.is_move_scaled(api.make_cache_desc(16, 8, "bf16"), source, source_at, cd, codes, scales, where.to(DEV), status)
+        return codes, scales, status
+
+    for call in (append, move):
+        want = call(torch.arange(n), n, -1)
+        assert want[-1].tolist() == [0] and not torch.equal(want[1], s0)
+        for holes in HOLES:
+            at, T = with_holes(n, holes, pad, g)
+            for bad, bits in ((-1, 0), (nb * bs, _lib.IS_ST_BLOCK_ID), (-2, _lib.IS_ST_BLOCK_ID)):
+                got = call(at, T, bad)
+                assert got[-1].tolist() == [bits if T > n else 0]
+                assert all(torch.equal(a, b) for a, b in zip(got[:-1], want[:-1])), (call.__name__, holes, bad)
+
+
+@pytest.mark.parametrize("T,window", [(5000, 0), (9000, 64), (700, 7)])
+def test_skipped_tokens_in_long_batches(T, window):
+    """Many requests' tokens with random ones left out, several tokens a CTA."""
+    g = torch.Generator().manual_seed(T)
+    H, D, bs, nb = 4, 128, 16, T // 16 + 1
+    slots = torch.randperm(nb, generator=g).repeat_interleave(bs)[:T] * bs + torch.arange(T) % bs
+    keep = torch.rand(T, generator=g) < 0.6
+    if window:
+        keep &= (torch.arange(T) // window) % 3 != 1     # whole stretches too
+    source = torch.randn(2, nb, bs, H, D, generator=g).to(torch.bfloat16).to(DEV)
+    c0, s0 = cache_of("int8", nb, bs, H, D, g)
+    cd, fd, got = api.make_cache_desc(bs, nb, "int8"), api.make_cache_desc(bs, nb, "bf16"), []
+    for at, from_slots in ((torch.where(keep, slots, -1), torch.arange(T)), (slots[keep], torch.arange(T)[keep])):
+        codes, scales, status = c0.clone(), s0.clone(), ints([0])
+        api.is_move_scaled(fd, source, from_slots.to(DEV), cd, codes, scales, at.to(DEV), status)
+        assert status.tolist() == [0]
+        got.append((codes, scales))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
