@@ -645,7 +645,8 @@ is_status_t is_attend_within(const is_attend_args_t* args, int64_t budget_ns, cu
  * it grows, those rows' codes become round(code * fp32(old / new)).  The new
  * codes are round(y * fp32(1 / scale)), to nearest even and saturated; y is the
  * key rotated in fp32 or the raw value.  Infinities saturate; NaN is 0 in INT8 and NaN
- * in E4M3.  Rows behind the tokens' are left as they are and mean nothing.  A
+ * in E4M3.  Rows of the block above the lowest of the tokens' that are not among them
+ * are left as they are and mean nothing.  A
  * block whose earlier rows count but whose scale is out of range keeps its
  * codes, and the tokens' K or V of that head are not written (IS_ST_SCALE).
  * A call waits at most 2 s for its copies of rows, then leaves tokens out
@@ -659,7 +660,9 @@ is_status_t is_append_scaled(const is_append_args_t* args, float* scales, cudaSt
 /* is_move_scaled: tokens of one layer of a plain cache (what is_inject wrote, for
  * instance: a segment's keys are rotated already) into a scaled one, from slot
  * from_slots[i] to slot slot_mapping[i].  A token with -1 in either is skipped;
- * so is, with IS_ST_BLOCK_ID, one with any other slot outside its cache. */
+ * so is, with IS_ST_BLOCK_ID, one with any other slot outside its cache.  What is
+ * skipped is as if it were not in the call: its slot is none of the tokens' rows, and a
+ * row that the block holds there below them keeps its meaning. */
 typedef struct {
   int32_t num_tokens;          /* >= 0 */
   int32_t num_kv_heads;

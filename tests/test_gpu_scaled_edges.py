@@ -155,3 +155,54 @@ def test_skipped_tokens_in_long_batches(T, window):
         assert status.tolist() == [0]
         got.append((codes, scales))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("bad,bits", [(-1, 0), (64, _lib.IS_ST_BLOCK_ID), (-3, _lib.IS_ST_BLOCK_ID)])
+def test_moved_tokens_without_a_source_count_for_nothing(cache, bad, bits):
+    """A row whose token has no source is none of the call's rows: below the others it is held, and keeps its value when the
+    scale grows; as a block's row 0 it does not make the block a fresh one."""
+    g = torch.Generator().manual_seed(17)
+    H, D, bs, nb = 2, 64, 16, 4
+    source = (4 * torch.randn(2, 4, 16, H, D, generator=g)).to(torch.bfloat16).to(DEV)
+    c0, s0 = cache_of(cache, nb, bs, H, D, g)
+    cd, fd = api.make_cache_desc(bs, nb, cache), api.make_cache_desc(16, 4, "bf16")
+
+    def move(slots, from_slots, s=s0):
+        codes, scales, status = c0.clone(), s.clone(), ints([0])
+        api.is_move_scaled(fd, source, ints(from_slots, torch.int64), cd, codes, scales, ints(slots, torch.int64), status)
+        return codes, scales, status.item()
+
+    for slots, from_slots in (([5, 6], [bad, 9]), ([0, 1], [bad, 9]), ([0, 1, 2, 3], [bad, bad, bad, 9]), ([7, 6, 8], [9, bad, 3]),
+                              ([16 + 15, 33, 32, 34], [4, 5, bad, 7]), ([3] * 40 + [4], [bad] * 40 + [1]), ([0, 16, 32], [bad] * 3)):
+        live = [i for i, f in enumerate(from_slots) if f != bad]
+        got = move(slots, from_slots)
+        want = move([slots[i] for i in live], [from_slots[i] for i in live])
+        assert got[2] == bits and want[2] == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    codes, scales, _ = move([5, 6], [bad, 9])            # row 5 was held: half a step of the new scale off at most
+    assert bool((scales[:, 0] > s0[:, 0]).all())
+    was, now = (sref.numbers(cache, c[:, 0, 5].cpu()) * s[:, 0, :, None].cpu().double() for c, s in ((c0, s0), (codes, scales)))
+    half = {"int8": 0.5, "e4m3": 16.0}[cache]
+    assert bool(((was - now).abs() <= half * (1 + 2.0 ** -10) * scales[:, 0, :, None].cpu().double()).all())
+    none = s0.clone()
+    none[:, 0] = math.nan                                # row 0 is not written, so the block is not fresh: its scale is missed
+    codes, scales, status = move([0, 1], [bad, 9], none)
+    assert status == bits | _lib.IS_ST_SCALE and torch.equal(codes, c0)
+
+
+def test_random_moves_without_some_sources():
+    g = torch.Generator().manual_seed(18)
+    for T, H, D, bs in ((300, 2, 64, 16), (2000, 3, 128, 7), (6000, 4, 64, 64)):
+        nb = -(-T // bs) + 1
+        slots = torch.randperm(nb, generator=g).repeat_interleave(bs)[:T] * bs + torch.arange(T) % bs
+        keep = torch.rand(T, generator=g) < 0.7
+        source = torch.randn(2, nb, bs, H, D, generator=g).to(torch.bfloat16).to(DEV)
+        c0, s0 = cache_of("int8", nb, bs, H, D, g)
+        cd, fd, got = api.make_cache_desc(bs, nb, "int8"), api.make_cache_desc(bs, nb, "bf16"), []
+        for at, from_slots in ((slots, torch.where(keep, torch.arange(T), -1)), (slots[keep], torch.arange(T)[keep])):
+            codes, scales, status = c0.clone(), s0.clone(), ints([0])
+            api.is_move_scaled(fd, source, from_slots.to(DEV), cd, codes, scales, at.to(DEV), status)
+            assert status.tolist() == [0]
+            got.append((codes, scales))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
