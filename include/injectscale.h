@@ -649,13 +649,19 @@ is_status_t is_attend_within(const is_attend_args_t* args, int64_t budget_ns, cu
  * are left as they are and mean nothing.  A
  * block whose earlier rows count but whose scale is out of range keeps its
  * codes, and the tokens' K or V of that head are not written (IS_ST_SCALE).
- * A call waits at most 2 s for its copies of rows, then leaves tokens out
- * (IS_ST_TIMEOUT). */
+ * Each wait for copies of rows has a limit of 2 s, after which tokens are left
+ * out (IS_ST_TIMEOUT): whole blocks of them, or, of a block that gets more rows than fit
+ * shared memory, some; writing the same tokens again makes good for it. */
 
 /* is_append_scaled: is_append into a scaled cache (args->cache of IS_INT8 or
  * IS_FP8_E4M3, any args->dtype).  q_out is that of is_append.  A refused token's
  * slot, if it lies in the cache, still counts as one of the call's rows. */
 is_status_t is_append_scaled(const is_append_args_t* args, float* scales, cudaStream_t stream);
+
+/* is_append_scaled_within, is_move_scaled_within: with the limit of each wait, as
+ * is_attend_within has it (0 <= budget_ns <= 2 s; the wait that lets copies in flight
+ * land before the kernel ends keeps 2 s). */
+is_status_t is_append_scaled_within(const is_append_args_t* args, float* scales, int64_t budget_ns, cudaStream_t stream);
 
 /* is_move_scaled: tokens of one layer of a plain cache (what is_inject wrote, for
  * instance: a segment's keys are rotated already) into a scaled one, from slot
@@ -679,6 +685,7 @@ typedef struct {
   int32_t reserved[2];         /* must be 0 */
 } is_move_args_t;
 is_status_t is_move_scaled(const is_move_args_t* args, cudaStream_t stream);
+is_status_t is_move_scaled_within(const is_move_args_t* args, int64_t budget_ns, cudaStream_t stream);
 
 /* is_read_scaled: tokens of a scaled cache back as rows, elements multiplied out in
  * fp32 and rounded once.  With unrotate 1 the keys are turned back by their

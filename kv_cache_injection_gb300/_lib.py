@@ -148,7 +148,9 @@ SIGNATURES = {
     "is_attend": [POINTER(AttendArgs), c_void_p],
     "is_attend_within": [POINTER(AttendArgs), c_int64, c_void_p],
     "is_append_scaled": [POINTER(AppendArgs), c_void_p, c_void_p],
+    "is_append_scaled_within": [POINTER(AppendArgs), c_void_p, c_int64, c_void_p],
     "is_move_scaled": [POINTER(MoveArgs), c_void_p],
+    "is_move_scaled_within": [POINTER(MoveArgs), c_int64, c_void_p],
     "is_read_scaled": [POINTER(ReadArgs), c_void_p],
     "is_attend_scaled": [POINTER(AttendArgs), c_void_p, c_void_p],
     "is_attend_scaled_within": [POINTER(AttendArgs), c_void_p, c_int64, c_void_p],

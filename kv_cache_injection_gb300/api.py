@@ -513,13 +513,17 @@ def _scales(scales, cache: CacheDesc, heads: int, device):
 
 
 def prepare_append_scaled(q, k, v, positions, slot_mapping, rope: RopeParams, cache: CacheDesc, layer_cache, scales, q_out,
-                          status_out, axes: RopeAxes | None = None, stream=None):
+                          status_out, axes: RopeAxes | None = None, stream=None, budget_ns: int | None = None):
     """is_append_scaled with every argument marshalled once: as prepare_append,
     into a scaled cache (dtype "int8" or "e4m3"); scales float32
-    [2][num_blocks][heads], in and out."""
+    [2][num_blocks][heads], in and out; budget_ns: the limit of each wait
+    (is_append_scaled_within)."""
     args, dev, H = _append_args(q, k, v, positions, slot_mapping, rope, cache, layer_cache, q_out, status_out, axes, True)
     keep = (q, k, v, positions, slot_mapping, layer_cache, scales, q_out, status_out)
-    return _prepared("is_append_scaled", args, keep, stream, dev, _scales(scales, cache, H, dev))
+    at = _scales(scales, cache, H, dev)
+    if budget_ns is None:
+        return _prepared("is_append_scaled", args, keep, stream, dev, at)
+    return _prepared("is_append_scaled_within", args, keep, stream, dev, at, c_int64(budget_ns))
 
 
 def is_append_scaled(*args, **kw) -> None:
@@ -528,10 +532,11 @@ def is_append_scaled(*args, **kw) -> None:
 
 
 def prepare_move_scaled(from_desc: CacheDesc, from_cache, from_slots, cache: CacheDesc, layer_cache, scales, slot_mapping,
-                        status_out, stream=None):
+                        status_out, stream=None, budget_ns: int | None = None):
     """is_move_scaled with every argument marshalled once: tokens at from_slots
     (int64 [T]) of the plain layer cache from_cache, to slot_mapping (int64 [T])
-    of the scaled cache layer_cache, scales."""
+    of the scaled cache layer_cache, scales; budget_ns: the limit of each wait
+    (is_move_scaled_within)."""
     dt, code = _float_code("from_cache", from_cache)
     if from_cache.dim() != 5:
         raise ValueError("from_cache must be [2][num_blocks][block_size][heads][head_dim]")
@@ -544,7 +549,9 @@ def prepare_move_scaled(from_desc: CacheDesc, from_cache, from_slots, cache: Cac
                     _scales(scales, cache, H, dev), _ptr(_typed("status_out", status_out, "int32", (1,), dev)),
                     from_desc, cache, (ctypes.c_int32 * 2)(0, 0))
     keep = (from_cache, from_slots, layer_cache, scales, slot_mapping, status_out)
-    return _prepared("is_move_scaled", args, keep, stream, dev)
+    if budget_ns is None:
+        return _prepared("is_move_scaled", args, keep, stream, dev)
+    return _prepared("is_move_scaled_within", args, keep, stream, dev, c_int64(budget_ns))
 
 
 def is_move_scaled(*args, **kw) -> None:

@@ -187,6 +187,7 @@ struct ScaledWriteArgs {
   int64_t v_scales;             // num_blocks * H
   int32_t block_size, block_shift;
   int32_t int8, rotate;
+  uint64_t wait_ns;             // limit of each wait for copies of rows
 };
 
 // is_read_scaled with its checks done.

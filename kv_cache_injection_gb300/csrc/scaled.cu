@@ -517,8 +517,12 @@ __global__ void __launch_bounds__(kThreads, kMostPerSm<STYLE>) scaled_write_kern
           s_turn[i * a.D + turn_at<VE>(g, e + VE, gv)] = v.y;
         }
       }
-      const bool in_time = __syncthreads_and(mbar_wait_bounded(landed, n_stage++ & 1u, kWaitBudgetNs));
-      if (!in_time && tid == 0) latch(a.status, IS_ST_TIMEOUT);
+      const uint32_t parity = n_stage++ & 1u;
+      const bool in_time = __syncthreads_and(mbar_wait_bounded(landed, parity, p.wait_ns));
+      if (!in_time && tid == 0) {
+        latch(a.status, IS_ST_TIMEOUT);
+        mbar_wait_bounded(landed, parity, kWaitBudgetNs);   // copies under way land before the shared memory is another CTA's
+      }
       return in_time;
     };
     // A warp takes a unit, or two warps where there are two, and gv lanes a row of it: vectors f and f + gv of the head.

@@ -291,11 +291,22 @@ extern "C" is_status_t is_append(const is_append_args_t* a, cudaStream_t stream)
   return launched(launch_append(p, *turns, LaunchCfg{stream, sms_of(dev), true}), "is_append launch");
 }
 
-extern "C" is_status_t is_append_scaled(const is_append_args_t* a, float* scales, cudaStream_t stream) {
+static is_status_t check_budget(int64_t budget_ns) {
+  if (budget_ns < 0 || budget_ns > (int64_t)kWaitBudgetNs)
+    return refuse(IS_ERR_INVALID_ARG, "budget_ns must be in [0, %llu]", (unsigned long long)kWaitBudgetNs);
+  return IS_OK;
+}
+
+extern "C" is_status_t is_append_scaled(const is_append_args_t* args, float* scales, cudaStream_t stream) {
+  return is_append_scaled_within(args, scales, (int64_t)kWaitBudgetNs, stream);
+}
+
+extern "C" is_status_t is_append_scaled_within(const is_append_args_t* a, float* scales, int64_t budget_ns, cudaStream_t stream) {
   ScaledWriteArgs w{};
   const AxisTurns* turns = nullptr;
   int dev = 0;
-  const is_status_t st = check_append(a, true, scales, &w.a, &turns, &dev);
+  is_status_t st = check_budget(budget_ns);
+  if (st == IS_OK) st = check_append(a, true, scales, &w.a, &turns, &dev);
   if (st != IS_OK || w.a.T == 0) return st;
   w.scales = scales;
   w.v_scales = (int64_t)a->cache.num_blocks * w.a.H;
@@ -303,6 +314,7 @@ extern "C" is_status_t is_append_scaled(const is_append_args_t* a, float* scales
   w.block_shift = shift_of(w.block_size);
   w.int8 = a->cache.dtype == IS_INT8;
   w.rotate = 1;
+  w.wait_ns = (uint64_t)budget_ns;
   DeviceGuard g(dev);
   return launched(launch_scaled_write(w, *turns, LaunchCfg{stream, sms_of(dev), true}), "is_append_scaled launch");
 }
@@ -318,10 +330,15 @@ static is_status_t check_rows(int T, int H, int D, int dtype) {
   return IS_OK;
 }
 
-extern "C" is_status_t is_move_scaled(const is_move_args_t* a, cudaStream_t stream) {
+extern "C" is_status_t is_move_scaled(const is_move_args_t* args, cudaStream_t stream) {
+  return is_move_scaled_within(args, (int64_t)kWaitBudgetNs, stream);
+}
+
+extern "C" is_status_t is_move_scaled_within(const is_move_args_t* a, int64_t budget_ns, cudaStream_t stream) {
   if (!a) return refuse(IS_ERR_INVALID_ARG, "args are NULL");
   const int T = a->num_tokens, H = a->num_kv_heads, D = a->head_dim;
-  is_status_t st = check_rows(T, H, D, a->dtype);
+  is_status_t st = check_budget(budget_ns);
+  if (st == IS_OK) st = check_rows(T, H, D, a->dtype);
   if (st == IS_OK && (a->reserved[0] | a->reserved[1]) != 0) st = refuse(IS_ERR_INVALID_ARG, "reserved must be 0");
   if (st == IS_OK && a->from.dtype == IS_FP8_E4M3) st = refuse(IS_ERR_UNSUPPORTED, "from_cache must be f32, bf16 or f16");
   if (st == IS_OK) st = check_layer_cache(a->from, a->dtype, a->from_cache);
@@ -360,6 +377,7 @@ extern "C" is_status_t is_move_scaled(const is_move_args_t* a, cudaStream_t stre
   w.block_size = a->cache.block_size;
   w.block_shift = shift_of(w.block_size);
   w.int8 = a->cache.dtype == IS_INT8;
+  w.wait_ns = (uint64_t)budget_ns;
   static const AxisTurns none{};
   DeviceGuard g(dev);
   return launched(launch_scaled_write(w, none, LaunchCfg{stream, sms_of(dev), true}), "is_move_scaled launch");
@@ -420,8 +438,8 @@ extern "C" is_status_t is_read_scaled(const is_read_args_t* a, cudaStream_t stre
 // is_attend_within, or with `scaled` is_attend_scaled_within.
 static is_status_t attend(const is_attend_args_t* a, bool scaled, const float* scales, int64_t budget_ns, cudaStream_t stream) {
   if (!a) return refuse(IS_ERR_INVALID_ARG, "args are NULL");
-  if (budget_ns < 0 || budget_ns > (int64_t)kWaitBudgetNs)
-    return refuse(IS_ERR_INVALID_ARG, "budget_ns must be in [0, %llu]", (unsigned long long)kWaitBudgetNs);
+  is_status_t st = check_budget(budget_ns);
+  if (st != IS_OK) return st;
   const int R = a->num_requests, T = a->num_tokens, Hq = a->num_q_heads, H = a->num_kv_heads, D = a->head_dim;
   if (R < 1 || R > IS_MAX_REQUESTS) return refuse(IS_ERR_INVALID_ARG, "num_requests must be in [1, IS_MAX_REQUESTS]");
   if (T < 0 || a->max_q_len < 1 || a->max_blocks_per_seq < 1 || a->window < 0)
@@ -434,7 +452,7 @@ static is_status_t attend(const is_attend_args_t* a, bool scaled, const float* s
   if (D != 64 && D != 128 && D != 256) return refuse(IS_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
   if (Hq > (1 << 16) || (int64_t)T * Hq > (1 << 30))
     return refuse(IS_ERR_UNSUPPORTED, "at most 65536 heads and 2^30 rows (num_tokens * num_q_heads)");
-  is_status_t st = scaled ? check_scaled_cache(a->cache, a->layer_cache, scales) : check_layer_cache(a->cache, a->dtype, a->layer_cache);
+  st = scaled ? check_scaled_cache(a->cache, a->layer_cache, scales) : check_layer_cache(a->cache, a->dtype, a->layer_cache);
   if (st == IS_OK && scaled && a->dtype == IS_F32) st = refuse(IS_ERR_UNSUPPORTED, "a scaled cache is attended with bf16 or fp16");
   if (st != IS_OK) return st;
   if (!a->q_start && T < R) return refuse(IS_ERR_INVALID_ARG, "without q_start there is one row per request");

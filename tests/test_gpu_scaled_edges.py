@@ -206,3 +206,74 @@ def test_random_moves_without_some_sources():
             assert status.tolist() == [0]
             got.append((codes, scales))
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("dtype,cache,H,D,bs,T", [("bf16", "int8", 8, 128, 16, 3000), ("f16", "e4m3", 3, 64, 32, 900),
+                                                  ("f32", "int8", 2, 256, 8, 400), ("bf16", "e4m3", 4, 128, 16, 40)])
+def test_writes_whose_waits_run_out(dtype, cache, H, D, bs, T):
+    """With limits that it cannot keep a write ends with IS_ST_TIMEOUT: each head of a block is as it was or as the whole
+    call writes it, and writing the same tokens again gives what one call gives."""
+    g = torch.Generator().manual_seed(23)
+    nb = -(-(T + 5) // bs) + 2
+    order = torch.randperm(nb, generator=g)
+    p = 5 + torch.arange(T)                              # the first block holds rows already
+    slots = (order[p // bs] * bs + p % bs).to(DEV)
+    c0, s0 = cache_of(cache, nb, bs, H, D, g)
+    cd, fd, td = api.make_cache_desc(bs, nb, cache), api.make_cache_desc(16, nb * bs // 16 + 1, dtype), ref.TORCH[dtype]
+    x = (2 * torch.randn(T, 2 * H, D, generator=g)).to(td).to(DEV)
+    source = torch.randn(2, nb * bs // 16 + 1, 16, H, D, generator=g).to(td).to(DEV)
+    from_slots = torch.randperm(nb * bs, generator=g)[:T].to(DEV)
+
+    def append(codes, scales, status, **kw):
+        api.is_append_scaled(None, x[:, :H], x[:, H:], p.to(torch.int32).to(DEV), slots, api.make_rope(1e4), cd, codes, scales, None,
+                             status, **kw)
+
+    def move(codes, scales, status, **kw):
+        api.is_move_scaled(fd, source, from_slots, cd, codes, scales, slots, status, **kw)
+
+    def of_heads(codes, scales):                         # a row of numbers for each K or V, block and head
+        return torch.cat([codes.transpose(2, 3).reshape(2, nb, H, -1).to(torch.int64), scales.view(torch.int32)[..., None].long()], -1)
+
+    for call in (append, move):
+        status, seen = ints([0]), 0
+        want_codes, want_scales = c0.clone(), s0.clone()
+        call(want_codes, want_scales, status)
+        assert status.item() == 0
+        before, want = of_heads(c0, s0), of_heads(want_codes, want_scales)
+        for budget in (0, 0, 300, 600, 1000, 2000, 5000, 0):
+            codes, scales = c0.clone(), s0.clone()
+            torch.cuda.synchronize()
+            call(codes, scales, status, budget_ns=budget)
+            bits = status.item()
+            seen |= bits
+            got = of_heads(codes, scales)
+            written = (got == want).all(-1)
+            assert bits in (0, _lib.IS_ST_TIMEOUT) and bool((written | (got == before).all(-1)).all())
+            assert bits or bool(written.all())
+            status.zero_()
+            call(codes, scales, status)
+            assert status.item() == 0 and torch.equal(codes, want_codes) and torch.equal(scales, want_scales)
+        assert seen == _lib.IS_ST_TIMEOUT or call is append   # whose rows may land while its sines are computed
+
+
+def test_waits_of_a_long_group_that_run_out():
+    """A block that gets more rows than fit a round, whose tokens come twice: left half-way, it is as it should be after the
+    same call again."""
+    g = torch.Generator().manual_seed(24)
+    H, D, bs, T = 2, 128, 1024, 900
+    c0, s0 = cache_of("int8", 2, bs, H, D, g)
+    source = (3 * torch.randn(2, 64, 16, H, D, generator=g)).to(torch.bfloat16).to(DEV)
+    args = api.make_cache_desc(16, 64, "bf16"), source, torch.randperm(1024, generator=g)[:T].to(DEV), api.make_cache_desc(bs, 2, "int8")
+    slots, status = (bs + 40 + torch.arange(T)).to(DEV), ints([0])
+    want_codes, want_scales = c0.clone(), s0.clone()
+    api.is_move_scaled(*args, want_codes, want_scales, slots, status)
+    assert status.item() == 0
+    for budget in (0, 500, 700, 900, 1200, 1500, 2000, 3000):
+        codes, scales = c0.clone(), s0.clone()
+        api.is_move_scaled(*args, codes, scales, slots, status, budget_ns=budget)
+        assert status.item() in (0, _lib.IS_ST_TIMEOUT)
+        status.zero_()
+        api.is_move_scaled(*args, codes, scales, slots, status)
+        assert status.item() == 0 and torch.equal(codes, want_codes) and torch.equal(scales, want_scales)
