@@ -38,15 +38,13 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "scaled_plan.h"
 
 namespace isk {
 
 namespace {
 
-// 128 threads and 32 KB of rows, five CTAs an SM: the steps of a CTA wait for one another, other CTAs fill the gaps (8000
-// tokens 37 us, 51 with 256 threads and 64 KB, 45 with 128 threads and 16 KB).
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+using namespace scaled;
 
 __device__ __forceinline__ float ld_table(const float* p) {   // see ld_param in append.cu
   float x;
@@ -265,17 +263,6 @@ struct Group {
   int32_t low;           // the lowest of its rows in the block: below it the block is held already
   int32_t live;          // some token is not skipped
 };
-constexpr int kWindow = 30;              // tokens of a CTA, at most (a warp looks at them and a neighbour)
-constexpr int kMaxGroups = 16;           // of a round
-constexpr int kMaxRows = 128;            // of a round
-constexpr int kDataBytes = 32768;        // of a round's rows: keys and values of the CTA's heads
-constexpr int kMaxUnits = 8;             // a head's keys, or its values
-
-// Rows of a round of a CTA with `heads_of` heads.
-inline int rows_of_round(int heads_of, int D, int bytes) {
-  const int n = kDataBytes / (2 * heads_of * D * bytes);
-  return n < kMaxRows ? n : kMaxRows;
-}
 
 // STYLE -1: no rotation (a move).  CTAs that an SM's registers hold: 44,000 moved tokens take 62.5 us with six, 69 with five.
 template <int STYLE>
@@ -800,41 +787,13 @@ __global__ void __launch_bounds__(kReadThreads) scaled_read_kernel(const ScaledR
 
 template <typename T, int STYLE, bool I8>
 cudaError_t launch_write_t(const ScaledWriteArgs& p, const AxisTurns& turns, const LaunchCfg& cfg) {
-  constexpr int VE = Vec<T>::N;
   const AppendArgs& a = p.a;
-  // Heads of a CTA: 4, 2 where a block's rows would not fit a round otherwise.
-  int heads_of = kMaxUnits / 2;
-  while (heads_of > 2 && rows_of_round(heads_of, a.D, (int)sizeof(T)) < std::min(p.block_size, kMaxRows)) heads_of /= 2;
-  // Tokens of a CTA: one while every SM gets one, then up to 16 or a block.  Most tokens of a prompt begin no group, and CTAs
-  // that end at once still hold up the others (8000 tokens with one a CTA: 74.6 us).
-  const int window = (int)std::min<int64_t>(std::min(kWindow, std::max(16, p.block_size)), std::max<int64_t>(1, a.T / cfg.num_sms));
-  // Two heads too while all CTAs fit at once: one token 5.5 -> 5.0 us, 1276 moved tokens 7.9 -> 6.9, a prompt of 1600 16.9 ->
-  // 15.3 (1000 single tokens 10.6 -> 11.3).
-  const int64_t windows = ((int64_t)a.T + window - 1) / window, at_once = 5LL * cfg.num_sms;
-  while (heads_of > 2 && windows * ((a.H + heads_of / 2 - 1) / (heads_of / 2)) <= at_once) heads_of /= 2;
-  // One head where two heads' rows of a block do not fit a round, CTAs have several tokens and no more than two times as many
-  // CTAs (most of which have no group then): 1276 tokens moved into blocks of 64 15.2 -> 9.7 us (8000 tokens would take 64,
-  // not 56, and 100 single ones 6.2, not 5.4).
-  if (heads_of == 2 && window > 1 && windows * a.H <= 2 * at_once &&
-      rows_of_round(2, a.D, (int)sizeof(T)) < std::min(p.block_size, kMaxRows))
-    heads_of = 1;
-  const int64_t group_ctas = windows * ((a.H + heads_of - 1) / heads_of);
-  // Warps to a token's queries: as many as keep a lane one batch busy while the SMs have room for 32 warps each.
-  const int64_t items = (int64_t)a.Hq * (a.D / VE / 2);
-  int share = 1;
-  while (share < 16 && (int64_t)a.T * share < 32LL * cfg.num_sms && (int64_t)share * 32 < items) share *= 2;
-  const int64_t q_ctas = a.Hq > 0 ? ((int64_t)a.T * share + kWarps - 1) / kWarps : 0;
-  if (group_ctas + q_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  // Queries' CTAs wait for memory and groups' for their steps: where not all fit at once they take turns (8000 tokens 41.3 us
-  // with the groups' first, 37.6 in turn; 100 tokens 5.7 and 6.1).
-  const int turns_of = group_ctas + q_ctas > at_once ? (int)std::min(group_ctas, q_ctas) : 0;
-  const int rows = rows_of_round(heads_of, a.D, (int)sizeof(T));
-  const size_t smem = (size_t)rows * (2 * heads_of * (a.D * sizeof(T) + sizeof(float)) + (STYLE >= 0 ? a.D * sizeof(float) : 0));
-  const size_t queries = STYLE >= 0 ? (size_t)kWarps * a.D * sizeof(float) : 0;
-  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(&scaled_write_kernel<T, STYLE, I8>), std::max(smem, queries));
+  const WritePlan w = plan_write(a.T, a.Hq, a.H, a.D, (int)sizeof(T), p.block_size, cfg.num_sms, STYLE >= 0);
+  if (w.group_ctas + w.query_ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(&scaled_write_kernel<T, STYLE, I8>), w.smem);
   if (e != cudaSuccess) return e;
-  return launch_ex(scaled_write_kernel<T, STYLE, I8>, dim3((unsigned)(group_ctas + q_ctas)), dim3(kThreads),
-                   std::max(smem, queries), cfg.stream, cfg.pdl, p, turns, (int)group_ctas, turns_of, window, heads_of, rows, share);
+  return launch_ex(scaled_write_kernel<T, STYLE, I8>, dim3((unsigned)(w.group_ctas + w.query_ctas)), dim3(kThreads), w.smem,
+                   cfg.stream, cfg.pdl, p, turns, (int)w.group_ctas, (int)w.turns, w.window, w.heads_of, w.rows, w.share);
 }
 
 template <typename T, bool I8>

@@ -44,16 +44,28 @@ is_status_t device_of(const void* p, const char* name, int* dev) {
   return IS_OK;
 }
 
-int sms_of(int dev) {
+// The SMs of a device, asked for once each.
+is_status_t sms_of(int dev, int* n) {
   static std::mutex mu;
   static int sms[64];
-  if (dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
-  if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    sms[dev] = 0;
-  }
-  return sms[dev];
+  const bool kept = dev >= 0 && dev < 64;
+  *n = kept ? sms[dev] : 0;
+  if (*n > 0) return IS_OK;
+  const cudaError_t e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return launched(e, "cudaDeviceGetAttribute");
+  if (kept) sms[dev] = *n;
+  return IS_OK;
+}
+
+// The launch of a call on its buffers' device.
+template <typename F>
+is_status_t launch_on(int dev, cudaStream_t stream, const char* what, F launch) {
+  int sms = 0;
+  const is_status_t st = sms_of(dev, &sms);
+  if (st != IS_OK) return st;
+  DeviceGuard g(dev);
+  return launched(launch(LaunchCfg{stream, sms, true}), what);
 }
 
 struct Span {
@@ -200,8 +212,7 @@ extern "C" is_status_t is_extend_block_table(const is_extend_args_t* a, cudaStre
   int dev = 0;
   st = device_of(a->slot_mapping_out, "slot_mapping_out", &dev);
   if (st != IS_OK) return st;
-  DeviceGuard g(dev);
-  return launched(launch_extend(*a, LaunchCfg{stream, sms_of(dev), true}), "is_extend_block_table launch");
+  return launch_on(dev, stream, "is_extend_block_table launch", [&](const LaunchCfg& cfg) { return launch_extend(*a, cfg); });
 }
 
 // The checks of is_append, or with `scaled` of is_append_scaled; *p is filled
@@ -287,8 +298,7 @@ extern "C" is_status_t is_append(const is_append_args_t* a, cudaStream_t stream)
   int dev = 0;
   const is_status_t st = check_append(a, false, nullptr, &p, &turns, &dev);
   if (st != IS_OK || p.T == 0) return st;
-  DeviceGuard g(dev);
-  return launched(launch_append(p, *turns, LaunchCfg{stream, sms_of(dev), true}), "is_append launch");
+  return launch_on(dev, stream, "is_append launch", [&](const LaunchCfg& cfg) { return launch_append(p, *turns, cfg); });
 }
 
 static is_status_t check_budget(int64_t budget_ns) {
@@ -315,8 +325,7 @@ extern "C" is_status_t is_append_scaled_within(const is_append_args_t* a, float*
   w.int8 = a->cache.dtype == IS_INT8;
   w.rotate = 1;
   w.wait_ns = (uint64_t)budget_ns;
-  DeviceGuard g(dev);
-  return launched(launch_scaled_write(w, *turns, LaunchCfg{stream, sms_of(dev), true}), "is_append_scaled launch");
+  return launch_on(dev, stream, "is_append_scaled launch", [&](const LaunchCfg& cfg) { return launch_scaled_write(w, *turns, cfg); });
 }
 
 // Tokens, heads and head_dim of a call that moves or reads rows of a scaled cache.
@@ -379,8 +388,7 @@ extern "C" is_status_t is_move_scaled_within(const is_move_args_t* a, int64_t bu
   w.int8 = a->cache.dtype == IS_INT8;
   w.wait_ns = (uint64_t)budget_ns;
   static const AxisTurns none{};
-  DeviceGuard g(dev);
-  return launched(launch_scaled_write(w, none, LaunchCfg{stream, sms_of(dev), true}), "is_move_scaled launch");
+  return launch_on(dev, stream, "is_move_scaled launch", [&](const LaunchCfg& cfg) { return launch_scaled_write(w, none, cfg); });
 }
 
 extern "C" is_status_t is_read_scaled(const is_read_args_t* a, cudaStream_t stream) {
@@ -431,8 +439,7 @@ extern "C" is_status_t is_read_scaled(const is_read_args_t* a, cudaStream_t stre
   r.int8 = a->cache.dtype == IS_INT8;
   r.block_size = a->cache.block_size;
   r.block_shift = shift_of(r.block_size);
-  DeviceGuard g(dev);
-  return launched(launch_scaled_read(r, *turns, LaunchCfg{stream, sms_of(dev), true}), "is_read_scaled launch");
+  return launch_on(dev, stream, "is_read_scaled launch", [&](const LaunchCfg& cfg) { return launch_scaled_read(r, *turns, cfg); });
 }
 
 // is_attend_within, or with `scaled` is_attend_scaled_within.
@@ -514,10 +521,9 @@ static is_status_t attend(const is_attend_args_t* a, bool scaled, const float* s
   p.v_scale = p.fp8 ? a->cache.v_scale : 1.f;
   p.wait_ns = (uint64_t)budget_ns;
   p.scales = scales;
-  DeviceGuard g(dev);
-  const LaunchCfg cfg{stream, sms_of(dev), true};
-  if (scaled) return launched(launch_attend_scaled(p, a->cache.dtype == IS_INT8, cfg), "is_attend_scaled launch");
-  return launched(launch_attend(p, cfg), "is_attend launch");
+  return launch_on(dev, stream, scaled ? "is_attend_scaled launch" : "is_attend launch", [&](const LaunchCfg& cfg) {
+    return scaled ? launch_attend_scaled(p, a->cache.dtype == IS_INT8, cfg) : launch_attend(p, cfg);
+  });
 }
 
 extern "C" is_status_t is_attend(const is_attend_args_t* args, cudaStream_t stream) {
