@@ -264,12 +264,9 @@ struct Group {
   int32_t live;          // some token is not skipped
 };
 
-// STYLE -1: no rotation (a move).  CTAs that an SM's registers hold: 44,000 moved tokens take 62.5 us with six, 69 with five.
-template <int STYLE>
-constexpr int kMostPerSm = STYLE < 0 ? 6 : 5;
-
+// STYLE -1: no rotation (a move).  (44,000 moved tokens take 62.5 us with six CTAs an SM, 69 with five.)
 template <typename T, int STYLE, bool I8>
-__global__ void __launch_bounds__(kThreads, kMostPerSm<STYLE>) scaled_write_kernel(const ScaledWriteArgs p, const __grid_constant__ AxisTurns at,
+__global__ void __launch_bounds__(kThreads, most_per_sm(STYLE >= 0)) scaled_write_kernel(const ScaledWriteArgs p, const __grid_constant__ AxisTurns at,
                                                                   int group_ctas, int turns_of, int window, int heads_of, int cap, int share) {
   constexpr int VE = Vec<T>::N;
   const AppendArgs& a = p.a;

@@ -60,3 +60,34 @@ def test_every_plan_covers_the_call(plan, bs, rotate):
                 need = w["rows"] * (2 * w["heads_of"] * (D * b + 4) + (4 * D if rotate else 0))
                 assert w["rows"] * 2 * w["heads_of"] * D * b <= 32768 and w["smem"] >= max(need, 16 * D if rotate else 0)
                 assert w["smem"] + 4096 <= 227 * 1024
+
+
+def places(heads_of, D, bytes, rotate, sms=152):
+    """CTAs that 228 KB of shared memory an SM and 64 K registers hold: 92 and 76 registers a thread come in eights."""
+    rows = min(128, 32768 // (2 * heads_of * D * bytes))
+    smem = max(rows * (2 * heads_of * (D * bytes + 4) + (4 * D if rotate else 0)), 16 * D if rotate else 0)
+    return sms * min(65536 // (128 * (96 if rotate else 80)), 228 * 1024 // (smem + 4096))
+
+
+@pytest.mark.parametrize("Hq,H,D", [(32, 8, 128), (28, 4, 128), (8, 8, 64), (8, 4, 256), (0, 8, 128)])
+def test_few_heads_only_where_their_ctas_fit(plan, Hq, H, D):
+    """Two heads a CTA where all CTAs fit at once, the queries' beside them, or the groups' take two thirds of the places."""
+    for rotate in (True, False):
+        for T in list(range(1, 400, 7)) + LENGTHS:
+            for bs in (8, 16):
+                w = plan(T, Hq if rotate else 0, H, D, bs=bs, rotate=rotate)
+                assert w["heads_of"] in ((2, 4) if D * 2 * 4 * bs * 2 <= 32768 else (2,))
+                if w["heads_of"] == 2 and D * 2 * 4 * bs * 2 <= 32768:
+                    most = places(2, D, 2, rotate)
+                    assert w["group_ctas"] <= most
+                    assert w["group_ctas"] + w["query_ctas"] <= 5 * 152 or w["query_ctas"] == 0 or 3 * w["group_ctas"] <= 2 * most
+            w = plan(T, Hq if rotate else 0, H, D, bs=64, rotate=rotate)
+            if w["heads_of"] == 1:
+                assert w["window"] > 1 and w["group_ctas"] <= (10 if rotate else 12) * 152
+
+
+def test_decode_steps_keep_to_the_form_that_fits(plan):
+    """Steps of single tokens, 32 + 8 heads: with two heads a CTA 160 of them needed a second wave of CTAs."""
+    assert [plan(T, 32, 8, 128)["heads_of"] for T in (1, 100, 120, 140, 160, 190, 305, 1000)] == [2, 2, 2, 4, 4, 4, 4, 4]
+    assert [plan(T, 0, 8, 128, rotate=False)["heads_of"] for T in (1, 1276, 3000, 44000)] == [2, 2, 2, 4]
+    assert [plan(T, 32, 8, 128, bs=64)["heads_of"] for T in (100, 1276, 8000)] == [2, 1, 2]
