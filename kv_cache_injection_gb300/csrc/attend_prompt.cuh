@@ -260,6 +260,22 @@ __device__ __forceinline__ int64_t units_of_request(const AttendArgs& a, const R
   return sum * a.H;
 }
 
+// One segment (a run's share of one item) as its workers need it, handed from
+// one loader thread to all warps through a ring in shared memory: the walk costs
+// the others no registers, and the CTA agrees on its segments whatever happens
+// to the caller's arrays meanwhile.
+struct Segment {
+  int32_t tiles;         // -1: the run has ended
+  int32_t k_lo, k_hi, rows;
+  int32_t k_see;         // first key that some row of the item sees
+  int32_t r;
+  int32_t lim0;          // position of the item's first token
+  int32_t head;
+  int32_t row0;          // first query row
+  int32_t slot;          // of the partial result; -1: the item is whole
+};
+constexpr int kSegments = 4;
+
 // The segments of a CTA's run, walked by one thread.
 template <int COST>
 struct Walk {
@@ -270,7 +286,20 @@ struct Walk {
   // of the current segment
   int head, k_lo, k_hi, rows, parts;
   bool whole, begins, at_start;
+  bool crosses;                          // the run's last item began here and goes on in the next CTA
 
+  // From the first tile of request `req`, whose first unit is number `first`.
+  __device__ __forceinline__ void start(const AttendArgs& a, int per, int64_t run_, int64_t u0, int64_t u1, int req, int64_t first) {
+    run = run_;
+    u = u_first = u0;
+    u_end = u1;
+    r = req;
+    base = first;
+    t = 0;
+    q = read_request(a, r, false);
+    x = tile_of<COST>(a, q, per, 0);
+    crosses = false;
+  }
   __device__ __forceinline__ bool next(const AttendArgs& a, int per) {
     while (u < u_end) {
       // the tile that unit u lies in
@@ -305,23 +334,35 @@ struct Walk {
     return false;
   }
   __device__ __forceinline__ int tiles() const { return k_hi > k_lo ? (k_hi - k_lo + kKeys - 1) / kKeys : 0; }
+  // The next segment for its workers, and what the join has to know of an item that crosses runs.
+  __device__ __forceinline__ void next_into(const AttendArgs& a, int per, Segment& g) {
+    if (next(a, per)) {
+      g.tiles = tiles();
+      g.k_lo = k_lo;
+      g.k_hi = k_hi;
+      g.k_see = x.see;
+      g.rows = rows;
+      g.r = r;
+      g.lim0 = q.seq - q.n + x.tok0;
+      g.head = head;
+      g.row0 = q.row0 + x.tok0;
+      g.slot = whole ? -1 : 2 * blockIdx.x + (at_start ? 0 : 1);
+      crosses = begins && !whole;
+      if (crosses) {
+        JoinRecord* rec = record_of(a, blockIdx.x);
+        rec->parts = parts;
+        rec->slot0 = g.slot;
+        rec->row0 = q.row0;
+        rec->head = head;
+        rec->rho0 = x.tok0 * a.G;
+        rec->rows = rows;
+      }
+    } else {
+      g.tiles = -1;
+      if (!crosses) record_of(a, blockIdx.x)->parts = 0;
+    }
+  }
 };
-
-// One segment (a run's share of one item) as its workers need it, handed from
-// one loader thread to all warps through a ring in shared memory: the walk costs
-// the others no registers, and the CTA agrees on its segments whatever happens
-// to the caller's arrays meanwhile.
-struct Segment {
-  int32_t tiles;         // -1: the run has ended
-  int32_t k_lo, k_hi, rows;
-  int32_t k_see;         // first key that some row of the item sees
-  int32_t r;
-  int32_t lim0;          // position of the item's first token
-  int32_t head;
-  int32_t row0;          // first query row
-  int32_t slot;          // of the partial result; -1: the item is whole
-};
-constexpr int kSegments = 4;
 
 struct Bars {
   uint64_t q_full, q_empty, done, v_tail;
@@ -891,17 +932,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
       // ---- scaled cache: segments, and the tiles' blocks, masks and scales ---------
       if constexpr (kScaled) {
         Walk<kCost> w;                                 // the first lane's
-        bool crosses = false, ok = true;
-        if (lane == 0) {
-          w.run = run;
-          w.u = w.u_first = u0;
-          w.u_end = u1;
-          w.r = s_req;
-          w.base = s_base;
-          w.t = 0;
-          w.q = read_request(a, w.r, false);
-          w.x = tile_of<kCost>(a, w.q, per, 0);
-        }
+        bool ok = true;
+        if (lane == 0) w.start(a, per, run, u0, u1, s_req, s_base);
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           ok = __all_sync(0xffffffffu, ok && wait_or_abort(smem_addr(bar), parity, abort_flag, limit_ns));
           return ok;
@@ -911,33 +943,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
           const uint32_t seg = n_seg % kSegments;
           if (!wait(&bars.seg_empty[seg], ((n_seg / kSegments) & 1u) ^ 1u)) break;
           Segment& g = s_seg[seg];
-          if (lane == 0) {
-            if (w.next(a, per)) {
-              g.tiles = w.tiles();
-              g.k_lo = w.k_lo;
-              g.k_hi = w.k_hi;
-              g.k_see = w.x.see;
-              g.rows = w.rows;
-              g.r = w.r;
-              g.lim0 = w.q.seq - w.q.n + w.x.tok0;
-              g.head = w.head;
-              g.row0 = w.q.row0 + w.x.tok0;
-              g.slot = w.whole ? -1 : 2 * blockIdx.x + (w.at_start ? 0 : 1);
-              crosses = w.begins && !w.whole;
-              if (crosses) {
-                JoinRecord* rec = record_of(a, blockIdx.x);
-                rec->parts = w.parts;
-                rec->slot0 = g.slot;
-                rec->row0 = w.q.row0;
-                rec->head = w.head;
-                rec->rho0 = w.x.tok0 * a.G;
-                rec->rows = w.rows;
-              }
-            } else {
-              g.tiles = -1;
-              if (!crosses) record_of(a, blockIdx.x)->parts = 0;
-            }
-          }
+          if (lane == 0) w.next_into(a, per, g);
           __syncwarp();
           const int n_tiles = g.tiles, k_lo = g.k_lo, k_hi = g.k_hi, k_see = g.k_see, rows = g.rows, head = g.head, row_at = g.row0;
           const int32_t* table = a.block_table + (size_t)g.r * a.max_blocks;
@@ -1160,49 +1166,13 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) attend_prompt_kernel(cons
       };
       auto barrier_loaders = [] { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kLoaders) : "memory"); };
       Walk<kCost> w;                                   // the first thread's
-      bool crosses = false;                            // the run's last item began here and goes on in the next CTA
-      if (lt == 0) {
-        w.run = run;
-        w.u = w.u_first = u0;
-        w.u_end = u1;
-        w.r = s_req;
-        w.base = s_base;
-        w.t = 0;
-        w.q = read_request(a, w.r, false);
-        w.x = tile_of<kCost>(a, w.q, per, 0);
-      }
+      if (lt == 0) w.start(a, per, run, u0, u1, s_req, s_base);
       for (uint32_t n_seg = 0;; ++n_seg) {
         const uint32_t seg = n_seg % kSegments;
         ok = agreed(wait_or_abort(smem_addr(&bars.seg_empty[seg]), ((n_seg / kSegments) & 1u) ^ 1u, abort_flag, limit_ns));
         if (!ok) break;
         Segment& g = s_seg[seg];
-        if (lt == 0) {
-          if (w.next(a, per)) {
-            g.tiles = w.tiles();
-            g.k_lo = w.k_lo;
-            g.k_hi = w.k_hi;
-            g.k_see = w.x.see;
-            g.rows = w.rows;
-            g.r = w.r;
-            g.lim0 = w.q.seq - w.q.n + w.x.tok0;
-            g.head = w.head;
-            g.row0 = w.q.row0 + w.x.tok0;
-            g.slot = w.whole ? -1 : 2 * blockIdx.x + (w.at_start ? 0 : 1);
-            crosses = w.begins && !w.whole;
-            if (crosses) {
-              JoinRecord* rec = record_of(a, blockIdx.x);
-              rec->parts = w.parts;
-              rec->slot0 = g.slot;
-              rec->row0 = w.q.row0;
-              rec->head = w.head;
-              rec->rho0 = w.x.tok0 * a.G;
-              rec->rows = w.rows;
-            }
-          } else {
-            g.tiles = -1;
-            if (!crosses) record_of(a, blockIdx.x)->parts = 0;
-          }
-        }
+        if (lt == 0) w.next_into(a, per, g);
         barrier_loaders();
         const int n_tiles = g.tiles, k_lo = g.k_lo, k_hi = g.k_hi, k_see = g.k_see, rows = g.rows, head = g.head, row_at = g.row0;
         const int32_t* table = a.block_table + (size_t)g.r * a.max_blocks;

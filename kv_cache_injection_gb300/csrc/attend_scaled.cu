@@ -17,9 +17,18 @@
 namespace isk {
 
 cudaError_t launch_attend_scaled(const AttendArgs& a, bool int8, const LaunchCfg& cfg) {
-  // As over an FP8 cache (launch_attend): more than 32 rows go to the prompt
-  // kernel where its shared memory has room and the scale is positive.  It takes
-  // a block's scales once for eight keys, so blocks have to be whole eights.
+  // More than 32 rows go to the prompt kernel where its shared memory has room
+  // and the scale is positive.  It takes a block's scales once for eight keys, so
+  // blocks have to be whole eights.  Its time hardly depends on the rows, this
+  // kernel's grows with every 16 of them, and where they meet depends on the
+  // requests.  Here and there, INT8, 32 + 8 heads: 4 requests of up to 131,000
+  // tokens, 32 rows 397 and 408 us, 36 rows 577 and 409; 16 of 900-2000, 32 rows 42
+  // and 45, 36 rows 57 and 45.  Of more requests the prompt kernel is ahead from 17
+  // rows on (100 of 300-2048, 16 rows 115 and 150 us, 32 rows 217 and 150; 64 of
+  // 500-8000, 32 rows 319 and 269), of a single short one not yet at 48 (1313
+  // tokens, 16 and 20): 32 rows lie between them.  Prompts that have to stay here:
+  // two of 2000-2500 tokens behind up to 8192, 4135 us over blocks of 7 where those
+  // of 8 take 622 there; with 8 + 4 heads of 256 3014.
   if (a.D <= 128 && a.block_size % 8 == 0 && a.G <= 64 && (int64_t)a.max_q * a.G > 32 && a.scale > 0.f)
     return a.dtype == IS_BF16 ? launch_attend_prompt_scaled_bf16(a, int8, cfg) : launch_attend_prompt_scaled_f16(a, int8, cfg);
   if (a.dtype == IS_BF16)

@@ -57,8 +57,6 @@ __device__ __forceinline__ uint32_t ld_table(const uint8_t* p) {
   return x;
 }
 
-__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
-
 // Of a power of two.  (What divides here mostly is one; a division by a variable takes 20 instructions, 64 bits wide 80.)
 __device__ __forceinline__ int log2_of(int x) { return 31 - __clz(x); }
 
@@ -379,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, most_per_sm(STYLE >= 0)) scaled_writ
     }
   }
   if (warp == 1 && lane < window && begin + lane < a.T) {   // what the rows' threads will read next
-    if (p.from) prefetch(p.from + begin + lane);
+    if (p.from) prefetch_l1(p.from + begin + lane);
     if constexpr (STYLE >= 0) {
-      for (int x = 0; x < a.n_axes; ++x) prefetch(a.positions + (size_t)x * a.T + begin + lane);
+      for (int x = 0; x < a.n_axes; ++x) prefetch_l1(a.positions + (size_t)x * a.T + begin + lane);
     }
   }
   while (true) {
