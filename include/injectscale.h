@@ -637,18 +637,18 @@ is_status_t is_attend_within(const is_attend_args_t* args, int64_t budget_ns, cu
  *
  * What is written: the tokens of a call that lie in one block are adjacent in
  * the batch (a packed batch's are), but for skipped ones, of which any number
- * may lie between them.  Slots of one call must be distinct.  With A the largest magnitude of their
- * finite elements of a head, K or V, and qmax 127 (INT8) or 448 (E4M3), the
- * block's scale becomes fp32(A / qmax), at least 2^-40 and at most 2^40; unless
+ * may lie between them.  Slots of one call must be distinct.  With A the largest
+ * magnitude of their finite elements of a head, K or V, and qmax 127 (INT8) or 448
+ * (E4M3), the block's scale becomes fp32(A / qmax), at least 2^-40 and at most 2^40; unless
  * row 0 of the block is among the tokens' rows, the rows below the lowest of
  * them are held already and the scale is not made smaller than it was.  Where
  * it grows, those rows' codes become round(code * fp32(old / new)).  The new
  * codes are round(y * fp32(1 / scale)), to nearest even and saturated; y is the
  * key rotated in fp32 or the raw value.  Infinities saturate; NaN is 0 in INT8 and NaN
  * in E4M3.  Rows of the block above the lowest of the tokens' that are not among them
- * are left as they are and mean nothing.  A
- * block whose earlier rows count but whose scale is out of range keeps its
- * codes, and the tokens' K or V of that head are not written (IS_ST_SCALE).
+ * are left as they are and mean nothing.  A block whose earlier rows count but whose
+ * scale is out of range keeps its codes, and the tokens' K or V of that head are not
+ * written (IS_ST_SCALE).
  * Each wait for copies of rows has a limit of 2 s, after which tokens are left
  * out (IS_ST_TIMEOUT): whole blocks of them, or, of a block that gets more rows than fit
  * shared memory, some; writing the same tokens again makes good for it. */

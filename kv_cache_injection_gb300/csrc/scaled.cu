@@ -4,9 +4,8 @@
 //
 // The rows that a call puts into one block share one scale per head, so the unit
 // of work is a group: the tokens of one block, between which others may lie that
-// have no slot.  With A the largest
-// finite magnitude of a head's new elements (keys rotated in fp32) and qmax 127
-// or 448,
+// have no slot.  With A the largest finite magnitude of a head's new elements (keys
+// rotated in fp32) and qmax 127 or 448,
 //   s = A / qmax, in [2^-40, 2^40]; beside earlier rows no smaller than their scale;
 //   code = round(y * (1 / s)), and earlier rows' codes round(code * s_old / s) if s grew.
 // A CTA takes the groups that begin in its tokens, as many at a time as there is
@@ -19,19 +18,19 @@
 //
 // The bytes would take 27 and 40 us in the two large cases below; the steps of a
 // round wait for one another and for memory, and what overlaps them is other CTAs
-// (the SMs issue in half of their slots).  Of the 63 us of the second case 18 are
+// (the SMs issue in half of their slots).  Of the 62 us of the second case 18 are
 // the codes, 7 the search and 38 the way to the rows and the rows themselves.
 // Short loops matter more than registers: rows kept in registers and unrolled took
 // 56 and 165 us, each CTA running once through code that it has to fetch first.
 // Bringing a piece of a CTA's heads while the one before is quantised, 16 KB each,
 // took 40 and 68 us: more steps for each byte.
 //
-// Measured: 8000 tokens, 32 + 8 heads of 128, bf16 to INT8, 183 MB: 36.4 us = 5.0
+// Measured: 8000 tokens, 32 + 8 heads of 128, bf16 to INT8, 183 MB: 36.9 us = 5.0
 // TB/s, 73 % of a plain copy (the queries alone 26); 44,000 moved tokens, 8 heads,
-// bf16 to E4M3 in blocks of 32, 271 MB: 63 us = 4.3 TB/s, blocks of 16 62 us; 1276
-// tokens moved 6.7 us; 1000 requests' single tokens 11.3 us; one token 4.7 us, the
-// latency of its steps.  Reading 36,000 tokens back (E4M3 to bf16, 223 MB) 35.7 us
-// = 6.3 TB/s, 92 % of a copy; 700 tokens with their keys turned back 3.4 us.
+// bf16 to E4M3 in blocks of 32, 271 MB: 62 us = 4.4 TB/s, blocks of 16 61 us; 1276
+// tokens moved 6.6 us; 1000 requests' single tokens 11.1 us; one token 4.6 us, the
+// latency of its steps.  Reading 36,000 tokens back (E4M3 to bf16, 223 MB) 35.6 us
+// = 6.3 TB/s, 92 % of a copy; 700 tokens with their keys turned back 3.2 us.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -262,7 +261,7 @@ struct Group {
   int32_t live;          // some token is not skipped
 };
 
-// STYLE -1: no rotation (a move).  (44,000 moved tokens take 62.5 us with six CTAs an SM, 69 with five.)
+// STYLE -1: no rotation (a move).  (44,000 moved tokens take 62 us with six CTAs an SM, 69 with five.)
 template <typename T, int STYLE, bool I8>
 __global__ void __launch_bounds__(kThreads, most_per_sm(STYLE >= 0)) scaled_write_kernel(const ScaledWriteArgs p, const __grid_constant__ AxisTurns at,
                                                                   int group_ctas, int turns_of, int window, int heads_of, int cap, int share) {
