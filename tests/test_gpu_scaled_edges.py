@@ -277,3 +277,78 @@ def test_waits_of_a_long_group_that_run_out():
         status.zero_()
         api.is_move_scaled(*args, codes, scales, slots, status)
         assert status.item() == 0 and torch.equal(codes, want_codes) and torch.equal(scales, want_scales)
+
+
+# ---------------------------------------------------------------- far holes, graphs and streams
+
+@pytest.mark.parametrize("gap", [1023, 1024, 1025, 2047, 2048, 2049, 6000])
+def test_holes_further_off_than_a_look(gap):
+    """More skipped tokens than a CTA looks at in one go: between a block's tokens, before the first and behind the last."""
+    g = torch.Generator().manual_seed(gap)
+    H, D, bs, nb = 2, 64, 16, 6
+    slots = torch.tensor([35, 36, 37, 40, 64, 65, 80, 8, 9])         # blocks 2 (from row 3), 4, 5 and 0
+    source = torch.randn(2, 2, 16, H, D, generator=g).to(torch.bfloat16).to(DEV)
+    c0, s0 = cache_of("int8", nb, bs, H, D, g)
+    cd, fd, n = api.make_cache_desc(bs, nb, "int8"), api.make_cache_desc(16, 2, "bf16"), len(slots)
+
+    def move(at, T):
+        codes, scales, status = c0.clone(), s0.clone(), ints([0])
+        where = torch.full((T,), -1, dtype=torch.int64)
+        from_slots = torch.full((T,), 3, dtype=torch.int64)
+        where[at], from_slots[at] = slots, torch.arange(n) + 5
+        api.is_move_scaled(fd, source, from_slots.to(DEV), cd, codes, scales, where.to(DEV), status)
+        assert status.tolist() == [0]
+        return codes, scales
+
+    want = move(torch.arange(n), n)
+    for holes, pad, behind in (({1: gap}, 0, 0), ({3: gap, 4: gap}, 7, gap), ({0: gap, 1: gap, 7: 40}, gap, 1), ({}, gap, gap)):
+        at, T = with_holes(n, holes, pad, g)
+        assert all(torch.equal(a, b) for a, b in zip(move(at, T + behind), want))
+
+
+def test_writes_with_holes_in_graphs_on_two_streams():
+    """Captured writes, one a stream, whose buffers' slots change between replays: skipped tokens come and go."""
+    g = torch.Generator().manual_seed(41)
+    H, Hq, D, bs, nb, T = 2, 4, 64, 16, 24, 300
+    rope, cd, fd = api.make_rope(1e4), api.make_cache_desc(bs, nb, "e4m3"), api.make_cache_desc(16, 20, "bf16")
+    order = torch.randperm(nb, generator=g)
+    slots = order[torch.arange(T) // bs] * bs + torch.arange(T) % bs
+    c0, s0 = cache_of("e4m3", nb, bs, H, D, g)
+    x = torch.randn(T, Hq + 2 * H, D, generator=g).to(torch.bfloat16).to(DEV)
+    source = torch.randn(2, 20, 16, H, D, generator=g).to(torch.bfloat16).to(DEV)
+    pos, from_slots = torch.arange(T, dtype=torch.int32, device=DEV), torch.randperm(320, generator=g)[:T].to(DEV)
+
+    def state():
+        return dict(codes=c0.clone(), scales=s0.clone(), at=slots.to(DEV), q=torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=DEV),
+                    status=ints([0]))
+
+    def call(kind, t, stream=None):
+        if kind:
+            api.is_move_scaled(fd, source, from_slots, cd, t["codes"], t["scales"], t["at"], t["status"], stream=stream)
+        else:
+            api.is_append_scaled(x[:, :Hq], x[:, Hq: Hq + H], x[:, Hq + H:], pos, t["at"], rope, cd, t["codes"], t["scales"], t["q"],
+                                 t["status"], stream=stream)
+    states, streams, graphs = [state(), state()], [torch.cuda.Stream() for _ in range(2)], []
+    for kind in range(2):
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=streams[kind]):
+            call(kind, states[kind], streams[kind])
+        graphs.append(graph)
+    for share in (0.0, 0.5, 0.9, 0.99, 1.0):
+        skip = torch.rand(T, generator=g) < share
+        for t in states:
+            t["at"].copy_(torch.where(skip, -1, slots))
+            t["codes"].copy_(c0)
+            t["scales"].copy_(s0)
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for kind, t in enumerate(states):
+            want = state()
+            want["at"].copy_(t["at"])
+            call(kind, want)
+            assert all(torch.equal(want[name].view(torch.uint8), t[name].view(torch.uint8)) for name in ("codes", "scales"))
+            assert t["status"].tolist() == [0] and (share < 1.0 or torch.equal(t["codes"], c0))
