@@ -468,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, most_per_sm(STYLE >= 0)) scaled_writ
           if (from < 0 || from >= p.n_from) row = -1;
         }
         if constexpr (STYLE >= 0) {
-          for (int x = 0; x < a.n_axes && row >= 0; ++x) {
-            const int32_t pos = a.positions[(size_t)x * a.T + t];
-            if (pos < 0 || pos >= IS_MAX_POSITION) {
+          for (int x = 0; x < a.n_axes; ++x) {
+            const int32_t pos = a.positions[(size_t)x * a.T + t];   // read in any case, beside the slot; of a skipped token it means nothing
+            if (row >= 0 && (pos < 0 || pos >= IS_MAX_POSITION)) {
               latch(a.status, IS_ST_POSITION);
               row = -1;
             }
